@@ -41,6 +41,7 @@
 #ifndef FA_GB300_H
 #define FA_GB300_H
 
+#include <stddef.h>
 #include <stdint.h>
 
 #ifdef __cplusplus
@@ -67,7 +68,8 @@ typedef enum {
     FA_ERR_CAUSAL = 13,         /* causal not in {0, 1, 2}                                   */
     FA_ERR_SHAPE = 14,          /* (fa_gemm) K or N not a multiple of 8 (16-byte rows)       */
     FA_ERR_ARG = 15,            /* an enum-like argument (dtype, output type, epilogue) is out of range */
-    FA_ERR_TOO_LARGE = 16       /* (fa_fwd_host_noalloc) the problem needs more than FA_HOST_NOALLOC_MAX_BYTES of staging */
+    FA_ERR_TOO_LARGE = 16       /* (fa_fwd_host_noalloc) the problem needs more than FA_HOST_NOALLOC_MAX_BYTES of staging;
+                                   (cache operators) the workspace is smaller than the call needs */
 } fa_status_t;
 
 /*
@@ -237,6 +239,80 @@ int fa_softmax_rows(const void *x, void *y, int rows, int cols, int dtype, fa_st
 int fa_fwd_host_noalloc(const void *q_h, const void *k_h, const void *v_h, void *o_h, float *lse_h,
                         int B, int Hq, int Hkv, int Sq, int Sk, int D, int causal, float scale,
                         int dtype, int chunks, fa_stream_t stream);
+
+/* ------------------------------------------------------------------ paged key/value cache
+ *
+ * The operators of a decoding loop over a cache: attention of drafted tokens (fa_tree_fwd), the
+ * cache's writes (fa_cache_append), the attention weight that its slots have received
+ * (fa_cache_weights) and eviction by that weight (fa_cache_evict).  The pages name no cache; the
+ * attention is the flash-attention section's, with the keys read through a page table.
+ *
+ * A cache holds the keys and values of B sequences in pages of `page` slots that any sequence may
+ * own.  Slot s of sequence b is row s % page of page table[b * max_pages + s / page] (of page
+ * b * max_pages + s / page without a table, i.e. a dense cache), the same for every KV head;
+ * `capacity` = max_pages * page slots a sequence.  Lengths and tables are device arrays that the
+ * kernels read when they run, so a captured graph follows them.  A length below 0 counts as 0, one
+ * above the capacity as the capacity.  A table entry outside [0, num_pages) that a length covers is a
+ * caller's mistake that touches no memory outside the cache: its slots read as zero keys and values
+ * and writes to them are dropped.
+ *
+ * All tensors are dense; pointers are device pointers on the current device, 16-byte aligned for
+ * k, v, q, o, k_new and v_new, 4-byte aligned otherwise.  Everything said above about ownership,
+ * asynchrony and threads holds.  A call uses its workspace until its work on `stream` is done: calls
+ * (and captured graphs) that may run at the same time need workspaces of their own.
+ */
+typedef struct fa_cache {
+    void *k, *v;              /* [num_pages, Hkv, page, D], bf16 (dtype 0) or fp16 (dtype 1) */
+    const int32_t *table;     /* [B, max_pages] page of each run of `page` slots, or NULL */
+    const int32_t *seq_len;   /* [B] slots in use */
+    int B, Hkv, D;            /* sequences, KV heads, head dimension (64, 128 or 256) */
+    int page;                 /* slots of a page, a multiple of 16 */
+    int max_pages;            /* pages a sequence may own: columns of `table` */
+    int num_pages;            /* pages of the pool */
+    int dtype;
+} fa_cache_t;
+
+/*
+ * fa_tree_fwd -- attention of each sequence's drafted tokens (a tree, a chain, or one token) over
+ * its cached slots and over the drafted tokens on the path to its root, itself included:
+ *   for sequence b, query head h, token t < draft_len[b], KV head c = h / (Hq / Hkv):
+ *     J = the seq_len[b] slots and { t, parent[t], parent[parent[t]], ... }
+ *     o[b,h,t,:], lse[b,h,t] = softmax attention over J, as fa_fwd's (natural-log lse, float32)
+ *   q, o         [B, Hq, T, D], k_new, v_new [B, Hkv, T, D]: the cache's type
+ *   lse          [B, Hq, T] float32
+ *   parent       [B, T]: the token that t follows, or -1 for a root; parents come before their
+ *                children, and an entry that is not in [0, t) makes t a root.  NULL: a chain (t follows t - 1)
+ *   draft_len    [B] drafted tokens of each sequence (clamped to [0, T]), or NULL: T.  Rows of o and
+ *                lse at or behind it are left as they were; tokens behind it are not read as keys
+ *   scale        > 0 and finite
+ *   workspace    fa_tree_workspace_bytes(Hq, Hkv, T, D) bytes, 32-byte aligned; needs no initial value
+ * The cache is only read: the drafted tokens are appended when they are accepted (fa_cache_append).
+ * What the cache holds behind a sequence's end, and tokens that a row does not see, have no effect
+ * on the row, NaN and infinities included.  The result does not vary from run to run.
+ * FA_ERR_TOO_LARGE: workspace_bytes is too small.  A device wait that gives up leaves NaN in the
+ * rows concerned (fa_device_status).
+ */
+size_t fa_tree_workspace_bytes(int Hq, int Hkv, int T, int D);
+int fa_tree_fwd(const fa_cache_t *cache, const void *q, const void *k_new, const void *v_new,
+                const int32_t *parent, const int32_t *draft_len, void *o, float *lse, int Hq, int T,
+                float scale, void *workspace, size_t workspace_bytes, fa_stream_t stream);
+
+/*
+ * fa_cache_append -- writes accepted tokens behind the slots in use: slot seq_len[b] + i of every KV
+ * head takes the key and value of token path[b, i], i < count[b].
+ *   k_new, v_new   [B, Hkv, T, D]: the cache's type
+ *   path           [B, T] indices into the T tokens, or NULL: token i.  An index outside [0, T) writes
+ *                  nothing to its slot
+ *   count          [B] tokens to write (clamped to [0, T]), or NULL (without a path): T
+ *   weight         [B, Hkv, capacity] float32 or NULL: the new slots' accumulated weight becomes 0
+ *   pos            [B, Hkv, capacity] int32 or NULL: the new slots' position becomes start[b] + i
+ *   start          [B], required with pos
+ * Tokens that do not fit behind the capacity are dropped.  seq_len is not changed (the layers of a
+ * model share it): the caller adds count to it after the last layer.
+ */
+int fa_cache_append(const fa_cache_t *cache, const void *k_new, const void *v_new, const int32_t *path,
+                    const int32_t *count, const int32_t *start, float *weight, int32_t *pos, int T,
+                    fa_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -15,4 +15,7 @@ def __getattr__(name):
                 "softmax_rows"):
         from . import binding
         return getattr(binding, name)
+    if name in ("KVCache", "tree_attention", "tree_workspace_bytes", "cache_append"):
+        from . import cache
+        return getattr(cache, name)
     raise AttributeError(name)

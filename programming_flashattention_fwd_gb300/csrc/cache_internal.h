@@ -1,0 +1,70 @@
+// cache_internal.h -- declarations shared by the host API of the cache operators (cache_api.cpp)
+// and their kernels.  Not part of the public ABI.
+#pragma once
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "cache_schedule.h"
+
+namespace fa {
+namespace cache {
+
+// CTAs that a workspace has room for; a launch uses at most one per SM and at most this many.
+constexpr int kMaxCtas = 160;
+constexpr int kRowTile = 128;
+
+// Where the slots of a sequence are: slot s on row s % page of page table[b * max_pages + s / page]
+// (page b * max_pages + s / page without a table).
+struct Pages {
+    const int32_t *table;
+    int page, max_pages, num_pages;
+};
+
+struct TreeParams {
+    TreeShape s;
+    Pages pages;
+    const int32_t *parent;   // [B, T] or null: token t follows t - 1
+    const void *v_new;       // [B, Hkv, T, D], also read by the maps
+    void *o;                 // [B, Hq, T, D]
+    float *lse;              // [B, Hq, T]
+    float *part_o;           // [2 * kMaxCtas][part_rows][D]
+    float *part_lse;         // [2 * kMaxCtas][part_rows], log2 units
+    int part_rows;           // min(rows, 128)
+    int box_rows;            // rows of one copy: gcd(page, 128), at most BN
+    int least;               // steps a CTA takes at least
+    float sl2;               // scale * log2 e
+    uint64_t timeout_ns;
+};
+
+struct TreeMaps {
+    CUtensorMap q, k, v, k_new, v_new;
+};
+
+int tree_keys(int D);        // keys per step
+cudaError_t launch_tree(int D, bool bf16, const TreeMaps &m, const TreeParams &p, cudaStream_t st);
+cudaError_t read_and_clear_tree_status(uint32_t *word);
+
+// ---------------------------------------------------------------- writing the cache
+struct AppendParams {
+    Pages pages;
+    uint4 *k, *v;                  // [num_pages, Hkv, page, D]
+    const uint4 *k_new, *v_new;    // [B, Hkv, T, D]
+    const int32_t *seq_len;        // [B]
+    const int32_t *path, *count;   // [B, T], [B]; null: every token in order
+    const int32_t *start;          // [B]: position of the first token written
+    float *weight;                 // [B, Hkv, capacity] or null
+    int32_t *pos;                  // [B, Hkv, capacity] or null
+    int B, Hkv, T, capacity;
+    int chunks;                    // 16-byte chunks of a row: D / 8
+    int blocks_per_head;           // blocks over the T tokens of one (sequence, KV head)
+};
+cudaError_t launch_append(const AppendParams &p, int blocks, cudaStream_t st);
+int append_tokens(int D);          // tokens of one block
+
+} // namespace cache
+
+// The watchdog words of the cache kernels (read with the other kernels' by fa_device_status).
+cudaError_t read_and_clear_cache_status(uint32_t *word);
+
+} // namespace fa

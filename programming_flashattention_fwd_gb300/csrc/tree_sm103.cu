@@ -1,0 +1,806 @@
+// tree_sm103.cu -- attention of drafted tokens over a paged key/value cache (fa_tree_fwd).
+//
+// For sequence b, KV head c, drafted token t and each query head h of c's group:
+//
+//     s_j = scale q.k_j over the n_b cached slots and the drafted tokens j on t's path to its root
+//     o   = sum_j exp(s_j - m) v_j / sum_j exp(s_j - m),   lse = m + ln sum_j exp(s_j - m)
+//
+// The rows of one KV head (heads of the group x drafted tokens, consecutive in memory) are packed
+// into 128-row tiles, so that K and V are read once for all of them; with fewer than about 280 rows
+// the kernel is bound by that read.  The keys of every unit (sequence, KV head, row tile) are cut so
+// that each CTA has the same number of key steps (cache_schedule.h); a unit that is cut leaves
+// normalised fp32 partial rows with their log-sum-exp in the workspace and a second kernel joins
+// them in the order of the keys, the same on every run.
+//
+// Per CTA (one per SM):
+//   warp 0        K / V producer: per step one TMA box per page and 64-column panel (each lane looks
+//                 up the page of its box), into a ring of NS slots
+//   warp 1        TMEM owner and MMA issuer: S = Q K^T, O += P V (tcgen05, fp32 in tensor memory)
+//   warp 2        Q producer
+//   warp 3        finds this CTA's share of the work
+//   warps 4-7,    softmax, one thread per row.  D <= 128: two groups take alternate key steps, each
+//   warps 8-11    with its own running maximum, sum and O accumulator, so that one group's softmax
+//                 runs beside the other's matrix products; they are joined in the epilogue, where
+//                 both read both accumulators (half of the columns each).  D = 256: one group (two
+//                 accumulators do not fit), with 64-key steps.
+//
+// Tensor memory: S_0, S_1 (BN columns each; P, 16-bit, overwrites its S), then the accumulators.
+//
+// Keys that a row must not see: scores are replaced by -inf, not summed with it, and the V rows
+// behind the last valid key of a step are zeroed in shared memory before P V, so that neither
+// what the cache holds behind a sequence's end nor its page's old contents reach the result.
+// Non-finite values in a drafted token's V are taken out of the matrix product and added, as what
+// they are, to the rows that see that token, so that they do not leak into other branches.
+#include <atomic>
+#include <cstdint>
+
+#include "cache_internal.h"
+#include "ptx.cuh"
+#include "watchdog.cuh"
+
+namespace fa {
+
+__device__ unsigned int g_tree_status;
+
+namespace cache {
+
+namespace {
+
+constexpr uint64_t kDefaultTimeoutNs = 2000000000ull;
+constexpr float kTau = 12.f;   // O is rescaled when the maximum grows by more than this (log2 units): P <= 4096 fits fp16
+
+enum Site : uint32_t {
+    S_EMPTY = 1, S_Q = 2, S_FULL = 3, S_P = 4, S_S = 5, S_PV = 6, S_DRAIN = 7, S_QFREE = 8, S_SMEM = 9, S_JOIN = 10, S_READ = 11
+};
+
+template <int D>
+struct Cfg {
+    static constexpr int BN = D == 256 ? 64 : 128;
+    static constexpr int NG = D == 256 ? 1 : 2;          // softmax groups
+    static constexpr int THREADS = 128 + 128 * NG;
+    static constexpr int PANELS = D / 64;
+    static constexpr int QPANEL = kRowTile * 128, QTILE = PANELS * QPANEL;
+    static constexpr int KVPANEL = BN * 128, KVTILE = PANELS * KVPANEL;
+    static constexpr int NS = D == 64 ? 12 : (D == 128 ? 6 : 5);   // 192, 192 and 160 KB of K / V in flight
+    static constexpr int OFF_RING = QTILE;
+    static constexpr int OFF_BAR = OFF_RING + NS * KVTILE;
+    static constexpr int NBAR = 2 + 2 * NS + 2 + 2 + 2 + 2 + 1;    // q, qfree, full, empty, S[2], P[2], PV[2], join, read, done
+    static constexpr int OFF_ML = OFF_BAR + ((NBAR * 8 + 15) / 16) * 16;   // [NG][128] (m, l)
+    static constexpr int OFF_MISC = OFF_ML + NG * 128 * 8;
+    static constexpr int BYTES = OFF_MISC + 48;
+    static_assert(BYTES <= 232448, "shared memory of one CTA");
+    // room to align the base to 1024 bytes, as far as there is any (the kernel checks what it got)
+    static constexpr int ALLOC = BYTES + 1024 <= 232448 ? BYTES + 1024 : 232448;
+    static constexpr uint32_t COL_O = 2 * BN;
+    static_assert(2 * BN + NG * D <= 512, "tensor-memory columns");
+};
+
+struct Misc {
+    uint32_t tmem;
+    int abort;
+    int nonfinite;      // 1 + index of the last segment whose drafted V held a non-finite value
+    TreeWalk walk;      // this CTA's share
+};
+
+// x is an infinity or a NaN, in a 16-bit pair: the pair with those halves cleared, and whether there were any.
+template <bool BF16>
+__device__ __forceinline__ uint32_t drop_nonfinite(uint32_t w, bool &any)
+{
+    constexpr uint32_t E = BF16 ? 0x7f80u : 0x7c00u;
+    const bool lo = (w & E) == E, hi = ((w >> 16) & E) == E;
+    any |= lo | hi;
+    return (lo ? 0u : (w & 0xffffu)) | (hi ? 0u : (w & 0xffff0000u));
+}
+
+template <bool BF16>
+__device__ __forceinline__ float half_to_float(uint16_t h)
+{
+    if constexpr (BF16) {
+        return __uint_as_float((uint32_t)h << 16);
+    } else {
+        float f;
+        asm("cvt.f32.f16 %0, %1;" : "=f"(f) : "h"(h));
+        return f;
+    }
+}
+
+// Bits of the drafted tokens lo .. lo + 32 W - 1 that token t sees: its path to the root (parents
+// come before their children; an entry that does not ends the path).
+template <int W>
+__device__ __forceinline__ void path_bits(const int32_t *parent, int t, int lo, uint32_t (&bits)[W])
+{
+#pragma unroll
+    for (int w = 0; w < W; ++w) bits[w] = 0;
+    if (!parent) {
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            const int c = t - lo - 32 * w;   // keys up to lo + 32 w + c
+            bits[w] = c < 0 ? 0u : (c >= 31 ? ~0u : (2u << c) - 1u);
+        }
+        return;
+    }
+    for (int j = t; j >= lo;) {
+        const int i = j - lo;
+#pragma unroll
+        for (int w = 0; w < W; ++w)
+            if ((i >> 5) == w) bits[w] |= 1u << (i & 31);
+        const int up = __ldg(parent + j);
+        if (up >= j) break;
+        j = up;
+    }
+}
+
+// This CTA's share: all steps are counted and the sequence that holds the first is found, by one warp.
+__device__ __forceinline__ void find_share(const TreeShape &s, int least, int lane, int cta, int grid, int *total_out,
+                                           int *G_out, TreeWalk *walk)
+{
+    const int U = s.Hkv * s.mtiles;
+    int total = 0;
+    for (int b = lane; b < s.B; b += 32) total += U * tree_len(s, b).nt;
+#pragma unroll
+    for (int d = 16; d; d >>= 1) total += __shfl_xor_sync(~0u, total, d);
+    const int G = ctas(total, grid, least);
+    const int begin = cta < G ? cut(total, G, cta) : total;
+    const int left = cta < G ? cut(total, G, cta + 1) - begin : 0;
+    int b0 = 0, before = 0;   // steps of the sequences before b0
+    for (; b0 < s.B; b0 += 32) {
+        const int b = b0 + lane;
+        const int mine = b < s.B ? U * tree_len(s, b).nt : 0;
+        int sum = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int x = __shfl_up_sync(~0u, sum, d);
+            if (lane >= d) sum += x;
+        }
+        const uint32_t past = __ballot_sync(~0u, before + sum > begin);
+        if (past) {
+            const int src = __ffs(past) - 1;
+            b0 += src;
+            before += __shfl_sync(~0u, sum - mine, src);
+            break;
+        }
+        before += __shfl_sync(~0u, sum, 31);
+    }
+    walk->b = b0;
+    walk->off = begin - before;
+    walk->left = left;
+    *total_out = total;
+    *G_out = G;
+}
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
+    tree_kernel(const __grid_constant__ TreeMaps maps, const __grid_constant__ TreeParams p)
+{
+    using C = Cfg<D>;
+    constexpr int BN = C::BN, NG = C::NG;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t pad = (1024u - (raw & 1023u)) & 1023u;
+    uint8_t *smem = smem_raw + pad;
+    const uint32_t sb = raw + pad;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t sRing = sb + C::OFF_RING, bar0 = sb + C::OFF_BAR;
+    const uint32_t barQ = bar0, barQfree = bar0 + 8;
+    auto bar_full = [&](int s) { return bar0 + 8u * (2 + s); };
+    auto bar_empty = [&](int s) { return bar0 + 8u * (2 + C::NS + s); };
+    const uint32_t barS = bar0 + 8u * (2 + 2 * C::NS), barP = barS + 16, barPV = barS + 32, barJoin = barS + 48,
+                   barRead = barS + 56, barDone = barS + 64;
+    float2 *ml = reinterpret_cast<float2 *>(smem + C::OFF_ML);
+    volatile Misc *misc = reinterpret_cast<volatile Misc *>(smem + C::OFF_MISC);
+    volatile int *abort_flag = &misc->abort;
+    unsigned int *status = &g_tree_status;
+    const uint64_t tmo = p.timeout_ns;
+
+    // the joining kernel may be scheduled from here on; it waits for this grid's end before it reads
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (pad + (uint32_t)C::BYTES > dynamic_smem_size_u32()) {
+        if (threadIdx.x == 0) atomicOr(status, 1u | (S_SMEM << 8));
+        return;
+    }
+    if (threadIdx.x == 0) {
+        mbar_init(barQ, 1);
+        mbar_init(barQfree, 1);
+        for (int s = 0; s < C::NS; ++s) {
+            mbar_init(bar_full(s), 1);
+            mbar_init(bar_empty(s), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(barS + 8 * i, 1);
+            mbar_init(barP + 8 * i, 4);
+            mbar_init(barPV + 8 * i, 1);
+        }
+        mbar_init(barJoin, 4 * NG);
+        mbar_init(barRead, 4 * NG);
+        mbar_init(barDone, 1);
+        misc->abort = 0;
+        misc->nonfinite = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(const_cast<uint32_t *>(&misc->tmem)), 512);
+        tmem_relinquish();
+    }
+    if (warp == 3) {
+        TreeWalk w;
+        int total, G;
+        find_share(p.s, p.least, lane, blockIdx.x, gridDim.x, &total, &G, &w);
+        if (lane == 0) {
+            misc->walk.b = w.b;
+            misc->walk.off = w.off;
+            misc->walk.left = w.left;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = misc->tmem;
+    TreeWalk walk{misc->walk.b, misc->walk.off, misc->walk.left};
+    const TreeWalk share = walk;
+    TreeSeg g;
+
+    auto wait_all = [&](uint32_t bar, uint32_t parity, uint32_t site) -> bool {
+        return __all_sync(0xffffffffu, bounded_wait(bar, parity, abort_flag, tmo, site, status)) != 0;
+    };
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ K / V producer
+        const Pages pg = p.pages;
+        const int boxes = BN / p.box_rows;            // boxes of a step (one panel)
+        const int box = lane / C::PANELS, pn = lane % C::PANELS;
+        const uint32_t box_off = (uint32_t)(pn * C::KVPANEL + box * p.box_rows * 128);
+        int use = 0;
+        bool ok = true;
+        // the page (and the row in it) of this lane's box of step kt
+        auto look = [&](const TreeSeg &g, int kt, int &pid, int &row) {
+            pid = -1;
+            row = 0;
+            if (kt >= g.len.kc || box >= boxes) return;
+            const int slot = kt * BN + box * p.box_rows;
+            if (slot >= g.len.n) return;
+            const int at = slot / pg.page;
+            row = slot - at * pg.page;
+            pid = pg.table ? __ldg(pg.table + (size_t)g.b * pg.max_pages + at) : g.b * pg.max_pages + at;
+            // a page that does not exist reads as zeros (past the end of the tensor)
+            if (pid < 0 || pid >= pg.num_pages) pid = pg.num_pages;
+        };
+        auto load = [&](const TreeSeg &g, bool is_v, int kt, int pid, int row) -> bool {
+            const int s = use % C::NS;
+            if (!wait_all(bar_empty(s), ((use / C::NS) & 1) ^ 1, S_EMPTY)) return false;
+            const uint32_t dst = sRing + s * C::KVTILE, bar = bar_full(s);
+            if (kt < g.len.kc) {
+                const int valid = min(boxes, cdiv(g.len.n - kt * BN, p.box_rows));
+                if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(valid * p.box_rows * 128 * C::PANELS));
+                __syncwarp();
+                if (pid >= 0) {
+                    const CUtensorMap *m = is_v ? &maps.v : &maps.k;
+                    asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                                 " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst + box_off),
+                                 "l"(reinterpret_cast<uint64_t>(m)), "r"(pn * 64), "r"(row), "r"(g.kvh), "r"(pid), "r"(bar)
+                                 : "memory");
+                }
+            } else {
+                if (lane == 0) mbar_arrive_expect_tx(bar, C::KVTILE);
+                __syncwarp();
+                if (lane < C::PANELS)
+                    tma_load_3d(dst + lane * C::KVPANEL, is_v ? &maps.v_new : &maps.k_new, lane * 64, (kt - g.len.kc) * BN,
+                                g.b * p.s.Hkv + g.kvh, bar);
+            }
+            ++use;
+            return true;
+        };
+        while (ok && walk.next(p.s, g)) {
+            int pid, row, pid1, row1;
+            look(g, g.k0, pid, row);
+            ok = load(g, false, g.k0, pid, row);
+            for (int kt = g.k0; ok && kt < g.k1; ++kt) {
+                if (kt + 1 < g.k1) {
+                    look(g, kt + 1, pid1, row1);
+                    ok = load(g, false, kt + 1, pid1, row1);
+                }
+                if (ok) ok = load(g, true, kt, pid, row);
+                pid = pid1;
+                row = row1;
+            }
+        }
+        if (lane == 0)
+            for (int x = max(0, use - C::NS); x < use; ++x)
+                bounded_wait(bar_full(x % C::NS), (x / C::NS) & 1, abort_flag, tmo, S_DRAIN, status, false);
+        __syncwarp();
+    } else if (warp == 2) {
+        // ------------------------------------------------------------ Q producer
+        if (lane == 0) {
+            int tau = 0;
+            for (; walk.next(p.s, g); ++tau) {
+                if (tau && !bounded_wait(barQfree, (tau - 1) & 1, abort_flag, tmo, S_QFREE, status)) break;
+                mbar_arrive_expect_tx(barQ, C::QTILE);
+#pragma unroll
+                for (int pn = 0; pn < C::PANELS; ++pn)
+                    tma_load_3d(sb + pn * C::QPANEL, &maps.q, pn * 64, g.mt * kRowTile, g.b * p.s.Hkv + g.kvh, barQ);
+            }
+            if (tau) bounded_wait(barQ, (tau - 1) & 1, abort_flag, tmo, S_DRAIN, status, false);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA issuer (whole warp)
+        constexpr uint32_t idS = idesc_f16(BF16, kRowTile, BN, false), idPV = idesc_f16(BF16, kRowTile, D, true);
+        constexpr uint32_t HI = sdesc_hi_sw128(1024);
+        auto slot = [&](int use) { return sRing + (uint32_t)(use % C::NS) * C::KVTILE; };
+        auto issue_s = [&](uint32_t gs, int use) {
+            const uint32_t sK = slot(use);
+#pragma unroll
+            for (int pn = 0; pn < C::PANELS; ++pn)
+                mma_ss_kk4_elect(tmem + (gs & 1) * BN, sdesc_lo(sb + pn * C::QPANEL, 16), sdesc_lo(sK + pn * C::KVPANEL, 16), HI,
+                                 idS, pn ? 1u : 0u);
+            tc_commit_elect(barS + 8u * (gs & 1));
+            tc_commit_elect(bar_empty(use % C::NS));
+        };
+        int use = 0, tau = 0;
+        uint32_t gs = 0;   // this CTA's key step: S buffer, barriers and softmax group gs & 1
+        bool ok = true;
+        for (; ok && walk.next(p.s, g); ++tau) {
+            const int nk = g.k1 - g.k0;
+            ok = wait_all(barQ, tau & 1, S_Q) && wait_all(bar_full(use % C::NS), (use / C::NS) & 1, S_FULL);
+            if (!ok) break;
+            tc_fence_after();
+            issue_s(gs, use);
+            if (nk == 1) tc_commit_elect(barQfree);
+            ++use;
+            for (int j = 0; j < nk; ++j, ++gs) {
+                if (j + 1 < nk) {
+                    ok = wait_all(bar_full(use % C::NS), (use / C::NS) & 1, S_FULL);
+                    if (!ok) break;
+                    tc_fence_after();
+                    issue_s(gs + 1, use);   // its S buffer held P(gs - 1), whose P V was issued before
+                    if (j + 2 == nk) tc_commit_elect(barQfree);
+                    ++use;
+                }
+                ok = wait_all(bar_full(use % C::NS), (use / C::NS) & 1, S_FULL) &&
+                     wait_all(barP + 8u * (gs & 1), (gs >> 1) & 1, S_P);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t dO = tmem + C::COL_O + (NG == 2 ? (gs & 1) * D : 0u);
+                const uint32_t vlo = sdesc_lo(slot(use), C::KVPANEL);
+#pragma unroll
+                for (int h = 0; h < BN / 64; ++h)
+                    mma_ts_mn4_elect(dO, tmem + (gs & 1) * BN + 32 * h, vlo + (uint32_t)((h * 8192) >> 4), HI, idPV,
+                                     (j < NG && h == 0) ? 0u : 1u);
+                tc_commit_elect(barPV + 8u * (gs & 1));
+                tc_commit_elect(bar_empty(use % C::NS));
+                ++use;
+            }
+        }
+        tc_commit_elect(barDone);
+        bounded_wait(barDone, 0, abort_flag, tmo, S_DRAIN, status, false);
+        __syncwarp();
+    } else if (warp >= 4) {
+        // ------------------------------------------------------------ softmax, epilogue
+        const int grp = NG == 2 ? (warp - 4) >> 2 : 0;
+        const int r = (threadIdx.x - 128) & 127;                  // row of the tile == TMEM lane
+        const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+        const float sl2 = p.sl2;
+        const uint64_t sl2x2 = f2_pack(sl2, sl2);
+        uint32_t gs0 = 0;
+        int use0 = 0, seg = 0;
+        bool ok = true;
+        for (; ok && walk.next(p.s, g); ++seg) {
+            const int nk = g.k1 - g.k0;
+            const int row = g.mt * kRowTile + r, t = row % p.s.T;
+            const bool live = row < p.s.rows && t < g.len.t;
+            const bool warp_live = __any_sync(~0u, live);
+            const int32_t *parent = p.parent ? p.parent + (size_t)g.b * p.s.T : nullptr;
+            float m_used = -INFINITY, l = 0.f;
+            bool first = true;
+            for (int j = NG == 2 ? (int)((gs0 ^ (uint32_t)grp) & 1u) : 0; j < nk; j += NG) {
+                const uint32_t gs = gs0 + j, bi = gs & 1, ph = (gs >> 1) & 1;
+                const uint32_t tS = tmem + lane_off + bi * BN;
+                const int kt = g.k0 + j;
+                const bool draft = kt >= g.len.kc;
+                const int base = draft ? (kt - g.len.kc) * BN : kt * BN;
+                const int valid = min(BN, (draft ? g.len.t : g.len.n) - base);
+                const bool masked = draft || valid < BN;
+                uint32_t bits[BN / 32];
+                if (masked) {
+                    if (draft && live) {
+                        path_bits<BN / 32>(parent, t, base, bits);
+                    } else {
+#pragma unroll
+                        for (int w = 0; w < BN / 32; ++w) {
+                            const int c = valid - 32 * w;
+                            bits[w] = c <= 0 || draft ? 0u : (c >= 32 ? ~0u : (1u << c) - 1u);
+                        }
+                    }
+                }
+                ok = wait_all(barS + 8u * bi, ph, S_S);
+                if (!ok) break;
+                tc_fence_after();
+                bool rescale = false;
+                float alpha = 1.f;
+                if (warp_live) {
+                    uint32_t sv[BN];
+                    float pm[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int c = 0; c < BN; c += 32)
+                        tmem_ld_red_max_x32(tS + c, *reinterpret_cast<uint32_t(*)[32]>(sv + c), pm[c / 32]);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int c = 0; c < BN; c += 32) reg_fence_x32(*reinterpret_cast<uint32_t(*)[32]>(sv + c));
+                    reg_fence_f4(pm[0], pm[1], pm[2], pm[3]);
+                    float *s = reinterpret_cast<float *>(sv);
+                    float mrow = fmaxf(fmax3(pm[0], pm[1], pm[2]), pm[3]);
+                    if (masked) {
+                        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                        for (int c = 0; c < BN; ++c) {
+                            if (!((bits[c >> 5] >> (c & 31)) & 1u)) s[c] = -INFINITY;
+                            mx[c & 3] = fmaxf(mx[c & 3], s[c]);
+                        }
+                        mrow = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]);
+                    }
+                    const float m_new = fmaxf(m_used, mrow * sl2);
+                    if (first || m_used == -INFINITY) {
+                        // nothing but zeros in this group's O so far
+                        m_used = m_new;
+                    } else if (m_new - m_used > kTau) {
+                        alpha = ex2_approx(m_used - m_new);
+                        l *= alpha;
+                        m_used = m_new;
+                        rescale = true;
+                    }
+                    const float msub = m_used == -INFINITY ? 0.f : m_used;
+                    const uint64_t negm2 = f2_pack(-msub, -msub);
+                    uint64_t sum2[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) sum2[i] = f2_pack(0.f, 0.f);
+#pragma unroll
+                    for (int c = 0; c < BN / 32; ++c) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const int i = 32 * c + 2 * e;
+                            float t0, t1;
+                            f2_unpack(f2_fma(f2_pack(s[i], s[i + 1]), sl2x2, negm2), t0, t1);
+                            const float p0 = ex2_approx(t0), p1 = ex2_approx(t1);
+                            sum2[e & 3] = f2_add(sum2[e & 3], f2_pack(p0, p1));
+                            pk[e] = pack2<BF16>(p0, p1);
+                        }
+                        tmem_st_x16(tS + 16 * c, pk);
+                    }
+                    float la, lb;
+                    f2_unpack(f2_add(f2_add(sum2[0], sum2[1]), f2_add(sum2[2], sum2[3])), la, lb);
+                    l += la + lb;
+                }
+                // O may be rescaled only once this accumulator's previous product is complete
+                if (__any_sync(~0u, rescale)) {
+                    const uint32_t prev = gs - NG;
+                    ok = wait_all(barPV + 8u * (prev & 1), (prev >> 1) & 1, S_PV);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t tO = tmem + lane_off + C::COL_O + (uint32_t)(grp * D);
+                    const uint64_t a2 = f2_pack(alpha, alpha);
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 32) {
+                        uint32_t ov[32];
+                        tmem_ld_x32(tO + c, ov);
+                        tmem_wait_ld();
+                        reg_fence_x32(ov);
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            float lo, hi;
+                            f2_unpack(f2_mul(f2_pack(__uint_as_float(ov[e]), __uint_as_float(ov[e + 1])), a2), lo, hi);
+                            ov[e] = __float_as_uint(lo);
+                            ov[e + 1] = __float_as_uint(hi);
+                        }
+                        tmem_st_x32(tO + c, ov);
+                    }
+                }
+                if (first && seg > 0) {
+                    // every warp is done with the epilogue of the segment before: with both
+                    // accumulators, the groups' maxima and sums and the non-finite mark
+                    ok = wait_all(barRead, (seg - 1) & 1, S_READ);
+                    if (!ok) break;
+                }
+                if (masked) {
+                    // V behind the last valid key is zeroed; a drafted V's non-finite values are taken out
+                    const int uv = use0 + (j + 1 < nk ? 2 * j + 2 : 2 * j + 1);
+                    ok = wait_all(bar_full(uv % C::NS), (uv / C::NS) & 1, S_FULL);
+                    if (!ok) break;
+                    const uint32_t sV = sRing + (uint32_t)(uv % C::NS) * C::KVTILE;
+                    const int dead = (BN - valid) * 8;   // 16-byte chunks of one panel
+                    for (int i = r; i < dead * C::PANELS; i += 128) {
+                        const int pn = i / dead;
+                        st_shared_v4(sV + pn * C::KVPANEL + valid * 128 + (i - pn * dead) * 16, 0u, 0u, 0u, 0u);
+                    }
+                    if (draft) {
+                        bool any = false;
+                        for (int i = r; i < valid * 8 * C::PANELS; i += 128) {
+                            const int pn = i / (valid * 8);
+                            const uint32_t a = sV + pn * C::KVPANEL + (i - pn * valid * 8) * 16;
+                            uint32_t w[4];
+                            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                                         : "r"(a)
+                                         : "memory");
+                            bool here = false;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) w[e] = drop_nonfinite<BF16>(w[e], here);
+                            if (here) st_shared_v4(a, w[0], w[1], w[2], w[3]);
+                            any |= here;
+                        }
+                        if (any) misc->nonfinite = seg + 1;
+                    }
+                    fence_proxy_async_smem();
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(barP + 8u * bi);
+                first = false;
+            }
+            if (!ok) break;
+            // ---- epilogue: join the groups' maxima and sums, then O
+            if (first && seg > 0) {   // a segment of one step, the other group's
+                ok = wait_all(barRead, (seg - 1) & 1, S_READ);
+                if (!ok) break;
+            }
+            ml[grp * 128 + r] = make_float2(m_used, l);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(barJoin);
+            ok = wait_all(barJoin, seg & 1, S_JOIN);
+            if (!ok) break;
+            float f0, f1 = 0.f, L, M;
+            if constexpr (NG == 2) {
+                const float2 a = ml[r], b = ml[128 + r];
+                M = fmaxf(a.x, b.x);
+                const float ms = M == -INFINITY ? 0.f : M;
+                f0 = a.y == 0.f ? 0.f : ex2_approx(a.x - ms);
+                f1 = b.y == 0.f ? 0.f : ex2_approx(b.x - ms);
+                L = f0 * a.y + f1 * b.y;
+                const float inv = L == 0.f ? 0.f : 1.f / L;
+                f0 *= inv;
+                f1 *= inv;
+            } else {
+                M = m_used;
+                L = l;
+                f0 = L == 0.f ? 0.f : 1.f / L;
+            }
+            // the last products of both groups (the last two steps of the segment, if it has two)
+            const uint32_t e1 = gs0 + nk - 1;
+            ok = wait_all(barPV + 8u * (e1 & 1), (e1 >> 1) & 1, S_PV);
+            if (ok && nk > 1) ok = wait_all(barPV + 8u * ((e1 - 1) & 1), ((e1 - 1) >> 1) & 1, S_PV);
+            if (!ok) break;
+            tc_fence_after();
+            const bool have0 = NG == 1 || nk > 1 || (gs0 & 1) == 0, have1 = NG == 2 && (nk > 1 || (gs0 & 1) == 1);
+            const bool whole = g.k0 == 0 && g.k1 == g.len.nt;
+            const bool odd = misc->nonfinite == seg + 1;   // rare: non-finite values in the drafted V
+            const size_t prow = (size_t)part_slot(blockIdx.x, g.k0) * p.part_rows + r;
+            const size_t orow = ((size_t)(g.b * p.s.Hkv + g.kvh)) * p.s.rows + row;
+            constexpr int COLS = D / NG;
+            if (warp_live) {
+#pragma unroll 1
+                for (int c = grp * COLS; c < (grp + 1) * COLS; c += 32) {
+                    float h[32];
+                    const uint32_t tO = tmem + lane_off + C::COL_O + c;
+                    if (have0) {
+                        uint32_t ov[32];
+                        tmem_ld_x32(tO, ov);
+                        tmem_wait_ld();
+                        reg_fence_x32(ov);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) h[e] = f0 == 0.f ? 0.f : __uint_as_float(ov[e]) * f0;
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) h[e] = 0.f;
+                    }
+                    if (have1) {
+                        uint32_t ov[32];
+                        tmem_ld_x32(tO + D, ov);
+                        tmem_wait_ld();
+                        reg_fence_x32(ov);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) h[e] = f1 == 0.f ? h[e] : fmaf(__uint_as_float(ov[e]), f1, h[e]);
+                    }
+                    if (!live) continue;
+                    if (odd) {
+                        // weights are positive, so a non-finite value counts as what it is
+                        for (int kt = max(g.k0, g.len.kc); kt < g.k1; ++kt) {
+                            const int lo = (kt - g.len.kc) * BN;
+                            uint32_t bits[BN / 32];
+                            path_bits<BN / 32>(parent, t, lo, bits);
+#pragma unroll
+                            for (int w = 0; w < BN / 32; ++w)
+                                for (uint32_t left = bits[w]; left; left &= left - 1) {
+                                    const int key = lo + 32 * w + __ffs(left) - 1;
+                                    if (key >= g.len.t) break;
+                                    const uint16_t *v = static_cast<const uint16_t *>(p.v_new) +
+                                                        ((size_t)(g.b * p.s.Hkv + g.kvh) * p.s.T + key) * D + c;
+#pragma unroll
+                                    for (int e = 0; e < 32; ++e) {
+                                        const float x = half_to_float<BF16>(__ldg(v + e));
+                                        if (!isfinite(x)) h[e] += x;
+                                    }
+                                }
+                        }
+                    }
+                    if (whole) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) pk[e] = pack2<BF16>(h[2 * e], h[2 * e + 1]);
+                        uint8_t *dst = static_cast<uint8_t *>(p.o) + (orow * D + c) * 2;
+#pragma unroll
+                        for (int q4 = 0; q4 < 4; ++q4)
+                            st_global_v4(dst + q4 * 16, pk[4 * q4], pk[4 * q4 + 1], pk[4 * q4 + 2], pk[4 * q4 + 3]);
+                    } else {
+                        float *dst = p.part_o + prow * D + c;
+#pragma unroll
+                        for (int q8 = 0; q8 < 4; ++q8) {
+                            uint32_t w[8];
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(h[8 * q8 + e]);
+                            st_global_v8(dst + 8 * q8, w);
+                        }
+                    }
+                }
+            }
+            if (live && grp == 0) {
+                const float lse2 = L == 0.f ? -INFINITY : M + lg2_approx(L);
+                if (whole)
+                    p.lse[orow] = lse2 * 0.69314718055994531f;
+                else
+                    p.part_lse[prow] = lse2;
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(barRead);
+            gs0 += nk;
+            use0 += 2 * nk;
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    } else if (warp >= 4 && warp < 8 && *abort_flag) {
+        // This CTA gave up on a wait: NaN into every row it was given, its parts included
+        const int r = threadIdx.x - 128;
+        const float nan = __uint_as_float(~0u);
+        walk = share;
+        while (walk.next(p.s, g)) {
+            const int row = g.mt * kRowTile + r;
+            if (row >= p.s.rows || row % p.s.T >= g.len.t) continue;
+            if (g.k0 == 0 && g.k1 == g.len.nt) {
+                const size_t orow = (size_t)(g.b * p.s.Hkv + g.kvh) * p.s.rows + row;
+                for (int c = 0; c < D * 2; c += 16)
+                    st_global_v4(static_cast<uint8_t *>(p.o) + orow * D * 2 + c, ~0u, ~0u, ~0u, ~0u);
+                p.lse[orow] = nan;
+            } else {
+                const size_t prow = (size_t)part_slot(blockIdx.x, g.k0) * p.part_rows + r;
+                for (int c = 0; c < D; ++c) p.part_o[prow * D + c] = nan;
+                p.part_lse[prow] = nan;
+            }
+        }
+    }
+}
+
+// Joins the parts of the units that a cut crosses: o = sum_i 2^(lse_i - M) o_i / sum_i 2^(lse_i - M).
+// Block x handles the unit whose first cut is the start of CTA x, one warp a row; the parts are
+// added in the order of the keys.
+constexpr int kJoinWarps = 4;
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_constant__ TreeParams p, int grid)
+{
+    constexpr int PER = D / 32;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int k = blockIdx.x + 1;
+    int total, G;
+    TreeWalk w;
+    TreeSeg g;
+    // lengths are inputs of the call, not results of the kernel before: they may be read at once
+    find_share(p.s, p.least, lane, k, grid, &total, &G, &w);
+    if (k >= G || !w.next(p.s, g) || g.k0 == 0) return;
+    const int u0 = cut(total, G, k) - g.k0, u1 = u0 + g.len.nt;
+    if (cut(total, G, k - 1) > u0) return;            // an earlier cut of the same unit
+    int parts = 2;                                    // CTA k - 1's and CTA k's
+    while (k + parts - 1 < G && cut(total, G, k + parts - 1) < u1) ++parts;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    for (int r = blockIdx.y * kJoinWarps + warp; r < p.part_rows; r += gridDim.y * kJoinWarps) {
+        const int row = g.mt * kRowTile + r;
+        if (row >= p.s.rows || row % p.s.T >= g.len.t) continue;
+        auto prow = [&](int i) { return (size_t)part_slot(k - 1 + i, i) * p.part_rows + r; };
+        float M = -INFINITY;
+        for (int i = lane; i < parts; i += 32) M = fmaxf(M, p.part_lse[prow(i)]);
+#pragma unroll
+        for (int d = 16; d; d >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, d));
+        const float ms = M == -INFINITY ? 0.f : M;
+        float acc[PER], sum = 0.f;
+#pragma unroll
+        for (int e = 0; e < PER; ++e) acc[e] = 0.f;
+#pragma unroll 4
+        for (int i = 0; i < parts; ++i) {
+            const size_t at = prow(i);
+            const float f = ex2_approx(p.part_lse[at] - ms);
+            sum += f;
+            const float *src = p.part_o + at * D + lane * PER;
+#pragma unroll
+            for (int e = 0; e < PER; ++e) acc[e] = fmaf(f, src[e], acc[e]);
+        }
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        const size_t orow = (size_t)(g.b * p.s.Hkv + g.kvh) * p.s.rows + row;
+        uint32_t pk[PER / 2];
+#pragma unroll
+        for (int e = 0; e < PER / 2; ++e) pk[e] = pack2<BF16>(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+        uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(p.o) + (orow * D + lane * PER) * 2);
+#pragma unroll
+        for (int e = 0; e < PER / 2; ++e) dst[e] = pk[e];
+        if (lane == 0) p.lse[orow] = sum == 0.f ? -INFINITY : (M + lg2_approx(sum)) * 0.69314718055994531f;
+    }
+}
+
+template <int D, bool BF16>
+cudaError_t launch_one(const TreeMaps &m, const TreeParams &p0, cudaStream_t st)
+{
+    auto kern = tree_kernel<D, BF16>;
+    static std::atomic<uint64_t> configured{0};
+    static std::atomic<int> sm_count[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    const uint64_t bit = 1ull << dev;
+    if (!(configured.load(std::memory_order_acquire) & bit)) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::ALLOC);
+        if (e != cudaSuccess) return e;
+        int nsm = 0;
+        e = cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev);
+        if (e != cudaSuccess) return e;
+        sm_count[dev].store(nsm, std::memory_order_relaxed);
+        configured.fetch_or(bit, std::memory_order_acq_rel);
+    }
+    TreeParams p = p0;
+    if (p.timeout_ns == 0) p.timeout_ns = kDefaultTimeoutNs;
+    const int grid = clampi(sm_count[dev].load(std::memory_order_relaxed), 1, kMaxCtas);
+    kern<<<grid, Cfg<D>::THREADS, Cfg<D>::ALLOC, st>>>(m, p);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || grid == 1) return e;
+    // the joining kernel is launched while the first one runs and waits for its end on the device
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid - 1, clampi(cdiv(p.part_rows, kJoinWarps), 1, 32));
+    cfg.blockDim = dim3(32 * kJoinWarps);
+    cfg.stream = st;
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, join_kernel<D, BF16>, p, grid);
+}
+
+} // namespace
+
+int tree_keys(int D) { return D == 256 ? 64 : 128; }
+
+cudaError_t launch_tree(int D, bool bf16, const TreeMaps &m, const TreeParams &p, cudaStream_t st)
+{
+    if (D == 64) return bf16 ? launch_one<64, true>(m, p, st) : launch_one<64, false>(m, p, st);
+    if (D == 128) return bf16 ? launch_one<128, true>(m, p, st) : launch_one<128, false>(m, p, st);
+    if (D == 256) return bf16 ? launch_one<256, true>(m, p, st) : launch_one<256, false>(m, p, st);
+    return cudaErrorInvalidValue;
+}
+
+cudaError_t read_and_clear_tree_status(uint32_t *word)
+{
+    unsigned int w = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(&w, g_tree_status, sizeof(w));
+    if (e != cudaSuccess) return e;
+    const unsigned int zero = 0;
+    e = cudaMemcpyToSymbol(g_tree_status, &zero, sizeof(zero));
+    if (word) *word = w;
+    return e;
+}
+
+} // namespace cache
+} // namespace fa

@@ -1,0 +1,119 @@
+// Host-side check of csrc/cache_schedule.h, built and run by tests/test_cache_cpu.py: under random
+// shapes, every step of every unit is given to exactly one CTA, CTAs get equal shares, the parts of a
+// cut unit lie in slots that no other part uses, and they are the parts that the joining kernel adds.
+#include <cstdio>
+#include <cstdlib>
+#include <map>
+#include <set>
+#include <vector>
+
+#include "cache_schedule.h"
+
+using namespace fa::cache;
+
+static int fail(const char *what) { std::printf("FAILED: %s\n", what); return 1; }
+
+static unsigned rnd(unsigned n) { return (unsigned)rand() % n; }
+
+// What find_share of the kernel computes, one sequence at a time.
+static TreeWalk share(const TreeShape &s, int least, int grid, int cta, int *total_out, int *G_out)
+{
+    int total = 0;
+    for (int b = 0; b < s.B; ++b) total += s.Hkv * s.mtiles * tree_len(s, b).nt;
+    const int G = ctas(total, grid, least);
+    const int begin = cta < G ? cut(total, G, cta) : total;
+    TreeWalk w{0, begin, cta < G ? cut(total, G, cta + 1) - begin : 0};
+    *total_out = total;
+    *G_out = G;
+    return w;
+}
+
+static int check_tree()
+{
+    for (int round = 0; round < 400; ++round) {
+        std::vector<int32_t> len(1 + rnd(9)), draft(len.size());
+        TreeShape s;
+        s.B = (int)len.size();
+        s.Hkv = 1 + rnd(4);
+        s.T = 1 + rnd(200);
+        s.rows = s.T * (1 + rnd(4));
+        s.mtiles = cdiv(s.rows, 128);
+        s.BN = rnd(2) ? 128 : 64;
+        s.capacity = 16 * (1 + rnd(300));
+        for (size_t b = 0; b < len.size(); ++b) {
+            len[b] = (int)rnd(s.capacity + 40) - 20;   // out of range on both sides, too
+            draft[b] = (int)rnd(s.T + 4) - 2;
+        }
+        s.seq_len = len.data();
+        s.draft_len = rnd(4) ? draft.data() : nullptr;
+        const int grid = 1 + rnd(160), least = 1 + rnd(4);
+        std::map<long long, std::vector<int>> unit;          // (b, kvh, mt) -> owner of each step
+        std::map<long long, std::vector<std::pair<int, int>>> parts;   // -> (k0, slot) of its parts
+        std::set<int> used;
+        int total = 0, G = 0, given = 0, most = 0, fewest = 1 << 30;
+        for (int c = 0; c < grid; ++c) {
+            TreeWalk w = share(s, least, grid, c, &total, &G);
+            int mine = 0;
+            TreeSeg g;
+            while (w.next(s, g)) {
+                const long long id = ((long long)g.b * s.Hkv + g.kvh) * s.mtiles + g.mt;
+                if (g.len.nt <= 0 || g.k0 < 0 || g.k1 <= g.k0 || g.k1 > g.len.nt || g.kvh >= s.Hkv || g.mt >= s.mtiles)
+                    return fail("a segment outside its unit");
+                auto &own = unit[id];
+                own.resize(g.len.nt, -1);
+                for (int k = g.k0; k < g.k1; ++k) {
+                    if (own[k] != -1) return fail("a step given twice");
+                    own[k] = c;
+                }
+                if (!(g.k0 == 0 && g.k1 == g.len.nt)) {
+                    const int slot = part_slot(c, g.k0);
+                    if (!used.insert(slot).second || slot >= 2 * grid) return fail("a part's slot");
+                    parts[id].push_back({g.k0, slot});
+                }
+                mine += g.k1 - g.k0;
+            }
+            if (c < G) {
+                most = mine > most ? mine : most;
+                fewest = mine < fewest ? mine : fewest;
+            } else if (mine) {
+                return fail("work behind the last CTA");
+            }
+            given += mine;
+        }
+        if (given != total) return fail("steps that nobody has");
+        if (total && most - fewest > 1) return fail("unequal shares");
+        size_t units = 0;
+        for (int b = 0; b < s.B; ++b) units += tree_len(s, b).nt ? (size_t)s.Hkv * s.mtiles : 0;
+        if (unit.size() != units) return fail("units that nobody has");
+        for (auto &u : unit)
+            for (int o : u.second)
+                if (o < 0) return fail("a step that nobody has");
+        // the joining kernel's view: block k of cut k
+        size_t joined = 0;
+        for (int k = 1; k < grid; ++k) {
+            int t2, G2;
+            TreeWalk w = share(s, least, grid, k, &t2, &G2);
+            TreeSeg g;
+            if (k >= G2 || !w.next(s, g) || g.k0 == 0) continue;
+            const int u0 = cut(t2, G2, k) - g.k0, u1 = u0 + g.len.nt;
+            if (cut(t2, G2, k - 1) > u0) continue;
+            int n = 2;
+            while (k + n - 1 < G2 && cut(t2, G2, k + n - 1) < u1) ++n;
+            const auto &want = parts[((long long)g.b * s.Hkv + g.kvh) * s.mtiles + g.mt];
+            if ((int)want.size() != n) return fail("the number of parts");
+            for (int i = 0; i < n; ++i)
+                if (part_slot(k - 1 + i, i) != want[i].second) return fail("the order of the parts");
+            ++joined;
+        }
+        if (joined != parts.size()) return fail("a cut unit that is not joined");
+    }
+    return 0;
+}
+
+int main()
+{
+    srand(1);
+    if (check_tree()) return 1;
+    std::printf("ok\n");
+    return 0;
+}
