@@ -314,6 +314,48 @@ int fa_cache_append(const fa_cache_t *cache, const void *k_new, const void *v_ne
                     const int32_t *count, const int32_t *start, float *weight, int32_t *pos, int T,
                     fa_stream_t stream);
 
+/*
+ * fa_cache_weights -- adds to each slot the attention weight that it receives from a set of queries:
+ *   out[b,c,s] = weight[b,c,s] + sum over the query heads h of KV head c and the rows i < count[b] that see s
+ *                of exp(scale q[b,h,t_i,:].k_s - lse[b,h,t_i]),      s < seq_len[b],
+ * t_i = path[b,i] (i without a path).  With causal 1 row i is the query of slot seq_len[b] - count[b] + i and sees
+ * the slots up to its own (a prompt, or drafted tokens after their append); with causal 0 it sees all.
+ *   q        [B, Hq, T, D] in the cache's type, lse [B, Hq, T] float32, as the attention left it: the softmax is
+ *            not computed again.  A row with lse = -inf saw nothing and adds nothing
+ *   path     [B, T] indices into the T rows of q and lse, or NULL.  An index outside [0, T) adds nothing
+ *   count    [B] (clamped to [0, T]), or NULL (without a path): T
+ *   weight   [B, Hkv, capacity] float32 or NULL (zero); out the same, and may be weight.  Slots at or
+ *            behind seq_len[b] are left as they were
+ *   scale    > 0 and finite;  T >= 1
+ *   workspace  fa_weights_workspace_bytes() bytes, 16-byte aligned; needs no initial value
+ * Sums are float32 in a fixed order: the result does not vary from run to run.
+ */
+size_t fa_weights_workspace_bytes(void);
+int fa_cache_weights(const fa_cache_t *cache, const void *q, const float *lse, const int32_t *path,
+                     const int32_t *count, const float *weight, float *out, int Hq, int T, int causal,
+                     float scale, void *workspace, size_t workspace_bytes, fa_stream_t stream);
+
+/*
+ * fa_cache_evict -- shrinks every (sequence, KV head) that uses more than `keep` slots to `keep`: it keeps the
+ * slots with a position below `first` or at or above next_pos[b] - last, then those of the largest
+ * weight (NaN counts as larger than any number), of equal ones the lowest slot.  Kept slots at or above `keep`, in
+ * order, move to the freed slots below it, in order: their key, value, weight and position.  A
+ * kept slot below `keep` stays where it is, so slots are not in the order of their positions afterwards;
+ * attention over a cache does not depend on the order, and pos says which token a slot holds.
+ *   weight, pos           [B, Hkv, capacity] float32, int32
+ *   weight_out, pos_out   the same for the slots kept, [0, min(seq_len[b], keep)); may be weight and pos.
+ *                         Other slots are left as they were
+ *   new_len               [B]: min(seq_len[b], keep).  Not seq_len itself (the layers of a model share it)
+ *   next_pos              [B] the position of the next token; required when last > 0
+ *   keep >= 1, first, last >= 0, first + last <= keep
+ *   workspace             fa_evict_workspace_bytes(B, Hkv, capacity, keep) bytes
+ * Keys and values are moved within the cache's pages; pages that new_len does not cover are free.
+ */
+size_t fa_evict_workspace_bytes(int B, int Hkv, int capacity, int keep);
+int fa_cache_evict(const fa_cache_t *cache, const float *weight, const int32_t *pos, float *weight_out,
+                   int32_t *pos_out, int32_t *new_len, const int32_t *next_pos, int keep, int first, int last,
+                   void *workspace, size_t workspace_bytes, fa_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -15,7 +15,9 @@ def __getattr__(name):
                 "softmax_rows"):
         from . import binding
         return getattr(binding, name)
-    if name in ("KVCache", "tree_attention", "tree_workspace_bytes", "cache_append"):
+    if name in ("KVCache", "tree_attention", "tree_workspace_bytes", "cache_append", "cache_weights",
+                "weights_workspace_bytes", "cache_evict", "evict_workspace_bytes"):
         from . import cache
-        return getattr(cache, name)
+        globals()[name] = value = getattr(cache, name)
+        return value
     raise AttributeError(name)

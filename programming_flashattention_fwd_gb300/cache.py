@@ -1,7 +1,8 @@
 """Operators of a paged key/value cache: argument marshalling over libfa_gb300.so.
 
 ``KVCache`` names the tensors of one layer's cache; ``tree_attention`` attends drafted tokens over
-it, ``cache_append`` writes accepted tokens.  include/fa.h defines each operator; as in
+it, ``cache_append`` writes accepted tokens, ``cache_weights`` adds up the attention that each slot
+receives and ``cache_evict`` shrinks the cache by it.  include/fa.h defines each operator; as in
 ``binding``, every step of the computation runs in the library's CUDA kernels and a non-zero
 status raises ``FaError``.
 """
@@ -32,6 +33,10 @@ _SIGNATURES = {
     "fa_tree_workspace_bytes": (_Z, [_I] * 4),
     "fa_tree_fwd": (_I, [_CP] + [_P] * 7 + [_I, _I, _F, _P, _Z, _P]),
     "fa_cache_append": (_I, [_CP] + [_P] * 7 + [_I, _P]),
+    "fa_weights_workspace_bytes": (_Z, []),
+    "fa_cache_weights": (_I, [_CP] + [_P] * 6 + [_I, _I, _I, _F, _P, _Z, _P]),
+    "fa_evict_workspace_bytes": (_Z, [_I] * 4),
+    "fa_cache_evict": (_I, [_CP] + [_P] * 6 + [_I, _I, _I, _P, _Z, _P]),
 }
 _lib = None
 
@@ -188,3 +193,69 @@ def cache_append(cache: KVCache, k_new, v_new, path=None, count=None, weight=Non
     lib = _library()
     with _OnDevice(dev):
         _run(lib.fa_cache_append(cache._ref, *args, T, _stream_handle(stream)))
+
+
+def weights_workspace_bytes() -> int:
+    """Bytes of the workspace of ``cache_weights``."""
+    return _library().fa_weights_workspace_bytes()
+
+
+def cache_weights(cache: KVCache, q, lse, weight=None, path=None, count=None, causal: bool = True,
+                  scale: Optional[float] = None, out=None, workspace=None, stream=None) -> torch.Tensor:
+    """Adds to each slot the attention weight that it receives from the rows of q (fa_cache_weights).
+
+    q [B, Hq, T, D], lse [B, Hq, T] as the attention left it; path [B, T] and count [B] int32 as in
+    ``cache_append`` (the accepted rows); causal: row i is the query of slot seq_len[b] - count[b] + i
+    and sees the slots up to its own.  weight [B, Hkv, capacity] float32 (None: zeros) is added to; the
+    result is written to out, which defaults to weight itself (without a weight, to a new tensor of zeros)."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 4:
+        raise ValueError("q must be a [B, Hq, T, D] tensor")
+    dev = cache.device
+    B, Hq, T, D = q.shape
+    if B != cache.B or D != cache.D:
+        raise ValueError(f"q must have the cache's {cache.B} sequences and head dimension {cache.D}")
+    if path is not None and count is None:
+        raise ValueError("a path needs count")
+    slots = (B, cache.Hkv, cache.capacity)
+    if out is None:
+        out = torch.zeros(slots, dtype=torch.float32, device=dev) if weight is None else weight
+    args = (_need("q", q, q.shape, cache.dtype, dev), _need("lse", lse, (B, Hq, T), torch.float32, dev),
+            _maybe("path", path, (B, T), torch.int32, dev), _maybe("count", count, (B,), torch.int32, dev),
+            _maybe("weight", weight, slots, torch.float32, dev), _need("out", out, slots, torch.float32, dev))
+    _check_stream_device(stream, dev)
+    lib = _library()
+    ws, size = _workspace(lib.fa_weights_workspace_bytes(), workspace, dev, stream)
+    with _OnDevice(dev):
+        _run(lib.fa_cache_weights(cache._ref, *args, Hq, T, int(bool(causal)), 1.0 / math.sqrt(D) if scale is None else scale,
+                                  ws.data_ptr(), size, _stream_handle(stream)))
+    return out
+
+
+def evict_workspace_bytes(B: int, Hkv: int, capacity: int, keep: int) -> int:
+    """Bytes of the workspace of ``cache_evict``."""
+    return _library().fa_evict_workspace_bytes(B, Hkv, capacity, keep)
+
+
+def cache_evict(cache: KVCache, weight, pos, keep: int, first: int = 0, last: int = 0, next_pos=None, weight_out=None,
+                pos_out=None, new_len=None, workspace=None, stream=None) -> torch.Tensor:
+    """Shrinks every sequence and KV head to `keep` slots (fa_cache_evict): the positions below `first`
+    and from next_pos[b] - last on are kept, then the slots of the largest weight (ties: the lowest slot);
+    kept slots at or above `keep` move to the freed ones below.  weight [B, Hkv, capacity] float32 and
+    pos int32 follow the slots, in place unless weight_out and pos_out are given.  Returns new_len [B]
+    int32 = min(seq_len, keep); seq_len itself is not changed."""
+    dev = cache.device
+    slots = (cache.B, cache.Hkv, cache.capacity)
+    if last and next_pos is None:
+        raise ValueError("last needs next_pos")
+    if new_len is None:
+        new_len = torch.empty(cache.B, dtype=torch.int32, device=dev)
+    w, p = _need("weight", weight, slots, torch.float32, dev), _need("pos", pos, slots, torch.int32, dev)
+    args = (w, p, w if weight_out is None else _need("weight_out", weight_out, slots, torch.float32, dev),
+            p if pos_out is None else _need("pos_out", pos_out, slots, torch.int32, dev),
+            _need("new_len", new_len, (cache.B,), torch.int32, dev), _maybe("next_pos", next_pos, (cache.B,), torch.int32, dev))
+    _check_stream_device(stream, dev)
+    lib = _library()
+    ws, size = _workspace(lib.fa_evict_workspace_bytes(cache.B, cache.Hkv, cache.capacity, keep), workspace, dev, stream)
+    with _OnDevice(dev):
+        _run(lib.fa_cache_evict(cache._ref, *args, keep, first, last, ws.data_ptr(), size, _stream_handle(stream)))
+    return new_len

@@ -115,7 +115,11 @@ namespace fa {
 
 cudaError_t read_and_clear_cache_status(uint32_t *word)
 {
-    return cache::read_and_clear_tree_status(word);
+    uint32_t tree = 0, weigh = 0;
+    cudaError_t e = cache::read_and_clear_tree_status(&tree);
+    if (e == cudaSuccess) e = cache::read_and_clear_weigh_status(&weigh);
+    *word = (tree & 1u) ? tree : weigh;
+    return e;
 }
 
 } // namespace fa
@@ -234,6 +238,124 @@ int fa_cache_append(const fa_cache_t *cache, const void *k_new, const void *v_ne
     p.chunks = D / 8;
     p.blocks_per_head = (int)tiles;
     return launch_append(p, (int)blocks, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
+}
+
+size_t fa_weights_workspace_bytes(void) { return (size_t)2 * kMaxCtas * 128 * 4; }
+
+int fa_cache_weights(const fa_cache_t *cache, const void *q, const float *lse, const int32_t *path, const int32_t *count,
+                     const float *weight, float *out, int Hq, int T, int causal, float scale, void *workspace,
+                     size_t workspace_bytes, fa_stream_t stream)
+{
+    int st = check_cache(cache);
+    if (st != FA_OK) return st;
+    const int B = cache->B, Hkv = cache->Hkv, D = cache->D;
+    if (T < 0) return FA_ERR_BAD_DIM;
+    if (Hq < 1 || Hq % Hkv != 0) return FA_ERR_HEADS;
+    if (!(std::isfinite(scale) && scale > 0.f)) return FA_ERR_SCALE;
+    if (causal != 0 && causal != 1) return FA_ERR_CAUSAL;
+    const int group = Hq / Hkv, NQ = weigh_rows(D), cap = cache->max_pages * cache->page;
+    if (B == 0 || cap == 0) return FA_OK;
+    if (T == 0) return FA_ERR_BAD_DIM;
+    const long long rows = (long long)group * T, kt = ((long long)cap + 127) / 128;
+    if (rows > 0x7fffffffLL - 128 || (double)B * Hq > 2147483647.0 ||
+        (double)B * Hkv * kt * ((double)group * ((T + NQ - 1) / NQ) + 1) > 2147483647.0)
+        return FA_ERR_BAD_DIM;
+    st = check_cache_pointers(cache);
+    if (st != FA_OK) return st;
+    if (!q || !lse || !out || !workspace || (path && !count)) return FA_ERR_NULL_PTR;
+    if (!aligned(q, 16) || !aligned(lse, 4) || !aligned(path, 4) || !aligned(count, 4) || !aligned(weight, 4) || !aligned(out, 4) ||
+        !aligned(workspace, 16))
+        return FA_ERR_ALIGN;
+    const size_t need = fa_weights_workspace_bytes();
+    if (workspace_bytes < need) return FA_ERR_TOO_LARGE;
+    const size_t nq = (size_t)B * Hq * T * D * 2, ns = (size_t)B * Hkv * cap * 4;
+    const Range all[] = {range(out, ns), range(workspace, need), range(q, nq), range(lse, (size_t)B * Hq * T * 4),
+                         range(cache->k, pool_bytes(cache)), range(cache->v, pool_bytes(cache)),
+                         range(cache->table, (size_t)B * cache->max_pages * 4), range(cache->seq_len, (size_t)B * 4),
+                         range(path, (size_t)B * T * 4), range(count, (size_t)B * 4),
+                         range(weight, weight == out ? 0 : ns)};   // in place is fine, a partial overlap is not
+    if (clash(all, sizeof(all) / sizeof(all[0]), 2)) return FA_ERR_ALIAS;
+    st = fa::check_device();
+    if (st != FA_OK) return st;
+
+    const bool bf16 = cache->dtype == 0;
+    WeighParams p;
+    std::memset(&p, 0, sizeof(p));
+    const int mode = path ? kPath : (T >= 128 ? kHeads : kRows);
+    p.s = WeighShape{B, Hkv, group, T, mode, causal, NQ, cap, cache->seq_len, count};
+    p.pages = pages_of(cache);
+    p.q = q;
+    p.lse = lse;
+    p.path = path;
+    p.weight = weight;
+    p.out = out;
+    p.part = static_cast<float *>(workspace);
+    p.box_rows = gcd(cache->page, 128);
+    p.least = 1;
+    p.sl2 = (float)((double)scale * 1.4426950408889634);
+    WeighMaps m;
+    std::memset(&m, 0, sizeof(m));
+    const long long eh[3] = {D, T, (long long)B * Hq}, er[3] = {D, rows, (long long)B * Hkv};
+    if (!encode(&m.q, q, bf16, 3, mode == kHeads ? eh : er, NQ) || !encode_pool(&m.k, cache->k, q, cache, p.box_rows))
+        return FA_ERR_TENSORMAP;
+    return launch_weigh(D, bf16, m, p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
+}
+
+size_t fa_evict_workspace_bytes(int B, int Hkv, int capacity, int keep)
+{
+    if (B < 1 || Hkv < 1 || keep < 1 || capacity <= keep) return 0;
+    return (size_t)B * Hkv * 2 * (keep < capacity - keep ? keep : capacity - keep) * 4;
+}
+
+int fa_cache_evict(const fa_cache_t *cache, const float *weight, const int32_t *pos, float *weight_out, int32_t *pos_out,
+                   int32_t *new_len, const int32_t *next_pos, int keep, int first, int last, void *workspace,
+                   size_t workspace_bytes, fa_stream_t stream)
+{
+    int st = check_cache(cache);
+    if (st != FA_OK) return st;
+    const int B = cache->B, Hkv = cache->Hkv, cap = cache->max_pages * cache->page;
+    if (keep < 1 || first < 0 || last < 0 || (long long)first + last > keep) return FA_ERR_BAD_DIM;
+    if (B == 0) return FA_OK;
+    if ((long long)B * Hkv * 8 > 0x7fffffffLL || (double)keep * cache->D > 8.0 * 2147483647.0 - 65536.0) return FA_ERR_BAD_DIM;
+    st = check_cache_pointers(cache);
+    if (st != FA_OK) return st;
+    const size_t need = fa_evict_workspace_bytes(B, Hkv, cap, keep);
+    if (!new_len || (cap > 0 && (!weight || !pos || !weight_out || !pos_out)) || (last > 0 && !next_pos) || (need && !workspace))
+        return FA_ERR_NULL_PTR;
+    if (!aligned(weight, 4) || !aligned(pos, 4) || !aligned(weight_out, 4) || !aligned(pos_out, 4) || !aligned(new_len, 4) ||
+        !aligned(next_pos, 4) || !aligned(workspace, 4))
+        return FA_ERR_ALIGN;
+    if (workspace_bytes < need) return FA_ERR_TOO_LARGE;
+    const size_t ns = (size_t)B * Hkv * cap * 4;
+    const Range all[] = {range(cache->k, pool_bytes(cache)), range(cache->v, pool_bytes(cache)), range(weight_out, ns), range(pos_out, ns),
+                         range(new_len, (size_t)B * 4), range(workspace, need), range(weight, weight == weight_out ? 0 : ns),
+                         range(pos, pos == pos_out ? 0 : ns), range(cache->table, (size_t)B * cache->max_pages * 4),
+                         range(cache->seq_len, (size_t)B * 4), range(next_pos, (size_t)B * 4)};
+    if (clash(all, sizeof(all) / sizeof(all[0]), 6)) return FA_ERR_ALIAS;
+    st = fa::check_device();
+    if (st != FA_OK) return st;
+    EvictParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.pages = pages_of(cache);
+    p.k = static_cast<uint4 *>(cache->k);
+    p.v = static_cast<uint4 *>(cache->v);
+    p.seq_len = cache->seq_len;
+    p.weight = weight;
+    p.pos = pos;
+    p.next_pos = next_pos;
+    p.weight_out = weight_out;
+    p.pos_out = pos_out;
+    p.new_len = new_len;
+    p.moves = static_cast<int32_t *>(workspace);
+    p.longest = keep < cap - keep ? keep : cap - keep;
+    p.B = B;
+    p.Hkv = Hkv;
+    p.capacity = cap;
+    p.chunks = cache->D / 8;
+    p.keep = keep;
+    p.first = first;
+    p.last = last;
+    return launch_evict(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
 }
 
 } // extern "C"

@@ -1,0 +1,74 @@
+// cache_device.cuh -- device code that the cache kernels share: finding a CTA's share of the work and
+// the pages of a step's copies.
+#pragma once
+#include <cstdint>
+
+#include "cache_internal.h"
+#include "ptx.cuh"
+
+namespace fa {
+namespace cache {
+
+struct Share {
+    int total, G;         // all steps, the CTAs that have some
+    int b, off, left;     // this CTA's: `left` steps from step `off` of sequence b
+};
+
+// CTA `cta`'s share of the line of steps, steps(b) of them in sequence b: one warp adds up the
+// lengths and finds the sequence that holds the share's first step.
+template <typename Steps>
+__device__ __forceinline__ Share find_share(int B, int least, int lane, int cta, int grid, Steps steps)
+{
+    Share s;
+    int sum = 0;
+    for (int b = lane; b < B; b += 32) sum += steps(b);
+#pragma unroll
+    for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
+    s.total = sum;
+    s.G = ctas(sum, grid, least);
+    const int begin = cta < s.G ? cut(sum, s.G, cta) : sum;
+    s.left = cta < s.G ? cut(sum, s.G, cta + 1) - begin : 0;
+    int before = 0;   // steps of the sequences before s.b
+    for (s.b = 0; s.b < B; s.b += 32) {
+        const int b = s.b + lane;
+        const int mine = b < B ? steps(b) : 0;
+        int upto = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int x = __shfl_up_sync(~0u, upto, d);
+            if (lane >= d) upto += x;
+        }
+        const uint32_t past = __ballot_sync(~0u, before + upto > begin);
+        if (past) {
+            const int src = __ffs(past) - 1;
+            s.b += src;
+            before += __shfl_sync(~0u, upto - mine, src);
+            break;
+        }
+        before += __shfl_sync(~0u, upto, 31);
+    }
+    s.off = begin - before;
+    return s;
+}
+
+// Page and row of slot `slot` of sequence b; a page that does not exist is given the number past the
+// last, which a tensor map reads as zeros.
+__device__ __forceinline__ void page_of(const Pages &pg, int b, int slot, int &pid, int &row)
+{
+    const int at = slot / pg.page;
+    row = slot - at * pg.page;
+    pid = pg.table ? __ldg(pg.table + (size_t)b * pg.max_pages + at) : b * pg.max_pages + at;
+    if (pid < 0 || pid >= pg.num_pages) pid = pg.num_pages;
+}
+
+// One box of a pool, (64 columns from x, box rows from `row`, KV head, page), global -> shared.
+__device__ __forceinline__ void load_page(uint32_t dst, const CUtensorMap *m, int x, int row, int kvh, int pid, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                 " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+                 "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(row), "r"(kvh), "r"(pid), "r"(bar)
+                 : "memory");
+}
+
+} // namespace cache
+} // namespace fa

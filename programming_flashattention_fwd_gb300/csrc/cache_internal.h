@@ -45,6 +45,30 @@ int tree_keys(int D);        // keys per step
 cudaError_t launch_tree(int D, bool bf16, const TreeMaps &m, const TreeParams &p, cudaStream_t st);
 cudaError_t read_and_clear_tree_status(uint32_t *word);
 
+// ---------------------------------------------------------------- accumulated attention weight
+struct WeighParams {
+    WeighShape s;
+    Pages pages;
+    const void *q;            // [B, Hq, T, D], read directly in kPath mode
+    const float *lse;         // [B, Hq, T]
+    const int32_t *path;      // [B, T] (kPath)
+    const float *weight;      // [B, Hkv, capacity] or null: zero
+    float *out;               // [B, Hkv, capacity]
+    float *part;              // [2 * kMaxCtas][128]
+    int box_rows;
+    int least;
+    float sl2;
+    uint64_t timeout_ns;
+};
+
+struct WeighMaps {
+    CUtensorMap k, q;         // q: (D, rows of a plane, planes), not used in kPath mode
+};
+
+int weigh_rows(int D);        // query rows of a step
+cudaError_t launch_weigh(int D, bool bf16, const WeighMaps &m, const WeighParams &p, cudaStream_t st);
+cudaError_t read_and_clear_weigh_status(uint32_t *word);
+
 // ---------------------------------------------------------------- writing the cache
 struct AppendParams {
     Pages pages;
@@ -61,6 +85,25 @@ struct AppendParams {
 };
 cudaError_t launch_append(const AppendParams &p, int blocks, cudaStream_t st);
 int append_tokens(int D);          // tokens of one block
+
+// ---------------------------------------------------------------- eviction
+struct EvictParams {
+    Pages pages;
+    uint4 *k, *v;                    // [num_pages, Hkv, page, D]
+    const int32_t *seq_len;          // [B]
+    const float *weight;             // [B, Hkv, capacity]
+    const int32_t *pos;              // [B, Hkv, capacity]
+    const int32_t *next_pos;         // [B] or null when last == 0
+    float *weight_out;               // may be weight
+    int32_t *pos_out;                // may be pos
+    int32_t *new_len;                // [B]
+    int32_t *moves;                  // [B * Hkv][2][longest]: freed slots, then the slots that move there
+    int longest;                     // min(keep, capacity - keep)
+    int B, Hkv, capacity, chunks;    // chunks: 16-byte chunks of a row
+    int keep, first, last;
+    int held;                        // keys of a CTA's slots held in shared memory
+};
+cudaError_t launch_evict(const EvictParams &p, cudaStream_t st);
 
 } // namespace cache
 

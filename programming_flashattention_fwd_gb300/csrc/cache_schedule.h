@@ -92,5 +92,128 @@ struct TreeWalk {
 // it starts in the middle of (slot 2 c) and the unit it leaves unfinished (slot 2 c + 1).
 __host__ __device__ __forceinline__ int part_slot(int c, int k0) { return 2 * c + (k0 == 0 ? 1 : 0); }
 
+// ---------------------------------------------------------------- accumulated attention weight
+// A unit is one 128-slot key tile of (sequence, KV head); its steps are the tiles of NQ query rows
+// that see any of it.  The rows come in `planes` of a KV head:
+//   heads    one plane a query head, rows in the order of their slots: with the causal mask the tiles
+//            before the first row that sees the key tile are left out (long prompts)
+//   rows     one plane with the rows of all heads of the group, head after head (short prompts)
+//   path     one plane with the accepted rows only, gathered by index, head after head
+enum WeighMode { kHeads = 0, kRows = 1, kPath = 2 };
+
+struct WeighShape {
+    int B, Hkv, group, T;
+    int mode, causal;
+    int NQ;                      // query rows of a step
+    int capacity;
+    const int32_t *seq_len;      // [B]
+    const int32_t *count;        // [B] or null: T
+};
+
+struct WeighLen {
+    int n, a;        // slots in use, query rows of a head
+    int off;         // row i sees the slots below off + i + 1 (causal)
+    int kt;          // units of a KV head: key tiles
+    int rows, qt;    // rows of a plane, their tiles
+    int planes;
+    int per;         // tiles by which the first tile moves on from one key tile to the next (0: never)
+    int w;           // key tile k starts at query tile max(0, per * k - w)
+};
+
+__host__ __device__ __forceinline__ WeighLen weigh_len(const WeighShape &s, int b)
+{
+    WeighLen l;
+    l.n = clampi(s.seq_len[b], 0, s.capacity);
+    l.a = s.count ? clampi(s.count[b], 0, s.T) : s.T;
+    l.off = l.n - l.a;
+    l.kt = cdiv(l.n, 128);
+    l.planes = s.mode == kHeads ? s.group : 1;
+    l.rows = l.a == 0 ? 0 : (s.mode == kHeads ? l.a : (s.mode == kPath ? s.group * l.a : s.group * s.T));
+    l.qt = cdiv(l.rows, s.NQ);
+    l.per = s.mode == kHeads && s.causal ? 128 / s.NQ : 0;
+    l.w = l.off >= 0 ? cdiv(l.off, s.NQ) : -((-l.off) / s.NQ);   // ceil(off / NQ)
+    return l;
+}
+
+// First query tile of key tile k.
+__host__ __device__ __forceinline__ int weigh_first(const WeighLen &l, int k)
+{
+    const int t = l.per * k - l.w;
+    return l.per && t > 0 ? t : 0;
+}
+
+// Steps of key tile k; a key tile that no row sees has one, which adds nothing.
+__host__ __device__ __forceinline__ int weigh_steps(const WeighLen &l, int k)
+{
+    return l.qt == 0 ? 1 : l.planes * (l.qt - weigh_first(l, k));
+}
+
+// Steps of the key tiles before k: with the first tile at max(0, per i - w), an arithmetic series.
+__host__ __device__ __forceinline__ int weigh_before(const WeighLen &l, int k)
+{
+    if (l.qt == 0) return k;
+    long long skipped = 0;
+    if (l.per) {
+        const int i0 = l.w <= 0 ? 0 : cdiv(l.w, l.per);   // first key tile with per i >= w
+        if (k > i0) {
+            const long long m = k - i0;
+            skipped = (long long)l.per * (i0 + (k - 1)) * m / 2 - (long long)l.w * m;
+        }
+    }
+    return (int)(l.planes * ((long long)k * l.qt - skipped));
+}
+
+// One CTA's share of one unit: steps [s0, s1) of the ns of key tile kt.
+struct WeighSeg {
+    int b, kvh, kt, s0, s1, ns, first;
+    WeighLen len;
+
+    // the plane and the query tile of step s
+    __host__ __device__ __forceinline__ void tile(int s, int &plane, int &qt) const
+    {
+        const int per = len.qt - first;
+        plane = per > 0 ? s / per : 0;
+        qt = per > 0 ? first + s - plane * per : 0;
+    }
+};
+
+struct WeighWalk {
+    int b, off, left;   // `left` steps from step `off` of sequence b
+
+    __host__ __device__ __forceinline__ bool next(const WeighShape &s, WeighSeg &g)
+    {
+        while (left > 0 && b < s.B) {
+            const WeighLen l = weigh_len(s, b);
+            const int one = weigh_before(l, l.kt), per = s.Hkv * one;
+            if (off >= per) {
+                off -= per;
+                ++b;
+                continue;
+            }
+            g.kvh = off / one;
+            const int in = off - g.kvh * one;
+            int lo = 0, hi = l.kt - 1;   // the key tile that holds step `in`
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) / 2;
+                if (weigh_before(l, mid) <= in)
+                    lo = mid;
+                else
+                    hi = mid - 1;
+            }
+            g.b = b;
+            g.kt = lo;
+            g.s0 = in - weigh_before(l, lo);
+            g.ns = weigh_steps(l, lo);
+            g.first = weigh_first(l, lo);
+            g.s1 = g.ns - g.s0 < left ? g.ns : g.s0 + left;
+            g.len = l;
+            off += g.s1 - g.s0;
+            left -= g.s1 - g.s0;
+            return true;
+        }
+        return false;
+    }
+};
+
 } // namespace cache
 } // namespace fa

@@ -34,6 +34,7 @@
 #include <atomic>
 #include <cstdint>
 
+#include "cache_device.cuh"
 #include "cache_internal.h"
 #include "ptx.cuh"
 #include "watchdog.cuh"
@@ -130,43 +131,8 @@ __device__ __forceinline__ void path_bits(const int32_t *parent, int t, int lo, 
     }
 }
 
-// This CTA's share: all steps are counted and the sequence that holds the first is found, by one warp.
-__device__ __forceinline__ void find_share(const TreeShape &s, int least, int lane, int cta, int grid, int *total_out,
-                                           int *G_out, TreeWalk *walk)
-{
-    const int U = s.Hkv * s.mtiles;
-    int total = 0;
-    for (int b = lane; b < s.B; b += 32) total += U * tree_len(s, b).nt;
-#pragma unroll
-    for (int d = 16; d; d >>= 1) total += __shfl_xor_sync(~0u, total, d);
-    const int G = ctas(total, grid, least);
-    const int begin = cta < G ? cut(total, G, cta) : total;
-    const int left = cta < G ? cut(total, G, cta + 1) - begin : 0;
-    int b0 = 0, before = 0;   // steps of the sequences before b0
-    for (; b0 < s.B; b0 += 32) {
-        const int b = b0 + lane;
-        const int mine = b < s.B ? U * tree_len(s, b).nt : 0;
-        int sum = mine;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int x = __shfl_up_sync(~0u, sum, d);
-            if (lane >= d) sum += x;
-        }
-        const uint32_t past = __ballot_sync(~0u, before + sum > begin);
-        if (past) {
-            const int src = __ffs(past) - 1;
-            b0 += src;
-            before += __shfl_sync(~0u, sum - mine, src);
-            break;
-        }
-        before += __shfl_sync(~0u, sum, 31);
-    }
-    walk->b = b0;
-    walk->off = begin - before;
-    walk->left = left;
-    *total_out = total;
-    *G_out = G;
-}
+// Steps of sequence b.
+__device__ __forceinline__ int tree_steps(const TreeShape &s, int b) { return s.Hkv * s.mtiles * tree_len(s, b).nt; }
 
 template <int D, bool BF16>
 __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
@@ -222,9 +188,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         tmem_relinquish();
     }
     if (warp == 3) {
-        TreeWalk w;
-        int total, G;
-        find_share(p.s, p.least, lane, blockIdx.x, gridDim.x, &total, &G, &w);
+        const Share w = find_share(p.s.B, p.least, lane, blockIdx.x, gridDim.x, [&](int b) { return tree_steps(p.s, b); });
         if (lane == 0) {
             misc->walk.b = w.b;
             misc->walk.off = w.off;
@@ -258,11 +222,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
             if (kt >= g.len.kc || box >= boxes) return;
             const int slot = kt * BN + box * p.box_rows;
             if (slot >= g.len.n) return;
-            const int at = slot / pg.page;
-            row = slot - at * pg.page;
-            pid = pg.table ? __ldg(pg.table + (size_t)g.b * pg.max_pages + at) : g.b * pg.max_pages + at;
-            // a page that does not exist reads as zeros (past the end of the tensor)
-            if (pid < 0 || pid >= pg.num_pages) pid = pg.num_pages;
+            page_of(pg, g.b, slot, pid, row);
         };
         auto load = [&](const TreeSeg &g, bool is_v, int kt, int pid, int row) -> bool {
             const int s = use % C::NS;
@@ -272,13 +232,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                 const int valid = min(boxes, cdiv(g.len.n - kt * BN, p.box_rows));
                 if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(valid * p.box_rows * 128 * C::PANELS));
                 __syncwarp();
-                if (pid >= 0) {
-                    const CUtensorMap *m = is_v ? &maps.v : &maps.k;
-                    asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-                                 " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst + box_off),
-                                 "l"(reinterpret_cast<uint64_t>(m)), "r"(pn * 64), "r"(row), "r"(g.kvh), "r"(pid), "r"(bar)
-                                 : "memory");
-                }
+                if (pid >= 0) load_page(dst + box_off, is_v ? &maps.v : &maps.k, pn * 64, row, g.kvh, pid, bar);
             } else {
                 if (lane == 0) mbar_arrive_expect_tx(bar, C::KVTILE);
                 __syncwarp();
@@ -696,11 +650,11 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
     constexpr int PER = D / 32;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int k = blockIdx.x + 1;
-    int total, G;
-    TreeWalk w;
-    TreeSeg g;
     // lengths are inputs of the call, not results of the kernel before: they may be read at once
-    find_share(p.s, p.least, lane, k, grid, &total, &G, &w);
+    const Share sh = find_share(p.s.B, p.least, lane, k, grid, [&](int b) { return tree_steps(p.s, b); });
+    const int total = sh.total, G = sh.G;
+    TreeWalk w{sh.b, sh.off, sh.left};
+    TreeSeg g;
     if (k >= G || !w.next(p.s, g) || g.k0 == 0) return;
     const int u0 = cut(total, G, k) - g.k0, u1 = u0 + g.len.nt;
     if (cut(total, G, k - 1) > u0) return;            // an earlier cut of the same unit

@@ -1,0 +1,528 @@
+// weigh_sm103.cu -- the attention weight that the slots of a cache have received (fa_cache_weights).
+//
+// For sequence b, KV head c and slot j of its n_b:
+//
+//     out[b, c, j] = weight[b, c, j] + sum_{h in c} sum_{i < count[b]} [j visible to i] exp(scale q_hi.k_j - lse_hi)
+//
+// where row i is the query of slot n_b - count[b] + i and, with the causal mask, sees the slots up to its
+// own.  The attention that made lse has left the probabilities behind, so one pass over Q K^T suffices:
+// no running maximum, no second product.
+//
+// The score tile is computed transposed, S^T = K Q^T: the keys are the 128 lanes of tensor memory and
+// the query rows its columns, so the sum over rows runs along the registers of one thread and no lanes
+// are joined.  One packed FMA, one exponential and one packed add a score: a long prompt is bound by the
+// tensor pipe and by the exponentials about equally (128 x 128 scores: 512 cycles of each at D = 128),
+// a drafting step by the one read of K.
+//
+// The steps (key tile x tile of query rows) are shared out evenly (cache_schedule.h).  A key tile that a
+// cut crosses leaves its parts in the workspace; a second kernel adds them in order, so the sums do
+// not vary from run to run.
+//
+// Per CTA (one per SM):
+//   warp 0        K producer (one box per page and panel) and, unless rows are gathered, Q producer
+//   warp 1        TMEM owner and MMA issuer, into four S^T buffers
+//   warps 2-3     lse and visible limit of each step's 128 rows; in path mode also the gathered Q tile
+//   warps 4-7,    the sums, one thread per key: the groups take alternate steps and are joined at the
+//   warps 8-11    end of a key tile
+// A K or Q tile stays where it is while consecutive steps use it.
+#include <atomic>
+#include <cstdint>
+
+#include "cache_device.cuh"
+#include "cache_internal.h"
+#include "ptx.cuh"
+#include "watchdog.cuh"
+
+namespace fa {
+
+__device__ unsigned int g_weigh_status;
+
+namespace cache {
+
+namespace {
+
+constexpr uint64_t kDefaultTimeoutNs = 2000000000ull;
+constexpr int THREADS = 384;
+constexpr int NB = 4;   // S^T buffers, 128 columns apart
+
+enum Site : uint32_t { S_KEMPTY = 1, S_QEMPTY = 2, S_KFULL = 3, S_QFULL = 4, S_FREE = 5, S_S = 6, S_ROWS = 7, S_DRAIN = 8, S_SMEM = 9, S_JOIN = 10, S_READ = 11 };
+
+template <int D>
+struct Cfg {
+    static constexpr int NQ = D == 256 ? 64 : 128;     // query rows of a step
+    static constexpr int PANELS = D / 64;
+    static constexpr int KPANEL = 128 * 128, KTILE = PANELS * KPANEL;
+    static constexpr int QPANEL = NQ * 128, QTILE = PANELS * QPANEL;
+    static constexpr int KS = D == 64 ? 6 : (D == 128 ? 3 : 2), QS = D == 64 ? 5 : (D == 128 ? 3 : 2);
+    static constexpr int OFF_Q = KS * KTILE;
+    static constexpr int OFF_BAR = OFF_Q + QS * QTILE;
+    static constexpr int NBAR = 2 * KS + 2 * QS + 3 * NB + 2 + 2 + 1;   // K, Q (full, empty); S, rows, free; join, read; done
+    static constexpr int OFF_ROWS = OFF_BAR + ((NBAR * 8 + 15) / 16) * 16;   // NB x { lse2[128], limit[128] }
+    static constexpr int OFF_JOIN = OFF_ROWS + NB * 1024;                    // [2][128] sums of the group that is not last
+    static constexpr int OFF_MISC = OFF_JOIN + 1024;
+    static constexpr int BYTES = OFF_MISC + 64;
+    static constexpr int ALLOC = BYTES + 1024;
+    static_assert(ALLOC <= 232448, "shared memory of one CTA");
+};
+
+struct Misc {
+    uint32_t tmem;
+    int abort;
+    int lowest[2 * NB];      // lowest limit of each half of a step's rows
+    WeighWalk walk;
+};
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(THREADS, 1)
+    weigh_kernel(const __grid_constant__ WeighMaps maps, const __grid_constant__ WeighParams p)
+{
+    using C = Cfg<D>;
+    constexpr int NQ = C::NQ;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t pad = (1024u - (raw & 1023u)) & 1023u;
+    uint8_t *smem = smem_raw + pad;
+    const uint32_t sb = raw + pad;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t sQ = sb + C::OFF_Q, bar0 = sb + C::OFF_BAR;
+    auto k_full = [&](int u) { return bar0 + 8u * (u % C::KS); };
+    auto k_empty = [&](int u) { return bar0 + 8u * (C::KS + u % C::KS); };
+    const uint32_t barQ0 = bar0 + 16u * C::KS;
+    auto q_full = [&](int u) { return barQ0 + 8u * (u % C::QS); };
+    auto q_empty = [&](int u) { return barQ0 + 8u * (C::QS + u % C::QS); };
+    const uint32_t barS = barQ0 + 16u * C::QS, barRows = barS + 8u * NB, barFree = barRows + 8u * NB, barJoin = barFree + 8u * NB,
+                   barRead = barJoin + 16, barDone = barRead + 16;
+    float *rows_lse = reinterpret_cast<float *>(smem + C::OFF_ROWS);
+    float *join = reinterpret_cast<float *>(smem + C::OFF_JOIN);
+    volatile Misc *misc = reinterpret_cast<volatile Misc *>(smem + C::OFF_MISC);
+    volatile int *abort_flag = &misc->abort;
+    unsigned int *status = &g_weigh_status;
+    const uint64_t tmo = p.timeout_ns;
+    const bool gather = p.s.mode == kPath;
+
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (pad + (uint32_t)C::BYTES > dynamic_smem_size_u32()) {
+        if (threadIdx.x == 0) atomicOr(status, 1u | (S_SMEM << 8));
+        return;
+    }
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::KS; ++s) {
+            mbar_init(k_full(s), 1);
+            mbar_init(k_empty(s), 1);
+        }
+        for (int s = 0; s < C::QS; ++s) {
+            mbar_init(q_full(s), gather ? 2 : 1);
+            mbar_init(q_empty(s), 1);
+        }
+        for (int i = 0; i < NB; ++i) {
+            mbar_init(barS + 8 * i, 1);
+            mbar_init(barRows + 8 * i, 2);
+            mbar_init(barFree + 8 * i, 4);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(barJoin + 8 * i, 4);
+            mbar_init(barRead + 8 * i, 4);
+        }
+        mbar_init(barDone, 1);
+        misc->abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(const_cast<uint32_t *>(&misc->tmem)), 512);
+        tmem_relinquish();
+    }
+    if (warp == 3) {
+        const Share w = find_share(p.s.B, p.least, lane, blockIdx.x, gridDim.x, [&](int b) {
+            const WeighLen l = weigh_len(p.s, b);
+            return p.s.Hkv * weigh_before(l, l.kt);
+        });
+        if (lane == 0) {
+            misc->walk.b = w.b;
+            misc->walk.off = w.off;
+            misc->walk.left = w.left;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = misc->tmem;
+    WeighWalk walk{misc->walk.b, misc->walk.off, misc->walk.left};
+    WeighSeg g;
+
+    auto wait_all = [&](uint32_t bar, uint32_t parity, uint32_t site) -> bool {
+        return __all_sync(0xffffffffu, bounded_wait(bar, parity, abort_flag, tmo, site, status)) != 0;
+    };
+    // Q tiles are told apart by (sequence, KV head, plane, tile); consecutive steps with the same one share it
+    struct Tile {
+        int b = -1, kvh = 0, plane = 0, qt = 0;
+        __device__ bool change(int b1, int kvh1, int plane1, int qt1)
+        {
+            const bool same = b == b1 && kvh == kvh1 && plane == plane1 && qt == qt1;
+            b = b1;
+            kvh = kvh1;
+            plane = plane1;
+            qt = qt1;
+            return !same;
+        }
+    };
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ K producer, Q producer
+        const int boxes = 128 / p.box_rows;
+        const int box = lane / C::PANELS, pn = lane % C::PANELS;
+        const uint32_t box_off = (uint32_t)(pn * C::KPANEL + box * p.box_rows * 128);
+        int ku = 0, qu = 0;
+        bool ok = true;
+        Tile at;
+        while (ok && walk.next(p.s, g)) {
+            int pid = -1, row = 0;
+            ok = wait_all(k_empty(ku), ((ku / C::KS) & 1) ^ 1, S_KEMPTY);
+            if (!ok) break;
+            const int left = g.len.n - g.kt * 128;
+            const int valid = min(boxes, cdiv(left, p.box_rows));
+            const uint32_t dst = sb + (uint32_t)(ku % C::KS) * C::KTILE, bar = k_full(ku);
+            if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(valid * p.box_rows * 128 * C::PANELS));
+            __syncwarp();
+            if (box < valid) {   // at most 8 boxes x PANELS: one for each lane at D = 256
+                page_of(p.pages, g.b, g.kt * 128 + box * p.box_rows, pid, row);
+                load_page(dst + box_off, &maps.k, pn * 64, row, g.kvh, pid, bar);
+            }
+            ++ku;
+            if (gather) continue;
+            for (int s = g.s0; ok && s < g.s1; ++s) {
+                int plane, qt;
+                g.tile(s, plane, qt);
+                if (!at.change(g.b, g.kvh, plane, qt)) continue;
+                ok = wait_all(q_empty(qu), ((qu / C::QS) & 1) ^ 1, S_QEMPTY);
+                if (!ok) break;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(q_full(qu), C::QTILE);
+#pragma unroll
+                    for (int pq = 0; pq < C::PANELS; ++pq)
+                        tma_load_3d(sQ + (uint32_t)(qu % C::QS) * C::QTILE + pq * C::QPANEL, &maps.q, pq * 64, qt * NQ,
+                                    (g.b * p.s.Hkv + g.kvh) * g.len.planes + plane, q_full(qu));
+                }
+                ++qu;
+            }
+        }
+        if (lane == 0) {
+            for (int x = max(0, ku - C::KS); x < ku; ++x) bounded_wait(k_full(x), (x / C::KS) & 1, abort_flag, tmo, S_DRAIN, status, false);
+            for (int x = max(0, qu - C::QS); x < qu; ++x) bounded_wait(q_full(x), (x / C::QS) & 1, abort_flag, tmo, S_DRAIN, status, false);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA issuer (whole warp)
+        constexpr uint32_t HI = sdesc_hi_sw128(1024);
+        int ku = 0, qu = 0;      // tiles taken so far
+        uint32_t st = 0;         // step: buffer st % NB
+        bool ok = true;
+        Tile at;
+        while (ok && walk.next(p.s, g)) {
+            if (ku) tc_commit_elect(k_empty(ku - 1));   // the last key tile's products are all issued
+            ok = wait_all(k_full(ku), (ku / C::KS) & 1, S_KFULL);
+            if (!ok) break;
+            const uint32_t sK = sb + (uint32_t)(ku % C::KS) * C::KTILE;
+            ++ku;
+            for (int s = g.s0; s < g.s1; ++s, ++st) {
+                int plane, qt;
+                g.tile(s, plane, qt);
+                if (at.change(g.b, g.kvh, plane, qt)) {
+                    if (qu) tc_commit_elect(q_empty(qu - 1));
+                    ok = wait_all(q_full(qu), (qu / C::QS) & 1, S_QFULL);
+                    if (!ok) break;
+                    ++qu;
+                }
+                const uint32_t bi = st % NB;
+                ok = wait_all(barFree + 8u * bi, ((st / NB) & 1) ^ 1, S_FREE);
+                if (!ok) break;
+                tc_fence_after();
+                // columns: the rows of this tile, to the next multiple of 16
+                const int cols = max(16, min(NQ, (g.len.rows - qt * NQ + 15) & ~15));
+                const uint32_t id = idesc_f16(BF16, 128, 16, false) + ((uint32_t)(cols - 16) >> 3 << 17);
+                const uint32_t sq = sQ + (uint32_t)((qu - 1) % C::QS) * C::QTILE;
+#pragma unroll
+                for (int pn = 0; pn < C::PANELS; ++pn)
+                    mma_ss_kk4_elect(tmem + bi * 128u, sdesc_lo(sK + pn * C::KPANEL, 16), sdesc_lo(sq + pn * C::QPANEL, 16), HI, id,
+                                     pn ? 1u : 0u);
+                tc_commit_elect(barS + 8u * bi);
+            }
+        }
+        tc_commit_elect(barDone);
+        bounded_wait(barDone, 0, abort_flag, tmo, S_DRAIN, status, false);
+        __syncwarp();
+    } else if (warp < 4) {
+        // ------------------------------------------------------------ rows: lse, limits, gathered queries
+        const int half = warp - 2;
+        int qu = 0;
+        uint32_t st = 0;
+        bool ok = true;
+        Tile at;
+        while (ok && walk.next(p.s, g)) {
+            const size_t head0 = (size_t)(g.b * p.s.Hkv + g.kvh) * p.s.group;   // first query head of the group
+            for (int s = g.s0; s < g.s1; ++s, ++st) {
+                int plane, qt;
+                g.tile(s, plane, qt);
+                if (at.change(g.b, g.kvh, plane, qt) && gather) {
+                    ok = wait_all(q_empty(qu), ((qu / C::QS) & 1) ^ 1, S_QEMPTY);
+                    if (!ok) break;
+                    const uint32_t dst = sQ + (uint32_t)(qu % C::QS) * C::QTILE;
+                    // rows to the next multiple of 16; 16-byte chunk c of row r at c ^ (r & 7) of its 128 bytes
+                    const int rows = min(NQ, max(16, (g.len.rows - qt * NQ + 15) & ~15));
+                    for (int x = threadIdx.x - 64; x < rows * (D / 8); x += 64) {
+                        const int r = x / (D / 8), ch = x % (D / 8), row = qt * NQ + r;
+                        uint4 v = make_uint4(0, 0, 0, 0);
+                        if (row < g.len.rows) {
+                            const int h = row / g.len.a, t = __ldg(p.path + (size_t)g.b * p.s.T + (row - h * g.len.a));
+                            if (t >= 0 && t < p.s.T)
+                                v = __ldg(reinterpret_cast<const uint4 *>(p.q) + ((head0 + h) * p.s.T + t) * (D / 8) + ch);
+                        }
+                        st_shared_v4(dst + (ch >> 3) * C::QPANEL + r * 128 + (((ch & 7) ^ (r & 7)) << 4), v.x, v.y, v.z, v.w);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(q_full(qu));
+                    ++qu;
+                }
+                const uint32_t bi = st % NB;
+                float lse2[2];
+                int limit[2], low = 0x7fffffff;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int c = half * 64 + 32 * e + lane, row = qt * NQ + c;
+                    int i = -1, h = plane, t = 0;      // order of the row, its head in the group, its place in q
+                    if (c < NQ && row < g.len.rows) {
+                        if (p.s.mode == kHeads) {
+                            i = t = row;
+                        } else if (p.s.mode == kRows) {
+                            h = row / p.s.T;
+                            i = t = row - h * p.s.T;
+                            if (i >= g.len.a) i = -1;
+                        } else {
+                            h = row / g.len.a;
+                            i = row - h * g.len.a;
+                            t = __ldg(p.path + (size_t)g.b * p.s.T + i);
+                            if (t < 0 || t >= p.s.T) i = -1;
+                        }
+                    }
+                    limit[e] = 0;
+                    lse2[e] = 0.f;
+                    if (i >= 0) {
+                        const float v = __ldg(p.lse + (head0 + h) * p.s.T + t);
+                        lse2[e] = v * 1.4426950408889634f;
+                        // a row that saw nothing gave nothing
+                        limit[e] = v == -INFINITY ? 0 : (p.s.causal ? clampi(g.len.off + i + 1, 0, g.len.n) : g.len.n);
+                    }
+                    low = min(low, limit[e]);
+                }
+                low = __reduce_min_sync(~0u, low);
+                ok = wait_all(barFree + 8u * bi, ((st / NB) & 1) ^ 1, S_FREE);
+                if (!ok) break;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int c = half * 64 + 32 * e + lane;
+                    rows_lse[bi * 256 + c] = lse2[e];
+                    reinterpret_cast<int *>(rows_lse)[bi * 256 + 128 + c] = limit[e];
+                }
+                if (lane == 0) misc->lowest[bi * 2 + half] = low;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(barRows + 8u * bi);
+            }
+        }
+    } else {
+        // ------------------------------------------------------------ sums, one thread per key
+        const int grp = (warp - 4) >> 2, r = (threadIdx.x - 128) & 127;
+        const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+        const uint64_t sl2x2 = f2_pack(p.sl2, p.sl2);
+        uint32_t st0 = 0;
+        int posts[2] = {0, 0};   // sums handed over so far by each group
+        bool ok = true;
+        while (ok && walk.next(p.s, g)) {
+            const int slot = g.kt * 128 + r, ns = g.s1 - g.s0;
+            const size_t at = (size_t)(g.b * p.s.Hkv + g.kvh) * p.s.capacity + slot;
+            const bool whole = g.s0 == 0 && g.s1 == g.ns, live = slot < g.len.n;
+            const int owner = (int)((st0 + ns - 1) & 1);     // the group of the last step
+            float base = 0.f, sum = 0.f;
+            if (grp == owner && whole && live && p.weight) base = p.weight[at];
+            for (int s = (int)((st0 ^ (uint32_t)grp) & 1u); s < ns; s += 2) {
+                const uint32_t st = st0 + s, bi = st % NB, ph = (st / NB) & 1;
+                int plane, qt;
+                g.tile(g.s0 + s, plane, qt);
+                ok = wait_all(barRows + 8u * bi, ph, S_ROWS) && wait_all(barS + 8u * bi, ph, S_S);
+                if (!ok) break;
+                tc_fence_after();
+                const float *lse2 = rows_lse + bi * 256;
+                const int *limit = reinterpret_cast<const int *>(lse2) + 128;
+                const int cols = min(NQ, g.len.rows - qt * NQ);
+                const bool masked = cols < NQ || min(misc->lowest[2 * bi], NQ > 64 ? misc->lowest[2 * bi + 1] : 0x7fffffff) < g.kt * 128 + 128;
+                uint64_t sum2[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sum2[i] = f2_pack(0.f, 0.f);
+#pragma unroll 1
+                for (int c = 0; c < cols; c += 32) {
+                    uint32_t sv[32];
+                    tmem_ld_x32(tmem + lane_off + bi * 128u + c, sv);
+                    tmem_wait_ld();
+                    reg_fence_x32(sv);
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4) {
+                        const float4 l = *reinterpret_cast<const float4 *>(lse2 + c + e);
+                        float x[4];
+                        f2_unpack(f2_fma(f2_pack(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1])), sl2x2, f2_pack(-l.x, -l.y)), x[0], x[1]);
+                        f2_unpack(f2_fma(f2_pack(__uint_as_float(sv[e + 2]), __uint_as_float(sv[e + 3])), sl2x2, f2_pack(-l.z, -l.w)), x[2], x[3]);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) x[i] = ex2_approx(x[i]);
+                        if (masked) {
+                            const int4 m = *reinterpret_cast<const int4 *>(limit + c + e);
+                            x[0] = slot < m.x ? x[0] : 0.f;
+                            x[1] = slot < m.y ? x[1] : 0.f;
+                            x[2] = slot < m.z ? x[2] : 0.f;
+                            x[3] = slot < m.w ? x[3] : 0.f;
+                        }
+                        sum2[(e >> 1) & 3] = f2_add(sum2[(e >> 1) & 3], f2_pack(x[0], x[1]));
+                        sum2[((e >> 1) + 1) & 3] = f2_add(sum2[((e >> 1) + 1) & 3], f2_pack(x[2], x[3]));
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(barFree + 8u * bi);
+                float la, lb;
+                f2_unpack(f2_add(f2_add(sum2[0], sum2[1]), f2_add(sum2[2], sum2[3])), la, lb);
+                sum += la + lb;
+            }
+            if (!ok) break;
+            if (ns > 1) {
+                // the other group hands its sum to the owner of the last step
+                const int other = owner ^ 1, post = posts[other]++;
+                if (grp == other) {
+                    if (post > 0) ok = wait_all(barRead + 8u * other, (post - 1) & 1, S_READ);
+                    if (!ok) break;
+                    join[other * 128 + r] = sum;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(barJoin + 8u * other);
+                } else {
+                    ok = wait_all(barJoin + 8u * other, post & 1, S_JOIN);
+                    if (!ok) break;
+                    sum += join[other * 128 + r];
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(barRead + 8u * other);
+                }
+            }
+            if (grp == owner && live) {
+                if (whole)
+                    p.out[at] = base + sum;
+                else
+                    p.part[(size_t)part_slot(blockIdx.x, g.s0) * 128 + r] = sum;
+            }
+            st0 += ns;
+        }
+    }
+
+    const WeighWalk share{misc->walk.b, misc->walk.off, misc->walk.left};
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    } else if (warp >= 4 && warp < 8 && *abort_flag) {
+        // This CTA gave up on a wait: NaN into every sum it was given
+        const int r = threadIdx.x - 128;
+        walk = share;
+        while (walk.next(p.s, g)) {
+            if (g.kt * 128 + r >= g.len.n) continue;
+            if (g.s0 == 0 && g.s1 == g.ns)
+                p.out[(size_t)(g.b * p.s.Hkv + g.kvh) * p.s.capacity + g.kt * 128 + r] = __uint_as_float(~0u);
+            else
+                p.part[(size_t)part_slot(blockIdx.x, g.s0) * 128 + r] = __uint_as_float(~0u);
+        }
+    }
+}
+
+// Adds the parts of the key tiles that a cut crosses, in the order of the steps; block x handles the
+// key tile whose first cut is the start of CTA x + 1.
+__global__ void __launch_bounds__(128) weigh_join_kernel(const __grid_constant__ WeighParams p, int grid)
+{
+    const int k = blockIdx.x + 1, lane = threadIdx.x & 31, r = threadIdx.x;
+    const Share sh = find_share(p.s.B, p.least, lane, k, grid, [&](int b) {
+        const WeighLen l = weigh_len(p.s, b);
+        return p.s.Hkv * weigh_before(l, l.kt);
+    });
+    WeighWalk w{sh.b, sh.off, sh.left};
+    WeighSeg g;
+    if (k >= sh.G || !w.next(p.s, g) || g.s0 == 0) return;
+    const int u0 = cut(sh.total, sh.G, k) - g.s0, u1 = u0 + g.ns;
+    if (cut(sh.total, sh.G, k - 1) > u0) return;          // an earlier cut of the same key tile
+    int parts = 2;
+    while (k + parts - 1 < sh.G && cut(sh.total, sh.G, k + parts - 1) < u1) ++parts;
+    const int slot = g.kt * 128 + r;
+    const size_t at = (size_t)(g.b * p.s.Hkv + g.kvh) * p.s.capacity + slot;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (slot >= g.len.n) return;
+    float sum = 0.f;
+    for (int i = 0; i < parts; ++i) sum += p.part[(size_t)part_slot(k - 1 + i, i) * 128 + r];
+    p.out[at] = (p.weight ? p.weight[at] : 0.f) + sum;
+}
+
+template <int D, bool BF16>
+cudaError_t launch_one(const WeighMaps &m, const WeighParams &p0, cudaStream_t st)
+{
+    auto kern = weigh_kernel<D, BF16>;
+    static std::atomic<uint64_t> configured{0};
+    static std::atomic<int> sm_count[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    const uint64_t bit = 1ull << dev;
+    if (!(configured.load(std::memory_order_acquire) & bit)) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::ALLOC);
+        if (e != cudaSuccess) return e;
+        int nsm = 0;
+        e = cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev);
+        if (e != cudaSuccess) return e;
+        sm_count[dev].store(nsm, std::memory_order_relaxed);
+        configured.fetch_or(bit, std::memory_order_acq_rel);
+    }
+    WeighParams p = p0;
+    if (p.timeout_ns == 0) p.timeout_ns = kDefaultTimeoutNs;
+    const int grid = clampi(sm_count[dev].load(std::memory_order_relaxed), 1, kMaxCtas);
+    kern<<<grid, THREADS, Cfg<D>::ALLOC, st>>>(m, p);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || grid == 1) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid - 1);
+    cfg.blockDim = dim3(128);
+    cfg.stream = st;
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, weigh_join_kernel, p, grid);
+}
+
+} // namespace
+
+int weigh_rows(int D) { return D == 256 ? 64 : 128; }
+
+cudaError_t launch_weigh(int D, bool bf16, const WeighMaps &m, const WeighParams &p, cudaStream_t st)
+{
+    if (D == 64) return bf16 ? launch_one<64, true>(m, p, st) : launch_one<64, false>(m, p, st);
+    if (D == 128) return bf16 ? launch_one<128, true>(m, p, st) : launch_one<128, false>(m, p, st);
+    if (D == 256) return bf16 ? launch_one<256, true>(m, p, st) : launch_one<256, false>(m, p, st);
+    return cudaErrorInvalidValue;
+}
+
+cudaError_t read_and_clear_weigh_status(uint32_t *word)
+{
+    unsigned int w = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(&w, g_weigh_status, sizeof(w));
+    if (e != cudaSuccess) return e;
+    const unsigned int zero = 0;
+    e = cudaMemcpyToSymbol(g_weigh_status, &zero, sizeof(zero));
+    if (word) *word = w;
+    return e;
+}
+
+} // namespace cache
+} // namespace fa

@@ -47,3 +47,41 @@ def attend(q, k_new, v_new, k, v, table, seq_len, parent, draft_len, scale):
                     av[b, h, i] = np.abs(vv).sum(0)
                     qk[b, h, i] = scale * (np.abs(kk) @ np.abs(q[b, h, i])).max()
     return o, lse, pv, av, qk
+
+
+def weigh(q, lse, k, table, seq_len, path, count, causal, scale, group):
+    """sum over rows and heads of exp(scale q.k - lse): [B, Hkv, slots in use] as a list per sequence, with
+    the largest scale sum |q||k| and |lse| among the rows that count."""
+    B, Hq, T, D = q.shape
+    out = []
+    for b in range(B):
+        n, a = int(seq_len[b]), min(max(int(count[b]), 0), T)
+        kc = slots_of(k, table[b], n)
+        s = np.zeros((Hq // group, n))
+        qk = top = 0.0
+        for i in range(a):
+            t = int(path[b][i]) if path is not None else i
+            if not 0 <= t < T:
+                continue
+            see = min(max(n - a + i + 1, 0), n) if causal else n
+            for h in range(Hq):
+                if lse[b, h, t] == -np.inf or see == 0:
+                    continue
+                kk = kc[h // group, :see]
+                s[h // group, :see] += np.exp(scale * (kk @ q[b, h, t]) - lse[b, h, t])
+                qk = max(qk, scale * (np.abs(kk) @ np.abs(q[b, h, t])).max())
+                top = max(top, abs(lse[b, h, t]))
+        out.append((s, qk, top))
+    return out
+
+
+def choose(weight, pos, n, keep, first, last, next_pos):
+    """(freed slots below keep, kept slots at or above it), in order."""
+    if n <= keep:
+        return [], []
+    def rank(s):
+        safe = pos[s] < first or (last > 0 and pos[s] >= next_pos - last)
+        w = float(weight[s])
+        return (not safe, not np.isnan(w), 0.0 if np.isnan(w) else -w, s)
+    kept = set(sorted(range(n), key=rank)[:keep])
+    return [s for s in range(keep) if s not in kept], [s for s in range(keep, n) if s in kept]

@@ -110,10 +110,82 @@ static int check_tree()
     return 0;
 }
 
+static int check_weigh()
+{
+    for (int round = 0; round < 400; ++round) {
+        std::vector<int32_t> len(1 + rnd(6)), count(len.size());
+        WeighShape s;
+        s.B = (int)len.size();
+        s.Hkv = 1 + rnd(3);
+        s.group = 1 + rnd(4);
+        s.T = 1 + rnd(rnd(2) ? 20 : 700);
+        s.mode = rnd(3);
+        s.causal = rnd(3) != 0;
+        s.NQ = rnd(2) ? 128 : 64;
+        s.capacity = 16 * (1 + rnd(60));
+        for (size_t b = 0; b < len.size(); ++b) {
+            len[b] = (int)rnd(s.capacity + 20) - 10;
+            count[b] = (int)rnd(s.T + 4) - 2;
+        }
+        s.seq_len = len.data();
+        s.count = rnd(4) ? count.data() : nullptr;
+        std::vector<int> base;
+        int total = 0;
+        for (int b = 0; b < s.B; ++b) {
+            const WeighLen l = weigh_len(s, b);
+            base.push_back(total);
+            int sum = 0;
+            for (int k = 0; k < l.kt; ++k) {
+                if (weigh_before(l, k) != sum) return fail("the steps before a key tile");
+                if (weigh_steps(l, k) < 1) return fail("a key tile without steps");
+                sum += weigh_steps(l, k);
+            }
+            if (weigh_before(l, l.kt) != sum) return fail("the steps of a head");
+            total += s.Hkv * sum;
+        }
+        const int grid = 1 + rnd(160), least = 1 + rnd(3), G = ctas(total, grid, least);
+        std::map<long long, std::set<int>> seen;   // (b, kvh, kt) -> its steps
+        std::map<long long, std::set<std::pair<int, int>>> tiles;
+        for (int c = 0; c < G; ++c) {
+            const int begin = cut(total, G, c);
+            int b = 0;
+            while (b + 1 < s.B && base[b + 1] <= begin) ++b;
+            WeighWalk w{b, begin - base[b], cut(total, G, c + 1) - begin};
+            WeighSeg g;
+            while (w.next(s, g)) {
+                const long long id = ((long long)g.b * s.Hkv + g.kvh) * 100000 + g.kt;
+                if (g.s0 < 0 || g.s1 <= g.s0 || g.s1 > g.ns || g.kt * 128 >= g.len.n) return fail("a segment outside its unit");
+                for (int i = g.s0; i < g.s1; ++i) {
+                    if (!seen[id].insert(i).second) return fail("a step given twice");
+                    int plane, qt;
+                    g.tile(i, plane, qt);
+                    if (plane < 0 || plane >= g.len.planes || qt < 0 || (g.len.qt && qt >= g.len.qt)) return fail("a query tile");
+                    tiles[id].insert({plane, qt});
+                }
+            }
+        }
+        // every row that sees a slot of a key tile lies in one of the unit's query tiles
+        for (int b = 0; b < s.B; ++b) {
+            const WeighLen l = weigh_len(s, b);
+            for (int h = 0; h < s.Hkv; ++h)
+                for (int k = 0; k < l.kt; ++k) {
+                    const long long id = ((long long)b * s.Hkv + h) * 100000 + k;
+                    if ((int)seen[id].size() != weigh_steps(l, k)) return fail("a step that nobody has");
+                    for (int plane = 0; plane < l.planes; ++plane)
+                        for (int r = 0; r < l.rows; ++r) {
+                            const bool sees = s.mode != kHeads || !s.causal || 128 * k < l.off + r + 1;
+                            if (sees && !tiles[id].count({plane, r / s.NQ})) return fail("a row that is left out");
+                        }
+                }
+        }
+    }
+    return 0;
+}
+
 int main()
 {
     srand(1);
-    if (check_tree()) return 1;
+    if (check_tree() || check_weigh()) return 1;
     std::printf("ok\n");
     return 0;
 }

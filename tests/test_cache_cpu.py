@@ -95,6 +95,47 @@ def test_append_empty(lib):
     assert append(lib, B=0, k_new=None) == 0 and append(lib, T=0, k_new=None) == 0
 
 
+def weights(lib, **over):
+    a = dict(ADDR, Hq=4, T=5, causal=1, scale=0.1, bytes=1 << 30)
+    a.update(over)
+    return lib.fa_cache_weights(cache_struct(**over), a["q"], a["lse"], a["path"], a["count"], a["weight"], a["weight_out"], a["Hq"],
+                                a["T"], a["causal"], a["scale"], a["ws"], a["bytes"], None)
+
+
+def evict(lib, **over):
+    a = dict(ADDR, keep=100, first=4, last=16, bytes=1 << 30)
+    a.update(over)
+    return lib.fa_cache_evict(cache_struct(**over), a["weight"], a["pos"], a["weight_out"], a["pos_out"], a["new_len"], a["next_pos"],
+                              a["keep"], a["first"], a["last"], a["ws"], a["bytes"], None)
+
+
+@pytest.mark.parametrize("over,code", BAD_CACHE + [
+    (dict(Hq=3), 3), (dict(Hq=0), 3), (dict(T=-1), 2), (dict(T=0), 2), (dict(scale=0.0), 7), (dict(scale=math.nan), 7),
+    (dict(causal=2), 13), (dict(causal=-1), 13), (dict(q=None), 1), (dict(lse=None), 1), (dict(count=None), 1),
+    (dict(weight_out=None), 1), (dict(ws=None), 1), (dict(q=ADDR["q"] + 8), 5), (dict(lse=ADDR["lse"] + 2), 5),
+    (dict(weight=ADDR["weight"] + 1), 5), (dict(ws=ADDR["ws"] + 4), 5), (dict(bytes=100), 16), (dict(weight_out=ADDR["weight"] + 4), 6),
+    (dict(weight_out=ADDR["k"]), 6), (dict(ws=ADDR["lse"]), 6), (dict(weight_out=ADDR["seq_len"]), 6),
+    (dict(B=1, Hkv=1, Hq=64, T=1 << 20, max_pages=1 << 16, num_pages=1 << 16), 2)])
+def test_weights_refusals(lib, over, code):
+    assert weights(lib, **over) == code
+
+
+@pytest.mark.parametrize("over,code", BAD_CACHE + [
+    (dict(keep=0), 2), (dict(first=-1), 2), (dict(last=-1), 2), (dict(first=50, last=51), 2), (dict(weight=None), 1), (dict(pos=None), 1),
+    (dict(weight_out=None), 1), (dict(pos_out=None), 1), (dict(new_len=None), 1), (dict(next_pos=None), 1), (dict(ws=None), 1),
+    (dict(bytes=1000), 16), (dict(weight=ADDR["weight"] + 2), 5), (dict(new_len=ADDR["new_len"] + 1), 5), (dict(ws=ADDR["ws"] + 2), 5),
+    (dict(weight_out=ADDR["weight"] + 4), 6), (dict(pos_out=ADDR["weight"]), 6), (dict(new_len=ADDR["seq_len"]), 6),
+    (dict(new_len=ADDR["next_pos"]), 6), (dict(ws=ADDR["pos"]), 6), (dict(weight_out=ADDR["v"]), 6), (dict(k=ADDR["v"]), 6)])
+def test_evict_refusals(lib, over, code):
+    assert evict(lib, **over) == code
+
+
+def test_weights_and_evict_empty(lib):
+    assert weights(lib, B=0, q=None) == 0 and weights(lib, max_pages=0, q=None) == 0
+    assert evict(lib, B=0, weight=None) == 0
+    assert lib.fa_evict_workspace_bytes(2, 2, 100, 100) == 0 and lib.fa_evict_workspace_bytes(2, 2, 100, 90) == 2 * 2 * 2 * 10 * 4
+
+
 class FakeCuda(torch.Tensor):
     """A CPU tensor that reports itself as living on a given CUDA device (no GPU needed)."""
     _dev = torch.device("cuda", 0)
@@ -164,3 +205,24 @@ def test_cache_append_checks_its_tensors(over, what):
     a.update(over)
     with pytest.raises(ValueError, match=what):
         fc.cache_append(**a)
+
+
+@pytest.mark.parametrize("over,what", [
+    (dict(q=on((2, 4, 5, 128))), "head dimension"), (dict(lse=on((2, 4, 6), torch.float32)), "lse"), (dict(path=on((2, 5), torch.int32)), "needs count"),
+    (dict(weight=on((2, 2, 48))), "weight"), (dict(out=on((2, 2, 49), torch.float32)), "out"), (dict(lse=on((2, 4, 5), torch.float32, 1)), "same GPU")])
+def test_cache_weights_checks_its_tensors(over, what):
+    a = dict(cache=make_cache(), q=on((2, 4, 5, 64)), lse=on((2, 4, 5), torch.float32), weight=on((2, 2, 48), torch.float32))
+    a.update(over)
+    with pytest.raises(ValueError, match=what):
+        fc.cache_weights(**a)
+
+
+@pytest.mark.parametrize("over,what", [
+    (dict(last=3), "needs next_pos"), (dict(weight=on((2, 2, 40), torch.float32)), "weight"), (dict(pos=on((2, 2, 48), torch.int64)), "pos"),
+    (dict(pos_out=on((2, 2, 48), torch.float32)), "pos_out"), (dict(new_len=on((3,), torch.int32)), "new_len"),
+    (dict(next_pos=on((2,), torch.int32, 1)), "same GPU")])
+def test_cache_evict_checks_its_tensors(over, what):
+    a = dict(cache=make_cache(), weight=on((2, 2, 48), torch.float32), pos=on((2, 2, 48), torch.int32), keep=20, new_len=on((2,), torch.int32))
+    a.update(over)
+    with pytest.raises(ValueError, match=what):
+        fc.cache_evict(**a)

@@ -12,12 +12,17 @@ Tolerances, from the arithmetic.  u = eps / 2 is the type's rounding (2^-8 bf16,
               least one weight of 1, half a step is 2^-25 sum_j |v_j| more.
                   |lse - ref| <= e + 2^-20 (1 + |ref|)
   append      a copy: equal.
+  weights     every term has the score's error e, the rounding of lse and of the exponent (2^-22 (1 + |lse|))
+              and the exponential's (2^-21); a sum of up to 32 tiles of 128 rows is at most 64 additions
+              deep (2^-18), the addition to the weight one more:
+                  |out - ref| <= (2 e + 2^-20 (1 + max |lse|) + 2^-18) sum + 2^-23 |ref|
+  eviction    copies and whole numbers: equal.
 """
 import numpy as np
 import pytest
 import torch
 
-from cache_oracle import attend
+from cache_oracle import attend, choose, weigh
 from programming_flashattention_fwd_gb300 import build as fa_build
 
 pytestmark = pytest.mark.gpu
@@ -269,3 +274,290 @@ def test_a_page_that_does_not_exist(fa):
         fa.cache_append(fa.KVCache(kd, vd, ints([17]), t2.cuda()), kn.cuda(), vn.cuda())
         torch.cuda.synchronize()
         assert torch.equal(kd.cpu().view(torch.int16), k.view(torch.int16))
+
+
+# ---------------------------------------------------------------- accumulated weights
+
+def run_weights(fa, dtype, Hq, Hkv, D, lens, counts, T, page, path=None, causal=True, seed=1, kind="out", poison=True, std=1.0):
+    g = torch.Generator().manual_seed(seed)
+    B, group = len(lens), Hq // Hkv
+    k, v, table = make_pool(g, lens, Hkv, D, page, dtype)
+    cap = table.shape[1] * page
+    q = normal(g, (B, Hq, T, D), dtype, std)
+    lse = torch.randn(B, Hq, T, generator=g) + 4.0
+    if path is not None:
+        path = np.asarray(path)
+    if T > 3:
+        lse[:, 0, 2] = -float("inf")      # a row that saw nothing
+    if poison:                            # rows that do not count hold anything
+        for b, a in enumerate(counts):
+            used = set(range(min(max(a, 0), T)) if path is None else [int(x) for x in path[b][:max(a, 0)]])
+            for t in range(T):
+                if t not in used:
+                    q[b, :, t], lse[b, :, t] = float("nan"), float("nan")
+    w = torch.rand(B, Hkv, cap, generator=g)
+    cache = fa.KVCache(k.cuda(), v.cuda(), ints(lens), table.cuda())
+    weight = None if kind == "none" else w.cuda()
+    out = torch.full((B, Hkv, cap), -3.0).cuda() if kind != "in place" else None
+    got = fa.cache_weights(cache, q.cuda(), lse.cuda(), weight, path=None if path is None else ints(path), count=ints(counts),
+                           causal=causal, out=out)
+    torch.cuda.synchronize()
+    assert fa.fa_device_status() == (0, 0)
+    assert got is (weight if kind == "in place" else out)
+    what = f"{dtype} Hq{Hq} Hkv{Hkv} D{D} {lens} {counts} T{T} page{page} {kind}"
+    ref = weigh(np64(q), np64(lse), np64(k), table.numpy(), lens, path, counts, causal, 1 / np.sqrt(D), group)
+    got, w = np64(got), np64(w)
+    for b, n in enumerate(lens):
+        total, qk, top = ref[b]
+        want = total + (0 if kind == "none" else w[b, :, :n])
+        tol = (2.0 ** -17 * qk + 2.0 ** -20 * (1 + top) + 2.0 ** -18) * total + 2.0 ** -23 * np.abs(want)
+        far = np.abs(got[b, :, :n] - want) - tol
+        assert np.isfinite(got[b, :, :n]).all() and (far.size == 0 or far.max() <= 1e-12), f"{what}: sequence {b}: {far.max():.3e} outside"
+        # slots that are not in use are left as they were
+        assert (got[b, :, n:] == (w[b, :, n:] if kind == "in place" else -3.0)).all(), what
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("heads", HEADS)
+def test_weights_of_prompts(fa, dtype, D, heads):
+    """Long enough for the tiles of one head; counts of zero, one and more than there are slots."""
+    run_weights(fa, dtype, *heads, D, [0, 1, 130, 300, 128, 70], [0, 1, 130, 200, 5, 90], 210, 16)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("T", [1, 7, 50, 127, 128, 129])
+@pytest.mark.parametrize("causal", [True, False])
+def test_weights_of_short_prompts(fa, D, T, causal):
+    run_weights(fa, "bf16", 8, 2, D, [400, 129, T], [T, max(1, T - 3), T], T, 48, causal=causal, seed=T)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("kind", ["out", "in place", "none"])
+def test_weights_of_accepted_tokens(fa, dtype, D, kind):
+    path = [[0, 2, 5, 8, -1, -1, -1, -1, -1], [8, -1, -1, -1, -1, -1, -1, -1, -1], list(range(9)), [-1] * 9, [3, 99, -7, 4, -1, -1, -1, -1, -1]]
+    run_weights(fa, dtype, 8, 2, D, [260, 500, 128, 40, 77], [4, 1, 9, 0, 4], 9, 32, path=path, kind=kind)
+
+
+def test_weights_of_many_accepted_tokens(fa):
+    """More gathered rows than one tile holds, and a row that counts twice."""
+    T = 70
+    run_weights(fa, "bf16", 8, 2, 128, [300, 200], [70, 40], T, 16, path=[list(range(T)), [0, 0] + list(range(1, T - 1))])
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_weights_cut_among_ctas(fa, D):
+    """Fewer key tiles than CTAs, many query tiles: key tiles are computed in parts."""
+    run_weights(fa, "fp16", 4, 1, D, [900], [900], 900, 128)
+
+
+def test_weights_with_large_scores(fa):
+    run_weights(fa, "bf16", 4, 2, 128, [200, 150], [150, 150], 150, 16, std=3.0)
+
+
+def test_weights_repeat_exactly(fa):
+    g = torch.Generator().manual_seed(3)
+    k, v, table = make_pool(g, [700], 2, 128, 16, "bf16")
+    q, lse = normal(g, (1, 8, 700, 128), "bf16").cuda(), torch.randn(1, 8, 700, generator=g).cuda() + 5
+    cache = fa.KVCache(k.cuda(), v.cuda(), ints([700]), table.cuda())
+    first = fa.cache_weights(cache, q, lse)
+    for _ in range(5):
+        assert torch.equal(fa.cache_weights(cache, q, lse), first)
+
+
+# ---------------------------------------------------------------- eviction
+
+def run_evict(fa, Hkv, D, lens, keep, page, first=0, last=0, cap=None, weight=None, in_place=True, seed=1, dtype="bf16", dense=False):
+    g = torch.Generator().manual_seed(seed)
+    B = len(lens)
+    room = 0 if cap is None else cap - max(lens)
+    k, v, table = make_pool(g, lens, Hkv, D, page, dtype, room=room, dense=dense)
+    cap = table.shape[1] * page
+    w = torch.randn(B, Hkv, cap, generator=g) if weight is None else weight(g, (B, Hkv, cap))
+    pos = torch.stack([torch.stack([torch.randperm(cap, generator=g) for _ in range(Hkv)]) for _ in range(B)]).to(torch.int32)
+    nxt = [n + 3 for n in lens]
+    kd, vd, wd, pd = k.cuda(), v.cuda(), w.cuda(), pos.cuda()
+    wo, po = (wd, pd) if in_place else (torch.full_like(wd, 5.0), torch.full_like(pd, -9))
+    cache = fa.KVCache(kd, vd, ints(lens), None if dense else table.cuda())
+    left = fa.cache_evict(cache, wd, pd, keep, first=first, last=last, next_pos=ints(nxt) if last else None,
+                          weight_out=None if in_place else wo, pos_out=None if in_place else po)
+    torch.cuda.synchronize()
+    assert left.tolist() == [min(n, keep) for n in lens]
+    rw, rp = (w.clone(), pos.clone()) if in_place else (torch.full_like(w, 5.0), torch.full_like(pos, -9))
+    for b, n in enumerate(lens):
+        m = min(n, keep)
+        for h in range(Hkv):
+            dst, src = choose(w[b, h].numpy(), pos[b, h].numpy(), n, keep, first, last, nxt[b])
+            assert len(dst) == len(src)
+            rw[b, h, :m], rp[b, h, :m] = w[b, h, :m], pos[b, h, :m]
+            for d, s in zip(dst, src):
+                rw[b, h, d], rp[b, h, d] = w[b, h, s], pos[b, h, s]
+                for x in (k, v):
+                    x[table[b, d // page], h, d % page] = x[table[b, s // page], h, s % page]
+    bits = lambda t: t.cpu().view(torch.int16)  # noqa: E731
+    assert torch.equal(bits(kd), bits(k)) and torch.equal(bits(vd), bits(v))
+    assert torch.equal(wo.cpu().view(torch.int32), rw.view(torch.int32)) and torch.equal(po.cpu(), rp)
+
+
+@pytest.mark.parametrize("in_place", [True, False])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("keep,first,last", [(1, 0, 0), (100, 4, 32), (333, 0, 7), (599, 3, 0)])
+def test_evict(fa, D, keep, first, last, in_place):
+    run_evict(fa, 2, D, [600, 0, 1, keep, keep + 1, 555], keep, 16, first, last, in_place=in_place, seed=keep, dtype="fp16")
+
+
+@pytest.mark.parametrize("page", [16, 48, 128])
+def test_evict_long(fa, page):
+    """Clusters of several CTAs."""
+    run_evict(fa, 1, 64, [9000, 5000], 3001, page, 4, 64)
+
+
+def test_evict_dense_cache(fa):
+    run_evict(fa, 3, 128, [176, 100], 60, 176, 2, 2, dense=True)
+
+
+TIES = {
+    "all equal": lambda g, s: torch.zeros(s),
+    "few values": lambda g, s: torch.randint(-2, 3, s, generator=g).float(),
+    "signed zeros": lambda g, s: torch.where(torch.rand(s, generator=g) < 0.5, -0.0, 0.0),
+    "infinities and NaN": lambda g, s: torch.tensor([float("inf"), -float("inf"), float("nan"), 0.0, 1e-45, -3.4e38])[torch.randint(0, 6, s, generator=g)],
+    "one outlier": lambda g, s: torch.where(torch.arange(s[-1]) == 77, 1e30, 1e-30 * torch.rand(s, generator=g)),
+}
+
+
+@pytest.mark.parametrize("kind", list(TIES))
+@pytest.mark.parametrize("n", [500, 4000])
+def test_evict_ties(fa, kind, n):
+    run_evict(fa, 2, 64, [n, n - 77], n // 3, 16, 4, 8, weight=TIES[kind])
+
+
+def test_evict_nothing(fa):
+    run_evict(fa, 2, 64, [50, 3], 64, 16, 4, 8, in_place=False)
+
+
+# ---------------------------------------------------------------- together
+
+@pytest.mark.parametrize("D,page", [(64, 16), (128, 48)])
+def test_a_decoding_loop(fa, D, page):
+    """Prompt, eviction, then drafting steps: attend, accept, append, weigh, evict.  The oracle keeps every
+    head's keys, values, weights and positions in float64 and is told only which tokens were accepted;
+    what the cache holds is compared with it at the end of every step."""
+    g = torch.Generator().manual_seed(11)
+    B, Hq, Hkv, T, keep, first, last = 2, 4, 2, 9, 60, 2, 8
+    group, scale = Hq // Hkv, 1 / np.sqrt(D)
+    prompt = [90, 75]
+    per = -(-130 // page)
+    pool = torch.zeros(B * per + 1, Hkv, page, D, dtype=torch.bfloat16).cuda()
+    table = torch.randperm(B * per + 1, generator=g)[:B * per].reshape(B, per)
+    seq = ints([0, 0])
+    cache = fa.KVCache(pool, pool.clone(), seq, ints(table))
+    cap = cache.capacity
+    weight, pos = torch.zeros(B, Hkv, cap).cuda(), torch.zeros(B, Hkv, cap, dtype=torch.int32).cuda()
+    nxt = ints([0, 0])
+    P = max(prompt)
+    q, kn, vn = (normal(g, (B, h, P, D), "bf16") for h in (Hq, Hkv, Hkv))
+    # the prompt: attention of a chain over the empty cache, then its keys and weights
+    o, lse = fa.tree_attention(q.cuda(), kn.cuda(), vn.cuda(), cache, draft_len=ints(prompt))
+    fa.cache_append(cache, kn.cuda(), vn.cuda(), count=ints(prompt), weight=weight, pos=pos, start=nxt)
+    seq += ints(prompt)
+    nxt += ints(prompt)
+    fa.cache_weights(cache, q.cuda(), lse, weight, count=ints(prompt))
+    none = np.zeros((1, Hkv, page, D))
+    chain = np.tile(np.arange(P) - 1, (B, 1))
+    ref = attend(np64(q), np64(kn), np64(vn), none, none, np.zeros((B, 1), int), [0, 0], chain, prompt, scale)
+    state = []     # [b][head]: keys, values, weights, positions in the order of the slots
+    for b in range(B):
+        state.append([])
+        for c in range(Hkv):
+            s = dict(k=np64(kn)[b, c, :prompt[b]], v=np64(vn)[b, c, :prompt[b]], w=np.zeros(prompt[b]), p=np.arange(prompt[b]))
+            for h in range(c * group, (c + 1) * group):
+                for i in range(prompt[b]):
+                    s["w"][:i + 1] += np.exp(scale * (s["k"][:i + 1] @ np64(q)[b, h, i]) - ref[1][b, h, i])
+            state[b].append(s)
+
+    def evict():
+        seq.copy_(fa.cache_evict(cache, weight, pos, keep, first=first, last=last, next_pos=nxt))
+        for b in range(B):
+            for c in range(Hkv):
+                s, n = state[b][c], len(state[b][c]["p"])
+                # the choice is the kernel's own: by its weights, which a rounding apart may order otherwise
+                kept = set(pos[b, c, :int(seq[b])].tolist())
+                assert len(kept) == min(n, keep)
+                safe = {int(x) for x in s["p"] if x < first or x >= int(nxt[b]) - last}
+                assert safe <= kept
+                if n > keep:
+                    low = min(s["w"][i] for i in range(n) if int(s["p"][i]) in kept - safe)
+                    high = max(s["w"][i] for i in range(n) if int(s["p"][i]) not in kept)
+                    assert low >= high * (1 - 1e-3)
+                dst = [i for i in range(min(n, keep)) if int(s["p"][i]) not in kept]
+                src = [i for i in range(keep, n) if int(s["p"][i]) in kept]
+                for x in s:
+                    s[x][dst] = s[x][src]
+                    s[x] = s[x][:keep].copy()
+
+    def compare():
+        for b in range(B):
+            for c in range(Hkv):
+                s, n = state[b][c], int(seq[b])
+                assert pos[b, c, :n].tolist() == s["p"].tolist()
+                at = [(int(table[b, i // page]), i % page) for i in range(n)]
+                assert (np.stack([np64(cache.k[x, c, r]) for x, r in at]) == s["k"]).all()
+                assert (np.stack([np64(cache.v[x, c, r]) for x, r in at]) == s["v"]).all()
+                # lse of the attention is within 2^-18 sum|q||k| scale + 2^-20 (1 + |lse|) < 2^-12 here: so are the weights
+                assert np.abs(np64(weight)[b, c, :n] - s["w"]).max() <= 2.0 ** -11 * s["w"].max()
+
+    evict()
+    compare()
+    for step in range(4):
+        q, kn, vn = (normal(g, (B, h, T, D), "bf16") for h in (Hq, Hkv, Hkv))
+        drafts = [T, T - step]
+        parent = np.stack([make_tree(g, T, "tree") for _ in range(B)])
+        o, lse = fa.tree_attention(q.cuda(), kn.cuda(), vn.cuda(), cache, parent=ints(parent), draft_len=ints(drafts))
+        accepted = []
+        for b in range(B):
+            path = [t for t in range(drafts[b]) if True]
+            leaf = path[int(torch.randint(0, len(path), (1,), generator=g))]
+            line = [leaf]
+            while parent[b][line[-1]] >= 0:
+                line.append(int(parent[b][line[-1]]))
+            accepted.append(line[::-1])
+        path = np.full((B, T), -1)
+        for b, a in enumerate(accepted):
+            path[b, :len(a)] = a
+        count = ints([len(a) for a in accepted])
+        for b in range(B):
+            for h in range(Hq):
+                s = state[b][h // group]
+                for t in range(drafts[b]):
+                    line = [t]
+                    while parent[b][line[-1]] >= 0:
+                        line.append(int(parent[b][line[-1]]))
+                    kk = np.concatenate([s["k"], np64(kn)[b, h // group, line]])
+                    vv = np.concatenate([s["v"], np64(vn)[b, h // group, line]])
+                    x = scale * (kk @ np64(q)[b, h, t])
+                    m = x.max()
+                    p = np.exp(x - m)
+                    assert abs(float(lse[b, h, t]) - (m + np.log(p.sum()))) <= 2.0 ** -12
+                    p /= p.sum()
+                    tol = 2.0 ** -8 * np.abs(p @ vv) + (2.0 ** -8 + 2.0 ** -11) * (p @ np.abs(vv))
+                    assert (np.abs(np64(o[b, h, t]) - p @ vv) <= tol).all()
+        fa.cache_append(cache, kn.cuda(), vn.cuda(), path=ints(path), count=count, weight=weight, pos=pos, start=nxt)
+        seq += count
+        nxt += count
+        fa.cache_weights(cache, q.cuda(), lse, weight, path=ints(path), count=count)
+        for b, a in enumerate(accepted):
+            for c in range(Hkv):
+                s, n0 = state[b][c], len(state[b][c]["p"])
+                s["k"] = np.concatenate([s["k"], np64(kn)[b, c, a]])
+                s["v"] = np.concatenate([s["v"], np64(vn)[b, c, a]])
+                s["w"] = np.concatenate([s["w"], np.zeros(len(a))])
+                s["p"] = np.concatenate([s["p"], int(nxt[b]) - len(a) + np.arange(len(a))])
+                for h in range(c * group, (c + 1) * group):
+                    for i, t in enumerate(a):
+                        see = n0 + i + 1
+                        x = scale * (s["k"][:see] @ np64(q)[b, h, t])
+                        s["w"][:see] += np.exp(x - x.max()) / np.exp(x - x.max()).sum()
+        evict()
+        compare()
+    assert fa.fa_device_status() == (0, 0)
