@@ -14,7 +14,8 @@
 namespace fa {
 namespace cache {
 
-__host__ __device__ __forceinline__ int cdiv(int a, int b) { return (int)(((long long)a + b - 1) / b); }
+// ceil(a / b) for a >= 0, b > 0, a + b below 2^32 (32-bit arithmetic: the walks below run in every role)
+__host__ __device__ __forceinline__ int cdiv(int a, int b) { return (int)(((uint32_t)a + (uint32_t)b - 1u) / (uint32_t)b); }
 __host__ __device__ __forceinline__ int clampi(int x, int lo, int hi) { return x < lo ? lo : (x > hi ? hi : x); }
 
 // First step of CTA c when G CTAs share `total` steps.
@@ -167,51 +168,78 @@ __host__ __device__ __forceinline__ int weigh_before(const WeighLen &l, int k)
 struct WeighSeg {
     int b, kvh, kt, s0, s1, ns, first;
     WeighLen len;
+};
 
-    // the plane and the query tile of step s
-    __host__ __device__ __forceinline__ void tile(int s, int &plane, int &qt) const
+// The plane and the query tile of a segment's steps, one after another.
+struct WeighTiles {
+    int plane, qt, first, end;
+
+    __host__ __device__ __forceinline__ explicit WeighTiles(const WeighSeg &g) : first(g.first), end(g.len.qt)
     {
-        const int per = len.qt - first;
-        plane = per > 0 ? s / per : 0;
-        qt = per > 0 ? first + s - plane * per : 0;
+        const int per = end - first;
+        plane = per > 0 && g.s0 ? g.s0 / per : 0;
+        qt = per > 0 ? first + g.s0 - plane * per : 0;
+    }
+    __host__ __device__ __forceinline__ void next()
+    {
+        if (++qt >= end) {
+            qt = first;
+            ++plane;
+        }
     }
 };
 
+// Walks a CTA's steps: `left` of them from step `s` of key tile kt.  The lengths are looked up and
+// the first key tile is searched for once a sequence, not once a key tile: a drafting step has one
+// step a key tile.
 struct WeighWalk {
-    int b, off, left;   // `left` steps from step `off` of sequence b
+    int left, b, kvh, kt, s;
+    WeighLen len;
 
-    __host__ __device__ __forceinline__ bool next(const WeighShape &s, WeighSeg &g)
+    // `steps` steps from step `off` of sequence b0
+    __host__ __device__ __forceinline__ WeighWalk(const WeighShape &sh, int b0, int off, int steps) : left(steps), b(b0), kvh(0), kt(0), s(0)
     {
-        while (left > 0 && b < s.B) {
-            const WeighLen l = weigh_len(s, b);
-            const int one = weigh_before(l, l.kt), per = s.Hkv * one;
-            if (off >= per) {
-                off -= per;
-                ++b;
-                continue;
-            }
-            g.kvh = off / one;
-            const int in = off - g.kvh * one;
-            int lo = 0, hi = l.kt - 1;   // the key tile that holds step `in`
-            while (lo < hi) {
-                const int mid = (lo + hi + 1) / 2;
-                if (weigh_before(l, mid) <= in)
-                    lo = mid;
-                else
-                    hi = mid - 1;
-            }
-            g.b = b;
-            g.kt = lo;
-            g.s0 = in - weigh_before(l, lo);
-            g.ns = weigh_steps(l, lo);
-            g.first = weigh_first(l, lo);
-            g.s1 = g.ns - g.s0 < left ? g.ns : g.s0 + left;
-            g.len = l;
-            off += g.s1 - g.s0;
-            left -= g.s1 - g.s0;
-            return true;
+        if (left <= 0) return;
+        len = weigh_len(sh, b);
+        const int one = weigh_before(len, len.kt);
+        kvh = off / one;
+        const int in = off - kvh * one;
+        int hi = len.kt - 1;
+        while (kt < hi) {   // the key tile that holds step `in` of the head
+            const int mid = (kt + hi + 1) / 2;
+            if (weigh_before(len, mid) <= in)
+                kt = mid;
+            else
+                hi = mid - 1;
         }
-        return false;
+        s = in - weigh_before(len, kt);
+    }
+
+    __host__ __device__ __forceinline__ bool next(const WeighShape &sh, WeighSeg &g)
+    {
+        if (left <= 0) return false;
+        if (kt == len.kt) {
+            kt = 0;
+            if (++kvh == sh.Hkv) {
+                kvh = 0;
+                do {
+                    if (++b >= sh.B) return false;
+                    len = weigh_len(sh, b);
+                } while (len.kt == 0);
+            }
+        }
+        g.b = b;
+        g.kvh = kvh;
+        g.kt = kt;
+        g.len = len;
+        g.first = weigh_first(len, kt);
+        g.ns = len.qt == 0 ? 1 : len.planes * (len.qt - g.first);
+        g.s0 = s;
+        g.s1 = g.ns - s < left ? g.ns : s + left;
+        left -= g.s1 - g.s0;
+        s = 0;
+        ++kt;
+        return true;
     }
 };
 

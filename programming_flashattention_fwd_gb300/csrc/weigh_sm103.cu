@@ -68,8 +68,8 @@ struct Cfg {
 struct Misc {
     uint32_t tmem;
     int abort;
-    int lowest[2 * NB];      // lowest limit of each half of a step's rows
-    WeighWalk walk;
+    int lowest[NB], cols[NB];   // of each step in flight: lowest limit of its rows, how many rows
+    int b, off, left;           // this CTA's share
 };
 
 template <int D, bool BF16>
@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         for (int i = 0; i < NB; ++i) {
             mbar_init(barS + 8 * i, 1);
-            mbar_init(barRows + 8 * i, 2);
+            mbar_init(barRows + 8 * i, 1);
             mbar_init(barFree + 8 * i, 4);
         }
         for (int i = 0; i < 2; ++i) {
@@ -137,16 +137,16 @@ __global__ void __launch_bounds__(THREADS, 1)
             return p.s.Hkv * weigh_before(l, l.kt);
         });
         if (lane == 0) {
-            misc->walk.b = w.b;
-            misc->walk.off = w.off;
-            misc->walk.left = w.left;
+            misc->b = w.b;
+            misc->off = w.off;
+            misc->left = w.left;
         }
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = misc->tmem;
-    WeighWalk walk{misc->walk.b, misc->walk.off, misc->walk.left};
+    WeighWalk walk(p.s, misc->b, misc->off, misc->left);
     WeighSeg g;
 
     auto wait_all = [&](uint32_t bar, uint32_t parity, uint32_t site) -> bool {
@@ -189,18 +189,17 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             ++ku;
             if (gather) continue;
-            for (int s = g.s0; ok && s < g.s1; ++s) {
-                int plane, qt;
-                g.tile(s, plane, qt);
-                if (!at.change(g.b, g.kvh, plane, qt)) continue;
+            WeighTiles t(g);
+            for (int s = g.s0; ok && s < g.s1; ++s, t.next()) {
+                if (!at.change(g.b, g.kvh, t.plane, t.qt)) continue;
                 ok = wait_all(q_empty(qu), ((qu / C::QS) & 1) ^ 1, S_QEMPTY);
                 if (!ok) break;
                 if (lane == 0) {
                     mbar_arrive_expect_tx(q_full(qu), C::QTILE);
 #pragma unroll
                     for (int pq = 0; pq < C::PANELS; ++pq)
-                        tma_load_3d(sQ + (uint32_t)(qu % C::QS) * C::QTILE + pq * C::QPANEL, &maps.q, pq * 64, qt * NQ,
-                                    (g.b * p.s.Hkv + g.kvh) * g.len.planes + plane, q_full(qu));
+                        tma_load_3d(sQ + (uint32_t)(qu % C::QS) * C::QTILE + pq * C::QPANEL, &maps.q, pq * 64, t.qt * NQ,
+                                    (g.b * p.s.Hkv + g.kvh) * g.len.planes + t.plane, q_full(qu));
                 }
                 ++qu;
             }
@@ -223,10 +222,9 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (!ok) break;
             const uint32_t sK = sb + (uint32_t)(ku % C::KS) * C::KTILE;
             ++ku;
-            for (int s = g.s0; s < g.s1; ++s, ++st) {
-                int plane, qt;
-                g.tile(s, plane, qt);
-                if (at.change(g.b, g.kvh, plane, qt)) {
+            WeighTiles t(g);
+            for (int s = g.s0; s < g.s1; ++s, ++st, t.next()) {
+                if (at.change(g.b, g.kvh, t.plane, t.qt)) {
                     if (qu) tc_commit_elect(q_empty(qu - 1));
                     ok = wait_all(q_full(qu), (qu / C::QS) & 1, S_QFULL);
                     if (!ok) break;
@@ -237,7 +235,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (!ok) break;
                 tc_fence_after();
                 // columns: the rows of this tile, to the next multiple of 16
-                const int cols = max(16, min(NQ, (g.len.rows - qt * NQ + 15) & ~15));
+                const int cols = max(16, min(NQ, (g.len.rows - t.qt * NQ + 15) & ~15));
                 const uint32_t id = idesc_f16(BF16, 128, 16, false) + ((uint32_t)(cols - 16) >> 3 << 17);
                 const uint32_t sq = sQ + (uint32_t)((qu - 1) % C::QS) * C::QTILE;
 #pragma unroll
@@ -252,29 +250,34 @@ __global__ void __launch_bounds__(THREADS, 1)
         __syncwarp();
     } else if (warp < 4) {
         // ------------------------------------------------------------ rows: lse, limits, gathered queries
+        // The two warps take alternate steps, a lane four neighbouring rows; what a tile's rows need is
+        // looked up once while consecutive steps use it.
         const int half = warp - 2;
         int qu = 0;
         uint32_t st = 0;
-        bool ok = true;
+        bool ok = true, fresh = true;
         Tile at;
+        float neg[4] = {0.f, 0.f, 0.f, 0.f};      // -lse, log2 units
+        int limit[4] = {0, 0, 0, 0}, low = 0, cols = 0;
         while (ok && walk.next(p.s, g)) {
             const size_t head0 = (size_t)(g.b * p.s.Hkv + g.kvh) * p.s.group;   // first query head of the group
-            for (int s = g.s0; s < g.s1; ++s, ++st) {
-                int plane, qt;
-                g.tile(s, plane, qt);
-                if (at.change(g.b, g.kvh, plane, qt) && gather) {
+            WeighTiles t(g);
+            for (int s = g.s0; s < g.s1; ++s, ++st, t.next()) {
+                const bool changed = at.change(g.b, g.kvh, t.plane, t.qt);
+                fresh |= changed;
+                if (changed && gather) {
                     ok = wait_all(q_empty(qu), ((qu / C::QS) & 1) ^ 1, S_QEMPTY);
                     if (!ok) break;
                     const uint32_t dst = sQ + (uint32_t)(qu % C::QS) * C::QTILE;
                     // rows to the next multiple of 16; 16-byte chunk c of row r at c ^ (r & 7) of its 128 bytes
-                    const int rows = min(NQ, max(16, (g.len.rows - qt * NQ + 15) & ~15));
+                    const int rows = min(NQ, max(16, (g.len.rows - t.qt * NQ + 15) & ~15));
                     for (int x = threadIdx.x - 64; x < rows * (D / 8); x += 64) {
-                        const int r = x / (D / 8), ch = x % (D / 8), row = qt * NQ + r;
+                        const int r = x / (D / 8), ch = x % (D / 8), row = t.qt * NQ + r;
                         uint4 v = make_uint4(0, 0, 0, 0);
                         if (row < g.len.rows) {
-                            const int h = row / g.len.a, t = __ldg(p.path + (size_t)g.b * p.s.T + (row - h * g.len.a));
-                            if (t >= 0 && t < p.s.T)
-                                v = __ldg(reinterpret_cast<const uint4 *>(p.q) + ((head0 + h) * p.s.T + t) * (D / 8) + ch);
+                            const int h = row / g.len.a, i = __ldg(p.path + (size_t)g.b * p.s.T + (row - h * g.len.a));
+                            if (i >= 0 && i < p.s.T)
+                                v = __ldg(reinterpret_cast<const uint4 *>(p.q) + ((head0 + h) * p.s.T + i) * (D / 8) + ch);
                         }
                         st_shared_v4(dst + (ch >> 3) * C::QPANEL + r * 128 + (((ch & 7) ^ (r & 7)) << 4), v.x, v.y, v.z, v.w);
                     }
@@ -283,47 +286,50 @@ __global__ void __launch_bounds__(THREADS, 1)
                     if (lane == 0) mbar_arrive(q_full(qu));
                     ++qu;
                 }
-                const uint32_t bi = st % NB;
-                float lse2[2];
-                int limit[2], low = 0x7fffffff;
+                if ((int)(st & 1) != half) continue;
+                if (fresh) {
+                    fresh = false;
+                    low = 0x7fffffff;
+                    cols = min(NQ, g.len.rows - t.qt * NQ);
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int c = half * 64 + 32 * e + lane, row = qt * NQ + c;
-                    int i = -1, h = plane, t = 0;      // order of the row, its head in the group, its place in q
-                    if (c < NQ && row < g.len.rows) {
-                        if (p.s.mode == kHeads) {
-                            i = t = row;
-                        } else if (p.s.mode == kRows) {
-                            h = row / p.s.T;
-                            i = t = row - h * p.s.T;
-                            if (i >= g.len.a) i = -1;
-                        } else {
-                            h = row / g.len.a;
-                            i = row - h * g.len.a;
-                            t = __ldg(p.path + (size_t)g.b * p.s.T + i);
-                            if (t < 0 || t >= p.s.T) i = -1;
+                    for (int e = 0; e < 4; ++e) {
+                        const int c = 4 * lane + e, row = t.qt * NQ + c;
+                        int i = -1, h = t.plane, x = 0;      // order of the row, its head in the group, its place in q
+                        if (c < cols) {
+                            if (p.s.mode == kHeads) {
+                                i = x = row;
+                            } else if (p.s.mode == kRows) {
+                                h = row / p.s.T;
+                                i = x = row - h * p.s.T;
+                                if (i >= g.len.a) i = -1;
+                            } else {
+                                h = row / g.len.a;
+                                i = row - h * g.len.a;
+                                x = __ldg(p.path + (size_t)g.b * p.s.T + i);
+                                if (x < 0 || x >= p.s.T) i = -1;
+                            }
                         }
+                        limit[e] = 0;
+                        neg[e] = 0.f;
+                        if (i >= 0) {
+                            const float v = __ldg(p.lse + (head0 + h) * p.s.T + x);
+                            neg[e] = v * -1.4426950408889634f;
+                            // a row that saw nothing gave nothing
+                            limit[e] = v == -INFINITY ? 0 : (p.s.causal ? clampi(g.len.off + i + 1, 0, g.len.n) : g.len.n);
+                        }
+                        if (c < NQ) low = min(low, limit[e]);
                     }
-                    limit[e] = 0;
-                    lse2[e] = 0.f;
-                    if (i >= 0) {
-                        const float v = __ldg(p.lse + (head0 + h) * p.s.T + t);
-                        lse2[e] = v * 1.4426950408889634f;
-                        // a row that saw nothing gave nothing
-                        limit[e] = v == -INFINITY ? 0 : (p.s.causal ? clampi(g.len.off + i + 1, 0, g.len.n) : g.len.n);
-                    }
-                    low = min(low, limit[e]);
+                    low = __reduce_min_sync(~0u, low);
                 }
-                low = __reduce_min_sync(~0u, low);
+                const uint32_t bi = st % NB;
                 ok = wait_all(barFree + 8u * bi, ((st / NB) & 1) ^ 1, S_FREE);
                 if (!ok) break;
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int c = half * 64 + 32 * e + lane;
-                    rows_lse[bi * 256 + c] = lse2[e];
-                    reinterpret_cast<int *>(rows_lse)[bi * 256 + 128 + c] = limit[e];
+                reinterpret_cast<float4 *>(rows_lse + bi * 256)[lane] = make_float4(neg[0], neg[1], neg[2], neg[3]);
+                reinterpret_cast<int4 *>(rows_lse + bi * 256 + 128)[lane] = make_int4(limit[0], limit[1], limit[2], limit[3]);
+                if (lane == 0) {
+                    misc->lowest[bi] = low;
+                    misc->cols[bi] = cols;
                 }
-                if (lane == 0) misc->lowest[bi * 2 + half] = low;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(barRows + 8u * bi);
             }
@@ -345,30 +351,24 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (grp == owner && whole && live && p.weight) base = p.weight[at];
             for (int s = (int)((st0 ^ (uint32_t)grp) & 1u); s < ns; s += 2) {
                 const uint32_t st = st0 + s, bi = st % NB, ph = (st / NB) & 1;
-                int plane, qt;
-                g.tile(g.s0 + s, plane, qt);
                 ok = wait_all(barRows + 8u * bi, ph, S_ROWS) && wait_all(barS + 8u * bi, ph, S_S);
                 if (!ok) break;
                 tc_fence_after();
-                const float *lse2 = rows_lse + bi * 256;
-                const int *limit = reinterpret_cast<const int *>(lse2) + 128;
-                const int cols = min(NQ, g.len.rows - qt * NQ);
-                const bool masked = cols < NQ || min(misc->lowest[2 * bi], NQ > 64 ? misc->lowest[2 * bi + 1] : 0x7fffffff) < g.kt * 128 + 128;
+                const float *neg = rows_lse + bi * 256;
+                const int *limit = reinterpret_cast<const int *>(neg) + 128;
+                const uint32_t tS = tmem + lane_off + bi * 128u;
+                const int cols = misc->cols[bi];
                 uint64_t sum2[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) sum2[i] = f2_pack(0.f, 0.f);
-#pragma unroll 1
-                for (int c = 0; c < cols; c += 32) {
-                    uint32_t sv[32];
-                    tmem_ld_x32(tmem + lane_off + bi * 128u + c, sv);
-                    tmem_wait_ld();
-                    reg_fence_x32(sv);
+                // 32 columns: exp2(s sl2 - lse2), two columns to an instruction but for the exponential
+                auto add = [&](const uint32_t(&sv)[32], int c, bool masked) {
 #pragma unroll
                     for (int e = 0; e < 32; e += 4) {
-                        const float4 l = *reinterpret_cast<const float4 *>(lse2 + c + e);
+                        const ulonglong2 l = *reinterpret_cast<const ulonglong2 *>(neg + c + e);
                         float x[4];
-                        f2_unpack(f2_fma(f2_pack(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1])), sl2x2, f2_pack(-l.x, -l.y)), x[0], x[1]);
-                        f2_unpack(f2_fma(f2_pack(__uint_as_float(sv[e + 2]), __uint_as_float(sv[e + 3])), sl2x2, f2_pack(-l.z, -l.w)), x[2], x[3]);
+                        f2_unpack(f2_fma(f2_pack(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1])), sl2x2, l.x), x[0], x[1]);
+                        f2_unpack(f2_fma(f2_pack(__uint_as_float(sv[e + 2]), __uint_as_float(sv[e + 3])), sl2x2, l.y), x[2], x[3]);
 #pragma unroll
                         for (int i = 0; i < 4; ++i) x[i] = ex2_approx(x[i]);
                         if (masked) {
@@ -380,6 +380,35 @@ __global__ void __launch_bounds__(THREADS, 1)
                         }
                         sum2[(e >> 1) & 3] = f2_add(sum2[(e >> 1) & 3], f2_pack(x[0], x[1]));
                         sum2[((e >> 1) + 1) & 3] = f2_add(sum2[((e >> 1) + 1) & 3], f2_pack(x[2], x[3]));
+                    }
+                };
+                if (misc->lowest[bi] >= g.kt * 128 + 128) {
+                    // every row sees the whole key tile: the next 32 columns are read while these are summed
+                    uint32_t va[32], vb[32];
+                    tmem_ld_x32(tS, va);
+                    tmem_wait_ld();
+                    reg_fence_x32(va);
+#pragma unroll
+                    for (int c = 0; c < NQ; c += 64) {
+                        tmem_ld_x32(tS + c + 32, vb);
+                        add(va, c, false);
+                        tmem_wait_ld();
+                        reg_fence_x32(vb);
+                        if (c + 64 < NQ) tmem_ld_x32(tS + c + 64, va);
+                        add(vb, c + 32, false);
+                        if (c + 64 < NQ) {
+                            tmem_wait_ld();
+                            reg_fence_x32(va);
+                        }
+                    }
+                } else {
+#pragma unroll 1
+                    for (int c = 0; c < cols; c += 32) {
+                        uint32_t sv[32];
+                        tmem_ld_x32(tS + c, sv);
+                        tmem_wait_ld();
+                        reg_fence_x32(sv);
+                        add(sv, c, true);
                     }
                 }
                 tc_fence_before();
@@ -417,7 +446,6 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
     }
 
-    const WeighWalk share{misc->walk.b, misc->walk.off, misc->walk.left};
     tc_fence_before();
     __syncthreads();
     if (warp == 1) {
@@ -427,7 +455,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     } else if (warp >= 4 && warp < 8 && *abort_flag) {
         // This CTA gave up on a wait: NaN into every sum it was given
         const int r = threadIdx.x - 128;
-        walk = share;
+        walk = WeighWalk(p.s, misc->b, misc->off, misc->left);
         while (walk.next(p.s, g)) {
             if (g.kt * 128 + r >= g.len.n) continue;
             if (g.s0 == 0 && g.s1 == g.ns)
@@ -447,9 +475,10 @@ __global__ void __launch_bounds__(128) weigh_join_kernel(const __grid_constant__
         const WeighLen l = weigh_len(p.s, b);
         return p.s.Hkv * weigh_before(l, l.kt);
     });
-    WeighWalk w{sh.b, sh.off, sh.left};
+    if (k >= sh.G) return;
+    WeighWalk w(p.s, sh.b, sh.off, sh.left);
     WeighSeg g;
-    if (k >= sh.G || !w.next(p.s, g) || g.s0 == 0) return;
+    if (!w.next(p.s, g) || g.s0 == 0) return;
     const int u0 = cut(sh.total, sh.G, k) - g.s0, u1 = u0 + g.ns;
     if (cut(sh.total, sh.G, k - 1) > u0) return;          // an earlier cut of the same key tile
     int parts = 2;

@@ -150,15 +150,15 @@ static int check_weigh()
             const int begin = cut(total, G, c);
             int b = 0;
             while (b + 1 < s.B && base[b + 1] <= begin) ++b;
-            WeighWalk w{b, begin - base[b], cut(total, G, c + 1) - begin};
+            WeighWalk w(s, b, begin - base[b], cut(total, G, c + 1) - begin);
             WeighSeg g;
             while (w.next(s, g)) {
                 const long long id = ((long long)g.b * s.Hkv + g.kvh) * 100000 + g.kt;
                 if (g.s0 < 0 || g.s1 <= g.s0 || g.s1 > g.ns || g.kt * 128 >= g.len.n) return fail("a segment outside its unit");
-                for (int i = g.s0; i < g.s1; ++i) {
+                WeighTiles t(g);
+                for (int i = g.s0; i < g.s1; ++i, t.next()) {
                     if (!seen[id].insert(i).second) return fail("a step given twice");
-                    int plane, qt;
-                    g.tile(i, plane, qt);
+                    const int plane = t.plane, qt = t.qt;
                     if (plane < 0 || plane >= g.len.planes || qt < 0 || (g.len.qt && qt >= g.len.qt)) return fail("a query tile");
                     tiles[id].insert({plane, qt});
                 }
