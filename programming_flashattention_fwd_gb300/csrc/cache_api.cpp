@@ -240,7 +240,7 @@ int fa_cache_append(const fa_cache_t *cache, const void *k_new, const void *v_ne
     return launch_append(p, (int)blocks, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
 }
 
-size_t fa_weights_workspace_bytes(void) { return (size_t)2 * kMaxCtas * 128 * 4; }
+size_t fa_weights_workspace_bytes(void) { return (size_t)2 * kMaxCtas * 256 * 4; }
 
 int fa_cache_weights(const fa_cache_t *cache, const void *q, const float *lse, const int32_t *path, const int32_t *count,
                      const float *weight, float *out, int Hq, int T, int causal, float scale, void *workspace,
@@ -282,7 +282,7 @@ int fa_cache_weights(const fa_cache_t *cache, const void *q, const float *lse, c
     WeighParams p;
     std::memset(&p, 0, sizeof(p));
     const int mode = path ? kPath : (T >= 128 ? kHeads : kRows);
-    p.s = WeighShape{B, Hkv, group, T, mode, causal, NQ, cap, cache->seq_len, count};
+    p.s = WeighShape{B, Hkv, group, T, mode, causal, NQ, mode == kHeads ? 256 : 128, cap, cache->seq_len, count};
     p.pages = pages_of(cache);
     p.q = q;
     p.lse = lse;

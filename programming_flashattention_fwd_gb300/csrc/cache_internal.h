@@ -54,7 +54,7 @@ struct WeighParams {
     const int32_t *path;      // [B, T] (kPath)
     const float *weight;      // [B, Hkv, capacity] or null: zero
     float *out;               // [B, Hkv, capacity]
-    float *part;              // [2 * kMaxCtas][128]
+    float *part;              // [2 * kMaxCtas][256]
     int box_rows;
     int least;
     float sl2;

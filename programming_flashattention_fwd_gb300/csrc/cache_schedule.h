@@ -94,7 +94,7 @@ struct TreeWalk {
 __host__ __device__ __forceinline__ int part_slot(int c, int k0) { return 2 * c + (k0 == 0 ? 1 : 0); }
 
 // ---------------------------------------------------------------- accumulated attention weight
-// A unit is one 128-slot key tile of (sequence, KV head); its steps are the tiles of NQ query rows
+// A unit is one key tile of `keys` slots of (sequence, KV head); its steps are the tiles of NQ query rows
 // that see any of it.  The rows come in `planes` of a KV head:
 //   heads    one plane a query head, rows in the order of their slots: with the causal mask the tiles
 //            before the first row that sees the key tile are left out (long prompts)
@@ -106,6 +106,7 @@ struct WeighShape {
     int B, Hkv, group, T;
     int mode, causal;
     int NQ;                      // query rows of a step
+    int keys;                    // slots of a key tile: 256 in kHeads mode, else 128
     int capacity;
     const int32_t *seq_len;      // [B]
     const int32_t *count;        // [B] or null: T
@@ -127,11 +128,11 @@ __host__ __device__ __forceinline__ WeighLen weigh_len(const WeighShape &s, int 
     l.n = clampi(s.seq_len[b], 0, s.capacity);
     l.a = s.count ? clampi(s.count[b], 0, s.T) : s.T;
     l.off = l.n - l.a;
-    l.kt = cdiv(l.n, 128);
+    l.kt = cdiv(l.n, s.keys);
     l.planes = s.mode == kHeads ? s.group : 1;
     l.rows = l.a == 0 ? 0 : (s.mode == kHeads ? l.a : (s.mode == kPath ? s.group * l.a : s.group * s.T));
     l.qt = cdiv(l.rows, s.NQ);
-    l.per = s.mode == kHeads && s.causal ? 128 / s.NQ : 0;
+    l.per = s.mode == kHeads && s.causal ? s.keys / s.NQ : 0;
     l.w = l.off >= 0 ? cdiv(l.off, s.NQ) : -((-l.off) / s.NQ);   // ceil(off / NQ)
     return l;
 }

@@ -22,8 +22,8 @@
 //   warp 0        K producer (one box per page and panel) and, unless rows are gathered, Q producer
 //   warp 1        TMEM owner and MMA issuer, into four S^T buffers
 //   warps 2-3     lse and visible limit of each step's 128 rows; in path mode also the gathered Q tile
-//   warps 4-7,    the sums, one thread per key: the groups take alternate steps and are joined at the
-//   warps 8-11    end of a key tile
+//   warps 4-19    the sums, one thread per key: four groups of four warps take the steps in turn, a
+//                 buffer each, and are joined at the end of a key tile
 // A K or Q tile stays where it is while consecutive steps use it.
 #include <atomic>
 #include <cstdint>
@@ -42,8 +42,8 @@ namespace cache {
 namespace {
 
 constexpr uint64_t kDefaultTimeoutNs = 2000000000ull;
-constexpr int THREADS = 384;
-constexpr int NB = 4;   // S^T buffers, 128 columns apart
+constexpr int NB = 4;   // S^T buffers, 128 columns apart, each with a group of four warps that sums it
+constexpr int THREADS = 128 + 128 * NB;
 
 enum Site : uint32_t { S_KEMPTY = 1, S_QEMPTY = 2, S_KFULL = 3, S_QFULL = 4, S_FREE = 5, S_S = 6, S_ROWS = 7, S_DRAIN = 8, S_SMEM = 9, S_JOIN = 10, S_READ = 11 };
 
@@ -53,13 +53,13 @@ struct Cfg {
     static constexpr int PANELS = D / 64;
     static constexpr int KPANEL = 128 * 128, KTILE = PANELS * KPANEL;
     static constexpr int QPANEL = NQ * 128, QTILE = PANELS * QPANEL;
-    static constexpr int KS = D == 64 ? 6 : (D == 128 ? 3 : 2), QS = D == 64 ? 5 : (D == 128 ? 3 : 2);
+    static constexpr int KS = D == 256 ? 2 : (D == 128 ? 4 : 8), QS = 2;   // K is streamed, Q changes now and then
     static constexpr int OFF_Q = KS * KTILE;
     static constexpr int OFF_BAR = OFF_Q + QS * QTILE;
-    static constexpr int NBAR = 2 * KS + 2 * QS + 3 * NB + 2 + 2 + 1;   // K, Q (full, empty); S, rows, free; join, read; done
+    static constexpr int NBAR = 2 * KS + 2 * QS + 3 * NB + 2 * NB + 1;   // K, Q (full, empty); S, rows, free; join, read; done
     static constexpr int OFF_ROWS = OFF_BAR + ((NBAR * 8 + 15) / 16) * 16;   // NB x { lse2[128], limit[128] }
-    static constexpr int OFF_JOIN = OFF_ROWS + NB * 1024;                    // [2][128] sums of the group that is not last
-    static constexpr int OFF_MISC = OFF_JOIN + 1024;
+    static constexpr int OFF_JOIN = OFF_ROWS + NB * 1024;                    // [NB][128] sums handed over
+    static constexpr int OFF_MISC = OFF_JOIN + NB * 512;
     static constexpr int BYTES = OFF_MISC + 64;
     static constexpr int ALLOC = BYTES + 1024;
     static_assert(ALLOC <= 232448, "shared memory of one CTA");
@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     auto q_full = [&](int u) { return barQ0 + 8u * (u % C::QS); };
     auto q_empty = [&](int u) { return barQ0 + 8u * (C::QS + u % C::QS); };
     const uint32_t barS = barQ0 + 16u * C::QS, barRows = barS + 8u * NB, barFree = barRows + 8u * NB, barJoin = barFree + 8u * NB,
-                   barRead = barJoin + 16, barDone = barRead + 16;
+                   barRead = barJoin + 8u * NB, barDone = barRead + 8u * NB;
     float *rows_lse = reinterpret_cast<float *>(smem + C::OFF_ROWS);
     float *join = reinterpret_cast<float *>(smem + C::OFF_JOIN);
     volatile Misc *misc = reinterpret_cast<volatile Misc *>(smem + C::OFF_MISC);
@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             mbar_init(barRows + 8 * i, 1);
             mbar_init(barFree + 8 * i, 4);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < NB; ++i) {
             mbar_init(barJoin + 8 * i, 4);
             mbar_init(barRead + 8 * i, 4);
         }
@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         constexpr uint32_t HI = sdesc_hi_sw128(1024);
         int ku = 0, qu = 0;      // tiles taken so far
         uint32_t st = 0;         // step: buffer st % NB
-        bool ok = true;
+        bool ok = true, held = false;   // held: the Q tile is to be released when the next one is taken
         Tile at;
         while (ok && walk.next(p.s, g)) {
             if (ku) tc_commit_elect(k_empty(ku - 1));   // the last key tile's products are all issued
@@ -225,10 +225,11 @@ __global__ void __launch_bounds__(THREADS, 1)
             WeighTiles t(g);
             for (int s = g.s0; s < g.s1; ++s, ++st, t.next()) {
                 if (at.change(g.b, g.kvh, t.plane, t.qt)) {
-                    if (qu) tc_commit_elect(q_empty(qu - 1));
+                    if (held) tc_commit_elect(q_empty(qu - 1));
                     ok = wait_all(q_full(qu), (qu / C::QS) & 1, S_QFULL);
                     if (!ok) break;
                     ++qu;
+                    held = true;
                 }
                 const uint32_t bi = st % NB;
                 ok = wait_all(barFree + 8u * bi, ((st / NB) & 1) ^ 1, S_FREE);
@@ -243,6 +244,10 @@ __global__ void __launch_bounds__(THREADS, 1)
                     mma_ss_kk4_elect(tmem + bi * 128u, sdesc_lo(sK + pn * C::KPANEL, 16), sdesc_lo(sq + pn * C::QPANEL, 16), HI, id,
                                      pn ? 1u : 0u);
                 tc_commit_elect(barS + 8u * bi);
+                if (s + 1 < g.s1) {   // the next step of a key tile always has another Q tile
+                    tc_commit_elect(q_empty(qu - 1));
+                    held = false;
+                }
             }
         }
         tc_commit_elect(barDone);
@@ -296,9 +301,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         const int c = 4 * lane + e, row = t.qt * NQ + c;
                         int i = -1, h = t.plane, x = 0;      // order of the row, its head in the group, its place in q
                         if (c < cols) {
-                            if (p.s.mode == kHeads) {
-                                i = x = row;
-                            } else if (p.s.mode == kRows) {
+                            if (p.s.mode == kRows) {
                                 h = row / p.s.T;
                                 i = x = row - h * p.s.T;
                                 if (i >= g.len.a) i = -1;
@@ -340,17 +343,17 @@ __global__ void __launch_bounds__(THREADS, 1)
         const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
         const uint64_t sl2x2 = f2_pack(p.sl2, p.sl2);
         uint32_t st0 = 0;
-        int posts[2] = {0, 0};   // sums handed over so far by each group
+        uint32_t posts = 0;   // parity of the sums that each group has handed over (bit), that it has any (bit + NB)
         bool ok = true;
         while (ok && walk.next(p.s, g)) {
             const int slot = g.kt * 128 + r, ns = g.s1 - g.s0;
             const size_t at = (size_t)(g.b * p.s.Hkv + g.kvh) * p.s.capacity + slot;
             const bool whole = g.s0 == 0 && g.s1 == g.ns, live = slot < g.len.n;
-            const int owner = (int)((st0 + ns - 1) & 1);     // the group of the last step
+            const int owner = (int)((st0 + ns - 1) % NB);    // the group of the last step
             float base = 0.f, sum = 0.f;
             if (grp == owner && whole && live && p.weight) base = p.weight[at];
-            for (int s = (int)((st0 ^ (uint32_t)grp) & 1u); s < ns; s += 2) {
-                const uint32_t st = st0 + s, bi = st % NB, ph = (st / NB) & 1;
+            for (int s = (int)(((uint32_t)grp - st0) % NB); s < ns; s += NB) {
+                const uint32_t st = st0 + s, bi = grp, ph = (st / NB) & 1;
                 ok = wait_all(barRows + 8u * bi, ph, S_ROWS) && wait_all(barS + 8u * bi, ph, S_S);
                 if (!ok) break;
                 tc_fence_after();
@@ -382,34 +385,17 @@ __global__ void __launch_bounds__(THREADS, 1)
                         sum2[((e >> 1) + 1) & 3] = f2_add(sum2[((e >> 1) + 1) & 3], f2_pack(x[2], x[3]));
                     }
                 };
-                if (misc->lowest[bi] >= g.kt * 128 + 128) {
-                    // every row sees the whole key tile: the next 32 columns are read while these are summed
-                    uint32_t va[32], vb[32];
-                    tmem_ld_x32(tS, va);
-                    tmem_wait_ld();
-                    reg_fence_x32(va);
-#pragma unroll
-                    for (int c = 0; c < NQ; c += 64) {
-                        tmem_ld_x32(tS + c + 32, vb);
-                        add(va, c, false);
-                        tmem_wait_ld();
-                        reg_fence_x32(vb);
-                        if (c + 64 < NQ) tmem_ld_x32(tS + c + 64, va);
-                        add(vb, c + 32, false);
-                        if (c + 64 < NQ) {
-                            tmem_wait_ld();
-                            reg_fence_x32(va);
-                        }
-                    }
-                } else {
+                const bool masked = misc->lowest[bi] < g.kt * 128 + 128;   // some row does not see the whole key tile
 #pragma unroll 1
-                    for (int c = 0; c < cols; c += 32) {
-                        uint32_t sv[32];
-                        tmem_ld_x32(tS + c, sv);
-                        tmem_wait_ld();
-                        reg_fence_x32(sv);
+                for (int c = 0; c < cols; c += 32) {
+                    uint32_t sv[32];
+                    tmem_ld_x32(tS + c, sv);
+                    tmem_wait_ld();
+                    reg_fence_x32(sv);
+                    if (masked)
                         add(sv, c, true);
-                    }
+                    else
+                        add(sv, c, false);
                 }
                 tc_fence_before();
                 __syncwarp();
@@ -419,28 +405,32 @@ __global__ void __launch_bounds__(THREADS, 1)
                 sum += la + lb;
             }
             if (!ok) break;
-            if (ns > 1) {
-                // the other group hands its sum to the owner of the last step
-                const int other = owner ^ 1, post = posts[other]++;
+            // the other groups of the segment hand their sums to the owner of its last step, which adds
+            // them in the order of their steps
+            for (int x = ns < NB ? ns - 1 : NB - 1; ok && x > 0; --x) {
+                const int other = (owner - x + NB) % NB;
+                const uint32_t par = (posts >> other) & 1u, any = (posts >> (NB + other)) & 1u;
+                posts = (posts ^ (1u << other)) | (1u << (NB + other));
                 if (grp == other) {
-                    if (post > 0) ok = wait_all(barRead + 8u * other, (post - 1) & 1, S_READ);
+                    if (any) ok = wait_all(barRead + 8u * other, par ^ 1u, S_READ);
                     if (!ok) break;
                     join[other * 128 + r] = sum;
                     __syncwarp();
                     if (lane == 0) mbar_arrive(barJoin + 8u * other);
-                } else {
-                    ok = wait_all(barJoin + 8u * other, post & 1, S_JOIN);
+                } else if (grp == owner) {
+                    ok = wait_all(barJoin + 8u * other, par, S_JOIN);
                     if (!ok) break;
                     sum += join[other * 128 + r];
                     __syncwarp();
                     if (lane == 0) mbar_arrive(barRead + 8u * other);
                 }
             }
+            if (!ok) break;
             if (grp == owner && live) {
                 if (whole)
                     p.out[at] = base + sum;
                 else
-                    p.part[(size_t)part_slot(blockIdx.x, g.s0) * 128 + r] = sum;
+                    p.part[(size_t)part_slot(blockIdx.x, g.s0) * 256 + r] = sum;
             }
             st0 += ns;
         }
@@ -461,14 +451,379 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (g.s0 == 0 && g.s1 == g.ns)
                 p.out[(size_t)(g.b * p.s.Hkv + g.kvh) * p.s.capacity + g.kt * 128 + r] = __uint_as_float(~0u);
             else
-                p.part[(size_t)part_slot(blockIdx.x, g.s0) * 128 + r] = __uint_as_float(~0u);
+                p.part[(size_t)part_slot(blockIdx.x, g.s0) * 256 + r] = __uint_as_float(~0u);
+        }
+    }
+}
+
+// ---------------------------------------------------------------- long prompts
+// Every query row against every earlier slot: bound by the tensor pipe and the exponentials, if the
+// operands keep up.  With K and Q both in shared memory the products alone read 64 KB of it per 128 x 128
+// scores at D = 128, all that it delivers in the 512 cycles of the products, and each Q tile is fetched for
+// one key tile only.  So a unit is two key tiles, copied into tensor memory once and used as the A operand
+// (lanes = keys), and each Q tile is multiplied with both: 48 KB of shared-memory traffic per 128 x 128
+// scores, the Q tile's own arrival included.
+//   tensor memory   K_0, K_1 (D / 2 columns each), then NBUF score buffers of NQ columns
+//   warps 0, 1, 2-3 as above;  warps 4-7 and 8-11 the sums of the first and the second key tile
+template <int D>
+struct Prompt {
+    static constexpr int THREADS = 384;
+    static constexpr int NQ = D == 256 ? 64 : 128;
+    static constexpr int NBUF = D == 256 ? 4 : 3;     // score buffers
+    static constexpr int NR = 4;                       // steps whose rows are looked up ahead
+    static constexpr int PANELS = D / 64;
+    static constexpr int KPANEL = 256 * 128, KPAIR = PANELS * KPANEL;   // both key tiles, 256 rows to a panel
+    static constexpr int QPANEL = NQ * 128, QTILE = PANELS * QPANEL;
+    static constexpr int QS = D == 256 ? 2 : (D == 128 ? 4 : 8);
+    static constexpr int OFF_Q = KPAIR;
+    static constexpr int OFF_BAR = OFF_Q + QS * QTILE;
+    static constexpr int NBAR = 2 + 2 * QS + 2 * NBUF + 2 * NR + 2;     // K, Q (full, empty); S (full, free); rows (full, free); unit, done
+    static constexpr int OFF_ROWS = OFF_BAR + ((NBAR * 8 + 15) / 16) * 16;   // NR x { -lse2[128], limit[128] }
+    static constexpr int OFF_MISC = OFF_ROWS + NR * 1024;
+    static constexpr int BYTES = OFF_MISC + 64;
+    static constexpr int ALLOC = BYTES + 1024;
+    static_assert(ALLOC <= 232448, "shared memory of one CTA");
+    static constexpr uint32_t COL_S = D;               // the scores start behind the two key tiles
+    static_assert(D + NBUF * NQ <= 512, "tensor-memory columns");
+};
+
+// One 64-column panel of 128 rows, 128-byte swizzled, into 32 tensor-memory columns (lane = row).
+__device__ __forceinline__ void copy_panel_elect(uint32_t t, uint32_t lo, uint32_t hi)
+{
+    asm volatile("{\n\t.reg .b32 ta, al;\n\t.reg .b64 a;\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+                 "mov.b64 a, {%1, %2};\n\t@e tcgen05.cp.cta_group::1.128x256b [%0], a;\n\t"
+                 "add.u32 ta, %0, 8;\n\tadd.u32 al, %1, 2;\n\tmov.b64 a, {al, %2};\n\t@e tcgen05.cp.cta_group::1.128x256b [ta], a;\n\t"
+                 "add.u32 ta, %0, 16;\n\tadd.u32 al, %1, 4;\n\tmov.b64 a, {al, %2};\n\t@e tcgen05.cp.cta_group::1.128x256b [ta], a;\n\t"
+                 "add.u32 ta, %0, 24;\n\tadd.u32 al, %1, 6;\n\tmov.b64 a, {al, %2};\n\t@e tcgen05.cp.cta_group::1.128x256b [ta], a;\n\t}"
+                 ::"r"(t), "r"(lo), "r"(hi)
+                 : "memory");
+}
+
+// Four K-steps of D(tmem) (+)= A(tmem) B(smem, K-major).
+__device__ __forceinline__ void mma_ts_k4_elect(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t hi, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile("{\n\t.reg .b32 ta, bl;\n\t.reg .b64 b;\n\t.reg .pred p, e, t;\n\t"
+                 "setp.ne.b32 p, %5, 0;\n\tsetp.eq.b32 t, 0, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+                 "mov.b64 b, {%2, %3};\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t"
+                 "add.u32 ta, %1, 8;\n\tadd.u32 bl, %2, 2;\n\tmov.b64 b, {bl, %3};\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [ta], b, %4, t;\n\t"
+                 "add.u32 ta, %1, 16;\n\tadd.u32 bl, %2, 4;\n\tmov.b64 b, {bl, %3};\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [ta], b, %4, t;\n\t"
+                 "add.u32 ta, %1, 24;\n\tadd.u32 bl, %2, 6;\n\tmov.b64 b, {bl, %3};\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [ta], b, %4, t;\n\t}"
+                 ::"r"(d), "r"(a), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate)
+                 : "memory");
+}
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(Prompt<D>::THREADS, 1)
+    weigh_prompt_kernel(const __grid_constant__ WeighMaps maps, const __grid_constant__ WeighParams p)
+{
+    using C = Prompt<D>;
+    constexpr int NQ = C::NQ;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t pad = (1024u - (raw & 1023u)) & 1023u;
+    uint8_t *smem = smem_raw + pad;
+    const uint32_t sb = raw + pad;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t sQ = sb + C::OFF_Q, bar0 = sb + C::OFF_BAR;
+    const uint32_t barK = bar0, barKfree = bar0 + 8;
+    auto q_full = [&](int u) { return bar0 + 8u * (2 + u % C::QS); };
+    auto q_empty = [&](int u) { return bar0 + 8u * (2 + C::QS + u % C::QS); };
+    const uint32_t barS0 = bar0 + 8u * (2 + 2 * C::QS);
+    auto s_full = [&](uint32_t t) { return barS0 + 8u * (t % C::NBUF); };
+    auto s_free = [&](uint32_t t) { return barS0 + 8u * (C::NBUF + t % C::NBUF); };
+    const uint32_t barR0 = barS0 + 16u * C::NBUF;
+    auto r_full = [&](uint32_t s) { return barR0 + 8u * (s % C::NR); };
+    auto r_free = [&](uint32_t s) { return barR0 + 8u * (C::NR + s % C::NR); };
+    const uint32_t barUnit = barR0 + 16u * C::NR, barDone = barUnit + 8;
+    float *rows_lse = reinterpret_cast<float *>(smem + C::OFF_ROWS);
+    volatile Misc *misc = reinterpret_cast<volatile Misc *>(smem + C::OFF_MISC);
+    volatile int *abort_flag = &misc->abort;
+    unsigned int *status = &g_weigh_status;
+    const uint64_t tmo = p.timeout_ns;
+
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (pad + (uint32_t)C::BYTES > dynamic_smem_size_u32()) {
+        if (threadIdx.x == 0) atomicOr(status, 1u | (S_SMEM << 8));
+        return;
+    }
+    if (threadIdx.x == 0) {
+        mbar_init(barK, 1);
+        mbar_init(barKfree, 1);
+        for (int s = 0; s < C::QS; ++s) {
+            mbar_init(q_full(s), 1);
+            mbar_init(q_empty(s), 1);
+        }
+        for (int i = 0; i < C::NBUF; ++i) {
+            mbar_init(s_full(i), 1);
+            mbar_init(s_free(i), 4);
+        }
+        for (int i = 0; i < C::NR; ++i) {
+            mbar_init(r_full(i), 1);
+            mbar_init(r_free(i), 8);
+        }
+        mbar_init(barUnit, 1);
+        mbar_init(barDone, 1);
+        misc->abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(const_cast<uint32_t *>(&misc->tmem)), 512);
+        tmem_relinquish();
+    }
+    if (warp == 3) {
+        const Share w = find_share(p.s.B, p.least, lane, blockIdx.x, gridDim.x, [&](int b) {
+            const WeighLen l = weigh_len(p.s, b);
+            return p.s.Hkv * weigh_before(l, l.kt);
+        });
+        if (lane == 0) {
+            misc->b = w.b;
+            misc->off = w.off;
+            misc->left = w.left;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = misc->tmem;
+    WeighWalk walk(p.s, misc->b, misc->off, misc->left);
+    WeighSeg g;
+
+    auto wait_all = [&](uint32_t bar, uint32_t parity, uint32_t site) -> bool {
+        return __all_sync(0xffffffffu, bounded_wait(bar, parity, abort_flag, tmo, site, status)) != 0;
+    };
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ K producer, Q producer
+        const int boxes = 256 / p.box_rows;
+        int unit = 0, qu = 0;
+        bool ok = true;
+        for (; ok && walk.next(p.s, g); ++unit) {
+            if (unit) ok = wait_all(barKfree, (unit - 1) & 1, S_KEMPTY);
+            if (!ok) break;
+            const int valid = min(boxes, cdiv(g.len.n - g.kt * 256, p.box_rows));
+            if (lane == 0) mbar_arrive_expect_tx(barK, (uint32_t)(valid * p.box_rows * 128 * C::PANELS));
+            __syncwarp();
+            for (int i = lane; i < valid * C::PANELS; i += 32) {
+                const int box = i / C::PANELS, pn = i % C::PANELS;
+                int pid, row;
+                page_of(p.pages, g.b, g.kt * 256 + box * p.box_rows, pid, row);
+                load_page(sb + (uint32_t)(pn * C::KPANEL + box * p.box_rows * 128), &maps.k, pn * 64, row, g.kvh, pid, barK);
+            }
+            WeighTiles t(g);
+            for (int s = g.s0; s < g.s1; ++s, t.next(), ++qu) {
+                ok = wait_all(q_empty(qu), ((qu / C::QS) & 1) ^ 1, S_QEMPTY);
+                if (!ok) break;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(q_full(qu), C::QTILE);
+#pragma unroll
+                    for (int pq = 0; pq < C::PANELS; ++pq)
+                        tma_load_3d(sQ + (uint32_t)(qu % C::QS) * C::QTILE + pq * C::QPANEL, &maps.q, pq * 64, t.qt * NQ,
+                                    (g.b * p.s.Hkv + g.kvh) * g.len.planes + t.plane, q_full(qu));
+                }
+            }
+        }
+        if (lane == 0) {
+            if (unit) bounded_wait(barK, (unit - 1) & 1, abort_flag, tmo, S_DRAIN, status, false);
+            for (int x = max(0, qu - C::QS); x < qu; ++x) bounded_wait(q_full(x), (x / C::QS) & 1, abort_flag, tmo, S_DRAIN, status, false);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA issuer (whole warp)
+        constexpr uint32_t HI = sdesc_hi_sw128(1024), id = idesc_f16(BF16, 128, NQ, false);
+        int unit = 0, qu = 0;
+        uint32_t t = 0;         // score tile
+        bool ok = true;
+        for (; ok && walk.next(p.s, g); ++unit) {
+            ok = wait_all(barK, unit & 1, S_KFULL);
+            // the products of the unit before, which read K from tensor memory, are done
+            if (ok && unit) ok = wait_all(barUnit, (unit - 1) & 1, S_KEMPTY);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int pn = 0; pn < C::PANELS; ++pn)
+                    copy_panel_elect(tmem + h * (D / 2) + pn * 32, sdesc_lo(sb + pn * C::KPANEL + h * 16384, 16), HI);
+            tc_commit_elect(barKfree);
+            for (int s = g.s0; s < g.s1; ++s, ++qu) {
+                ok = wait_all(q_full(qu), (qu / C::QS) & 1, S_QFULL);
+                if (!ok) break;
+                const uint32_t sq = sQ + (uint32_t)(qu % C::QS) * C::QTILE;
+#pragma unroll
+                for (int h = 0; h < 2; ++h, ++t) {
+                    ok = wait_all(s_free(t), ((t / C::NBUF) & 1) ^ 1, S_FREE);
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int pn = 0; pn < C::PANELS; ++pn)
+                        mma_ts_k4_elect(tmem + C::COL_S + (t % C::NBUF) * NQ, tmem + h * (D / 2) + pn * 32, sdesc_lo(sq + pn * C::QPANEL, 16),
+                                        HI, id, pn ? 1u : 0u);
+                    tc_commit_elect(s_full(t));
+                }
+                if (!ok) break;
+                tc_commit_elect(q_empty(qu));
+            }
+            tc_commit_elect(barUnit);
+        }
+        tc_commit_elect(barDone);
+        bounded_wait(barDone, 0, abort_flag, tmo, S_DRAIN, status, false);
+        __syncwarp();
+    } else if (warp < 4) {
+        // ------------------------------------------------------------ rows: lse and limits, alternate steps
+        uint32_t st = 0;
+        bool ok = true;
+        while (ok && walk.next(p.s, g)) {
+            const size_t head0 = (size_t)(g.b * p.s.Hkv + g.kvh) * p.s.group;
+            WeighTiles t(g);
+            for (int s = g.s0; s < g.s1; ++s, ++st, t.next()) {
+                if ((int)(st & 1) != warp - 2) continue;
+                float neg[4];
+                int limit[4], low = 0x7fffffff;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int c = 4 * lane + e, i = t.qt * NQ + c;
+                    neg[e] = 0.f;
+                    limit[e] = 0;
+                    if (c < NQ && i < g.len.a) {
+                        const float v = __ldg(p.lse + (head0 + t.plane) * p.s.T + i);
+                        neg[e] = v * -1.4426950408889634f;
+                        // a row that saw nothing gave nothing
+                        limit[e] = v == -INFINITY ? 0 : (p.s.causal ? clampi(g.len.off + i + 1, 0, g.len.n) : g.len.n);
+                    }
+                    if (c < NQ) low = min(low, limit[e]);
+                }
+                low = __reduce_min_sync(~0u, low);
+                const uint32_t ri = st % C::NR;
+                ok = wait_all(r_free(st), ((st / C::NR) & 1) ^ 1, S_FREE);
+                if (!ok) break;
+                reinterpret_cast<float4 *>(rows_lse + ri * 256)[lane] = make_float4(neg[0], neg[1], neg[2], neg[3]);
+                reinterpret_cast<int4 *>(rows_lse + ri * 256 + 128)[lane] = make_int4(limit[0], limit[1], limit[2], limit[3]);
+                if (lane == 0) misc->lowest[ri] = low;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(r_full(st));
+            }
+        }
+    } else {
+        // ------------------------------------------------------------ sums, one thread per key
+        const int grp = (warp - 4) >> 2, r = (threadIdx.x - 128) & 127;
+        const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+        const uint64_t sl2x2 = f2_pack(p.sl2, p.sl2);
+        uint32_t st = 0;
+        bool ok = true;
+        while (ok && walk.next(p.s, g)) {
+            const int key0 = g.kt * 256 + grp * 128, slot = key0 + r;
+            const size_t at = (size_t)(g.b * p.s.Hkv + g.kvh) * p.s.capacity + slot;
+            const bool whole = g.s0 == 0 && g.s1 == g.ns, live = slot < g.len.n;
+            float base = 0.f, sum = 0.f;
+            if (whole && live && p.weight) base = p.weight[at];
+            for (int s = g.s0; s < g.s1; ++s, ++st) {
+                const uint32_t t = 2 * st + grp, ri = st % C::NR;
+                ok = wait_all(r_full(st), (st / C::NR) & 1, S_ROWS) && wait_all(s_full(t), (t / C::NBUF) & 1, S_S);
+                if (!ok) break;
+                tc_fence_after();
+                const float *neg = rows_lse + ri * 256;
+                const int *limit = reinterpret_cast<const int *>(neg) + 128;
+                const uint32_t tS = tmem + lane_off + C::COL_S + (t % C::NBUF) * NQ;
+                uint64_t sum2[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sum2[i] = f2_pack(0.f, 0.f);
+                // 32 columns: exp2(s sl2 - lse2), two columns to an instruction but for the exponential
+                auto add = [&](const uint32_t(&sv)[32], int c, bool masked) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4) {
+                        const ulonglong2 l = *reinterpret_cast<const ulonglong2 *>(neg + c + e);
+                        float x[4];
+                        f2_unpack(f2_fma(f2_pack(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1])), sl2x2, l.x), x[0], x[1]);
+                        f2_unpack(f2_fma(f2_pack(__uint_as_float(sv[e + 2]), __uint_as_float(sv[e + 3])), sl2x2, l.y), x[2], x[3]);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) x[i] = ex2_approx(x[i]);
+                        if (masked) {
+                            const int4 m = *reinterpret_cast<const int4 *>(limit + c + e);
+                            x[0] = slot < m.x ? x[0] : 0.f;
+                            x[1] = slot < m.y ? x[1] : 0.f;
+                            x[2] = slot < m.z ? x[2] : 0.f;
+                            x[3] = slot < m.w ? x[3] : 0.f;
+                        }
+                        sum2[(e >> 1) & 3] = f2_add(sum2[(e >> 1) & 3], f2_pack(x[0], x[1]));
+                        sum2[((e >> 1) + 1) & 3] = f2_add(sum2[((e >> 1) + 1) & 3], f2_pack(x[2], x[3]));
+                    }
+                };
+                if (misc->lowest[ri] >= key0 + 128) {
+                    // every row sees the whole key tile: the next 32 columns are read while these are summed
+                    uint32_t va[32], vb[32];
+                    tmem_ld_x32(tS, va);
+                    tmem_wait_ld();
+                    reg_fence_x32(va);
+#pragma unroll
+                    for (int c = 0; c < NQ; c += 64) {
+                        tmem_ld_x32(tS + c + 32, vb);
+                        add(va, c, false);
+                        tmem_wait_ld();
+                        reg_fence_x32(vb);
+                        if (c + 64 < NQ) tmem_ld_x32(tS + c + 64, va);
+                        add(vb, c + 32, false);
+                        if (c + 64 < NQ) {
+                            tmem_wait_ld();
+                            reg_fence_x32(va);
+                        }
+                    }
+                } else {
+#pragma unroll 1
+                    for (int c = 0; c < NQ; c += 32) {
+                        uint32_t sv[32];
+                        tmem_ld_x32(tS + c, sv);
+                        tmem_wait_ld();
+                        reg_fence_x32(sv);
+                        add(sv, c, true);
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(s_free(t));
+                    mbar_arrive(r_free(st));
+                }
+                float la, lb;
+                f2_unpack(f2_add(f2_add(sum2[0], sum2[1]), f2_add(sum2[2], sum2[3])), la, lb);
+                sum += la + lb;
+            }
+            if (!ok) break;
+            if (live) {
+                if (whole)
+                    p.out[at] = base + sum;
+                else
+                    p.part[(size_t)part_slot(blockIdx.x, g.s0) * 256 + grp * 128 + r] = sum;
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    } else if (warp >= 4 && *abort_flag) {
+        // This CTA gave up on a wait: NaN into every sum it was given
+        const int r = threadIdx.x - 128;
+        walk = WeighWalk(p.s, misc->b, misc->off, misc->left);
+        while (walk.next(p.s, g)) {
+            const int slot = g.kt * 256 + r;
+            if (slot >= g.len.n) continue;
+            if (g.s0 == 0 && g.s1 == g.ns)
+                p.out[(size_t)(g.b * p.s.Hkv + g.kvh) * p.s.capacity + slot] = __uint_as_float(~0u);
+            else
+                p.part[(size_t)part_slot(blockIdx.x, g.s0) * 256 + r] = __uint_as_float(~0u);
         }
     }
 }
 
 // Adds the parts of the key tiles that a cut crosses, in the order of the steps; block x handles the
 // key tile whose first cut is the start of CTA x + 1.
-__global__ void __launch_bounds__(128) weigh_join_kernel(const __grid_constant__ WeighParams p, int grid)
+__global__ void __launch_bounds__(256) weigh_join_kernel(const __grid_constant__ WeighParams p, int grid)
 {
     const int k = blockIdx.x + 1, lane = threadIdx.x & 31, r = threadIdx.x;
     const Share sh = find_share(p.s.B, p.least, lane, k, grid, [&](int b) {
@@ -483,19 +838,20 @@ __global__ void __launch_bounds__(128) weigh_join_kernel(const __grid_constant__
     if (cut(sh.total, sh.G, k - 1) > u0) return;          // an earlier cut of the same key tile
     int parts = 2;
     while (k + parts - 1 < sh.G && cut(sh.total, sh.G, k + parts - 1) < u1) ++parts;
-    const int slot = g.kt * 128 + r;
+    const int slot = g.kt * p.s.keys + r;
     const size_t at = (size_t)(g.b * p.s.Hkv + g.kvh) * p.s.capacity + slot;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (slot >= g.len.n) return;
+    if (slot >= g.len.n || r >= p.s.keys) return;
     float sum = 0.f;
-    for (int i = 0; i < parts; ++i) sum += p.part[(size_t)part_slot(k - 1 + i, i) * 128 + r];
+    for (int i = 0; i < parts; ++i) sum += p.part[(size_t)part_slot(k - 1 + i, i) * 256 + r];
     p.out[at] = (p.weight ? p.weight[at] : 0.f) + sum;
 }
 
-template <int D, bool BF16>
+template <int D, bool BF16, bool HEADS>
 cudaError_t launch_one(const WeighMaps &m, const WeighParams &p0, cudaStream_t st)
 {
-    auto kern = weigh_kernel<D, BF16>;
+    auto kern = HEADS ? weigh_prompt_kernel<D, BF16> : weigh_kernel<D, BF16>;
+    constexpr int threads = HEADS ? Prompt<D>::THREADS : THREADS, smem = HEADS ? Prompt<D>::ALLOC : Cfg<D>::ALLOC;
     static std::atomic<uint64_t> configured{0};
     static std::atomic<int> sm_count[64];
     int dev = 0;
@@ -504,7 +860,7 @@ cudaError_t launch_one(const WeighMaps &m, const WeighParams &p0, cudaStream_t s
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     const uint64_t bit = 1ull << dev;
     if (!(configured.load(std::memory_order_acquire) & bit)) {
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::ALLOC);
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
         int nsm = 0;
         e = cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev);
@@ -515,12 +871,12 @@ cudaError_t launch_one(const WeighMaps &m, const WeighParams &p0, cudaStream_t s
     WeighParams p = p0;
     if (p.timeout_ns == 0) p.timeout_ns = kDefaultTimeoutNs;
     const int grid = clampi(sm_count[dev].load(std::memory_order_relaxed), 1, kMaxCtas);
-    kern<<<grid, THREADS, Cfg<D>::ALLOC, st>>>(m, p);
+    kern<<<grid, threads, smem, st>>>(m, p);
     e = cudaGetLastError();
     if (e != cudaSuccess || grid == 1) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid - 1);
-    cfg.blockDim = dim3(128);
+    cfg.blockDim = dim3((unsigned)p.s.keys);
     cfg.stream = st;
     cudaLaunchAttribute attr = {};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -536,9 +892,12 @@ int weigh_rows(int D) { return D == 256 ? 64 : 128; }
 
 cudaError_t launch_weigh(int D, bool bf16, const WeighMaps &m, const WeighParams &p, cudaStream_t st)
 {
-    if (D == 64) return bf16 ? launch_one<64, true>(m, p, st) : launch_one<64, false>(m, p, st);
-    if (D == 128) return bf16 ? launch_one<128, true>(m, p, st) : launch_one<128, false>(m, p, st);
-    if (D == 256) return bf16 ? launch_one<256, true>(m, p, st) : launch_one<256, false>(m, p, st);
+#define WEIGH_CASE(DD, BB, HH) \
+    if (D == DD && bf16 == BB && (p.s.mode == kHeads) == HH) return launch_one<DD, BB, HH>(m, p, st);
+    WEIGH_CASE(64, true, true) WEIGH_CASE(64, true, false) WEIGH_CASE(64, false, true) WEIGH_CASE(64, false, false)
+    WEIGH_CASE(128, true, true) WEIGH_CASE(128, true, false) WEIGH_CASE(128, false, true) WEIGH_CASE(128, false, false)
+    WEIGH_CASE(256, true, true) WEIGH_CASE(256, true, false) WEIGH_CASE(256, false, true) WEIGH_CASE(256, false, false)
+#undef WEIGH_CASE
     return cudaErrorInvalidValue;
 }
 

@@ -122,6 +122,7 @@ static int check_weigh()
         s.mode = rnd(3);
         s.causal = rnd(3) != 0;
         s.NQ = rnd(2) ? 128 : 64;
+        s.keys = s.mode == kHeads ? 256 : 128;
         s.capacity = 16 * (1 + rnd(60));
         for (size_t b = 0; b < len.size(); ++b) {
             len[b] = (int)rnd(s.capacity + 20) - 10;
@@ -154,7 +155,7 @@ static int check_weigh()
             WeighSeg g;
             while (w.next(s, g)) {
                 const long long id = ((long long)g.b * s.Hkv + g.kvh) * 100000 + g.kt;
-                if (g.s0 < 0 || g.s1 <= g.s0 || g.s1 > g.ns || g.kt * 128 >= g.len.n) return fail("a segment outside its unit");
+                if (g.s0 < 0 || g.s1 <= g.s0 || g.s1 > g.ns || g.kt * s.keys >= g.len.n) return fail("a segment outside its unit");
                 WeighTiles t(g);
                 for (int i = g.s0; i < g.s1; ++i, t.next()) {
                     if (!seen[id].insert(i).second) return fail("a step given twice");
@@ -173,7 +174,7 @@ static int check_weigh()
                     if ((int)seen[id].size() != weigh_steps(l, k)) return fail("a step that nobody has");
                     for (int plane = 0; plane < l.planes; ++plane)
                         for (int r = 0; r < l.rows; ++r) {
-                            const bool sees = s.mode != kHeads || !s.causal || 128 * k < l.off + r + 1;
+                            const bool sees = s.mode != kHeads || !s.causal || s.keys * k < l.off + r + 1;
                             if (sees && !tiles[id].count({plane, r / s.NQ})) return fail("a row that is left out");
                         }
                 }
