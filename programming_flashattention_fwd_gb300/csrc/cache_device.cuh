@@ -5,6 +5,7 @@
 
 #include "cache_internal.h"
 #include "ptx.cuh"
+#include "watchdog.cuh"
 
 namespace fa {
 namespace cache {
@@ -50,6 +51,47 @@ __device__ __forceinline__ Share find_share(int B, int least, int lane, int cta,
     s.off = begin - before;
     return s;
 }
+
+// One probe of a phase by the whole (converged) warp, combined by a vote.
+__device__ __forceinline__ bool mbar_try_all(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p, q;\n\t"
+                 "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                 "vote.sync.all.pred q, p, 0xffffffff;\n\t"
+                 "selp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(ok)
+                 : "r"(bar), "r"(parity)
+                 : "memory");
+    return ok != 0;
+}
+
+// A wait of the whole warp: usually the first probe succeeds (a few instructions instead of the
+// bounded loop's), and every lane learns the same outcome.
+struct WarpWait {
+    volatile int *abort_flag;
+    uint64_t timeout_ns;
+    unsigned int *status;
+
+    __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity, uint32_t site) const
+    {
+        if (mbar_try_all(bar, parity)) return true;
+        return __all_sync(0xffffffffu, bounded_wait(bar, parity, abort_flag, timeout_ns, site, status)) != 0;
+    }
+};
+
+// Place and phase of the next entry of a ring of N, without divisions.
+template <int N>
+struct Ring {
+    uint32_t at = 0, phase = 0;
+    __device__ __forceinline__ void next()
+    {
+        if (++at == N) {
+            at = 0;
+            phase ^= 1;
+        }
+    }
+};
 
 // Page and row of slot `slot` of sequence b; a page that does not exist is given the number past the
 // last, which a tensor map reads as zeros.
