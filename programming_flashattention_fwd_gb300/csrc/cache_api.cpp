@@ -129,8 +129,8 @@ extern "C" {
 size_t fa_tree_workspace_bytes(int Hq, int Hkv, int T, int D)
 {
     if (Hkv < 1 || Hq < 1 || Hq % Hkv != 0 || T < 1 || D < 1) return 0;
-    const long long rows = (long long)(Hq / Hkv) * T;
-    const size_t part = rows < kRowTile ? (size_t)rows : (size_t)kRowTile;
+    const long long rows = (long long)(Hq / Hkv) * T, tile = tree_tile(D, rows);
+    const size_t part = (size_t)(rows < tile ? rows : tile);
     return align16((size_t)2 * kMaxCtas * part * 4) + (size_t)2 * kMaxCtas * part * D * 4;
 }
 
@@ -145,10 +145,11 @@ int fa_tree_fwd(const fa_cache_t *cache, const void *q, const void *k_new, const
     if (Hq < 1 || Hq % Hkv != 0) return FA_ERR_HEADS;
     if (!(std::isfinite(scale) && scale > 0.f)) return FA_ERR_SCALE;
     if (B == 0 || T == 0) return FA_OK;
-    const long long rows = (long long)(Hq / Hkv) * T, mt = (rows + kRowTile - 1) / kRowTile;
-    const int BN = tree_keys(D), cap = cache->max_pages * cache->page;
+    const long long rows = (long long)(Hq / Hkv) * T;
+    const int tile = tree_tile(D, rows), BN = 1 << tree_log_keys(D), cap = cache->max_pages * cache->page;
+    const long long mt = (rows + tile - 1) / tile;
     const long long steps = ((long long)cap + BN - 1) / BN + (T + BN - 1) / BN;
-    if (rows > 0x7fffffffLL - kRowTile || (double)B * Hkv * mt * steps > 2147483647.0) return FA_ERR_BAD_DIM;
+    if (rows > 0x7fffffffLL - 256 || (double)B * Hkv * mt * steps > 2147483647.0) return FA_ERR_BAD_DIM;
     st = check_cache_pointers(cache);
     if (st != FA_OK) return st;
     if (!q || !k_new || !v_new || !o || !lse || !workspace) return FA_ERR_NULL_PTR;
@@ -171,20 +172,27 @@ int fa_tree_fwd(const fa_cache_t *cache, const void *q, const void *k_new, const
     TreeMaps m;
     std::memset(&m, 0, sizeof(m));
     const long long eq[3] = {D, rows, (long long)B * Hkv}, en[3] = {D, T, (long long)B * Hkv};
-    if (!encode(&m.q, q, bf16, 3, eq, kRowTile) || !encode(&m.k_new, k_new, bf16, 3, en, BN) ||
+    // a tile of up to 64 rows leaves the other rows of its 128-row operand to whatever is behind it (no one
+    // reads what becomes of them), so that two query tiles fit where one of 128 rows does
+    const bool small = rows <= 64;
+    const int q_rows = small ? (int)((rows + 7) / 8 * 8) : kRowTile;
+    if (!encode(&m.q, q, bf16, 3, eq, q_rows) || !encode(&m.k_new, k_new, bf16, 3, en, BN) ||
         !encode(&m.v_new, v_new, bf16, 3, en, BN) || !encode_pool(&m.k, cache->k, q, cache, box) ||
         !encode_pool(&m.v, cache->v, q, cache, box))
         return FA_ERR_TENSORMAP;
 
     TreeParams p;
     std::memset(&p, 0, sizeof(p));
-    p.s = TreeShape{B, Hkv, T, (int)rows, (int)mt, BN, cap, cache->seq_len, draft_len};
+    p.s = TreeShape{B, Hkv, T, (int)rows, tile, (int)mt, tree_log_keys(D), cap, cache->seq_len, draft_len};
     p.pages = pages_of(cache);
     p.parent = parent;
     p.v_new = v_new;
     p.o = o;
     p.lse = lse;
-    p.part_rows = rows < kRowTile ? (int)rows : kRowTile;
+    p.part_rows = rows < tile ? (int)rows : tile;
+    p.q_panel = small ? 8192 : 16384;
+    p.q_bufs = small ? 2 : 1;
+    p.q_box = q_rows * 128;
     p.part_o = static_cast<float *>(workspace);
     p.part_lse = p.part_o + (size_t)2 * kMaxCtas * p.part_rows * D;
     p.box_rows = box;

@@ -30,7 +30,9 @@ struct TreeParams {
     float *lse;              // [B, Hq, T]
     float *part_o;           // [2 * kMaxCtas][part_rows][D]
     float *part_lse;         // [2 * kMaxCtas][part_rows], log2 units
-    int part_rows;           // min(rows, 128)
+    int part_rows;           // min(rows, tile)
+    int q_panel, q_box;      // bytes of a 64-column panel of a query tile in shared memory, and of one copy into it
+    int q_bufs;              // query tiles in flight
     int box_rows;            // rows of one copy: gcd(page, 128), at most BN
     int least;               // steps a CTA takes at least
     float sl2;               // scale * log2 e
@@ -41,7 +43,8 @@ struct TreeMaps {
     CUtensorMap q, k, v, k_new, v_new;
 };
 
-int tree_keys(int D);        // keys per step
+int tree_log_keys(int D);                // log2 of the keys per step
+int tree_tile(int D, long long rows);    // rows of a unit: 128, or 256 (two row tiles share K and V)
 cudaError_t launch_tree(int D, bool bf16, const TreeMaps &m, const TreeParams &p, cudaStream_t st);
 cudaError_t read_and_clear_tree_status(uint32_t *word);
 

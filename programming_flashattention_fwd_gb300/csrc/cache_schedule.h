@@ -28,12 +28,13 @@ __host__ __device__ __forceinline__ int ctas(int total, int grid, int least)
 }
 
 // ---------------------------------------------------------------- attention for drafted tokens
-// A unit is one 128-row tile of (sequence, KV head); its rows are (head in the group, token).
-// Its steps are the key tiles of the cache, then the key tiles of the drafted tokens.
+// A unit is one tile of `tile` rows (128, or 256: two row tiles side by side) of (sequence, KV head); its
+// rows are (head in the group, token).  Its steps are the key tiles of the cache, then the key tiles of
+// the drafted tokens.
 struct TreeShape {
     int B, Hkv, T, rows;         // rows = (Hq / Hkv) * T
-    int mtiles;                  // 128-row tiles of `rows`
-    int BN;                      // keys per step
+    int tile, units;             // units = tiles of `rows`
+    int lbn;                     // log2 of the keys per step
     int capacity;                // slots of a sequence: max_pages * page
     const int32_t *seq_len;      // [B]
     const int32_t *draft_len;    // [B] or null: T
@@ -47,10 +48,11 @@ struct TreeLen {
 __host__ __device__ __forceinline__ TreeLen tree_len(const TreeShape &s, int b)
 {
     TreeLen l;
+    const int up = (1 << s.lbn) - 1;
     l.n = clampi(s.seq_len[b], 0, s.capacity);
     l.t = s.draft_len ? clampi(s.draft_len[b], 0, s.T) : s.T;
-    l.kc = cdiv(l.n, s.BN);
-    l.nt = l.t > 0 ? l.kc + cdiv(l.t, s.BN) : 0;
+    l.kc = (l.n + up) >> s.lbn;
+    l.nt = l.t > 0 ? l.kc + ((l.t + up) >> s.lbn) : 0;
     return l;
 }
 
@@ -62,30 +64,42 @@ struct TreeSeg {
 
 // Walks a CTA's steps: `left` steps from step `off` of sequence b.
 struct TreeWalk {
-    int b, off, left;
+    int left, b, kvh, mt, k;
+    TreeLen len;
+
+    __host__ __device__ __forceinline__ TreeWalk(const TreeShape &s, int b0, int off, int steps) : left(steps), b(b0), kvh(0), mt(0), k(0)
+    {
+        if (left <= 0) return;
+        len = tree_len(s, b);
+        const int u = off / len.nt;
+        k = off - u * len.nt;
+        kvh = u / s.units;
+        mt = u - kvh * s.units;
+    }
 
     __host__ __device__ __forceinline__ bool next(const TreeShape &s, TreeSeg &g)
     {
-        while (left > 0 && b < s.B) {
-            const TreeLen l = tree_len(s, b);
-            const int per = s.Hkv * s.mtiles * l.nt;
-            if (off >= per) {
-                off -= per;
-                ++b;
-                continue;
+        if (left <= 0) return false;
+        if (mt == s.units) {
+            mt = 0;
+            if (++kvh == s.Hkv) {
+                kvh = 0;
+                do {
+                    if (++b >= s.B) return false;
+                    len = tree_len(s, b);
+                } while (len.nt == 0);
             }
-            const int u = off / l.nt;
-            g.b = b;
-            g.kvh = u / s.mtiles;
-            g.mt = u - g.kvh * s.mtiles;
-            g.k0 = off - u * l.nt;
-            g.k1 = l.nt - g.k0 < left ? l.nt : g.k0 + left;
-            g.len = l;
-            off += g.k1 - g.k0;
-            left -= g.k1 - g.k0;
-            return true;
         }
-        return false;
+        g.b = b;
+        g.kvh = kvh;
+        g.mt = mt;
+        g.k0 = k;
+        g.k1 = len.nt - k < left ? len.nt : k + left;
+        g.len = len;
+        left -= g.k1 - g.k0;
+        k = 0;
+        ++mt;
+        return true;
     }
 };
 

@@ -14,15 +14,18 @@
 //
 // Per CTA (one per SM):
 //   warp 0        K / V producer: per step one TMA box per page and 64-column panel (each lane looks
-//                 up the page of its box), into a ring of NS slots
+//                 up the page of its box, a step ahead), into a ring of NS slots
 //   warp 1        TMEM owner and MMA issuer: S = Q K^T, O += P V (tcgen05, fp32 in tensor memory)
 //   warp 2        Q producer
 //   warp 3        finds this CTA's share of the work
-//   warps 4-7,    softmax, one thread per row.  D <= 128: two groups take alternate key steps, each
-//   warps 8-11    with its own running maximum, sum and O accumulator, so that one group's softmax
-//                 runs beside the other's matrix products; they are joined in the epilogue, where
-//                 both read both accumulators (half of the columns each).  D = 256: one group (two
-//                 accumulators do not fit), with 64-key steps.
+//   warps 4-7,    softmax, one thread per row, in two groups (one at D = 256) so that one group's softmax
+//   warps 8-11    runs beside the other's matrix products:
+//     up to 128 rows    the groups take alternate key steps, each with its own running maximum, sum and O;
+//                       they are joined in the epilogue, where both read both accumulators (half of
+//                       the columns each)
+//     more (PAIR)       each group has a row tile of its own and takes every step: K and V are read once
+//                       for 256 rows
+//     D = 256           one group, 64-key steps (two accumulators do not fit)
 //
 // Tensor memory: S_0, S_1 (BN columns each; P, 16-bit, overwrites its S), then the accumulators.
 //
@@ -54,18 +57,21 @@ enum Site : uint32_t {
     S_EMPTY = 1, S_Q = 2, S_FULL = 3, S_P = 4, S_S = 5, S_PV = 6, S_DRAIN = 7, S_QFREE = 8, S_SMEM = 9, S_JOIN = 10, S_READ = 11
 };
 
-template <int D>
+template <int D, bool PAIR>
 struct Cfg {
-    static constexpr int BN = D == 256 ? 64 : 128;
+    static constexpr int LBN = D == 256 ? 6 : 7, BN = 1 << LBN;
     static constexpr int NG = D == 256 ? 1 : 2;          // softmax groups
+    static constexpr int STRIDE = PAIR ? 1 : NG;         // key steps from one of a group to its next
     static constexpr int THREADS = 128 + 128 * NG;
     static constexpr int PANELS = D / 64;
-    static constexpr int QPANEL = kRowTile * 128, QTILE = PANELS * QPANEL;
+    static constexpr int QTILE = PANELS * 16384;         // one tile of 128 rows, or two of up to 64
+    static constexpr int QAREA = PAIR ? 2 * QTILE : QTILE;
     static constexpr int KVPANEL = BN * 128, KVTILE = PANELS * KVPANEL;
-    static constexpr int NS = D == 64 ? 12 : (D == 128 ? 6 : 5);   // 192, 192 and 160 KB of K / V in flight
-    static constexpr int OFF_RING = QTILE;
+    // 160 or 192 KB of K / V in flight (6 slots, against 5: 6.76 and 6.7 TB/s over a long cache at D = 128)
+    static constexpr int NS = D == 64 ? 12 : (D == 128 && !PAIR ? 6 : 5);
+    static constexpr int OFF_RING = QAREA;
     static constexpr int OFF_BAR = OFF_RING + NS * KVTILE;
-    static constexpr int NBAR = 2 + 2 * NS + 2 + 2 + 2 + 2 + 1;    // q, qfree, full, empty, S[2], P[2], PV[2], join, read, done
+    static constexpr int NBAR = 4 + 2 * NS + 2 + 2 + 2 + 2 + 1;    // q[2], qfree[2], full, empty, S[2], P[2], PV[2], join, read, done
     static constexpr int OFF_ML = OFF_BAR + ((NBAR * 8 + 15) / 16) * 16;   // [NG][128] (m, l)
     static constexpr int OFF_MISC = OFF_ML + NG * 128 * 8;
     static constexpr int BYTES = OFF_MISC + 48;
@@ -74,13 +80,14 @@ struct Cfg {
     static constexpr int ALLOC = BYTES + 1024 <= 232448 ? BYTES + 1024 : 232448;
     static constexpr uint32_t COL_O = 2 * BN;
     static_assert(2 * BN + NG * D <= 512, "tensor-memory columns");
+    static_assert(!PAIR || NG == 2, "two row tiles, two groups");
 };
 
 struct Misc {
     uint32_t tmem;
     int abort;
     int nonfinite;      // 1 + index of the last segment whose drafted V held a non-finite value
-    TreeWalk walk;      // this CTA's share
+    int b, off, left;   // this CTA's share
 };
 
 // x is an infinity or a NaN, in a 16-bit pair: the pair with those halves cleared, and whether there were any.
@@ -132,13 +139,13 @@ __device__ __forceinline__ void path_bits(const int32_t *parent, int t, int lo, 
 }
 
 // Steps of sequence b.
-__device__ __forceinline__ int tree_steps(const TreeShape &s, int b) { return s.Hkv * s.mtiles * tree_len(s, b).nt; }
+__device__ __forceinline__ int tree_steps(const TreeShape &s, int b) { return s.Hkv * s.units * tree_len(s, b).nt; }
 
-template <int D, bool BF16>
-__global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
+template <int D, bool BF16, bool PAIR>
+__global__ void __launch_bounds__(Cfg<D, PAIR>::THREADS, 1)
     tree_kernel(const __grid_constant__ TreeMaps maps, const __grid_constant__ TreeParams p)
 {
-    using C = Cfg<D>;
+    using C = Cfg<D, PAIR>;
     constexpr int BN = C::BN, NG = C::NG;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
@@ -147,10 +154,11 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
     const uint32_t sb = raw + pad;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t sRing = sb + C::OFF_RING, bar0 = sb + C::OFF_BAR;
-    const uint32_t barQ = bar0, barQfree = bar0 + 8;
-    auto bar_full = [&](int s) { return bar0 + 8u * (2 + s); };
-    auto bar_empty = [&](int s) { return bar0 + 8u * (2 + C::NS + s); };
-    const uint32_t barS = bar0 + 8u * (2 + 2 * C::NS), barP = barS + 16, barPV = barS + 32, barJoin = barS + 48,
+    auto bar_q = [&](uint32_t i) { return bar0 + 8u * i; };
+    auto bar_qfree = [&](uint32_t i) { return bar0 + 16u + 8u * i; };
+    auto bar_full = [&](uint32_t s) { return bar0 + 8u * (4 + s); };
+    auto bar_empty = [&](uint32_t s) { return bar0 + 8u * (4 + C::NS + s); };
+    const uint32_t barS = bar0 + 8u * (4 + 2 * C::NS), barP = barS + 16, barPV = barS + 32, barJoin = barS + 48,
                    barRead = barS + 56, barDone = barS + 64;
     float2 *ml = reinterpret_cast<float2 *>(smem + C::OFF_ML);
     volatile Misc *misc = reinterpret_cast<volatile Misc *>(smem + C::OFF_MISC);
@@ -164,47 +172,50 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         if (threadIdx.x == 0) atomicOr(status, 1u | (S_SMEM << 8));
         return;
     }
-    if (threadIdx.x == 0) {
-        mbar_init(barQ, 1);
-        mbar_init(barQfree, 1);
-        for (int s = 0; s < C::NS; ++s) {
-            mbar_init(bar_full(s), 1);
-            mbar_init(bar_empty(s), 1);
+    if (warp == 0) {
+        if (lane == 0) {
+            for (int i = 0; i < 2; ++i) {
+                mbar_init(bar_q(i), 1);
+                mbar_init(bar_qfree(i), 1);
+                mbar_init(barS + 8 * i, 1);
+                mbar_init(barP + 8 * i, 4);
+                mbar_init(barPV + 8 * i, 1);
+            }
+            for (int s = 0; s < C::NS; ++s) {
+                mbar_init(bar_full(s), 1);
+                mbar_init(bar_empty(s), 1);
+            }
+            mbar_init(barJoin, 4 * NG);
+            mbar_init(barRead, 4 * NG);
+            mbar_init(barDone, 1);
+            misc->abort = 0;
+            misc->nonfinite = 0;
+            fence_mbar_init();
         }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(barS + 8 * i, 1);
-            mbar_init(barP + 8 * i, 4);
-            mbar_init(barPV + 8 * i, 1);
-        }
-        mbar_init(barJoin, 4 * NG);
-        mbar_init(barRead, 4 * NG);
-        mbar_init(barDone, 1);
-        misc->abort = 0;
-        misc->nonfinite = 0;
-        fence_mbar_init();
-    }
-    if (warp == 1) {
+    } else if (warp == 1) {
         tmem_alloc(smem_u32(const_cast<uint32_t *>(&misc->tmem)), 512);
         tmem_relinquish();
-    }
-    if (warp == 3) {
+    } else if (warp == 2) {
+        if (lane < 5) tma_prefetch_map(lane == 0 ? &maps.q : lane == 1 ? &maps.k : lane == 2 ? &maps.v : lane == 3 ? &maps.k_new : &maps.v_new);
+    } else if (warp == 3) {
         const Share w = find_share(p.s.B, p.least, lane, blockIdx.x, gridDim.x, [&](int b) { return tree_steps(p.s, b); });
         if (lane == 0) {
-            misc->walk.b = w.b;
-            misc->walk.off = w.off;
-            misc->walk.left = w.left;
+            misc->b = w.b;
+            misc->off = w.off;
+            misc->left = w.left;
         }
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = misc->tmem;
-    TreeWalk walk{misc->walk.b, misc->walk.off, misc->walk.left};
-    const TreeWalk share = walk;
-    TreeSeg g;
+    TreeWalk walk(p.s, misc->b, misc->off, misc->left);
+    TreeSeg g = {};
+    const WarpWait wait_all{abort_flag, tmo, status};
 
-    auto wait_all = [&](uint32_t bar, uint32_t parity, uint32_t site) -> bool {
-        return __all_sync(0xffffffffu, bounded_wait(bar, parity, abort_flag, tmo, site, status)) != 0;
+    // keys of step kt that there are
+    auto valid_of = [&](const TreeSeg &g, int kt) {
+        return kt < g.len.kc ? min(BN, g.len.n - kt * BN) : min(BN, g.len.t - (kt - g.len.kc) * BN);
     };
 
     if (warp == 0) {
@@ -213,21 +224,19 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         const int boxes = BN / p.box_rows;            // boxes of a step (one panel)
         const int box = lane / C::PANELS, pn = lane % C::PANELS;
         const uint32_t box_off = (uint32_t)(pn * C::KVPANEL + box * p.box_rows * 128);
+        Ring<C::NS> ring;
         int use = 0;
         bool ok = true;
         // the page (and the row in it) of this lane's box of step kt
-        auto look = [&](const TreeSeg &g, int kt, int &pid, int &row) {
+        auto look = [&](int kt, int &pid, int &row) {
             pid = -1;
             row = 0;
-            if (kt >= g.len.kc || box >= boxes) return;
             const int slot = kt * BN + box * p.box_rows;
-            if (slot >= g.len.n) return;
-            page_of(pg, g.b, slot, pid, row);
+            if (kt < g.len.kc && box < boxes && slot < g.len.n) page_of(pg, g.b, slot, pid, row);
         };
-        auto load = [&](const TreeSeg &g, bool is_v, int kt, int pid, int row) -> bool {
-            const int s = use % C::NS;
-            if (!wait_all(bar_empty(s), ((use / C::NS) & 1) ^ 1, S_EMPTY)) return false;
-            const uint32_t dst = sRing + s * C::KVTILE, bar = bar_full(s);
+        auto load = [&](bool is_v, int kt, int pid, int row) -> bool {
+            if (!wait_all(bar_empty(ring.at), ring.phase ^ 1, S_EMPTY)) return false;
+            const uint32_t dst = sRing + ring.at * C::KVTILE, bar = bar_full(ring.at);
             if (kt < g.len.kc) {
                 const int valid = min(boxes, cdiv(g.len.n - kt * BN, p.box_rows));
                 if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(valid * p.box_rows * 128 * C::PANELS));
@@ -240,21 +249,23 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                     tma_load_3d(dst + lane * C::KVPANEL, is_v ? &maps.v_new : &maps.k_new, lane * 64, (kt - g.len.kc) * BN,
                                 g.b * p.s.Hkv + g.kvh, bar);
             }
+            ring.next();
             ++use;
             return true;
         };
         while (ok && walk.next(p.s, g)) {
-            int pid, row, pid1, row1;
-            look(g, g.k0, pid, row);
-            ok = load(g, false, g.k0, pid, row);
+            int pid, row, pid1, row1, pid2, row2;
+            look(g.k0, pid, row);
+            look(g.k0 + 1, pid1, row1);
+            ok = load(false, g.k0, pid, row);
             for (int kt = g.k0; ok && kt < g.k1; ++kt) {
-                if (kt + 1 < g.k1) {
-                    look(g, kt + 1, pid1, row1);
-                    ok = load(g, false, kt + 1, pid1, row1);
-                }
-                if (ok) ok = load(g, true, kt, pid, row);
+                look(kt + 2, pid2, row2);   // used in the next round
+                if (kt + 1 < g.k1) ok = load(false, kt + 1, pid1, row1);
+                if (ok) ok = load(true, kt, pid, row);
                 pid = pid1;
                 row = row1;
+                pid1 = pid2;
+                row1 = row2;
             }
         }
         if (lane == 0)
@@ -266,62 +277,113 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         if (lane == 0) {
             int tau = 0;
             for (; walk.next(p.s, g); ++tau) {
-                if (tau && !bounded_wait(barQfree, (tau - 1) & 1, abort_flag, tmo, S_QFREE, status)) break;
-                mbar_arrive_expect_tx(barQ, C::QTILE);
+                const int i = p.q_bufs == 2 ? tau & 1 : 0, u = p.q_bufs == 2 ? tau >> 1 : tau;   // buffer, its use
+                if (u && !bounded_wait(bar_qfree(i), (u - 1) & 1, abort_flag, tmo, S_QFREE, status)) break;
+                mbar_arrive_expect_tx(bar_q(i), (uint32_t)(p.q_box * C::PANELS * (PAIR ? 2 : 1)));
+                const uint32_t dst = sb + (uint32_t)i * C::PANELS * p.q_panel;
 #pragma unroll
-                for (int pn = 0; pn < C::PANELS; ++pn)
-                    tma_load_3d(sb + pn * C::QPANEL, &maps.q, pn * 64, g.mt * kRowTile, g.b * p.s.Hkv + g.kvh, barQ);
+                for (int h = 0; h < (PAIR ? 2 : 1); ++h)   // a second tile past the last row is filled with zeros
+#pragma unroll
+                    for (int pn = 0; pn < C::PANELS; ++pn)
+                        tma_load_3d(dst + h * C::QTILE + pn * p.q_panel, &maps.q, pn * 64, g.mt * p.s.tile + h * kRowTile,
+                                    g.b * p.s.Hkv + g.kvh, bar_q(i));
             }
-            if (tau) bounded_wait(barQ, (tau - 1) & 1, abort_flag, tmo, S_DRAIN, status, false);
+            for (int x = max(0, tau - p.q_bufs); x < tau; ++x) {
+                const int i = p.q_bufs == 2 ? x & 1 : 0, u = p.q_bufs == 2 ? x >> 1 : x;
+                bounded_wait(bar_q(i), u & 1, abort_flag, tmo, S_DRAIN, status, false);
+            }
         }
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer (whole warp)
         constexpr uint32_t idS = idesc_f16(BF16, kRowTile, BN, false), idPV = idesc_f16(BF16, kRowTile, D, true);
         constexpr uint32_t HI = sdesc_hi_sw128(1024);
-        auto slot = [&](int use) { return sRing + (uint32_t)(use % C::NS) * C::KVTILE; };
-        auto issue_s = [&](uint32_t gs, int use) {
-            const uint32_t sK = slot(use);
+        Ring<C::NS> ring;
+        int tau = 0;
+        uint32_t gs = 0;   // this CTA's key step
+        uint32_t sQ = sb;
+        bool ok = true;
+        // S_i = Q K^T with the key tile of ring slot `at`; ready on barS
+        auto issue_s = [&](uint32_t i, uint32_t q, uint32_t at) {
+            const uint32_t sK = sRing + at * C::KVTILE;
 #pragma unroll
             for (int pn = 0; pn < C::PANELS; ++pn)
-                mma_ss_kk4_elect(tmem + (gs & 1) * BN, sdesc_lo(sb + pn * C::QPANEL, 16), sdesc_lo(sK + pn * C::KVPANEL, 16), HI,
-                                 idS, pn ? 1u : 0u);
-            tc_commit_elect(barS + 8u * (gs & 1));
-            tc_commit_elect(bar_empty(use % C::NS));
+                mma_ss_kk4_elect(tmem + i * BN, sdesc_lo(q + pn * p.q_panel, 16), sdesc_lo(sK + pn * C::KVPANEL, 16), HI, idS, pn ? 1u : 0u);
+            tc_commit_elect(barS + 8u * i);
         };
-        int use = 0, tau = 0;
-        uint32_t gs = 0;   // this CTA's key step: S buffer, barriers and softmax group gs & 1
-        bool ok = true;
+        // O_acc += P_i V with the value tile of ring slot `at`, 64 keys at a time (all of them, or the half that holds
+        // the valid ones); done on barPV
+        auto issue_pv = [&](uint32_t i, uint32_t acc, uint32_t at, int valid, bool first) {
+            const uint32_t vlo = sdesc_lo(sRing + at * C::KVTILE, C::KVPANEL);
+#pragma unroll
+            for (int h = 0; h < BN / 64; ++h)
+                if (h == 0 || valid > 64)
+                    mma_ts_mn4_elect(tmem + C::COL_O + acc * D, tmem + i * BN + 32 * h, vlo + (uint32_t)((h * 8192) >> 4), HI, idPV,
+                                     first && h == 0 ? 0u : 1u);
+            tc_commit_elect(barPV + 8u * i);
+        };
         for (; ok && walk.next(p.s, g); ++tau) {
             const int nk = g.k1 - g.k0;
-            ok = wait_all(barQ, tau & 1, S_Q) && wait_all(bar_full(use % C::NS), (use / C::NS) & 1, S_FULL);
+            const uint32_t qi = p.q_bufs == 2 ? tau & 1 : 0, qu = p.q_bufs == 2 ? tau >> 1 : tau;
+            sQ = sb + qi * C::PANELS * p.q_panel;
+            ok = wait_all(bar_q(qi), qu & 1, S_Q) && wait_all(bar_full(ring.at), ring.phase, S_FULL);
             if (!ok) break;
             tc_fence_after();
-            issue_s(gs, use);
-            if (nk == 1) tc_commit_elect(barQfree);
-            ++use;
+            if constexpr (PAIR) {
+                issue_s(0, sQ, ring.at);
+                issue_s(1, sQ + C::QTILE, ring.at);
+            } else {
+                issue_s(gs & 1, sQ, ring.at);
+            }
+            tc_commit_elect(bar_empty(ring.at));
+            if (nk == 1) tc_commit_elect(bar_qfree(qi));
+            ring.next();
             for (int j = 0; j < nk; ++j, ++gs) {
-                if (j + 1 < nk) {
-                    ok = wait_all(bar_full(use % C::NS), (use / C::NS) & 1, S_FULL);
+                const int valid = valid_of(g, g.k0 + j);
+                const bool more = j + 1 < nk;
+                uint32_t kat = 0;
+                if constexpr (PAIR) {
+                    // per step: P V of tile a, its next S, P V of tile b, its next S; an S follows the P V that read its buffer
+                    if (more) {
+                        ok = wait_all(bar_full(ring.at), ring.phase, S_FULL);
+                        if (!ok) break;
+                        kat = ring.at;
+                        ring.next();
+                    }
+                    ok = wait_all(bar_full(ring.at), ring.phase, S_FULL);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        ok = ok && wait_all(barP + 8u * i, gs & 1, S_P);
+                        if (!ok) break;
+                        tc_fence_after();
+                        issue_pv(i, i, ring.at, valid, j == 0);
+                        if (i == 1) tc_commit_elect(bar_empty(ring.at));
+                        if (more) {
+                            issue_s(i, sQ + i * C::QTILE, kat);
+                            if (i == 1) {
+                                tc_commit_elect(bar_empty(kat));
+                                if (j + 2 == nk) tc_commit_elect(bar_qfree(qi));
+                            }
+                        }
+                    }
+                    if (!ok) break;
+                } else {
+                    if (more) {
+                        ok = wait_all(bar_full(ring.at), ring.phase, S_FULL);
+                        if (!ok) break;
+                        tc_fence_after();
+                        issue_s((gs + 1) & 1, sQ, ring.at);   // its buffer held P(gs - 1), whose P V was issued before
+                        tc_commit_elect(bar_empty(ring.at));
+                        if (j + 2 == nk) tc_commit_elect(bar_qfree(qi));
+                        ring.next();
+                    }
+                    ok = wait_all(bar_full(ring.at), ring.phase, S_FULL) && wait_all(barP + 8u * (gs & 1), (gs >> 1) & 1, S_P);
                     if (!ok) break;
                     tc_fence_after();
-                    issue_s(gs + 1, use);   // its S buffer held P(gs - 1), whose P V was issued before
-                    if (j + 2 == nk) tc_commit_elect(barQfree);
-                    ++use;
+                    issue_pv(gs & 1, NG == 2 ? gs & 1 : 0, ring.at, valid, j < NG);
+                    tc_commit_elect(bar_empty(ring.at));
                 }
-                ok = wait_all(bar_full(use % C::NS), (use / C::NS) & 1, S_FULL) &&
-                     wait_all(barP + 8u * (gs & 1), (gs >> 1) & 1, S_P);
-                if (!ok) break;
-                tc_fence_after();
-                const uint32_t dO = tmem + C::COL_O + (NG == 2 ? (gs & 1) * D : 0u);
-                const uint32_t vlo = sdesc_lo(slot(use), C::KVPANEL);
-#pragma unroll
-                for (int h = 0; h < BN / 64; ++h)
-                    mma_ts_mn4_elect(dO, tmem + (gs & 1) * BN + 32 * h, vlo + (uint32_t)((h * 8192) >> 4), HI, idPV,
-                                     (j < NG && h == 0) ? 0u : 1u);
-                tc_commit_elect(barPV + 8u * (gs & 1));
-                tc_commit_elect(bar_empty(use % C::NS));
-                ++use;
+                ring.next();
             }
         }
         tc_commit_elect(barDone);
@@ -339,24 +401,25 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         bool ok = true;
         for (; ok && walk.next(p.s, g); ++seg) {
             const int nk = g.k1 - g.k0;
-            const int row = g.mt * kRowTile + r, t = row % p.s.T;
+            const int urow = (PAIR ? grp * kRowTile : 0) + r;      // row of the unit
+            const int row = g.mt * p.s.tile + urow, t = row % p.s.T;
             const bool live = row < p.s.rows && t < g.len.t;
             const bool warp_live = __any_sync(~0u, live);
             const int32_t *parent = p.parent ? p.parent + (size_t)g.b * p.s.T : nullptr;
             float m_used = -INFINITY, l = 0.f;
             bool first = true;
-            for (int j = NG == 2 ? (int)((gs0 ^ (uint32_t)grp) & 1u) : 0; j < nk; j += NG) {
-                const uint32_t gs = gs0 + j, bi = gs & 1, ph = (gs >> 1) & 1;
+            for (int j = PAIR || NG == 1 ? 0 : (int)((gs0 ^ (uint32_t)grp) & 1u); j < nk; j += C::STRIDE) {
+                const uint32_t gs = gs0 + j;
+                const uint32_t bi = PAIR ? (uint32_t)grp : gs & 1, ph = PAIR ? gs & 1 : (gs >> 1) & 1;   // S buffer, its phase
                 const uint32_t tS = tmem + lane_off + bi * BN;
                 const int kt = g.k0 + j;
                 const bool draft = kt >= g.len.kc;
-                const int base = draft ? (kt - g.len.kc) * BN : kt * BN;
-                const int valid = min(BN, (draft ? g.len.t : g.len.n) - base);
+                const int valid = valid_of(g, kt);
                 const bool masked = draft || valid < BN;
                 uint32_t bits[BN / 32];
                 if (masked) {
                     if (draft && live) {
-                        path_bits<BN / 32>(parent, t, base, bits);
+                        path_bits<BN / 32>(parent, t, (kt - g.len.kc) * BN, bits);
                     } else {
 #pragma unroll
                         for (int w = 0; w < BN / 32; ++w) {
@@ -370,28 +433,9 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                 tc_fence_after();
                 bool rescale = false;
                 float alpha = 1.f;
-                if (warp_live) {
-                    uint32_t sv[BN];
-                    float pm[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                    for (int c = 0; c < BN; c += 32)
-                        tmem_ld_red_max_x32(tS + c, *reinterpret_cast<uint32_t(*)[32]>(sv + c), pm[c / 32]);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int c = 0; c < BN; c += 32) reg_fence_x32(*reinterpret_cast<uint32_t(*)[32]>(sv + c));
-                    reg_fence_f4(pm[0], pm[1], pm[2], pm[3]);
-                    float *s = reinterpret_cast<float *>(sv);
-                    float mrow = fmaxf(fmax3(pm[0], pm[1], pm[2]), pm[3]);
-                    if (masked) {
-                        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                        for (int c = 0; c < BN; ++c) {
-                            if (!((bits[c >> 5] >> (c & 31)) & 1u)) s[c] = -INFINITY;
-                            mx[c & 3] = fmaxf(mx[c & 3], s[c]);
-                        }
-                        mrow = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]);
-                    }
-                    const float m_new = fmaxf(m_used, mrow * sl2);
+                // the running maximum with this step's: what the sums are relative to, and whether O must follow
+                auto grow = [&](float mrow) {
+                    const float m_new = fmaxf(m_used, live ? mrow * sl2 : -INFINITY);
                     if (first || m_used == -INFINITY) {
                         // nothing but zeros in this group's O so far
                         m_used = m_new;
@@ -401,6 +445,19 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                         m_used = m_new;
                         rescale = true;
                     }
+                };
+                if (warp_live && !masked) {
+                    uint32_t sv[BN];
+                    float pm[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int c = 0; c < BN; c += 32)
+                        tmem_ld_red_max_x32(tS + c, *reinterpret_cast<uint32_t(*)[32]>(sv + c), pm[c / 32]);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int c = 0; c < BN; c += 32) reg_fence_x32(*reinterpret_cast<uint32_t(*)[32]>(sv + c));
+                    reg_fence_f4(pm[0], pm[1], pm[2], pm[3]);
+                    grow(fmaxf(fmax3(pm[0], pm[1], pm[2]), pm[3]));
+                    const float *s = reinterpret_cast<const float *>(sv);
                     const float msub = m_used == -INFINITY ? 0.f : m_used;
                     const uint64_t negm2 = f2_pack(-msub, -msub);
                     uint64_t sum2[4];
@@ -423,11 +480,50 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                     float la, lb;
                     f2_unpack(f2_add(f2_add(sum2[0], sum2[1]), f2_add(sum2[2], sum2[3])), la, lb);
                     l += la + lb;
+                } else if (warp_live) {
+                    // Masked step (one or two a unit): 32 keys at a time, up to the last valid one and read twice, in a
+                    // short loop.  P is written for whole halves of 64 keys, which is what P V takes.
+                    auto word = [&](int c) { return BN == 64 ? (c ? bits[1] : bits[0]) : (c < 2 ? (c ? bits[1] : bits[0]) : (c == 2 ? bits[BN / 32 - 2] : bits[BN / 32 - 1])); };
+                    const int chunks = (valid + 31) >> 5;
+                    float mrow = -INFINITY;
+#pragma unroll 1
+                    for (int c = 0; c < chunks; ++c) {
+                        uint32_t sv[32];
+                        tmem_ld_x32(tS + 32 * c, sv);
+                        const uint32_t w = word(c);
+                        tmem_wait_ld();
+                        reg_fence_x32(sv);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) mrow = fmaxf(mrow, (w >> e) & 1u ? __uint_as_float(sv[e]) : -INFINITY);
+                    }
+                    grow(mrow);
+                    const float msub = m_used == -INFINITY ? 0.f : m_used;
+                    // P of 32 keys overwrites the scores of 16: the scores of later keys are read first
+                    uint32_t sv[32];
+                    tmem_ld_x32(tS, sv);
+#pragma unroll 1
+                    for (int c = 0; c < ((valid + 63) >> 6) * 2; ++c) {
+                        const uint32_t w = word(c);
+                        tmem_wait_ld();
+                        reg_fence_x32(sv);
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const float p0 = (w >> (2 * e)) & 1u ? ex2_approx(fmaf(__uint_as_float(sv[2 * e]), sl2, -msub)) : 0.f;
+                            const float p1 = (w >> (2 * e + 1)) & 1u ? ex2_approx(fmaf(__uint_as_float(sv[2 * e + 1]), sl2, -msub)) : 0.f;
+                            l += p0 + p1;
+                            pk[e] = pack2<BF16>(p0, p1);
+                        }
+                        if (c + 1 < BN / 32) tmem_ld_x32(tS + 32 * (c + 1), sv);
+                        tmem_wait_ld();
+                        reg_fence_x32(sv);
+                        tmem_st_x16(tS + 16 * c, pk);
+                    }
                 }
                 // O may be rescaled only once this accumulator's previous product is complete
                 if (__any_sync(~0u, rescale)) {
-                    const uint32_t prev = gs - NG;
-                    ok = wait_all(barPV + 8u * (prev & 1), (prev >> 1) & 1, S_PV);
+                    const uint32_t prev = gs - C::STRIDE;
+                    ok = PAIR ? wait_all(barPV + 8u * bi, prev & 1, S_PV) : wait_all(barPV + 8u * (prev & 1), (prev >> 1) & 1, S_PV);
                     if (!ok) break;
                     tc_fence_after();
                     const uint32_t tO = tmem + lane_off + C::COL_O + (uint32_t)(grp * D);
@@ -454,33 +550,34 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                     ok = wait_all(barRead, (seg - 1) & 1, S_READ);
                     if (!ok) break;
                 }
-                if (masked) {
-                    // V behind the last valid key is zeroed; a drafted V's non-finite values are taken out
+                if (masked && (!PAIR || grp == 0)) {
+                    // V behind the last valid key is zeroed; a drafted V's non-finite values are taken out.  (In a pair
+                    // the first group does it: its product is issued before the second's.)
                     const int uv = use0 + (j + 1 < nk ? 2 * j + 2 : 2 * j + 1);
                     ok = wait_all(bar_full(uv % C::NS), (uv / C::NS) & 1, S_FULL);
                     if (!ok) break;
                     const uint32_t sV = sRing + (uint32_t)(uv % C::NS) * C::KVTILE;
-                    const int dead = (BN - valid) * 8;   // 16-byte chunks of one panel
-                    for (int i = r; i < dead * C::PANELS; i += 128) {
-                        const int pn = i / dead;
-                        st_shared_v4(sV + pn * C::KVPANEL + valid * 128 + (i - pn * dead) * 16, 0u, 0u, 0u, 0u);
-                    }
+                    const int dead = (((valid + 63) & ~63) - valid) * 8;   // 16-byte chunks of one panel
+#pragma unroll 1
+                    for (int pn = 0; pn < C::PANELS; ++pn)
+                        for (int i = r; i < dead; i += 128) st_shared_v4(sV + pn * C::KVPANEL + valid * 128 + i * 16, 0u, 0u, 0u, 0u);
                     if (draft) {
                         bool any = false;
-                        for (int i = r; i < valid * 8 * C::PANELS; i += 128) {
-                            const int pn = i / (valid * 8);
-                            const uint32_t a = sV + pn * C::KVPANEL + (i - pn * valid * 8) * 16;
-                            uint32_t w[4];
-                            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                                         : "r"(a)
-                                         : "memory");
-                            bool here = false;
+#pragma unroll 1
+                        for (int pn = 0; pn < C::PANELS; ++pn)
+                            for (int i = r; i < valid * 8; i += 128) {
+                                const uint32_t a = sV + pn * C::KVPANEL + i * 16;
+                                uint32_t w[4];
+                                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                             : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                                             : "r"(a)
+                                             : "memory");
+                                bool here = false;
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) w[e] = drop_nonfinite<BF16>(w[e], here);
-                            if (here) st_shared_v4(a, w[0], w[1], w[2], w[3]);
-                            any |= here;
-                        }
+                                for (int e = 0; e < 4; ++e) w[e] = drop_nonfinite<BF16>(w[e], here);
+                                if (here) st_shared_v4(a, w[0], w[1], w[2], w[3]);
+                                any |= here;
+                            }
                         if (any) misc->nonfinite = seg + 1;
                     }
                     fence_proxy_async_smem();
@@ -502,8 +599,9 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
             if (lane == 0) mbar_arrive(barJoin);
             ok = wait_all(barJoin, seg & 1, S_JOIN);
             if (!ok) break;
-            float f0, f1 = 0.f, L, M;
-            if constexpr (NG == 2) {
+            constexpr bool SPLIT = NG == 2 && !PAIR;       // two accumulators of the same rows
+            float f0, f1 = 0.f, L = l, M = m_used;
+            if constexpr (SPLIT) {
                 const float2 a = ml[r], b = ml[128 + r];
                 M = fmaxf(a.x, b.x);
                 const float ms = M == -INFINITY ? 0.f : M;
@@ -514,30 +612,32 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                 f0 *= inv;
                 f1 *= inv;
             } else {
-                M = m_used;
-                L = l;
                 f0 = L == 0.f ? 0.f : 1.f / L;
             }
-            // the last products of both groups (the last two steps of the segment, if it has two)
+            // the last products: this group's, or both groups' (the segment's last two steps, if it has two)
             const uint32_t e1 = gs0 + nk - 1;
-            ok = wait_all(barPV + 8u * (e1 & 1), (e1 >> 1) & 1, S_PV);
-            if (ok && nk > 1) ok = wait_all(barPV + 8u * ((e1 - 1) & 1), ((e1 - 1) >> 1) & 1, S_PV);
+            if constexpr (PAIR) {
+                ok = wait_all(barPV + 8u * grp, e1 & 1, S_PV);
+            } else {
+                ok = wait_all(barPV + 8u * (e1 & 1), (e1 >> 1) & 1, S_PV);
+                if (ok && nk > 1) ok = wait_all(barPV + 8u * ((e1 - 1) & 1), ((e1 - 1) >> 1) & 1, S_PV);
+            }
             if (!ok) break;
             tc_fence_after();
-            const bool have0 = NG == 1 || nk > 1 || (gs0 & 1) == 0, have1 = NG == 2 && (nk > 1 || (gs0 & 1) == 1);
+            const bool have0 = !SPLIT || nk > 1 || (gs0 & 1) == 0, have1 = SPLIT && (nk > 1 || (gs0 & 1) == 1);
             const bool whole = g.k0 == 0 && g.k1 == g.len.nt;
             const bool odd = misc->nonfinite == seg + 1;   // rare: non-finite values in the drafted V
-            const size_t prow = (size_t)part_slot(blockIdx.x, g.k0) * p.part_rows + r;
+            const size_t prow = (size_t)part_slot(blockIdx.x, g.k0) * p.part_rows + urow;
             const size_t orow = ((size_t)(g.b * p.s.Hkv + g.kvh)) * p.s.rows + row;
-            constexpr int COLS = D / NG;
+            constexpr int COLS = SPLIT ? D / 2 : D;        // columns of this group
+            const uint32_t tO0 = tmem + lane_off + C::COL_O + (PAIR ? grp * D : 0);
             if (warp_live) {
 #pragma unroll 1
-                for (int c = grp * COLS; c < (grp + 1) * COLS; c += 32) {
+                for (int c = SPLIT ? grp * COLS : 0, cn = 0; cn < COLS; c += 32, cn += 32) {
                     float h[32];
-                    const uint32_t tO = tmem + lane_off + C::COL_O + c;
                     if (have0) {
                         uint32_t ov[32];
-                        tmem_ld_x32(tO, ov);
+                        tmem_ld_x32(tO0 + c, ov);
                         tmem_wait_ld();
                         reg_fence_x32(ov);
 #pragma unroll
@@ -548,7 +648,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                     }
                     if (have1) {
                         uint32_t ov[32];
-                        tmem_ld_x32(tO + D, ov);
+                        tmem_ld_x32(tO0 + D + c, ov);
                         tmem_wait_ld();
                         reg_fence_x32(ov);
 #pragma unroll
@@ -561,19 +661,20 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                             const int lo = (kt - g.len.kc) * BN;
                             uint32_t bits[BN / 32];
                             path_bits<BN / 32>(parent, t, lo, bits);
+#pragma unroll 1
+                            for (int key = lo; key < min(lo + BN, g.len.t); ++key) {
+                                uint32_t w = bits[0];
 #pragma unroll
-                            for (int w = 0; w < BN / 32; ++w)
-                                for (uint32_t left = bits[w]; left; left &= left - 1) {
-                                    const int key = lo + 32 * w + __ffs(left) - 1;
-                                    if (key >= g.len.t) break;
-                                    const uint16_t *v = static_cast<const uint16_t *>(p.v_new) +
-                                                        ((size_t)(g.b * p.s.Hkv + g.kvh) * p.s.T + key) * D + c;
+                                for (int x = 1; x < BN / 32; ++x) w = (key - lo) >> 5 == x ? bits[x] : w;
+                                if (!((w >> ((key - lo) & 31)) & 1u)) continue;
+                                const uint16_t *v = static_cast<const uint16_t *>(p.v_new) +
+                                                    ((size_t)(g.b * p.s.Hkv + g.kvh) * p.s.T + key) * D + c;
 #pragma unroll
-                                    for (int e = 0; e < 32; ++e) {
-                                        const float x = half_to_float<BF16>(__ldg(v + e));
-                                        if (!isfinite(x)) h[e] += x;
-                                    }
+                                for (int e = 0; e < 32; ++e) {
+                                    const float x = half_to_float<BF16>(__ldg(v + e));
+                                    if (!isfinite(x)) h[e] += x;
                                 }
+                            }
                         }
                     }
                     if (whole) {
@@ -596,7 +697,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                     }
                 }
             }
-            if (live && grp == 0) {
+            if (live && (!SPLIT || grp == 0)) {
                 const float lse2 = L == 0.f ? -INFINITY : M + lg2_approx(L);
                 if (whole)
                     p.lse[orow] = lse2 * 0.69314718055994531f;
@@ -617,23 +718,24 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         __syncwarp();
         tc_fence_after();
         tmem_dealloc(tmem, 512);
-    } else if (warp >= 4 && warp < 8 && *abort_flag) {
+    } else if (warp >= 4 && *abort_flag) {
         // This CTA gave up on a wait: NaN into every row it was given, its parts included
-        const int r = threadIdx.x - 128;
         const float nan = __uint_as_float(~0u);
-        walk = share;
-        while (walk.next(p.s, g)) {
-            const int row = g.mt * kRowTile + r;
-            if (row >= p.s.rows || row % p.s.T >= g.len.t) continue;
-            if (g.k0 == 0 && g.k1 == g.len.nt) {
-                const size_t orow = (size_t)(g.b * p.s.Hkv + g.kvh) * p.s.rows + row;
-                for (int c = 0; c < D * 2; c += 16)
-                    st_global_v4(static_cast<uint8_t *>(p.o) + orow * D * 2 + c, ~0u, ~0u, ~0u, ~0u);
-                p.lse[orow] = nan;
-            } else {
-                const size_t prow = (size_t)part_slot(blockIdx.x, g.k0) * p.part_rows + r;
-                for (int c = 0; c < D; ++c) p.part_o[prow * D + c] = nan;
-                p.part_lse[prow] = nan;
+        TreeWalk again(p.s, misc->b, misc->off, misc->left);
+        while (again.next(p.s, g)) {
+            for (int urow = threadIdx.x - 128; urow < p.s.tile; urow += 128 * NG) {
+                const int row = g.mt * p.s.tile + urow;
+                if (row >= p.s.rows || row % p.s.T >= g.len.t) continue;
+                if (g.k0 == 0 && g.k1 == g.len.nt) {
+                    const size_t orow = (size_t)(g.b * p.s.Hkv + g.kvh) * p.s.rows + row;
+                    for (int c = 0; c < D * 2; c += 16)
+                        st_global_v4(static_cast<uint8_t *>(p.o) + orow * D * 2 + c, ~0u, ~0u, ~0u, ~0u);
+                    p.lse[orow] = nan;
+                } else {
+                    const size_t prow = (size_t)part_slot(blockIdx.x, g.k0) * p.part_rows + urow;
+                    for (int c = 0; c < D; ++c) p.part_o[prow * D + c] = nan;
+                    p.part_lse[prow] = nan;
+                }
             }
         }
     }
@@ -653,16 +755,17 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
     // lengths are inputs of the call, not results of the kernel before: they may be read at once
     const Share sh = find_share(p.s.B, p.least, lane, k, grid, [&](int b) { return tree_steps(p.s, b); });
     const int total = sh.total, G = sh.G;
-    TreeWalk w{sh.b, sh.off, sh.left};
+    if (k >= G) return;
+    TreeWalk w(p.s, sh.b, sh.off, sh.left);
     TreeSeg g;
-    if (k >= G || !w.next(p.s, g) || g.k0 == 0) return;
+    if (!w.next(p.s, g) || g.k0 == 0) return;
     const int u0 = cut(total, G, k) - g.k0, u1 = u0 + g.len.nt;
     if (cut(total, G, k - 1) > u0) return;            // an earlier cut of the same unit
     int parts = 2;                                    // CTA k - 1's and CTA k's
     while (k + parts - 1 < G && cut(total, G, k + parts - 1) < u1) ++parts;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     for (int r = blockIdx.y * kJoinWarps + warp; r < p.part_rows; r += gridDim.y * kJoinWarps) {
-        const int row = g.mt * kRowTile + r;
+        const int row = g.mt * p.s.tile + r;
         if (row >= p.s.rows || row % p.s.T >= g.len.t) continue;
         auto prow = [&](int i) { return (size_t)part_slot(k - 1 + i, i) * p.part_rows + r; };
         float M = -INFINITY;
@@ -694,10 +797,11 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
     }
 }
 
-template <int D, bool BF16>
+template <int D, bool BF16, bool PAIR>
 cudaError_t launch_one(const TreeMaps &m, const TreeParams &p0, cudaStream_t st)
 {
-    auto kern = tree_kernel<D, BF16>;
+    using C = Cfg<D, PAIR>;
+    auto kern = tree_kernel<D, BF16, PAIR>;
     static std::atomic<uint64_t> configured{0};
     static std::atomic<int> sm_count[64];
     int dev = 0;
@@ -706,7 +810,7 @@ cudaError_t launch_one(const TreeMaps &m, const TreeParams &p0, cudaStream_t st)
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     const uint64_t bit = 1ull << dev;
     if (!(configured.load(std::memory_order_acquire) & bit)) {
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::ALLOC);
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::ALLOC);
         if (e != cudaSuccess) return e;
         int nsm = 0;
         e = cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev);
@@ -717,7 +821,7 @@ cudaError_t launch_one(const TreeMaps &m, const TreeParams &p0, cudaStream_t st)
     TreeParams p = p0;
     if (p.timeout_ns == 0) p.timeout_ns = kDefaultTimeoutNs;
     const int grid = clampi(sm_count[dev].load(std::memory_order_relaxed), 1, kMaxCtas);
-    kern<<<grid, Cfg<D>::THREADS, Cfg<D>::ALLOC, st>>>(m, p);
+    kern<<<grid, C::THREADS, C::ALLOC, st>>>(m, p);
     e = cudaGetLastError();
     if (e != cudaSuccess || grid == 1) return e;
     // the joining kernel is launched while the first one runs and waits for its end on the device
@@ -735,13 +839,19 @@ cudaError_t launch_one(const TreeMaps &m, const TreeParams &p0, cudaStream_t st)
 
 } // namespace
 
-int tree_keys(int D) { return D == 256 ? 64 : 128; }
+int tree_log_keys(int D) { return D == 256 ? 6 : 7; }
+
+int tree_tile(int D, long long rows) { return rows > kRowTile && D != 256 ? 2 * kRowTile : kRowTile; }
 
 cudaError_t launch_tree(int D, bool bf16, const TreeMaps &m, const TreeParams &p, cudaStream_t st)
 {
-    if (D == 64) return bf16 ? launch_one<64, true>(m, p, st) : launch_one<64, false>(m, p, st);
-    if (D == 128) return bf16 ? launch_one<128, true>(m, p, st) : launch_one<128, false>(m, p, st);
-    if (D == 256) return bf16 ? launch_one<256, true>(m, p, st) : launch_one<256, false>(m, p, st);
+    const bool pair = p.s.tile > kRowTile;
+#define TREE_CASE(DD, BB, PP) \
+    if (D == DD && bf16 == BB && pair == PP) return launch_one<DD, BB, PP>(m, p, st);
+    TREE_CASE(64, true, false) TREE_CASE(64, true, true) TREE_CASE(64, false, false) TREE_CASE(64, false, true)
+    TREE_CASE(128, true, false) TREE_CASE(128, true, true) TREE_CASE(128, false, false) TREE_CASE(128, false, true)
+    TREE_CASE(256, true, false) TREE_CASE(256, false, false)
+#undef TREE_CASE
     return cudaErrorInvalidValue;
 }
 

@@ -19,13 +19,18 @@ static unsigned rnd(unsigned n) { return (unsigned)rand() % n; }
 static TreeWalk share(const TreeShape &s, int least, int grid, int cta, int *total_out, int *G_out)
 {
     int total = 0;
-    for (int b = 0; b < s.B; ++b) total += s.Hkv * s.mtiles * tree_len(s, b).nt;
+    for (int b = 0; b < s.B; ++b) total += s.Hkv * s.units * tree_len(s, b).nt;
     const int G = ctas(total, grid, least);
-    const int begin = cta < G ? cut(total, G, cta) : total;
-    TreeWalk w{0, begin, cta < G ? cut(total, G, cta + 1) - begin : 0};
+    int begin = cta < G ? cut(total, G, cta) : total, b = 0;
+    const int left = cta < G ? cut(total, G, cta + 1) - begin : 0;
+    for (; b < s.B; ++b) {
+        const int one = s.Hkv * s.units * tree_len(s, b).nt;
+        if (begin < one) break;
+        begin -= one;
+    }
     *total_out = total;
     *G_out = G;
-    return w;
+    return TreeWalk(s, b, begin, left);
 }
 
 static int check_tree()
@@ -37,8 +42,9 @@ static int check_tree()
         s.Hkv = 1 + rnd(4);
         s.T = 1 + rnd(200);
         s.rows = s.T * (1 + rnd(4));
-        s.mtiles = cdiv(s.rows, 128);
-        s.BN = rnd(2) ? 128 : 64;
+        s.tile = rnd(2) ? 128 : 256;
+        s.units = cdiv(s.rows, s.tile);
+        s.lbn = rnd(2) ? 7 : 6;
         s.capacity = 16 * (1 + rnd(300));
         for (size_t b = 0; b < len.size(); ++b) {
             len[b] = (int)rnd(s.capacity + 40) - 20;   // out of range on both sides, too
@@ -56,8 +62,8 @@ static int check_tree()
             int mine = 0;
             TreeSeg g;
             while (w.next(s, g)) {
-                const long long id = ((long long)g.b * s.Hkv + g.kvh) * s.mtiles + g.mt;
-                if (g.len.nt <= 0 || g.k0 < 0 || g.k1 <= g.k0 || g.k1 > g.len.nt || g.kvh >= s.Hkv || g.mt >= s.mtiles)
+                const long long id = ((long long)g.b * s.Hkv + g.kvh) * s.units + g.mt;
+                if (g.len.nt <= 0 || g.k0 < 0 || g.k1 <= g.k0 || g.k1 > g.len.nt || g.kvh >= s.Hkv || g.mt >= s.units)
                     return fail("a segment outside its unit");
                 auto &own = unit[id];
                 own.resize(g.len.nt, -1);
@@ -83,7 +89,7 @@ static int check_tree()
         if (given != total) return fail("steps that nobody has");
         if (total && most - fewest > 1) return fail("unequal shares");
         size_t units = 0;
-        for (int b = 0; b < s.B; ++b) units += tree_len(s, b).nt ? (size_t)s.Hkv * s.mtiles : 0;
+        for (int b = 0; b < s.B; ++b) units += tree_len(s, b).nt ? (size_t)s.Hkv * s.units : 0;
         if (unit.size() != units) return fail("units that nobody has");
         for (auto &u : unit)
             for (int o : u.second)
@@ -99,7 +105,7 @@ static int check_tree()
             if (cut(t2, G2, k - 1) > u0) continue;
             int n = 2;
             while (k + n - 1 < G2 && cut(t2, G2, k + n - 1) < u1) ++n;
-            const auto &want = parts[((long long)g.b * s.Hkv + g.kvh) * s.mtiles + g.mt];
+            const auto &want = parts[((long long)g.b * s.Hkv + g.kvh) * s.units + g.mt];
             if ((int)want.size() != n) return fail("the number of parts");
             for (int i = 0; i < n; ++i)
                 if (part_slot(k - 1 + i, i) != want[i].second) return fail("the order of the parts");
