@@ -348,7 +348,7 @@ int fa_cache_weights(const fa_cache_t *cache, const void *q, const float *lse, c
  *   new_len               [B]: min(seq_len[b], keep).  Not seq_len itself (the layers of a model share it)
  *   next_pos              [B] the position of the next token; required when last > 0
  *   keep >= 1, first, last >= 0, first + last <= keep
- *   workspace             fa_evict_workspace_bytes(B, Hkv, capacity, keep) bytes
+ *   workspace             fa_evict_workspace_bytes(B, Hkv, capacity, keep) bytes, 8-byte aligned
  * Keys and values are moved within the cache's pages; pages that new_len does not cover are free.
  */
 size_t fa_evict_workspace_bytes(int B, int Hkv, int capacity, int keep);

@@ -9,34 +9,31 @@ status raises ``FaError``.
 from __future__ import annotations
 
 import ctypes
-import math
+import functools
+import struct
+import threading
 from typing import Optional, Tuple
 
 import torch
 
+from . import binding as _b
 from .binding import FaError, _check_stream_device, _OnDevice, _stream_handle, fa_strerror, load_library
 
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1}
+_I32, _F32 = torch.int32, torch.float32
 
+# fa_cache_t of include/fa.h: k, v, table, seq_len; B, Hkv, D, page, max_pages, num_pages, dtype
+_PACK = struct.Struct("PPPP7i4x").pack
 
-class _CacheStruct(ctypes.Structure):
-    """fa_cache_t of include/fa.h."""
-    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("table", ctypes.c_void_p),
-                ("seq_len", ctypes.c_void_p), ("B", ctypes.c_int), ("Hkv", ctypes.c_int), ("D", ctypes.c_int),
-                ("page", ctypes.c_int), ("max_pages", ctypes.c_int), ("num_pages", ctypes.c_int),
-                ("dtype", ctypes.c_int)]
-
-
-_P, _I, _F, _Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
-_CP = ctypes.POINTER(_CacheStruct)
+_P, _I, _F, _Z, _C = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t, ctypes.c_char_p
 _SIGNATURES = {
     "fa_tree_workspace_bytes": (_Z, [_I] * 4),
-    "fa_tree_fwd": (_I, [_CP] + [_P] * 7 + [_I, _I, _F, _P, _Z, _P]),
-    "fa_cache_append": (_I, [_CP] + [_P] * 7 + [_I, _P]),
+    "fa_tree_fwd": (_I, [_C] + [_P] * 7 + [_I, _I, _F, _P, _Z, _P]),
+    "fa_cache_append": (_I, [_C] + [_P] * 7 + [_I, _P]),
     "fa_weights_workspace_bytes": (_Z, []),
-    "fa_cache_weights": (_I, [_CP] + [_P] * 6 + [_I, _I, _I, _F, _P, _Z, _P]),
+    "fa_cache_weights": (_I, [_C] + [_P] * 6 + [_I, _I, _I, _F, _P, _Z, _P]),
     "fa_evict_workspace_bytes": (_Z, [_I] * 4),
-    "fa_cache_evict": (_I, [_CP] + [_P] * 6 + [_I, _I, _I, _P, _Z, _P]),
+    "fa_cache_evict": (_I, [_C] + [_P] * 6 + [_I, _I, _I, _P, _Z, _P]),
 }
 _lib = None
 
@@ -52,36 +49,67 @@ def _library() -> ctypes.CDLL:
     return _lib
 
 
-def _run(st: int) -> None:
-    if st != 0:
-        raise FaError(st, fa_strerror(st))
-
-
-def _need(name: str, t, shape, dtype, device) -> int:
-    """The address of a dense CUDA tensor of this shape, type and device."""
+def _refuse(name: str, t, shape, dtype, index: int):
+    """What is wrong with a tensor that _need does not take."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device} but the cache is on {device}: "
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device} but the cache is on cuda:{index}: "
                          "every tensor of one call must be on the same GPU")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _maybe(name: str, t, shape, dtype, device) -> Optional[int]:
-    return None if t is None else _need(name, t, shape, dtype, device)
+def _need(name: str, t, shape, dtype, index: int) -> int:
+    """The address of a dense CUDA tensor of this shape and type on this device."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    return _refuse(name, t, shape, dtype, index)
 
 
-def _keep_for(t: torch.Tensor, stream) -> None:
-    """A temporary used on `stream` must not be reused by the current stream's later work before it is done."""
-    if stream is not None:
-        s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device=t.device)
-        t.record_stream(s)
+def _launch(fn, index: int, stream, args) -> None:
+    """fn(*args, stream handle) with the cache's device current; raises on a non-zero status."""
+    if stream is None and _b._raw_stream is not None and _b._cur_device is not None and _b._cur_device() == index:
+        st = fn(*args, _b._raw_stream(index))
+    else:
+        device = torch.device("cuda", index)
+        _check_stream_device(stream, device)
+        with _OnDevice(device):
+            st = fn(*args, _stream_handle(stream))
+    if st != 0:
+        raise FaError(st, fa_strerror(st))
+
+
+_local = threading.local()
+
+
+def _workspace(need: int, given: Optional[torch.Tensor], like: torch.Tensor, stream) -> Tuple[torch.Tensor, int, int]:
+    """A workspace on like's device, its address and size: the caller's, or else one that this thread keeps
+    for the current stream, whose calls run one after another.  A call that is captured into a graph, or
+    that names a stream, gets one of its own."""
+    index = like.get_device()
+    if given is not None:
+        if given.get_device() != index or not given.is_contiguous():
+            raise ValueError("workspace must be a contiguous CUDA tensor on the cache's device")
+        return given, given.data_ptr(), given.nbytes
+    if stream is None and _b._raw_stream is not None and _b._cur_device is not None and _b._cur_device() == index \
+            and not torch.cuda.is_current_stream_capturing():
+        kept, key = _local.__dict__, (index, _b._raw_stream(index))
+        ws = kept.get(key)
+        if ws is None or ws[2] < need:
+            t = like.new_empty(need, dtype=torch.uint8)
+            ws = kept[key] = (t, t.data_ptr(), need)
+        return ws
+    t = like.new_empty(need, dtype=torch.uint8)
+    if stream is not None:   # not to be reused by the current stream's later work before `stream` is done with it
+        t.record_stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device=like.device))
+    return t, t.data_ptr(), need
 
 
 class KVCache:
@@ -94,48 +122,55 @@ class KVCache:
 
     Holds references to the tensors and no state of its own: update seq_len and table in place.
     """
-    __slots__ = ("k", "v", "seq_len", "table", "device", "dtype", "B", "Hkv", "D", "page", "capacity", "_c", "_ref")
+    __slots__ = ("k", "v", "seq_len", "table", "index", "dtype", "B", "Hkv", "D", "page", "capacity", "_c")
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, seq_len: torch.Tensor, table: Optional[torch.Tensor] = None):
         if not isinstance(k, torch.Tensor) or k.dim() != 4:
             raise ValueError("k must be a [num_pages, Hkv, page, D] tensor")
-        if k.dtype not in _DTYPES:
+        code = _DTYPES.get(k.dtype)
+        if code is None:
             raise ValueError(f"a cache is bf16 or fp16, not {k.dtype}")
-        if not k.is_cuda:
+        index = k.get_device()
+        if index < 0:
             raise ValueError("k must be a CUDA tensor")
-        dev, dt = k.device, k.dtype
-        num, Hkv, page, D = k.shape
+        shape = k.shape
+        num, Hkv, page, D = shape
         if not isinstance(seq_len, torch.Tensor) or seq_len.dim() != 1:
             raise ValueError("seq_len must be a [B] tensor")
         B = seq_len.shape[0]
         if table is None:
-            per = num // B if B else 0
+            per, at = num // B if B else 0, 0
         else:
             if not isinstance(table, torch.Tensor) or table.dim() != 2:
                 raise ValueError("table must be a [B, max_pages] tensor")
             per = table.shape[1]
-        self._c = _CacheStruct(_need("k", k, k.shape, dt, dev), _need("v", v, k.shape, dt, dev),
-                               _maybe("table", table, (B, per), torch.int32, dev),
-                               _need("seq_len", seq_len, (B,), torch.int32, dev), B, Hkv, D, page, per, num, _DTYPES[dt])
-        self._ref = ctypes.pointer(self._c)
+            at = _need("table", table, (B, per), _I32, index)
+        dt = k.dtype
+        self._c = _PACK(_need("k", k, shape, dt, index), _need("v", v, shape, dt, index), at,
+                        _need("seq_len", seq_len, (B,), _I32, index), B, Hkv, D, page, per, num, code)
         self.k, self.v, self.seq_len, self.table = k, v, seq_len, table
-        self.device, self.dtype, self.B, self.Hkv, self.D, self.page = dev, dt, B, Hkv, D, page
+        self.index, self.dtype, self.B, self.Hkv, self.D, self.page = index, dt, B, Hkv, D, page
         self.capacity = per * page
 
+    @property
+    def device(self) -> torch.device:
+        return self.k.device
 
+
+@functools.lru_cache(maxsize=256)
 def tree_workspace_bytes(Hq: int, Hkv: int, T: int, D: int) -> int:
     """Bytes of the workspace of ``tree_attention`` for T drafted tokens."""
     return _library().fa_tree_workspace_bytes(Hq, Hkv, T, D)
 
 
-def _workspace(need: int, given: Optional[torch.Tensor], device, stream) -> Tuple[torch.Tensor, int]:
-    if given is None:
-        ws = torch.empty(max(need, 1), dtype=torch.uint8, device=device)
-        _keep_for(ws, stream)
-        return ws, need
-    if not given.is_cuda or given.device != device or not given.is_contiguous():
-        raise ValueError("workspace must be a contiguous CUDA tensor on the cache's device")
-    return given, given.numel() * given.element_size()
+def _queries(q, cache: KVCache):
+    """The sizes of q [B, Hq, T, D], which must fit the cache."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 4:
+        raise ValueError("q must be a [B, Hq, T, D] tensor")
+    shape = q.shape
+    if shape[0] != cache.B or shape[3] != cache.D:
+        raise ValueError(f"q must have the cache's {cache.B} sequences and head dimension {cache.D}")
+    return shape
 
 
 def tree_attention(q, k_new, v_new, cache: KVCache, parent=None, draft_len=None, scale: Optional[float] = None,
@@ -146,27 +181,22 @@ def tree_attention(q, k_new, v_new, cache: KVCache, parent=None, draft_len=None,
     root; None: a chain), draft_len [B] int32 (None: T).  Returns (o [B, Hq, T, D], lse [B, Hq, T]
     float32), in o and lse where they are given; rows at or behind draft_len are not written.
     scale defaults to D ** -0.5.  workspace: tree_workspace_bytes(...) bytes that no other call in
-    flight uses; allocated when None."""
-    if not isinstance(q, torch.Tensor) or q.dim() != 4:
-        raise ValueError("q must be a [B, Hq, T, D] tensor")
-    dev, dt = cache.device, cache.dtype
-    B, Hq, T, D = q.shape
-    if B != cache.B or D != cache.D:
-        raise ValueError(f"q must have the cache's {cache.B} sequences and head dimension {cache.D}")
-    new = (B, cache.Hkv, T, D)
+    flight uses; None: one that is kept for the calling thread's current stream."""
+    shape = _queries(q, cache)
+    B, Hq, T, D = shape
+    i, dt, Hkv = cache.index, cache.dtype, cache.Hkv
+    new, rows = (B, Hkv, T, D), (B, Hq, T)
     if o is None:
         o = torch.empty_like(q)
     if lse is None:
-        lse = torch.empty((B, Hq, T), dtype=torch.float32, device=dev)
-    lib = _library()
-    args = (_need("q", q, q.shape, dt, dev), _need("k_new", k_new, new, dt, dev), _need("v_new", v_new, new, dt, dev),
-            _maybe("parent", parent, (B, T), torch.int32, dev), _maybe("draft_len", draft_len, (B,), torch.int32, dev),
-            _need("o", o, q.shape, dt, dev), _need("lse", lse, (B, Hq, T), torch.float32, dev))
-    _check_stream_device(stream, dev)
-    ws, size = _workspace(lib.fa_tree_workspace_bytes(Hq, cache.Hkv, T, D), workspace, dev, stream)
-    with _OnDevice(dev):
-        _run(lib.fa_tree_fwd(cache._ref, *args, Hq, T, 1.0 / math.sqrt(D) if scale is None else scale, ws.data_ptr(), size,
-                             _stream_handle(stream)))
+        lse = q.new_empty(rows, dtype=_F32)
+    lib = _lib or _library()
+    args = (cache._c, _need("q", q, shape, dt, i), _need("k_new", k_new, new, dt, i), _need("v_new", v_new, new, dt, i),
+            None if parent is None else _need("parent", parent, (B, T), _I32, i),
+            None if draft_len is None else _need("draft_len", draft_len, (B,), _I32, i),
+            _need("o", o, shape, dt, i), _need("lse", lse, rows, _F32, i), Hq, T, D ** -0.5 if scale is None else scale)
+    ws, at, size = _workspace(tree_workspace_bytes(Hq, Hkv, T, D), workspace, q, stream)
+    _launch(lib.fa_tree_fwd, i, stream, args + (at, size))
     return o, lse
 
 
@@ -178,23 +208,23 @@ def cache_append(cache: KVCache, k_new, v_new, path=None, count=None, weight=Non
     where given.  seq_len is not changed: add count to it after the last layer."""
     if not isinstance(k_new, torch.Tensor) or k_new.dim() != 4:
         raise ValueError("k_new must be a [B, Hkv, T, D] tensor")
-    dev, dt, T = cache.device, cache.dtype, k_new.shape[2]
-    B = cache.B
-    new, slots = (B, cache.Hkv, T, cache.D), (B, cache.Hkv, cache.capacity)
+    i, dt, B, Hkv, T = cache.index, cache.dtype, cache.B, cache.Hkv, k_new.shape[2]
+    new, slots = (B, Hkv, T, cache.D), (B, Hkv, cache.capacity)
     if path is not None and count is None:
         raise ValueError("a path needs count")
     if pos is not None and start is None:
         raise ValueError("pos needs start")
-    args = (_need("k_new", k_new, new, dt, dev), _need("v_new", v_new, new, dt, dev),
-            _maybe("path", path, (B, T), torch.int32, dev), _maybe("count", count, (B,), torch.int32, dev),
-            _maybe("start", start, (B,), torch.int32, dev), _maybe("weight", weight, slots, torch.float32, dev),
-            _maybe("pos", pos, slots, torch.int32, dev))
-    _check_stream_device(stream, dev)
-    lib = _library()
-    with _OnDevice(dev):
-        _run(lib.fa_cache_append(cache._ref, *args, T, _stream_handle(stream)))
+    lib = _lib or _library()
+    _launch(lib.fa_cache_append, i, stream,
+            (cache._c, _need("k_new", k_new, new, dt, i), _need("v_new", v_new, new, dt, i),
+             None if path is None else _need("path", path, (B, T), _I32, i),
+             None if count is None else _need("count", count, (B,), _I32, i),
+             None if start is None else _need("start", start, (B,), _I32, i),
+             None if weight is None else _need("weight", weight, slots, _F32, i),
+             None if pos is None else _need("pos", pos, slots, _I32, i), T))
 
 
+@functools.lru_cache(maxsize=1)
 def weights_workspace_bytes() -> int:
     """Bytes of the workspace of ``cache_weights``."""
     return _library().fa_weights_workspace_bytes()
@@ -208,29 +238,26 @@ def cache_weights(cache: KVCache, q, lse, weight=None, path=None, count=None, ca
     ``cache_append`` (the accepted rows); causal: row i is the query of slot seq_len[b] - count[b] + i
     and sees the slots up to its own.  weight [B, Hkv, capacity] float32 (None: zeros) is added to; the
     result is written to out, which defaults to weight itself (without a weight, to a new tensor of zeros)."""
-    if not isinstance(q, torch.Tensor) or q.dim() != 4:
-        raise ValueError("q must be a [B, Hq, T, D] tensor")
-    dev = cache.device
-    B, Hq, T, D = q.shape
-    if B != cache.B or D != cache.D:
-        raise ValueError(f"q must have the cache's {cache.B} sequences and head dimension {cache.D}")
+    shape = _queries(q, cache)
+    B, Hq, T, D = shape
+    i = cache.index
     if path is not None and count is None:
         raise ValueError("a path needs count")
     slots = (B, cache.Hkv, cache.capacity)
     if out is None:
-        out = torch.zeros(slots, dtype=torch.float32, device=dev) if weight is None else weight
-    args = (_need("q", q, q.shape, cache.dtype, dev), _need("lse", lse, (B, Hq, T), torch.float32, dev),
-            _maybe("path", path, (B, T), torch.int32, dev), _maybe("count", count, (B,), torch.int32, dev),
-            _maybe("weight", weight, slots, torch.float32, dev), _need("out", out, slots, torch.float32, dev))
-    _check_stream_device(stream, dev)
-    lib = _library()
-    ws, size = _workspace(lib.fa_weights_workspace_bytes(), workspace, dev, stream)
-    with _OnDevice(dev):
-        _run(lib.fa_cache_weights(cache._ref, *args, Hq, T, int(bool(causal)), 1.0 / math.sqrt(D) if scale is None else scale,
-                                  ws.data_ptr(), size, _stream_handle(stream)))
+        out = q.new_zeros(slots, dtype=_F32) if weight is None else weight
+    lib = _lib or _library()
+    args = (cache._c, _need("q", q, shape, cache.dtype, i), _need("lse", lse, (B, Hq, T), _F32, i),
+            None if path is None else _need("path", path, (B, T), _I32, i),
+            None if count is None else _need("count", count, (B,), _I32, i),
+            None if weight is None else _need("weight", weight, slots, _F32, i), _need("out", out, slots, _F32, i),
+            Hq, T, 1 if causal else 0, D ** -0.5 if scale is None else scale)
+    ws, at, size = _workspace(weights_workspace_bytes(), workspace, q, stream)
+    _launch(lib.fa_cache_weights, i, stream, args + (at, size))
     return out
 
 
+@functools.lru_cache(maxsize=256)
 def evict_workspace_bytes(B: int, Hkv: int, capacity: int, keep: int) -> int:
     """Bytes of the workspace of ``cache_evict``."""
     return _library().fa_evict_workspace_bytes(B, Hkv, capacity, keep)
@@ -243,19 +270,17 @@ def cache_evict(cache: KVCache, weight, pos, keep: int, first: int = 0, last: in
     kept slots at or above `keep` move to the freed ones below.  weight [B, Hkv, capacity] float32 and
     pos int32 follow the slots, in place unless weight_out and pos_out are given.  Returns new_len [B]
     int32 = min(seq_len, keep); seq_len itself is not changed."""
-    dev = cache.device
-    slots = (cache.B, cache.Hkv, cache.capacity)
+    i, B = cache.index, cache.B
+    slots = (B, cache.Hkv, cache.capacity)
     if last and next_pos is None:
         raise ValueError("last needs next_pos")
     if new_len is None:
-        new_len = torch.empty(cache.B, dtype=torch.int32, device=dev)
-    w, p = _need("weight", weight, slots, torch.float32, dev), _need("pos", pos, slots, torch.int32, dev)
-    args = (w, p, w if weight_out is None else _need("weight_out", weight_out, slots, torch.float32, dev),
-            p if pos_out is None else _need("pos_out", pos_out, slots, torch.int32, dev),
-            _need("new_len", new_len, (cache.B,), torch.int32, dev), _maybe("next_pos", next_pos, (cache.B,), torch.int32, dev))
-    _check_stream_device(stream, dev)
-    lib = _library()
-    ws, size = _workspace(lib.fa_evict_workspace_bytes(cache.B, cache.Hkv, cache.capacity, keep), workspace, dev, stream)
-    with _OnDevice(dev):
-        _run(lib.fa_cache_evict(cache._ref, *args, keep, first, last, ws.data_ptr(), size, _stream_handle(stream)))
+        new_len = cache.seq_len.new_empty(B)
+    w, p = _need("weight", weight, slots, _F32, i), _need("pos", pos, slots, _I32, i)
+    lib = _lib or _library()
+    args = (cache._c, w, p, w if weight_out is None else _need("weight_out", weight_out, slots, _F32, i),
+            p if pos_out is None else _need("pos_out", pos_out, slots, _I32, i), _need("new_len", new_len, (B,), _I32, i),
+            None if next_pos is None else _need("next_pos", next_pos, (B,), _I32, i), keep, first, last)
+    ws, at, size = _workspace(evict_workspace_bytes(B, cache.Hkv, cache.capacity, keep), workspace, cache.k, stream)
+    _launch(lib.fa_cache_evict, i, stream, args + (at, size))
     return new_len

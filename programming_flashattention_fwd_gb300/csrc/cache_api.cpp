@@ -312,7 +312,7 @@ int fa_cache_weights(const fa_cache_t *cache, const void *q, const float *lse, c
 size_t fa_evict_workspace_bytes(int B, int Hkv, int capacity, int keep)
 {
     if (B < 1 || Hkv < 1 || keep < 1 || capacity <= keep) return 0;
-    return (size_t)B * Hkv * 2 * (keep < capacity - keep ? keep : capacity - keep) * 4;
+    return (size_t)B * Hkv * (keep < capacity - keep ? keep : capacity - keep) * 2 * sizeof(uint2);
 }
 
 int fa_cache_evict(const fa_cache_t *cache, const float *weight, const int32_t *pos, float *weight_out, int32_t *pos_out,
@@ -324,6 +324,7 @@ int fa_cache_evict(const fa_cache_t *cache, const float *weight, const int32_t *
     const int B = cache->B, Hkv = cache->Hkv, cap = cache->max_pages * cache->page;
     if (keep < 1 || first < 0 || last < 0 || (long long)first + last > keep) return FA_ERR_BAD_DIM;
     if (B == 0) return FA_OK;
+    if ((double)cache->num_pages * Hkv * cache->page > 4294967000.0) return FA_ERR_BAD_DIM;
     if ((long long)B * Hkv * 8 > 0x7fffffffLL || (double)keep * cache->D > 8.0 * 2147483647.0 - 65536.0) return FA_ERR_BAD_DIM;
     st = check_cache_pointers(cache);
     if (st != FA_OK) return st;
@@ -331,7 +332,7 @@ int fa_cache_evict(const fa_cache_t *cache, const float *weight, const int32_t *
     if (!new_len || (cap > 0 && (!weight || !pos || !weight_out || !pos_out)) || (last > 0 && !next_pos) || (need && !workspace))
         return FA_ERR_NULL_PTR;
     if (!aligned(weight, 4) || !aligned(pos, 4) || !aligned(weight_out, 4) || !aligned(pos_out, 4) || !aligned(new_len, 4) ||
-        !aligned(next_pos, 4) || !aligned(workspace, 4))
+        !aligned(next_pos, 4) || !aligned(workspace, 8))
         return FA_ERR_ALIGN;
     if (workspace_bytes < need) return FA_ERR_TOO_LARGE;
     const size_t ns = (size_t)B * Hkv * cap * 4;
@@ -354,8 +355,9 @@ int fa_cache_evict(const fa_cache_t *cache, const float *weight, const int32_t *
     p.weight_out = weight_out;
     p.pos_out = pos_out;
     p.new_len = new_len;
-    p.moves = static_cast<int32_t *>(workspace);
-    p.longest = keep < cap - keep ? keep : cap - keep;
+    p.longest = keep < cap - keep ? keep : (cap > keep ? cap - keep : 0);
+    p.from = static_cast<uint2 *>(workspace);
+    p.to = p.from + (size_t)B * Hkv * p.longest;
     p.B = B;
     p.Hkv = Hkv;
     p.capacity = cap;

@@ -100,11 +100,11 @@ struct EvictParams {
     float *weight_out;               // may be weight
     int32_t *pos_out;                // may be pos
     int32_t *new_len;                // [B]
-    int32_t *moves;                  // [B * Hkv][2][longest]: freed slots, then the slots that move there
+    uint2 *from, *to;                // [B * Hkv][longest] (row, slot): slots that move, freed slots they move to
     int longest;                     // min(keep, capacity - keep)
     int B, Hkv, capacity, chunks;    // chunks: 16-byte chunks of a row
     int keep, first, last;
-    int held;                        // keys of a CTA's slots held in shared memory
+    int held, paged;                 // keys and page numbers of a CTA's slots held in shared memory
 };
 cudaError_t launch_evict(const EvictParams &p, cudaStream_t st);
 

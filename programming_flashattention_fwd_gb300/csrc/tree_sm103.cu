@@ -742,14 +742,16 @@ __global__ void __launch_bounds__(Cfg<D, PAIR>::THREADS, 1)
 }
 
 // Joins the parts of the units that a cut crosses: o = sum_i 2^(lse_i - M) o_i / sum_i 2^(lse_i - M).
-// Block x handles the unit whose first cut is the start of CTA x, one warp a row; the parts are
-// added in the order of the keys.
-constexpr int kJoinWarps = 4;
+// Block x handles the unit whose first cut is the start of CTA x + 1.  A row in a few parts takes one warp;
+// one in many parts (a sequence over the whole GPU) up to eight, every eighth part each, so that it costs
+// two round trips to L2.  The parts are added in the same order on every run.
+constexpr int kJoinWarps = 8;
 
 template <int D, bool BF16>
 __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_constant__ TreeParams p, int grid)
 {
     constexpr int PER = D / 32;
+    __shared__ float sums[kJoinWarps][D];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int k = blockIdx.x + 1;
     // lengths are inputs of the call, not results of the kernel before: they may be read at once
@@ -764,36 +766,54 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
     int parts = 2;                                    // CTA k - 1's and CTA k's
     while (k + parts - 1 < G && cut(total, G, k + parts - 1) < u1) ++parts;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    for (int r = blockIdx.y * kJoinWarps + warp; r < p.part_rows; r += gridDim.y * kJoinWarps) {
-        const int row = g.mt * p.s.tile + r;
-        if (row >= p.s.rows || row % p.s.T >= g.len.t) continue;
+    const int wide = parts <= 4 ? 1 : (parts <= 8 ? 2 : kJoinWarps);    // warps of a row
+    const int lead = warp & ~(wide - 1), sub = warp & (wide - 1), rows = kJoinWarps / wide;
+    for (int r0 = blockIdx.y * rows; r0 < p.part_rows; r0 += gridDim.y * rows) {
+        const int r = r0 + warp / wide, row = g.mt * p.s.tile + r;
+        const bool live = r < p.part_rows && row < p.s.rows && row % p.s.T < g.len.t;
         auto prow = [&](int i) { return (size_t)part_slot(k - 1 + i, i) * p.part_rows + r; };
-        float M = -INFINITY;
-        for (int i = lane; i < parts; i += 32) M = fmaxf(M, p.part_lse[prow(i)]);
-#pragma unroll
-        for (int d = 16; d; d >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, d));
-        const float ms = M == -INFINITY ? 0.f : M;
-        float acc[PER], sum = 0.f;
+        float acc[PER], sum = 0.f, M = -INFINITY;
 #pragma unroll
         for (int e = 0; e < PER; ++e) acc[e] = 0.f;
+        if (live) {
+            // every warp of the row: the maximum and the sum of all parts' weights
+            const float mine = lane < parts ? p.part_lse[prow(lane)] : -INFINITY;
+            M = mine;
+            for (int i = lane + 32; i < parts; i += 32) M = fmaxf(M, p.part_lse[prow(i)]);
+#pragma unroll
+            for (int d = 16; d; d >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, d));
+            const float ms = M == -INFINITY ? 0.f : M;
+            sum = lane < parts ? ex2_approx(mine - ms) : 0.f;
+            for (int i = lane + 32; i < parts; i += 32) sum += ex2_approx(p.part_lse[prow(i)] - ms);
+#pragma unroll
+            for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
+            // this warp's parts
 #pragma unroll 4
-        for (int i = 0; i < parts; ++i) {
-            const size_t at = prow(i);
-            const float f = ex2_approx(p.part_lse[at] - ms);
-            sum += f;
-            const float *src = p.part_o + at * D + lane * PER;
+            for (int i = sub; i < parts; i += wide) {
+                const float f = ex2_approx((i < 32 ? __shfl_sync(~0u, mine, i & 31) : p.part_lse[prow(i)]) - ms);
+                const float *src = p.part_o + prow(i) * D + lane * PER;
 #pragma unroll
-            for (int e = 0; e < PER; ++e) acc[e] = fmaf(f, src[e], acc[e]);
+                for (int e = 0; e < PER; ++e) acc[e] = fmaf(f, src[e], acc[e]);
+            }
         }
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        const size_t orow = (size_t)(g.b * p.s.Hkv + g.kvh) * p.s.rows + row;
-        uint32_t pk[PER / 2];
+        if (wide > 1) {
 #pragma unroll
-        for (int e = 0; e < PER / 2; ++e) pk[e] = pack2<BF16>(acc[2 * e] * inv, acc[2 * e + 1] * inv);
-        uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(p.o) + (orow * D + lane * PER) * 2);
+            for (int e = 0; e < PER; ++e) sums[warp][lane * PER + e] = acc[e];
+            __syncthreads();
+            if (sub == 0)
+                for (int x = 1; x < wide; ++x)
 #pragma unroll
-        for (int e = 0; e < PER / 2; ++e) dst[e] = pk[e];
-        if (lane == 0) p.lse[orow] = sum == 0.f ? -INFINITY : (M + lg2_approx(sum)) * 0.69314718055994531f;
+                    for (int e = 0; e < PER; ++e) acc[e] += sums[lead + x][lane * PER + e];
+            __syncthreads();
+        }
+        if (live && sub == 0) {
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            const size_t orow = (size_t)(g.b * p.s.Hkv + g.kvh) * p.s.rows + row;
+            uint32_t *dst = static_cast<uint32_t *>(p.o) + (orow * D + lane * PER) / 2;
+#pragma unroll
+            for (int e = 0; e < PER / 2; ++e) dst[e] = pack2<BF16>(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+            if (lane == 0) p.lse[orow] = sum == 0.f ? -INFINITY : (M + lg2_approx(sum)) * 0.69314718055994531f;
+        }
     }
 }
 
@@ -826,7 +846,7 @@ cudaError_t launch_one(const TreeMaps &m, const TreeParams &p0, cudaStream_t st)
     if (e != cudaSuccess || grid == 1) return e;
     // the joining kernel is launched while the first one runs and waits for its end on the device
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid - 1, clampi(cdiv(p.part_rows, kJoinWarps), 1, 32));
+    cfg.gridDim = dim3(grid - 1, clampi(p.part_rows, 1, 16));
     cfg.blockDim = dim3(32 * kJoinWarps);
     cfg.stream = st;
     cudaLaunchAttribute attr = {};

@@ -1,6 +1,5 @@
 """The cache operators' host side: the work schedule, the C ABI's refusals (made before any CUDA call)
 and the binding's checks.  No GPU needed."""
-import ctypes
 import math
 import os
 import subprocess
@@ -40,7 +39,7 @@ CACHE = dict(B=2, Hkv=2, D=128, page=64, max_pages=8, num_pages=20, dtype=0)
 def cache_struct(**over):
     a = dict(CACHE, **{n: ADDR[n] for n in ("k", "v", "table", "seq_len")})
     a.update({k: v for k, v in over.items() if k in a})
-    return ctypes.byref(fc._CacheStruct(*(a[n] for n, _ in fc._CacheStruct._fields_)))
+    return fc._PACK(*(a[n] or 0 for n in ("k", "v", "table", "seq_len", "B", "Hkv", "D", "page", "max_pages", "num_pages", "dtype")))
 
 
 def tree(lib, **over):
@@ -133,7 +132,7 @@ def test_evict_refusals(lib, over, code):
 def test_weights_and_evict_empty(lib):
     assert weights(lib, B=0, q=None) == 0 and weights(lib, max_pages=0, q=None) == 0
     assert evict(lib, B=0, weight=None) == 0
-    assert lib.fa_evict_workspace_bytes(2, 2, 100, 100) == 0 and lib.fa_evict_workspace_bytes(2, 2, 100, 90) == 2 * 2 * 2 * 10 * 4
+    assert lib.fa_evict_workspace_bytes(2, 2, 100, 100) == 0 and lib.fa_evict_workspace_bytes(2, 2, 100, 90) == 2 * 2 * 10 * 16
 
 
 class FakeCuda(torch.Tensor):
@@ -147,6 +146,9 @@ class FakeCuda(torch.Tensor):
     @property
     def device(self):
         return self._dev
+
+    def get_device(self):
+        return self._dev.index
 
 
 def on(shape, dtype=torch.bfloat16, idx=0):
@@ -190,7 +192,7 @@ def tree_args(**over):
     (dict(q=on((2, 5, 4, 64)).transpose(1, 2)), "contiguous")])
 def test_tree_attention_checks_its_tensors(over, what, monkeypatch, lib):
     called = []
-    monkeypatch.setattr(fc, "_run", lambda *a: called.append(1))
+    monkeypatch.setattr(fc, "_launch", lambda *a: called.append(1))
     with pytest.raises(ValueError, match=what):
         fc.tree_attention(**tree_args(**over))
     assert not called
@@ -226,3 +228,16 @@ def test_cache_evict_checks_its_tensors(over, what):
     a.update(over)
     with pytest.raises(ValueError, match=what):
         fc.cache_evict(**a)
+
+
+def test_struct_is_the_header_s(tmp_path):
+    """The packed fields of the binding against the C compiler's layout of fa_cache_t."""
+    src = tmp_path / "layout.c"
+    src.write_text('#include <stdio.h>\n#include <stddef.h>\n#include "fa.h"\nint main(void) { printf("%zu %zu %zu %zu %zu\\n", sizeof(fa_cache_t), '
+                   'offsetof(fa_cache_t, seq_len), offsetof(fa_cache_t, B), offsetof(fa_cache_t, page), offsetof(fa_cache_t, dtype)); return 0; }\n')
+    exe = str(tmp_path / "layout")
+    subprocess.run(["gcc", f"-I{fa_build.INCLUDE}", str(src), "-o", exe], check=True)
+    got = [int(x) for x in subprocess.run([exe], capture_output=True, text=True, check=True).stdout.split()]
+    packed = fc._PACK(1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 11)
+    assert got == [len(packed), 24, 32, 44, 56]
+    assert packed[32:60] == b"".join(x.to_bytes(4, "little") for x in range(5, 12))
