@@ -107,8 +107,6 @@ bool encode_pool(CUtensorMap *m, const void *base, const void *any, const fa_cac
     return encode(m, c->num_pages > 0 ? base : any, c->dtype == 0, 4, ext, rows);
 }
 
-size_t align16(size_t x) { return (x + 15) & ~(size_t)15; }
-
 } // namespace
 
 namespace fa {
@@ -131,7 +129,7 @@ size_t fa_tree_workspace_bytes(int Hq, int Hkv, int T, int D)
     if (Hkv < 1 || Hq < 1 || Hq % Hkv != 0 || T < 1 || D < 1) return 0;
     const long long rows = (long long)(Hq / Hkv) * T, tile = tree_tile(D, rows);
     const size_t part = (size_t)(rows < tile ? rows : tile);
-    return align16((size_t)2 * kMaxCtas * part * 4) + (size_t)2 * kMaxCtas * part * D * 4;
+    return (size_t)kMaxCtas * sizeof(Cut) + (size_t)2 * kMaxCtas * part * (D + 1) * 4;
 }
 
 int fa_tree_fwd(const fa_cache_t *cache, const void *q, const void *k_new, const void *v_new, const int32_t *parent,
@@ -193,7 +191,8 @@ int fa_tree_fwd(const fa_cache_t *cache, const void *q, const void *k_new, const
     p.q_panel = small ? 8192 : 16384;
     p.q_bufs = small ? 2 : 1;
     p.q_box = q_rows * 128;
-    p.part_o = static_cast<float *>(workspace);
+    p.cuts = static_cast<Cut *>(workspace);
+    p.part_o = reinterpret_cast<float *>(p.cuts + kMaxCtas);   // a multiple of 32 bytes on
     p.part_lse = p.part_o + (size_t)2 * kMaxCtas * p.part_rows * D;
     p.box_rows = box;
     p.least = 2;
@@ -248,7 +247,7 @@ int fa_cache_append(const fa_cache_t *cache, const void *k_new, const void *v_ne
     return launch_append(p, (int)blocks, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
 }
 
-size_t fa_weights_workspace_bytes(void) { return (size_t)2 * kMaxCtas * 256 * 4; }
+size_t fa_weights_workspace_bytes(void) { return (size_t)kMaxCtas * sizeof(Cut) + (size_t)2 * kMaxCtas * 256 * 4; }
 
 int fa_cache_weights(const fa_cache_t *cache, const void *q, const float *lse, const int32_t *path, const int32_t *count,
                      const float *weight, float *out, int Hq, int T, int causal, float scale, void *workspace,
@@ -297,7 +296,8 @@ int fa_cache_weights(const fa_cache_t *cache, const void *q, const float *lse, c
     p.path = path;
     p.weight = weight;
     p.out = out;
-    p.part = static_cast<float *>(workspace);
+    p.cuts = static_cast<Cut *>(workspace);
+    p.part = reinterpret_cast<float *>(p.cuts + kMaxCtas);
     p.box_rows = gcd(cache->page, 128);
     p.least = 1;
     p.sl2 = (float)((double)scale * 1.4426950408889634);

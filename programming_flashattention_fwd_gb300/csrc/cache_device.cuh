@@ -21,10 +21,10 @@ template <typename Steps>
 __device__ __forceinline__ Share find_share(int B, int least, int lane, int cta, int grid, Steps steps)
 {
     Share s;
-    int sum = 0;
-    for (int b = lane; b < B; b += 32) sum += steps(b);
-#pragma unroll
-    for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
+    const int head = lane < B ? steps(lane) : 0;   // the first 32 sequences are looked up once
+    int sum = head;
+    for (int b = lane + 32; b < B; b += 32) sum += steps(b);
+    sum = __reduce_add_sync(~0u, sum);
     s.total = sum;
     s.G = ctas(sum, grid, least);
     const int begin = cta < s.G ? cut(sum, s.G, cta) : sum;
@@ -32,7 +32,7 @@ __device__ __forceinline__ Share find_share(int B, int least, int lane, int cta,
     int before = 0;   // steps of the sequences before s.b
     for (s.b = 0; s.b < B; s.b += 32) {
         const int b = s.b + lane;
-        const int mine = b < B ? steps(b) : 0;
+        const int mine = s.b == 0 ? head : (b < B ? steps(b) : 0);
         int upto = mine;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {

@@ -21,6 +21,14 @@ struct Pages {
     int page, max_pages, num_pages;
 };
 
+// A cut unit, left by the CTA whose share starts with its first cut for whoever joins its parts.
+struct Cut {
+    int b, kvh, tile;   // which unit
+    int parts;          // 0: nothing to join here
+    int n;              // slots (weights) or drafted tokens (attention) of the sequence
+    int pad[3];
+};
+
 struct TreeParams {
     TreeShape s;
     Pages pages;
@@ -30,6 +38,7 @@ struct TreeParams {
     float *lse;              // [B, Hq, T]
     float *part_o;           // [2 * kMaxCtas][part_rows][D]
     float *part_lse;         // [2 * kMaxCtas][part_rows], log2 units
+    Cut *cuts;               // [kMaxCtas]
     int part_rows;           // min(rows, tile)
     int q_panel, q_box;      // bytes of a 64-column panel of a query tile in shared memory, and of one copy into it
     int q_bufs;              // query tiles in flight
@@ -58,6 +67,7 @@ struct WeighParams {
     const float *weight;      // [B, Hkv, capacity] or null: zero
     float *out;               // [B, Hkv, capacity]
     float *part;              // [2 * kMaxCtas][256]
+    Cut *cuts;                // [kMaxCtas]
     int box_rows;
     int least;
     float sl2;

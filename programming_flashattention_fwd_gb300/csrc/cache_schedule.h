@@ -18,8 +18,20 @@ namespace cache {
 __host__ __device__ __forceinline__ int cdiv(int a, int b) { return (int)(((uint32_t)a + (uint32_t)b - 1u) / (uint32_t)b); }
 __host__ __device__ __forceinline__ int clampi(int x, int lo, int hi) { return x < lo ? lo : (x > hi ? hi : x); }
 
-// First step of CTA c when G CTAs share `total` steps.
-__host__ __device__ __forceinline__ int cut(int total, int G, int c) { return (int)((long long)total * c / G); }
+// First step of CTA c when G CTAs share `total` steps (32-bit arithmetic while the product fits: the
+// 64-bit division is some hundred cycles of a kernel's start).
+__host__ __device__ __forceinline__ int cut(int total, int G, int c)
+{
+    if ((uint32_t)total < (1u << 23) && (uint32_t)c < 512u) return (int)((uint32_t)total * (uint32_t)c / (uint32_t)G);
+    return (int)((long long)total * c / G);
+}
+
+// The CTA that has a step: the last one whose first step is not behind it.
+__host__ __device__ __forceinline__ int cta_of(int total, int G, int step)
+{
+    if ((uint32_t)total < (1u << 23) && (uint32_t)G < 512u) return (int)(((uint32_t)(step + 1) * (uint32_t)G - 1u) / (uint32_t)total);
+    return (int)(((long long)(step + 1) * G - 1) / total);
+}
 
 // CTAs that share `total` steps: at most `grid`, and no fewer than `least` steps each.
 __host__ __device__ __forceinline__ int ctas(int total, int grid, int least)
@@ -67,6 +79,8 @@ struct TreeWalk {
     int left, b, kvh, mt, k;
     TreeLen len;
 
+    TreeWalk() = default;
+
     __host__ __device__ __forceinline__ TreeWalk(const TreeShape &s, int b0, int off, int steps) : left(steps), b(b0), kvh(0), mt(0), k(0)
     {
         if (left <= 0) return;
@@ -106,6 +120,15 @@ struct TreeWalk {
 // Workspace slot of the part that CTA c computes of a unit it shares: a CTA shares at most the unit
 // it starts in the middle of (slot 2 c) and the unit it leaves unfinished (slot 2 c + 1).
 __host__ __device__ __forceinline__ int part_slot(int c, int k0) { return 2 * c + (k0 == 0 ? 1 : 0); }
+
+// Parts of the unit (n steps) that CTA c's share starts in, at step k0 of it, if that is the unit's first cut
+// (they are CTA c - 1's, c's and so on); else 0.
+__host__ __device__ __forceinline__ int parts_from(int total, int G, int c, int k0, int n)
+{
+    if (k0 <= 0) return 0;
+    const int u0 = cut(total, G, c) - k0;
+    return cut(total, G, c - 1) > u0 ? 0 : cta_of(total, G, u0 + n - 1) - c + 2;
+}
 
 // ---------------------------------------------------------------- accumulated attention weight
 // A unit is one key tile of `keys` slots of (sequence, KV head); its steps are the tiles of NQ query rows
@@ -210,6 +233,8 @@ struct WeighTiles {
 struct WeighWalk {
     int left, b, kvh, kt, s;
     WeighLen len;
+
+    WeighWalk() = default;
 
     // `steps` steps from step `off` of sequence b0
     __host__ __device__ __forceinline__ WeighWalk(const WeighShape &sh, int b0, int off, int steps) : left(steps), b(b0), kvh(0), kt(0), s(0)

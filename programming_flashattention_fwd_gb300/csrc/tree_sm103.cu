@@ -74,7 +74,7 @@ struct Cfg {
     static constexpr int NBAR = 4 + 2 * NS + 2 + 2 + 2 + 2 + 1;    // q[2], qfree[2], full, empty, S[2], P[2], PV[2], join, read, done
     static constexpr int OFF_ML = OFF_BAR + ((NBAR * 8 + 15) / 16) * 16;   // [NG][128] (m, l)
     static constexpr int OFF_MISC = OFF_ML + NG * 128 * 8;
-    static constexpr int BYTES = OFF_MISC + 48;
+    static constexpr int BYTES = OFF_MISC + 64;
     static_assert(BYTES <= 232448, "shared memory of one CTA");
     // room to align the base to 1024 bytes, as far as there is any (the kernel checks what it got)
     static constexpr int ALLOC = BYTES + 1024 <= 232448 ? BYTES + 1024 : 232448;
@@ -87,7 +87,7 @@ struct Misc {
     uint32_t tmem;
     int abort;
     int nonfinite;      // 1 + index of the last segment whose drafted V held a non-finite value
-    int b, off, left;   // this CTA's share
+    TreeWalk share;     // this CTA's share, not walked yet
 };
 
 // x is an infinity or a NaN, in a 16-bit pair: the pair with those halves cleared, and whether there were any.
@@ -199,17 +199,19 @@ __global__ void __launch_bounds__(Cfg<D, PAIR>::THREADS, 1)
         if (lane < 5) tma_prefetch_map(lane == 0 ? &maps.q : lane == 1 ? &maps.k : lane == 2 ? &maps.v : lane == 3 ? &maps.k_new : &maps.v_new);
     } else if (warp == 3) {
         const Share w = find_share(p.s.B, p.least, lane, blockIdx.x, gridDim.x, [&](int b) { return tree_steps(p.s, b); });
+        const TreeWalk mine(p.s, w.b, w.off, w.left);
         if (lane == 0) {
-            misc->b = w.b;
-            misc->off = w.off;
-            misc->left = w.left;
+            const_cast<Misc *>(misc)->share = mine;
+            Cut c = {};
+            if (w.left > 0) c = Cut{mine.b, mine.kvh, mine.mt, parts_from(w.total, w.G, blockIdx.x, mine.k, mine.len.nt), mine.len.t, {}};
+            p.cuts[blockIdx.x] = c;
         }
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = misc->tmem;
-    TreeWalk walk(p.s, misc->b, misc->off, misc->left);
+    TreeWalk walk = const_cast<const Misc *>(misc)->share;
     TreeSeg g = {};
     const WarpWait wait_all{abort_flag, tmo, status};
 
@@ -721,7 +723,7 @@ __global__ void __launch_bounds__(Cfg<D, PAIR>::THREADS, 1)
     } else if (warp >= 4 && *abort_flag) {
         // This CTA gave up on a wait: NaN into every row it was given, its parts included
         const float nan = __uint_as_float(~0u);
-        TreeWalk again(p.s, misc->b, misc->off, misc->left);
+        TreeWalk again = const_cast<const Misc *>(misc)->share;
         while (again.next(p.s, g)) {
             for (int urow = threadIdx.x - 128; urow < p.s.tile; urow += 128 * NG) {
                 const int row = g.mt * p.s.tile + urow;
@@ -742,58 +744,67 @@ __global__ void __launch_bounds__(Cfg<D, PAIR>::THREADS, 1)
 }
 
 // Joins the parts of the units that a cut crosses: o = sum_i 2^(lse_i - M) o_i / sum_i 2^(lse_i - M).
-// Block x handles the unit whose first cut is the start of CTA x + 1.  A row in a few parts takes one warp;
-// one in many parts (a sequence over the whole GPU) up to eight, every eighth part each, so that it costs
-// two round trips to L2.  The parts are added in the same order on every run.
-constexpr int kJoinWarps = 8;
+// Block x looks whether CTA x + 1 left such a unit (the unit's first cut is the start of its share).  A row in
+// a few parts takes one warp; one in many parts (a sequence over the whole GPU) all four, every fourth part
+// each.  The parts are added in the same order on every run.
+constexpr int kJoinWarps = 4;
 
 template <int D, bool BF16>
-__global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_constant__ TreeParams p, int grid)
+__global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_constant__ TreeParams p)
 {
-    constexpr int PER = D / 32;
+    constexpr int PER = D / 32, FEW = 4;
     __shared__ float sums[kJoinWarps][D];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int k = blockIdx.x + 1;
-    // lengths are inputs of the call, not results of the kernel before: they may be read at once
-    const Share sh = find_share(p.s.B, p.least, lane, k, grid, [&](int b) { return tree_steps(p.s, b); });
-    const int total = sh.total, G = sh.G;
-    if (k >= G) return;
-    TreeWalk w(p.s, sh.b, sh.off, sh.left);
-    TreeSeg g;
-    if (!w.next(p.s, g) || g.k0 == 0) return;
-    const int u0 = cut(total, G, k) - g.k0, u1 = u0 + g.len.nt;
-    if (cut(total, G, k - 1) > u0) return;            // an earlier cut of the same unit
-    int parts = 2;                                    // CTA k - 1's and CTA k's
-    while (k + parts - 1 < G && cut(total, G, k + parts - 1) < u1) ++parts;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int wide = parts <= 4 ? 1 : (parts <= 8 ? 2 : kJoinWarps);    // warps of a row
-    const int lead = warp & ~(wide - 1), sub = warp & (wide - 1), rows = kJoinWarps / wide;
+    const Cut c = p.cuts[blockIdx.x + 1];
+    const int parts = c.parts;
+    if (parts == 0) return;
+    const int wide = parts > 2 * FEW ? kJoinWarps : 1;            // warps of a row
+    const int sub = wide > 1 ? warp : 0, rows = kJoinWarps / wide;
     for (int r0 = blockIdx.y * rows; r0 < p.part_rows; r0 += gridDim.y * rows) {
-        const int r = r0 + warp / wide, row = g.mt * p.s.tile + r;
-        const bool live = r < p.part_rows && row < p.s.rows && row % p.s.T < g.len.t;
-        auto prow = [&](int i) { return (size_t)part_slot(k - 1 + i, i) * p.part_rows + r; };
+        const int r = r0 + (wide > 1 ? 0 : warp), row = c.tile * p.s.tile + r;
+        const bool live = r < p.part_rows && row < p.s.rows && row % p.s.T < c.n;
+        auto prow = [&](int i) { return (size_t)part_slot((int)blockIdx.x + i, i) * p.part_rows + r; };
         float acc[PER], sum = 0.f, M = -INFINITY;
 #pragma unroll
         for (int e = 0; e < PER; ++e) acc[e] = 0.f;
         if (live) {
-            // every warp of the row: the maximum and the sum of all parts' weights
+            // the first rows are on their way while the weights (every warp: of all parts) are worked out
+            float x[FEW][PER];
+            auto fetch = [&](int i0) {
+#pragma unroll
+                for (int j = 0; j < FEW; ++j)
+#pragma unroll
+                    for (int e = 0; e < PER; e += 2) {
+                        const int i = i0 + j * wide;
+                        const float2 v = i < parts ? *reinterpret_cast<const float2 *>(p.part_o + prow(i) * D + lane * PER + e) : make_float2(0.f, 0.f);
+                        x[j][e] = v.x;
+                        x[j][e + 1] = v.y;
+                    }
+            };
             const float mine = lane < parts ? p.part_lse[prow(lane)] : -INFINITY;
+            fetch(sub);
             M = mine;
             for (int i = lane + 32; i < parts; i += 32) M = fmaxf(M, p.part_lse[prow(i)]);
 #pragma unroll
             for (int d = 16; d; d >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, d));
             const float ms = M == -INFINITY ? 0.f : M;
-            sum = lane < parts ? ex2_approx(mine - ms) : 0.f;
+            const float w = lane < parts ? ex2_approx(mine - ms) : 0.f;
+            sum = w;
             for (int i = lane + 32; i < parts; i += 32) sum += ex2_approx(p.part_lse[prow(i)] - ms);
 #pragma unroll
             for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
-            // this warp's parts
-#pragma unroll 4
-            for (int i = sub; i < parts; i += wide) {
-                const float f = ex2_approx((i < 32 ? __shfl_sync(~0u, mine, i & 31) : p.part_lse[prow(i)]) - ms);
-                const float *src = p.part_o + prow(i) * D + lane * PER;
+#pragma unroll 1
+            for (int i0 = sub; i0 < parts; i0 += FEW * wide) {
+                if (i0 != sub) fetch(i0);
 #pragma unroll
-                for (int e = 0; e < PER; ++e) acc[e] = fmaf(f, src[e], acc[e]);
+                for (int j = 0; j < FEW; ++j) {
+                    const int i = i0 + j * wide;
+                    if (i >= parts) break;
+                    const float f = i < 32 ? __shfl_sync(~0u, w, i & 31) : ex2_approx(p.part_lse[prow(i)] - ms);
+#pragma unroll
+                    for (int e = 0; e < PER; ++e) acc[e] = fmaf(f, x[j][e], acc[e]);
+                }
             }
         }
         if (wide > 1) {
@@ -801,14 +812,15 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
             for (int e = 0; e < PER; ++e) sums[warp][lane * PER + e] = acc[e];
             __syncthreads();
             if (sub == 0)
-                for (int x = 1; x < wide; ++x)
 #pragma unroll
-                    for (int e = 0; e < PER; ++e) acc[e] += sums[lead + x][lane * PER + e];
+                for (int x = 1; x < kJoinWarps; ++x)
+#pragma unroll
+                    for (int e = 0; e < PER; ++e) acc[e] += sums[x][lane * PER + e];
             __syncthreads();
         }
         if (live && sub == 0) {
             const float inv = sum == 0.f ? 0.f : 1.f / sum;
-            const size_t orow = (size_t)(g.b * p.s.Hkv + g.kvh) * p.s.rows + row;
+            const size_t orow = (size_t)(c.b * p.s.Hkv + c.kvh) * p.s.rows + row;
             uint32_t *dst = static_cast<uint32_t *>(p.o) + (orow * D + lane * PER) / 2;
 #pragma unroll
             for (int e = 0; e < PER / 2; ++e) dst[e] = pack2<BF16>(acc[2 * e] * inv, acc[2 * e + 1] * inv);
@@ -846,7 +858,7 @@ cudaError_t launch_one(const TreeMaps &m, const TreeParams &p0, cudaStream_t st)
     if (e != cudaSuccess || grid == 1) return e;
     // the joining kernel is launched while the first one runs and waits for its end on the device
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid - 1, clampi(p.part_rows, 1, 16));
+    cfg.gridDim = dim3(grid - 1, clampi(p.part_rows, 1, 32));
     cfg.blockDim = dim3(32 * kJoinWarps);
     cfg.stream = st;
     cudaLaunchAttribute attr = {};
@@ -854,7 +866,7 @@ cudaError_t launch_one(const TreeMaps &m, const TreeParams &p0, cudaStream_t st)
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, join_kernel<D, BF16>, p, grid);
+    return cudaLaunchKernelEx(&cfg, join_kernel<D, BF16>, p);
 }
 
 } // namespace

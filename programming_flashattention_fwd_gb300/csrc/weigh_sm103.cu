@@ -60,7 +60,7 @@ struct Cfg {
     static constexpr int OFF_ROWS = OFF_BAR + ((NBAR * 8 + 15) / 16) * 16;   // NB x { lse2[128], limit[128] }
     static constexpr int OFF_JOIN = OFF_ROWS + NB * 1024;                    // [NB][128] sums handed over
     static constexpr int OFF_MISC = OFF_JOIN + NB * 512;
-    static constexpr int BYTES = OFF_MISC + 64;
+    static constexpr int BYTES = OFF_MISC + 128;
     static constexpr int ALLOC = BYTES + 1024;
     static_assert(ALLOC <= 232448, "shared memory of one CTA");
 };
@@ -69,7 +69,7 @@ struct Misc {
     uint32_t tmem;
     int abort;
     int lowest[NB], cols[NB];   // of each step in flight: lowest limit of its rows, how many rows
-    int b, off, left;           // this CTA's share
+    WeighWalk share;            // this CTA's share, not walked yet
 };
 
 template <int D, bool BF16>
@@ -136,17 +136,19 @@ __global__ void __launch_bounds__(THREADS, 1)
             const WeighLen l = weigh_len(p.s, b);
             return p.s.Hkv * weigh_before(l, l.kt);
         });
+        const WeighWalk mine(p.s, w.b, w.off, w.left);
         if (lane == 0) {
-            misc->b = w.b;
-            misc->off = w.off;
-            misc->left = w.left;
+            const_cast<Misc *>(misc)->share = mine;
+            Cut c = {};
+            if (w.left > 0) c = Cut{mine.b, mine.kvh, mine.kt, parts_from(w.total, w.G, blockIdx.x, mine.s, weigh_steps(mine.len, mine.kt)), mine.len.n, {}};
+            p.cuts[blockIdx.x] = c;
         }
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = misc->tmem;
-    WeighWalk walk(p.s, misc->b, misc->off, misc->left);
+    WeighWalk walk = const_cast<const Misc *>(misc)->share;
     WeighSeg g;
 
     const WarpWait wait_all{abort_flag, tmo, status};
@@ -443,7 +445,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     } else if (warp >= 4 && warp < 8 && *abort_flag) {
         // This CTA gave up on a wait: NaN into every sum it was given
         const int r = threadIdx.x - 128;
-        walk = WeighWalk(p.s, misc->b, misc->off, misc->left);
+        walk = const_cast<const Misc *>(misc)->share;
         while (walk.next(p.s, g)) {
             if (g.kt * 128 + r >= g.len.n) continue;
             if (g.s0 == 0 && g.s1 == g.ns)
@@ -478,7 +480,7 @@ struct Prompt {
     static constexpr int NBAR = 2 + 2 * QS + 2 * NBUF + 2 * NR + 2;     // K, Q (full, empty); S (full, free); rows (full, free); unit, done
     static constexpr int OFF_ROWS = OFF_BAR + ((NBAR * 8 + 15) / 16) * 16;   // NR x { -lse2[128], limit[128] }
     static constexpr int OFF_MISC = OFF_ROWS + NR * 1024;
-    static constexpr int BYTES = OFF_MISC + 64;
+    static constexpr int BYTES = OFF_MISC + 128;
     static constexpr int ALLOC = BYTES + 1024;
     static_assert(ALLOC <= 232448, "shared memory of one CTA");
     static constexpr uint32_t COL_S = D;               // the scores start behind the two key tiles
@@ -576,17 +578,19 @@ __global__ void __launch_bounds__(Prompt<D>::THREADS, 1)
             const WeighLen l = weigh_len(p.s, b);
             return p.s.Hkv * weigh_before(l, l.kt);
         });
+        const WeighWalk mine(p.s, w.b, w.off, w.left);
         if (lane == 0) {
-            misc->b = w.b;
-            misc->off = w.off;
-            misc->left = w.left;
+            const_cast<Misc *>(misc)->share = mine;
+            Cut c = {};
+            if (w.left > 0) c = Cut{mine.b, mine.kvh, mine.kt, parts_from(w.total, w.G, blockIdx.x, mine.s, weigh_steps(mine.len, mine.kt)), mine.len.n, {}};
+            p.cuts[blockIdx.x] = c;
         }
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = misc->tmem;
-    WeighWalk walk(p.s, misc->b, misc->off, misc->left);
+    WeighWalk walk = const_cast<const Misc *>(misc)->share;
     WeighSeg g;
 
     const WarpWait wait_all{abort_flag, tmo, status};
@@ -805,7 +809,7 @@ __global__ void __launch_bounds__(Prompt<D>::THREADS, 1)
     } else if (warp >= 4 && *abort_flag) {
         // This CTA gave up on a wait: NaN into every sum it was given
         const int r = threadIdx.x - 128;
-        walk = WeighWalk(p.s, misc->b, misc->off, misc->left);
+        walk = const_cast<const Misc *>(misc)->share;
         while (walk.next(p.s, g)) {
             const int slot = g.kt * 256 + r;
             if (slot >= g.len.n) continue;
@@ -817,30 +821,21 @@ __global__ void __launch_bounds__(Prompt<D>::THREADS, 1)
     }
 }
 
-// Adds the parts of the key tiles that a cut crosses, in the order of the steps; block x handles the
-// key tile whose first cut is the start of CTA x + 1.
-__global__ void __launch_bounds__(256) weigh_join_kernel(const __grid_constant__ WeighParams p, int grid)
+// Adds the parts of the key tiles that a cut crosses, in the order of the steps; block x looks whether CTA
+// x + 1 left such a key tile (its first cut is the start of that CTA's share).
+__global__ void __launch_bounds__(256) weigh_join_kernel(const __grid_constant__ WeighParams p)
 {
-    const int k = blockIdx.x + 1, lane = threadIdx.x & 31, r = threadIdx.x;
-    const Share sh = find_share(p.s.B, p.least, lane, k, grid, [&](int b) {
-        const WeighLen l = weigh_len(p.s, b);
-        return p.s.Hkv * weigh_before(l, l.kt);
-    });
-    if (k >= sh.G) return;
-    WeighWalk w(p.s, sh.b, sh.off, sh.left);
-    WeighSeg g;
-    if (!w.next(p.s, g) || g.s0 == 0) return;
-    const int u0 = cut(sh.total, sh.G, k) - g.s0, u1 = u0 + g.ns;
-    if (cut(sh.total, sh.G, k - 1) > u0) return;          // an earlier cut of the same key tile
-    int parts = 2;
-    while (k + parts - 1 < sh.G && cut(sh.total, sh.G, k + parts - 1) < u1) ++parts;
-    const int slot = g.kt * p.s.keys + r;
-    const size_t at = (size_t)(g.b * p.s.Hkv + g.kvh) * p.s.capacity + slot;
+    const int r = threadIdx.x;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (slot >= g.len.n || r >= p.s.keys) return;
+    const Cut c = p.cuts[blockIdx.x + 1];
+    const int slot = c.tile * p.s.keys + r;
+    if (c.parts == 0 || slot >= c.n) return;
+    const size_t at = (size_t)(c.b * p.s.Hkv + c.kvh) * p.s.capacity + slot;
+    const float base = p.weight ? p.weight[at] : 0.f;
     float sum = 0.f;
-    for (int i = 0; i < parts; ++i) sum += p.part[(size_t)part_slot(k - 1 + i, i) * 256 + r];
-    p.out[at] = (p.weight ? p.weight[at] : 0.f) + sum;
+#pragma unroll 4
+    for (int i = 0; i < c.parts; ++i) sum += p.part[(size_t)part_slot((int)blockIdx.x + i, i) * 256 + r];
+    p.out[at] = base + sum;
 }
 
 // KIND 0: gathered or packed rows; 1: a prompt; 2: a long prompt, with the loop over a tile's columns
@@ -884,7 +879,7 @@ cudaError_t launch_one(const WeighMaps &m, const WeighParams &p0, cudaStream_t s
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, weigh_join_kernel, p, grid);
+    return cudaLaunchKernelEx(&cfg, weigh_join_kernel, p);
 }
 
 } // namespace

@@ -100,11 +100,9 @@ static int check_tree()
             int t2, G2;
             TreeWalk w = share(s, least, grid, k, &t2, &G2);
             TreeSeg g;
-            if (k >= G2 || !w.next(s, g) || g.k0 == 0) continue;
-            const int u0 = cut(t2, G2, k) - g.k0, u1 = u0 + g.len.nt;
-            if (cut(t2, G2, k - 1) > u0) continue;
-            int n = 2;
-            while (k + n - 1 < G2 && cut(t2, G2, k + n - 1) < u1) ++n;
+            if (k >= G2 || !w.next(s, g)) continue;
+            const int n = parts_from(t2, G2, k, g.k0, g.len.nt);
+            if (n == 0) continue;
             const auto &want = parts[((long long)g.b * s.Hkv + g.kvh) * s.units + g.mt];
             if ((int)want.size() != n) return fail("the number of parts");
             for (int i = 0; i < n; ++i)
@@ -112,6 +110,10 @@ static int check_tree()
             ++joined;
         }
         if (joined != parts.size()) return fail("a cut unit that is not joined");
+        for (int step = 0; step < total; step += 1 + rnd(50)) {
+            const int c = cta_of(total, G, step);
+            if (cut(total, G, c) > step || cut(total, G, c + 1) <= step) return fail("the CTA of a step");
+        }
     }
     return 0;
 }
@@ -189,10 +191,22 @@ static int check_weigh()
     return 0;
 }
 
+static int check_cuts()
+{
+    // both widths of the arithmetic, and the line between them
+    for (int total : {1, 2, 159, 8388607, 8388608, 8388609, 2147483647})
+        for (int G : {1, 2, 151, 152, 160})
+            for (int c = 0; c <= G && total >= G; ++c) {
+                if (cut(total, G, c) != (int)((long long)total * c / G)) return fail("a cut");
+                if (c < G && (cta_of(total, G, cut(total, G, c)) != c || (c && cta_of(total, G, cut(total, G, c) - 1) != c - 1))) return fail("the CTA of a cut");
+            }
+    return 0;
+}
+
 int main()
 {
     srand(1);
-    if (check_tree() || check_weigh()) return 1;
+    if (check_cuts() || check_tree() || check_weigh()) return 1;
     std::printf("ok\n");
     return 0;
 }
