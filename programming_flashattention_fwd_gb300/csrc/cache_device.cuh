@@ -10,6 +10,12 @@
 namespace fa {
 namespace cache {
 
+// Waits for the end of the kernels that this one may overlap (launch_overlapped): before the first access to
+// memory that they may write, and before the first write that they may read or overwrite.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// From here on the next kernel may be scheduled, once every CTA has come this far.
+__device__ __forceinline__ void grid_done_soon() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 struct Share {
     int total, G;         // all steps, the CTAs that have some
     int b, off, left;     // this CTA's: `left` steps from step `off` of sequence b

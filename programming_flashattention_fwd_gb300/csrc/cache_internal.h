@@ -14,6 +14,27 @@ namespace cache {
 constexpr int kMaxCtas = 160;
 constexpr int kRowTile = 128;
 
+// Launches a kernel that may be scheduled while the kernel before it on the stream drains; it waits on the
+// device (grid_wait) before it touches memory.  Back to back this hides the launch and the kernel's start.
+template <typename Kernel, typename... Args>
+cudaError_t launch_overlapped(Kernel kern, dim3 grid, unsigned threads, size_t smem, unsigned cluster, cudaStream_t st, Args... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2] = {};
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 // Where the slots of a sequence are: slot s on row s % page of page table[b * max_pages + s / page]
 // (page b * max_pages + s / page without a table).
 struct Pages {

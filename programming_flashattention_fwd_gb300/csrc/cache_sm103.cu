@@ -3,6 +3,7 @@
 #include <atomic>
 #include <cstdint>
 
+#include "cache_device.cuh"
 #include "cache_internal.h"
 
 namespace fa {
@@ -30,6 +31,8 @@ constexpr int kAppendThreads = 256;
 
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_constant__ AppendParams p)
 {
+    grid_wait();
+    grid_done_soon();
     const int head = blockIdx.x / p.blocks_per_head, tile = blockIdx.x - head * p.blocks_per_head;
     const int b = head / p.Hkv, h = head - b * p.Hkv;
     const int i = tile * (kAppendThreads / p.chunks) + threadIdx.x / p.chunks, ch = threadIdx.x % p.chunks;
@@ -132,6 +135,8 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const __grid_co
     __shared__ int cta_a, cta_b, cta_match;
     __shared__ int s_digit, s_need, s_count;
     __shared__ unsigned long long s_last;
+    grid_wait();
+    grid_done_soon();
     const int C = cluster_size(), rank = cluster_rank();
     const int head = blockIdx.x / C, b = head / p.Hkv, h = head - b * p.Hkv;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -424,26 +429,14 @@ cudaError_t launch_evict(const EvictParams &p0, cudaStream_t st)
     p.held = per < kHeldMost ? per : kHeldMost;
     const int pages = per / p.pages.page + 2;
     p.paged = pages < 4096 ? pages : 4096;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(heads * C));
-    cfg.blockDim = dim3(kEvictThreads);
-    cfg.dynamicSmemBytes = (size_t)(p.held + p.paged) * 4;
-    cfg.stream = st;
-    cudaLaunchAttribute attr = {};
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = (unsigned)C;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, evict_kernel, p);
+    return launch_overlapped(evict_kernel, dim3((unsigned)(heads * C)), kEvictThreads, (size_t)(p.held + p.paged) * 4, (unsigned)C, st, p);
 }
 
 int append_tokens(int D) { return kAppendThreads / (D / 8); }
 
 cudaError_t launch_append(const AppendParams &p, int blocks, cudaStream_t st)
 {
-    append_kernel<<<blocks, kAppendThreads, 0, st>>>(p);
-    return cudaGetLastError();
+    return launch_overlapped(append_kernel, dim3((unsigned)blocks), kAppendThreads, 0, 1, st, p);
 }
 
 } // namespace cache

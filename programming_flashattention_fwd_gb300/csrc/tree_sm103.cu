@@ -166,8 +166,7 @@ __global__ void __launch_bounds__(Cfg<D, PAIR>::THREADS, 1)
     unsigned int *status = &g_tree_status;
     const uint64_t tmo = p.timeout_ns;
 
-    // the joining kernel may be scheduled from here on; it waits for this grid's end before it reads
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    grid_done_soon();
     if (pad + (uint32_t)C::BYTES > dynamic_smem_size_u32()) {
         if (threadIdx.x == 0) atomicOr(status, 1u | (S_SMEM << 8));
         return;
@@ -198,6 +197,7 @@ __global__ void __launch_bounds__(Cfg<D, PAIR>::THREADS, 1)
     } else if (warp == 2) {
         if (lane < 5) tma_prefetch_map(lane == 0 ? &maps.q : lane == 1 ? &maps.k : lane == 2 ? &maps.v : lane == 3 ? &maps.k_new : &maps.v_new);
     } else if (warp == 3) {
+        grid_wait();
         const Share w = find_share(p.s.B, p.least, lane, blockIdx.x, gridDim.x, [&](int b) { return tree_steps(p.s, b); });
         const TreeWalk mine(p.s, w.b, w.off, w.left);
         if (lane == 0) {
@@ -210,6 +210,7 @@ __global__ void __launch_bounds__(Cfg<D, PAIR>::THREADS, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    grid_wait();   // every thread: what it reads and writes from here on may be the kernel's before
     const uint32_t tmem = misc->tmem;
     TreeWalk walk = const_cast<const Misc *>(misc)->share;
     TreeSeg g = {};
@@ -755,7 +756,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
     constexpr int PER = D / 32, FEW = 4;
     __shared__ float sums[kJoinWarps][D];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    grid_wait();
+    grid_done_soon();
     const Cut c = p.cuts[blockIdx.x + 1];
     const int parts = c.parts;
     if (parts == 0) return;
@@ -853,20 +855,9 @@ cudaError_t launch_one(const TreeMaps &m, const TreeParams &p0, cudaStream_t st)
     TreeParams p = p0;
     if (p.timeout_ns == 0) p.timeout_ns = kDefaultTimeoutNs;
     const int grid = clampi(sm_count[dev].load(std::memory_order_relaxed), 1, kMaxCtas);
-    kern<<<grid, C::THREADS, C::ALLOC, st>>>(m, p);
-    e = cudaGetLastError();
+    e = launch_overlapped(kern, dim3(grid), C::THREADS, C::ALLOC, 1, st, m, p);
     if (e != cudaSuccess || grid == 1) return e;
-    // the joining kernel is launched while the first one runs and waits for its end on the device
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid - 1, clampi(p.part_rows, 1, 32));
-    cfg.blockDim = dim3(32 * kJoinWarps);
-    cfg.stream = st;
-    cudaLaunchAttribute attr = {};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, join_kernel<D, BF16>, p);
+    return launch_overlapped(join_kernel<D, BF16>, dim3(grid - 1, clampi(p.part_rows, 1, 32)), 32 * kJoinWarps, 0, 1, st, p);
 }
 
 } // namespace

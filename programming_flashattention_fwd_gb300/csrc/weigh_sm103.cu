@@ -100,7 +100,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint64_t tmo = p.timeout_ns;
     const bool gather = p.s.mode == kPath;
 
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    grid_done_soon();
     if (pad + (uint32_t)C::BYTES > dynamic_smem_size_u32()) {
         if (threadIdx.x == 0) atomicOr(status, 1u | (S_SMEM << 8));
         return;
@@ -132,6 +132,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         tmem_relinquish();
     }
     if (warp == 3) {
+        grid_wait();
         const Share w = find_share(p.s.B, p.least, lane, blockIdx.x, gridDim.x, [&](int b) {
             const WeighLen l = weigh_len(p.s, b);
             return p.s.Hkv * weigh_before(l, l.kt);
@@ -147,6 +148,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    grid_wait();   // every thread: what it reads and writes from here on may be the kernel's before
     const uint32_t tmem = misc->tmem;
     WeighWalk walk = const_cast<const Misc *>(misc)->share;
     WeighSeg g;
@@ -544,7 +546,7 @@ __global__ void __launch_bounds__(Prompt<D>::THREADS, 1)
     unsigned int *status = &g_weigh_status;
     const uint64_t tmo = p.timeout_ns;
 
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    grid_done_soon();
     if (pad + (uint32_t)C::BYTES > dynamic_smem_size_u32()) {
         if (threadIdx.x == 0) atomicOr(status, 1u | (S_SMEM << 8));
         return;
@@ -574,6 +576,7 @@ __global__ void __launch_bounds__(Prompt<D>::THREADS, 1)
         tmem_relinquish();
     }
     if (warp == 3) {
+        grid_wait();
         const Share w = find_share(p.s.B, p.least, lane, blockIdx.x, gridDim.x, [&](int b) {
             const WeighLen l = weigh_len(p.s, b);
             return p.s.Hkv * weigh_before(l, l.kt);
@@ -589,6 +592,7 @@ __global__ void __launch_bounds__(Prompt<D>::THREADS, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    grid_wait();   // every thread: what it reads and writes from here on may be the kernel's before
     const uint32_t tmem = misc->tmem;
     WeighWalk walk = const_cast<const Misc *>(misc)->share;
     WeighSeg g;
@@ -826,7 +830,8 @@ __global__ void __launch_bounds__(Prompt<D>::THREADS, 1)
 __global__ void __launch_bounds__(256) weigh_join_kernel(const __grid_constant__ WeighParams p)
 {
     const int r = threadIdx.x;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    grid_wait();
+    grid_done_soon();
     const Cut c = p.cuts[blockIdx.x + 1];
     const int slot = c.tile * p.s.keys + r;
     if (c.parts == 0 || slot >= c.n) return;
@@ -867,19 +872,9 @@ cudaError_t launch_one(const WeighMaps &m, const WeighParams &p0, cudaStream_t s
     WeighParams p = p0;
     if (p.timeout_ns == 0) p.timeout_ns = kDefaultTimeoutNs;
     const int grid = clampi(sm_count[dev].load(std::memory_order_relaxed), 1, kMaxCtas);
-    kern<<<grid, threads, smem, st>>>(m, p);
-    e = cudaGetLastError();
+    e = launch_overlapped(kern, dim3(grid), threads, smem, 1, st, m, p);
     if (e != cudaSuccess || grid == 1) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid - 1);
-    cfg.blockDim = dim3((unsigned)p.s.keys);
-    cfg.stream = st;
-    cudaLaunchAttribute attr = {};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, weigh_join_kernel, p);
+    return launch_overlapped(weigh_join_kernel, dim3(grid - 1), p.s.keys, 0, 1, st, p);
 }
 
 } // namespace
