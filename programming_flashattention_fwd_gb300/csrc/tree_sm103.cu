@@ -13,11 +13,11 @@
 // them in the order of the keys, the same on every run.
 //
 // Per CTA (one per SM):
-//   warp 0        K / V producer: per step one TMA box per page and 64-column panel (each lane looks
-//                 up the page of its box, a step ahead), into a ring of NS slots
+//   warps 0, 3    K and V producers: per step one TMA box per page and 64-column panel (each lane looks
+//                 up the page of its box, a step ahead), into one ring of NS slots in the order in
+//                 which the products take them (K_0, K_1, V_0, K_2, V_1, ...).  Warp 3 finds the CTA's share first.
 //   warp 1        TMEM owner and MMA issuer: S = Q K^T, O += P V (tcgen05, fp32 in tensor memory)
 //   warp 2        Q producer
-//   warp 3        finds this CTA's share of the work
 //   warps 4-7,    softmax, one thread per row, in two groups (one at D = 256) so that one group's softmax
 //   warps 8-11    runs beside the other's matrix products:
 //     up to 128 rows    the groups take alternate key steps, each with its own running maximum, sum and O;
@@ -221,59 +221,58 @@ __global__ void __launch_bounds__(Cfg<D, PAIR>::THREADS, 1)
         return kt < g.len.kc ? min(BN, g.len.n - kt * BN) : min(BN, g.len.t - (kt - g.len.kc) * BN);
     };
 
-    if (warp == 0) {
-        // ------------------------------------------------------------ K / V producer
-        const Pages pg = p.pages;
+    if (warp == 0 || warp == 3) {
+        // ------------------------------------------------------------ K producer, V producer
+        const bool is_v = warp == 3;
+        const CUtensorMap *pool = is_v ? &maps.v : &maps.k, *fresh = is_v ? &maps.v_new : &maps.k_new;
         const int boxes = BN / p.box_rows;            // boxes of a step (one panel)
         const int box = lane / C::PANELS, pn = lane % C::PANELS;
         const uint32_t box_off = (uint32_t)(pn * C::KVPANEL + box * p.box_rows * 128);
-        Ring<C::NS> ring;
-        int use = 0;
+        int use0 = 0, last = 0;                       // the segment's first place in the ring, this warp's last
+        uint32_t issued = 0;                          // bit i: place last - i is this warp's
         bool ok = true;
         // the page (and the row in it) of this lane's box of step kt
         auto look = [&](int kt, int &pid, int &row) {
             pid = -1;
             row = 0;
             const int slot = kt * BN + box * p.box_rows;
-            if (kt < g.len.kc && box < boxes && slot < g.len.n) page_of(pg, g.b, slot, pid, row);
-        };
-        auto load = [&](bool is_v, int kt, int pid, int row) -> bool {
-            if (!wait_all(bar_empty(ring.at), ring.phase ^ 1, S_EMPTY)) return false;
-            const uint32_t dst = sRing + ring.at * C::KVTILE, bar = bar_full(ring.at);
-            if (kt < g.len.kc) {
-                const int valid = min(boxes, cdiv(g.len.n - kt * BN, p.box_rows));
-                if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(valid * p.box_rows * 128 * C::PANELS));
-                __syncwarp();
-                if (pid >= 0) load_page(dst + box_off, is_v ? &maps.v : &maps.k, pn * 64, row, g.kvh, pid, bar);
-            } else {
-                if (lane == 0) mbar_arrive_expect_tx(bar, C::KVTILE);
-                __syncwarp();
-                if (lane < C::PANELS)
-                    tma_load_3d(dst + lane * C::KVPANEL, is_v ? &maps.v_new : &maps.k_new, lane * 64, (kt - g.len.kc) * BN,
-                                g.b * p.s.Hkv + g.kvh, bar);
-            }
-            ring.next();
-            ++use;
-            return true;
+            if (kt < g.len.kc && box < boxes && slot < g.len.n) page_of(p.pages, g.b, slot, pid, row);
         };
         while (ok && walk.next(p.s, g)) {
-            int pid, row, pid1, row1, pid2, row2;
+            const int nk = g.k1 - g.k0;
+            int pid, row, pid1, row1;
             look(g.k0, pid, row);
-            look(g.k0 + 1, pid1, row1);
-            ok = load(false, g.k0, pid, row);
-            for (int kt = g.k0; ok && kt < g.k1; ++kt) {
-                look(kt + 2, pid2, row2);   // used in the next round
-                if (kt + 1 < g.k1) ok = load(false, kt + 1, pid1, row1);
-                if (ok) ok = load(true, kt, pid, row);
+            for (int j = 0; j < nk; ++j) {
+                const int kt = g.k0 + j;
+                look(kt + 1, pid1, row1);   // used in the next round
+                // K_0, K_1, V_0, K_2, V_1, ..., V_last
+                const int use = use0 + (is_v ? (j + 1 < nk ? 2 * j + 2 : 2 * j + 1) : (j ? 2 * j - 1 : 0));
+                const uint32_t at = (uint32_t)use % C::NS, bar = bar_full(at), dst = sRing + at * C::KVTILE;
+                ok = wait_all(bar_empty(at), (((uint32_t)use / C::NS) & 1) ^ 1, S_EMPTY);
+                if (!ok) break;
+                if (kt < g.len.kc) {
+                    const int valid = min(boxes, cdiv(g.len.n - kt * BN, p.box_rows));
+                    if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(valid * p.box_rows * 128 * C::PANELS));
+                    __syncwarp();
+                    if (pid >= 0) load_page(dst + box_off, pool, pn * 64, row, g.kvh, pid, bar);
+                } else {
+                    if (lane == 0) mbar_arrive_expect_tx(bar, C::KVTILE);
+                    __syncwarp();
+                    if (lane < C::PANELS)
+                        tma_load_3d(dst + lane * C::KVPANEL, fresh, lane * 64, (kt - g.len.kc) * BN, g.b * p.s.Hkv + g.kvh, bar);
+                }
+                issued = (issued << (use - last)) | 1u;
+                last = use;
                 pid = pid1;
                 row = row1;
-                pid1 = pid2;
-                row1 = row2;
             }
+            use0 += 2 * nk;
         }
-        if (lane == 0)
-            for (int x = max(0, use - C::NS); x < use; ++x)
-                bounded_wait(bar_full(x % C::NS), (x / C::NS) & 1, abort_flag, tmo, S_DRAIN, status, false);
+        // after an abort nobody else waits for the loads in flight: they land before the CTA ends
+        if (lane == 0 && *abort_flag)
+            for (int i = 0; i < C::NS; ++i)
+                if ((issued >> i) & 1u)
+                    bounded_wait(bar_full((uint32_t)(last - i) % C::NS), ((uint32_t)(last - i) / C::NS) & 1, abort_flag, tmo, S_DRAIN, status, false);
         __syncwarp();
     } else if (warp == 2) {
         // ------------------------------------------------------------ Q producer
