@@ -87,6 +87,7 @@ def _launch(fn, index: int, stream, args) -> None:
 
 
 _local = threading.local()
+_capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", torch.cuda.is_current_stream_capturing)
 
 
 def _workspace(need: int, given: Optional[torch.Tensor], like: torch.Tensor, stream) -> Tuple[torch.Tensor, int, int]:
@@ -99,14 +100,14 @@ def _workspace(need: int, given: Optional[torch.Tensor], like: torch.Tensor, str
             raise ValueError("workspace must be a contiguous CUDA tensor on the cache's device")
         return given, given.data_ptr(), given.nbytes
     if stream is None and _b._raw_stream is not None and _b._cur_device is not None and _b._cur_device() == index \
-            and not torch.cuda.is_current_stream_capturing():
+            and not _capturing():
         kept, key = _local.__dict__, (index, _b._raw_stream(index))
         ws = kept.get(key)
         if ws is None or ws[2] < need:
-            t = like.new_empty(need, dtype=torch.uint8)
+            t = torch.empty(need, dtype=torch.uint8, device=like.device)
             ws = kept[key] = (t, t.data_ptr(), need)
         return ws
-    t = like.new_empty(need, dtype=torch.uint8)
+    t = torch.empty(need, dtype=torch.uint8, device=like.device)
     if stream is not None:   # not to be reused by the current stream's later work before `stream` is done with it
         t.record_stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device=like.device))
     return t, t.data_ptr(), need
@@ -189,7 +190,7 @@ def tree_attention(q, k_new, v_new, cache: KVCache, parent=None, draft_len=None,
     if o is None:
         o = torch.empty_like(q)
     if lse is None:
-        lse = q.new_empty(rows, dtype=_F32)
+        lse = torch.empty(rows, dtype=_F32, device=q.device)
     lib = _lib or _library()
     args = (cache._c, _need("q", q, shape, dt, i), _need("k_new", k_new, new, dt, i), _need("v_new", v_new, new, dt, i),
             None if parent is None else _need("parent", parent, (B, T), _I32, i),
@@ -245,7 +246,7 @@ def cache_weights(cache: KVCache, q, lse, weight=None, path=None, count=None, ca
         raise ValueError("a path needs count")
     slots = (B, cache.Hkv, cache.capacity)
     if out is None:
-        out = q.new_zeros(slots, dtype=_F32) if weight is None else weight
+        out = torch.zeros(slots, dtype=_F32, device=q.device) if weight is None else weight
     lib = _lib or _library()
     args = (cache._c, _need("q", q, shape, cache.dtype, i), _need("lse", lse, (B, Hq, T), _F32, i),
             None if path is None else _need("path", path, (B, T), _I32, i),
@@ -275,7 +276,7 @@ def cache_evict(cache: KVCache, weight, pos, keep: int, first: int = 0, last: in
     if last and next_pos is None:
         raise ValueError("last needs next_pos")
     if new_len is None:
-        new_len = cache.seq_len.new_empty(B)
+        new_len = torch.empty(B, dtype=_I32, device=cache.device)
     w, p = _need("weight", weight, slots, _F32, i), _need("pos", pos, slots, _I32, i)
     lib = _lib or _library()
     args = (cache._c, w, p, w if weight_out is None else _need("weight_out", weight_out, slots, _F32, i),

@@ -99,15 +99,17 @@ struct Ring {
     }
 };
 
-// Page and row of slot `slot` of sequence b; a page that does not exist is given the number past the
-// last, which a tensor map reads as zeros.
+// Page and row of slot `slot` of sequence b, as the table has it.  (Nothing is done with the number here, so
+// that a look-up made ahead does not wait for it.)
 __device__ __forceinline__ void page_of(const Pages &pg, int b, int slot, int &pid, int &row)
 {
     const int at = slot / pg.page;
     row = slot - at * pg.page;
     pid = pg.table ? __ldg(pg.table + (size_t)b * pg.max_pages + at) : b * pg.max_pages + at;
-    if (pid < 0 || pid >= pg.num_pages) pid = pg.num_pages;
 }
+
+// A page that does not exist is given the number past the last, which a tensor map reads as zeros.
+__device__ __forceinline__ int real_page(const Pages &pg, int pid) { return pid < 0 || pid >= pg.num_pages ? pg.num_pages : pid; }
 
 // One box of a pool, (64 columns from x, box rows from `row`, KV head, page), global -> shared.
 __device__ __forceinline__ void load_page(uint32_t dst, const CUtensorMap *m, int x, int row, int kvh, int pid, uint32_t bar)

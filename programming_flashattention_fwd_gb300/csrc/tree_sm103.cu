@@ -233,14 +233,12 @@ __global__ void __launch_bounds__(Cfg<D, PAIR>::THREADS, 1)
         bool ok = true;
         // the page (and the row in it) of this lane's box of step kt
         auto look = [&](int kt, int &pid, int &row) {
-            pid = -1;
-            row = 0;
             const int slot = kt * BN + box * p.box_rows;
             if (kt < g.len.kc && box < boxes && slot < g.len.n) page_of(p.pages, g.b, slot, pid, row);
         };
         while (ok && walk.next(p.s, g)) {
             const int nk = g.k1 - g.k0;
-            int pid, row, pid1, row1;
+            int pid = 0, row = 0, pid1 = 0, row1 = 0;
             look(g.k0, pid, row);
             for (int j = 0; j < nk; ++j) {
                 const int kt = g.k0 + j;
@@ -254,7 +252,7 @@ __global__ void __launch_bounds__(Cfg<D, PAIR>::THREADS, 1)
                     const int valid = min(boxes, cdiv(g.len.n - kt * BN, p.box_rows));
                     if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(valid * p.box_rows * 128 * C::PANELS));
                     __syncwarp();
-                    if (pid >= 0) load_page(dst + box_off, pool, pn * 64, row, g.kvh, pid, bar);
+                    if (box < valid) load_page(dst + box_off, pool, pn * 64, row, g.kvh, real_page(p.pages, pid), bar);
                 } else {
                     if (lane == 0) mbar_arrive_expect_tx(bar, C::KVTILE);
                     __syncwarp();

@@ -176,23 +176,29 @@ __global__ void __launch_bounds__(THREADS, 1)
         int ku = 0, qu = 0;
         bool ok = true;
         Tile at;
-        while (ok && walk.next(p.s, g)) {
-            int pid = -1, row = 0;
+        // the page of this lane's box is looked up a key tile ahead
+        int pid = -1, row = 0;
+        auto look = [&](const WeighSeg &g) {
+            if (box < boxes && g.kt * 128 + box * p.box_rows < g.len.n) page_of(p.pages, g.b, g.kt * 128 + box * p.box_rows, pid, row);
+        };
+        bool more = walk.next(p.s, g);
+        if (more) look(g);
+        while (ok && more) {
+            WeighSeg ahead = {};
+            const int pid0 = pid, row0 = row;
+            more = walk.next(p.s, ahead);
+            if (more) look(ahead);
             ok = wait_all(k_empty(ku), ((ku / C::KS) & 1) ^ 1, S_KEMPTY);
             if (!ok) break;
-            const int left = g.len.n - g.kt * 128;
-            const int valid = min(boxes, cdiv(left, p.box_rows));
+            const int valid = min(boxes, cdiv(g.len.n - g.kt * 128, p.box_rows));
             const uint32_t dst = sb + (uint32_t)(ku % C::KS) * C::KTILE, bar = k_full(ku);
             if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(valid * p.box_rows * 128 * C::PANELS));
             __syncwarp();
-            if (box < valid) {   // at most 8 boxes x PANELS: one for each lane at D = 256
-                page_of(p.pages, g.b, g.kt * 128 + box * p.box_rows, pid, row);
-                load_page(dst + box_off, &maps.k, pn * 64, row, g.kvh, pid, bar);
-            }
+            // at most 8 boxes x PANELS: one for each lane at D = 256
+            if (box < valid) load_page(dst + box_off, &maps.k, pn * 64, row0, g.kvh, real_page(p.pages, pid0), bar);
             ++ku;
-            if (gather) continue;
             WeighTiles t(g);
-            for (int s = g.s0; ok && s < g.s1; ++s, t.next()) {
+            for (int s = g.s0; !gather && ok && s < g.s1; ++s, t.next()) {
                 if (!at.change(g.b, g.kvh, t.plane, t.qt)) continue;
                 ok = wait_all(q_empty(qu), ((qu / C::QS) & 1) ^ 1, S_QEMPTY);
                 if (!ok) break;
@@ -205,6 +211,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
                 ++qu;
             }
+            g = ahead;
         }
         if (lane == 0) {
             for (int x = max(0, ku - C::KS); x < ku; ++x) bounded_wait(k_full(x), (x / C::KS) & 1, abort_flag, tmo, S_DRAIN, status, false);
@@ -614,7 +621,7 @@ __global__ void __launch_bounds__(Prompt<D>::THREADS, 1)
                 const int box = i / C::PANELS, pn = i % C::PANELS;
                 int pid, row;
                 page_of(p.pages, g.b, g.kt * 256 + box * p.box_rows, pid, row);
-                load_page(sb + (uint32_t)(pn * C::KPANEL + box * p.box_rows * 128), &maps.k, pn * 64, row, g.kvh, pid, barK);
+                load_page(sb + (uint32_t)(pn * C::KPANEL + box * p.box_rows * 128), &maps.k, pn * 64, row, g.kvh, real_page(p.pages, pid), barK);
             }
             WeighTiles t(g);
             for (int s = g.s0; s < g.s1; ++s, t.next(), ++qu) {
