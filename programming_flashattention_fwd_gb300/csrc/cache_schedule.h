@@ -227,6 +227,13 @@ struct WeighTiles {
     }
 };
 
+// One CTA's share of one head where all key tiles have the same steps (kRows, kPath): `steps` of them, from
+// step s of key tile kt, ns to a key tile.
+struct WeighRun {
+    int b, kvh, kt, s, steps, ns;
+    WeighLen len;
+};
+
 // Walks a CTA's steps: `left` of them from step `s` of key tile kt.  The lengths are looked up and
 // the first key tile is searched for once a sequence, not once a key tile: a drafting step has one
 // step a key tile.
@@ -255,7 +262,8 @@ struct WeighWalk {
         s = in - weigh_before(len, kt);
     }
 
-    __host__ __device__ __forceinline__ bool next(const WeighShape &sh, WeighSeg &g)
+    // to the next head that has key tiles, behind the last one of a head
+    __host__ __device__ __forceinline__ bool settle(const WeighShape &sh)
     {
         if (left <= 0) return false;
         if (kt == len.kt) {
@@ -268,6 +276,31 @@ struct WeighWalk {
                 } while (len.kt == 0);
             }
         }
+        return true;
+    }
+
+    // a head at a time (kRows, kPath): a drafting step has one step a key tile, and what is done for each
+    // key tile is what bounds it
+    __host__ __device__ __forceinline__ bool next_run(const WeighShape &sh, WeighRun &r)
+    {
+        if (!settle(sh)) return false;
+        r.b = b;
+        r.kvh = kvh;
+        r.kt = kt;
+        r.s = s;
+        r.len = len;
+        r.ns = len.qt > 0 ? len.qt : 1;
+        const int all = (len.kt - kt) * r.ns - s;
+        r.steps = all < left ? all : left;
+        left -= r.steps;
+        kt = len.kt;
+        s = 0;
+        return true;
+    }
+
+    __host__ __device__ __forceinline__ bool next(const WeighShape &sh, WeighSeg &g)
+    {
+        if (!settle(sh)) return false;
         g.b = b;
         g.kvh = kvh;
         g.kt = kt;

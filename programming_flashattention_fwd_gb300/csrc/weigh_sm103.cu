@@ -85,11 +85,11 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t sb = raw + pad;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t sQ = sb + C::OFF_Q, bar0 = sb + C::OFF_BAR;
-    auto k_full = [&](int u) { return bar0 + 8u * (u % C::KS); };
-    auto k_empty = [&](int u) { return bar0 + 8u * (C::KS + u % C::KS); };
+    auto k_full = [&](uint32_t i) { return bar0 + 8u * i; };
+    auto k_empty = [&](uint32_t i) { return bar0 + 8u * (C::KS + i); };
     const uint32_t barQ0 = bar0 + 16u * C::KS;
-    auto q_full = [&](int u) { return barQ0 + 8u * (u % C::QS); };
-    auto q_empty = [&](int u) { return barQ0 + 8u * (C::QS + u % C::QS); };
+    auto q_full = [&](uint32_t i) { return barQ0 + 8u * i; };
+    auto q_empty = [&](uint32_t i) { return barQ0 + 8u * (C::QS + i); };
     const uint32_t barS = barQ0 + 16u * C::QS, barRows = barS + 8u * NB, barFree = barRows + 8u * NB, barJoin = barFree + 8u * NB,
                    barRead = barJoin + 8u * NB, barDone = barRead + 8u * NB;
     float *rows_lse = reinterpret_cast<float *>(smem + C::OFF_ROWS);
@@ -151,22 +151,10 @@ __global__ void __launch_bounds__(THREADS, 1)
     grid_wait();   // every thread: what it reads and writes from here on may be the kernel's before
     const uint32_t tmem = misc->tmem;
     WeighWalk walk = const_cast<const Misc *>(misc)->share;
-    WeighSeg g;
-
+    WeighRun g;
     const WarpWait wait_all{abort_flag, tmo, status};
-    // Q tiles are told apart by (sequence, KV head, plane, tile); consecutive steps with the same one share it
-    struct Tile {
-        int b = -1, kvh = 0, plane = 0, qt = 0;
-        __device__ bool change(int b1, int kvh1, int plane1, int qt1)
-        {
-            const bool same = b == b1 && kvh == kvh1 && plane == plane1 && qt == qt1;
-            b = b1;
-            kvh = kvh1;
-            plane = plane1;
-            qt = qt1;
-            return !same;
-        }
-    };
+    // A Q tile is taken anew with every head, and with every step where a key tile has several: then the
+    // tiles 0 .. ns - 1 follow one another again and again.
 
     if (warp == 0) {
         // ------------------------------------------------------------ K producer, Q producer
@@ -174,89 +162,96 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int box = lane / C::PANELS, pn = lane % C::PANELS;
         const uint32_t box_off = (uint32_t)(pn * C::KPANEL + box * p.box_rows * 128);
         int ku = 0, qu = 0;
+        Ring<C::KS> k;
+        Ring<C::QS> q;
         bool ok = true;
-        Tile at;
-        // the page of this lane's box is looked up a key tile ahead
-        int pid = -1, row = 0;
-        auto look = [&](const WeighSeg &g) {
-            if (box < boxes && g.kt * 128 + box * p.box_rows < g.len.n) page_of(p.pages, g.b, g.kt * 128 + box * p.box_rows, pid, row);
-        };
-        bool more = walk.next(p.s, g);
-        if (more) look(g);
-        while (ok && more) {
-            WeighSeg ahead = {};
-            const int pid0 = pid, row0 = row;
-            more = walk.next(p.s, ahead);
-            if (more) look(ahead);
-            ok = wait_all(k_empty(ku), ((ku / C::KS) & 1) ^ 1, S_KEMPTY);
-            if (!ok) break;
-            const int valid = min(boxes, cdiv(g.len.n - g.kt * 128, p.box_rows));
-            const uint32_t dst = sb + (uint32_t)(ku % C::KS) * C::KTILE, bar = k_full(ku);
-            if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(valid * p.box_rows * 128 * C::PANELS));
-            __syncwarp();
-            // at most 8 boxes x PANELS: one for each lane at D = 256
-            if (box < valid) load_page(dst + box_off, &maps.k, pn * 64, row0, g.kvh, real_page(p.pages, pid0), bar);
-            ++ku;
-            WeighTiles t(g);
-            for (int s = g.s0; !gather && ok && s < g.s1; ++s, t.next()) {
-                if (!at.change(g.b, g.kvh, t.plane, t.qt)) continue;
-                ok = wait_all(q_empty(qu), ((qu / C::QS) & 1) ^ 1, S_QEMPTY);
+        while (ok && walk.next_run(p.s, g)) {
+            const int units = (g.s + g.steps + g.ns - 1) / g.ns;
+            int pid = 0, row = 0, pid1 = 0, row1 = 0;
+            auto look = [&](int kt, int &pid, int &row) {
+                if (box < boxes && kt * 128 + box * p.box_rows < g.len.n) page_of(p.pages, g.b, kt * 128 + box * p.box_rows, pid, row);
+            };
+            look(g.kt, pid, row);
+            int step = 0;      // steps whose Q tile has been loaded
+            for (int u = 0; ok && u < units; ++u, ++ku, k.next()) {
+                const int kt = g.kt + u;
+                look(kt + 1, pid1, row1);   // used in the next round
+                ok = wait_all(k_empty(k.at), k.phase ^ 1, S_KEMPTY);
                 if (!ok) break;
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(q_full(qu), C::QTILE);
+                const int valid = min(boxes, cdiv(g.len.n - kt * 128, p.box_rows));
+                if (lane == 0) mbar_arrive_expect_tx(k_full(k.at), (uint32_t)(valid * p.box_rows * 128 * C::PANELS));
+                __syncwarp();
+                // at most 8 boxes x PANELS: one for each lane at D = 256
+                if (box < valid) load_page(sb + k.at * C::KTILE + box_off, &maps.k, pn * 64, row, g.kvh, real_page(p.pages, pid), k_full(k.at));
+                pid = pid1;
+                row = row1;
+                if (gather) continue;
+                const int last = min(g.steps, (u + 1) * g.ns - g.s);   // steps up to the end of this key tile
+                for (; ok && step < last; ++step) {
+                    if (g.ns == 1 && step > 0) continue;
+                    ok = wait_all(q_empty(q.at), q.phase ^ 1, S_QEMPTY);
+                    if (!ok) break;
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(q_full(q.at), C::QTILE);
 #pragma unroll
-                    for (int pq = 0; pq < C::PANELS; ++pq)
-                        tma_load_3d(sQ + (uint32_t)(qu % C::QS) * C::QTILE + pq * C::QPANEL, &maps.q, pq * 64, t.qt * NQ,
-                                    (g.b * p.s.Hkv + g.kvh) * g.len.planes + t.plane, q_full(qu));
+                        for (int pq = 0; pq < C::PANELS; ++pq)
+                            tma_load_3d(sQ + q.at * C::QTILE + pq * C::QPANEL, &maps.q, pq * 64, (g.s + step) % g.ns * NQ, g.b * p.s.Hkv + g.kvh,
+                                        q_full(q.at));
+                    }
+                    ++qu;
+                    q.next();
                 }
-                ++qu;
             }
-            g = ahead;
         }
         if (lane == 0) {
-            for (int x = max(0, ku - C::KS); x < ku; ++x) bounded_wait(k_full(x), (x / C::KS) & 1, abort_flag, tmo, S_DRAIN, status, false);
-            for (int x = max(0, qu - C::QS); x < qu; ++x) bounded_wait(q_full(x), (x / C::QS) & 1, abort_flag, tmo, S_DRAIN, status, false);
+            for (int x = max(0, ku - C::KS); x < ku; ++x) bounded_wait(k_full(x % C::KS), (x / C::KS) & 1, abort_flag, tmo, S_DRAIN, status, false);
+            for (int x = max(0, qu - C::QS); x < qu; ++x) bounded_wait(q_full(x % C::QS), (x / C::QS) & 1, abort_flag, tmo, S_DRAIN, status, false);
         }
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer (whole warp)
         constexpr uint32_t HI = sdesc_hi_sw128(1024);
-        int ku = 0, qu = 0;      // tiles taken so far
-        uint32_t st = 0;         // step: buffer st % NB
-        bool ok = true, held = false;   // held: the Q tile is to be released when the next one is taken
-        Tile at;
-        while (ok && walk.next(p.s, g)) {
-            if (ku) tc_commit_elect(k_empty(ku - 1));   // the last key tile's products are all issued
-            ok = wait_all(k_full(ku), (ku / C::KS) & 1, S_KFULL);
-            if (!ok) break;
-            const uint32_t sK = sb + (uint32_t)(ku % C::KS) * C::KTILE;
-            ++ku;
-            WeighTiles t(g);
-            for (int s = g.s0; s < g.s1; ++s, ++st, t.next()) {
-                if (at.change(g.b, g.kvh, t.plane, t.qt)) {
-                    if (held) tc_commit_elect(q_empty(qu - 1));
-                    ok = wait_all(q_full(qu), (qu / C::QS) & 1, S_QFULL);
+        Ring<C::KS> k;                       // the next K tile, the next Q tile
+        Ring<C::QS> q;
+        Ring<NB> st;                         // the step's buffer
+        uint32_t k_old = 0, q_old = 0;       // tiles in use, and whether there are any to give back
+        bool k_held = false, q_held = false, ok = true;
+        while (ok && walk.next_run(p.s, g)) {
+            int s = g.s;                     // step of the key tile
+            for (int i = 0; i < g.steps; ++i, st.next()) {
+                if (i == 0 || s == 0) {
+                    if (k_held) tc_commit_elect(k_empty(k_old));   // the last key tile's products are all issued
+                    ok = wait_all(k_full(k.at), k.phase, S_KFULL);
                     if (!ok) break;
-                    ++qu;
-                    held = true;
+                    k_old = k.at;
+                    k_held = true;
+                    k.next();
                 }
-                const uint32_t bi = st % NB;
-                ok = wait_all(barFree + 8u * bi, ((st / NB) & 1) ^ 1, S_FREE);
+                if (i == 0 || g.ns > 1) {
+                    if (q_held) tc_commit_elect(q_empty(q_old));
+                    ok = wait_all(q_full(q.at), q.phase, S_QFULL);
+                    if (!ok) break;
+                    q_old = q.at;
+                    q_held = true;
+                    q.next();
+                }
+                ok = wait_all(barFree + 8u * st.at, st.phase ^ 1, S_FREE);
                 if (!ok) break;
                 tc_fence_after();
                 // columns: the rows of this tile, to the next multiple of 16
-                const int cols = max(16, min(NQ, (g.len.rows - t.qt * NQ + 15) & ~15));
+                const int cols = max(16, min(NQ, (g.len.rows - s * NQ + 15) & ~15));
                 const uint32_t id = idesc_f16(BF16, 128, 16, false) + ((uint32_t)(cols - 16) >> 3 << 17);
-                const uint32_t sq = sQ + (uint32_t)((qu - 1) % C::QS) * C::QTILE;
+                const uint32_t sK = sb + k_old * C::KTILE, sq = sQ + q_old * C::QTILE;
 #pragma unroll
                 for (int pn = 0; pn < C::PANELS; ++pn)
-                    mma_ss_kk4_elect(tmem + bi * 128u, sdesc_lo(sK + pn * C::KPANEL, 16), sdesc_lo(sq + pn * C::QPANEL, 16), HI, id,
+                    mma_ss_kk4_elect(tmem + st.at * 128u, sdesc_lo(sK + pn * C::KPANEL, 16), sdesc_lo(sq + pn * C::QPANEL, 16), HI, id,
                                      pn ? 1u : 0u);
-                tc_commit_elect(barS + 8u * bi);
-                if (s + 1 < g.s1) {   // the next step of a key tile always has another Q tile
-                    tc_commit_elect(q_empty(qu - 1));
-                    held = false;
+                tc_commit_elect(barS + 8u * st.at);
+                if (g.ns > 1) {   // the next step has another Q tile
+                    tc_commit_elect(q_empty(q_old));
+                    q_held = false;
                 }
+                if (++s == g.ns) s = 0;
             }
         }
         tc_commit_elect(barDone);
@@ -267,83 +262,77 @@ __global__ void __launch_bounds__(THREADS, 1)
         // The two warps take alternate steps, a lane four neighbouring rows; what a tile's rows need is
         // looked up once while consecutive steps use it.
         const int half = warp - 2;
-        int qu = 0;
-        uint32_t st = 0;
-        bool ok = true, fresh = true;
-        Tile at;
-        float neg[4] = {0.f, 0.f, 0.f, 0.f};      // -lse, log2 units
-        int limit[4] = {0, 0, 0, 0}, low = 0, cols = 0;
-        while (ok && walk.next(p.s, g)) {
+        Ring<C::QS> q;
+        Ring<NB> st;
+        bool ok = true;
+        while (ok && walk.next_run(p.s, g)) {
             const size_t head0 = (size_t)(g.b * p.s.Hkv + g.kvh) * p.s.group;   // first query head of the group
-            WeighTiles t(g);
-            for (int s = g.s0; s < g.s1; ++s, ++st, t.next()) {
-                const bool changed = at.change(g.b, g.kvh, t.plane, t.qt);
-                fresh |= changed;
-                if (changed && gather) {
-                    ok = wait_all(q_empty(qu), ((qu / C::QS) & 1) ^ 1, S_QEMPTY);
+            const int32_t *path = p.path + (gather ? (size_t)g.b * p.s.T : 0);
+            float neg[4] = {0.f, 0.f, 0.f, 0.f};      // -lse, log2 units
+            int limit[4] = {0, 0, 0, 0}, low = 0, cols = 0;
+            bool fresh = true;
+            int s = g.s;
+            for (int i = 0; i < g.steps; ++i, st.next(), s = s + 1 == g.ns ? 0 : s + 1) {
+                const int row0 = s * NQ;
+                if (gather && (i == 0 || g.ns > 1)) {
+                    ok = wait_all(q_empty(q.at), q.phase ^ 1, S_QEMPTY);
                     if (!ok) break;
-                    const uint32_t dst = sQ + (uint32_t)(qu % C::QS) * C::QTILE;
+                    const uint32_t dst = sQ + q.at * C::QTILE;
                     // rows to the next multiple of 16; 16-byte chunk c of row r at c ^ (r & 7) of its 128 bytes
-                    const int rows = min(NQ, max(16, (g.len.rows - t.qt * NQ + 15) & ~15));
+                    const int rows = min(NQ, max(16, (g.len.rows - row0 + 15) & ~15));
                     for (int x = threadIdx.x - 64; x < rows * (D / 8); x += 64) {
-                        const int r = x / (D / 8), ch = x % (D / 8), row = t.qt * NQ + r;
+                        const int r = x / (D / 8), ch = x % (D / 8), row = row0 + r;
                         uint4 v = make_uint4(0, 0, 0, 0);
                         if (row < g.len.rows) {
-                            const int h = row / g.len.a, i = __ldg(p.path + (size_t)g.b * p.s.T + (row - h * g.len.a));
-                            if (i >= 0 && i < p.s.T)
-                                v = __ldg(reinterpret_cast<const uint4 *>(p.q) + ((head0 + h) * p.s.T + i) * (D / 8) + ch);
+                            const int h = row / g.len.a, t = __ldg(path + (row - h * g.len.a));
+                            if (t >= 0 && t < p.s.T)
+                                v = __ldg(reinterpret_cast<const uint4 *>(p.q) + ((head0 + h) * p.s.T + t) * (D / 8) + ch);
                         }
                         st_shared_v4(dst + (ch >> 3) * C::QPANEL + r * 128 + (((ch & 7) ^ (r & 7)) << 4), v.x, v.y, v.z, v.w);
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(q_full(qu));
-                    ++qu;
+                    if (lane == 0) mbar_arrive(q_full(q.at));
+                    q.next();
                 }
-                if ((int)(st & 1) != half) continue;
-                if (fresh) {
+                if ((int)(st.at & 1) != half) continue;
+                if (fresh || g.ns > 1) {
                     fresh = false;
                     low = 0x7fffffff;
-                    cols = min(NQ, g.len.rows - t.qt * NQ);
+                    cols = min(NQ, g.len.rows - row0);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const int c = 4 * lane + e, row = t.qt * NQ + c;
-                        int i = -1, h = t.plane, x = 0;      // order of the row, its head in the group, its place in q
+                        const int c = 4 * lane + e, row = row0 + c;
+                        int order = -1, h = 0, t = 0;      // order of the row, its head in the group, its place in q
                         if (c < cols) {
-                            if (p.s.mode == kRows) {
-                                h = row / p.s.T;
-                                i = x = row - h * p.s.T;
-                                if (i >= g.len.a) i = -1;
-                            } else {
-                                h = row / g.len.a;
-                                i = row - h * g.len.a;
-                                x = __ldg(p.path + (size_t)g.b * p.s.T + i);
-                                if (x < 0 || x >= p.s.T) i = -1;
-                            }
+                            const int len = gather ? g.len.a : p.s.T;
+                            h = row / len;
+                            order = t = row - h * len;
+                            if (gather) t = __ldg(path + order);
+                            if (order >= g.len.a || t < 0 || t >= p.s.T) order = -1;
                         }
                         limit[e] = 0;
                         neg[e] = 0.f;
-                        if (i >= 0) {
-                            const float v = __ldg(p.lse + (head0 + h) * p.s.T + x);
+                        if (order >= 0) {
+                            const float v = __ldg(p.lse + (head0 + h) * p.s.T + t);
                             neg[e] = v * -1.4426950408889634f;
                             // a row that saw nothing gave nothing
-                            limit[e] = v == -INFINITY ? 0 : (p.s.causal ? clampi(g.len.off + i + 1, 0, g.len.n) : g.len.n);
+                            limit[e] = v == -INFINITY ? 0 : (p.s.causal ? clampi(g.len.off + order + 1, 0, g.len.n) : g.len.n);
                         }
                         if (c < NQ) low = min(low, limit[e]);
                     }
                     low = __reduce_min_sync(~0u, low);
                 }
-                const uint32_t bi = st % NB;
-                ok = wait_all(barFree + 8u * bi, ((st / NB) & 1) ^ 1, S_FREE);
+                ok = wait_all(barFree + 8u * st.at, st.phase ^ 1, S_FREE);
                 if (!ok) break;
-                reinterpret_cast<float4 *>(rows_lse + bi * 256)[lane] = make_float4(neg[0], neg[1], neg[2], neg[3]);
-                reinterpret_cast<int4 *>(rows_lse + bi * 256 + 128)[lane] = make_int4(limit[0], limit[1], limit[2], limit[3]);
+                reinterpret_cast<float4 *>(rows_lse + st.at * 256)[lane] = make_float4(neg[0], neg[1], neg[2], neg[3]);
+                reinterpret_cast<int4 *>(rows_lse + st.at * 256 + 128)[lane] = make_int4(limit[0], limit[1], limit[2], limit[3]);
                 if (lane == 0) {
-                    misc->lowest[bi] = low;
-                    misc->cols[bi] = cols;
+                    misc->lowest[st.at] = low;
+                    misc->cols[st.at] = cols;
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(barRows + 8u * bi);
+                if (lane == 0) mbar_arrive(barRows + 8u * st.at);
             }
         }
     } else {
@@ -351,97 +340,119 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int grp = (warp - 4) >> 2, r = (threadIdx.x - 128) & 127;
         const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
         const uint64_t sl2x2 = f2_pack(p.sl2, p.sl2);
-        uint32_t st0 = 0;
+        uint32_t st0 = 0;     // steps before
         uint32_t posts = 0;   // parity of the sums that each group has handed over (bit), that it has any (bit + NB)
         bool ok = true;
-        while (ok && walk.next(p.s, g)) {
-            const int slot = g.kt * 128 + r, ns = g.s1 - g.s0;
-            const size_t at = (size_t)(g.b * p.s.Hkv + g.kvh) * p.s.capacity + slot;
-            const bool whole = g.s0 == 0 && g.s1 == g.ns, live = slot < g.len.n;
-            const int owner = (int)((st0 + ns - 1) % NB);    // the group of the last step
-            float base = 0.f, sum = 0.f;
-            if (grp == owner && whole && live && p.weight) base = p.weight[at];
-            for (int s = (int)(((uint32_t)grp - st0) % NB); s < ns; s += NB) {
-                const uint32_t st = st0 + s, bi = grp, ph = (st / NB) & 1;
-                ok = wait_all(barRows + 8u * bi, ph, S_ROWS) && wait_all(barS + 8u * bi, ph, S_S);
-                if (!ok) break;
-                tc_fence_after();
-                const float *neg = rows_lse + bi * 256;
-                const int *limit = reinterpret_cast<const int *>(neg) + 128;
-                const uint32_t tS = tmem + lane_off + bi * 128u;
-                const int cols = misc->cols[bi];
-                uint64_t sum2[4];
+        // what this key receives in step `st` (this group's: buffer grp)
+        auto receive = [&](uint32_t st, int key0, float &sum) -> bool {
+            const uint32_t bi = grp, ph = (st / NB) & 1;
+            const int slot = key0 + r;
+            if (!wait_all(barRows + 8u * bi, ph, S_ROWS) || !wait_all(barS + 8u * bi, ph, S_S)) return false;
+            tc_fence_after();
+            const float *neg = rows_lse + bi * 256;
+            const int *limit = reinterpret_cast<const int *>(neg) + 128;
+            const uint32_t tS = tmem + lane_off + bi * 128u;
+            const int cols = misc->cols[bi];
+            uint64_t sum2[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) sum2[i] = f2_pack(0.f, 0.f);
-                // 32 columns: exp2(s sl2 - lse2), two columns to an instruction but for the exponential
-                auto add = [&](const uint32_t(&sv)[32], int c, bool masked) {
+            for (int i = 0; i < 4; ++i) sum2[i] = f2_pack(0.f, 0.f);
+            // 32 columns: exp2(s sl2 - lse2), two columns to an instruction but for the exponential
+            auto add = [&](const uint32_t(&sv)[32], int c, bool masked) {
 #pragma unroll
-                    for (int e = 0; e < 32; e += 4) {
-                        const ulonglong2 l = *reinterpret_cast<const ulonglong2 *>(neg + c + e);
-                        float x[4];
-                        f2_unpack(f2_fma(f2_pack(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1])), sl2x2, l.x), x[0], x[1]);
-                        f2_unpack(f2_fma(f2_pack(__uint_as_float(sv[e + 2]), __uint_as_float(sv[e + 3])), sl2x2, l.y), x[2], x[3]);
+                for (int e = 0; e < 32; e += 4) {
+                    const ulonglong2 l = *reinterpret_cast<const ulonglong2 *>(neg + c + e);
+                    float x[4];
+                    f2_unpack(f2_fma(f2_pack(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1])), sl2x2, l.x), x[0], x[1]);
+                    f2_unpack(f2_fma(f2_pack(__uint_as_float(sv[e + 2]), __uint_as_float(sv[e + 3])), sl2x2, l.y), x[2], x[3]);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) x[i] = ex2_approx(x[i]);
-                        if (masked) {
-                            const int4 m = *reinterpret_cast<const int4 *>(limit + c + e);
-                            x[0] = slot < m.x ? x[0] : 0.f;
-                            x[1] = slot < m.y ? x[1] : 0.f;
-                            x[2] = slot < m.z ? x[2] : 0.f;
-                            x[3] = slot < m.w ? x[3] : 0.f;
-                        }
-                        sum2[(e >> 1) & 3] = f2_add(sum2[(e >> 1) & 3], f2_pack(x[0], x[1]));
-                        sum2[((e >> 1) + 1) & 3] = f2_add(sum2[((e >> 1) + 1) & 3], f2_pack(x[2], x[3]));
+                    for (int i = 0; i < 4; ++i) x[i] = ex2_approx(x[i]);
+                    if (masked) {
+                        const int4 m = *reinterpret_cast<const int4 *>(limit + c + e);
+                        x[0] = slot < m.x ? x[0] : 0.f;
+                        x[1] = slot < m.y ? x[1] : 0.f;
+                        x[2] = slot < m.z ? x[2] : 0.f;
+                        x[3] = slot < m.w ? x[3] : 0.f;
                     }
-                };
-                const bool masked = misc->lowest[bi] < g.kt * 128 + 128;   // some row does not see the whole key tile
+                    sum2[(e >> 1) & 3] = f2_add(sum2[(e >> 1) & 3], f2_pack(x[0], x[1]));
+                    sum2[((e >> 1) + 1) & 3] = f2_add(sum2[((e >> 1) + 1) & 3], f2_pack(x[2], x[3]));
+                }
+            };
+            const bool masked = misc->lowest[bi] < key0 + 128;   // some row does not see the whole key tile
 #pragma unroll 1
-                for (int c = 0; c < cols; c += 32) {
-                    uint32_t sv[32];
-                    tmem_ld_x32(tS + c, sv);
-                    tmem_wait_ld();
-                    reg_fence_x32(sv);
-                    if (masked)
-                        add(sv, c, true);
-                    else
-                        add(sv, c, false);
-                }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(barFree + 8u * bi);
-                float la, lb;
-                f2_unpack(f2_add(f2_add(sum2[0], sum2[1]), f2_add(sum2[2], sum2[3])), la, lb);
-                sum += la + lb;
-            }
-            if (!ok) break;
-            // the other groups of the segment hand their sums to the owner of its last step, which adds
-            // them in the order of their steps
-            for (int x = ns < NB ? ns - 1 : NB - 1; ok && x > 0; --x) {
-                const int other = (owner - x + NB) % NB;
-                const uint32_t par = (posts >> other) & 1u, any = (posts >> (NB + other)) & 1u;
-                posts = (posts ^ (1u << other)) | (1u << (NB + other));
-                if (grp == other) {
-                    if (any) ok = wait_all(barRead + 8u * other, par ^ 1u, S_READ);
-                    if (!ok) break;
-                    join[other * 128 + r] = sum;
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(barJoin + 8u * other);
-                } else if (grp == owner) {
-                    ok = wait_all(barJoin + 8u * other, par, S_JOIN);
-                    if (!ok) break;
-                    sum += join[other * 128 + r];
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(barRead + 8u * other);
-                }
-            }
-            if (!ok) break;
-            if (grp == owner && live) {
-                if (whole)
-                    p.out[at] = base + sum;
+            for (int c = 0; c < cols; c += 32) {
+                uint32_t sv[32];
+                tmem_ld_x32(tS + c, sv);
+                tmem_wait_ld();
+                reg_fence_x32(sv);
+                if (masked)
+                    add(sv, c, true);
                 else
-                    p.part[(size_t)part_slot(blockIdx.x, g.s0) * 256 + r] = sum;
+                    add(sv, c, false);
             }
-            st0 += ns;
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(barFree + 8u * bi);
+            float la, lb;
+            f2_unpack(f2_add(f2_add(sum2[0], sum2[1]), f2_add(sum2[2], sum2[3])), la, lb);
+            sum += la + lb;
+            return true;
+        };
+        while (ok && walk.next_run(p.s, g)) {
+            const size_t head = (size_t)(g.b * p.s.Hkv + g.kvh) * p.s.capacity;
+            if (g.ns == 1) {
+                // a step is a key tile, and no other group has a part in it
+                for (int i = (int)(((uint32_t)grp - st0) % NB); i < g.steps; i += NB) {
+                    const int key0 = (g.kt + i) * 128, slot = key0 + r;
+                    const bool live = slot < g.len.n;
+                    float sum = 0.f;
+                    const float base = live && p.weight ? p.weight[head + slot] : 0.f;
+                    ok = receive(st0 + i, key0, sum);
+                    if (!ok) break;
+                    if (live) p.out[head + slot] = base + sum;
+                }
+                st0 += g.steps;
+                continue;
+            }
+            int done = 0;
+            for (int kt = g.kt, s0 = g.s; ok && done < g.steps; ++kt, s0 = 0) {
+                const int ns = min(g.steps - done, g.ns - s0);           // this CTA's steps of the key tile
+                const int key0 = kt * 128, slot = key0 + r;
+                const bool whole = ns == g.ns, live = slot < g.len.n;
+                const int owner = (int)((st0 + ns - 1) % NB);            // the group of the last step
+                float base = 0.f, sum = 0.f;
+                if (grp == owner && whole && live && p.weight) base = p.weight[head + slot];
+                for (int i = (int)(((uint32_t)grp - st0) % NB); ok && i < ns; i += NB) ok = receive(st0 + i, key0, sum);
+                if (!ok) break;
+                // the other groups of the key tile hand their sums to the owner of its last step, which adds
+                // them in the order of their steps
+                for (int x = ns < NB ? ns - 1 : NB - 1; ok && x > 0; --x) {
+                    const int other = (owner - x + NB) % NB;
+                    const uint32_t par = (posts >> other) & 1u, any = (posts >> (NB + other)) & 1u;
+                    posts = (posts ^ (1u << other)) | (1u << (NB + other));
+                    if (grp == other) {
+                        if (any) ok = wait_all(barRead + 8u * other, par ^ 1u, S_READ);
+                        if (!ok) break;
+                        join[other * 128 + r] = sum;
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(barJoin + 8u * other);
+                    } else if (grp == owner) {
+                        ok = wait_all(barJoin + 8u * other, par, S_JOIN);
+                        if (!ok) break;
+                        sum += join[other * 128 + r];
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(barRead + 8u * other);
+                    }
+                }
+                if (!ok) break;
+                if (grp == owner && live) {
+                    if (whole)
+                        p.out[head + slot] = base + sum;
+                    else
+                        p.part[(size_t)part_slot(blockIdx.x, s0) * 256 + r] = sum;
+                }
+                st0 += ns;
+                done += ns;
+            }
         }
     }
 
@@ -455,6 +466,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         // This CTA gave up on a wait: NaN into every sum it was given
         const int r = threadIdx.x - 128;
         walk = const_cast<const Misc *>(misc)->share;
+        WeighSeg g;
         while (walk.next(p.s, g)) {
             if (g.kt * 128 + r >= g.len.n) continue;
             if (g.s0 == 0 && g.s1 == g.ns)

@@ -172,6 +172,22 @@ static int check_weigh()
                     tiles[id].insert({plane, qt});
                 }
             }
+            if (s.mode == kHeads) continue;
+            // the same share a head at a time
+            WeighWalk v(s, b, begin - base[b], cut(total, G, c + 1) - begin), u(s, b, begin - base[b], cut(total, G, c + 1) - begin);
+            WeighRun r;
+            while (v.next_run(s, r)) {
+                if (r.steps < 1 || r.len.planes != 1) return fail("a run");
+                for (int i = 0, kt = r.kt, at = r.s; i < r.steps;) {
+                    if (!u.next(s, g) || g.b != r.b || g.kvh != r.kvh || g.kt != kt || g.s0 != at || g.ns != r.ns || g.first != 0)
+                        return fail("a run and its segments");
+                    i += g.s1 - g.s0;
+                    at = 0;
+                    ++kt;
+                    if (i > r.steps) return fail("a run's end");
+                }
+            }
+            if (u.next(s, g)) return fail("a segment without a run");
         }
         // every row that sees a slot of a key tile lies in one of the unit's query tiles
         for (int b = 0; b < s.B; ++b) {
