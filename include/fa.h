@@ -120,8 +120,8 @@ const char *fa_strerror(int status);
  * that long.  The attention kernels then leave the call's outputs visibly invalid: every
  * query row of every CTA that gave up holds NaN in o and in lse (rows of other CTAs hold
  * their results), so a caller that does not poll this word still sees NaN, never a stale or
- * partial value that looks like a result.  (fa_gemm and fa_softmax_rows outputs of such a
- * call are unspecified.)
+ * partial value that looks like a result; fa_cache_weights does the same with its sums.  (fa_gemm
+ * and fa_softmax_rows outputs of such a call are unspecified.)
  * *detail (if non-NULL) receives the raw word: bit 0 = timeout, bits 8..15 = the wait
  * site that expired first.
  */
@@ -329,6 +329,7 @@ int fa_cache_append(const fa_cache_t *cache, const void *k_new, const void *v_ne
  *   scale    > 0 and finite;  T >= 1
  *   workspace  fa_weights_workspace_bytes() bytes, 16-byte aligned; needs no initial value
  * Sums are float32 in a fixed order: the result does not vary from run to run.
+ * A device wait that gives up leaves NaN in the sums concerned (fa_device_status).
  */
 size_t fa_weights_workspace_bytes(void);
 int fa_cache_weights(const fa_cache_t *cache, const void *q, const float *lse, const int32_t *path,
@@ -355,6 +356,22 @@ size_t fa_evict_workspace_bytes(int B, int Hkv, int capacity, int keep);
 int fa_cache_evict(const fa_cache_t *cache, const float *weight, const int32_t *pos, float *weight_out,
                    int32_t *pos_out, int32_t *new_len, const int32_t *next_pos, int keep, int first, int last,
                    void *workspace, size_t workspace_bytes, fa_stream_t stream);
+
+/*
+ * fa_tree_debug, fa_weights_debug -- test hooks: fa_tree_fwd and fa_cache_weights with an explicit limit of each
+ * device wait (timeout_ns, 0 = the default of 2 s) and a fault-injection mask (inject bit 0: every CTA with
+ * work leaves out the load of its first V tile, or K tile, so that the wait for it expires; bit 1: only
+ * CTA 0).  The call then records FA_ERR_DEVICE_TIMEOUT and leaves NaN in the rows of o and lse, or the sums,
+ * of the CTAs that gave up and of the units that they share with others; the others hold their results.
+ */
+int fa_tree_debug(const fa_cache_t *cache, const void *q, const void *k_new, const void *v_new,
+                  const int32_t *parent, const int32_t *draft_len, void *o, float *lse, int Hq, int T,
+                  float scale, void *workspace, size_t workspace_bytes, fa_stream_t stream,
+                  uint64_t timeout_ns, uint32_t inject);
+int fa_weights_debug(const fa_cache_t *cache, const void *q, const float *lse, const int32_t *path,
+                     const int32_t *count, const float *weight, float *out, int Hq, int T, int causal,
+                     float scale, void *workspace, size_t workspace_bytes, fa_stream_t stream,
+                     uint64_t timeout_ns, uint32_t inject);
 
 #ifdef __cplusplus
 }

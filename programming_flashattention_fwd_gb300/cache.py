@@ -32,6 +32,8 @@ _SIGNATURES = {
     "fa_cache_append": (_I, [_C] + [_P] * 7 + [_I, _P]),
     "fa_weights_workspace_bytes": (_Z, []),
     "fa_cache_weights": (_I, [_C] + [_P] * 6 + [_I, _I, _I, _F, _P, _Z, _P]),
+    "fa_tree_debug": (_I, [_C] + [_P] * 7 + [_I, _I, _F, _P, _Z, _P, ctypes.c_uint64, ctypes.c_uint32]),
+    "fa_weights_debug": (_I, [_C] + [_P] * 6 + [_I, _I, _I, _F, _P, _Z, _P, ctypes.c_uint64, ctypes.c_uint32]),
     "fa_evict_workspace_bytes": (_Z, [_I] * 4),
     "fa_cache_evict": (_I, [_C] + [_P] * 6 + [_I, _I, _I, _P, _Z, _P]),
 }

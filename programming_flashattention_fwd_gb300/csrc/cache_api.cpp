@@ -132,9 +132,9 @@ size_t fa_tree_workspace_bytes(int Hq, int Hkv, int T, int D)
     return (size_t)kMaxCtas * sizeof(Cut) + (size_t)2 * kMaxCtas * part * (D + 1) * 4;
 }
 
-int fa_tree_fwd(const fa_cache_t *cache, const void *q, const void *k_new, const void *v_new, const int32_t *parent,
-                const int32_t *draft_len, void *o, float *lse, int Hq, int T, float scale, void *workspace,
-                size_t workspace_bytes, fa_stream_t stream)
+int fa_tree_debug(const fa_cache_t *cache, const void *q, const void *k_new, const void *v_new, const int32_t *parent,
+                  const int32_t *draft_len, void *o, float *lse, int Hq, int T, float scale, void *workspace,
+                  size_t workspace_bytes, fa_stream_t stream, uint64_t timeout_ns, uint32_t inject)
 {
     int st = check_cache(cache);
     if (st != FA_OK) return st;
@@ -197,7 +197,16 @@ int fa_tree_fwd(const fa_cache_t *cache, const void *q, const void *k_new, const
     p.box_rows = box;
     p.least = 2;
     p.sl2 = (float)((double)scale * 1.4426950408889634);
+    p.timeout_ns = timeout_ns;
+    p.inject = inject;
     return launch_tree(D, bf16, m, p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
+}
+
+int fa_tree_fwd(const fa_cache_t *cache, const void *q, const void *k_new, const void *v_new, const int32_t *parent,
+                const int32_t *draft_len, void *o, float *lse, int Hq, int T, float scale, void *workspace,
+                size_t workspace_bytes, fa_stream_t stream)
+{
+    return fa_tree_debug(cache, q, k_new, v_new, parent, draft_len, o, lse, Hq, T, scale, workspace, workspace_bytes, stream, 0, 0);
 }
 
 int fa_cache_append(const fa_cache_t *cache, const void *k_new, const void *v_new, const int32_t *path, const int32_t *count,
@@ -249,9 +258,9 @@ int fa_cache_append(const fa_cache_t *cache, const void *k_new, const void *v_ne
 
 size_t fa_weights_workspace_bytes(void) { return (size_t)kMaxCtas * sizeof(Cut) + (size_t)2 * kMaxCtas * 256 * 4; }
 
-int fa_cache_weights(const fa_cache_t *cache, const void *q, const float *lse, const int32_t *path, const int32_t *count,
+int fa_weights_debug(const fa_cache_t *cache, const void *q, const float *lse, const int32_t *path, const int32_t *count,
                      const float *weight, float *out, int Hq, int T, int causal, float scale, void *workspace,
-                     size_t workspace_bytes, fa_stream_t stream)
+                     size_t workspace_bytes, fa_stream_t stream, uint64_t timeout_ns, uint32_t inject)
 {
     int st = check_cache(cache);
     if (st != FA_OK) return st;
@@ -301,12 +310,21 @@ int fa_cache_weights(const fa_cache_t *cache, const void *q, const float *lse, c
     p.box_rows = gcd(cache->page, 128);
     p.least = 1;
     p.sl2 = (float)((double)scale * 1.4426950408889634);
+    p.timeout_ns = timeout_ns;
+    p.inject = inject;
     WeighMaps m;
     std::memset(&m, 0, sizeof(m));
     const long long eh[3] = {D, T, (long long)B * Hq}, er[3] = {D, rows, (long long)B * Hkv};
     if (!encode(&m.q, q, bf16, 3, mode == kHeads ? eh : er, NQ) || !encode_pool(&m.k, cache->k, q, cache, p.box_rows))
         return FA_ERR_TENSORMAP;
     return launch_weigh(D, bf16, m, p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
+}
+
+int fa_cache_weights(const fa_cache_t *cache, const void *q, const float *lse, const int32_t *path, const int32_t *count,
+                     const float *weight, float *out, int Hq, int T, int causal, float scale, void *workspace,
+                     size_t workspace_bytes, fa_stream_t stream)
+{
+    return fa_weights_debug(cache, q, lse, path, count, weight, out, Hq, T, causal, scale, workspace, workspace_bytes, stream, 0, 0);
 }
 
 size_t fa_evict_workspace_bytes(int B, int Hkv, int capacity, int keep)

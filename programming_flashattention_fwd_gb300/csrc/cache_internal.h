@@ -66,7 +66,8 @@ struct TreeParams {
     int box_rows;            // rows of one copy: gcd(page, 128), at most BN
     int least;               // steps a CTA takes at least
     float sl2;               // scale * log2 e
-    uint64_t timeout_ns;
+    uint64_t timeout_ns;     // limit of a wait (0: the default)
+    uint32_t inject;         // fault injection: the first V tile is never loaded (bit 0: in every CTA, bit 1: in CTA 0)
 };
 
 struct TreeMaps {
@@ -92,7 +93,8 @@ struct WeighParams {
     int box_rows;
     int least;
     float sl2;
-    uint64_t timeout_ns;
+    uint64_t timeout_ns;      // limit of a wait (0: the default)
+    uint32_t inject;          // fault injection: the first K tile is never loaded (bit 0: in every CTA, bit 1: in CTA 0)
 };
 
 struct WeighMaps {

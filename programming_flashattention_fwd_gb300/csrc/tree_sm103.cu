@@ -230,6 +230,7 @@ __global__ void __launch_bounds__(Cfg<D, PAIR>::THREADS, 1)
         const uint32_t box_off = (uint32_t)(pn * C::KVPANEL + box * p.box_rows * 128);
         int use0 = 0, last = 0;                       // the segment's first place in the ring, this warp's last
         uint32_t issued = 0;                          // bit i: place last - i is this warp's
+        bool skip = is_v && ((p.inject & 1u) || ((p.inject & 2u) && blockIdx.x == 0));
         bool ok = true;
         // the page (and the row in it) of this lane's box of step kt
         auto look = [&](int kt, int &pid, int &row) {
@@ -248,6 +249,12 @@ __global__ void __launch_bounds__(Cfg<D, PAIR>::THREADS, 1)
                 const uint32_t at = (uint32_t)use % C::NS, bar = bar_full(at), dst = sRing + at * C::KVTILE;
                 ok = wait_all(bar_empty(at), (((uint32_t)use / C::NS) & 1) ^ 1, S_EMPTY);
                 if (!ok) break;
+                if (skip) {
+                    skip = false;
+                    pid = pid1;
+                    row = row1;
+                    continue;
+                }
                 if (kt < g.len.kc) {
                     const int valid = min(boxes, cdiv(g.len.n - kt * BN, p.box_rows));
                     if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(valid * p.box_rows * 128 * C::PANELS));

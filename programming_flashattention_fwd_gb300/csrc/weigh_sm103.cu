@@ -162,6 +162,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int box = lane / C::PANELS, pn = lane % C::PANELS;
         const uint32_t box_off = (uint32_t)(pn * C::KPANEL + box * p.box_rows * 128);
         int ku = 0, qu = 0;
+        int skip = -1;   // the key tile that a fault injection leaves out
+        const bool inject = (p.inject & 1u) || ((p.inject & 2u) && blockIdx.x == 0);
         Ring<C::KS> k;
         Ring<C::QS> q;
         bool ok = true;
@@ -179,10 +181,14 @@ __global__ void __launch_bounds__(THREADS, 1)
                 ok = wait_all(k_empty(k.at), k.phase ^ 1, S_KEMPTY);
                 if (!ok) break;
                 const int valid = min(boxes, cdiv(g.len.n - kt * 128, p.box_rows));
-                if (lane == 0) mbar_arrive_expect_tx(k_full(k.at), (uint32_t)(valid * p.box_rows * 128 * C::PANELS));
-                __syncwarp();
-                // at most 8 boxes x PANELS: one for each lane at D = 256
-                if (box < valid) load_page(sb + k.at * C::KTILE + box_off, &maps.k, pn * 64, row, g.kvh, real_page(p.pages, pid), k_full(k.at));
+                if (skip >= 0 || !inject) {
+                    if (lane == 0) mbar_arrive_expect_tx(k_full(k.at), (uint32_t)(valid * p.box_rows * 128 * C::PANELS));
+                    __syncwarp();
+                    // at most 8 boxes x PANELS: one for each lane at D = 256
+                    if (box < valid) load_page(sb + k.at * C::KTILE + box_off, &maps.k, pn * 64, row, g.kvh, real_page(p.pages, pid), k_full(k.at));
+                } else {
+                    skip = ku;
+                }
                 pid = pid1;
                 row = row1;
                 if (gather) continue;
@@ -204,7 +210,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
         }
         if (lane == 0) {
-            for (int x = max(0, ku - C::KS); x < ku; ++x) bounded_wait(k_full(x % C::KS), (x / C::KS) & 1, abort_flag, tmo, S_DRAIN, status, false);
+            for (int x = max(0, ku - C::KS); x < ku; ++x)
+                if (x != skip) bounded_wait(k_full(x % C::KS), (x / C::KS) & 1, abort_flag, tmo, S_DRAIN, status, false);
             for (int x = max(0, qu - C::QS); x < qu; ++x) bounded_wait(q_full(x % C::QS), (x / C::QS) & 1, abort_flag, tmo, S_DRAIN, status, false);
         }
         __syncwarp();
@@ -621,13 +628,14 @@ __global__ void __launch_bounds__(Prompt<D>::THREADS, 1)
     if (warp == 0) {
         // ------------------------------------------------------------ K producer, Q producer
         const int boxes = 256 / p.box_rows;
+        const bool inject = (p.inject & 1u) || ((p.inject & 2u) && blockIdx.x == 0);   // the first key tile is left out
         int unit = 0, qu = 0;
         bool ok = true;
         for (; ok && walk.next(p.s, g); ++unit) {
             if (unit) ok = wait_all(barKfree, (unit - 1) & 1, S_KEMPTY);
             if (!ok) break;
-            const int valid = min(boxes, cdiv(g.len.n - g.kt * 256, p.box_rows));
-            if (lane == 0) mbar_arrive_expect_tx(barK, (uint32_t)(valid * p.box_rows * 128 * C::PANELS));
+            const int valid = inject && unit == 0 ? 0 : min(boxes, cdiv(g.len.n - g.kt * 256, p.box_rows));
+            if (lane == 0 && valid > 0) mbar_arrive_expect_tx(barK, (uint32_t)(valid * p.box_rows * 128 * C::PANELS));
             __syncwarp();
             for (int i = lane; i < valid * C::PANELS; i += 32) {
                 const int box = i / C::PANELS, pn = i % C::PANELS;
@@ -649,7 +657,7 @@ __global__ void __launch_bounds__(Prompt<D>::THREADS, 1)
             }
         }
         if (lane == 0) {
-            if (unit) bounded_wait(barK, (unit - 1) & 1, abort_flag, tmo, S_DRAIN, status, false);
+            if (unit && !(inject && unit == 1)) bounded_wait(barK, (unit - 1) & 1, abort_flag, tmo, S_DRAIN, status, false);
             for (int x = max(0, qu - C::QS); x < qu; ++x) bounded_wait(q_full(x), (x / C::QS) & 1, abort_flag, tmo, S_DRAIN, status, false);
         }
         __syncwarp();

@@ -561,3 +561,307 @@ def test_a_decoding_loop(fa, D, page):
         evict()
         compare()
     assert fa.fa_device_status() == (0, 0)
+
+
+# ---------------------------------------------------------------- streams, graphs, threads
+
+def small_case(fa, seed, lens=(300, 77), D=128, T=5, Hq=8, Hkv=2, page=16):
+    g = torch.Generator().manual_seed(seed)
+    B = len(lens)
+    k, v, table = make_pool(g, list(lens), Hkv, D, page, "bf16", room=T)
+    cap = table.shape[1] * page
+    c = dict(cache=fa.KVCache(k.cuda(), v.cuda(), ints(lens), table.cuda()), q=normal(g, (B, Hq, T, D), "bf16").cuda(),
+             kn=normal(g, (B, Hkv, T, D), "bf16").cuda(), vn=normal(g, (B, Hkv, T, D), "bf16").cuda(),
+             weight=torch.rand(B, Hkv, cap, generator=g).cuda(), pos=torch.arange(cap, dtype=torch.int32).expand(B, Hkv, cap).contiguous().cuda())
+    all_four(fa, c)    # once: the eviction moves rows, the same ones every time, so that from now on a step repeats exactly
+    return c
+
+
+def all_four(fa, c, stream=None, **kw):
+    """One step: attention, append, weights, eviction into separate buffers; its results."""
+    cache = c["cache"]
+    o, lse = fa.tree_attention(c["q"], c["kn"], c["vn"], cache, stream=stream)
+    fa.cache_append(cache, c["kn"], c["vn"], stream=stream)
+    out = torch.zeros_like(c["weight"])
+    fa.cache_weights(cache, c["q"], lse, c["weight"], out=out, stream=stream)
+    wo, po = torch.zeros_like(c["weight"]), torch.zeros_like(c["pos"])
+    left = fa.cache_evict(cache, c["weight"], c["pos"], 60, weight_out=wo, pos_out=po, stream=stream)
+    return [o, lse, out, wo, po, left]
+
+
+def test_another_stream(fa):
+    """Everything on a stream that is not the current one, named and entered, behind a long wait."""
+    c = small_case(fa, 21)
+    want = [t.clone() for t in all_four(fa, c)]
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    for how in ("named", "handle", "entered"):
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(20_000_000)
+        if how == "entered":
+            with torch.cuda.stream(s):
+                got = all_four(fa, c)
+        else:
+            got = all_four(fa, c, stream=s if how == "named" else s.cuda_stream)
+            # the current stream's allocations meanwhile must not meet the call's workspaces
+            junk = [torch.full((1 << 18,), float("nan"), device="cuda") for _ in range(8)]
+        s.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b), how
+        torch.cuda.synchronize()
+    del junk
+
+
+def test_two_streams_at_once(fa):
+    cs = [small_case(fa, 30 + i, lens=(900 + 50 * i, 400)) for i in range(2)]
+    want = [[t.clone() for t in all_four(fa, c)] for c in cs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cs]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(10):
+        got = []
+        for s, c in zip(streams, cs):
+            with torch.cuda.stream(s):
+                got.append(all_four(fa, c))
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_two_threads_on_one_stream(fa):
+    import threading
+    cs = [small_case(fa, 40 + i, lens=(700, 300 + 80 * i)) for i in range(2)]
+    want = [[t.clone() for t in all_four(fa, c)] for c in cs]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(i):
+        for _ in range(30):
+            got = all_four(fa, cs[i])
+            torch.cuda.synchronize()
+            if not all(torch.equal(x, y) for x, y in zip(got, want[i])):
+                bad.append(i)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
+
+
+def test_captured_graphs_follow_the_lengths(fa):
+    """Two graphs captured on one stream and replayed at once on two; lengths and tables change between replays."""
+    cs = [small_case(fa, 50 + i, lens=(500, 200)) for i in range(2)]
+    graphs, outs = [], []
+    for c in cs:
+        c["cache"].k.nan_to_num_(0, 0, 0), c["cache"].v.nan_to_num_(0, 0, 0)   # every page will be somebody's
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            torch.zeros(1000, device="cuda").zero_()          # a memset node before the first call
+            out = all_four(fa, c)
+        graphs.append(g)
+        outs.append(out)
+    streams = [torch.cuda.Stream() for _ in cs]
+    for lens in ((500, 200), (0, 37), (129, 500), (16, 1)):
+        want = []
+        for c in cs:
+            c["cache"].seq_len.copy_(ints(lens))
+            c["cache"].table.copy_(c["cache"].table.flip(1))
+        torch.cuda.synchronize()
+        for c in cs:
+            all_four(fa, c)                                     # once: its eviction moves rows, the same ones every time
+            want.append([t.clone() for t in all_four(fa, c)])
+        torch.cuda.synchronize()
+        for out in outs:
+            out[0].fill_(7), out[1].fill_(7)
+        torch.cuda.synchronize()
+        for s, g in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for out, w in zip(outs, want):
+            for a, b in zip(out, w):
+                assert torch.equal(a, b), lens
+
+
+def test_given_workspace(fa):
+    c = small_case(fa, 60)
+    want = [t.clone() for t in all_four(fa, c)]
+    ws = torch.full((1 << 23,), 255, dtype=torch.uint8, device="cuda")       # NaN patterns: no initial value is needed
+    o, lse = fa.tree_attention(c["q"], c["kn"], c["vn"], c["cache"], workspace=ws)
+    ws.fill_(255)
+    out = fa.cache_weights(c["cache"], c["q"], lse, c["weight"], out=torch.zeros_like(c["weight"]), workspace=ws)
+    ws.fill_(255)
+    wo = torch.zeros_like(c["weight"])
+    fa.cache_evict(c["cache"], c["weight"], c["pos"], 60, weight_out=wo, pos_out=torch.zeros_like(c["pos"]), workspace=ws)
+    assert torch.equal(o, want[0]) and torch.equal(lse, want[1]) and torch.equal(out, want[2]) and torch.equal(wo, want[3])
+    from programming_flashattention_fwd_gb300.binding import FaError
+    with pytest.raises(FaError) as e:
+        fa.tree_attention(c["q"], c["kn"], c["vn"], c["cache"], workspace=ws[:1024])
+    assert e.value.status == 16
+
+
+# ---------------------------------------------------------------- the edges of the sizes
+
+def test_lengths_out_of_range_are_clamped(fa):
+    c = small_case(fa, 70, lens=(64, 64), T=4, page=16)
+    cache, cap = c["cache"], c["cache"].capacity
+    results = []
+    for lens in ([cap + 1000, -5], [cap, 0]):
+        cache.seq_len.copy_(ints(lens))
+        cache.k.nan_to_num_(0, 0, 0), cache.v.nan_to_num_(0, 0, 0)
+        o, lse = fa.tree_attention(c["q"], c["kn"], c["vn"], cache, draft_len=ints([2000, 3]), o=torch.zeros_like(c["q"]))
+        out = fa.cache_weights(cache, c["q"], lse, c["weight"], count=ints([99, -3]), path=ints([[0, 1, 2, 3]] * 2), out=torch.zeros_like(c["weight"]))
+        results.append((o, lse[0], out))
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
+    assert fa.fa_device_status() == (0, 0)
+
+
+def test_many_sequences_with_weights(fa):
+    """More sequences than one warp looks at in one go."""
+    lens = [int(x) for x in np.random.default_rng(5).integers(0, 400, 75)]
+    run_weights(fa, "bf16", 2, 1, 64, lens, [min(n, 3 + i % 40) for i, n in enumerate(lens)], 50, 16)
+    run_weights(fa, "bf16", 2, 1, 64, lens, [min(n, 3 + i % 140) for i, n in enumerate(lens)], 150, 16)
+
+
+def test_weights_of_a_long_prompt(fa):
+    """The variant for long prompts: its sums against the oracle's, with one head."""
+    run_weights(fa, "bf16", 1, 1, 64, [4200], [4200], 4200, 128, poison=False)
+
+
+def test_pool_of_more_than_32_bits(fa):
+    """Pages at the far end of a pool of more than 2^32 elements."""
+    g = torch.Generator().manual_seed(80)
+    page, Hkv, D, n, T = 128, 2, 64, 300, 6
+    num = (2 ** 32 + 2 ** 28) // (Hkv * page * D)
+    k, v, table = make_pool(g, [n], Hkv, D, page, "bf16", room=T)
+    far = torch.arange(num - table.shape[1], num)[None]
+    K, V = (torch.empty(num, Hkv, page, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    K[far[0].cuda()], V[far[0].cuda()] = k[table[0].long()].cuda(), v[table[0].long()].cuda()
+    q, kn, vn = (normal(g, (1, h, T, D), "bf16").cuda() for h in (4, Hkv, Hkv))
+    caches = [fa.KVCache(k.cuda(), v.cuda(), ints([n]), table.cuda()), fa.KVCache(K, V, ints([n]), ints(far))]
+    w0 = torch.rand(1, Hkv, caches[0].capacity, generator=g)
+    results = []
+    for c in caches:
+        weight, pos = w0.cuda(), torch.arange(c.capacity, dtype=torch.int32).expand(1, Hkv, c.capacity).contiguous().cuda()
+        o, lse = fa.tree_attention(q, kn, vn, c)
+        fa.cache_append(c, kn, vn)
+        c.seq_len.add_(T)
+        fa.cache_weights(c, q, lse, weight)
+        fa.cache_evict(c, weight, pos, 200)
+        o2, lse2 = fa.tree_attention(q, kn, vn, c)
+        results.append((o, lse, weight, pos, o2, lse2))
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
+
+
+def test_evict_more_slots_than_fit_in_shared_memory(fa):
+    """One head with more slots a CTA than keys are held for, and tables of more pages."""
+    n, keep, page = 400_000, 150_000, 16
+    g = torch.Generator().manual_seed(81)
+    k = torch.zeros(-(-n // page), 1, page, 64, dtype=torch.bfloat16, device="cuda")
+    k[:, 0, :, 0] = (torch.arange(n, device="cuda") % 251).reshape(-1, page).to(torch.bfloat16)
+    v = k.clone()
+    for kind in ("spread", "ties"):
+        w = torch.rand(1, 1, k.shape[0] * page, generator=g) if kind == "spread" else torch.zeros(1, 1, k.shape[0] * page)
+        pos = torch.arange(w.shape[2], dtype=torch.int32)[None, None]
+        K, V, wd, pd = k.clone(), v.clone(), w.cuda(), pos.cuda()
+        fa.cache_evict(fa.KVCache(K, V, ints([n])), wd, pd, keep, first=5, last=100, next_pos=ints([n]))
+        dst, src = choose(w[0, 0].numpy(), pos[0, 0].numpy(), n, keep, 5, 100, n)
+        pr = pos[0, 0].clone()
+        pr[dst] = pr[src]
+        assert torch.equal(pd[0, 0, :keep].cpu(), pr[:keep])
+        assert torch.equal(K.reshape(-1, 64)[:keep, 0].cpu(), (pr[:keep] % 251).to(torch.bfloat16)) and torch.equal(K, V)
+        assert torch.equal(wd[0, 0, :keep].cpu(), w[0, 0][pr[:keep].long()])
+
+
+@pytest.mark.parametrize("D", [64, 256])
+def test_tree_non_finite_marks_do_not_outlive_their_unit(fa, D):
+    """Many units a CTA, some with non-finite drafted values: the others' rows are what they were."""
+    g = torch.Generator().manual_seed(82)
+    B, Hkv, T = 320, 2, 3
+    k, v, table = make_pool(g, [10] * B, Hkv, D, 16, "bf16")
+    q, kn, vn = (normal(g, (B, Hkv, T, D), "bf16") for _ in range(3))
+    parent = np.tile(np.array([-1, 0, 0]), (B, 1))
+    cache = fa.KVCache(k.cuda(), v.cuda(), ints([10] * B), table.cuda())
+    o1, l1 = fa.tree_attention(q.cuda(), kn.cuda(), vn.cuda(), cache, parent=ints(parent))
+    bad = torch.rand(B, generator=g) < 0.3
+    vn[bad, :, 1, 5] = float("inf")
+    o2, l2 = fa.tree_attention(q.cuda(), kn.cuda(), vn.cuda(), cache, parent=ints(parent))
+    want = o1.clone()
+    want[bad.cuda(), :, 1, 5] = float("inf")
+    assert torch.equal(o2, want) and torch.equal(l1, l2)
+
+
+# ---------------------------------------------------------------- waits that give up
+
+def debug_call(fa, fn, cache, args, tail):
+    from programming_flashattention_fwd_gb300 import cache as fc
+    st = getattr(fc._library(), fn)(cache._c, *[None if a is None else a.data_ptr() for a in args], *tail)
+    assert st == 0
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("D,Hq", [(64, 4), (128, 4), (128, 80), (256, 4)])
+@pytest.mark.parametrize("inject", [1, 2])
+def test_tree_waits_are_bounded(fa, D, Hq, inject):
+    """A V tile that never comes: the call ends, the status says so, the rows concerned are NaN, the others right
+    and the next call as well.  (Hq = 80: two row tiles side by side.)"""
+    g = torch.Generator().manual_seed(90)
+    B, Hkv, T, n = 40, 2, 4, 700
+    k, v, table = make_pool(g, [n] * B, Hkv, D, 16, "bf16")
+    q, kn, vn = (normal(g, (B, h, T, D), "bf16").cuda() for h in (Hq, Hkv, Hkv))
+    cache = fa.KVCache(k.cuda(), v.cuda(), ints([n] * B), table.cuda())
+    want = fa.tree_attention(q, kn, vn, cache)
+    o, lse = torch.zeros_like(q), torch.zeros(B, Hq, T, device="cuda")
+    size = fa.tree_workspace_bytes(Hq, Hkv, T, D)
+    ws = torch.zeros(size, dtype=torch.uint8, device="cuda")
+    debug_call(fa, "fa_tree_debug", cache, (q, kn, vn, None, None, o, lse),
+               (Hq, T, D ** -0.5, ws.data_ptr(), size, torch.cuda.current_stream().cuda_stream, 3_000_000, inject))
+    st, word = fa.fa_device_status()
+    assert st == 12 and word & 1
+    gone = torch.isnan(lse)
+    assert gone.any() and torch.equal(torch.isnan(o).all(3), gone) and torch.equal(torch.isnan(o).any(3), gone)
+    assert torch.equal(o[~gone], want[0][~gone]) and torch.equal(lse[~gone], want[1][~gone])
+    if inject == 1:
+        assert gone.all()
+    else:
+        heads = gone.reshape(B, Hkv, -1)                  # CTA 0 has the first units; what it shares goes with it
+        assert heads[0, 0].any() and not heads[-1].any()
+    assert fa.fa_device_status() == (0, 0)
+    again = fa.tree_attention(q, kn, vn, cache)
+    assert torch.equal(again[0], want[0]) and torch.equal(again[1], want[1]) and fa.fa_device_status() == (0, 0)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("T,with_path", [(6, True), (40, False), (300, False)])
+@pytest.mark.parametrize("inject", [1, 2])
+def test_weights_waits_are_bounded(fa, D, T, with_path, inject):
+    g = torch.Generator().manual_seed(91)
+    B, Hq, Hkv, n = 24, 4, 2, 1100
+    k, v, table = make_pool(g, [n] * B, Hkv, D, 16, "bf16")
+    q, lse = normal(g, (B, Hq, T, D), "bf16").cuda(), torch.randn(B, Hq, T, generator=g).cuda() + 4
+    cache = fa.KVCache(k.cuda(), v.cuda(), ints([n] * B), table.cuda())
+    path, count = (ints([list(range(T))] * B), ints([T] * B)) if with_path else (None, None)
+    want = fa.cache_weights(cache, q, lse, path=path, count=count)
+    out = torch.zeros_like(want)
+    size = fa.weights_workspace_bytes()
+    ws = torch.zeros(size, dtype=torch.uint8, device="cuda")
+    debug_call(fa, "fa_weights_debug", cache, (q, lse, path, count, None, out),
+               (Hq, T, 1, D ** -0.5, ws.data_ptr(), size, torch.cuda.current_stream().cuda_stream, 3_000_000, inject))
+    st, word = fa.fa_device_status()
+    assert st == 12 and word & 1
+    used = torch.arange(cache.capacity, device="cuda") < n
+    gone = torch.isnan(out)
+    assert gone.any() and not gone[..., ~used].any()
+    assert torch.equal(out[~gone], want[~gone])
+    if inject == 1:
+        assert gone[..., used].all()
+    else:
+        assert gone[0, 0].any() and not gone[-1].any()
+    assert torch.equal(fa.cache_weights(cache, q, lse, path=path, count=count), want) and fa.fa_device_status() == (0, 0)
