@@ -75,10 +75,17 @@ def _need(name: str, t, shape, dtype, index: int) -> int:
     return _refuse(name, t, shape, dtype, index)
 
 
-def _launch(fn, index: int, stream, args) -> None:
-    """fn(*args, stream handle) with the cache's device current; raises on a non-zero status."""
+def _current(index: int, stream) -> Optional[int]:
+    """The handle of the current stream, if the call is for it and the cache's device is the current one."""
     if stream is None and _b._raw_stream is not None and _b._cur_device is not None and _b._cur_device() == index:
-        st = fn(*args, _b._raw_stream(index))
+        return _b._raw_stream(index)
+    return None
+
+
+def _launch(fn, index: int, stream, current: Optional[int], args) -> None:
+    """fn(*args, stream handle) with the cache's device current; raises on a non-zero status."""
+    if current is not None:
+        st = fn(*args, current)
     else:
         device = torch.device("cuda", index)
         _check_stream_device(stream, device)
@@ -92,27 +99,45 @@ _local = threading.local()
 _capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", torch.cuda.is_current_stream_capturing)
 
 
-def _workspace(need: int, given: Optional[torch.Tensor], like: torch.Tensor, stream) -> Tuple[torch.Tensor, int, int]:
-    """A workspace on like's device, its address and size: the caller's, or else one that this thread keeps
-    for the current stream, whose calls run one after another.  A call that is captured into a graph, or
-    that names a stream, gets one of its own."""
-    index = like.get_device()
+def _kept(index: int, current: Optional[int]) -> Optional[dict]:
+    """What this thread keeps for the current stream, whose calls run one after another: its workspace and
+    a stock of small results.  None where a call is to have its own: it names a stream, or is captured into a graph."""
+    if current is None or _capturing():
+        return None
+    kept, key = _local.__dict__, (index, current)
+    entry = kept.get(key)
+    if entry is None:
+        entry = kept[key] = {}
+    return entry
+
+
+def _workspace(need: int, given: Optional[torch.Tensor], like: torch.Tensor, stream, kept) -> Tuple[torch.Tensor, int, int]:
+    """A workspace on like's device, its address and size: the caller's, the kept one, or one for this call."""
     if given is not None:
-        if given.get_device() != index or not given.is_contiguous():
+        if given.get_device() != like.get_device() or not given.is_contiguous():
             raise ValueError("workspace must be a contiguous CUDA tensor on the cache's device")
         return given, given.data_ptr(), given.nbytes
-    if stream is None and _b._raw_stream is not None and _b._cur_device is not None and _b._cur_device() == index \
-            and not _capturing():
-        kept, key = _local.__dict__, (index, _b._raw_stream(index))
-        ws = kept.get(key)
+    if kept is not None:
+        ws = kept.get("workspace")
         if ws is None or ws[2] < need:
             t = torch.empty(need, dtype=torch.uint8, device=like.device)
-            ws = kept[key] = (t, t.data_ptr(), need)
+            ws = kept["workspace"] = (t, t.data_ptr(), need)
         return ws
     t = torch.empty(need, dtype=torch.uint8, device=like.device)
     if stream is not None:   # not to be reused by the current stream's later work before `stream` is done with it
         t.record_stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device=like.device))
     return t, t.data_ptr(), need
+
+
+def _lengths(B: int, device: torch.device, kept) -> torch.Tensor:
+    """A new [B] int32 tensor.  From a stock of 64 that are made together: an allocation of its own is about a
+    third of what an eviction's call costs the host."""
+    if kept is None:
+        return torch.empty(B, dtype=_I32, device=device)
+    stock = kept.get(B)
+    if not stock:
+        stock = kept[B] = list(torch.empty((64, B), dtype=_I32, device=device).unbind(0))
+    return stock.pop()
 
 
 class KVCache:
@@ -149,7 +174,9 @@ class KVCache:
             per = table.shape[1]
             at = _need("table", table, (B, per), _I32, index)
         dt = k.dtype
-        self._c = _PACK(_need("k", k, shape, dt, index), _need("v", v, shape, dt, index), at,
+        if not k.is_contiguous():
+            raise ValueError("k must be contiguous")
+        self._c = _PACK(k.data_ptr(), _need("v", v, shape, dt, index), at,
                         _need("seq_len", seq_len, (B,), _I32, index), B, Hkv, D, page, per, num, code)
         self.k, self.v, self.seq_len, self.table = k, v, seq_len, table
         self.index, self.dtype, self.B, self.Hkv, self.D, self.page = index, dt, B, Hkv, D, page
@@ -198,8 +225,9 @@ def tree_attention(q, k_new, v_new, cache: KVCache, parent=None, draft_len=None,
             None if parent is None else _need("parent", parent, (B, T), _I32, i),
             None if draft_len is None else _need("draft_len", draft_len, (B,), _I32, i),
             _need("o", o, shape, dt, i), _need("lse", lse, rows, _F32, i), Hq, T, D ** -0.5 if scale is None else scale)
-    ws, at, size = _workspace(tree_workspace_bytes(Hq, Hkv, T, D), workspace, q, stream)
-    _launch(lib.fa_tree_fwd, i, stream, args + (at, size))
+    current = _current(i, stream)
+    ws, at, size = _workspace(tree_workspace_bytes(Hq, Hkv, T, D), workspace, q, stream, _kept(i, current))
+    _launch(lib.fa_tree_fwd, i, stream, current, args + (at, size))
     return o, lse
 
 
@@ -218,13 +246,13 @@ def cache_append(cache: KVCache, k_new, v_new, path=None, count=None, weight=Non
     if pos is not None and start is None:
         raise ValueError("pos needs start")
     lib = _lib or _library()
-    _launch(lib.fa_cache_append, i, stream,
-            (cache._c, _need("k_new", k_new, new, dt, i), _need("v_new", v_new, new, dt, i),
-             None if path is None else _need("path", path, (B, T), _I32, i),
-             None if count is None else _need("count", count, (B,), _I32, i),
-             None if start is None else _need("start", start, (B,), _I32, i),
-             None if weight is None else _need("weight", weight, slots, _F32, i),
-             None if pos is None else _need("pos", pos, slots, _I32, i), T))
+    args = (cache._c, _need("k_new", k_new, new, dt, i), _need("v_new", v_new, new, dt, i),
+            None if path is None else _need("path", path, (B, T), _I32, i),
+            None if count is None else _need("count", count, (B,), _I32, i),
+            None if start is None else _need("start", start, (B,), _I32, i),
+            None if weight is None else _need("weight", weight, slots, _F32, i),
+            None if pos is None else _need("pos", pos, slots, _I32, i), T)
+    _launch(lib.fa_cache_append, i, stream, _current(i, stream), args)
 
 
 @functools.lru_cache(maxsize=1)
@@ -255,8 +283,9 @@ def cache_weights(cache: KVCache, q, lse, weight=None, path=None, count=None, ca
             None if count is None else _need("count", count, (B,), _I32, i),
             None if weight is None else _need("weight", weight, slots, _F32, i), _need("out", out, slots, _F32, i),
             Hq, T, 1 if causal else 0, D ** -0.5 if scale is None else scale)
-    ws, at, size = _workspace(weights_workspace_bytes(), workspace, q, stream)
-    _launch(lib.fa_cache_weights, i, stream, args + (at, size))
+    current = _current(i, stream)
+    ws, at, size = _workspace(weights_workspace_bytes(), workspace, q, stream, _kept(i, current))
+    _launch(lib.fa_cache_weights, i, stream, current, args + (at, size))
     return out
 
 
@@ -277,13 +306,18 @@ def cache_evict(cache: KVCache, weight, pos, keep: int, first: int = 0, last: in
     slots = (B, cache.Hkv, cache.capacity)
     if last and next_pos is None:
         raise ValueError("last needs next_pos")
-    if new_len is None:
-        new_len = torch.empty(B, dtype=_I32, device=cache.device)
     w, p = _need("weight", weight, slots, _F32, i), _need("pos", pos, slots, _I32, i)
+    wo = w if weight_out is None else _need("weight_out", weight_out, slots, _F32, i)
+    po = p if pos_out is None else _need("pos_out", pos_out, slots, _I32, i)
+    nxt = None if next_pos is None else _need("next_pos", next_pos, (B,), _I32, i)
+    if new_len is not None:
+        _need("new_len", new_len, (B,), _I32, i)
     lib = _lib or _library()
-    args = (cache._c, w, p, w if weight_out is None else _need("weight_out", weight_out, slots, _F32, i),
-            p if pos_out is None else _need("pos_out", pos_out, slots, _I32, i), _need("new_len", new_len, (B,), _I32, i),
-            None if next_pos is None else _need("next_pos", next_pos, (B,), _I32, i), keep, first, last)
-    ws, at, size = _workspace(evict_workspace_bytes(B, cache.Hkv, cache.capacity, keep), workspace, cache.k, stream)
-    _launch(lib.fa_cache_evict, i, stream, args + (at, size))
+    current = _current(i, stream)
+    kept = _kept(i, current)
+    if new_len is None:
+        new_len = _lengths(B, cache.device, kept)
+    ws, at, size = _workspace(evict_workspace_bytes(B, cache.Hkv, cache.capacity, keep), workspace, cache.k, stream, kept)
+    _launch(lib.fa_cache_evict, i, stream, current,
+            (cache._c, w, p, wo, po, new_len.data_ptr(), nxt, keep, first, last, at, size))
     return new_len
