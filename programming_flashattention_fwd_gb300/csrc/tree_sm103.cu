@@ -171,6 +171,7 @@ __global__ void __launch_bounds__(Cfg<D, PAIR>::THREADS, 1)
         if (threadIdx.x == 0) atomicOr(status, 1u | (S_SMEM << 8));
         return;
     }
+    int total = 0, ctas = 1;   // (warp 3) all steps, the CTAs that share them
     if (warp == 0) {
         if (lane == 0) {
             for (int i = 0; i < 2; ++i) {
@@ -200,12 +201,9 @@ __global__ void __launch_bounds__(Cfg<D, PAIR>::THREADS, 1)
         grid_wait();
         const Share w = find_share(p.s.B, p.least, lane, blockIdx.x, gridDim.x, [&](int b) { return tree_steps(p.s, b); });
         const TreeWalk mine(p.s, w.b, w.off, w.left);
-        if (lane == 0) {
-            const_cast<Misc *>(misc)->share = mine;
-            Cut c = {};
-            if (w.left > 0) c = Cut{mine.b, mine.kvh, mine.mt, parts_from(w.total, w.G, blockIdx.x, mine.k, mine.len.nt), mine.len.t, {}};
-            p.cuts[blockIdx.x] = c;
-        }
+        total = w.total;
+        ctas = w.G;
+        if (lane == 0) const_cast<Misc *>(misc)->share = mine;
     }
     tc_fence_before();
     __syncthreads();
@@ -230,6 +228,11 @@ __global__ void __launch_bounds__(Cfg<D, PAIR>::THREADS, 1)
         const uint32_t box_off = (uint32_t)(pn * C::KVPANEL + box * p.box_rows * 128);
         int use0 = 0, last = 0;                       // the segment's first place in the ring, this warp's last
         uint32_t issued = 0;                          // bit i: place last - i is this warp's
+        if (is_v && lane == 0) {   // for the joining kernel
+            Cut c = {};
+            if (walk.left > 0) c = Cut{walk.b, walk.kvh, walk.mt, parts_from(total, ctas, blockIdx.x, walk.k, walk.len.nt), walk.len.t, {}};
+            p.cuts[blockIdx.x] = c;
+        }
         bool skip = is_v && ((p.inject & 1u) || ((p.inject & 2u) && blockIdx.x == 0));
         bool ok = true;
         // the page (and the row in it) of this lane's box of step kt
@@ -757,7 +760,7 @@ constexpr int kJoinWarps = 4;
 template <int D, bool BF16>
 __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_constant__ TreeParams p)
 {
-    constexpr int PER = D / 32, FEW = 4;
+    constexpr int PER = D / 32, FEW = 5;
     __shared__ float sums[kJoinWarps][D];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     grid_wait();
