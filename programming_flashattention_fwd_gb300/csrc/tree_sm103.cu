@@ -664,8 +664,7 @@ __global__ void __launch_bounds__(Cfg<D, PAIR>::THREADS, 1)
 #pragma unroll
                         for (int e = 0; e < 32; ++e) h[e] = f1 == 0.f ? h[e] : fmaf(__uint_as_float(ov[e]), f1, h[e]);
                     }
-                    if (!live) continue;
-                    if (odd) {
+                    if (live && odd) {
                         // weights are positive, so a non-finite value counts as what it is
                         for (int kt = max(g.k0, g.len.kc); kt < g.k1; ++kt) {
                             const int lo = (kt - g.len.kc) * BN;
@@ -687,7 +686,7 @@ __global__ void __launch_bounds__(Cfg<D, PAIR>::THREADS, 1)
                             }
                         }
                     }
-                    if (whole) {
+                    if (live && whole) {
                         uint32_t pk[16];
 #pragma unroll
                         for (int e = 0; e < 16; ++e) pk[e] = pack2<BF16>(h[2 * e], h[2 * e + 1]);
@@ -695,7 +694,7 @@ __global__ void __launch_bounds__(Cfg<D, PAIR>::THREADS, 1)
 #pragma unroll
                         for (int q4 = 0; q4 < 4; ++q4)
                             st_global_v4(dst + q4 * 16, pk[4 * q4], pk[4 * q4 + 1], pk[4 * q4 + 2], pk[4 * q4 + 3]);
-                    } else {
+                    } else if (live) {
                         float *dst = p.part_o + prow * D + c;
 #pragma unroll
                         for (int q8 = 0; q8 < 4; ++q8) {
@@ -705,6 +704,7 @@ __global__ void __launch_bounds__(Cfg<D, PAIR>::THREADS, 1)
                             st_global_v8(dst + 8 * q8, w);
                         }
                     }
+                    __syncwarp();   // the next columns are read by all lanes together
                 }
             }
             if (live && (!SPLIT || grp == 0)) {
