@@ -254,7 +254,8 @@ int fa_fwd_host_noalloc(const void *q_h, const void *k_h, const void *v_h, void 
  * kernels read when they run, so a captured graph follows them.  A length below 0 counts as 0, one
  * above the capacity as the capacity.  A table entry outside [0, num_pages) that a length covers is a
  * caller's mistake that touches no memory outside the cache: its slots read as zero keys and values
- * and writes to them are dropped.
+ * and writes to them are dropped.  Sequences may share pages that are only read; a page that
+ * fa_cache_append or fa_cache_evict writes to must belong to one sequence.
  *
  * All tensors are dense; pointers are device pointers on the current device, 16-byte aligned for
  * k, v, q, o, k_new and v_new, 4-byte aligned otherwise.  Everything said above about ownership,
@@ -287,6 +288,8 @@ typedef struct fa_cache {
  *   scale        > 0 and finite
  *   workspace    fa_tree_workspace_bytes(Hq, Hkv, T, D) bytes, 32-byte aligned; needs no initial value
  * The cache is only read: the drafted tokens are appended when they are accepted (fa_cache_append).
+ * Every drafted token is a key of every row until the mask decides, which suits drafts and short chunks of a
+ * prompt; fa_fwd leaves out the key tiles above the diagonal of a long one.
  * What the cache holds behind a sequence's end, and tokens that a row does not see, have no effect
  * on the row, NaN and infinities included.  The result does not vary from run to run.
  * FA_ERR_TOO_LARGE: workspace_bytes is too small.  A device wait that gives up leaves NaN in the

@@ -306,6 +306,8 @@ def cache_evict(cache: KVCache, weight, pos, keep: int, first: int = 0, last: in
     slots = (B, cache.Hkv, cache.capacity)
     if last and next_pos is None:
         raise ValueError("last needs next_pos")
+    if not 0 < keep < 2 ** 31 or not 0 <= first < 2 ** 31 or not 0 <= last < 2 ** 31:
+        raise ValueError("keep must be positive, first and last not negative")
     w, p = _need("weight", weight, slots, _F32, i), _need("pos", pos, slots, _I32, i)
     wo = w if weight_out is None else _need("weight_out", weight_out, slots, _F32, i)
     po = p if pos_out is None else _need("pos_out", pos_out, slots, _I32, i)

@@ -69,6 +69,9 @@ bool clash(const Range *all, int n, int written)
 
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
+// Positive and finite, with its factor log2 e too.
+bool good_scale(float s) { return s > 0.f && std::isfinite((float)((double)s * 1.4426950408889634)); }
+
 int gcd(int a, int b) { return b ? gcd(b, a % b) : a; }
 
 // Checks of a cache's own fields, shared by every entry point.
@@ -83,7 +86,8 @@ int check_cache(const fa_cache_t *c)
     const long long cap = (long long)c->max_pages * c->page;
     if (cap > 0x7fffff00LL || (long long)c->B * c->Hkv > 0x7fffffffLL || (long long)c->B * c->max_pages > 0x7fffffffLL)
         return FA_ERR_BAD_DIM;
-    if (!c->table && (long long)c->B * c->max_pages > c->num_pages) return FA_ERR_BAD_DIM;
+    // slots without any page to be in; a dense cache without pages enough
+    if ((c->num_pages == 0 && cap > 0) || (!c->table && (long long)c->B * c->max_pages > c->num_pages)) return FA_ERR_BAD_DIM;
     return FA_OK;
 }
 
@@ -99,8 +103,8 @@ size_t pool_bytes(const fa_cache_t *c) { return (size_t)c->num_pages * c->Hkv * 
 
 Pages pages_of(const fa_cache_t *c) { return Pages{c->table, c->page, c->max_pages, c->num_pages}; }
 
-// K or V of a cache as a (D, page, Hkv, num_pages) tensor.  An empty pool (which no length can make a
-// kernel read) is given one page of extent so that the map can be encoded over any valid address.
+// K or V of a cache as a (D, page, Hkv, num_pages) tensor.  An empty pool (the capacity is 0 then, so no length
+// makes a kernel read it) is given one page of extent so that the map can be encoded over any valid address.
 bool encode_pool(CUtensorMap *m, const void *base, const void *any, const fa_cache_t *c, int rows)
 {
     const long long ext[4] = {c->D, c->page, c->Hkv, c->num_pages > 0 ? c->num_pages : 1};
@@ -141,7 +145,7 @@ int fa_tree_debug(const fa_cache_t *cache, const void *q, const void *k_new, con
     const int B = cache->B, Hkv = cache->Hkv, D = cache->D;
     if (T < 0) return FA_ERR_BAD_DIM;
     if (Hq < 1 || Hq % Hkv != 0) return FA_ERR_HEADS;
-    if (!(std::isfinite(scale) && scale > 0.f)) return FA_ERR_SCALE;
+    if (!good_scale(scale)) return FA_ERR_SCALE;
     if (B == 0 || T == 0) return FA_OK;
     const long long rows = (long long)(Hq / Hkv) * T;
     const int tile = tree_tile(D, rows), BN = 1 << tree_log_keys(D), cap = cache->max_pages * cache->page;
@@ -267,7 +271,7 @@ int fa_weights_debug(const fa_cache_t *cache, const void *q, const float *lse, c
     const int B = cache->B, Hkv = cache->Hkv, D = cache->D;
     if (T < 0) return FA_ERR_BAD_DIM;
     if (Hq < 1 || Hq % Hkv != 0) return FA_ERR_HEADS;
-    if (!(std::isfinite(scale) && scale > 0.f)) return FA_ERR_SCALE;
+    if (!good_scale(scale)) return FA_ERR_SCALE;
     if (causal != 0 && causal != 1) return FA_ERR_CAUSAL;
     const int group = Hq / Hkv, NQ = weigh_rows(D), cap = cache->max_pages * cache->page;
     if (B == 0 || cap == 0) return FA_OK;

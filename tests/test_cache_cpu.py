@@ -58,13 +58,13 @@ def append(lib, **over):
 
 BAD_CACHE = [(dict(B=-1), 2), (dict(max_pages=-1), 2), (dict(num_pages=-1), 2), (dict(Hkv=0), 3), (dict(D=96), 4),
              (dict(D=32), 4), (dict(page=8), 2), (dict(page=24), 2), (dict(page=0), 2), (dict(dtype=2), 15),
-             (dict(max_pages=1 << 26), 2), (dict(table=None, max_pages=11), 2), (dict(seq_len=None), 1),
+             (dict(max_pages=1 << 26), 2), (dict(num_pages=0), 2), (dict(table=None, max_pages=11), 2), (dict(seq_len=None), 1),
              (dict(k=None), 1), (dict(v=None), 1), (dict(k=ADDR["k"] + 8), 5), (dict(seq_len=ADDR["seq_len"] + 2), 5)]
 
 
 @pytest.mark.parametrize("over,code", BAD_CACHE + [
     (dict(Hq=3), 3), (dict(Hq=0), 3), (dict(T=-1), 2), (dict(scale=0.0), 7), (dict(scale=-0.1), 7), (dict(scale=math.nan), 7),
-    (dict(scale=math.inf), 7), (dict(q=None), 1), (dict(k_new=None), 1), (dict(v_new=None), 1), (dict(o=None), 1),
+    (dict(scale=math.inf), 7), (dict(scale=3e38), 7), (dict(q=None), 1), (dict(k_new=None), 1), (dict(v_new=None), 1), (dict(o=None), 1),
     (dict(lse=None), 1), (dict(ws=None), 1), (dict(q=ADDR["q"] + 8), 5), (dict(lse=ADDR["lse"] + 2), 5),
     (dict(parent=ADDR["parent"] + 1), 5), (dict(ws=ADDR["ws"] + 16), 5), (dict(bytes=1000), 16), (dict(o=ADDR["q"]), 6),
     (dict(o=ADDR["k"] + 64), 6), (dict(lse=ADDR["o"] + 16), 6), (dict(ws=ADDR["v"]), 6), (dict(lse=ADDR["draft_len"]), 6),
@@ -220,7 +220,7 @@ def test_cache_weights_checks_its_tensors(over, what):
 
 
 @pytest.mark.parametrize("over,what", [
-    (dict(last=3), "needs next_pos"), (dict(weight=on((2, 2, 40), torch.float32)), "weight"), (dict(pos=on((2, 2, 48), torch.int64)), "pos"),
+    (dict(last=3), "needs next_pos"), (dict(keep=0), "positive"), (dict(keep=2 ** 32 + 5), "positive"), (dict(first=-1), "negative"), (dict(weight=on((2, 2, 40), torch.float32)), "weight"), (dict(pos=on((2, 2, 48), torch.int64)), "pos"),
     (dict(pos_out=on((2, 2, 48), torch.float32)), "pos_out"), (dict(new_len=on((3,), torch.int32)), "new_len"),
     (dict(next_pos=on((2,), torch.int32, 1)), "same GPU")])
 def test_cache_evict_checks_its_tensors(over, what):
