@@ -75,22 +75,38 @@ def _need(name: str, t, shape, dtype, index: int) -> int:
     return _refuse(name, t, shape, dtype, index)
 
 
-def _current(index: int, stream) -> Optional[int]:
-    """The handle of the current stream, if the call is for it and the cache's device is the current one."""
-    if stream is None and _b._raw_stream is not None and _b._cur_device is not None and _b._cur_device() == index:
+def _on(stream, cache: "KVCache", fn, *args):
+    """fn(*args) with `stream` (a torch.cuda.Stream or a handle) current.  What the call allocates and fills then
+    belongs to that stream: memory of the current stream's may still be in use by what runs there."""
+    device = cache.device
+    _check_stream_device(stream, device)
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = int(stream)
+        stream = torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
+    user = torch.cuda.current_stream(device)
+    with torch.cuda.stream(stream):
+        result = fn(*args)
+    # results are for the caller's stream, which may outlast their last reference
+    for t in result if isinstance(result, tuple) else (result,):
+        if t is not None:
+            t.record_stream(user)
+    return result
+
+
+def _current(index: int) -> Optional[int]:
+    """The handle of the current stream, if the cache's device is the current one."""
+    if _b._raw_stream is not None and _b._cur_device is not None and _b._cur_device() == index:
         return _b._raw_stream(index)
     return None
 
 
-def _launch(fn, index: int, stream, current: Optional[int], args) -> None:
+def _launch(fn, index: int, current: Optional[int], args) -> None:
     """fn(*args, stream handle) with the cache's device current; raises on a non-zero status."""
     if current is not None:
         st = fn(*args, current)
     else:
-        device = torch.device("cuda", index)
-        _check_stream_device(stream, device)
-        with _OnDevice(device):
-            st = fn(*args, _stream_handle(stream))
+        with _OnDevice(torch.device("cuda", index)):
+            st = fn(*args, _stream_handle(None))
     if st != 0:
         raise FaError(st, fa_strerror(st))
 
@@ -101,7 +117,8 @@ _capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", torch.cuda.is_c
 
 def _kept(index: int, current: Optional[int]) -> Optional[dict]:
     """What this thread keeps for the current stream, whose calls run one after another: its workspace and
-    a stock of small results.  None where a call is to have its own: it names a stream, or is captured into a graph."""
+    a stock of small results.  None where a call is to have its own: on another device than the current one, or
+    captured into a graph."""
     if current is None or _capturing():
         return None
     kept, key = _local.__dict__, (index, current)
@@ -111,7 +128,7 @@ def _kept(index: int, current: Optional[int]) -> Optional[dict]:
     return entry
 
 
-def _workspace(need: int, given: Optional[torch.Tensor], like: torch.Tensor, stream, kept) -> Tuple[torch.Tensor, int, int]:
+def _workspace(need: int, given: Optional[torch.Tensor], like: torch.Tensor, kept) -> Tuple[torch.Tensor, int, int]:
     """A workspace on like's device, its address and size: the caller's, the kept one, or one for this call."""
     if given is not None:
         if given.get_device() != like.get_device() or not given.is_contiguous():
@@ -124,8 +141,6 @@ def _workspace(need: int, given: Optional[torch.Tensor], like: torch.Tensor, str
             ws = kept["workspace"] = (t, t.data_ptr(), need)
         return ws
     t = torch.empty(need, dtype=torch.uint8, device=like.device)
-    if stream is not None:   # not to be reused by the current stream's later work before `stream` is done with it
-        t.record_stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device=like.device))
     return t, t.data_ptr(), need
 
 
@@ -211,7 +226,11 @@ def tree_attention(q, k_new, v_new, cache: KVCache, parent=None, draft_len=None,
     root; None: a chain), draft_len [B] int32 (None: T).  Returns (o [B, Hq, T, D], lse [B, Hq, T]
     float32), in o and lse where they are given; rows at or behind draft_len are not written.
     scale defaults to D ** -0.5.  workspace: tree_workspace_bytes(...) bytes that no other call in
-    flight uses; None: one that is kept for the calling thread's current stream."""
+    flight uses; None: one that is kept for the calling thread and the stream, or, in a call that is
+    captured into a graph, one of the graph's own.  stream (of this and the other operators): where the call
+    runs, and what it allocates then belongs to; None: the current stream."""
+    if stream is not None:
+        return _on(stream, cache, tree_attention, q, k_new, v_new, cache, parent, draft_len, scale, o, lse, workspace)
     shape = _queries(q, cache)
     B, Hq, T, D = shape
     i, dt, Hkv = cache.index, cache.dtype, cache.Hkv
@@ -225,9 +244,9 @@ def tree_attention(q, k_new, v_new, cache: KVCache, parent=None, draft_len=None,
             None if parent is None else _need("parent", parent, (B, T), _I32, i),
             None if draft_len is None else _need("draft_len", draft_len, (B,), _I32, i),
             _need("o", o, shape, dt, i), _need("lse", lse, rows, _F32, i), Hq, T, D ** -0.5 if scale is None else scale)
-    current = _current(i, stream)
-    ws, at, size = _workspace(tree_workspace_bytes(Hq, Hkv, T, D), workspace, q, stream, _kept(i, current))
-    _launch(lib.fa_tree_fwd, i, stream, current, args + (at, size))
+    current = _current(i)
+    ws, at, size = _workspace(tree_workspace_bytes(Hq, Hkv, T, D), workspace, q, _kept(i, current))
+    _launch(lib.fa_tree_fwd, i, current, args + (at, size))
     return o, lse
 
 
@@ -237,6 +256,8 @@ def cache_append(cache: KVCache, k_new, v_new, path=None, count=None, weight=Non
     (token i without a path) of k_new, v_new [B, Hkv, T, D], i < count[b] (None: T).  weight
     [B, Hkv, capacity] float32 becomes 0 and pos [B, Hkv, capacity] int32 start[b] + i at the new slots,
     where given.  seq_len is not changed: add count to it after the last layer."""
+    if stream is not None:
+        return _on(stream, cache, cache_append, cache, k_new, v_new, path, count, weight, pos, start)
     if not isinstance(k_new, torch.Tensor) or k_new.dim() != 4:
         raise ValueError("k_new must be a [B, Hkv, T, D] tensor")
     i, dt, B, Hkv, T = cache.index, cache.dtype, cache.B, cache.Hkv, k_new.shape[2]
@@ -252,7 +273,7 @@ def cache_append(cache: KVCache, k_new, v_new, path=None, count=None, weight=Non
             None if start is None else _need("start", start, (B,), _I32, i),
             None if weight is None else _need("weight", weight, slots, _F32, i),
             None if pos is None else _need("pos", pos, slots, _I32, i), T)
-    _launch(lib.fa_cache_append, i, stream, _current(i, stream), args)
+    _launch(lib.fa_cache_append, i, _current(i), args)
 
 
 @functools.lru_cache(maxsize=1)
@@ -269,6 +290,8 @@ def cache_weights(cache: KVCache, q, lse, weight=None, path=None, count=None, ca
     ``cache_append`` (the accepted rows); causal: row i is the query of slot seq_len[b] - count[b] + i
     and sees the slots up to its own.  weight [B, Hkv, capacity] float32 (None: zeros) is added to; the
     result is written to out, which defaults to weight itself (without a weight, to a new tensor of zeros)."""
+    if stream is not None:
+        return _on(stream, cache, cache_weights, cache, q, lse, weight, path, count, causal, scale, out, workspace)
     shape = _queries(q, cache)
     B, Hq, T, D = shape
     i = cache.index
@@ -283,9 +306,9 @@ def cache_weights(cache: KVCache, q, lse, weight=None, path=None, count=None, ca
             None if count is None else _need("count", count, (B,), _I32, i),
             None if weight is None else _need("weight", weight, slots, _F32, i), _need("out", out, slots, _F32, i),
             Hq, T, 1 if causal else 0, D ** -0.5 if scale is None else scale)
-    current = _current(i, stream)
-    ws, at, size = _workspace(weights_workspace_bytes(), workspace, q, stream, _kept(i, current))
-    _launch(lib.fa_cache_weights, i, stream, current, args + (at, size))
+    current = _current(i)
+    ws, at, size = _workspace(weights_workspace_bytes(), workspace, q, _kept(i, current))
+    _launch(lib.fa_cache_weights, i, current, args + (at, size))
     return out
 
 
@@ -302,6 +325,9 @@ def cache_evict(cache: KVCache, weight, pos, keep: int, first: int = 0, last: in
     kept slots at or above `keep` move to the freed ones below.  weight [B, Hkv, capacity] float32 and
     pos int32 follow the slots, in place unless weight_out and pos_out are given.  Returns new_len [B]
     int32 = min(seq_len, keep); seq_len itself is not changed."""
+    if stream is not None:
+        return _on(stream, cache, cache_evict, cache, weight, pos, keep, first, last, next_pos, weight_out, pos_out, new_len,
+                   workspace)
     i, B = cache.index, cache.B
     slots = (B, cache.Hkv, cache.capacity)
     if last and next_pos is None:
@@ -315,11 +341,11 @@ def cache_evict(cache: KVCache, weight, pos, keep: int, first: int = 0, last: in
     if new_len is not None:
         _need("new_len", new_len, (B,), _I32, i)
     lib = _lib or _library()
-    current = _current(i, stream)
+    current = _current(i)
     kept = _kept(i, current)
     if new_len is None:
         new_len = _lengths(B, cache.device, kept)
-    ws, at, size = _workspace(evict_workspace_bytes(B, cache.Hkv, cache.capacity, keep), workspace, cache.k, stream, kept)
-    _launch(lib.fa_cache_evict, i, stream, current,
+    ws, at, size = _workspace(evict_workspace_bytes(B, cache.Hkv, cache.capacity, keep), workspace, cache.k, kept)
+    _launch(lib.fa_cache_evict, i, current,
             (cache._c, w, p, wo, po, new_len.data_ptr(), nxt, keep, first, last, at, size))
     return new_len

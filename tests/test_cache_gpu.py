@@ -613,6 +613,30 @@ def test_another_stream(fa):
     del junk
 
 
+def test_a_named_stream_has_its_own_memory(fa):
+    """A block that the current stream has freed, while work there is still to write it, must not be part of a call
+    on another stream; nor may zeros be filled in by the current stream."""
+    c = small_case(fa, 22)
+    q, kn, vn, cache = c["q"], c["kn"], c["vn"], c["cache"]
+    want = [t.clone() for t in fa.tree_attention(q, kn, vn, cache)]
+    want.append(fa.cache_weights(cache, q, want[1]).clone())
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    sizes = sorted({fa.tree_workspace_bytes(q.shape[1], kn.shape[1], q.shape[2], q.shape[3]), fa.weights_workspace_bytes(),
+                    q.nbytes, want[1].nbytes, want[2].nbytes})
+    for how in (s, s.cuda_stream):
+        torch.cuda._sleep(100_000_000)
+        for size in sizes:          # written behind the wait, free for the current stream at once
+            for _ in range(4):
+                torch.empty(size, dtype=torch.uint8, device="cuda").fill_(0xff)
+        o, lse = fa.tree_attention(q, kn, vn, cache, stream=how)
+        w = fa.cache_weights(cache, q, want[1], stream=how)
+        s.synchronize()
+        torch.cuda.synchronize()
+        for a, b in zip((o, lse, w), want):
+            assert torch.equal(a, b)
+
+
 def test_two_streams_at_once(fa):
     cs = [small_case(fa, 30 + i, lens=(900 + 50 * i, 400)) for i in range(2)]
     want = [[t.clone() for t in all_four(fa, c)] for c in cs]
