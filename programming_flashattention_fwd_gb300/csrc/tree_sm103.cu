@@ -409,9 +409,9 @@ __global__ void __launch_bounds__(Cfg<D, PAIR>::THREADS, 1)
         uint32_t gs0 = 0;
         int use0 = 0, seg = 0;
         bool ok = true;
+        const int urow = (PAIR ? grp * kRowTile : 0) + r;          // row of the unit
         for (; ok && walk.next(p.s, g); ++seg) {
             const int nk = g.k1 - g.k0;
-            const int urow = (PAIR ? grp * kRowTile : 0) + r;      // row of the unit
             const int row = g.mt * p.s.tile + urow, t = row % p.s.T;
             const bool live = row < p.s.rows && t < g.len.t;
             const bool warp_live = __any_sync(~0u, live);
@@ -508,11 +508,12 @@ __global__ void __launch_bounds__(Cfg<D, PAIR>::THREADS, 1)
                     }
                     grow(mrow);
                     const float msub = m_used == -INFINITY ? 0.f : m_used;
+                    float sum0 = 0.f, sum1 = 0.f;
                     // P of 32 keys overwrites the scores of 16: the scores of later keys are read first
                     uint32_t sv[32];
                     tmem_ld_x32(tS, sv);
 #pragma unroll 1
-                    for (int c = 0; c < ((valid + 63) >> 6) * 2; ++c) {
+                    for (int c = 0; c < chunks; ++c) {
                         const uint32_t w = word(c);
                         tmem_wait_ld();
                         reg_fence_x32(sv);
@@ -521,13 +522,19 @@ __global__ void __launch_bounds__(Cfg<D, PAIR>::THREADS, 1)
                         for (int e = 0; e < 16; ++e) {
                             const float p0 = (w >> (2 * e)) & 1u ? ex2_approx(fmaf(__uint_as_float(sv[2 * e]), sl2, -msub)) : 0.f;
                             const float p1 = (w >> (2 * e + 1)) & 1u ? ex2_approx(fmaf(__uint_as_float(sv[2 * e + 1]), sl2, -msub)) : 0.f;
-                            l += p0 + p1;
+                            sum0 += p0;
+                            sum1 += p1;
                             pk[e] = pack2<BF16>(p0, p1);
                         }
                         if (c + 1 < BN / 32) tmem_ld_x32(tS + 32 * (c + 1), sv);
                         tmem_wait_ld();
                         reg_fence_x32(sv);
                         tmem_st_x16(tS + 16 * c, pk);
+                    }
+                    l += sum0 + sum1;
+                    if (chunks & 1) {
+                        const uint32_t none[16] = {};
+                        tmem_st_x16(tS + 16 * chunks, none);
                     }
                 }
                 // O may be rescaled only once this accumulator's previous product is complete
@@ -567,10 +574,12 @@ __global__ void __launch_bounds__(Cfg<D, PAIR>::THREADS, 1)
                     ok = wait_all(bar_full(uv % C::NS), (uv / C::NS) & 1, S_FULL);
                     if (!ok) break;
                     const uint32_t sV = sRing + (uint32_t)(uv % C::NS) * C::KVTILE;
-                    const int dead = (((valid + 63) & ~63) - valid) * 8;   // 16-byte chunks of one panel
+                    // 16-byte chunks of one panel; what is behind the last token of all sequences was zeroed when it was loaded
+                    const int end = draft ? min(BN, p.s.T - (kt - g.len.kc) * BN) : BN, dead = (min((valid + 63) & ~63, end) - valid) * 8;
 #pragma unroll 1
                     for (int pn = 0; pn < C::PANELS; ++pn)
                         for (int i = r; i < dead; i += 128) st_shared_v4(sV + pn * C::KVPANEL + valid * 128 + i * 16, 0u, 0u, 0u, 0u);
+                    bool wrote = dead > 0;
                     if (draft) {
                         bool any = false;
 #pragma unroll 1
@@ -589,8 +598,9 @@ __global__ void __launch_bounds__(Cfg<D, PAIR>::THREADS, 1)
                                 any |= here;
                             }
                         if (any) misc->nonfinite = seg + 1;
+                        wrote |= any;
                     }
-                    fence_proxy_async_smem();
+                    if (wrote) fence_proxy_async_smem();
                 }
                 tmem_wait_st();
                 tc_fence_before();
@@ -641,28 +651,23 @@ __global__ void __launch_bounds__(Cfg<D, PAIR>::THREADS, 1)
             const size_t orow = ((size_t)(g.b * p.s.Hkv + g.kvh)) * p.s.rows + row;
             constexpr int COLS = SPLIT ? D / 2 : D;        // columns of this group
             const uint32_t tO0 = tmem + lane_off + C::COL_O + (PAIR ? grp * D : 0);
+            if (!have0) f0 = 0.f;
+            if (!have1) f1 = 0.f;
             if (warp_live) {
+                // 16 columns at a time: the code is fetched anew after the key steps, and its length counts more than the loads'
 #pragma unroll 1
-                for (int c = SPLIT ? grp * COLS : 0, cn = 0; cn < COLS; c += 32, cn += 32) {
-                    float h[32];
-                    if (have0) {
-                        uint32_t ov[32];
-                        tmem_ld_x32(tO0 + c, ov);
-                        tmem_wait_ld();
-                        reg_fence_x32(ov);
+                for (int c = SPLIT ? grp * COLS : 0, cn = 0; cn < COLS; c += 16, cn += 16) {
+                    uint32_t oa[16], ob[16];
+                    tmem_ld_x16(tO0 + c, oa);
+                    if constexpr (SPLIT) tmem_ld_x16(tO0 + D + c, ob);
+                    tmem_wait_ld();
+                    reg_fence_x16(oa);
+                    if constexpr (SPLIT) reg_fence_x16(ob);
+                    float h[16];
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) h[e] = f0 == 0.f ? 0.f : __uint_as_float(ov[e]) * f0;
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) h[e] = 0.f;
-                    }
-                    if (have1) {
-                        uint32_t ov[32];
-                        tmem_ld_x32(tO0 + D + c, ov);
-                        tmem_wait_ld();
-                        reg_fence_x32(ov);
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) h[e] = f1 == 0.f ? h[e] : fmaf(__uint_as_float(ov[e]), f1, h[e]);
+                    for (int e = 0; e < 16; ++e) {
+                        h[e] = f0 == 0.f ? 0.f : __uint_as_float(oa[e]) * f0;
+                        if constexpr (SPLIT) h[e] = f1 == 0.f ? h[e] : fmaf(__uint_as_float(ob[e]), f1, h[e]);
                     }
                     if (live && odd) {
                         // weights are positive, so a non-finite value counts as what it is
@@ -679,7 +684,7 @@ __global__ void __launch_bounds__(Cfg<D, PAIR>::THREADS, 1)
                                 const uint16_t *v = static_cast<const uint16_t *>(p.v_new) +
                                                     ((size_t)(g.b * p.s.Hkv + g.kvh) * p.s.T + key) * D + c;
 #pragma unroll
-                                for (int e = 0; e < 32; ++e) {
+                                for (int e = 0; e < 16; ++e) {
                                     const float x = half_to_float<BF16>(__ldg(v + e));
                                     if (!isfinite(x)) h[e] += x;
                                 }
@@ -687,17 +692,17 @@ __global__ void __launch_bounds__(Cfg<D, PAIR>::THREADS, 1)
                         }
                     }
                     if (live && whole) {
-                        uint32_t pk[16];
+                        uint32_t pk[8];
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) pk[e] = pack2<BF16>(h[2 * e], h[2 * e + 1]);
+                        for (int e = 0; e < 8; ++e) pk[e] = pack2<BF16>(h[2 * e], h[2 * e + 1]);
                         uint8_t *dst = static_cast<uint8_t *>(p.o) + (orow * D + c) * 2;
 #pragma unroll
-                        for (int q4 = 0; q4 < 4; ++q4)
+                        for (int q4 = 0; q4 < 2; ++q4)
                             st_global_v4(dst + q4 * 16, pk[4 * q4], pk[4 * q4 + 1], pk[4 * q4 + 2], pk[4 * q4 + 3]);
                     } else if (live) {
                         float *dst = p.part_o + prow * D + c;
 #pragma unroll
-                        for (int q8 = 0; q8 < 4; ++q8) {
+                        for (int q8 = 0; q8 < 2; ++q8) {
                             uint32_t w[8];
 #pragma unroll
                             for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(h[8 * q8 + e]);
