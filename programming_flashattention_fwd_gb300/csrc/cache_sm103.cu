@@ -26,7 +26,8 @@ __device__ __forceinline__ long long row_of(const Pages &pg, int Hkv, int b, int
 // slot n_b + i of every KV head takes the key and value of token path[b, i] (token i without a
 // path), i < count[b]; its accumulated weight starts at 0 and its position is start[b] + i.  A copy,
 // bound by memory: a thread moves 16 bytes of K and of V, neighbouring threads neighbouring bytes
-// of a row.
+// of a row.  16384 tokens of 8 KV heads at D = 128 (134 MB read and written) take 22.6 us, 6.0 TB/s;
+// the accepted tokens of a step (8 x 24) 2.5 us, which is the launch.
 constexpr int kAppendThreads = 256;
 
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_constant__ AppendParams p)
@@ -69,6 +70,11 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
 // the other, and the i-th of these moves to the i-th of those: sources and destinations never meet, so the
 // rows move in place, in parallel, and no other row is touched.  The lists hold rows, so that a move is two
 // dependent round trips: its list entries, then its rows.
+//
+// Bound by latency: about ten cluster-wide steps, each a barrier and a round trip through distributed shared
+// memory or DRAM, and the moves at the end.  Measured, 8 KV heads, D = 128: 8 x 4160 slots to 4096 12.2 us, 4 x
+// 16384 to 2048 34 us (63 MB: 1.8 TB/s); 16 heads, D = 64, 16 x up to 2000 slots to 777 20.5 us.  kCandidates of
+// 64 to 512 take the same time.
 constexpr int kEvictThreads = 512, kEvictWarps = kEvictThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kBins = 2048, kCandidates = 512;
@@ -421,10 +427,15 @@ cudaError_t launch_evict(const EvictParams &p0, cudaStream_t st)
         if (e != cudaSuccess) return e;
         configured.fetch_or(1ull << dev, std::memory_order_acq_rel);
     }
-    // CTAs of a head: up to two in each SM, so that all clusters run at once, with 1024 slots each at least
+    // CTAs of a head: one to an SM, with 1024 slots each at least, and a second one to an SM (all clusters run at
+    // once) where each would have more than 6144 slots and moves, a move counted as four.  With and without the second
+    // (us, 8 KV heads, D = 128): 8 x 4160 -> 4096 slots 14.3, 12.2; 16 x 4160 -> 4096 15.0, 13.4; 4 x 16384 -> 2048
+    // 35.2, 34.4; 16 x 5120 -> 4096 37.3, 46.0; 8 x 12288 -> 1024 29.9, 36.8; 16 x 8192 -> 8000 20.9, 24.2;
+    // 8 x 65536 -> 4096 110, 165.
     const int heads = p.B * p.Hkv;
     int C = 1;
-    while (C < kMaxCluster && heads * C * 2 <= 304 && p.capacity > 1024 * C) C *= 2;
+    while (C < kMaxCluster && heads * C * 2 <= 152 && p.capacity > 1024 * C) C *= 2;
+    if (C < kMaxCluster && heads * C * 2 <= 304 && p.capacity + 4ll * p.longest > 6144ll * C) C *= 2;
     const int per = cdiv(p.capacity, C);
     p.held = per < kHeldMost ? per : kHeldMost;
     const int pages = per / p.pages.page + 2;

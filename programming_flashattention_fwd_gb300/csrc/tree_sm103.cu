@@ -6,14 +6,25 @@
 //     o   = sum_j exp(s_j - m) v_j / sum_j exp(s_j - m),   lse = m + ln sum_j exp(s_j - m)
 //
 // The rows of one KV head (heads of the group x drafted tokens, consecutive in memory) are packed
-// into 128-row tiles, so that K and V are read once for all of them; with fewer than about 280 rows
-// the kernel is bound by that read.  The keys of every unit (sequence, KV head, row tile) are cut so
-// that each CTA has the same number of key steps (cache_schedule.h); a unit that is cut leaves
-// normalised fp32 partial rows with their log-sum-exp in the workspace and a second kernel joins
-// them in the order of the keys, the same on every run.
+// into 128-row tiles, so that K and V are read once for all of them.  A key costs 4 D flops a row and
+// 4 D bytes: with fewer than about 280 rows the read bounds the kernel.  The keys of every unit
+// (sequence, KV head, row tile) are cut so that each CTA has the same number of key steps
+// (cache_schedule.h); a unit that is cut leaves normalised fp32 partial rows with their log-sum-exp in
+// the workspace and a second kernel joins them in the order of the keys, the same on every run.
+// (Joined by the last CTA to arrive instead, with counters and fences: one token over 4096 slots 24.8
+// instead of 17 us, 8 x 64 tokens over 16384 138 instead of 102.)
+//
+// Measured, 8 sequences, 32 heads over 8 KV heads, bf16, of 6.8 TB/s copied:
+//     D = 64, 131072 slots    one token 6.8 TB/s, 32 tokens 6.3     D = 256, 65536 slots   7.2, 6.9
+//     D = 128, 131072 slots   one token 6.8 TB/s (16-slot pages 6.7), 32 tokens 6.8, 64 tokens (256 rows,
+//                             where the softmax is as busy as memory) 5.6
+// Short calls are a chain of latencies (start, one unit, second kernel): one sequence, one token, 10.4 us
+// over 16 slots and 11.2 over 4096.  So are many short units, about 3.5 us each of an SM's time beside
+// the reads: 64 x 128 slots 25 us, 64 x 1024 54.6 (4.9 TB/s), 64 x 4096 172 (6.2 TB/s).
 //
 // Per CTA (one per SM):
-//   warps 0, 3    K and V producers: per step one TMA box per page and 64-column panel (each lane looks
+//   warps 0, 3    K and V producers (one warp for both: 5.5 instead of 6.4 TB/s at D = 64, 4.9 instead of
+//                 6.4 with 16-slot pages): per step one TMA box per page and 64-column panel (each lane looks
 //                 up the page of its box, a step ahead), into one ring of NS slots in the order in
 //                 which the products take them (K_0, K_1, V_0, K_2, V_1, ...).  Warp 3 finds the CTA's share first.
 //   warp 1        TMEM owner and MMA issuer: S = Q K^T, O += P V (tcgen05, fp32 in tensor memory)
@@ -24,7 +35,7 @@
 //                       they are joined in the epilogue, where both read both accumulators (half of
 //                       the columns each)
 //     more (PAIR)       each group has a row tile of its own and takes every step: K and V are read once
-//                       for 256 rows
+//                       for 256 rows (8 x 64 tokens over up to 16384 slots 102 us, a row tile by itself 139)
 //     D = 256           one group, 64-key steps (two accumulators do not fit)
 //
 // Tensor memory: S_0, S_1 (BN columns each; P, 16-bit, overwrites its S), then the accumulators.

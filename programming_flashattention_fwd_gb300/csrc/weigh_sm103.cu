@@ -14,6 +14,14 @@
 // tensor pipe and by the exponentials about equally (128 x 128 scores: 512 cycles of each at D = 128),
 // a drafting step by the one read of K.
 //
+// Measured, 32 heads over 8 KV heads, bf16:
+//     16 rows a head over 4 x 131072 slots    D = 64 5.0 TB/s (115 us), D = 128 6.4 (173 us; 16-slot pages 4.7:
+//                                             one warp issues a box a page), D = 256 6.7 (326 us)
+//     a prompt over itself, causal            8192 tokens: D = 64 205 us, D = 128 208 us (1320 TFLOP/s), D = 256
+//                                             344 us (1600); 2048 tokens, D = 128: 28 us; 16384: 765 us (1440)
+//     few rows over a short cache             8 to 10 us: start, one tile, second kernel
+// D = 64 has as many exponentials as D = 128 for half the products, and is bound by them.
+//
 // The steps (key tile x tile of query rows) are shared out evenly (cache_schedule.h).  A key tile that a
 // cut crosses leaves its parts in the workspace; a second kernel adds them in order, so the sums do
 // not vary from run to run.
