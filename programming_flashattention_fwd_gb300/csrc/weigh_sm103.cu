@@ -15,8 +15,8 @@
 // a drafting step by the one read of K.
 //
 // Measured, 32 heads over 8 KV heads, bf16:
-//     16 rows a head over 4 x 131072 slots    D = 64 5.0 TB/s (115 us), D = 128 6.4 (173 us; 16-slot pages 4.7:
-//                                             one warp issues a box a page), D = 256 6.7 (326 us)
+//     16 rows a head over 4 x 131072 slots    D = 64 5.7 TB/s (100 us), D = 128 6.3 (175 us; 16-slot pages 6.2),
+//                                             D = 256 6.7 (326 us); one token over 64 x 1024 slots 4.4 (32 us)
 //     a prompt over itself, causal            8192 tokens: D = 64 205 us, D = 128 208 us (1320 TFLOP/s), D = 256
 //                                             344 us (1600); 2048 tokens, D = 128: 28 us; 16384: 765 us (1440)
 //     few rows over a short cache             8 to 10 us: start, one tile, second kernel
@@ -27,7 +27,8 @@
 // not vary from run to run.
 //
 // Per CTA (one per SM):
-//   warp 0        K producer (one box per page and panel) and, unless rows are gathered, Q producer
+//   warps 0, 20   K producers, alternate key tiles (one box per page and panel; one warp for all: D = 64 4.9 TB/s,
+//                 D = 128 6.4, with 16-slot pages 3.2 and 4.7); warp 0 is the Q producer too, unless rows are gathered
 //   warp 1        TMEM owner and MMA issuer, into four S^T buffers
 //   warps 2-3     lse and visible limit of each step's 128 rows; in path mode also the gathered Q tile
 //   warps 4-19    the sums, one thread per key: four groups of four warps take the steps in turn, a
@@ -51,7 +52,7 @@ namespace {
 
 constexpr uint64_t kDefaultTimeoutNs = 2000000000ull;
 constexpr int NB = 4;   // S^T buffers, 128 columns apart, each with a group of four warps that sums it
-constexpr int THREADS = 128 + 128 * NB;
+constexpr int THREADS = 128 + 128 * NB + 32;
 
 enum Site : uint32_t { S_KEMPTY = 1, S_QEMPTY = 2, S_KFULL = 3, S_QFULL = 4, S_FREE = 5, S_S = 6, S_ROWS = 7, S_DRAIN = 8, S_SMEM = 9, S_JOIN = 10, S_READ = 11 };
 
@@ -164,14 +165,15 @@ __global__ void __launch_bounds__(THREADS, 1)
     // A Q tile is taken anew with every head, and with every step where a key tile has several: then the
     // tiles 0 .. ns - 1 follow one another again and again.
 
-    if (warp == 0) {
-        // ------------------------------------------------------------ K producer, Q producer
+    if (warp == 0 || warp == 4 + 4 * NB) {
+        // ------------------------------------------------------------ K producers, Q producer
+        const int who = warp == 0 ? 0 : 1;   // this warp's key tiles: every other one
         const int boxes = 128 / p.box_rows;
         const int box = lane / C::PANELS, pn = lane % C::PANELS;
         const uint32_t box_off = (uint32_t)(pn * C::KPANEL + box * p.box_rows * 128);
         int ku = 0, qu = 0;
         int skip = -1;   // the key tile that a fault injection leaves out
-        const bool inject = (p.inject & 1u) || ((p.inject & 2u) && blockIdx.x == 0);
+        const bool inject = who == 0 && ((p.inject & 1u) || ((p.inject & 2u) && blockIdx.x == 0));
         Ring<C::KS> k;
         Ring<C::QS> q;
         bool ok = true;
@@ -181,25 +183,27 @@ __global__ void __launch_bounds__(THREADS, 1)
             auto look = [&](int kt, int &pid, int &row) {
                 if (box < boxes && kt * 128 + box * p.box_rows < g.len.n) page_of(p.pages, g.b, kt * 128 + box * p.box_rows, pid, row);
             };
-            look(g.kt, pid, row);
+            look(g.kt + ((ku ^ who) & 1), pid, row);
             int step = 0;      // steps whose Q tile has been loaded
             for (int u = 0; ok && u < units; ++u, ++ku, k.next()) {
                 const int kt = g.kt + u;
-                look(kt + 1, pid1, row1);   // used in the next round
-                ok = wait_all(k_empty(k.at), k.phase ^ 1, S_KEMPTY);
-                if (!ok) break;
-                const int valid = min(boxes, cdiv(g.len.n - kt * 128, p.box_rows));
-                if (skip >= 0 || !inject) {
-                    if (lane == 0) mbar_arrive_expect_tx(k_full(k.at), (uint32_t)(valid * p.box_rows * 128 * C::PANELS));
-                    __syncwarp();
-                    // at most 8 boxes x PANELS: one for each lane at D = 256
-                    if (box < valid) load_page(sb + k.at * C::KTILE + box_off, &maps.k, pn * 64, row, g.kvh, real_page(p.pages, pid), k_full(k.at));
-                } else {
-                    skip = ku;
+                if (((ku ^ who) & 1) == 0) {
+                    look(kt + 2, pid1, row1);   // used in this warp's next round
+                    ok = wait_all(k_empty(k.at), k.phase ^ 1, S_KEMPTY);
+                    if (!ok) break;
+                    const int valid = min(boxes, cdiv(g.len.n - kt * 128, p.box_rows));
+                    if (skip >= 0 || !inject) {
+                        if (lane == 0) mbar_arrive_expect_tx(k_full(k.at), (uint32_t)(valid * p.box_rows * 128 * C::PANELS));
+                        __syncwarp();
+                        // at most 8 boxes x PANELS: one for each lane at D = 256
+                        if (box < valid) load_page(sb + k.at * C::KTILE + box_off, &maps.k, pn * 64, row, g.kvh, real_page(p.pages, pid), k_full(k.at));
+                    } else {
+                        skip = ku;
+                    }
+                    pid = pid1;
+                    row = row1;
                 }
-                pid = pid1;
-                row = row1;
-                if (gather) continue;
+                if (gather || who) continue;
                 const int last = min(g.steps, (u + 1) * g.ns - g.s);   // steps up to the end of this key tile
                 for (; ok && step < last; ++step) {
                     if (g.ns == 1 && step > 0) continue;
@@ -219,7 +223,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         if (lane == 0) {
             for (int x = max(0, ku - C::KS); x < ku; ++x)
-                if (x != skip) bounded_wait(k_full(x % C::KS), (x / C::KS) & 1, abort_flag, tmo, S_DRAIN, status, false);
+                if (x != skip && ((x ^ who) & 1) == 0) bounded_wait(k_full(x % C::KS), (x / C::KS) & 1, abort_flag, tmo, S_DRAIN, status, false);
             for (int x = max(0, qu - C::QS); x < qu; ++x) bounded_wait(q_full(x % C::QS), (x / C::QS) & 1, abort_flag, tmo, S_DRAIN, status, false);
         }
         __syncwarp();
