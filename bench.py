@@ -76,11 +76,16 @@ TARGET_FRAC = 0.60    # of the dense bf16 peak, stated for the D = 128 workloads
 # The sources each timed kernel is built from: its own translation unit plus the shared
 # device headers and the host code that encodes its tensor maps and launch shape.
 COMMON_SOURCES = ("ptx.cuh", "watchdog.cuh", "fa_internal.h", "fa_api.cpp")
+CACHE_SOURCES = ("cache_api.cpp", "cache_device.cuh", "cache_internal.h", "cache_schedule.h")
 KERNEL_SOURCES = {
     "fa::fa_fwd_kernel": ("fa_fwd_sm103.cu", "schedule.h"),
     "fa::fa_fwd1_kernel": ("fa_fwd1_sm103.cu", "schedule.h"),
     "fa::gemm::gemm_kernel": ("gemm_sm103.cu",),
     "fa::sm::softmax_regs_kernel": ("softmax_sm103.cu",),
+    "fa::cache::tree_kernel": ("tree_sm103.cu",) + CACHE_SOURCES,
+    "fa::cache::weigh_kernel": ("weigh_sm103.cu",) + CACHE_SOURCES,
+    "fa::cache::weigh_prompt_kernel": ("weigh_sm103.cu",) + CACHE_SOURCES,
+    "fa::cache::evict_kernel": ("cache_sm103.cu",) + CACHE_SOURCES,
 }
 
 

@@ -18,8 +18,8 @@
 //     D = 64, 131072 slots    one token 6.8 TB/s, 32 tokens 6.3     D = 256, 65536 slots   7.2, 6.9
 //     D = 128, 131072 slots   one token 6.8 TB/s (16-slot pages 6.7), 32 tokens 6.8, 64 tokens (256 rows,
 //                             where the softmax is as busy as memory) 5.6
-// Short calls are a chain of latencies (start, one unit, second kernel): one sequence, one token, 10.4 us
-// over 16 slots and 11.2 over 4096.  So are many short units, about 3.5 us each of an SM's time beside
+// Short calls are a chain of latencies (start, one unit, second kernel): one sequence, one token, 10 us
+// over 16 slots and 11 over 4096.  So are many short units, about 3.5 us each of an SM's time beside
 // the reads: 64 x 128 slots 25 us, 64 x 1024 54.6 (4.9 TB/s), 64 x 4096 172 (6.2 TB/s).
 //
 // Per CTA (one per SM):
