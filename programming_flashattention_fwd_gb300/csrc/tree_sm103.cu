@@ -19,8 +19,9 @@
 //     D = 128, 131072 slots   one token 6.8 TB/s (16-slot pages 6.7), 32 tokens 6.8, 64 tokens (256 rows,
 //                             where the softmax is as busy as memory) 5.6
 // Short calls are a chain of latencies (start, one unit, second kernel): one sequence, one token, 10 us
-// over 16 slots and 11 over 4096.  So are many short units, about 3.5 us each of an SM's time beside
-// the reads: 64 x 128 slots 25 us, 64 x 1024 54.6 (4.9 TB/s), 64 x 4096 172 (6.2 TB/s).
+// over 16 slots and 11 over 4096.  So are many short units, about 3 us each of an SM's time, which
+// the reads of the next one only partly cover: 64 x 128 slots 23 us, 64 x 512 38 (3.5 TB/s), 64 x 1024 53 (5.1), 64 x
+// 4096 171 (6.3).
 //
 // Per CTA (one per SM):
 //   warps 0, 3    K and V producers (one warp for both: 5.5 instead of 6.4 TB/s at D = 64, 4.9 instead of
@@ -420,6 +421,11 @@ __global__ void __launch_bounds__(Cfg<D, PAIR>::THREADS, 1)
         uint32_t gs0 = 0;
         int use0 = 0, seg = 0;
         bool ok = true;
+        // Scores read once, by unrolled code, or twice, by a short loop: the loop where memory is the bound, since what a
+        // launch and a unit's end cost is mostly code fetched anew (D = 128: 64 x 512 slots 38 instead of 45 us, 8 x
+        // 131072 620 either way), not beside a second row tile, nor at D = 64, where a step is half as long
+        // (64 x 1024 slots 41 and 45 us, 64 x 4096 105 and 93, 8 x 131072 351 and 320).
+        constexpr bool UNROLLED = PAIR || D == 64;
         const int urow = (PAIR ? grp * kRowTile : 0) + r;          // row of the unit
         for (; ok && walk.next(p.s, g); ++seg) {
             const int nk = g.k1 - g.k0;
@@ -467,7 +473,7 @@ __global__ void __launch_bounds__(Cfg<D, PAIR>::THREADS, 1)
                         rescale = true;
                     }
                 };
-                if (warp_live && !masked) {
+                if (UNROLLED && warp_live && !masked) {
                     uint32_t sv[BN];
                     float pm[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -502,48 +508,61 @@ __global__ void __launch_bounds__(Cfg<D, PAIR>::THREADS, 1)
                     f2_unpack(f2_add(f2_add(sum2[0], sum2[1]), f2_add(sum2[2], sum2[3])), la, lb);
                     l += la + lb;
                 } else if (warp_live) {
-                    // Masked step (one or two a unit): 32 keys at a time, up to the last valid one and read twice, in a
-                    // short loop.  P is written for whole halves of 64 keys, which is what P V takes.
-                    auto word = [&](int c) { return BN == 64 ? (c ? bits[1] : bits[0]) : (c < 2 ? (c ? bits[1] : bits[0]) : (c == 2 ? bits[BN / 32 - 2] : bits[BN / 32 - 1])); };
-                    const int chunks = (valid + 31) >> 5;
-                    float mrow = -INFINITY;
-#pragma unroll 1
-                    for (int c = 0; c < chunks; ++c) {
-                        uint32_t sv[32];
-                        tmem_ld_x32(tS + 32 * c, sv);
-                        const uint32_t w = word(c);
-                        tmem_wait_ld();
-                        reg_fence_x32(sv);
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) mrow = fmaxf(mrow, (w >> e) & 1u ? __uint_as_float(sv[e]) : -INFINITY);
-                    }
-                    grow(mrow);
-                    const float msub = m_used == -INFINITY ? 0.f : m_used;
-                    float sum0 = 0.f, sum1 = 0.f;
-                    // P of 32 keys overwrites the scores of 16: the scores of later keys are read first
+                    // The maximum, then P, 32 keys at a time in a short loop
+                    const int chunks = masked ? (valid + 31) >> 5 : BN / 32;
                     uint32_t sv[32];
+                    if (masked) {
+                        // hidden scores become -inf, up to the last valid one
+                        auto word = [&](int c) { return BN == 64 ? (c ? bits[1] : bits[0]) : (c < 2 ? (c ? bits[1] : bits[0]) : (c == 2 ? bits[BN / 32 - 2] : bits[BN / 32 - 1])); };
+                        float mrow = -INFINITY;
+#pragma unroll 1
+                        for (int c = 0; c < chunks; ++c) {
+                            tmem_ld_x32(tS + 32 * c, sv);
+                            const uint32_t w = word(c);
+                            tmem_wait_ld();
+                            reg_fence_x32(sv);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) {
+                                if (!((w >> e) & 1u)) sv[e] = 0xff800000u;
+                                mrow = fmaxf(mrow, __uint_as_float(sv[e]));
+                            }
+                            tmem_st_x32(tS + 32 * c, sv);
+                        }
+                        tmem_wait_st();
+                        grow(mrow);
+                    } else {
+                        float pm[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                        for (int c = 0; c < BN; c += 32) tmem_ld_red_max_x32(tS + c, sv, pm[c / 32]);
+                        tmem_wait_ld();
+                        reg_fence_f4(pm[0], pm[1], pm[2], pm[3]);
+                        grow(fmaxf(fmax3(pm[0], pm[1], pm[2]), pm[3]));
+                    }
+                    const float msub = m_used == -INFINITY ? 0.f : m_used;
+                    const uint64_t negm2 = f2_pack(-msub, -msub);
+                    uint64_t sum2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
+                    // P of 32 keys overwrites the scores of 16: the scores of later keys are never where it goes
                     tmem_ld_x32(tS, sv);
 #pragma unroll 1
                     for (int c = 0; c < chunks; ++c) {
-                        const uint32_t w = word(c);
                         tmem_wait_ld();
                         reg_fence_x32(sv);
                         uint32_t pk[16];
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
-                            const float p0 = (w >> (2 * e)) & 1u ? ex2_approx(fmaf(__uint_as_float(sv[2 * e]), sl2, -msub)) : 0.f;
-                            const float p1 = (w >> (2 * e + 1)) & 1u ? ex2_approx(fmaf(__uint_as_float(sv[2 * e + 1]), sl2, -msub)) : 0.f;
-                            sum0 += p0;
-                            sum1 += p1;
+                            float t0, t1;
+                            f2_unpack(f2_fma(f2_pack(__uint_as_float(sv[2 * e]), __uint_as_float(sv[2 * e + 1])), sl2x2, negm2), t0, t1);
+                            const float p0 = ex2_approx(t0), p1 = ex2_approx(t1);
+                            sum2[e & 1] = f2_add(sum2[e & 1], f2_pack(p0, p1));
                             pk[e] = pack2<BF16>(p0, p1);
                         }
-                        if (c + 1 < BN / 32) tmem_ld_x32(tS + 32 * (c + 1), sv);
-                        tmem_wait_ld();
-                        reg_fence_x32(sv);
+                        if (c + 1 < chunks) tmem_ld_x32(tS + 32 * (c + 1), sv);
                         tmem_st_x16(tS + 16 * c, pk);
                     }
-                    l += sum0 + sum1;
-                    if (chunks & 1) {
+                    float la, lb;
+                    f2_unpack(f2_add(sum2[0], sum2[1]), la, lb);
+                    l += la + lb;
+                    if (chunks & 1) {   // P is taken for whole halves of 64 keys
                         const uint32_t none[16] = {};
                         tmem_st_x16(tS + 16 * chunks, none);
                     }
