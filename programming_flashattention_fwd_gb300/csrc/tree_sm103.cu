@@ -37,7 +37,7 @@
 //                       the columns each)
 //     more (PAIR)       each group has a row tile of its own and takes every step: K and V are read once
 //                       for 256 rows (8 x 64 tokens over up to 16384 slots 102 us, a row tile by itself 139)
-//     D = 256           one group, 64-key steps (two accumulators do not fit)
+//     D = 256           one group, 64-key steps (two accumulators do not fit); the other reads half of the result
 //
 // Tensor memory: S_0, S_1 (BN columns each; P, 16-bit, overwrites its S), then the accumulators.
 //
@@ -72,9 +72,9 @@ enum Site : uint32_t {
 template <int D, bool PAIR>
 struct Cfg {
     static constexpr int LBN = D == 256 ? 6 : 7, BN = 1 << LBN;
-    static constexpr int NG = D == 256 ? 1 : 2;          // softmax groups
+    static constexpr int NG = D == 256 ? 1 : 2;          // groups that take key steps, of the two that read the result
     static constexpr int STRIDE = PAIR ? 1 : NG;         // key steps from one of a group to its next
-    static constexpr int THREADS = 128 + 128 * NG;
+    static constexpr int THREADS = 128 + 128 * 2;
     static constexpr int PANELS = D / 64;
     static constexpr int QTILE = PANELS * 16384;         // one tile of 128 rows, or two of up to 64
     static constexpr int QAREA = PAIR ? 2 * QTILE : QTILE;
@@ -84,8 +84,8 @@ struct Cfg {
     static constexpr int OFF_RING = QAREA;
     static constexpr int OFF_BAR = OFF_RING + NS * KVTILE;
     static constexpr int NBAR = 4 + 2 * NS + 2 + 2 + 2 + 2 + 1;    // q[2], qfree[2], full, empty, S[2], P[2], PV[2], join, read, done
-    static constexpr int OFF_ML = OFF_BAR + ((NBAR * 8 + 15) / 16) * 16;   // [NG][128] (m, l)
-    static constexpr int OFF_MISC = OFF_ML + NG * 128 * 8;
+    static constexpr int OFF_ML = OFF_BAR + ((NBAR * 8 + 15) / 16) * 16;   // [2][128] (m, l)
+    static constexpr int OFF_MISC = OFF_ML + 2 * 128 * 8;
     static constexpr int BYTES = OFF_MISC + 64;
     static_assert(BYTES <= 232448, "shared memory of one CTA");
     // room to align the base to 1024 bytes, as far as there is any (the kernel checks what it got)
@@ -197,8 +197,8 @@ __global__ void __launch_bounds__(Cfg<D, PAIR>::THREADS, 1)
                 mbar_init(bar_full(s), 1);
                 mbar_init(bar_empty(s), 1);
             }
-            mbar_init(barJoin, 4 * NG);
-            mbar_init(barRead, 4 * NG);
+            mbar_init(barJoin, 8);
+            mbar_init(barRead, 8);
             mbar_init(barDone, 1);
             misc->abort = 0;
             misc->nonfinite = 0;
@@ -413,7 +413,7 @@ __global__ void __launch_bounds__(Cfg<D, PAIR>::THREADS, 1)
         __syncwarp();
     } else if (warp >= 4) {
         // ------------------------------------------------------------ softmax, epilogue
-        const int grp = NG == 2 ? (warp - 4) >> 2 : 0;
+        const int grp = (warp - 4) >> 2;
         const int r = (threadIdx.x - 128) & 127;                  // row of the tile == TMEM lane
         const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
         const float sl2 = p.sl2;
@@ -435,7 +435,7 @@ __global__ void __launch_bounds__(Cfg<D, PAIR>::THREADS, 1)
             const int32_t *parent = p.parent ? p.parent + (size_t)g.b * p.s.T : nullptr;
             float m_used = -INFINITY, l = 0.f;
             bool first = true;
-            for (int j = PAIR || NG == 1 ? 0 : (int)((gs0 ^ (uint32_t)grp) & 1u); j < nk; j += C::STRIDE) {
+            for (int j = grp >= NG ? nk : PAIR || NG == 1 ? 0 : (int)((gs0 ^ (uint32_t)grp) & 1u); j < nk; j += C::STRIDE) {
                 const uint32_t gs = gs0 + j;
                 const uint32_t bi = PAIR ? (uint32_t)grp : gs & 1, ph = PAIR ? gs & 1 : (gs >> 1) & 1;   // S buffer, its phase
                 const uint32_t tS = tmem + lane_off + bi * BN;
@@ -650,6 +650,7 @@ __global__ void __launch_bounds__(Cfg<D, PAIR>::THREADS, 1)
             ok = wait_all(barJoin, seg & 1, S_JOIN);
             if (!ok) break;
             constexpr bool SPLIT = NG == 2 && !PAIR;       // two accumulators of the same rows
+            constexpr bool HALF = !PAIR;                   // each group reads half of the columns
             float f0, f1 = 0.f, L = l, M = m_used;
             if constexpr (SPLIT) {
                 const float2 a = ml[r], b = ml[128 + r];
@@ -662,6 +663,10 @@ __global__ void __launch_bounds__(Cfg<D, PAIR>::THREADS, 1)
                 f0 *= inv;
                 f1 *= inv;
             } else {
+                if constexpr (NG == 1) {
+                    L = ml[r].y;
+                    M = ml[r].x;
+                }
                 f0 = L == 0.f ? 0.f : 1.f / L;
             }
             // the last products: this group's, or both groups' (the segment's last two steps, if it has two)
@@ -679,14 +684,14 @@ __global__ void __launch_bounds__(Cfg<D, PAIR>::THREADS, 1)
             const bool odd = misc->nonfinite == seg + 1;   // rare: non-finite values in the drafted V
             const size_t prow = (size_t)part_slot(blockIdx.x, g.k0) * p.part_rows + urow;
             const size_t orow = ((size_t)(g.b * p.s.Hkv + g.kvh)) * p.s.rows + row;
-            constexpr int COLS = SPLIT ? D / 2 : D;        // columns of this group
+            constexpr int COLS = HALF ? D / 2 : D;         // columns of this group
             const uint32_t tO0 = tmem + lane_off + C::COL_O + (PAIR ? grp * D : 0);
             if (!have0) f0 = 0.f;
             if (!have1) f1 = 0.f;
             if (warp_live) {
                 // 16 columns at a time: the code is fetched anew after the key steps, and its length counts more than the loads'
 #pragma unroll 1
-                for (int c = SPLIT ? grp * COLS : 0, cn = 0; cn < COLS; c += 16, cn += 16) {
+                for (int c = HALF ? grp * COLS : 0, cn = 0; cn < COLS; c += 16, cn += 16) {
                     uint32_t oa[16], ob[16];
                     tmem_ld_x16(tO0 + c, oa);
                     if constexpr (SPLIT) tmem_ld_x16(tO0 + D + c, ob);
@@ -742,7 +747,7 @@ __global__ void __launch_bounds__(Cfg<D, PAIR>::THREADS, 1)
                     __syncwarp();   // the next columns are read by all lanes together
                 }
             }
-            if (live && (!SPLIT || grp == 0)) {
+            if (live && (!HALF || grp == 0)) {
                 const float lse2 = L == 0.f ? -INFINITY : M + lg2_approx(L);
                 if (whole)
                     p.lse[orow] = lse2 * 0.69314718055994531f;
@@ -768,7 +773,7 @@ __global__ void __launch_bounds__(Cfg<D, PAIR>::THREADS, 1)
         const float nan = __uint_as_float(~0u);
         TreeWalk again = const_cast<const Misc *>(misc)->share;
         while (again.next(p.s, g)) {
-            for (int urow = threadIdx.x - 128; urow < p.s.tile; urow += 128 * NG) {
+            for (int urow = threadIdx.x - 128; urow < p.s.tile; urow += 256) {
                 const int row = g.mt * p.s.tile + urow;
                 if (row >= p.s.rows || row % p.s.T >= g.len.t) continue;
                 if (g.k0 == 0 && g.k1 == g.len.nt) {
