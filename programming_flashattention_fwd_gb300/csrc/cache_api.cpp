@@ -199,7 +199,6 @@ int fa_tree_debug(const fa_cache_t *cache, const void *q, const void *k_new, con
     p.part_o = reinterpret_cast<float *>(p.cuts + kMaxCtas);   // a multiple of 32 bytes on
     p.part_lse = p.part_o + (size_t)2 * kMaxCtas * p.part_rows * D;
     p.box_rows = box;
-    p.least = 1;
     p.sl2 = (float)((double)scale * 1.4426950408889634);
     p.timeout_ns = timeout_ns;
     p.inject = inject;
@@ -312,7 +311,6 @@ int fa_weights_debug(const fa_cache_t *cache, const void *q, const float *lse, c
     p.cuts = static_cast<Cut *>(workspace);
     p.part = reinterpret_cast<float *>(p.cuts + kMaxCtas);
     p.box_rows = gcd(cache->page, 128);
-    p.least = 1;
     p.sl2 = (float)((double)scale * 1.4426950408889634);
     p.timeout_ns = timeout_ns;
     p.inject = inject;

@@ -24,7 +24,7 @@ struct Share {
 // CTA `cta`'s share of the line of steps, steps(b) of them in sequence b: one warp adds up the
 // lengths and finds the sequence that holds the share's first step.
 template <typename Steps>
-__device__ __forceinline__ Share find_share(int B, int least, int lane, int cta, int grid, Steps steps)
+__device__ __forceinline__ Share find_share(int B, int lane, int cta, int grid, Steps steps)
 {
     Share s;
     const int head = lane < B ? steps(lane) : 0;   // the first 32 sequences are looked up once
@@ -32,9 +32,10 @@ __device__ __forceinline__ Share find_share(int B, int least, int lane, int cta,
     for (int b = lane + 32; b < B; b += 32) sum += steps(b);
     sum = __reduce_add_sync(~0u, sum);
     s.total = sum;
-    s.G = ctas(sum, grid, least);
-    const int begin = cta < s.G ? cut(sum, s.G, cta) : sum;
-    s.left = cta < s.G ? cut(sum, s.G, cta + 1) - begin : 0;
+    s.G = ctas(sum, grid, 1);
+    const int at = cta + (lane & 1), edge = at < s.G ? cut(sum, s.G, at) : sum;   // both ends of the share at once
+    const int begin = __shfl_sync(~0u, edge, 0);
+    s.left = __shfl_sync(~0u, edge, 1) - begin;
     int before = 0;   // steps of the sequences before s.b
     for (s.b = 0; s.b < B; s.b += 32) {
         const int b = s.b + lane;

@@ -64,7 +64,6 @@ struct TreeParams {
     int q_panel, q_box;      // bytes of a 64-column panel of a query tile in shared memory, and of one copy into it
     int q_bufs;              // query tiles in flight
     int box_rows;            // rows of one copy: gcd(page, 128), at most BN
-    int least;               // steps a CTA takes at least
     float sl2;               // scale * log2 e
     uint64_t timeout_ns;     // limit of a wait (0: the default)
     uint32_t inject;         // fault injection: the first V tile is never loaded (bit 0: in every CTA, bit 1: in CTA 0)
@@ -91,7 +90,6 @@ struct WeighParams {
     float *part;              // [2 * kMaxCtas][256]
     Cut *cuts;                // [kMaxCtas]
     int box_rows;
-    int least;
     float sl2;
     uint64_t timeout_ns;      // limit of a wait (0: the default)
     uint32_t inject;          // fault injection: the first K tile is never loaded (bit 0: in every CTA, bit 1: in CTA 0)

@@ -16,6 +16,17 @@ namespace cache {
 
 // ceil(a / b) for a >= 0, b > 0, a + b below 2^32 (32-bit arithmetic: the walks below run in every role)
 __host__ __device__ __forceinline__ int cdiv(int a, int b) { return (int)(((uint32_t)a + (uint32_t)b - 1u) / (uint32_t)b); }
+// a / b and ceil(a / b) for a >= 0 and a power of two b: a division costs a kernel's start some hundred cycles
+__host__ __device__ __forceinline__ int shift_of(int b)
+{
+#ifdef __CUDA_ARCH__
+    return 31 - __clz(b);
+#else
+    return __builtin_ctz((unsigned)b);
+#endif
+}
+__host__ __device__ __forceinline__ int div2(int a, int b) { return a >> shift_of(b); }
+__host__ __device__ __forceinline__ int cdiv2(int a, int b) { return (int)(((uint32_t)a + (uint32_t)b - 1u) >> shift_of(b)); }
 __host__ __device__ __forceinline__ int clampi(int x, int lo, int hi) { return x < lo ? lo : (x > hi ? hi : x); }
 
 // First step of CTA c when G CTAs share `total` steps (32-bit arithmetic while the product fits: the
@@ -142,7 +153,7 @@ enum WeighMode { kHeads = 0, kRows = 1, kPath = 2 };
 struct WeighShape {
     int B, Hkv, group, T;
     int mode, causal;
-    int NQ;                      // query rows of a step
+    int NQ;                      // query rows of a step, a power of two
     int keys;                    // slots of a key tile: 256 in kHeads mode, else 128
     int capacity;
     const int32_t *seq_len;      // [B]
@@ -165,12 +176,12 @@ __host__ __device__ __forceinline__ WeighLen weigh_len(const WeighShape &s, int 
     l.n = clampi(s.seq_len[b], 0, s.capacity);
     l.a = s.count ? clampi(s.count[b], 0, s.T) : s.T;
     l.off = l.n - l.a;
-    l.kt = cdiv(l.n, s.keys);
+    l.kt = cdiv2(l.n, s.keys);
     l.planes = s.mode == kHeads ? s.group : 1;
     l.rows = l.a == 0 ? 0 : (s.mode == kHeads ? l.a : (s.mode == kPath ? s.group * l.a : s.group * s.T));
-    l.qt = cdiv(l.rows, s.NQ);
-    l.per = s.mode == kHeads && s.causal ? s.keys / s.NQ : 0;
-    l.w = l.off >= 0 ? cdiv(l.off, s.NQ) : -((-l.off) / s.NQ);   // ceil(off / NQ)
+    l.qt = cdiv2(l.rows, s.NQ);
+    l.per = s.mode == kHeads && s.causal ? div2(s.keys, s.NQ) : 0;
+    l.w = l.off >= 0 ? cdiv2(l.off, s.NQ) : -div2(-l.off, s.NQ);   // ceil(off / NQ)
     return l;
 }
 
@@ -193,7 +204,7 @@ __host__ __device__ __forceinline__ int weigh_before(const WeighLen &l, int k)
     if (l.qt == 0) return k;
     long long skipped = 0;
     if (l.per) {
-        const int i0 = l.w <= 0 ? 0 : cdiv(l.w, l.per);   // first key tile with per i >= w
+        const int i0 = l.w <= 0 ? 0 : cdiv2(l.w, l.per);   // first key tile with per i >= w
         if (k > i0) {
             const long long m = k - i0;
             skipped = (long long)l.per * (i0 + (k - 1)) * m / 2 - (long long)l.w * m;
@@ -252,6 +263,7 @@ struct WeighWalk {
         kvh = off / one;
         const int in = off - kvh * one;
         int hi = len.kt - 1;
+        if (!len.per) kt = hi = in / weigh_steps(len, 0);
         while (kt < hi) {   // the key tile that holds step `in` of the head
             const int mid = (kt + hi + 1) / 2;
             if (weigh_before(len, mid) <= in)

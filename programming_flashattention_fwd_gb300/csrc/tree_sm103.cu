@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(Cfg<D, PAIR>::THREADS, 1)
         if (lane < 5) tma_prefetch_map(lane == 0 ? &maps.q : lane == 1 ? &maps.k : lane == 2 ? &maps.v : lane == 3 ? &maps.k_new : &maps.v_new);
     } else if (warp == 3) {
         grid_wait();
-        const Share w = find_share(p.s.B, p.least, lane, blockIdx.x, gridDim.x, [&](int b) { return tree_steps(p.s, b); });
+        const Share w = find_share(p.s.B, lane, blockIdx.x, gridDim.x, [&](int b) { return tree_steps(p.s, b); });
         const TreeWalk mine(p.s, w.b, w.off, w.left);
         total = w.total;
         ctas = w.G;

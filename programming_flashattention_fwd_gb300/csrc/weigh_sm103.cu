@@ -140,19 +140,17 @@ __global__ void __launch_bounds__(THREADS, 1)
         tmem_alloc(smem_u32(const_cast<uint32_t *>(&misc->tmem)), 512);
         tmem_relinquish();
     }
+    int total = 0, ctas = 1;   // (warp 3) all steps, the CTAs that share them
     if (warp == 3) {
         grid_wait();
-        const Share w = find_share(p.s.B, p.least, lane, blockIdx.x, gridDim.x, [&](int b) {
+        const Share w = find_share(p.s.B, lane, blockIdx.x, gridDim.x, [&](int b) {
             const WeighLen l = weigh_len(p.s, b);
             return p.s.Hkv * weigh_before(l, l.kt);
         });
         const WeighWalk mine(p.s, w.b, w.off, w.left);
-        if (lane == 0) {
-            const_cast<Misc *>(misc)->share = mine;
-            Cut c = {};
-            if (w.left > 0) c = Cut{mine.b, mine.kvh, mine.kt, parts_from(w.total, w.G, blockIdx.x, mine.s, weigh_steps(mine.len, mine.kt)), mine.len.n, {}};
-            p.cuts[blockIdx.x] = c;
-        }
+        total = w.total;
+        ctas = w.G;
+        if (lane == 0) const_cast<Misc *>(misc)->share = mine;
     }
     tc_fence_before();
     __syncthreads();
@@ -280,6 +278,11 @@ __global__ void __launch_bounds__(THREADS, 1)
         // ------------------------------------------------------------ rows: lse, limits, gathered queries
         // The two warps take alternate steps, a lane four neighbouring rows; what a tile's rows need is
         // looked up once while consecutive steps use it.
+        if (warp == 3 && lane == 0) {   // for the joining kernel
+            Cut c = {};
+            if (walk.left > 0) c = Cut{walk.b, walk.kvh, walk.kt, parts_from(total, ctas, blockIdx.x, walk.s, weigh_steps(walk.len, walk.kt)), walk.len.n, {}};
+            p.cuts[blockIdx.x] = c;
+        }
         const int half = warp - 2;
         Ring<C::QS> q;
         Ring<NB> st;
@@ -613,19 +616,17 @@ __global__ void __launch_bounds__(Prompt<D>::THREADS, 1)
         tmem_alloc(smem_u32(const_cast<uint32_t *>(&misc->tmem)), 512);
         tmem_relinquish();
     }
+    int total = 0, ctas = 1;   // (warp 3) all steps, the CTAs that share them
     if (warp == 3) {
         grid_wait();
-        const Share w = find_share(p.s.B, p.least, lane, blockIdx.x, gridDim.x, [&](int b) {
+        const Share w = find_share(p.s.B, lane, blockIdx.x, gridDim.x, [&](int b) {
             const WeighLen l = weigh_len(p.s, b);
             return p.s.Hkv * weigh_before(l, l.kt);
         });
         const WeighWalk mine(p.s, w.b, w.off, w.left);
-        if (lane == 0) {
-            const_cast<Misc *>(misc)->share = mine;
-            Cut c = {};
-            if (w.left > 0) c = Cut{mine.b, mine.kvh, mine.kt, parts_from(w.total, w.G, blockIdx.x, mine.s, weigh_steps(mine.len, mine.kt)), mine.len.n, {}};
-            p.cuts[blockIdx.x] = c;
-        }
+        total = w.total;
+        ctas = w.G;
+        if (lane == 0) const_cast<Misc *>(misc)->share = mine;
     }
     tc_fence_before();
     __syncthreads();
@@ -748,6 +749,12 @@ __global__ void __launch_bounds__(Prompt<D>::THREADS, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(r_full(st));
             }
+        }
+        if (warp == 3 && lane == 0) {   // for the joining kernel
+            const WeighWalk own = const_cast<const Misc *>(misc)->share;
+            Cut c = {};
+            if (own.left > 0) c = Cut{own.b, own.kvh, own.kt, parts_from(total, ctas, blockIdx.x, own.s, weigh_steps(own.len, own.kt)), own.len.n, {}};
+            p.cuts[blockIdx.x] = c;
         }
     } else {
         // ------------------------------------------------------------ sums, one thread per key
