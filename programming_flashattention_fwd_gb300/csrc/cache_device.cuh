@@ -112,13 +112,48 @@ __device__ __forceinline__ void page_of(const Pages &pg, int b, int slot, int &p
 // A page that does not exist is given the number past the last, which a tensor map reads as zeros.
 __device__ __forceinline__ int real_page(const Pages &pg, int pid) { return pid < 0 || pid >= pg.num_pages ? pg.num_pages : pid; }
 
-// One box of a pool, (64 columns from x, box rows from `row`, KV head, page), global -> shared.
-__device__ __forceinline__ void load_page(uint32_t dst, const CUtensorMap *m, int x, int row, int kvh, int pid, uint32_t bar)
+// The pages of a sequence's boxes (box_rows slots each, a power of two of them to a key tile), 32 boxes at a time, a box
+// to a lane, and the next 32 on their way: a look-up takes longer than a key tile.
+struct PageRun {
+    int page, row, next_page, next_row;
+
+    __device__ __forceinline__ void look(const Pages &pg, int box_rows, int b, int n, int box, int &p, int &r)
+    {
+        const uint32_t slot = (uint32_t)box * box_rows;
+        p = r = 0;
+        if (slot < (uint32_t)n) page_of(pg, b, (int)slot, p, r);
+        p = real_page(pg, p);
+    }
+    // box `first` is needed next; `start`: the first one of a run
+    __device__ __forceinline__ void at(const Pages &pg, int box_rows, int b, int n, int first, int lane, bool start)
+    {
+        if (start) look(pg, box_rows, b, n, (first & ~31) + lane, page, row);
+        if (!start && (first & 31) == 0) {
+            page = next_page;
+            row = next_row;
+        }
+        if (start || (first & 31) == 0) look(pg, box_rows, b, n, (first & ~31) + 32 + lane, next_page, next_row);
+    }
+};
+
+// The boxes 0 .. valid - 1 of a tile of keys, each of box_rows rows of one page and PANELS panels of 64 columns,
+// global -> shared: lane `from` + i holds box i's page and row in it.  The whole warp calls it and one lane issues.
+template <int PANELS>
+__device__ __forceinline__ void load_boxes(uint32_t dst, uint32_t panel, uint32_t box, const CUtensorMap *m, int kvh, int page, int row, int from,
+                                           int valid, uint32_t bar)
 {
-    asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-                 " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
-                 "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(row), "r"(kvh), "r"(pid), "r"(bar)
-                 : "memory");
+    const uint64_t map = reinterpret_cast<uint64_t>(m);
+#pragma unroll 4
+    for (int i = 0; i < valid; ++i, dst += box) {
+        const int p = __shfl_sync(~0u, page, from + i), r = __shfl_sync(~0u, row, from + i);
+#pragma unroll
+        for (int pn = 0; pn < PANELS; ++pn)
+            asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+                         "@e cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                         " [%0], [%1, {%2, %3, %4, %5}], [%6];\n\t}" ::"r"(dst + pn * panel),
+                         "l"(map), "r"(pn * 64), "r"(r), "r"(kvh), "r"(p), "r"(bar)
+                         : "memory");
+    }
 }
 
 } // namespace cache

@@ -25,9 +25,10 @@
 //
 // Per CTA (one per SM):
 //   warps 0, 3    K and V producers (one warp for both: 5.5 instead of 6.4 TB/s at D = 64, 4.9 instead of
-//                 6.4 with 16-slot pages): per step one TMA box per page and 64-column panel (each lane looks
-//                 up the page of its box, a step ahead), into one ring of NS slots in the order in
-//                 which the products take them (K_0, K_1, V_0, K_2, V_1, ...).  Warp 3 finds the CTA's share first.
+//                 6.4 with 16-slot pages): per step one TMA box per page and 64-column panel, into one ring of NS
+//                 slots in the order in which the products take them (K_0, K_1, V_0, K_2, V_1, ...).  Pages are looked
+//                 up 32 boxes ahead (a step ahead: with 16-slot pages 189 instead of 172 us over 8 x 65536 slots at
+//                 D = 64, 323 instead of 315 at 128).  Warp 3 finds the CTA's share first.
 //   warp 1        TMEM owner and MMA issuer: S = Q K^T, O += P V (tcgen05, fp32 in tensor memory)
 //   warp 2        Q producer
 //   warps 4-7,    softmax, one thread per row, in two groups (one at D = 256) so that one group's softmax
@@ -235,9 +236,7 @@ __global__ void __launch_bounds__(Cfg<D, PAIR>::THREADS, 1)
         // ------------------------------------------------------------ K producer, V producer
         const bool is_v = warp == 3;
         const CUtensorMap *pool = is_v ? &maps.v : &maps.k, *fresh = is_v ? &maps.v_new : &maps.k_new;
-        const int boxes = BN / p.box_rows;            // boxes of a step (one panel)
-        const int box = lane / C::PANELS, pn = lane % C::PANELS;
-        const uint32_t box_off = (uint32_t)(pn * C::KVPANEL + box * p.box_rows * 128);
+        const int boxes = div2(BN, p.box_rows);       // boxes of a step (one panel)
         int use0 = 0, last = 0;                       // the segment's first place in the ring, this warp's last
         uint32_t issued = 0;                          // bit i: place last - i is this warp's
         if (is_v && lane == 0) {   // for the joining kernel
@@ -247,18 +246,12 @@ __global__ void __launch_bounds__(Cfg<D, PAIR>::THREADS, 1)
         }
         bool skip = is_v && ((p.inject & 1u) || ((p.inject & 2u) && blockIdx.x == 0));
         bool ok = true;
-        // the page (and the row in it) of this lane's box of step kt
-        auto look = [&](int kt, int &pid, int &row) {
-            const int slot = kt * BN + box * p.box_rows;
-            if (kt < g.len.kc && box < boxes && slot < g.len.n) page_of(p.pages, g.b, slot, pid, row);
-        };
+        PageRun run;
         while (ok && walk.next(p.s, g)) {
             const int nk = g.k1 - g.k0;
-            int pid = 0, row = 0, pid1 = 0, row1 = 0;
-            look(g.k0, pid, row);
             for (int j = 0; j < nk; ++j) {
                 const int kt = g.k0 + j;
-                look(kt + 1, pid1, row1);   // used in the next round
+                run.at(p.pages, p.box_rows, g.b, g.len.n, kt * boxes, lane, j == 0);
                 // K_0, K_1, V_0, K_2, V_1, ..., V_last
                 const int use = use0 + (is_v ? (j + 1 < nk ? 2 * j + 2 : 2 * j + 1) : (j ? 2 * j - 1 : 0));
                 const uint32_t at = (uint32_t)use % C::NS, bar = bar_full(at), dst = sRing + at * C::KVTILE;
@@ -266,15 +259,13 @@ __global__ void __launch_bounds__(Cfg<D, PAIR>::THREADS, 1)
                 if (!ok) break;
                 if (skip) {
                     skip = false;
-                    pid = pid1;
-                    row = row1;
                     continue;
                 }
                 if (kt < g.len.kc) {
-                    const int valid = min(boxes, cdiv(g.len.n - kt * BN, p.box_rows));
+                    const int valid = min(boxes, cdiv2(g.len.n - kt * BN, p.box_rows));
                     if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(valid * p.box_rows * 128 * C::PANELS));
                     __syncwarp();
-                    if (box < valid) load_page(dst + box_off, pool, pn * 64, row, g.kvh, real_page(p.pages, pid), bar);
+                    load_boxes<C::PANELS>(dst, C::KVPANEL, p.box_rows * 128, pool, g.kvh, run.page, run.row, kt * boxes & 31, valid, bar);
                 } else {
                     if (lane == 0) mbar_arrive_expect_tx(bar, C::KVTILE);
                     __syncwarp();
@@ -283,8 +274,6 @@ __global__ void __launch_bounds__(Cfg<D, PAIR>::THREADS, 1)
                 }
                 issued = (issued << (use - last)) | 1u;
                 last = use;
-                pid = pid1;
-                row = row1;
             }
             use0 += 2 * nk;
         }

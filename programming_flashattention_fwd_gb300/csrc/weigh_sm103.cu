@@ -166,9 +166,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (warp == 0 || warp == 4 + 4 * NB) {
         // ------------------------------------------------------------ K producers, Q producer
         const int who = warp == 0 ? 0 : 1;   // this warp's key tiles: every other one
-        const int boxes = 128 / p.box_rows;
-        const int box = lane / C::PANELS, pn = lane % C::PANELS;
-        const uint32_t box_off = (uint32_t)(pn * C::KPANEL + box * p.box_rows * 128);
+        const int boxes = div2(128, p.box_rows);
         int ku = 0, qu = 0;
         int skip = -1;   // the key tile that a fault injection leaves out
         const bool inject = who == 0 && ((p.inject & 1u) || ((p.inject & 2u) && blockIdx.x == 0));
@@ -177,29 +175,25 @@ __global__ void __launch_bounds__(THREADS, 1)
         bool ok = true;
         while (ok && walk.next_run(p.s, g)) {
             const int units = (g.s + g.steps + g.ns - 1) / g.ns;
-            int pid = 0, row = 0, pid1 = 0, row1 = 0;
-            auto look = [&](int kt, int &pid, int &row) {
-                if (box < boxes && kt * 128 + box * p.box_rows < g.len.n) page_of(p.pages, g.b, kt * 128 + box * p.box_rows, pid, row);
-            };
-            look(g.kt + ((ku ^ who) & 1), pid, row);
+            PageRun run;
+            bool start = true;
             int step = 0;      // steps whose Q tile has been loaded
             for (int u = 0; ok && u < units; ++u, ++ku, k.next()) {
                 const int kt = g.kt + u;
+                run.at(p.pages, p.box_rows, g.b, g.len.n, kt * boxes, lane, start);
+                start = false;
                 if (((ku ^ who) & 1) == 0) {
-                    look(kt + 2, pid1, row1);   // used in this warp's next round
                     ok = wait_all(k_empty(k.at), k.phase ^ 1, S_KEMPTY);
                     if (!ok) break;
-                    const int valid = min(boxes, cdiv(g.len.n - kt * 128, p.box_rows));
+                    const int valid = min(boxes, cdiv2(g.len.n - kt * 128, p.box_rows));
                     if (skip >= 0 || !inject) {
                         if (lane == 0) mbar_arrive_expect_tx(k_full(k.at), (uint32_t)(valid * p.box_rows * 128 * C::PANELS));
                         __syncwarp();
-                        // at most 8 boxes x PANELS: one for each lane at D = 256
-                        if (box < valid) load_page(sb + k.at * C::KTILE + box_off, &maps.k, pn * 64, row, g.kvh, real_page(p.pages, pid), k_full(k.at));
+                        load_boxes<C::PANELS>(sb + k.at * C::KTILE, C::KPANEL, p.box_rows * 128, &maps.k, g.kvh, run.page, run.row, kt * boxes & 31,
+                                              valid, k_full(k.at));
                     } else {
                         skip = ku;
                     }
-                    pid = pid1;
-                    row = row1;
                 }
                 if (gather || who) continue;
                 const int last = min(g.steps, (u + 1) * g.ns - g.s);   // steps up to the end of this key tile
@@ -640,22 +634,19 @@ __global__ void __launch_bounds__(Prompt<D>::THREADS, 1)
 
     if (warp == 0) {
         // ------------------------------------------------------------ K producer, Q producer
-        const int boxes = 256 / p.box_rows;
+        const int boxes = div2(256, p.box_rows);
         const bool inject = (p.inject & 1u) || ((p.inject & 2u) && blockIdx.x == 0);   // the first key tile is left out
         int unit = 0, qu = 0;
         bool ok = true;
         for (; ok && walk.next(p.s, g); ++unit) {
             if (unit) ok = wait_all(barKfree, (unit - 1) & 1, S_KEMPTY);
             if (!ok) break;
-            const int valid = inject && unit == 0 ? 0 : min(boxes, cdiv(g.len.n - g.kt * 256, p.box_rows));
+            const int valid = inject && unit == 0 ? 0 : min(boxes, cdiv2(g.len.n - g.kt * 256, p.box_rows));
             if (lane == 0 && valid > 0) mbar_arrive_expect_tx(barK, (uint32_t)(valid * p.box_rows * 128 * C::PANELS));
             __syncwarp();
-            for (int i = lane; i < valid * C::PANELS; i += 32) {
-                const int box = i / C::PANELS, pn = i % C::PANELS;
-                int pid, row;
-                page_of(p.pages, g.b, g.kt * 256 + box * p.box_rows, pid, row);
-                load_page(sb + (uint32_t)(pn * C::KPANEL + box * p.box_rows * 128), &maps.k, pn * 64, row, g.kvh, real_page(p.pages, pid), barK);
-            }
+            int pid = 0, row = 0;
+            if (lane < valid) page_of(p.pages, g.b, g.kt * 256 + lane * p.box_rows, pid, row);
+            load_boxes<C::PANELS>(sb, C::KPANEL, p.box_rows * 128, &maps.k, g.kvh, real_page(p.pages, pid), row, 0, valid, barK);
             WeighTiles t(g);
             for (int s = g.s0; s < g.s1; ++s, t.next(), ++qu) {
                 ok = wait_all(q_empty(qu), ((qu / C::QS) & 1) ^ 1, S_QEMPTY);
