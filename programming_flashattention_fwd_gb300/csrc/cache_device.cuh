@@ -124,15 +124,16 @@ struct PageRun {
         if (slot < (uint32_t)n) page_of(pg, b, (int)slot, p, r);
         p = real_page(pg, p);
     }
-    // box `first` is needed next; `start`: the first one of a run
-    __device__ __forceinline__ void at(const Pages &pg, int box_rows, int b, int n, int first, int lane, bool start)
+    // box `first` is needed next, of boxes below `end`; `start`: the first one of a run
+    __device__ __forceinline__ void at(const Pages &pg, int box_rows, int b, int n, int first, int end, int lane, bool start)
     {
         if (start) look(pg, box_rows, b, n, (first & ~31) + lane, page, row);
         if (!start && (first & 31) == 0) {
             page = next_page;
             row = next_row;
         }
-        if (start || (first & 31) == 0) look(pg, box_rows, b, n, (first & ~31) + 32 + lane, next_page, next_row);
+        const int next = (first & ~31) + 32;
+        if ((start || (first & 31) == 0) && next < end) look(pg, box_rows, b, n, next + lane, next_page, next_row);
     }
 };
 
@@ -143,7 +144,7 @@ __device__ __forceinline__ void load_boxes(uint32_t dst, uint32_t panel, uint32_
                                            int valid, uint32_t bar)
 {
     const uint64_t map = reinterpret_cast<uint64_t>(m);
-#pragma unroll 4
+#pragma unroll (PANELS == 1 ? 2 : 1)   // short code for the start; D = 64 takes boxes twice as fast
     for (int i = 0; i < valid; ++i, dst += box) {
         const int p = __shfl_sync(~0u, page, from + i), r = __shfl_sync(~0u, row, from + i);
 #pragma unroll

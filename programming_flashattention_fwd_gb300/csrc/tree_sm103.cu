@@ -15,20 +15,20 @@
 // instead of 17 us, 8 x 64 tokens over 16384 138 instead of 102.)
 //
 // Measured, 8 sequences, 32 heads over 8 KV heads, bf16, of 6.8 TB/s copied:
-//     D = 64, 131072 slots    one token 6.8 TB/s, 32 tokens 6.3     D = 256, 65536 slots   7.2, 6.9
-//     D = 128, 131072 slots   one token 6.8 TB/s (16-slot pages 6.7), 32 tokens 6.8, 64 tokens (256 rows,
-//                             where the softmax is as busy as memory) 5.6
+//     D = 64, 131072 slots    one token 6.8 TB/s, 32 tokens 6.7     D = 256, 65536 slots   7.2, 7.0
+//     D = 128, 131072 slots   one token 7.0 TB/s (16-slot pages too), 32 tokens 6.9, 64 tokens (256 rows,
+//                             where the softmax is as busy as memory) 6.0
 // Short calls are a chain of latencies (start, one unit, second kernel): one sequence, one token, 10 us
 // over 16 slots and 11 over 4096.  So are many short units, about 3 us each of an SM's time, which
-// the reads of the next one only partly cover: 64 x 128 slots 23 us, 64 x 512 38 (3.5 TB/s), 64 x 1024 53 (5.1), 64 x
-// 4096 171 (6.3).
+// the reads of the next one only partly cover: 64 x 128 slots 23 us, 64 x 512 39 (3.4 TB/s), 64 x 1024 52 (5.1), 64 x
+// 4096 169 (6.4).
 //
 // Per CTA (one per SM):
 //   warps 0, 3    K and V producers (one warp for both: 5.5 instead of 6.4 TB/s at D = 64, 4.9 instead of
 //                 6.4 with 16-slot pages): per step one TMA box per page and 64-column panel, into one ring of NS
 //                 slots in the order in which the products take them (K_0, K_1, V_0, K_2, V_1, ...).  Pages are looked
-//                 up 32 boxes ahead (a step ahead: with 16-slot pages 189 instead of 172 us over 8 x 65536 slots at
-//                 D = 64, 323 instead of 315 at 128).  Warp 3 finds the CTA's share first.
+//                 up 32 boxes ahead (a step ahead: with 16-slot pages 189 instead of 179 us over 8 x 65536 slots at
+//                 D = 64, 323 instead of 314 at 128).  Warp 3 finds the CTA's share first.
 //   warp 1        TMEM owner and MMA issuer: S = Q K^T, O += P V (tcgen05, fp32 in tensor memory)
 //   warp 2        Q producer
 //   warps 4-7,    softmax, one thread per row, in two groups (one at D = 256) so that one group's softmax
@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(Cfg<D, PAIR>::THREADS, 1)
             const int nk = g.k1 - g.k0;
             for (int j = 0; j < nk; ++j) {
                 const int kt = g.k0 + j;
-                run.at(p.pages, p.box_rows, g.b, g.len.n, kt * boxes, lane, j == 0);
+                run.at(p.pages, p.box_rows, g.b, g.len.n, kt * boxes, g.k1 * boxes, lane, j == 0);
                 // K_0, K_1, V_0, K_2, V_1, ..., V_last
                 const int use = use0 + (is_v ? (j + 1 < nk ? 2 * j + 2 : 2 * j + 1) : (j ? 2 * j - 1 : 0));
                 const uint32_t at = (uint32_t)use % C::NS, bar = bar_full(at), dst = sRing + at * C::KVTILE;

@@ -15,10 +15,10 @@
 // a drafting step by the one read of K.
 //
 // Measured, 32 heads over 8 KV heads, bf16:
-//     16 rows a head over 4 x 131072 slots    D = 64 5.7 TB/s (100 us), D = 128 6.3 (175 us; 16-slot pages 6.2),
-//                                             D = 256 6.7 (326 us); one token over 64 x 1024 slots 4.4 (32 us)
-//     a prompt over itself, causal            8192 tokens: D = 64 205 us, D = 128 208 us (1320 TFLOP/s), D = 256
-//                                             344 us (1600); 2048 tokens, D = 128: 28 us; 16384: 765 us (1440)
+//     16 rows a head over 4 x 131072 slots    D = 64 5.8 TB/s (98 us; 16-slot pages 4.3), D = 128 6.4 (172 us; 6.3),
+//                                             D = 256 6.8 (321 us; 6.5); one token over 64 x 1024 slots 4.5 (31 us)
+//     a prompt over itself, causal            8192 tokens: D = 64 204 us, D = 128 208 us (1320 TFLOP/s), D = 256
+//                                             344 us (1600); 2048 tokens, D = 128: 26 us; 16384: 770 us (1430)
 //     few rows over a short cache             8 to 10 us: start, one tile, second kernel
 // D = 64 has as many exponentials as D = 128 for half the products, and is bound by them.
 //
@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             int step = 0;      // steps whose Q tile has been loaded
             for (int u = 0; ok && u < units; ++u, ++ku, k.next()) {
                 const int kt = g.kt + u;
-                run.at(p.pages, p.box_rows, g.b, g.len.n, kt * boxes, lane, start);
+                run.at(p.pages, p.box_rows, g.b, g.len.n, kt * boxes, (g.kt + units) * boxes, lane, start);
                 start = false;
                 if (((ku ^ who) & 1) == 0) {
                     ok = wait_all(k_empty(k.at), k.phase ^ 1, S_KEMPTY);
