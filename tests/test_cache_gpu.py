@@ -130,6 +130,16 @@ def test_tree_pages(fa, page):
     run_tree(fa, "bf16", 4, 2, 128, [page - 1, 300, 2 * page, page + 1], [5, 4, 5, 1], 5, page, seed=page)
 
 
+MANY_PAGES = [(64, 16), (128, 16), (128, 48), (256, 16), (64, 80)]
+
+
+@pytest.mark.parametrize("D,page", MANY_PAGES)
+def test_tree_many_small_pages(fa, D, page):
+    """A CTA's run of keys takes more pages than are looked up at a time, from any place in a group of them."""
+    lens = [1000 + 53 * i for i in range(20)]
+    run_tree(fa, "bf16", 8, 8, D, lens, [1 + i % 2 for i in range(20)], 2, page, seed=D + page)
+
+
 @pytest.mark.parametrize("D", [64, 128, 256])
 def test_tree_dense_cache(fa, D):
     run_tree(fa, "fp16", 4, 2, D, [100, 161, 0], [3, 2, 3], 3, 176, dense=True)
@@ -344,6 +354,13 @@ def test_weights_of_many_accepted_tokens(fa):
     """More gathered rows than one tile holds, and a row that counts twice."""
     T = 70
     run_weights(fa, "bf16", 8, 2, 128, [300, 200], [70, 40], T, 16, path=[list(range(T)), [0, 0] + list(range(1, T - 1))])
+
+
+@pytest.mark.parametrize("D,page", MANY_PAGES)
+@pytest.mark.parametrize("with_path", [False, True])
+def test_weights_many_small_pages(fa, D, page, with_path):
+    lens = [1000 + 53 * i for i in range(20)]
+    run_weights(fa, "bf16", 8, 8, D, lens, [2] * 20, 2, page, path=[[1, 0]] * 20 if with_path else None, seed=D + page)
 
 
 @pytest.mark.parametrize("D", [64, 128, 256])
