@@ -116,9 +116,8 @@ _capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", torch.cuda.is_c
 
 
 def _kept(index: int, current: Optional[int]) -> Optional[dict]:
-    """What this thread keeps for the current stream, whose calls run one after another: its workspace and
-    a stock of small results.  None where a call is to have its own: on another device than the current one, or
-    captured into a graph."""
+    """What this thread keeps for the current stream, whose calls run one after another: its workspace.  None
+    where a call is to have its own: on another device than the current one, or captured into a graph."""
     if current is None or _capturing():
         return None
     kept, key = _local.__dict__, (index, current)
@@ -142,17 +141,6 @@ def _workspace(need: int, given: Optional[torch.Tensor], like: torch.Tensor, kep
         return ws
     t = torch.empty(need, dtype=torch.uint8, device=like.device)
     return t, t.data_ptr(), need
-
-
-def _lengths(B: int, device: torch.device, kept) -> torch.Tensor:
-    """A new [B] int32 tensor.  From a stock of 64 that are made together: an allocation of its own is about a
-    third of what an eviction's call costs the host."""
-    if kept is None:
-        return torch.empty(B, dtype=_I32, device=device)
-    stock = kept.get(B)
-    if not stock:
-        stock = kept[B] = list(torch.empty((64, B), dtype=_I32, device=device).unbind(0))
-    return stock.pop()
 
 
 class KVCache:
@@ -324,7 +312,8 @@ def cache_evict(cache: KVCache, weight, pos, keep: int, first: int = 0, last: in
     and from next_pos[b] - last on are kept, then the slots of the largest weight (ties: the lowest slot);
     kept slots at or above `keep` move to the freed ones below.  weight [B, Hkv, capacity] float32 and
     pos int32 follow the slots, in place unless weight_out and pos_out are given.  Returns new_len [B]
-    int32 = min(seq_len, keep); seq_len itself is not changed."""
+    int32 = min(seq_len, keep), a tensor of its own unless one is given (which saves the host an allocation);
+    seq_len itself is not changed."""
     if stream is not None:
         return _on(stream, cache, cache_evict, cache, weight, pos, keep, first, last, next_pos, weight_out, pos_out, new_len,
                    workspace)
@@ -344,7 +333,7 @@ def cache_evict(cache: KVCache, weight, pos, keep: int, first: int = 0, last: in
     current = _current(i)
     kept = _kept(i, current)
     if new_len is None:
-        new_len = _lengths(B, cache.device, kept)
+        new_len = torch.empty(B, dtype=_I32, device=cache.device)
     ws, at, size = _workspace(evict_workspace_bytes(B, cache.Hkv, cache.capacity, keep), workspace, cache.k, kept)
     _launch(lib.fa_cache_evict, i, current,
             (cache._c, w, p, wo, po, new_len.data_ptr(), nxt, keep, first, last, at, size))

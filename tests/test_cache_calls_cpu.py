@@ -1,0 +1,47 @@
+"""Calls of the cache operators as a user's program makes them, as far as they go without a GPU: what a call returns
+and what it does with the tensors that it is given."""
+import io
+
+import pytest
+import torch
+
+from programming_flashattention_fwd_gb300 import cache as fc
+from test_cache_cpu import FakeCuda, lib, make_cache, on  # noqa: F401
+
+
+@pytest.fixture
+def host(monkeypatch):
+    """The binding with the launch left out and its allocations on the host."""
+    calls = []
+    monkeypatch.setattr(fc, "_launch", lambda fn, index, current, args: calls.append(args))
+    monkeypatch.setattr(fc, "_current", lambda index: 5)
+    monkeypatch.setattr(fc, "_capturing", lambda: False)
+    monkeypatch.setattr(fc, "_workspace", lambda *a: (None, 0, 0))
+    monkeypatch.setattr(fc.KVCache, "device", property(lambda self: torch.device("cpu")))
+    return calls
+
+
+def evict(cache):
+    return fc.cache_evict(cache, on((2, 2, 48), torch.float32), on((2, 2, 48), torch.int32), 20)
+
+
+def test_new_lengths_are_ordinary_tensors(host, lib):  # noqa: F811
+    """The lengths that an eviction returns have nothing in common with those of other calls: not the mode that
+    another call ran under, not a version counter, not storage."""
+    cache = make_cache()
+    with torch.inference_mode():
+        inner = evict(cache)
+    assert inner.is_inference()
+    a, b = evict(cache), evict(cache)
+    assert not a.is_inference() and not b.is_inference()
+    a.fill_(1).add_(1)                                           # an inference tensor cannot be changed here
+    x = torch.ones(4, requires_grad=True)
+    y = (x[b.fill_(0).long()] * 2).sum() + x.index_select(0, b).sum()
+    a.add_(1)                                                    # b is saved as an index: its counter must not move
+    y.backward()
+    assert torch.equal(x.grad, torch.tensor([6.0, 0, 0, 0]))
+    f = io.BytesIO()
+    torch.save(b, f)
+    alone = io.BytesIO()
+    torch.save(b.clone(), alone)
+    assert len(f.getvalue()) == len(alone.getvalue()) and b.untyped_storage().nbytes() == 8
