@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import operator
 import struct
 import threading
 from typing import Optional, Tuple
@@ -143,6 +144,15 @@ def _workspace(need: int, given: Optional[torch.Tensor], like: torch.Tensor, kep
     return t, t.data_ptr(), need
 
 
+def _fixed(name: str) -> property:
+    """A tensor of a KVCache, whose address the cache's calls pass on: another one in its place would not be seen by
+    them, so only the same one may be assigned (which is what `cache.seq_len += count` does after it has added)."""
+    def assign(self, t):
+        if t is not getattr(self, "_" + name):
+            raise AttributeError(f"a KVCache keeps the {name} that it was made with: change that in place, or make another KVCache")
+    return property(operator.attrgetter("_" + name), assign)
+
+
 class KVCache:
     """The keys and values of B sequences in pages (fa_cache_t).
 
@@ -151,9 +161,11 @@ class KVCache:
     table    [B, max_pages] int32: the page of each run of `page` slots; None for a dense cache,
              whose pages belong to the sequences in order (num_pages // B each)
 
-    Holds references to the tensors and no state of its own: update seq_len and table in place.
+    Holds references to the tensors and no state of its own: update seq_len and table in place (another tensor in
+    their place is refused).
     """
-    __slots__ = ("k", "v", "seq_len", "table", "index", "dtype", "B", "Hkv", "D", "page", "capacity", "_c")
+    __slots__ = ("_k", "_v", "_seq_len", "_table", "index", "dtype", "B", "Hkv", "D", "page", "capacity", "_c")
+    k, v, seq_len, table = (_fixed(name) for name in ("k", "v", "seq_len", "table"))
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, seq_len: torch.Tensor, table: Optional[torch.Tensor] = None):
         if not isinstance(k, torch.Tensor) or k.dim() != 4:
@@ -181,13 +193,13 @@ class KVCache:
             raise ValueError("k must be contiguous")
         self._c = _PACK(k.data_ptr(), _need("v", v, shape, dt, index), at,
                         _need("seq_len", seq_len, (B,), _I32, index), B, Hkv, D, page, per, num, code)
-        self.k, self.v, self.seq_len, self.table = k, v, seq_len, table
+        self._k, self._v, self._seq_len, self._table = k, v, seq_len, table
         self.index, self.dtype, self.B, self.Hkv, self.D, self.page = index, dt, B, Hkv, D, page
         self.capacity = per * page
 
     @property
     def device(self) -> torch.device:
-        return self.k.device
+        return self._k.device
 
 
 @functools.lru_cache(maxsize=256)

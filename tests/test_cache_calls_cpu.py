@@ -45,3 +45,17 @@ def test_new_lengths_are_ordinary_tensors(host, lib):  # noqa: F811
     alone = io.BytesIO()
     torch.save(b.clone(), alone)
     assert len(f.getvalue()) == len(alone.getvalue()) and b.untyped_storage().nbytes() == 8
+
+
+@pytest.mark.parametrize("name", ["k", "v", "seq_len", "table"])
+def test_a_cache_keeps_its_tensors(name):
+    """A tensor assigned in the place of one that the cache was made with would be passed over in silence: refused.
+    What is changed in place is what the calls see, whichever way it is written."""
+    cache = make_cache()
+    before = getattr(cache, name)
+    with pytest.raises(AttributeError, match=name):
+        setattr(cache, name, before.clone())
+    assert getattr(cache, name) is before
+    cache.seq_len += 3
+    assert cache.seq_len.tolist() == [3, 3] and fc._PACK(cache.k.data_ptr(), cache.v.data_ptr(), cache.table.data_ptr(),
+                                                         cache.seq_len.data_ptr(), 2, 2, 64, 16, 3, 6, 0) == cache._c
