@@ -349,7 +349,9 @@ int fa_cache_weights(const fa_cache_t *cache, const void *q, const float *lse, c
  *   weight, pos           [B, Hkv, capacity] float32, int32
  *   weight_out, pos_out   the same for the slots kept, [0, min(seq_len[b], keep)); may be weight and pos.
  *                         Other slots are left as they were
- *   new_len               [B]: min(seq_len[b], keep).  Not seq_len itself (the layers of a model share it)
+ *   new_len               [B]: min(seq_len[b], keep).  Not seq_len itself: the layers of a model share it, and one that
+ *                         found it shortened would evict nothing and lose the slots behind.  The caller copies new_len
+ *                         into it after the last layer
  *   next_pos              [B] the position of the next token; required when last > 0
  *   keep >= 1, first, last >= 0, first + last <= keep
  *   workspace             fa_evict_workspace_bytes(B, Hkv, capacity, keep) bytes, 8-byte aligned

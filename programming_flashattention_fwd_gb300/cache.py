@@ -289,7 +289,8 @@ def cache_weights(cache: KVCache, q, lse, weight=None, path=None, count=None, ca
     q [B, Hq, T, D], lse [B, Hq, T] as the attention left it; path [B, T] and count [B] int32 as in
     ``cache_append`` (the accepted rows); causal: row i is the query of slot seq_len[b] - count[b] + i
     and sees the slots up to its own.  weight [B, Hkv, capacity] float32 (None: zeros) is added to; the
-    result is written to out, which defaults to weight itself (without a weight, to a new tensor of zeros)."""
+    result is written to out, which defaults to weight itself (without a weight, to a new tensor of zeros).  For
+    accepted tokens it follows their append in every layer and seq_len += count."""
     if stream is not None:
         return _on(stream, cache, cache_weights, cache, q, lse, weight, path, count, causal, scale, out, workspace)
     shape = _queries(q, cache)
@@ -325,7 +326,8 @@ def cache_evict(cache: KVCache, weight, pos, keep: int, first: int = 0, last: in
     kept slots at or above `keep` move to the freed ones below.  weight [B, Hkv, capacity] float32 and
     pos int32 follow the slots, in place unless weight_out and pos_out are given.  Returns new_len [B]
     int32 = min(seq_len, keep), a tensor of its own unless one is given (which saves the host an allocation);
-    seq_len itself is not changed."""
+    seq_len itself is not changed: the layers of a model share it, and one that found it shortened would evict
+    nothing and lose the slots behind.  Copy new_len into it after the last layer."""
     if stream is not None:
         return _on(stream, cache, cache_evict, cache, weight, pos, keep, first, last, next_pos, weight_out, pos_out, new_len,
                    workspace)
