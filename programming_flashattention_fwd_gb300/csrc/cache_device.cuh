@@ -11,7 +11,9 @@ namespace fa {
 namespace cache {
 
 // Waits for the end of the kernels that this one may overlap (launch_overlapped): before the first access to
-// memory that they may write, and before the first write that they may read or overwrite.
+// memory that they may write, and before the first write that they may read or overwrite.  What they have written is
+// read by ordinary loads: a non-coherent one is for data that nobody writes while the reading kernel runs, and
+// this kernel runs since before those have ended.
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 // From here on the next kernel may be scheduled, once every CTA has come this far.
 __device__ __forceinline__ void grid_done_soon() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
@@ -106,7 +108,7 @@ __device__ __forceinline__ void page_of(const Pages &pg, int b, int slot, int &p
 {
     const int at = slot / pg.page;
     row = slot - at * pg.page;
-    pid = pg.table ? __ldg(pg.table + (size_t)b * pg.max_pages + at) : b * pg.max_pages + at;
+    pid = pg.table ? pg.table[(size_t)b * pg.max_pages + at] : b * pg.max_pages + at;
 }
 
 // A page that does not exist is given the number past the last, which a tensor map reads as zeros.

@@ -17,7 +17,7 @@ __device__ __forceinline__ long long row_of(const Pages &pg, int Hkv, int b, int
 {
     const int at = slot / pg.page;
     if (slot < 0 || at >= pg.max_pages) return -1;
-    const int pid = pg.table ? __ldg(pg.table + (size_t)b * pg.max_pages + at) : b * pg.max_pages + at;
+    const int pid = pg.table ? pg.table[(size_t)b * pg.max_pages + at] : b * pg.max_pages + at;
     if (pid < 0 || pid >= pg.num_pages) return -1;
     return ((long long)pid * Hkv + h) * pg.page + (slot - at * pg.page);
 }
@@ -37,23 +37,24 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
     const int head = blockIdx.x / p.blocks_per_head, tile = blockIdx.x - head * p.blocks_per_head;
     const int b = head / p.Hkv, h = head - b * p.Hkv;
     const int i = tile * (kAppendThreads / p.chunks) + threadIdx.x / p.chunks, ch = threadIdx.x % p.chunks;
-    const int count = p.count ? min(__ldg(p.count + b), p.T) : p.T;
+    const int count = p.count ? min(p.count[b], p.T) : p.T;
     if (i >= count) return;
-    const int src = p.path ? __ldg(p.path + (size_t)b * p.T + i) : i;
+    const int src = p.path ? p.path[(size_t)b * p.T + i] : i;
     if (src < 0 || src >= p.T) return;
-    const long long slot = (long long)max(__ldg(p.seq_len + b), 0) + i;
+    const long long slot = (long long)max(p.seq_len[b], 0) + i;
     if (slot >= p.capacity) return;
+    const int start = p.pos ? p.start[b] : 0;
     const long long row = row_of(p.pages, p.Hkv, b, h, (int)slot);
     if (row >= 0) {
         const size_t from = ((size_t)head * p.T + src) * p.chunks + ch, to = (size_t)row * p.chunks + ch;
-        const uint4 k = __ldg(p.k_new + from), v = __ldg(p.v_new + from);
+        const uint4 k = p.k_new[from], v = p.v_new[from];
         p.k[to] = k;
         p.v[to] = v;
     }
     if (ch == 0) {
         const size_t at = (size_t)head * p.capacity + (size_t)slot;
         if (p.weight) p.weight[at] = 0.f;
-        if (p.pos) p.pos[at] = __ldg(p.start + b) + i;
+        if (p.pos) p.pos[at] = start + i;
     }
 }
 
@@ -146,8 +147,8 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const __grid_co
     const int C = cluster_size(), rank = cluster_rank();
     const int head = blockIdx.x / C, b = head / p.Hkv, h = head - b * p.Hkv;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int next_pos = p.last > 0 ? __ldg(p.next_pos + b) : 0;
-    const int n = min(max(__ldg(p.seq_len + b), 0), p.capacity), m = p.keep;
+    const int next_pos = p.last > 0 ? p.next_pos[b] : 0;
+    const int n = min(max(p.seq_len[b], 0), p.capacity), m = p.keep;
     const size_t base = (size_t)head * p.capacity;
     if (h == 0 && rank == 0 && tid == 0) p.new_len[b] = min(n, m);
     const bool copy_w = p.weight_out != p.weight, copy_p = p.pos_out != p.pos;
@@ -177,14 +178,14 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const __grid_co
         if (i < p.paged)
             pid = pages[i];
         else
-            pid = p.pages.table ? __ldg(p.pages.table + (size_t)b * p.pages.max_pages + at) : b * p.pages.max_pages + at;
+            pid = p.pages.table ? p.pages.table[(size_t)b * p.pages.max_pages + at] : b * p.pages.max_pages + at;
         if (pid < 0 || pid >= p.pages.num_pages) return kNoRow;
         return ((uint32_t)pid * p.Hkv + h) * p.pages.page + (s - at * p.pages.page);
     };
 
     for (int i = tid; i < kBins; i += kEvictThreads) hist[i] = 0;
     for (int i = tid; i < p.paged && (page0 + i) * p.pages.page < hi; i += kEvictThreads)
-        pages[i] = p.pages.table ? __ldg(p.pages.table + (size_t)b * p.pages.max_pages + page0 + i) : b * p.pages.max_pages + page0 + i;
+        pages[i] = p.pages.table ? p.pages.table[(size_t)b * p.pages.max_pages + page0 + i] : b * p.pages.max_pages + page0 + i;
     if (tid == 0) cta_match = 0;
     __syncthreads();
     // every slot once: its key, the first histogram (11 bits), and, where the results go elsewhere, a copy of

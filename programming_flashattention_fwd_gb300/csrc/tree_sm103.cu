@@ -145,7 +145,7 @@ __device__ __forceinline__ void path_bits(const int32_t *parent, int t, int lo, 
 #pragma unroll
         for (int w = 0; w < W; ++w)
             if ((i >> 5) == w) bits[w] |= 1u << (i & 31);
-        const int up = __ldg(parent + j);
+        const int up = parent[j];
         if (up >= j) break;
         j = up;
     }
@@ -709,7 +709,7 @@ __global__ void __launch_bounds__(Cfg<D, PAIR>::THREADS, 1)
                                                     ((size_t)(g.b * p.s.Hkv + g.kvh) * p.s.T + key) * D + c;
 #pragma unroll
                                 for (int e = 0; e < 16; ++e) {
-                                    const float x = half_to_float<BF16>(__ldg(v + e));
+                                    const float x = half_to_float<BF16>(v[e]);
                                     if (!isfinite(x)) h[e] += x;
                                 }
                             }

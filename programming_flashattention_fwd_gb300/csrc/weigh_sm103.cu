@@ -296,15 +296,24 @@ __global__ void __launch_bounds__(THREADS, 1)
                     const uint32_t dst = sQ + q.at * C::QTILE;
                     // rows to the next multiple of 16; 16-byte chunk c of row r at c ^ (r & 7) of its 128 bytes
                     const int rows = min(NQ, max(16, (g.len.rows - row0 + 15) & ~15));
-                    for (int x = threadIdx.x - 64; x < rows * (D / 8); x += 64) {
-                        const int r = x / (D / 8), ch = x % (D / 8), row = row0 + r;
-                        uint4 v = make_uint4(0, 0, 0, 0);
-                        if (row < g.len.rows) {
-                            const int h = row / g.len.a, t = __ldg(path + (row - h * g.len.a));
-                            if (t >= 0 && t < p.s.T)
-                                v = __ldg(reinterpret_cast<const uint4 *>(p.q) + ((head0 + h) * p.s.T + t) * (D / 8) + ch);
+                    // (four of a thread's chunks are read before the first is stored)
+                    const int all = rows * (D / 8);
+                    for (int x0 = threadIdx.x - 64; x0 < all; x0 += 4 * 64) {
+                        uint4 v[4];
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) {
+                            const int x = x0 + 64 * u, row = row0 + x / (D / 8);
+                            v[u] = make_uint4(0, 0, 0, 0);
+                            if (x < all && row < g.len.rows) {
+                                const int h = row / g.len.a, t = path[row - h * g.len.a];
+                                if (t >= 0 && t < p.s.T) v[u] = static_cast<const uint4 *>(p.q)[((head0 + h) * p.s.T + t) * (D / 8) + x % (D / 8)];
+                            }
                         }
-                        st_shared_v4(dst + (ch >> 3) * C::QPANEL + r * 128 + (((ch & 7) ^ (r & 7)) << 4), v.x, v.y, v.z, v.w);
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) {
+                            const int x = x0 + 64 * u, r = x / (D / 8), ch = x % (D / 8);
+                            if (x < all) st_shared_v4(dst + (ch >> 3) * C::QPANEL + r * 128 + (((ch & 7) ^ (r & 7)) << 4), v[u].x, v[u].y, v[u].z, v[u].w);
+                        }
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
@@ -324,13 +333,13 @@ __global__ void __launch_bounds__(THREADS, 1)
                             const int len = gather ? g.len.a : p.s.T;
                             h = row / len;
                             order = t = row - h * len;
-                            if (gather) t = __ldg(path + order);
+                            if (gather) t = path[order];
                             if (order >= g.len.a || t < 0 || t >= p.s.T) order = -1;
                         }
                         limit[e] = 0;
                         neg[e] = 0.f;
                         if (order >= 0) {
-                            const float v = __ldg(p.lse + (head0 + h) * p.s.T + t);
+                            const float v = p.lse[(head0 + h) * p.s.T + t];
                             neg[e] = v * -1.4426950408889634f;
                             // a row that saw nothing gave nothing
                             limit[e] = v == -INFINITY ? 0 : (p.s.causal ? clampi(g.len.off + order + 1, 0, g.len.n) : g.len.n);
@@ -723,7 +732,7 @@ __global__ void __launch_bounds__(Prompt<D>::THREADS, 1)
                     neg[e] = 0.f;
                     limit[e] = 0;
                     if (c < NQ && i < g.len.a) {
-                        const float v = __ldg(p.lse + (head0 + t.plane) * p.s.T + i);
+                        const float v = p.lse[(head0 + t.plane) * p.s.T + i];
                         neg[e] = v * -1.4426950408889634f;
                         // a row that saw nothing gave nothing
                         limit[e] = v == -INFINITY ? 0 : (p.s.causal ? clampi(g.len.off + i + 1, 0, g.len.n) : g.len.n);

@@ -1,10 +1,13 @@
 """Calls of the cache operators as a user's program makes them, as far as they go without a GPU: what a call returns
 and what it does with the tensors that it is given."""
 import io
+import os
+import re
 
 import pytest
 import torch
 
+from programming_flashattention_fwd_gb300 import build as fa_build
 from programming_flashattention_fwd_gb300 import cache as fc
 from test_cache_cpu import FakeCuda, lib, make_cache, on  # noqa: F401
 
@@ -59,3 +62,12 @@ def test_a_cache_keeps_its_tensors(name):
     cache.seq_len += 3
     assert cache.seq_len.tolist() == [3, 3] and fc._PACK(cache.k.data_ptr(), cache.v.data_ptr(), cache.table.data_ptr(),
                                                          cache.seq_len.data_ptr(), 2, 2, 64, 16, 3, 6, 0) == cache._c
+
+
+@pytest.mark.parametrize("name", ["cache_device.cuh", "cache_schedule.h", "cache_sm103.cu", "tree_sm103.cu", "weigh_sm103.cu"])
+def test_overlapped_kernels_load_coherently(name):
+    """The cache kernels run while the kernel before them ends.  A non-coherent load asks for data that nobody writes
+    while the kernel that reads it runs, which what that kernel leaves behind is not."""
+    with open(os.path.join(fa_build.CSRC, name)) as f:
+        code = re.sub(r"//.*", "", f.read())
+    assert not re.search(r"__ldg|\.nc\b|__restrict__", code)

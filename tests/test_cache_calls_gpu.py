@@ -53,3 +53,90 @@ def test_the_readme_s_loop(fa):  # noqa: F811
         assert all((moved[x] != b["pos"][x]).any() for x in range(B))
         for x in ("k", "v", "weight", "pos"):
             assert torch.equal(a[x], b[x]), x
+
+
+def test_calls_with_nothing_between(fa):  # noqa: F811
+    """Attention, its weights (causal=False: before the append) and an eviction by them, one behind the other, so that each
+    starts while the one before ends and reads what that one writes: lse, weights, rows.  New queries every time, in the
+    same buffers, against the same calls with a wait behind each."""
+    g = torch.Generator().manual_seed(120)
+    B, Hq, Hkv, D, T, page, n, keep = 8, 8, 2, 128, 6, 64, 700, 650
+    per = -(-(n + T) // page)
+    table = ints(torch.randperm(B * per, generator=g).reshape(B, per))
+    a = layer(g, B, Hq, Hkv, D, T, B * per, page, per * page)
+    b = {x: t.clone() for x, t in a.items()}
+    path, count = ints([[0, 2, 3, -1, -1, -1]] * B), ints([3] * B)
+
+    def step(c, wait):
+        cache = c["cache"]
+        fa.tree_attention(c["q"], c["kn"], c["vn"], cache, o=c["o"], lse=c["lse"])
+        wait()
+        fa.cache_weights(cache, c["q"], c["lse"], c["weight"], path=path, count=count, causal=False)
+        wait()
+        fa.cache_evict(cache, c["weight"], c["pos"], keep, first=2, last=20, next_pos=c["next"], new_len=c["seq"])
+        wait()
+        fa.tree_attention(c["q"], c["kn"], c["vn"], cache, o=c["o2"], lse=c["lse2"])
+        wait()
+        fa.cache_append(cache, c["kn"], c["vn"], path=path, count=count, weight=c["weight"], pos=c["pos"], start=c["next"])
+        wait()
+        return [c[x] for x in ("o", "lse", "weight", "pos", "k", "v", "o2", "lse2", "seq")]
+
+    for c in (a, b):
+        c.update(seq=ints([n] * B), next=ints([n] * B), o=torch.zeros_like(c["q"]), lse=torch.zeros(B, Hq, T, device="cuda"))
+        c.update(o2=torch.zeros_like(c["q"]), lse2=torch.zeros_like(c["lse"]), len=ints([n] * B))
+        c["cache"] = fa.KVCache(c["k"], c["v"], c["len"], table)
+    for _ in range(12):
+        q = normal(g, tuple(a["q"].shape), "bf16").cuda()
+        for c in (a, b):
+            c["q"].copy_(q)
+            c["len"].fill_(n)
+        torch.cuda.synchronize()
+        got = step(a, lambda: None)
+        want = step(b, torch.cuda.synchronize)
+        torch.cuda.synchronize()
+        for i, (x, y) in enumerate(zip(got, want)):
+            assert torch.equal(x, y), i
+        assert a["seq"].tolist() == [keep] * B
+
+
+def test_a_forked_capture(fa):  # noqa: F811
+    """Two layers' attention on two streams of one capture, joined before what reads both; replayed with new queries."""
+    g = torch.Generator().manual_seed(130)
+    B, Hq, Hkv, D, T, page, n = 2, 8, 2, 64, 4, 32, 500
+    per = -(-n // page)
+    table = ints(torch.randperm(B * per, generator=g).reshape(B, per))
+    layers = [layer(g, B, Hq, Hkv, D, T, B * per, page, per * page) for _ in range(2)]
+    seq = ints([n, n - 37])
+    caches = [fa.KVCache(c["k"], c["v"], seq, table) for c in layers]
+
+    def calls(fork):
+        main, other, out = torch.cuda.current_stream(), torch.cuda.Stream() if fork else torch.cuda.current_stream(), []
+        if fork:
+            other.wait_stream(main)
+        for s, c, cache in zip((main, other), layers, caches):
+            with torch.cuda.stream(s):
+                out += fa.tree_attention(c["q"], c["kn"], c["vn"], cache)
+        if fork:
+            main.wait_stream(other)
+        for i, (c, cache) in enumerate(zip(layers, caches)):
+            out.append(fa.cache_weights(cache, c["q"], out[2 * i + 1], c["weight"], causal=False, out=torch.zeros_like(c["weight"])))
+        return out
+
+    calls(False)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = calls(True)
+    for _ in range(4):
+        for c in layers:
+            c["q"].copy_(normal(g, tuple(c["q"].shape), "bf16"))
+        seq.copy_(ints([n - 10, n]))
+        want = calls(False)
+        torch.cuda.synchronize()
+        for x in got:
+            x.fill_(7)
+        graph.replay()
+        torch.cuda.synchronize()
+        for c, i in zip(layers, (4, 5)):
+            got[i].masked_fill_(got[i] == 7, 0)        # slots that are not in use are left as they were
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
