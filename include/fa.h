@@ -53,14 +53,13 @@ typedef struct CUstream_st *fa_stream_t;
 
 typedef enum {
     FA_OK = 0,
-    FA_ERR_NULL_PTR = 1,        /* q, k, v, o or lse (a tensor that the call needs) is NULL for a non-empty problem */
-    FA_ERR_BAD_DIM = 2,         /* B, Sq, Sk < 0, or Sk == 0 while B*Hq*Sq > 0, or too large; (cache operators) a page
-                                   that is no multiple of 16, slots without pages, T, keep, first or last out of range */
+    FA_ERR_NULL_PTR = 1,        /* q, k, v, o or lse is NULL for a non-empty problem        */
+    FA_ERR_BAD_DIM = 2,         /* B, Sq, Sk < 0, or Sk == 0 while B*Hq*Sq > 0, or too large */
     FA_ERR_HEADS = 3,           /* Hq < 1, Hkv < 1, or Hq % Hkv != 0                         */
     FA_ERR_UNSUPPORTED_D = 4,   /* D not in {64, 128, 256} (or not supported by the chosen kernel) */
-    FA_ERR_ALIGN = 5,           /* q/k/v/o not 16-byte aligned, or lse (any other tensor) not 4-byte aligned */
-    FA_ERR_ALIAS = 6,           /* o or lse (a tensor that is written) overlaps an input or another output */
-    FA_ERR_SCALE = 7,           /* scale is NaN or infinite; (cache operators) or not positive */
+    FA_ERR_ALIGN = 5,           /* q/k/v/o not 16-byte aligned, or lse not 4-byte aligned    */
+    FA_ERR_ALIAS = 6,           /* o or lse overlaps an input or each other                  */
+    FA_ERR_SCALE = 7,           /* scale is NaN or infinite                                  */
     FA_ERR_NO_DEVICE = 8,       /* no CUDA device / runtime error querying it                */
     FA_ERR_ARCH = 9,            /* current device is not compute capability 10.3 (sm_103)    */
     FA_ERR_TENSORMAP = 10,      /* cuTensorMapEncodeTiled unavailable or rejected the layout */
@@ -124,9 +123,7 @@ const char *fa_strerror(int status);
  * partial value that looks like a result; fa_cache_weights does the same with its sums.  (fa_gemm
  * and fa_softmax_rows outputs of such a call are unspecified.)
  * *detail (if non-NULL) receives the raw word: bit 0 = timeout, bits 8..15 = the wait
- * site that expired first.  Each kernel has a word of its own; one call reads and clears all of
- * them and reports the first that is set: forward (two tiles, one tile), GEMM, row softmax,
- * attention over a cache, weights of a cache.
+ * site that expired first.
  */
 int fa_device_status(fa_stream_t stream, uint32_t *detail);
 
@@ -253,12 +250,12 @@ int fa_fwd_host_noalloc(const void *q_h, const void *k_h, const void *v_h, void 
  * A cache holds the keys and values of B sequences in pages of `page` slots that any sequence may
  * own.  Slot s of sequence b is row s % page of page table[b * max_pages + s / page] (of page
  * b * max_pages + s / page without a table, i.e. a dense cache), the same for every KV head;
- * `capacity` = max_pages * page slots a sequence, at most 2^31 - 1025.  Lengths and tables are device arrays that the
+ * `capacity` = max_pages * page slots a sequence.  Lengths and tables are device arrays that the
  * kernels read when they run, so a captured graph follows them.  A length below 0 counts as 0, one
  * above the capacity as the capacity.  A table entry outside [0, num_pages) that a length covers is a
  * caller's mistake that touches no memory outside the cache: its slots read as zero keys and values
  * and writes to them are dropped.  Sequences may share pages that are only read; a page that
- * fa_cache_append or fa_cache_evict writes to must belong to one sequence, and stand in its table once.
+ * fa_cache_append or fa_cache_evict writes to must belong to one sequence.
  *
  * All tensors are dense; pointers are device pointers on the current device, 16-byte aligned for
  * k, v, q, o, k_new and v_new, 4-byte aligned otherwise.  Everything said above about ownership,
@@ -369,9 +366,8 @@ int fa_cache_evict(const fa_cache_t *cache, const float *weight, const int32_t *
  * fa_tree_debug, fa_weights_debug -- test hooks: fa_tree_fwd and fa_cache_weights with an explicit limit of each
  * device wait (timeout_ns, 0 = the default of 2 s) and a fault-injection mask (inject bit 0: every CTA with
  * work leaves out the load of its first V tile, or K tile, so that the wait for it expires; bit 1: only
- * CTA 0; bit 2, attention: every CTA acts as if its shared memory were too small).  The call then records
- * FA_ERR_DEVICE_TIMEOUT and leaves NaN in the rows of o and lse, or the sums, of the CTAs that gave up and of the
- * units that they share with others; the others hold their results.
+ * CTA 0).  The call then records FA_ERR_DEVICE_TIMEOUT and leaves NaN in the rows of o and lse, or the sums,
+ * of the CTAs that gave up and of the units that they share with others; the others hold their results.
  */
 int fa_tree_debug(const fa_cache_t *cache, const void *q, const void *k_new, const void *v_new,
                   const int32_t *parent, const int32_t *draft_len, void *o, float *lse, int Hq, int T,

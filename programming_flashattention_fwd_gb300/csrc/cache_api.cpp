@@ -84,8 +84,7 @@ int check_cache(const fa_cache_t *c)
     if (c->D != 64 && c->D != 128 && c->D != 256) return FA_ERR_UNSUPPORTED_D;
     if (c->page < 16 || c->page % 16 != 0) return FA_ERR_BAD_DIM;
     const long long cap = (long long)c->max_pages * c->page;
-    // the kernels' loops step over a sequence's end by up to 512 slots, in 32 bits
-    if (cap > 0x7fffffffLL - 1024 || (long long)c->B * c->Hkv > 0x7fffffffLL || (long long)c->B * c->max_pages > 0x7fffffffLL)
+    if (cap > 0x7fffff00LL || (long long)c->B * c->Hkv > 0x7fffffffLL || (long long)c->B * c->max_pages > 0x7fffffffLL)
         return FA_ERR_BAD_DIM;
     // slots without any page to be in; a dense cache without pages enough
     if ((c->num_pages == 0 && cap > 0) || (!c->table && (long long)c->B * c->max_pages > c->num_pages)) return FA_ERR_BAD_DIM;
@@ -113,6 +112,19 @@ bool encode_pool(CUtensorMap *m, const void *base, const void *any, const fa_cac
 }
 
 } // namespace
+
+namespace fa {
+
+cudaError_t read_and_clear_cache_status(uint32_t *word)
+{
+    uint32_t tree = 0, weigh = 0;
+    cudaError_t e = cache::read_and_clear_tree_status(&tree);
+    if (e == cudaSuccess) e = cache::read_and_clear_weigh_status(&weigh);
+    *word = (tree & 1u) ? tree : weigh;
+    return e;
+}
+
+} // namespace fa
 
 extern "C" {
 

@@ -10,7 +10,6 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
-#include "cache_internal.h"
 #include "fa.h"
 #include "fa_internal.h"
 #include "schedule.h"
@@ -289,13 +288,12 @@ const char *fa_strerror(int status)
     switch (status) {
     case FA_OK: return "FA_OK: success";
     case FA_ERR_NULL_PTR: return "FA_ERR_NULL_PTR: a tensor pointer is NULL";
-    case FA_ERR_BAD_DIM: return "FA_ERR_BAD_DIM: negative size, Sk == 0 for a non-empty problem, or problem too large (a cache: page not a multiple of 16, "
-                                "no pages for its slots, T == 0, keep < 1 or first + last > keep)";
+    case FA_ERR_BAD_DIM: return "FA_ERR_BAD_DIM: negative size, Sk == 0 for a non-empty problem, or problem too large";
     case FA_ERR_HEADS: return "FA_ERR_HEADS: Hq and Hkv must be >= 1 with Hq % Hkv == 0";
     case FA_ERR_UNSUPPORTED_D: return "FA_ERR_UNSUPPORTED_D: D must be 64, 128 or 256 (and supported by the selected kernel)";
-    case FA_ERR_ALIGN: return "FA_ERR_ALIGN: 16-bit tensors must be 16-byte aligned, others 4-byte aligned (a workspace as its operator says)";
-    case FA_ERR_ALIAS: return "FA_ERR_ALIAS: a tensor that is written overlaps another one";
-    case FA_ERR_SCALE: return "FA_ERR_SCALE: scale is NaN or infinite (a cache: or not positive)";
+    case FA_ERR_ALIGN: return "FA_ERR_ALIGN: q/k/v/o must be 16-byte aligned and lse 4-byte aligned";
+    case FA_ERR_ALIAS: return "FA_ERR_ALIAS: o or lse overlaps an input or each other";
+    case FA_ERR_SCALE: return "FA_ERR_SCALE: scale is NaN or infinite";
     case FA_ERR_NO_DEVICE: return "FA_ERR_NO_DEVICE: no usable CUDA device";
     case FA_ERR_ARCH: return "FA_ERR_ARCH: the current device is not sm_103 (GB300)";
     case FA_ERR_TENSORMAP: return "FA_ERR_TENSORMAP: TMA descriptor encoding failed";
@@ -304,23 +302,21 @@ const char *fa_strerror(int status)
     case FA_ERR_CAUSAL: return "FA_ERR_CAUSAL: causal must be 0 (none), 1 (top-left) or 2 (bottom-right)";
     case FA_ERR_SHAPE: return "FA_ERR_SHAPE: matrix rows must be 16-byte multiples (K and N multiples of 8)";
     case FA_ERR_ARG: return "FA_ERR_ARG: dtype, output type or epilogue selector out of range";
-    case FA_ERR_TOO_LARGE: return "FA_ERR_TOO_LARGE: the problem needs more staging than FA_HOST_NOALLOC_MAX_BYTES, or more workspace than it was given";
+    case FA_ERR_TOO_LARGE: return "FA_ERR_TOO_LARGE: the problem needs more staging than FA_HOST_NOALLOC_MAX_BYTES";
     default: return "unknown fa status code";
     }
 }
 
 int fa_device_status(fa_stream_t stream, uint32_t *detail)
 {
-    // every kernel's word is read and cleared; of those that are set the first in this order is reported
-    uint32_t word[6] = {};
-    if (fa::read_and_clear_status(reinterpret_cast<cudaStream_t>(stream), &word[0]) != cudaSuccess ||
-        fa::read_and_clear_fa1_status(&word[1]) != cudaSuccess || fa::read_and_clear_gemm_status(&word[2]) != cudaSuccess ||
-        fa::read_and_clear_softmax_status(&word[3]) != cudaSuccess || fa::cache::read_and_clear_tree_status(&word[4]) != cudaSuccess ||
-        fa::cache::read_and_clear_weigh_status(&word[5]) != cudaSuccess)
-        return FA_ERR_NO_DEVICE;
-    uint32_t w = word[0];
-    for (uint32_t x : word)
-        if (!(w & 1u)) w = x;
+    uint32_t w = 0, wg = 0;
+    if (fa::read_and_clear_status(reinterpret_cast<cudaStream_t>(stream), &w) != cudaSuccess) return FA_ERR_NO_DEVICE;
+    uint32_t w1 = 0;
+    if (fa::read_and_clear_gemm_status(&wg) != cudaSuccess) return FA_ERR_NO_DEVICE;
+    if (fa::read_and_clear_fa1_status(&w1) != cudaSuccess) return FA_ERR_NO_DEVICE;
+    uint32_t ws = 0;
+    if (fa::read_and_clear_softmax_status(&ws) != cudaSuccess) return FA_ERR_NO_DEVICE;
+    if (!(w & 1u)) w = (w1 & 1u) ? w1 : ((wg & 1u) ? wg : ws);   // attention kernels checked first
     if (detail) *detail = w;
     return (w & 1u) ? FA_ERR_DEVICE_TIMEOUT : FA_OK;
 }

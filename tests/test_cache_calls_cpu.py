@@ -9,7 +9,6 @@ import torch
 
 from programming_flashattention_fwd_gb300 import build as fa_build
 from programming_flashattention_fwd_gb300 import cache as fc
-import test_cache_cpu as abi
 from test_cache_cpu import FakeCuda, lib, make_cache, on  # noqa: F401
 
 
@@ -72,35 +71,3 @@ def test_overlapped_kernels_load_coherently(name):
     with open(os.path.join(fa_build.CSRC, name)) as f:
         code = re.sub(r"//.*", "", f.read())
     assert not re.search(r"__ldg|\.nc\b|__restrict__", code)
-
-
-@pytest.mark.parametrize("call", ["tree", "append", "weights", "evict"])
-def test_capacities_that_loops_cannot_step_over_are_refused(lib, call):  # noqa: F811
-    """A loop over the slots goes past a sequence's end by up to its step before it stops: the sum has to fit 32 bits."""
-    assert getattr(abi, call)(lib, page=64, max_pages=0x7fffff00 // 64) == 2      # 255 below 2^31
-    assert getattr(abi, call)(lib, page=64, max_pages=(0x7fffffff - 1024) // 64 + 1) == 2
-
-
-def test_a_cache_kernel_is_nothing_to_the_others():
-    """A change to the cache's kernels leaves the sources of the other kernels alone, and so what was measured of them:
-    their status words meet in the host API only."""
-    for name in ("fa_fwd_sm103.cu", "fa_fwd1_sm103.cu", "gemm_sm103.cu", "softmax_sm103.cu", "fa_internal.h", "ptx.cuh", "watchdog.cuh"):
-        with open(os.path.join(fa_build.CSRC, name)) as f:
-            assert not re.search("cache_internal|cache_status|tree_status|weigh_status", f.read()), name
-
-
-@pytest.mark.parametrize("call,over,words", [
-    ("tree", dict(bytes=1000), ["workspace"]), ("tree", dict(scale=-1.0), ["positive"]), ("tree", dict(page=24), ["page", "16"]),
-    ("append", dict(weight=abi.ADDR["pos"]), ["written", "overlaps"]), ("evict", dict(first=50, last=51), ["first", "last", "keep"]),
-    ("weights", dict(T=0), ["T == 0"]), ("weights", dict(lse=abi.ADDR["lse"] + 2), ["4-byte"])])
-def test_messages_name_what_is_wrong(lib, call, over, words):  # noqa: F811
-    """The message of a refused call is about that call, not about the forward's arguments alone."""
-    message = lib.fa_strerror(getattr(abi, call)(lib, **over)).decode()
-    assert all(w in message for w in words), message
-
-
-@pytest.mark.parametrize("name", ["cache_schedule.h", "cache_sm103.cu", "tree_sm103.cu", "weigh_sm103.cu"])
-def test_the_number_of_sms_is_the_device_s(name):
-    """Launch shapes follow the device that the call runs on, not the 152 SMs of the one that they were measured on."""
-    with open(os.path.join(fa_build.CSRC, name)) as f:
-        assert not re.search(r"\b(152|304)\b", re.sub(r"//.*", "", f.read()))
