@@ -366,8 +366,9 @@ int fa_cache_evict(const fa_cache_t *cache, const float *weight, const int32_t *
  * fa_tree_debug, fa_weights_debug -- test hooks: fa_tree_fwd and fa_cache_weights with an explicit limit of each
  * device wait (timeout_ns, 0 = the default of 2 s) and a fault-injection mask (inject bit 0: every CTA with
  * work leaves out the load of its first V tile, or K tile, so that the wait for it expires; bit 1: only
- * CTA 0).  The call then records FA_ERR_DEVICE_TIMEOUT and leaves NaN in the rows of o and lse, or the sums,
- * of the CTAs that gave up and of the units that they share with others; the others hold their results.
+ * CTA 0; bit 2, attention: every CTA acts as if its shared memory were too small).  The call then records
+ * FA_ERR_DEVICE_TIMEOUT and leaves NaN in the rows of o and lse, or the sums, of the CTAs that gave up and of the
+ * units that they share with others; the others hold their results.
  */
 int fa_tree_debug(const fa_cache_t *cache, const void *q, const void *k_new, const void *v_new,
                   const int32_t *parent, const int32_t *draft_len, void *o, float *lse, int Hq, int T,

@@ -66,7 +66,7 @@ struct TreeParams {
     int box_rows;            // rows of one copy: gcd(page, 128), at most BN
     float sl2;               // scale * log2 e
     uint64_t timeout_ns;     // limit of a wait (0: the default)
-    uint32_t inject;         // fault injection: the first V tile is never loaded (bit 0: in every CTA, bit 1: in CTA 0)
+    uint32_t inject;         // fault injection: the first V tile is never loaded (bit 0: in every CTA, bit 1: in CTA 0); bit 2: no room
 };
 
 struct TreeMaps {

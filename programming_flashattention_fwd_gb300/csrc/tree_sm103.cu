@@ -154,6 +154,53 @@ __device__ __forceinline__ void path_bits(const int32_t *parent, int t, int lo, 
 // Steps of sequence b.
 __device__ __forceinline__ int tree_steps(const TreeShape &s, int b) { return s.Hkv * s.units * tree_len(s, b).nt; }
 
+// NaN into every row of a CTA's share, its parts included: threads `first`, first + step, ... take a row each.
+template <int D>
+__device__ __forceinline__ void leave_nan(const TreeParams &p, TreeWalk walk, int first, int step)
+{
+    const float nan = __uint_as_float(~0u);
+    TreeSeg g;
+    while (walk.next(p.s, g)) {
+        for (int urow = first; urow < p.s.tile; urow += step) {
+            const int row = g.mt * p.s.tile + urow;
+            if (row >= p.s.rows || row % p.s.T >= g.len.t) continue;
+            if (g.k0 == 0 && g.k1 == g.len.nt) {
+                const size_t orow = (size_t)(g.b * p.s.Hkv + g.kvh) * p.s.rows + row;
+                for (int c = 0; c < D * 2; c += 16)
+                    st_global_v4(static_cast<uint8_t *>(p.o) + orow * D * 2 + c, ~0u, ~0u, ~0u, ~0u);
+                p.lse[orow] = nan;
+            } else {
+                const size_t prow = (size_t)part_slot(blockIdx.x, g.k0) * p.part_rows + urow;
+                for (int c = 0; c < D; ++c) p.part_o[prow * D + c] = nan;
+                p.part_lse[prow] = nan;
+            }
+        }
+    }
+}
+
+// For the joining kernel: the cut unit that the share starts in, if the unit's first cut is there.
+__device__ __forceinline__ Cut cut_of(const TreeWalk &walk, int total, int ctas)
+{
+    Cut c = {};
+    if (walk.left > 0) c = Cut{walk.b, walk.kvh, walk.mt, parts_from(total, ctas, blockIdx.x, walk.k, walk.len.nt), walk.len.t, {}};
+    return c;
+}
+
+// A CTA that the alignment of its shared memory leaves no room in: it does nothing but what the joining kernel and the
+// caller rely on, without shared memory (each warp looks the share up for itself).
+template <int D>
+__device__ __noinline__ void no_room(const TreeParams &p)
+{
+    grid_wait();
+    const Share w = find_share(p.s.B, threadIdx.x & 31, blockIdx.x, gridDim.x, [&](int b) { return tree_steps(p.s, b); });
+    const TreeWalk mine(p.s, w.b, w.off, w.left);
+    if (threadIdx.x == 0) {
+        atomicOr(&g_tree_status, 1u | (S_SMEM << 8));
+        p.cuts[blockIdx.x] = cut_of(mine, w.total, w.G);
+    }
+    leave_nan<D>(p, mine, threadIdx.x, blockDim.x);
+}
+
 template <int D, bool BF16, bool PAIR>
 __global__ void __launch_bounds__(Cfg<D, PAIR>::THREADS, 1)
     tree_kernel(const __grid_constant__ TreeMaps maps, const __grid_constant__ TreeParams p)
@@ -180,8 +227,8 @@ __global__ void __launch_bounds__(Cfg<D, PAIR>::THREADS, 1)
     const uint64_t tmo = p.timeout_ns;
 
     grid_done_soon();
-    if (pad + (uint32_t)C::BYTES > dynamic_smem_size_u32()) {
-        if (threadIdx.x == 0) atomicOr(status, 1u | (S_SMEM << 8));
+    if (pad + (uint32_t)C::BYTES > dynamic_smem_size_u32() || (p.inject & 4u)) {
+        no_room<D>(p);
         return;
     }
     int total = 0, ctas = 1;   // (warp 3) all steps, the CTAs that share them
@@ -239,11 +286,7 @@ __global__ void __launch_bounds__(Cfg<D, PAIR>::THREADS, 1)
         const int boxes = div2(BN, p.box_rows);       // boxes of a step (one panel)
         int use0 = 0, last = 0;                       // the segment's first place in the ring, this warp's last
         uint32_t issued = 0;                          // bit i: place last - i is this warp's
-        if (is_v && lane == 0) {   // for the joining kernel
-            Cut c = {};
-            if (walk.left > 0) c = Cut{walk.b, walk.kvh, walk.mt, parts_from(total, ctas, blockIdx.x, walk.k, walk.len.nt), walk.len.t, {}};
-            p.cuts[blockIdx.x] = c;
-        }
+        if (is_v && lane == 0) p.cuts[blockIdx.x] = cut_of(walk, total, ctas);
         bool skip = is_v && ((p.inject & 1u) || ((p.inject & 2u) && blockIdx.x == 0));
         bool ok = true;
         PageRun run;
@@ -758,25 +801,7 @@ __global__ void __launch_bounds__(Cfg<D, PAIR>::THREADS, 1)
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     } else if (warp >= 4 && *abort_flag) {
-        // This CTA gave up on a wait: NaN into every row it was given, its parts included
-        const float nan = __uint_as_float(~0u);
-        TreeWalk again = const_cast<const Misc *>(misc)->share;
-        while (again.next(p.s, g)) {
-            for (int urow = threadIdx.x - 128; urow < p.s.tile; urow += 256) {
-                const int row = g.mt * p.s.tile + urow;
-                if (row >= p.s.rows || row % p.s.T >= g.len.t) continue;
-                if (g.k0 == 0 && g.k1 == g.len.nt) {
-                    const size_t orow = (size_t)(g.b * p.s.Hkv + g.kvh) * p.s.rows + row;
-                    for (int c = 0; c < D * 2; c += 16)
-                        st_global_v4(static_cast<uint8_t *>(p.o) + orow * D * 2 + c, ~0u, ~0u, ~0u, ~0u);
-                    p.lse[orow] = nan;
-                } else {
-                    const size_t prow = (size_t)part_slot(blockIdx.x, g.k0) * p.part_rows + urow;
-                    for (int c = 0; c < D; ++c) p.part_o[prow * D + c] = nan;
-                    p.part_lse[prow] = nan;
-                }
-            }
-        }
+        leave_nan<D>(p, const_cast<const Misc *>(misc)->share, threadIdx.x - 128, 256);   // this CTA gave up on a wait
     }
 }
 

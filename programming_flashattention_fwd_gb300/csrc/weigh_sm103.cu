@@ -54,7 +54,7 @@ constexpr uint64_t kDefaultTimeoutNs = 2000000000ull;
 constexpr int NB = 4;   // S^T buffers, 128 columns apart, each with a group of four warps that sums it
 constexpr int THREADS = 128 + 128 * NB + 32;
 
-enum Site : uint32_t { S_KEMPTY = 1, S_QEMPTY = 2, S_KFULL = 3, S_QFULL = 4, S_FREE = 5, S_S = 6, S_ROWS = 7, S_DRAIN = 8, S_SMEM = 9, S_JOIN = 10, S_READ = 11 };
+enum Site : uint32_t { S_KEMPTY = 1, S_QEMPTY = 2, S_KFULL = 3, S_QFULL = 4, S_FREE = 5, S_S = 6, S_ROWS = 7, S_DRAIN = 8, S_JOIN = 10, S_READ = 11 };
 
 template <int D>
 struct Cfg {
@@ -70,7 +70,7 @@ struct Cfg {
     static constexpr int OFF_JOIN = OFF_ROWS + NB * 1024;                    // [NB][128] sums handed over
     static constexpr int OFF_MISC = OFF_JOIN + NB * 512;
     static constexpr int BYTES = OFF_MISC + 128;
-    static constexpr int ALLOC = BYTES + 1024;
+    static constexpr int ALLOC = BYTES + 1024;   // the base is aligned to 1024 bytes, wherever it is
     static_assert(ALLOC <= 232448, "shared memory of one CTA");
 };
 
@@ -110,10 +110,6 @@ __global__ void __launch_bounds__(THREADS, 1)
     const bool gather = p.s.mode == kPath;
 
     grid_done_soon();
-    if (pad + (uint32_t)C::BYTES > dynamic_smem_size_u32()) {
-        if (threadIdx.x == 0) atomicOr(status, 1u | (S_SMEM << 8));
-        return;
-    }
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::KS; ++s) {
             mbar_init(k_full(s), 1);
@@ -527,7 +523,7 @@ struct Prompt {
     static constexpr int OFF_ROWS = OFF_BAR + ((NBAR * 8 + 15) / 16) * 16;   // NR x { -lse2[128], limit[128] }
     static constexpr int OFF_MISC = OFF_ROWS + NR * 1024;
     static constexpr int BYTES = OFF_MISC + 128;
-    static constexpr int ALLOC = BYTES + 1024;
+    static constexpr int ALLOC = BYTES + 1024;   // the base is aligned to 1024 bytes, wherever it is
     static_assert(ALLOC <= 232448, "shared memory of one CTA");
     static constexpr uint32_t COL_S = D;               // the scores start behind the two key tiles
     static_assert(D + NBUF * NQ <= 512, "tensor-memory columns");
@@ -591,10 +587,6 @@ __global__ void __launch_bounds__(Prompt<D>::THREADS, 1)
     const uint64_t tmo = p.timeout_ns;
 
     grid_done_soon();
-    if (pad + (uint32_t)C::BYTES > dynamic_smem_size_u32()) {
-        if (threadIdx.x == 0) atomicOr(status, 1u | (S_SMEM << 8));
-        return;
-    }
     if (threadIdx.x == 0) {
         mbar_init(barK, 1);
         mbar_init(barKfree, 1);

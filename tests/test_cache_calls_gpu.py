@@ -7,7 +7,7 @@ import numpy as np
 import pytest
 import torch
 
-from test_cache_gpu import fa, ints, normal, pytestmark  # noqa: F401
+from test_cache_gpu import debug_call, fa, ints, normal, pytestmark  # noqa: F401
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
@@ -140,3 +140,29 @@ def test_a_forked_capture(fa):  # noqa: F811
         for c, i in zip(layers, (4, 5)):
             got[i].masked_fill_(got[i] == 7, 0)        # slots that are not in use are left as they were
         assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
+@pytest.mark.parametrize("D,Hq", [(64, 4), (128, 4), (128, 80), (256, 4)])
+def test_ctas_without_room(fa, D, Hq):  # noqa: F811
+    """CTAs that act as if their shared memory were too small: the call ends, the status says so, every row is NaN, those of
+    units that are joined from parts too (the workspace holds nothing that the joining kernel may go by), rows
+    behind draft_len are as they were, and the next call is right.  (Hq = 80: two row tiles side by side.)"""
+    g = torch.Generator().manual_seed(140)
+    B, Hkv, T, page, n = 12, 2, 5, 64, 1500
+    per = -(-n // page)
+    c = layer(g, B, Hq, Hkv, D, T, B * per, page, per * page)
+    cache = fa.KVCache(c["k"], c["v"], ints([n] * B), ints(torch.arange(B * per).reshape(B, per)))
+    drafts = ints([5, 4, 0] * 4)
+    want = fa.tree_attention(c["q"], c["kn"], c["vn"], cache, draft_len=drafts, o=torch.full_like(c["q"], 7), lse=torch.full((B, Hq, T), 9.0).cuda())
+    o, lse = torch.full_like(c["q"], 7), torch.full((B, Hq, T), 9.0, device="cuda")
+    size = fa.tree_workspace_bytes(Hq, Hkv, T, D)
+    ws = torch.full((size,), 255, dtype=torch.uint8, device="cuda")
+    debug_call(fa, "fa_tree_debug", cache, (c["q"], c["kn"], c["vn"], None, drafts, o, lse),
+               (Hq, T, D ** -0.5, ws.data_ptr(), size, torch.cuda.current_stream().cuda_stream, 0, 4))
+    st, word = fa.fa_device_status()
+    assert st == 12 and word & 0xff01 == 0x901
+    live = torch.arange(T, device="cuda") < drafts[:, None, None]
+    live = live.expand(B, Hq, T)
+    assert torch.isnan(o[live]).all() and torch.isnan(lse[live]).all() and (o[~live] == 7).all() and (lse[~live] == 9).all()
+    again = fa.tree_attention(c["q"], c["kn"], c["vn"], cache, draft_len=drafts, o=o, lse=lse)
+    assert torch.equal(again[0], want[0]) and torch.equal(again[1], want[1]) and fa.fa_device_status() == (0, 0)
