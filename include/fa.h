@@ -250,7 +250,7 @@ int fa_fwd_host_noalloc(const void *q_h, const void *k_h, const void *v_h, void 
  * A cache holds the keys and values of B sequences in pages of `page` slots that any sequence may
  * own.  Slot s of sequence b is row s % page of page table[b * max_pages + s / page] (of page
  * b * max_pages + s / page without a table, i.e. a dense cache), the same for every KV head;
- * `capacity` = max_pages * page slots a sequence.  Lengths and tables are device arrays that the
+ * `capacity` = max_pages * page slots a sequence, at most 2^31 - 1025.  Lengths and tables are device arrays that the
  * kernels read when they run, so a captured graph follows them.  A length below 0 counts as 0, one
  * above the capacity as the capacity.  A table entry outside [0, num_pages) that a length covers is a
  * caller's mistake that touches no memory outside the cache: its slots read as zero keys and values

@@ -84,7 +84,8 @@ int check_cache(const fa_cache_t *c)
     if (c->D != 64 && c->D != 128 && c->D != 256) return FA_ERR_UNSUPPORTED_D;
     if (c->page < 16 || c->page % 16 != 0) return FA_ERR_BAD_DIM;
     const long long cap = (long long)c->max_pages * c->page;
-    if (cap > 0x7fffff00LL || (long long)c->B * c->Hkv > 0x7fffffffLL || (long long)c->B * c->max_pages > 0x7fffffffLL)
+    // the kernels' loops step over a sequence's end by up to 512 slots, in 32 bits
+    if (cap > 0x7fffffffLL - 1024 || (long long)c->B * c->Hkv > 0x7fffffffLL || (long long)c->B * c->max_pages > 0x7fffffffLL)
         return FA_ERR_BAD_DIM;
     // slots without any page to be in; a dense cache without pages enough
     if ((c->num_pages == 0 && cap > 0) || (!c->table && (long long)c->B * c->max_pages > c->num_pages)) return FA_ERR_BAD_DIM;

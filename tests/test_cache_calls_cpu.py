@@ -9,6 +9,7 @@ import torch
 
 from programming_flashattention_fwd_gb300 import build as fa_build
 from programming_flashattention_fwd_gb300 import cache as fc
+import test_cache_cpu as abi
 from test_cache_cpu import FakeCuda, lib, make_cache, on  # noqa: F401
 
 
@@ -71,3 +72,10 @@ def test_overlapped_kernels_load_coherently(name):
     with open(os.path.join(fa_build.CSRC, name)) as f:
         code = re.sub(r"//.*", "", f.read())
     assert not re.search(r"__ldg|\.nc\b|__restrict__", code)
+
+
+@pytest.mark.parametrize("call", ["tree", "append", "weights", "evict"])
+def test_capacities_that_loops_cannot_step_over_are_refused(lib, call):  # noqa: F811
+    """A loop over the slots goes past a sequence's end by up to its step before it stops: the sum has to fit 32 bits."""
+    assert getattr(abi, call)(lib, page=64, max_pages=0x7fffff00 // 64) == 2      # 255 below 2^31
+    assert getattr(abi, call)(lib, page=64, max_pages=(0x7fffffff - 1024) // 64 + 1) == 2
