@@ -123,7 +123,9 @@ const char *fa_strerror(int status);
  * partial value that looks like a result; fa_cache_weights does the same with its sums.  (fa_gemm
  * and fa_softmax_rows outputs of such a call are unspecified.)
  * *detail (if non-NULL) receives the raw word: bit 0 = timeout, bits 8..15 = the wait
- * site that expired first.
+ * site that expired first.  Each kernel has a word of its own; one call reads and clears all of
+ * them and reports the first that is set: forward (two tiles, one tile), GEMM, row softmax,
+ * attention over a cache, weights of a cache.
  */
 int fa_device_status(fa_stream_t stream, uint32_t *detail);
 
@@ -255,7 +257,7 @@ int fa_fwd_host_noalloc(const void *q_h, const void *k_h, const void *v_h, void 
  * above the capacity as the capacity.  A table entry outside [0, num_pages) that a length covers is a
  * caller's mistake that touches no memory outside the cache: its slots read as zero keys and values
  * and writes to them are dropped.  Sequences may share pages that are only read; a page that
- * fa_cache_append or fa_cache_evict writes to must belong to one sequence.
+ * fa_cache_append or fa_cache_evict writes to must belong to one sequence, and stand in its table once.
  *
  * All tensors are dense; pointers are device pointers on the current device, 16-byte aligned for
  * k, v, q, o, k_new and v_new, 4-byte aligned otherwise.  Everything said above about ownership,

@@ -114,19 +114,6 @@ bool encode_pool(CUtensorMap *m, const void *base, const void *any, const fa_cac
 
 } // namespace
 
-namespace fa {
-
-cudaError_t read_and_clear_cache_status(uint32_t *word)
-{
-    uint32_t tree = 0, weigh = 0;
-    cudaError_t e = cache::read_and_clear_tree_status(&tree);
-    if (e == cudaSuccess) e = cache::read_and_clear_weigh_status(&weigh);
-    *word = (tree & 1u) ? tree : weigh;
-    return e;
-}
-
-} // namespace fa
-
 extern "C" {
 
 size_t fa_tree_workspace_bytes(int Hq, int Hkv, int T, int D)

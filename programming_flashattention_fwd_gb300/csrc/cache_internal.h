@@ -141,7 +141,4 @@ cudaError_t launch_evict(const EvictParams &p, cudaStream_t st);
 
 } // namespace cache
 
-// The watchdog words of the cache kernels (read with the other kernels' by fa_device_status).
-cudaError_t read_and_clear_cache_status(uint32_t *word);
-
 } // namespace fa

@@ -10,6 +10,7 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
+#include "cache_internal.h"
 #include "fa.h"
 #include "fa_internal.h"
 #include "schedule.h"
@@ -309,14 +310,16 @@ const char *fa_strerror(int status)
 
 int fa_device_status(fa_stream_t stream, uint32_t *detail)
 {
-    uint32_t w = 0, wg = 0;
-    if (fa::read_and_clear_status(reinterpret_cast<cudaStream_t>(stream), &w) != cudaSuccess) return FA_ERR_NO_DEVICE;
-    uint32_t w1 = 0;
-    if (fa::read_and_clear_gemm_status(&wg) != cudaSuccess) return FA_ERR_NO_DEVICE;
-    if (fa::read_and_clear_fa1_status(&w1) != cudaSuccess) return FA_ERR_NO_DEVICE;
-    uint32_t ws = 0;
-    if (fa::read_and_clear_softmax_status(&ws) != cudaSuccess) return FA_ERR_NO_DEVICE;
-    if (!(w & 1u)) w = (w1 & 1u) ? w1 : ((wg & 1u) ? wg : ws);   // attention kernels checked first
+    // every kernel's word is read and cleared; of those that are set the first in this order is reported
+    uint32_t word[6] = {};
+    if (fa::read_and_clear_status(reinterpret_cast<cudaStream_t>(stream), &word[0]) != cudaSuccess ||
+        fa::read_and_clear_fa1_status(&word[1]) != cudaSuccess || fa::read_and_clear_gemm_status(&word[2]) != cudaSuccess ||
+        fa::read_and_clear_softmax_status(&word[3]) != cudaSuccess || fa::cache::read_and_clear_tree_status(&word[4]) != cudaSuccess ||
+        fa::cache::read_and_clear_weigh_status(&word[5]) != cudaSuccess)
+        return FA_ERR_NO_DEVICE;
+    uint32_t w = word[0];
+    for (uint32_t x : word)
+        if (!(w & 1u)) w = x;
     if (detail) *detail = w;
     return (w & 1u) ? FA_ERR_DEVICE_TIMEOUT : FA_OK;
 }

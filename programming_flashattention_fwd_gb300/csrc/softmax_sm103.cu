@@ -18,7 +18,6 @@
 
 #include <cuda_bf16.h>
 
-#include "cache_internal.h"
 #include "fa_internal.h"
 #include "ptx.cuh"
 #include "watchdog.cuh"
@@ -461,11 +460,6 @@ cudaError_t read_and_clear_softmax_status(uint32_t *word)
     if (e != cudaSuccess) return e;
     const unsigned int zero = 0;
     e = cudaMemcpyToSymbol(g_softmax_status, &zero, sizeof(zero));
-    if (e != cudaSuccess) return e;
-    // last in the chain of status words: the cache kernels'
-    uint32_t wc = 0;
-    e = read_and_clear_cache_status(&wc);
-    if (!(w & 1u)) w = wc;
     if (word) *word = w;
     return e;
 }

@@ -79,3 +79,11 @@ def test_capacities_that_loops_cannot_step_over_are_refused(lib, call):  # noqa:
     """A loop over the slots goes past a sequence's end by up to its step before it stops: the sum has to fit 32 bits."""
     assert getattr(abi, call)(lib, page=64, max_pages=0x7fffff00 // 64) == 2      # 255 below 2^31
     assert getattr(abi, call)(lib, page=64, max_pages=(0x7fffffff - 1024) // 64 + 1) == 2
+
+
+def test_a_cache_kernel_is_nothing_to_the_others():
+    """A change to the cache's kernels leaves the sources of the other kernels alone, and so what was measured of them:
+    their status words meet in the host API only."""
+    for name in ("fa_fwd_sm103.cu", "fa_fwd1_sm103.cu", "gemm_sm103.cu", "softmax_sm103.cu", "fa_internal.h", "ptx.cuh", "watchdog.cuh"):
+        with open(os.path.join(fa_build.CSRC, name)) as f:
+            assert not re.search("cache_internal|cache_status|tree_status|weigh_status", f.read()), name

@@ -166,3 +166,22 @@ def test_ctas_without_room(fa, D, Hq):  # noqa: F811
     assert torch.isnan(o[live]).all() and torch.isnan(lse[live]).all() and (o[~live] == 7).all() and (lse[~live] == 9).all()
     again = fa.tree_attention(c["q"], c["kn"], c["vn"], cache, draft_len=drafts, o=o, lse=lse)
     assert torch.equal(again[0], want[0]) and torch.equal(again[1], want[1]) and fa.fa_device_status() == (0, 0)
+
+
+def test_one_call_reads_the_words_of_all_kernels(fa):  # noqa: F811
+    """Attention and weights that both gave up before anyone asked: reported once, both words cleared."""
+    g = torch.Generator().manual_seed(150)
+    B, Hq, Hkv, D, T, page, n = 2, 4, 2, 64, 3, 16, 300
+    per = -(-n // page)
+    c = layer(g, B, Hq, Hkv, D, T, B * per, page, per * page)
+    cache = fa.KVCache(c["k"], c["v"], ints([n] * B), ints(torch.arange(B * per).reshape(B, per)))
+    o, lse, out = torch.zeros_like(c["q"]), torch.zeros(B, Hq, T, device="cuda"), torch.zeros_like(c["weight"])
+    ws = torch.zeros(max(fa.tree_workspace_bytes(Hq, Hkv, T, D), fa.weights_workspace_bytes()), dtype=torch.uint8, device="cuda")
+    stream = torch.cuda.current_stream().cuda_stream
+    debug_call(fa, "fa_tree_debug", cache, (c["q"], c["kn"], c["vn"], None, None, o, lse),
+               (Hq, T, D ** -0.5, ws.data_ptr(), ws.nbytes, stream, 3_000_000, 1))
+    debug_call(fa, "fa_weights_debug", cache, (c["q"], lse, None, None, None, out),
+               (Hq, T, 1, D ** -0.5, ws.data_ptr(), ws.nbytes, stream, 3_000_000, 1))
+    st, word = fa.fa_device_status()
+    assert st == 12 and word & 1 and torch.isnan(lse).all() and torch.isnan(out[..., :n]).all()
+    assert fa.fa_device_status() == (0, 0)
