@@ -53,13 +53,14 @@ typedef struct CUstream_st *fa_stream_t;
 
 typedef enum {
     FA_OK = 0,
-    FA_ERR_NULL_PTR = 1,        /* q, k, v, o or lse is NULL for a non-empty problem        */
-    FA_ERR_BAD_DIM = 2,         /* B, Sq, Sk < 0, or Sk == 0 while B*Hq*Sq > 0, or too large */
+    FA_ERR_NULL_PTR = 1,        /* q, k, v, o or lse (a tensor that the call needs) is NULL for a non-empty problem */
+    FA_ERR_BAD_DIM = 2,         /* B, Sq, Sk < 0, or Sk == 0 while B*Hq*Sq > 0, or too large; (cache operators) a page
+                                   that is no multiple of 16, slots without pages, T, keep, first or last out of range */
     FA_ERR_HEADS = 3,           /* Hq < 1, Hkv < 1, or Hq % Hkv != 0                         */
     FA_ERR_UNSUPPORTED_D = 4,   /* D not in {64, 128, 256} (or not supported by the chosen kernel) */
-    FA_ERR_ALIGN = 5,           /* q/k/v/o not 16-byte aligned, or lse not 4-byte aligned    */
-    FA_ERR_ALIAS = 6,           /* o or lse overlaps an input or each other                  */
-    FA_ERR_SCALE = 7,           /* scale is NaN or infinite                                  */
+    FA_ERR_ALIGN = 5,           /* q/k/v/o not 16-byte aligned, or lse (any other tensor) not 4-byte aligned */
+    FA_ERR_ALIAS = 6,           /* o or lse (a tensor that is written) overlaps an input or another output */
+    FA_ERR_SCALE = 7,           /* scale is NaN or infinite; (cache operators) or not positive */
     FA_ERR_NO_DEVICE = 8,       /* no CUDA device / runtime error querying it                */
     FA_ERR_ARCH = 9,            /* current device is not compute capability 10.3 (sm_103)    */
     FA_ERR_TENSORMAP = 10,      /* cuTensorMapEncodeTiled unavailable or rejected the layout */

@@ -289,12 +289,13 @@ const char *fa_strerror(int status)
     switch (status) {
     case FA_OK: return "FA_OK: success";
     case FA_ERR_NULL_PTR: return "FA_ERR_NULL_PTR: a tensor pointer is NULL";
-    case FA_ERR_BAD_DIM: return "FA_ERR_BAD_DIM: negative size, Sk == 0 for a non-empty problem, or problem too large";
+    case FA_ERR_BAD_DIM: return "FA_ERR_BAD_DIM: negative size, Sk == 0 for a non-empty problem, or problem too large (a cache: page not a multiple of 16, "
+                                "no pages for its slots, T == 0, keep < 1 or first + last > keep)";
     case FA_ERR_HEADS: return "FA_ERR_HEADS: Hq and Hkv must be >= 1 with Hq % Hkv == 0";
     case FA_ERR_UNSUPPORTED_D: return "FA_ERR_UNSUPPORTED_D: D must be 64, 128 or 256 (and supported by the selected kernel)";
-    case FA_ERR_ALIGN: return "FA_ERR_ALIGN: q/k/v/o must be 16-byte aligned and lse 4-byte aligned";
-    case FA_ERR_ALIAS: return "FA_ERR_ALIAS: o or lse overlaps an input or each other";
-    case FA_ERR_SCALE: return "FA_ERR_SCALE: scale is NaN or infinite";
+    case FA_ERR_ALIGN: return "FA_ERR_ALIGN: 16-bit tensors must be 16-byte aligned, others 4-byte aligned (a workspace as its operator says)";
+    case FA_ERR_ALIAS: return "FA_ERR_ALIAS: a tensor that is written overlaps another one";
+    case FA_ERR_SCALE: return "FA_ERR_SCALE: scale is NaN or infinite (a cache: or not positive)";
     case FA_ERR_NO_DEVICE: return "FA_ERR_NO_DEVICE: no usable CUDA device";
     case FA_ERR_ARCH: return "FA_ERR_ARCH: the current device is not sm_103 (GB300)";
     case FA_ERR_TENSORMAP: return "FA_ERR_TENSORMAP: TMA descriptor encoding failed";
@@ -303,7 +304,7 @@ const char *fa_strerror(int status)
     case FA_ERR_CAUSAL: return "FA_ERR_CAUSAL: causal must be 0 (none), 1 (top-left) or 2 (bottom-right)";
     case FA_ERR_SHAPE: return "FA_ERR_SHAPE: matrix rows must be 16-byte multiples (K and N multiples of 8)";
     case FA_ERR_ARG: return "FA_ERR_ARG: dtype, output type or epilogue selector out of range";
-    case FA_ERR_TOO_LARGE: return "FA_ERR_TOO_LARGE: the problem needs more staging than FA_HOST_NOALLOC_MAX_BYTES";
+    case FA_ERR_TOO_LARGE: return "FA_ERR_TOO_LARGE: the problem needs more staging than FA_HOST_NOALLOC_MAX_BYTES, or more workspace than it was given";
     default: return "unknown fa status code";
     }
 }

@@ -87,3 +87,13 @@ def test_a_cache_kernel_is_nothing_to_the_others():
     for name in ("fa_fwd_sm103.cu", "fa_fwd1_sm103.cu", "gemm_sm103.cu", "softmax_sm103.cu", "fa_internal.h", "ptx.cuh", "watchdog.cuh"):
         with open(os.path.join(fa_build.CSRC, name)) as f:
             assert not re.search("cache_internal|cache_status|tree_status|weigh_status", f.read()), name
+
+
+@pytest.mark.parametrize("call,over,words", [
+    ("tree", dict(bytes=1000), ["workspace"]), ("tree", dict(scale=-1.0), ["positive"]), ("tree", dict(page=24), ["page", "16"]),
+    ("append", dict(weight=abi.ADDR["pos"]), ["written", "overlaps"]), ("evict", dict(first=50, last=51), ["first", "last", "keep"]),
+    ("weights", dict(T=0), ["T == 0"]), ("weights", dict(lse=abi.ADDR["lse"] + 2), ["4-byte"])])
+def test_messages_name_what_is_wrong(lib, call, over, words):  # noqa: F811
+    """The message of a refused call is about that call, not about the forward's arguments alone."""
+    message = lib.fa_strerror(getattr(abi, call)(lib, **over)).decode()
+    assert all(w in message for w in words), message
