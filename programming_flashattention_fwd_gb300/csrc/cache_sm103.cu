@@ -72,10 +72,15 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
 // rows move in place, in parallel, and no other row is touched.  The lists hold rows, so that a move is two
 // dependent round trips: its list entries, then its rows.
 //
-// Bound by latency: about ten cluster-wide steps, each a barrier and a round trip through distributed shared
-// memory or DRAM, and the moves at the end.  Measured, 8 KV heads, D = 128: 8 x 4160 slots to 4096 12.2 us, 4 x
-// 16384 to 2048 34 us (63 MB: 1.8 TB/s); 16 heads, D = 64, 16 x up to 2000 slots to 777 20.5 us.  kCandidates of
-// 64 to 512 take the same time.
+// Bound by latency: four walks over a CTA's slots (weights, candidates, counts, lists) and 4 cluster barriers (6 where
+// a second histogram is needed), most of them followed by a round trip through distributed shared memory; then the
+// moves.  Measured, 8 KV heads, D = 128: 8 x 4160 slots to 4096 12.2 us, 4 x 16384 to 2048 34 us (63 MB: 1.8 TB/s); 16
+// heads, D = 64, 16 x up to 2000 slots to 777 20.5 us.  Cycles of the phases at 2 GHz, with the clock read between them,
+// in first calls of the three cases: weights, positions and first histogram 6300 - 8600, 9900 - 12800, 6000 - 9100;
+// histograms added 2900 - 4400, 4300 - 5900, 2200 - 2900; candidates collected and ranked 5000, 11000 - 12600, 3800; moves
+// counted 3400, 4200, 2500 and listed 1700, 5600, 3300; last barrier 2900, 1900, 50; moves 3400 - 4100, 25000 - 26600,
+// 14300 - 16300.
+// kCandidates of 64 to 512 take the same time.
 constexpr int kEvictThreads = 512, kEvictWarps = kEvictThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kBins = 2048, kCandidates = 512;
@@ -418,6 +423,7 @@ cudaError_t launch_evict(const EvictParams &p0, cudaStream_t st)
 {
     EvictParams p = p0;
     static std::atomic<uint64_t> configured{0};
+    static std::atomic<int> sm_count[64];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -426,17 +432,22 @@ cudaError_t launch_evict(const EvictParams &p0, cudaStream_t st)
     if (!(configured.load(std::memory_order_acquire) & (1ull << dev))) {
         e = cudaFuncSetAttribute(evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (kHeldMost + 4096) * 4);
         if (e != cudaSuccess) return e;
+        int nsm = 0;
+        e = cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev);
+        if (e != cudaSuccess) return e;
+        sm_count[dev].store(nsm, std::memory_order_relaxed);
         configured.fetch_or(1ull << dev, std::memory_order_acq_rel);
     }
     // CTAs of a head: one to an SM, with 1024 slots each at least, and a second one to an SM (all clusters run at
-    // once) where each would have more than 6144 slots and moves, a move counted as four.  With and without the second
-    // (us, 8 KV heads, D = 128): 8 x 4160 -> 4096 slots 14.3, 12.2; 16 x 4160 -> 4096 15.0, 13.4; 4 x 16384 -> 2048
-    // 35.2, 34.4; 16 x 5120 -> 4096 37.3, 46.0; 8 x 12288 -> 1024 29.9, 36.8; 16 x 8192 -> 8000 20.9, 24.2;
-    // 8 x 65536 -> 4096 110, 165.
-    const int heads = p.B * p.Hkv;
+    // once) where each would have more than 7168 slots and moves, a move counted as four.  The lengths are not known
+    // here, so the capacity stands for them.  With and without the second (us, 8 KV heads, D = 128; slots and moves of
+    // a CTA without it): 8 x 4160 -> 4096 slots (2208) 14.3, 12.2; 16 x 4160 -> 4096 (4416) 15.0, 13.4; 4 x 16384 -> 2048
+    // (6144) 35.2, 34.4; 8 x 12288 -> 1024 (8192) 29.9, 36.8; 16 x 8192 -> 8000 (8960) 20.9, 24.2; 16 x 5120 -> 4096 (9216)
+    // 37.3, 46.0; 8 x 65536 -> 4096 (40960) 110, 165.
+    const int heads = p.B * p.Hkv, sms = sm_count[dev].load(std::memory_order_relaxed);
     int C = 1;
-    while (C < kMaxCluster && heads * C * 2 <= 152 && p.capacity > 1024 * C) C *= 2;
-    if (C < kMaxCluster && heads * C * 2 <= 304 && p.capacity + 4ll * p.longest > 6144ll * C) C *= 2;
+    while (C < kMaxCluster && heads * C * 2 <= sms && p.capacity > 1024 * C) C *= 2;
+    if (C < kMaxCluster && heads * C * 2 <= 2 * sms && p.capacity + 4ll * p.longest > 7168ll * C) C *= 2;
     const int per = cdiv(p.capacity, C);
     p.held = per < kHeldMost ? per : kHeldMost;
     const int pages = per / p.pages.page + 2;

@@ -97,3 +97,10 @@ def test_messages_name_what_is_wrong(lib, call, over, words):  # noqa: F811
     """The message of a refused call is about that call, not about the forward's arguments alone."""
     message = lib.fa_strerror(getattr(abi, call)(lib, **over)).decode()
     assert all(w in message for w in words), message
+
+
+@pytest.mark.parametrize("name", ["cache_schedule.h", "cache_sm103.cu", "tree_sm103.cu", "weigh_sm103.cu"])
+def test_the_number_of_sms_is_the_device_s(name):
+    """Launch shapes follow the device that the call runs on, not the 152 SMs of the one that they were measured on."""
+    with open(os.path.join(fa_build.CSRC, name)) as f:
+        assert not re.search(r"\b(152|304)\b", re.sub(r"//.*", "", f.read()))
