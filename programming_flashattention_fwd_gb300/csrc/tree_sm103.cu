@@ -718,8 +718,6 @@ __global__ void __launch_bounds__(Cfg<D, PAIR>::THREADS, 1)
             const size_t orow = ((size_t)(g.b * p.s.Hkv + g.kvh)) * p.s.rows + row;
             constexpr int COLS = HALF ? D / 2 : D;         // columns of this group
             const uint32_t tO0 = tmem + lane_off + C::COL_O + (PAIR ? grp * D : 0);
-            if (!have0) f0 = 0.f;
-            if (!have1) f1 = 0.f;
             if (warp_live) {
                 // 16 columns at a time: the code is fetched anew after the key steps, and its length counts more than the loads'
 #pragma unroll 1
@@ -733,8 +731,9 @@ __global__ void __launch_bounds__(Cfg<D, PAIR>::THREADS, 1)
                     float h[16];
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
-                        h[e] = f0 == 0.f ? 0.f : __uint_as_float(oa[e]) * f0;
-                        if constexpr (SPLIT) h[e] = f1 == 0.f ? h[e] : fmaf(__uint_as_float(ob[e]), f1, h[e]);
+                        // an accumulator without a step holds anything; one with a factor of 0 may hold a non-finite value
+                        h[e] = have0 ? __uint_as_float(oa[e]) * f0 : 0.f;
+                        if constexpr (SPLIT) h[e] = have1 ? fmaf(__uint_as_float(ob[e]), f1, h[e]) : h[e];
                     }
                     if (live && odd) {
                         // weights are positive, so a non-finite value counts as what it is

@@ -185,3 +185,66 @@ def test_one_call_reads_the_words_of_all_kernels(fa):  # noqa: F811
     st, word = fa.fa_device_status()
     assert st == 12 and word & 1 and torch.isnan(lse).all() and torch.isnan(out[..., :n]).all()
     assert fa.fa_device_status() == (0, 0)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("D,Hq", [(64, 4), (128, 4), (64, 96), (128, 96), (256, 4)])
+def test_a_non_finite_value_in_use_is_not_lost(fa, dtype, D, Hq):  # noqa: F811
+    """An infinity in a cached value that every row sees, with a weight of e^-240 (0 in 32 bits): the result is not finite
+    there, wherever the keys are cut (many equal sequences: in every place), and right everywhere else."""
+    g = torch.Generator().manual_seed(160)
+    B, Hkv, T, page, n, per = 40, 2, 3, 64, 200, 4
+    c = layer(g, B, Hq, Hkv, D, T, B * per, page, per * page)
+    k, v, q, kn, vn = (c[x].to(torch.bfloat16 if dtype == "bf16" else torch.float16) for x in ("k", "v", "q", "kn", "vn"))
+    q[..., 0], kn[..., 0] = D ** 0.5, 0
+    k[..., 0] = 0
+    k[2::per, ..., 0], k[3::per, ..., 0] = 240, 240              # slots from 128 on: a later key step
+    cache = fa.KVCache(k, v, ints([n] * B), ints(torch.arange(B * per).reshape(B, per)))
+    want, want_lse = fa.tree_attention(q, kn, vn, cache)
+    v[0::per, :, 7, 5] = float("inf")                            # slot 7
+    o, lse = fa.tree_attention(q, kn, vn, cache)
+    assert torch.isfinite(want).all() and not torch.isfinite(o[..., 5]).any()
+    rest = [d for d in range(D) if d != 5]
+    assert torch.equal(o[..., rest], want[..., rest]) and torch.equal(lse, want_lse)
+
+
+def test_calls_with_nothing_to_do(fa):  # noqa: F811
+    """No drafted, counted or cached token in any sequence: nothing is written but the lengths."""
+    g = torch.Generator().manual_seed(170)
+    B, Hq, Hkv, D, T, page = 3, 4, 2, 128, 5, 16
+    c = layer(g, B, Hq, Hkv, D, T, B * 4, page, 4 * page)
+    seq, none = ints([0, 20, 33]), ints([0, 0, -2])
+    cache = fa.KVCache(c["k"], c["v"], seq, ints(torch.arange(B * 4).reshape(B, 4)))
+    before = {x: t.clone() for x, t in c.items()}
+    o, lse = fa.tree_attention(c["q"], c["kn"], c["vn"], cache, draft_len=none, o=torch.full_like(c["q"], 7), lse=torch.full((B, Hq, T), 9.0).cuda())
+    assert (o == 7).all() and (lse == 9).all()
+    fa.cache_append(cache, c["kn"], c["vn"], count=none, weight=c["weight"], pos=c["pos"], start=seq)
+    for T2 in (5, 200):                                          # packed rows, and the tiles of a prompt
+        q, l = torch.full((B, Hq, T2, D), float("nan"), dtype=torch.bfloat16, device="cuda"), torch.full((B, Hq, T2), float("nan"), device="cuda")
+        fa.cache_weights(cache, q, l, c["weight"], count=none)
+    fa.cache_weights(cache, q, l, c["weight"], path=ints(torch.zeros(B, 200)), count=none)
+    seq.zero_()
+    fa.cache_weights(cache, q, l, c["weight"])
+    assert fa.cache_evict(cache, c["weight"], c["pos"], 4).tolist() == [0, 0, 0]
+    for x in before:
+        assert torch.equal(c[x], before[x]), x
+    assert fa.fa_device_status() == (0, 0)
+
+
+@pytest.mark.parametrize("which", ["weight_out", "pos_out"])
+def test_evict_with_one_of_its_results_elsewhere(fa, which):  # noqa: F811
+    g = torch.Generator().manual_seed(180)
+    B, Hkv, D, page, n, keep = 2, 2, 64, 16, 500, 333
+    per = -(-n // page)
+    c = layer(g, B, 4, Hkv, D, 1, B * per, page, per * page)
+    outs, kept = [], []
+    for other in (False, True):
+        k, v, w, p = (c[x].clone() for x in ("k", "v", "weight", "pos"))
+        cache = fa.KVCache(k, v, ints([n, n - 3]), ints(torch.arange(B * per).reshape(B, per)))
+        given = {which: torch.zeros_like(w if which == "weight_out" else p)} if other else {}
+        fa.cache_evict(cache, w, p, keep, first=2, last=9, next_pos=ints([n, n - 3]), **given)
+        outs.append([x[..., :keep] for x in (given.get("weight_out", w), given.get("pos_out", p))] + [k, v])
+        kept.append((w, p))
+    assert all(torch.equal(a, b) for a, b in zip(*outs))
+    same = 0 if which == "weight_out" else 1                     # the one whose result went elsewhere is as it was
+    assert torch.equal(kept[1][same], c["weight" if same == 0 else "pos"])
