@@ -347,7 +347,7 @@ def cache_evict(cache: KVCache, weight, pos, keep: int, first: int = 0, last: in
     current = _current(i)
     kept = _kept(i, current)
     if new_len is None:
-        new_len = torch.empty(B, dtype=_I32, device=cache.device)
+        new_len = torch.empty_like(cache.seq_len)
     ws, at, size = _workspace(evict_workspace_bytes(B, cache.Hkv, cache.capacity, keep), workspace, cache.k, kept)
     _launch(lib.fa_cache_evict, i, current,
             (cache._c, w, p, wo, po, new_len.data_ptr(), nxt, keep, first, last, at, size))
