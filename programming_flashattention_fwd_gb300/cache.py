@@ -201,6 +201,10 @@ class KVCache:
     def device(self) -> torch.device:
         return self._k.device
 
+    def __reduce__(self):
+        # a copy is made from its tensors: a deep one has others, at other addresses
+        return KVCache, (self._k, self._v, self._seq_len, self._table)
+
 
 @functools.lru_cache(maxsize=256)
 def tree_workspace_bytes(Hq: int, Hkv: int, T: int, D: int) -> int:

@@ -1,5 +1,6 @@
 """Calls of the cache operators as a user's program makes them, as far as they go without a GPU: what a call returns
 and what it does with the tensors that it is given."""
+import copy
 import io
 import os
 import re
@@ -104,3 +105,14 @@ def test_the_number_of_sms_is_the_device_s(name):
     """Launch shapes follow the device that the call runs on, not the 152 SMs of the one that they were measured on."""
     with open(os.path.join(fa_build.CSRC, name)) as f:
         assert not re.search(r"\b(152|304)\b", re.sub(r"//.*", "", f.read()))
+
+
+def test_a_copied_cache_is_one_of_its_tensors(monkeypatch):
+    """A copy's calls work on the copy's own tensors: the same ones for a shallow copy, others for a deep one."""
+    monkeypatch.setattr(FakeCuda, "__deepcopy__", lambda self, memo: memo.setdefault(id(self), on(self.shape, self.dtype)))
+    cache = make_cache()
+    assert copy.copy(cache)._c == cache._c and copy.copy(cache).seq_len is cache.seq_len
+    other = copy.deepcopy({"layers": [cache, make_cache(seq_len=cache.seq_len)]})["layers"]
+    for c in other:
+        assert c._c == fc._PACK(c.k.data_ptr(), c.v.data_ptr(), c.table.data_ptr(), c.seq_len.data_ptr(), 2, 2, 64, 16, 3, 6, 0)
+        assert c.k.data_ptr() != cache.k.data_ptr() and c.seq_len is other[0].seq_len
