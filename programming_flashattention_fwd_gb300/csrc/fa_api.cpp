@@ -293,7 +293,7 @@ const char *fa_strerror(int status)
                                 "no pages for its slots, T == 0, keep < 1 or first + last > keep)";
     case FA_ERR_HEADS: return "FA_ERR_HEADS: Hq and Hkv must be >= 1 with Hq % Hkv == 0";
     case FA_ERR_UNSUPPORTED_D: return "FA_ERR_UNSUPPORTED_D: D must be 64, 128 or 256 (and supported by the selected kernel)";
-    case FA_ERR_ALIGN: return "FA_ERR_ALIGN: 16-bit tensors must be 16-byte aligned, others 4-byte aligned (a workspace as its operator says)";
+    case FA_ERR_ALIGN: return "FA_ERR_ALIGN: q/k/v/o and matrices must be 16-byte aligned, lse and other tensors 4-byte aligned, a workspace as documented";
     case FA_ERR_ALIAS: return "FA_ERR_ALIAS: a tensor that is written overlaps another one";
     case FA_ERR_SCALE: return "FA_ERR_SCALE: scale is NaN or infinite (a cache: or not positive)";
     case FA_ERR_NO_DEVICE: return "FA_ERR_NO_DEVICE: no usable CUDA device";
