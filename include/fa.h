@@ -345,7 +345,8 @@ int fa_cache_weights(const fa_cache_t *cache, const void *q, const float *lse, c
 /*
  * fa_cache_evict -- shrinks every (sequence, KV head) that uses more than `keep` slots to `keep`: it keeps the
  * slots with a position below `first` or at or above next_pos[b] - last, then those of the largest
- * weight (NaN counts as larger than any number), of equal ones the lowest slot.  Kept slots at or above `keep`, in
+ * weight (NaN counts as larger than any number), of equal ones the lowest slot (and where positions at or above
+ * next_pos[b], or the same one twice, protect more than `keep` slots, the lowest of those).  Kept slots at or above `keep`, in
  * order, move to the freed slots below it, in order: their key, value, weight and position.  A
  * kept slot below `keep` stays where it is, so slots are not in the order of their positions afterwards;
  * attention over a cache does not depend on the order, and pos says which token a slot holds.

@@ -248,3 +248,25 @@ def test_evict_with_one_of_its_results_elsewhere(fa, which):  # noqa: F811
     assert all(torch.equal(a, b) for a, b in zip(*outs))
     same = 0 if which == "weight_out" else 1                     # the one whose result went elsewhere is as it was
     assert torch.equal(kept[1][same], c["weight" if same == 0 else "pos"])
+
+
+def test_evict_with_more_protected_slots_than_it_keeps(fa):  # noqa: F811
+    """Positions at or above next_pos, or the same one again and again: the lowest protected slots stay, in order."""
+    g = torch.Generator().manual_seed(190)
+    B, Hkv, D, page, n, keep = 2, 2, 64, 16, 3000, 700
+    per = -(-n // page)
+    c = layer(g, B, 4, Hkv, D, 1, B * per, page, per * page)
+    safe = torch.rand(B, Hkv, per * page, generator=g) < 0.5
+    pos = torch.where(safe, torch.where(torch.rand(safe.shape, generator=g) < 0.3, 1, n + 5), n - 200).to(torch.int32)
+    k, v, w, p = c["k"].clone(), c["v"].clone(), c["weight"].clone(), pos.cuda()
+    fa.cache_evict(fa.KVCache(k, v, ints([n] * B), ints(torch.arange(B * per).reshape(B, per))), w, p, keep, first=2, last=9, next_pos=ints([n] * B))
+    K, V = (x.reshape(B, per, Hkv, page, D).transpose(1, 2).reshape(B, Hkv, -1, D) for x in (c["k"], c["v"]))
+    K2, V2 = (x.reshape(B, per, Hkv, page, D).transpose(1, 2).reshape(B, Hkv, -1, D) for x in (k, v))
+    for b in range(B):
+        for h in range(Hkv):
+            kept = torch.nonzero(safe[b, h, :n])[:keep, 0]
+            slots = torch.arange(keep)
+            slots[~safe[b, h, :keep]] = kept[kept >= keep]
+            slots = slots.cuda()
+            assert torch.equal(w[b, h, :keep], c["weight"][b, h, slots]) and torch.equal(p[b, h, :keep].cpu(), pos[b, h, slots.cpu()])
+            assert torch.equal(K2[b, h, :keep], K[b, h, slots]) and torch.equal(V2[b, h, :keep], V[b, h, slots])

@@ -64,6 +64,8 @@ def attend64(q, kn, vn, per_seq, parent, drafts, scale):
     cpu = lambda x: x.reshape(group, t, *x.shape[1:]).cpu().numpy()  # noqa: E731
     for b in range(B):
         t, n = drafts[b], per_seq[b][0].shape[1]
+        if t == 0:
+            continue
         see = torch.zeros(T, n + t, dtype=torch.bool)
         see[:, :n] = True
         for i in range(t):
