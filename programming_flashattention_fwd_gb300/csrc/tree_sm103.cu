@@ -16,13 +16,13 @@
 // now, and the comparison has not been made again.)
 //
 // Measured, 8 sequences, 32 heads over 8 KV heads, bf16, of 6.8 TB/s copied:
-//     D = 64, 131072 slots    one token 6.8 TB/s, 32 tokens 6.7     D = 256, 65536 slots   7.2, 7.0
+//     D = 64, 131072 slots    one token 6.8 TB/s, 32 tokens 6.7     D = 256, 65536 slots   7.2, 7.1
 //     D = 128, 131072 slots   one token 7.0 TB/s (16-slot pages too), 32 tokens 6.9, 64 tokens (256 rows,
-//                             where the softmax is as busy as memory) 6.0
+//                             where the softmax is as busy as memory) 6.1
 // Short calls are a chain of latencies (start, one unit, second kernel): one sequence, one token, 10 us
 // over 16 slots and 11 over 4096.  So are many short units, about 3 us each of an SM's time, which
 // the reads of the next one only partly cover: 64 x 128 slots 23 us, 64 x 512 39 (3.4 TB/s), 64 x 1024 52 (5.1), 64 x
-// 4096 169 (6.4).
+// 4096 171 (6.3).
 //
 // Per CTA (one per SM):
 //   warps 0, 3    K and V producers (one warp for both: 5.5 instead of 6.4 TB/s at D = 64, 4.9 instead of
@@ -38,7 +38,7 @@
 //                       they are joined in the epilogue, where both read both accumulators (half of
 //                       the columns each)
 //     more (PAIR)       each group has a row tile of its own and takes every step: K and V are read once
-//                       for 256 rows (8 x 64 tokens over up to 16384 slots 102 us, a row tile by itself 139)
+//                       for 256 rows (8 x 64 tokens over up to 16384 slots 102 us, now 93; a row tile by itself 139)
 //     D = 256           one group, 64-key steps (two accumulators do not fit); the other reads half of the result
 //
 // Tensor memory: S_0, S_1 (BN columns each; P, 16-bit, overwrites its S), then the accumulators.

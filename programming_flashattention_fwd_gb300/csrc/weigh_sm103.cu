@@ -15,10 +15,11 @@
 // a drafting step by the one read of K.
 //
 // Measured, 32 heads over 8 KV heads, bf16:
-//     16 rows a head over 4 x 131072 slots    D = 64 5.8 TB/s (98 us; 16-slot pages 4.3), D = 128 6.4 (172 us; 6.3),
-//                                             D = 256 6.8 (321 us; 6.5); one token over 64 x 1024 slots 4.5 (31 us)
-//     a prompt over itself, causal            8192 tokens: D = 64 204 us, D = 128 208 us (1320 TFLOP/s), D = 256
-//                                             344 us (1600); 2048 tokens, D = 128: 26 us; 16384: 770 us (1430)
+//     16 rows a head over 4 x 131072 slots    D = 64 5.9 TB/s (96 us; 16-slot pages 4.3), D = 128 6.5 (170 us; 6.3),
+//                                             D = 256 6.8 (319 us; 6.6); one token over 64 x 1024 slots 4.5 (31 us)
+//     a prompt over itself, causal            8192 tokens: D = 64 203 us, D = 128 208 us (1320 TFLOP/s), D = 256
+//                                             340 us (1620); 2048 tokens, D = 128: 26 us; 16384: 770 us (1430) in
+//                                             bursts, 830 to 850 when repeated for seconds (power limit, 1.9 GHz)
 //     few rows over a short cache             8 to 10 us: start, one tile, second kernel
 // D = 64 has as many exponentials as D = 128 for half the products, and is bound by them.
 //
