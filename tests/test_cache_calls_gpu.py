@@ -270,3 +270,40 @@ def test_evict_with_more_protected_slots_than_it_keeps(fa):  # noqa: F811
             slots = slots.cuda()
             assert torch.equal(w[b, h, :keep], c["weight"][b, h, slots]) and torch.equal(p[b, h, :keep].cpu(), pos[b, h, slots.cpu()])
             assert torch.equal(K2[b, h, :keep], K[b, h, slots]) and torch.equal(V2[b, h, :keep], V[b, h, slots])
+
+
+@pytest.mark.parametrize("D,page", [(64, 16), (128, 48), (256, 32)])
+def test_what_the_lengths_do_not_cover_is_not_used(fa, D, page):  # noqa: F811
+    """Table entries behind a sequence's pages, drafted rows behind draft_len and their parents, path entries behind count,
+    weights and positions behind seq_len hold anything: the results are those with clean ones."""
+    g = torch.Generator().manual_seed(200 + D)
+    B, Hq, Hkv, T, per, n, drafts, counts = 4, 8, 2, 9, 40, [0, 1, 500, 37], [9, 0, 4, 7], [2, 0, 3, 7]
+    c = layer(g, B, Hq, Hkv, D, T, B * per, page, per * page)
+    parent, path = torch.tensor([[-1, 0, 1, 1, 0, 4, 2, 6, 7]] * B), torch.arange(T).repeat(B, 1)
+    clean = torch.arange(B * per).reshape(B, per)
+    results = []
+    for dirty in (False, True):
+        x = {k: t.clone() for k, t in c.items()}
+        table, par, way, seq = clean.clone(), parent.clone(), path.clone(), ints(n)
+        if dirty:
+            for b in range(B):
+                table[b, -(-(n[b] + counts[b]) // page):] = torch.tensor([-1, 2 ** 31 - 1, -2 ** 31, 7])[torch.randint(0, 4, (1,), generator=g)]
+                par[b, drafts[b]:], way[b, counts[b]:] = 2 ** 31 - 1, -2 ** 31
+                x["q"][b, :, drafts[b]:], x["kn"][b, :, drafts[b]:], x["vn"][b, :, drafts[b]:] = float("nan"), float("inf"), float("nan")
+                x["weight"][b, :, n[b] + counts[b]:], x["pos"][b, :, n[b] + counts[b]:] = float("nan"), -2 ** 31
+        cache = fa.KVCache(x["k"], x["v"], seq, ints(table))
+        o, lse = fa.tree_attention(x["q"], x["kn"], x["vn"], cache, parent=ints(par), draft_len=ints(drafts), o=torch.full_like(x["q"], 7),
+                                   lse=torch.full((B, Hq, T), 9.0, device="cuda"))
+        kept = lse.clone()
+        if dirty:
+            for b in range(B):
+                kept[b, :, drafts[b]:] = float("nan")
+        fa.cache_append(cache, x["kn"], x["vn"], path=ints(way), count=ints(counts), weight=x["weight"], pos=x["pos"], start=seq.clone())
+        seq += ints(counts)
+        fa.cache_weights(cache, x["q"], kept, x["weight"], path=ints(way), count=ints(counts))
+        left = fa.cache_evict(cache, x["weight"], x["pos"], 30, first=2, last=5, next_pos=seq)
+        live = [(x["weight"][b, :, :m], x["pos"][b, :, :m]) for b, m in enumerate(left.tolist())]
+        results.append([o, lse, x["k"], x["v"], left] + [t for pair in live for t in pair])
+    assert fa.fa_device_status() == (0, 0)
+    for i, (a, b) in enumerate(zip(*results)):
+        assert torch.equal(a, b), i
