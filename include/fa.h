@@ -126,7 +126,7 @@ const char *fa_strerror(int status);
  * *detail (if non-NULL) receives the raw word: bit 0 = timeout, bits 8..15 = the wait
  * site that expired first.  Each kernel has a word of its own; one call reads and clears all of
  * them and reports the first that is set: forward (two tiles, one tile), GEMM, row softmax,
- * attention over a cache, weights of a cache.
+ * attention over a cache, weights of a cache, gradients of attention.
  */
 int fa_device_status(fa_stream_t stream, uint32_t *detail);
 
@@ -146,6 +146,42 @@ int fa_fwd_debug(const void *q, const void *k, const void *v, void *o, float *ls
                  int B, int Hq, int Hkv, int Sq, int Sk, int D, int causal, float scale,
                  fa_stream_t stream, int is_fp16, uint64_t timeout_ns, uint32_t inject,
                  int kernel, float tau);
+
+/*
+ * fa_bwd -- the gradients of fa_fwd (dtype 0, bf16) or fa_fwd_fp16 (dtype 1), from its inputs, its results and the gradients
+ * of these; the probabilities are computed again from lse:
+ *     p_ij    = exp(scale q_i.k_j - lse_i) for the keys j that query i sees, else 0
+ *     delta_i = sum_d do_id o_id - dlse_i
+ *     ds_ij   = p_ij (do_i.v_j - delta_i)
+ *     dq_i    = scale sum_j ds_ij k_j
+ *     dk_j    = scale sum_hi ds_ij q_i,   dv_j = sum_hi p_ij do_i      (all query heads h of the KV head)
+ *   q .. lse     as fa_fwd took and left them, with its sizes, causal and scale
+ *   d_o          [B, Hq, Sq, D], gradient of o;  dlse [B, Hq, Sq] float32, gradient of lse, or NULL: zero
+ *   dq, dk, dv   like q, k, v: written whole.  dq may be NULL (not computed), and so may dk and dv, both
+ *   workspace    fa_bwd_workspace_bytes(...) bytes, 32-byte aligned; needs no initial value.  A call uses it until its work
+ *                on `stream` is done: calls (and captured graphs) that may run at the same time need workspaces of their own
+ * A query that sees nothing (lse = -inf) adds nothing, a key that no query sees has zero gradients; with Sq == 0 dk and dv are
+ * zeros.  Sums are float32 in a fixed order: the result does not vary from run to run.  p and ds are rounded to
+ * the 16-bit type before the sums over them (in fp16, |do_i.v_j - delta_i| above 65504 becomes infinite).  Inputs are expected to
+ * be finite: an infinity or NaN in a row reaches what shares a tile with it, also where the mask parts them.
+ * FA_ERR_TOO_LARGE: workspace_bytes is too small.  A device wait that gives up leaves NaN in the rows concerned
+ * (fa_device_status).
+ */
+size_t fa_bwd_workspace_bytes(int B, int Hq, int Hkv, int Sq, int Sk, int D);
+int fa_bwd(const void *q, const void *k, const void *v, const void *o, const float *lse, const void *d_o, const float *dlse,
+           void *dq, void *dk, void *dv, int B, int Hq, int Hkv, int Sq, int Sk, int D, int causal, float scale,
+           int dtype, void *workspace, size_t workspace_bytes, fa_stream_t stream);
+
+/*
+ * fa_bwd_debug -- test hook: fa_bwd with an explicit limit of each device wait (timeout_ns, 0 = the default of 2 s)
+ * and a fault-injection mask (inject bit 0: every CTA leaves out the load of its first tile of v or d_o, so that the wait for it
+ * expires; bit 1: only CTA 0).  The call then records FA_ERR_DEVICE_TIMEOUT and leaves NaN in the rows of dq, dk and dv
+ * of the CTAs that gave up; the others hold their results.
+ */
+int fa_bwd_debug(const void *q, const void *k, const void *v, const void *o, const float *lse, const void *d_o,
+                 const float *dlse, void *dq, void *dk, void *dv, int B, int Hq, int Hkv, int Sq, int Sk, int D, int causal,
+                 float scale, int dtype, void *workspace, size_t workspace_bytes, fa_stream_t stream,
+                 uint64_t timeout_ns, uint32_t inject);
 
 /*
  * fa_gemm -- tiled matrix product with an optional fused epilogue, the tutorial's building

@@ -20,4 +20,8 @@ def __getattr__(name):
         from . import cache
         globals()[name] = value = getattr(cache, name)
         return value
+    if name in ("attention_bwd", "bwd_workspace_bytes", "attention_ad"):
+        from . import grad
+        globals()[name] = value = getattr(grad, name)
+        return value
     raise AttributeError(name)

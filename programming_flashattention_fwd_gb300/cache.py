@@ -61,7 +61,7 @@ def _refuse(name: str, t, shape, dtype, index: int):
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
     if t.get_device() != index:
-        raise ValueError(f"{name} is on {t.device} but the cache is on cuda:{index}: "
+        raise ValueError(f"{name} is on {t.device} but the call is on cuda:{index}: "
                          "every tensor of one call must be on the same GPU")
     raise ValueError(f"{name} must be contiguous")
 

@@ -1,0 +1,179 @@
+// bwd_api.cpp -- fa_bwd of include/fa.h: argument checks (before any CUDA call), the division of its workspace, tensor
+// maps and the launches.
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "bwd_internal.h"
+#include "fa.h"
+#include "fa_internal.h"
+
+namespace {
+
+using namespace fa::bwd;
+
+struct Range {
+    uintptr_t at;
+    size_t bytes;
+};
+
+Range range(const void *p, size_t bytes) { return Range{reinterpret_cast<uintptr_t>(p), p ? bytes : 0}; }
+bool overlap(Range a, Range b) { return a.bytes && b.bytes && a.at < b.at + b.bytes && b.at < a.at + a.bytes; }
+bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+// In exchange for fp16's short range the probabilities are held 2^12 times as large there: those below 2^-14, most of
+// them in a long row, would be subnormal.
+float shift_of(int dtype) { return dtype == 1 ? 12.f : 0.f; }
+
+// What a call's workspace holds: lse and delta of the padded rows, then the sums of cut units.
+struct Plan {
+    Shape q, kv;
+    long long pad;
+    size_t vec, part_q, part_kv;   // bytes of one vector, of dQ's parts, of dK's (and again of dV's)
+    size_t bytes() const { return 2 * vec + part_q + 2 * part_kv; }
+};
+
+Plan plan_of(int B, int Hq, int Hkv, int Sq, int Sk, int D, int causal)
+{
+    Plan p;
+    p.pad = ((long long)Sq + kRows - 1) / kRows * kRows;
+    p.vec = (size_t)B * Hq * p.pad * 4;
+    p.q = make_shape(true, B, Hq, Hkv, Sq, Sk, D, causal);
+    p.kv = make_shape(false, B, Hq, Hkv, Sq, Sk, D, causal);
+    p.part_q = p.q.parts > 1 ? (size_t)p.q.num * kRows * D * 4 : 0;
+    p.part_kv = p.kv.parts > 1 ? (size_t)p.kv.num * kRows * D * 4 : 0;
+    return p;
+}
+
+// Sizes that the schedule's 32-bit counts hold.
+int check_sizes(int B, int Hq, int Hkv, int Sq, int Sk, int D, int causal)
+{
+    if (B < 0 || Sq < 0 || Sk < 0) return FA_ERR_BAD_DIM;
+    if (Hq < 1 || Hkv < 1 || Hq % Hkv != 0) return FA_ERR_HEADS;
+    if (D != 64 && D != 128 && D != 256) return FA_ERR_UNSUPPORTED_D;
+    if (causal < 0 || causal > 2) return FA_ERR_CAUSAL;
+    // padded rows are counted, and a step's first column is multiplied out, in 32 bits
+    if (Sq > 0x7fffffff - 256 || Sk > 0x7fffffff - 256) return FA_ERR_BAD_DIM;
+    const double Tq = std::ceil(Sq / 64.0), Tk = std::ceil(Sk / 64.0), most = 2147483647.0;
+    if ((double)B * Hq * (Tq > Tk ? Tq : Tk) > most || (double)(Hq / Hkv) * Tq > most) return FA_ERR_BAD_DIM;
+    return FA_OK;
+}
+
+} // namespace
+
+extern "C" {
+
+size_t fa_bwd_workspace_bytes(int B, int Hq, int Hkv, int Sq, int Sk, int D)
+{
+    if (check_sizes(B, Hq, Hkv, Sq, Sk, D, 0) != FA_OK || B == 0 || Sq == 0 || Sk == 0) return 0;
+    return plan_of(B, Hq, Hkv, Sq, Sk, D, 0).bytes();
+}
+
+int fa_bwd_debug(const void *q, const void *k, const void *v, const void *o, const float *lse, const void *d_o, const float *dlse, void *dq, void *dk, void *dv,
+                 int B, int Hq, int Hkv, int Sq, int Sk, int D, int causal, float scale, int dtype, void *workspace, size_t workspace_bytes, fa_stream_t stream,
+                 uint64_t timeout_ns, uint32_t inject)
+{
+    int st = check_sizes(B, Hq, Hkv, Sq, Sk, D, causal);
+    if (st != FA_OK) return st;
+    if (dtype != 0 && dtype != 1) return FA_ERR_ARG;
+    if (!std::isfinite((float)((double)scale * 1.4426950408889634))) return FA_ERR_SCALE;
+    if (B == 0) return FA_OK;
+    if (Sk == 0 && Sq > 0) return FA_ERR_BAD_DIM;
+    if (Sq == 0 && Sk == 0) return FA_OK;
+    const size_t nq = (size_t)B * Hq * Sq * D * 2, nk = (size_t)B * Hkv * Sk * D * 2, nl = (size_t)B * Hq * Sq * 4;
+    if (!dk != !dv) return FA_ERR_NULL_PTR;
+    if (Sq > 0 && (!q || !k || !v || !o || !lse || !d_o || !workspace)) return FA_ERR_NULL_PTR;
+    if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(o, 16) || !aligned(d_o, 16) || !aligned(dq, 16) || !aligned(dk, 16) ||
+        !aligned(dv, 16) || !aligned(lse, 4) || !aligned(dlse, 4) || !aligned(workspace, 32))
+        return FA_ERR_ALIGN;
+    const Plan plan = plan_of(B, Hq, Hkv, Sq, Sk, D, causal);
+    const size_t need = Sq > 0 ? plan.bytes() : 0;
+    if (workspace_bytes < need) return FA_ERR_TOO_LARGE;
+    const Range all[] = {range(dq, nq), range(dk, nk), range(dv, nk), range(workspace, need), range(q, nq), range(k, nk),
+                         range(v, nk), range(o, nq), range(d_o, nq), range(lse, nl), range(dlse, nl)};
+    for (int i = 0; i < 4; ++i)
+        for (int j = 0; j < (int)(sizeof(all) / sizeof(all[0])); ++j)
+            if (i != j && overlap(all[i], all[j])) return FA_ERR_ALIAS;
+    if (!dq && !dk) return FA_OK;
+    st = fa::check_device();
+    if (st != FA_OK) return st;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (Sq == 0) {   // no query: the sums over them are empty
+        if (dk && (cudaMemsetAsync(dk, 0, nk, s) != cudaSuccess || cudaMemsetAsync(dv, 0, nk, s) != cudaSuccess)) return FA_ERR_LAUNCH;
+        return FA_OK;
+    }
+
+    const bool bf16 = dtype == 0;
+    const int BN = step_rows(D);
+    const long long zq = (long long)B * Hq, zk = (long long)B * Hkv;
+    Maps mq, mk;
+    std::memset(&mq, 0, sizeof(mq));
+    std::memset(&mk, 0, sizeof(mk));
+    using fa::encode_tiles;
+    if (dq && (!encode_tiles(&mq.r1, q, bf16, D, Sq, zq, kRows) || !encode_tiles(&mq.r2, d_o, bf16, D, Sq, zq, kRows) ||
+               !encode_tiles(&mq.s1, k, bf16, D, Sk, zk, BN) || !encode_tiles(&mq.s2, v, bf16, D, Sk, zk, BN)))
+        return FA_ERR_TENSORMAP;
+    if (dk && (!encode_tiles(&mk.r1, k, bf16, D, Sk, zk, kRows) || !encode_tiles(&mk.r2, v, bf16, D, Sk, zk, kRows) ||
+               !encode_tiles(&mk.s1, q, bf16, D, Sq, zq, BN) || !encode_tiles(&mk.s2, d_o, bf16, D, Sq, zq, BN)))
+        return FA_ERR_TENSORMAP;
+
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    float *vec_nl = reinterpret_cast<float *>(ws), *vec_dc = reinterpret_cast<float *>(ws + plan.vec);
+    float *part_q = reinterpret_cast<float *>(ws + 2 * plan.vec), *part_k = reinterpret_cast<float *>(ws + 2 * plan.vec + plan.part_q),
+          *part_v = reinterpret_cast<float *>(ws + 2 * plan.vec + plan.part_q + plan.part_kv);
+    Params p;
+    std::memset(&p, 0, sizeof(p));
+    p.nl = vec_nl;
+    p.dc = vec_dc;
+    p.pad = (int)plan.pad;
+    p.sl2 = (float)((double)scale * 1.4426950408889634);
+    const float shift = shift_of(dtype);
+    p.dscale = std::exp2f(-shift);
+    p.out_scale = scale;
+    p.out_v_scale = p.dscale;
+    p.timeout_ns = timeout_ns;
+    p.inject = inject;
+    cudaError_t e = launch_prep(o, d_o, lse, dlse, vec_nl, vec_dc, zq, Sq, p.pad, D, bf16, shift, s);
+    if (e == cudaSuccess && dk) {
+        Params a = p;
+        a.s = plan.kv;
+        a.out = dk;
+        a.out_v = dv;
+        a.al32 = aligned(dk, 32) && aligned(dv, 32);
+        if (plan.kv.parts > 1) {
+            a.part = part_k;
+            a.part_v = part_v;
+        }
+        if (D == 256) {
+            e = launch_bwd(kV, D, bf16, mk, a, s);
+            if (e == cudaSuccess) e = launch_bwd(kK, D, bf16, mk, a, s);
+        } else {
+            e = launch_bwd(kKV, D, bf16, mk, a, s);
+        }
+    }
+    if (e == cudaSuccess && dq) {
+        Params a = p;
+        a.s = plan.q;
+        a.out = dq;
+        a.al32 = aligned(dq, 32);
+        if (plan.q.parts > 1) a.part = part_q;
+        e = launch_bwd(kQ, D, bf16, mq, a, s);
+    }
+    if (e == cudaSuccess && dk && plan.kv.parts > 1) {
+        e = launch_join(part_k, dk, plan.kv, D, bf16, p.out_scale, s);
+        if (e == cudaSuccess) e = launch_join(part_v, dv, plan.kv, D, bf16, p.out_v_scale, s);
+    }
+    if (e == cudaSuccess && dq && plan.q.parts > 1) e = launch_join(part_q, dq, plan.q, D, bf16, p.out_scale, s);
+    return e == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
+}
+
+int fa_bwd(const void *q, const void *k, const void *v, const void *o, const float *lse, const void *d_o, const float *dlse, void *dq, void *dk, void *dv, int B,
+           int Hq, int Hkv, int Sq, int Sk, int D, int causal, float scale, int dtype, void *workspace, size_t workspace_bytes, fa_stream_t stream)
+{
+    return fa_bwd_debug(q, k, v, o, lse, d_o, dlse, dq, dk, dv, B, Hq, Hkv, Sq, Sk, D, causal, scale, dtype, workspace, workspace_bytes, stream, 0, 0);
+}
+
+} // extern "C"

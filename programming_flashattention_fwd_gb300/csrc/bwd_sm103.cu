@@ -1,0 +1,715 @@
+// bwd_sm103.cu -- attention's backward pass (fa_bwd).
+//
+// With p_ij = exp(scale q_i.k_j - lse_i) recomputed from the forward pass's lse, delta_i = do_i.o_i - dlse_i and
+// ds_ij = p_ij (do_i.v_j - delta_i):
+//   dq_i = scale sum_j ds_ij k_j,   dk_j = scale sum_i ds_ij q_i,   dv_j = sum_i p_ij do_i.
+//
+// Two passes, each of which keeps a tile of 128 rows and its sums on the chip and streams the other side past it:
+// one over the keys (dK and dV together, summed over the query heads of a group), one over the queries (dQ).  Scores and
+// do.v are computed in both, 7 products instead of 5; in exchange nothing is added up in memory: no atomics, no fp32
+// copy of dQ, and the result does not vary from run to run.  One pass would also have to turn ds round through shared memory
+// for dQ, whose reads and writes there would take as long as the two products that it saves: per 128 x 128 scores at
+// D = 128 shared memory would be busy for about 4100 cycles in one pass, and 2300 + 1300 in the two.
+//
+// Resident rows are the lanes of tensor memory: a kernel of the first pass computes S^T = K Q^T and dP^T = V dO^T, so that P^T
+// and dS^T, as 16-bit pairs over their scores, are operands of dV += P^T dO and dK += dS^T Q where they lie; the
+// second pass computes S = Q K^T, dP = dO V^T and dQ += dS K.
+//
+//   warp 0       TMA producer of streamed tiles (first, second, first, ...) into a ring
+//   warp 1       TMEM owner and MMA issuer (whole warp; one elected lane issues)
+//   warp 2       TMA producer of resident tiles, and of the streamed rows' lse and delta (first pass)
+//   warps 4-11   probabilities, their gradients and the results: a thread per resident row and half of a step's columns
+//
+// Order of the products, for the first pass: dP(i) while P(i) is computed; dV(i) and S(i + 1) while dS(i) is computed from
+// dP(i); dK(i), dP(i + 1) while P(i + 1) is.  Tensor memory has room for one S and one dP at D = 128 (256 columns) beside the two sums.
+#include <atomic>
+#include <cstdint>
+
+#include <cuda_fp16.h>
+
+#include "bwd_internal.h"
+#include "cache_device.cuh"
+#include "ptx.cuh"
+#include "watchdog.cuh"
+
+namespace fa {
+namespace bwd {
+
+__device__ unsigned int g_bwd_status;
+
+namespace {
+
+constexpr int THREADS = 384;
+constexpr int kComputeWarps = 8;
+constexpr uint64_t kDefaultTimeoutNs = 2000000000ull;
+
+enum Site : uint32_t { S_EMPTY = 1, S_RES = 2, S_FULL = 3, S_P = 4, S_S = 5, S_DP = 6, S_DS = 7, S_ACC = 8, S_VEC = 9, S_DRAIN = 10, S_SMEM = 11 };
+
+template <int MODE, int D_>
+struct Cfg {
+    static constexpr int D = D_;
+    static constexpr bool ROWQ = MODE == kQ;
+    static constexpr bool HAS_DS = MODE != kV;                 // dP, dS and dQ or dK
+    static constexpr bool HAS_DV = MODE == kKV || MODE == kV;
+    static constexpr int BN = step_rows(D);
+    static constexpr int PANELS = D / 64;
+    // Resident operands in tensor memory (16-bit pairs, D / 2 columns), where it has room: a product with both
+    // operands in shared memory takes as long to read them as to compute.
+    static constexpr bool A1T = MODE == kQ || D == 256;
+    static constexpr bool A2T = MODE == kQ && D <= 128;
+    static constexpr int NSB = (MODE == kV || (D == 64)) ? 2 : 1;   // score buffers
+    static constexpr uint32_t COL_S = 0;
+    static constexpr uint32_t COL_DP = COL_S + NSB * BN;
+    static constexpr uint32_t COL_ACC = COL_DP + (HAS_DS ? BN : 0);
+    static constexpr uint32_t COL_ACCV = COL_ACC + (HAS_DS ? D : 0);
+    static constexpr uint32_t COL_A1 = COL_ACCV + (HAS_DV ? D : 0);
+    static constexpr uint32_t COL_A2 = COL_A1 + (A1T ? D / 2 : 0);
+    static_assert(COL_A2 + (A2T ? D / 2 : 0) <= 512, "tensor-memory columns");
+
+    static constexpr int RTILE = kRows * D * 2, RPANEL = kRows * 128;
+    static constexpr int STILE = BN * D * 2, SPANEL = BN * 128;
+    static constexpr int NR = HAS_DS ? 2 : 1;                  // resident operands
+    static constexpr int NSLOT = D == 64 ? 8 : (D == 128 ? 5 : (MODE == kV ? 4 : 3));
+    static constexpr int NVEC = ROWQ ? 0 : 2;                  // buffers of streamed lse and delta
+    static constexpr int VEC = 2 * BN * 4;
+    static constexpr int OFF_R = 0;
+    static constexpr int OFF_RING = NR * RTILE;
+    static constexpr int OFF_VEC = OFF_RING + NSLOT * STILE;
+    static constexpr int OFF_BAR = OFF_VEC + NVEC * VEC;
+    static constexpr int NBAR = 2 * NSLOT + 2 + 2 + 2 + 1 + 1 + 1 + 2 + 2;
+    static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
+    static constexpr int BYTES = OFF_MISC + 16;
+    static constexpr int ALLOC = BYTES + 1024 <= 232448 ? BYTES + 1024 : 232448;
+    static_assert(BYTES <= 232448, "shared memory");
+};
+
+// Four K-steps (K = 64) with A from tensor memory, at columns a_tmem + 0, T1, T2, T3; B advances BSTEP 16-byte units a step: 2 where
+// it is K-major, 128 where it is MN-major.
+template <uint32_t T1, uint32_t T2, uint32_t T3, uint32_t BSTEP>
+__device__ __forceinline__ void mma_ts4_elect(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t hi, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile("{\n\t.reg .b32 ta, bl;\n\t.reg .b64 b;\n\t.reg .pred p, e, t;\n\t"
+                 "setp.ne.b32 p, %5, 0;\n\tsetp.eq.b32 t, 0, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+                 "mov.b64 b, {%2, %3};\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t"
+                 "add.u32 ta, %1, %6;\n\tadd.u32 bl, %2, %9;\n\tmov.b64 b, {bl, %3};\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [ta], b, %4, t;\n\t"
+                 "add.u32 ta, %1, %7;\n\tadd.u32 bl, bl, %9;\n\tmov.b64 b, {bl, %3};\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [ta], b, %4, t;\n\t"
+                 "add.u32 ta, %1, %8;\n\tadd.u32 bl, bl, %9;\n\tmov.b64 b, {bl, %3};\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [ta], b, %4, t;\n\t}" ::"r"(d_tmem),
+                 "r"(a_tmem), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate), "n"(T1), "n"(T2), "n"(T3), "n"(BSTEP)
+                 : "memory");
+}
+
+// 16 columns of a 128-row, K-major operand into 8 columns of tensor memory (lane = row).
+__device__ __forceinline__ void copy_elect(uint32_t t_dst, uint32_t s_lo, uint32_t hi)
+{
+    asm volatile("{\n\t.reg .b64 a;\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tmov.b64 a, {%1, %2};\n\t"
+                 "@e tcgen05.cp.cta_group::1.128x256b [%0], a;\n\t}" ::"r"(t_dst), "r"(s_lo), "r"(hi)
+                 : "memory");
+}
+
+__device__ __forceinline__ void ld_shared_2x64(uint32_t addr, uint64_t &a, uint64_t &b)
+{
+    asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "r"(addr) : "memory");
+}
+
+// Row r of tile t of a result, columns [c0, c0 + n): 32 sums a time out of tensor memory, scaled and rounded (or, for a
+// part of a cut unit, as they are).
+template <int D, bool BF16>
+__device__ __forceinline__ void write_row(uint32_t tAcc, void *out, float *part, size_t row, bool valid, int c0, int n, float scale, uint32_t al32)
+{
+    const uint64_t s2 = f2_pack(scale, scale);
+#pragma unroll 1
+    for (int c = c0; c < c0 + n; c += 32) {
+        uint32_t v[32];
+        tmem_ld_x32(tAcc + c, v);
+        tmem_wait_ld();
+        reg_fence_x32(v);
+        if (part) {
+            float *to = part + row * D + c;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) st_global_v8(to + 8 * i, v + 8 * i);
+            continue;
+        }
+        uint32_t pk[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            float lo, hi;
+            f2_unpack(f2_mul(f2_pack(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), s2), lo, hi);
+            pk[e] = pack2<BF16>(lo, hi);
+        }
+        uint8_t *to = static_cast<uint8_t *>(out) + (row * D + c) * 2;
+        if (valid) {
+            if (al32) {
+                st_global_v8(to, pk);
+                st_global_v8(to + 32, pk + 8);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) st_global_v4(to + 16 * i, pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+            }
+        }
+        __syncwarp();   // the next load takes the whole warp
+    }
+}
+
+// The same row filled with `word` (zero, or all ones: NaN in every type).
+template <int D>
+__device__ __forceinline__ void fill_row(void *out, float *part, size_t row, bool valid, int c0, int n, uint32_t word)
+{
+    if (part) {
+        for (int c = c0; c < c0 + n; c += 4) st_global_v4(part + row * D + c, word, word, word, word);
+    } else if (valid) {
+        for (int c = c0; c < c0 + n; c += 8) st_global_v4(static_cast<uint8_t *>(out) + (row * D + c) * 2, word, word, word, word);
+    }
+}
+
+template <int MODE, int D, bool BF16>
+__global__ void __launch_bounds__(THREADS, 1)
+    bwd_kernel(const __grid_constant__ CUtensorMap tmR1, const __grid_constant__ CUtensorMap tmR2, const __grid_constant__ CUtensorMap tmS1,
+               const __grid_constant__ CUtensorMap tmS2, const __grid_constant__ Params p)
+{
+    using C = Cfg<MODE, D>;
+    constexpr int BN = C::BN;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t pad = (1024u - (raw & 1023u)) & 1023u;
+    uint8_t *smem = smem_raw + pad;
+    const uint32_t sb = raw + pad;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    const uint32_t sR1 = sb + C::OFF_R, sR2 = sR1 + C::RTILE, sRing = sb + C::OFF_RING, sVec = sb + C::OFF_VEC, bar0 = sb + C::OFF_BAR;
+    auto bar_full = [&](uint32_t s) { return bar0 + 8u * s; };
+    auto bar_empty = [&](uint32_t s) { return bar0 + 8u * (C::NSLOT + s); };
+    const uint32_t barRes = bar0 + 8u * (2 * C::NSLOT);   // resident tiles loaded
+    const uint32_t barFree = barRes + 8;                  // resident tiles no longer read
+    // Step g signals S ready and P written (or S read) on barS / barP + 8 (g & 1), phase (g / 2) & 1: with two score buffers
+    // the threads that compute may be a step ahead of the MMA warp's wait.
+    const uint32_t barS = barRes + 16, barP = barRes + 32;
+    const uint32_t barDP = barRes + 48, barDS = barRes + 56, barAcc = barRes + 64;
+    const uint32_t barVec = barRes + 72, barVecFree = barRes + 88;
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(smem + C::OFF_MISC);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 4);
+    unsigned int *status = &g_bwd_status;
+    const uint64_t tmo = p.timeout_ns;
+
+    const int r = (warp & 3) * 32 + lane;   // resident row of a computing thread
+    const int half = (warp - 4) >> 2;       // its half of a step's columns and of the results' columns
+    auto each_unit_filled = [&](uint32_t word) {
+        Unit u;
+        for (int round = 0; unit_at<C::ROWQ, BN>(p.s, gridDim.x, blockIdx.x, round, u); ++round) {
+            const int row = u.t * kRows + r;
+            const bool valid = row < p.s.rows;
+            const size_t at = p.part || p.part_v ? (size_t)u.slot * kRows + r : (size_t)u.z * p.s.rows + row;
+            if (C::HAS_DS) fill_row<D>(p.out, p.part, at, valid, half * (D / 2), D / 2, word);
+            if (C::HAS_DV) fill_row<D>(p.out_v, p.part_v, at, valid, half * (D / 2), D / 2, word);
+        }
+    };
+
+    if (pad + (uint32_t)C::BYTES > dynamic_smem_size_u32()) {
+        if (threadIdx.x == 0) atomicOr(status, 1u | (S_SMEM << 8));
+        if (warp >= 4) each_unit_filled(~0u);
+        return;
+    }
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::NSLOT; ++s) {
+            mbar_init(bar_full(s), 1);
+            mbar_init(bar_empty(s), 1);
+        }
+        mbar_init(barRes, 1);
+        mbar_init(barFree, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(barS + 8 * i, 1);
+            mbar_init(barP + 8 * i, kComputeWarps);
+            mbar_init(barVec + 8 * i, 1);
+            mbar_init(barVecFree + 8 * i, kComputeWarps);
+        }
+        mbar_init(barDP, 1);
+        mbar_init(barDS, kComputeWarps);
+        mbar_init(barAcc, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(tmem_holder), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_holder;
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ streamed tiles, in the order of their first use
+        if (lane == 0) {
+            uint32_t use = 0, skip = ~0u;
+            const bool inj = (p.inject & 1u) || ((p.inject & 2u) && blockIdx.x == 0);
+            const uint64_t keep = l2_policy_evict_last();
+            bool ok = true;
+            auto load = [&](const CUtensorMap *m, int tile, int plane, bool second) {
+                const uint32_t s = use % C::NSLOT;
+                if (!bounded_wait(bar_empty(s), ((use / C::NSLOT) & 1) ^ 1, abort_flag, tmo, S_EMPTY, status)) return false;
+                if (inj && second && skip == ~0u) {
+                    skip = use++;
+                    return true;
+                }
+                mbar_arrive_expect_tx(bar_full(s), C::STILE);
+#pragma unroll
+                for (int pn = 0; pn < C::PANELS; ++pn)
+                    tma_load_3d_hint(sRing + s * C::STILE + pn * C::SPANEL, m, pn * 64, tile * BN, plane, bar_full(s), keep);
+                ++use;
+                return true;
+            };
+            Unit u;
+            for (int round = 0; ok && unit_at<C::ROWQ, BN>(p.s, gridDim.x, blockIdx.x, round, u); ++round) {
+                int plane = u.plane, tile = u.tile;
+                for (int j = 0; j < u.n && ok; ++j) {
+                    ok = load(&tmS1, tile, plane, false) && load(&tmS2, tile, plane, true);
+                    if (++tile == u.end) {
+                        tile = u.first;
+                        ++plane;
+                    }
+                }
+            }
+            for (uint32_t x = use > C::NSLOT ? use - C::NSLOT : 0; x < use; ++x)
+                if (x != skip) bounded_wait(bar_full(x % C::NSLOT), (x / C::NSLOT) & 1, abort_flag, tmo, S_DRAIN, status, false);
+        }
+    } else if (warp == 2) {
+        // ------------------------------------------------------------ resident tiles; lse and delta of streamed queries
+        if (lane == 0) {
+            uint32_t units = 0, g = 0;
+            bool ok = true;
+            Unit u;
+            for (int round = 0; ok && unit_at<C::ROWQ, BN>(p.s, gridDim.x, blockIdx.x, round, u); ++round) {
+                if (u.n == 0) continue;
+                if (units > 0 && !bounded_wait(barFree, (units - 1) & 1, abort_flag, tmo, S_RES, status)) break;
+                mbar_arrive_expect_tx(barRes, C::NR * C::RTILE);
+#pragma unroll
+                for (int pn = 0; pn < C::PANELS; ++pn) {
+                    tma_load_3d(sR1 + pn * C::RPANEL, &tmR1, pn * 64, u.t * kRows, u.z, barRes);
+                    if (C::HAS_DS) tma_load_3d(sR2 + pn * C::RPANEL, &tmR2, pn * 64, u.t * kRows, u.z, barRes);
+                }
+                ++units;
+                if constexpr (!C::ROWQ) {
+                    int plane = u.plane, tile = u.tile;
+                    for (int j = 0; j < u.n && ok; ++j, ++g) {
+                        const uint32_t v = g & 1;
+                        ok = bounded_wait(barVecFree + 8 * v, ((g >> 1) & 1) ^ 1, abort_flag, tmo, S_VEC, status);
+                        if (!ok) break;
+                        const size_t at = (size_t)plane * p.pad + (size_t)tile * BN;
+                        mbar_arrive_expect_tx(barVec + 8 * v, C::VEC);
+                        bulk_load(sVec + v * C::VEC, p.nl + at, BN * 4, barVec + 8 * v);
+                        bulk_load(sVec + v * C::VEC + BN * 4, p.dc + at, BN * 4, barVec + 8 * v);
+                        if (++tile == u.end) {
+                            tile = u.first;
+                            ++plane;
+                        }
+                    }
+                }
+            }
+            if (units > 0) bounded_wait(barRes, (units - 1) & 1, abort_flag, tmo, S_DRAIN, status, false);
+            for (uint32_t x = g > 2 ? g - 2 : 0; x < g; ++x) bounded_wait(barVec + 8 * (x & 1), (x >> 1) & 1, abort_flag, tmo, S_DRAIN, status, false);
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA issuer (whole warp)
+        constexpr uint32_t idS = idesc_f16(BF16, kRows, BN, false), idAcc = idesc_f16(BF16, kRows, D, true);
+        constexpr uint32_t HI = sdesc_hi_sw128(1024);
+        const cache::WarpWait wait{abort_flag, tmo, status};
+        auto slot = [&](uint32_t use) { return sRing + (use % C::NSLOT) * C::STILE; };
+        auto wait_full = [&](uint32_t use) { return wait(bar_full(use % C::NSLOT), (use / C::NSLOT) & 1, S_FULL); };
+        auto free_slot = [&](uint32_t use) { tc_commit_elect(bar_empty(use % C::NSLOT)); };
+        // scores: D columns of the resident operand against BN streamed rows (both K-major)
+        auto issue_scores = [&](uint32_t d, bool in_tmem, uint32_t tA, uint32_t sA, uint32_t sB) {
+#pragma unroll
+            for (int pn = 0; pn < C::PANELS; ++pn) {
+                const uint32_t blo = sdesc_lo(sB + pn * C::SPANEL, 16);
+                if (in_tmem)
+                    mma_ts4_elect<8, 16, 24, 2>(d, tA + 32 * pn, blo, HI, idS, pn > 0);
+                else
+                    mma_ss_kk4_elect(d, sdesc_lo(sA + pn * C::RPANEL, 16), blo, HI, idS, pn > 0);
+            }
+        };
+        // sums += (P or dS, 16-bit pairs, each half of the columns over its own scores) x streamed rows (MN-major)
+        auto issue_sums = [&](uint32_t d, uint32_t tP, uint32_t sB, bool first) {
+            const uint32_t blo = sdesc_lo(sB, C::SPANEL);
+            if constexpr (BN == 128) {
+                mma_ts4_elect<8, 16, 24, 128>(d, tP, blo, HI, idAcc, first ? 0u : 1u);
+                mma_ts4_elect<8, 16, 24, 128>(d, tP + 64, blo + 512, HI, idAcc, 1u);
+            } else {
+                mma_ts4_elect<8, 32, 40, 128>(d, tP, blo, HI, idAcc, first ? 0u : 1u);
+            }
+        };
+        auto tS = [&](uint32_t gs) { return tmem + C::COL_S + (C::NSB == 2 ? (gs & 1) * BN : 0); };
+        uint32_t g = 0, units = 0;   // steps and units so far; step g's tiles are the ring's loads 2 g and 2 g + 1
+        bool ok = true;
+        auto do_s = [&](uint32_t gs) {
+            if (!wait_full(2 * gs)) return false;
+            tc_fence_after();
+            issue_scores(tS(gs), C::A1T, tmem + C::COL_A1, sR1, slot(2 * gs));
+            tc_commit_elect(barS + 8 * (gs & 1));
+            if (!C::HAS_DS) free_slot(2 * gs);
+            return true;
+        };
+        auto do_dp = [&](uint32_t gs, bool last) {
+            if (!wait_full(2 * gs + 1)) return false;
+            tc_fence_after();
+            issue_scores(tmem + C::COL_DP, C::A2T, tmem + C::COL_A2, sR2, slot(2 * gs + 1));
+            tc_commit_elect(barDP);
+            if (!C::HAS_DV) free_slot(2 * gs + 1);
+            if (last && !(C::A1T && C::A2T)) tc_commit_elect(barFree);   // S and dP were the readers of the resident tiles
+            return true;
+        };
+        Unit u;
+        for (int round = 0; ok && unit_at<C::ROWQ, BN>(p.s, gridDim.x, blockIdx.x, round, u); ++round) {
+            if (u.n == 0) continue;
+            ok = wait(barRes, units & 1, S_RES);
+            if (!ok) break;
+            ++units;
+            tc_fence_after();
+            // The readers of the operands' columns, the scores of the unit before, are done: their last results were
+            // read before the last wait above.
+#pragma unroll
+            for (int pn = 0; pn < C::PANELS; ++pn)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    if (C::A1T) copy_elect(tmem + C::COL_A1 + 32 * pn + 8 * k, sdesc_lo(sR1 + pn * C::RPANEL, 16) + 2 * k, HI);
+                    if (C::A2T) copy_elect(tmem + C::COL_A2 + 32 * pn + 8 * k, sdesc_lo(sR2 + pn * C::RPANEL, 16) + 2 * k, HI);
+                }
+            if (C::A1T && (C::A2T || !C::HAS_DS)) tc_commit_elect(barFree);
+            ok = do_s(g);
+            if (ok && C::HAS_DS) ok = do_dp(g, u.n == 1);
+            for (int j = 0; j < u.n && ok; ++j) {
+                const uint32_t gs = g + j;
+                const bool more = j + 1 < u.n;
+                if (C::NSB == 2 && more) ok = do_s(gs + 1);
+                ok = ok && wait(barP + 8 * (gs & 1), (gs >> 1) & 1, S_P);
+                if (!ok) break;
+                tc_fence_after();
+                if constexpr (C::HAS_DV) {
+                    if (!C::HAS_DS) {   // otherwise dP's products have waited for the tile
+                        ok = wait_full(2 * gs + 1);
+                        if (!ok) break;
+                        tc_fence_after();
+                    }
+                    issue_sums(tmem + C::COL_ACCV, tS(gs), slot(2 * gs + 1), j == 0);
+                    free_slot(2 * gs + 1);
+                }
+                if (C::NSB == 1 && more) ok = do_s(gs + 1);
+                if constexpr (C::HAS_DS) {
+                    ok = ok && wait(barDS, gs & 1, S_DS);
+                    if (!ok) break;
+                    tc_fence_after();
+                    issue_sums(tmem + C::COL_ACC, tmem + C::COL_DP, slot(2 * gs), j == 0);
+                    free_slot(2 * gs);
+                    if (more) ok = do_dp(gs + 1, j + 2 == u.n);
+                }
+            }
+            if (!ok) break;
+            tc_commit_elect(barAcc);
+            g += u.n;
+        }
+        if (!ok) tc_commit_elect(barAcc);   // everything issued ends before tensor memory is given back
+        bounded_wait(barAcc, (units - 1) & 1, abort_flag, tmo, S_DRAIN, status, false);
+        if (ok && units > 0) {   // no arrival is still on its way to this CTA's barriers when it ends
+            bounded_wait(barFree, (units - 1) & 1, abort_flag, tmo, S_DRAIN, status, false);
+            for (uint32_t x = 2 * g > C::NSLOT ? 2 * g - C::NSLOT : 0; x < 2 * g; ++x)
+                bounded_wait(bar_empty(x % C::NSLOT), (x / C::NSLOT) & 1, abort_flag, tmo, S_DRAIN, status, false);
+        }
+        __syncwarp();
+    } else if (warp >= 4) {
+        // ------------------------------------------------------------ probabilities, gradients, results
+        constexpr int HB = BN / 2;   // columns of a thread
+        const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+        const cache::WarpWait wait{abort_flag, tmo, status};
+        const uint64_t sl2 = f2_pack(p.sl2, p.sl2), cc = f2_pack(p.dscale, p.dscale);
+        auto publish = [&](uint32_t bar) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar);
+        };
+        uint32_t g = 0, units = 0;
+        bool ok = true;
+        Unit u;
+        for (int round = 0; ok && unit_at<C::ROWQ, BN>(p.s, gridDim.x, blockIdx.x, round, u); ++round) {
+            const int row = u.t * kRows + r;
+            const bool valid = row < p.s.rows, parts = p.s.parts > 1;
+            const size_t at = parts ? (size_t)u.slot * kRows + r : (size_t)u.z * p.s.rows + row;
+            float *part = parts ? p.part : nullptr, *part_v = parts ? p.part_v : nullptr;
+            if (u.n == 0) {   // nothing is seen: the sums are empty
+                if (C::HAS_DS) fill_row<D>(p.out, part, at, valid, half * (D / 2), D / 2, 0u);
+                if (C::HAS_DV) fill_row<D>(p.out_v, part_v, at, valid, half * (D / 2), D / 2, 0u);
+                continue;
+            }
+            uint64_t nl_row = 0, dc_row = 0;
+            if constexpr (C::ROWQ) {   // the padded rows behind Sq have entries too
+                const float nl = p.nl[(size_t)u.z * p.pad + row], dc = p.dc[(size_t)u.z * p.pad + row];
+                nl_row = f2_pack(nl, nl);
+                dc_row = f2_pack(dc, dc);
+            }
+            int tile = u.tile;
+            for (int j = 0; j < u.n; ++j) {
+                const uint32_t gs = g + j, par = (gs >> 1) & 1;
+                const uint32_t tSb = tmem + lane_off + C::COL_S + (C::NSB == 2 ? (gs & 1) * BN : 0) + half * HB;
+                const uint32_t vec = sVec + (gs & 1) * C::VEC + half * HB * 4;
+                if (!C::ROWQ) ok = wait(barVec + 8 * (gs & 1), par, S_VEC);
+                ok = ok && wait(barS + 8 * (gs & 1), par, S_S);
+                if (!ok) break;
+                tc_fence_after();
+                uint32_t sv[HB];
+#pragma unroll
+                for (int c = 0; c < HB; c += 32) tmem_ld_x32(tSb + c, *reinterpret_cast<uint32_t(*)[32]>(sv + c));
+                tmem_wait_ld();
+#pragma unroll
+                for (int c = 0; c < HB; c += 32) reg_fence_x32(*reinterpret_cast<uint32_t(*)[32]>(sv + c));
+                if (!C::HAS_DV) publish(barP + 8 * (gs & 1));   // the scores may be overwritten
+                float *s = reinterpret_cast<float *>(sv);
+#pragma unroll
+                for (int c = 0; c < HB; c += 4) {
+                    uint64_t n0 = nl_row, n1 = nl_row;
+                    if constexpr (!C::ROWQ) ld_shared_2x64(vec + 4 * c, n0, n1);
+                    float t0, t1, t2, t3;
+                    f2_unpack(f2_fma(f2_pack(s[c], s[c + 1]), sl2, n0), t0, t1);
+                    f2_unpack(f2_fma(f2_pack(s[c + 2], s[c + 3]), sl2, n1), t2, t3);
+                    s[c] = ex2_approx(t0);
+                    s[c + 1] = ex2_approx(t1);
+                    s[c + 2] = ex2_approx(t2);
+                    s[c + 3] = ex2_approx(t3);
+                }
+                // Masked pairs; streamed queries behind the last have lse = inf, that is p = 0, already.
+                const int base = tile * BN;
+                if constexpr (C::ROWQ) {
+                    if (base + BN > p.s.cols || (p.s.causal && base + BN - 1 > u.t * kRows + p.s.coff)) {
+                        long long lim = p.s.cols - 1;
+                        if (p.s.causal) lim = min(lim, (long long)row + p.s.coff);
+                        const int last = (int)max(lim - base - half * HB, -1ll);
+#pragma unroll
+                        for (int c = 0; c < HB; ++c)
+                            if (c > last) s[c] = 0.f;
+                    }
+                } else if (p.s.causal && (long long)u.t * kRows + kRows - 1 - p.s.coff > base) {
+                    const long long lim = (long long)row - p.s.coff - base - half * HB;
+                    const int from = (int)min(max(lim, 0ll), (long long)HB);
+#pragma unroll
+                    for (int c = 0; c < HB; ++c)
+                        if (c < from) s[c] = 0.f;
+                }
+                if constexpr (C::HAS_DV) {
+#pragma unroll
+                    for (int c = 0; c < HB; c += 32) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) pk[e] = pack2<BF16>(s[c + 2 * e], s[c + 2 * e + 1]);
+                        tmem_st_x16(tSb + c / 2, pk);
+                    }
+                    tmem_wait_st();
+                    publish(barP + 8 * (gs & 1));
+                }
+                if constexpr (C::HAS_DS) {
+                    const uint32_t tDP = tmem + lane_off + C::COL_DP + half * HB;
+                    ok = wait(barDP, gs & 1, S_DP);
+                    if (!ok) break;
+                    tc_fence_after();
+                    uint32_t ds[HB / 2];
+#pragma unroll
+                    for (int c = 0; c < HB; c += 32) {
+                        uint32_t dv[32];
+                        tmem_ld_x32(tDP + c, dv);
+                        tmem_wait_ld();
+                        reg_fence_x32(dv);
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4) {
+                            uint64_t d0 = dc_row, d1 = dc_row;
+                            if constexpr (!C::ROWQ) ld_shared_2x64(vec + BN * 4 + 4 * (c + e), d0, d1);   
+                            const uint64_t x0 = f2_fma(f2_pack(__uint_as_float(dv[e]), __uint_as_float(dv[e + 1])), cc, d0);
+                            const uint64_t x1 = f2_fma(f2_pack(__uint_as_float(dv[e + 2]), __uint_as_float(dv[e + 3])), cc, d1);
+                            float a, b;
+                            f2_unpack(f2_mul(x0, f2_pack(s[c + e], s[c + e + 1])), a, b);
+                            ds[(c + e) / 2] = pack2<BF16>(a, b);
+                            f2_unpack(f2_mul(x1, f2_pack(s[c + e + 2], s[c + e + 3])), a, b);
+                            ds[(c + e) / 2 + 1] = pack2<BF16>(a, b);
+                        }
+                    }
+#pragma unroll
+                    for (int c = 0; c < HB; c += 32) tmem_st_x16(tDP + c / 2, *reinterpret_cast<uint32_t(*)[16]>(ds + c / 2));
+                    tmem_wait_st();
+                    publish(barDS);
+                }
+                if (!C::ROWQ) {
+                    if (!C::HAS_DS) __syncwarp();
+                    if (lane == 0) mbar_arrive(barVecFree + 8 * (gs & 1));
+                }
+                if (++tile == u.end) tile = u.first;
+            }
+            ok = ok && wait(barAcc, units & 1, S_ACC);
+            if (!ok) break;
+            tc_fence_after();
+            g += u.n;
+            ++units;
+            if (C::HAS_DS) write_row<D, BF16>(tmem + lane_off + C::COL_ACC, p.out, part, at, valid, half * (D / 2), D / 2, p.out_scale, p.al32);
+            if (C::HAS_DV) write_row<D, BF16>(tmem + lane_off + C::COL_ACCV, p.out_v, part_v, at, valid, half * (D / 2), D / 2, p.out_v_scale, p.al32);
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    } else if (warp >= 4 && *abort_flag) {
+        each_unit_filled(~0u);   // this CTA gave up on a wait: NaN in every row that it was given
+    }
+}
+
+template <int MODE, int D, bool BF16>
+cudaError_t launch_one(const Maps &m, const Params &p, cudaStream_t stream)
+{
+    using C = Cfg<MODE, D>;
+    auto kern = bwd_kernel<MODE, D, BF16>;
+    static std::atomic<uint64_t> configured{0};
+    static std::atomic<int> sm_count[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    const uint64_t bit = 1ull << dev;
+    if (!(configured.load(std::memory_order_acquire) & bit)) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::ALLOC);
+        if (e != cudaSuccess) return e;
+        int nsm = 0;
+        e = cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev);
+        if (e != cudaSuccess) return e;
+        sm_count[dev].store(nsm, std::memory_order_relaxed);
+        configured.fetch_or(bit, std::memory_order_acq_rel);
+    }
+    Params q = p;
+    if (q.timeout_ns == 0) q.timeout_ns = kDefaultTimeoutNs;
+    const int sms = sm_count[dev].load(std::memory_order_relaxed), grid = q.s.num < sms ? q.s.num : sms;
+    kern<<<grid, THREADS, C::ALLOC, stream>>>(m.r1, m.r2, m.s1, m.s2, q);
+    return cudaGetLastError();
+}
+
+// ---------------------------------------------------------------- lse and delta
+// nl = -lse log2 e + shift and dc = (do.o - dlse) 2^-shift of every row, sums in fp32; rows at or behind Sq, and rows that saw nothing
+// (lse = -inf), get nl = -inf, so that their probabilities are 0 without another mask.  Bound by memory: do and o
+// are read once, 16 bytes a lane, D / 8 lanes a row.
+constexpr int kPrepThreads = 256;
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kPrepThreads) prep_kernel(const uint4 *o, const uint4 *d_o, const float *lse, const float *dlse, float *nl, float *dc,
+                                                            long long rows, int Sq, int pad, float shift, float down)
+{
+    constexpr int L = D / 8;
+    const long long i = (long long)blockIdx.x * (kPrepThreads / L) + threadIdx.x / L;   // row of the padded arrays
+    const int lane = threadIdx.x % L;
+    if (i >= rows) return;
+    const long long plane = i / pad;
+    const int q = (int)(i - plane * pad);
+    float sum = 0.f;
+    const size_t row = (size_t)plane * Sq + q;
+    if (q < Sq) {
+        const uint4 a = o[row * L + lane], b = d_o[row * L + lane];
+        const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            float2 f, g;
+            if (BF16) {
+                f = make_float2(__uint_as_float(x[e] << 16), __uint_as_float(x[e] & 0xffff0000u));
+                g = make_float2(__uint_as_float(y[e] << 16), __uint_as_float(y[e] & 0xffff0000u));
+            } else {
+                f = __half22float2(*reinterpret_cast<const __half2 *>(&x[e]));
+                g = __half22float2(*reinterpret_cast<const __half2 *>(&y[e]));
+            }
+            sum = fmaf(f.x, g.x, fmaf(f.y, g.y, sum));
+        }
+    }
+#pragma unroll
+    for (int d = L / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
+    if (lane == 0) {
+        float n = -INFINITY, c = 0.f;
+        if (q < Sq) {
+            const float l = lse[row];
+            n = l == -INFINITY ? -INFINITY : fmaf(-l, 1.4426950408889634f, shift);
+            c = -(sum - (dlse ? dlse[row] : 0.f)) * down;
+        }
+        nl[i] = n;
+        dc[i] = c;
+    }
+}
+
+template <int D, bool BF16>
+cudaError_t prep_one(const void *o, const void *d_o, const float *lse, const float *dlse, float *nl, float *dc, long long planes, int Sq, int pad, float shift,
+                     cudaStream_t st)
+{
+    constexpr int per = kPrepThreads / (D / 8);
+    const long long rows = planes * pad, blocks = (rows + per - 1) / per;
+    prep_kernel<D, BF16><<<(unsigned)blocks, kPrepThreads, 0, st>>>(static_cast<const uint4 *>(o), static_cast<const uint4 *>(d_o), lse, dlse, nl, dc, rows, Sq, pad,
+                                                                   shift, exp2f(-shift));
+    return cudaGetLastError();
+}
+
+// ---------------------------------------------------------------- parts of cut units, added in their order
+template <bool BF16>
+__global__ void __launch_bounds__(256) join_kernel(const float4 *part, uint2 *out, int parts, int rows, int tiles, int quads, long long n, float scale)
+{
+    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;   // four columns of one row of a unit
+    if (i >= n) return;
+    const int in_unit = kRows * quads;
+    const long long unit = i / in_unit;
+    const int e = (int)(i - unit * in_unit), row = (int)(unit % tiles) * kRows + e / quads;
+    if (row >= rows) return;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = 0; k < parts; ++k) {
+        const float4 x = part[(unit * parts + k) * in_unit + e];
+        s.x += x.x;
+        s.y += x.y;
+        s.z += x.z;
+        s.w += x.w;
+    }
+    out[((unit / tiles) * rows + row) * quads + e % quads] = make_uint2(pack2<BF16>(s.x * scale, s.y * scale), pack2<BF16>(s.z * scale, s.w * scale));
+}
+
+} // namespace
+
+cudaError_t launch_prep(const void *o, const void *d_o, const float *lse, const float *dlse, float *nl, float *dc, long long planes, int Sq, int pad, int D,
+                        bool bf16, float shift, cudaStream_t st)
+{
+#define CASE(DD, BB) if (D == DD && bf16 == BB) return prep_one<DD, BB>(o, d_o, lse, dlse, nl, dc, planes, Sq, pad, shift, st);
+    CASE(64, true) CASE(64, false) CASE(128, true) CASE(128, false) CASE(256, true) CASE(256, false)
+#undef CASE
+    return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_bwd(int mode, int D, bool bf16, const Maps &m, const Params &p, cudaStream_t st)
+{
+#define CASE(MM, DD) if (mode == MM && D == DD) return bf16 ? launch_one<MM, DD, true>(m, p, st) : launch_one<MM, DD, false>(m, p, st);
+    CASE(kQ, 64) CASE(kQ, 128) CASE(kQ, 256) CASE(kKV, 64) CASE(kKV, 128) CASE(kK, 256) CASE(kV, 256)
+#undef CASE
+    return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_join(const float *part, void *out, const Shape &s, int D, bool bf16, float scale, cudaStream_t st)
+{
+    const long long n = (long long)s.planes * s.tiles * kRows * (D / 4);
+    const unsigned blocks = (unsigned)((n + 255) / 256);
+    if (bf16)
+        join_kernel<true><<<blocks, 256, 0, st>>>(reinterpret_cast<const float4 *>(part), static_cast<uint2 *>(out), s.parts, s.rows, s.tiles, D / 4, n, scale);
+    else
+        join_kernel<false><<<blocks, 256, 0, st>>>(reinterpret_cast<const float4 *>(part), static_cast<uint2 *>(out), s.parts, s.rows, s.tiles, D / 4, n, scale);
+    return cudaGetLastError();
+}
+
+cudaError_t read_and_clear_bwd_status(uint32_t *word)
+{
+    unsigned int w = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(&w, g_bwd_status, sizeof(w));
+    if (e != cudaSuccess) return e;
+    const unsigned int zero = 0;
+    e = cudaMemcpyToSymbol(g_bwd_status, &zero, sizeof(zero));
+    if (word) *word = w;
+    return e;
+}
+
+} // namespace bwd
+} // namespace fa

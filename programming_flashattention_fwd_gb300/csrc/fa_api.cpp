@@ -10,6 +10,7 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
+#include "bwd_internal.h"
 #include "cache_internal.h"
 #include "fa.h"
 #include "fa_internal.h"
@@ -63,6 +64,12 @@ bool encode(EncodeTiledFn enc, CUtensorMap *m, const void *base, bool bf16, int 
 } // namespace
 
 namespace fa {
+
+bool encode_tiles(CUtensorMap *m, const void *base, bool bf16, int D, int S, long long planes, int rows)
+{
+    const EncodeTiledFn enc = get_encode_fn();
+    return enc && encode(enc, m, base, bf16, D, S, planes, rows);
+}
 
 // Device checks shared by every entry point (current device must be sm_103).
 int check_device()
@@ -312,11 +319,11 @@ const char *fa_strerror(int status)
 int fa_device_status(fa_stream_t stream, uint32_t *detail)
 {
     // every kernel's word is read and cleared; of those that are set the first in this order is reported
-    uint32_t word[6] = {};
+    uint32_t word[7] = {};
     if (fa::read_and_clear_status(reinterpret_cast<cudaStream_t>(stream), &word[0]) != cudaSuccess ||
         fa::read_and_clear_fa1_status(&word[1]) != cudaSuccess || fa::read_and_clear_gemm_status(&word[2]) != cudaSuccess ||
         fa::read_and_clear_softmax_status(&word[3]) != cudaSuccess || fa::cache::read_and_clear_tree_status(&word[4]) != cudaSuccess ||
-        fa::cache::read_and_clear_weigh_status(&word[5]) != cudaSuccess)
+        fa::cache::read_and_clear_weigh_status(&word[5]) != cudaSuccess || fa::bwd::read_and_clear_bwd_status(&word[6]) != cudaSuccess)
         return FA_ERR_NO_DEVICE;
     uint32_t w = word[0];
     for (uint32_t x : word)

@@ -57,6 +57,10 @@ int check_fwd_args(const void *q, const void *k, const void *v, const void *o, c
                    int Hkv, int Sq, int Sk, int D, int causal, float scale, int kernel);
 int check_device();
 
+// The tensor map of a dense [planes, S, D] 16-bit tensor: a 3-D (D, S, planes) view, boxes of 64 columns x `rows` rows,
+// 128B swizzle.  False where it cannot be encoded.
+bool encode_tiles(CUtensorMap *m, const void *base, bool bf16, int D, int S, long long planes, int rows);
+
 // Launches the forward kernel for (D, dtype, causal).  Returns the cudaGetLastError() of the launch.
 cudaError_t launch_fwd(int D, bool bf16, bool causal, const Maps &maps, const Params &p, cudaStream_t stream);
 

@@ -1,0 +1,118 @@
+"""The gradients of attention: argument marshalling over libfa_gb300.so.
+
+``attention_bwd`` is fa_bwd of include/fa.h; ``attention_ad`` is ``attention`` as a node of torch's autograd graph, whose
+backward is ``attention_bwd``.  As in ``binding``, every step of the computation runs in the library's CUDA kernels and a non-zero
+status raises ``FaError``.
+"""
+from __future__ import annotations
+
+import ctypes
+import functools
+from typing import Optional, Tuple
+
+import torch
+
+from . import binding as _b
+from .binding import load_library
+from .cache import _capturing, _current, _DTYPES, _F32, _kept, _launch, _need, _on, _workspace
+
+_P, _I, _F, _Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+_lib = None
+
+
+def _library() -> ctypes.CDLL:
+    global _lib
+    if _lib is None:
+        lib = load_library()
+        lib.fa_bwd_workspace_bytes.restype, lib.fa_bwd_workspace_bytes.argtypes = _Z, [_I] * 6
+        lib.fa_bwd.restype, lib.fa_bwd.argtypes = _I, [_P] * 10 + [_I] * 7 + [_F, _I, _P, _Z, _P]
+        lib.fa_bwd_debug.restype = _I
+        lib.fa_bwd_debug.argtypes = [_P] * 10 + [_I] * 7 + [_F, _I, _P, _Z, _P, ctypes.c_uint64, ctypes.c_uint32]
+        _lib = lib
+    return _lib
+
+
+@functools.lru_cache(maxsize=256)
+def bwd_workspace_bytes(B: int, Hq: int, Hkv: int, Sq: int, Sk: int, D: int) -> int:
+    """Bytes of the workspace of ``attention_bwd``."""
+    return _library().fa_bwd_workspace_bytes(B, Hq, Hkv, Sq, Sk, D)
+
+
+def attention_bwd(q, k, v, o, lse, do, causal=False, scale: Optional[float] = None, dlse=None, dq=None, dk=None, dv=None, workspace=None,
+                  stream=None, need_q: bool = True, need_kv: bool = True) -> Tuple[Optional[torch.Tensor], Optional[torch.Tensor], Optional[torch.Tensor]]:
+    """The gradients (dq, dk, dv) of ``attention`` (fa_bwd): q, k, v, causal and scale as it took them, o and lse as it
+    left them, do the gradient of o and dlse [B, Hq, Sq] float32 that of lse (None: zero).
+
+    Results are written to dq, dk and dv where they are given.  need_q, need_kv: False leaves dq, or dk and dv, out (None is
+    returned for them).  workspace: bwd_workspace_bytes(...) bytes that no other call in flight uses; None: one that is kept for the calling
+    thread and the stream, or, in a call that is captured into a graph, one of the graph's own.  stream: where the call
+    runs, and what it allocates then belongs to; None: the current stream."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 4 or not isinstance(k, torch.Tensor) or k.dim() != 4:
+        raise ValueError("q, k, v must be 4-D [B, H, S, D] tensors")
+    if stream is not None:
+        return _on(stream, q, attention_bwd, q, k, v, o, lse, do, causal, scale, dlse, dq, dk, dv, workspace, None, need_q, need_kv)
+    i, dt = q.get_device(), q.dtype
+    code = _DTYPES.get(dt)
+    if code is None:
+        raise ValueError(f"attention is bf16 or fp16, not {dt}")
+    if i < 0:
+        raise ValueError("q must be a CUDA tensor")
+    shape, keys = q.shape, k.shape
+    B, Hq, Sq, D = shape
+    Hkv, Sk = keys[1], keys[2]
+    if keys[0] != B or keys[3] != D:
+        raise ValueError("k and v must be [B, Hkv, Sk, D] with q's B and D")
+    if (not need_q and dq is not None) or (not need_kv and (dk is not None or dv is not None)):
+        raise ValueError("a result is given that is not to be computed")
+    rows = shape[:3]
+    args = [_need("q", q, shape, dt, i), _need("k", k, keys, dt, i), _need("v", v, keys, dt, i), _need("o", o, shape, dt, i),
+            _need("lse", lse, rows, _F32, i), _need("do", do, shape, dt, i), None if dlse is None else _need("dlse", dlse, rows, _F32, i)]
+    current = _current(i)
+    kept = _kept(i, current)
+    if need_q:
+        dq = torch.empty_like(q) if dq is None else dq
+        args.append(_need("dq", dq, shape, dt, i))
+    else:
+        args.append(None)
+    if need_kv:
+        dk = torch.empty_like(k) if dk is None else dk
+        dv = torch.empty_like(v) if dv is None else dv
+        args += [_need("dk", dk, keys, dt, i), _need("dv", dv, keys, dt, i)]
+    else:
+        args += [None, None]
+    lib = _lib or _library()
+    _, at, size = _workspace(bwd_workspace_bytes(B, Hq, Hkv, Sq, Sk, D), workspace, q, kept)
+    _launch(lib.fa_bwd, i, current, (*args, B, Hq, Hkv, Sq, Sk, D, _b._causal_code(causal), D ** -0.5 if scale is None else float(scale), code, at, size))
+    return dq, dk, dv
+
+
+class _Attention(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, causal, scale):
+        o, lse = _b.attention(q, k, v, causal=causal, scale=scale)
+        ctx.save_for_backward(q, k, v, o, lse)
+        ctx.how = causal, scale
+        ctx.set_materialize_grads(False)
+        return o, lse
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, do, dlse):
+        q, k, v, o, lse = ctx.saved_tensors
+        if do is None and dlse is None:
+            return None, None, None, None, None
+        do = torch.zeros_like(o) if do is None else do.contiguous()
+        need = ctx.needs_input_grad
+        dq, dk, dv = attention_bwd(q, k, v, o, lse, do, *ctx.how, dlse=None if dlse is None else dlse.contiguous(), need_q=need[0],
+                                   need_kv=need[1] or need[2])
+        return dq, dk, dv, None, None
+
+
+def attention_ad(q, k, v, causal=False, scale: Optional[float] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """``attention`` for training: (o, lse), both differentiable by torch's autograd with respect to q, k and v.
+
+    Not for a call that is captured into a CUDA graph: the gradient nodes of leaves that an eager graph shares belong to that graph's
+    stream.  A captured step calls ``attention`` and ``attention_bwd``."""
+    if torch.is_grad_enabled() and any(isinstance(x, torch.Tensor) and x.requires_grad for x in (q, k, v)) and _capturing():
+        raise RuntimeError("attention_ad is not captured into a graph: call attention and attention_bwd there")
+    return _Attention.apply(q, k, v, causal, scale)
