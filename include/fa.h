@@ -183,6 +183,41 @@ int fa_bwd_debug(const void *q, const void *k, const void *v, const void *o, con
                  float scale, int dtype, void *workspace, size_t workspace_bytes, fa_stream_t stream,
                  uint64_t timeout_ns, uint32_t inject);
 
+/* ------------------------------------------------------------------ rotary positions
+ *
+ * A head's first `rot` elements are rot / 2 pairs, each of which turns by an angle that grows with the token's
+ * position; what remains of the head passes as it is:
+ *     (a, b) -> amplitude (a cos t - b sin t, a sin t + b cos t),   t = position * frequency[p]
+ * The pair is elements p and p + rot / 2 (interleaved 0) or 2p and 2p + 1 (interleaved 1).
+ */
+typedef struct fa_rotary_table {
+    const uint64_t *freq;     /* [rot / 2] device array: frequency / (2 pi) * 2^64, turns of a position in 64-bit fixed point */
+    int D, rot;               /* head dimension (64, 128 or 256); rotated elements: even, 0 .. D */
+    int interleaved;
+    float amplitude;          /* finite; usually 1 */
+} fa_rotary_table_t;
+
+/* Heads of tokens anywhere in memory, e.g. those of q, k or v in the rows of one projection: element e of head h of token t of
+ * sequence b is data[b * stride_b + h * stride_h + t * stride_t + e].  data is 16-byte aligned, strides are not negative and
+ * multiples of 8 (where the extent is above 1). */
+typedef struct fa_heads {
+    void *data;
+    int64_t stride_b, stride_h, stride_t;   /* in elements */
+    int heads;
+} fa_heads_t;
+
+/*
+ * fa_rotary -- rotates the heads x[i] of B sequences of T tokens into y[i] (i < n, n 1 or 2: queries and keys in one launch),
+ * which may be x[i] itself, at the same strides.  dtype 0 bf16, 1 fp16.
+ *   position   [B, T] of each token, or NULL; start [B] position of each sequence's first token, or NULL; both NULL: token t is
+ *              at position t.  Both given: FA_ERR_ARG.  Any int32 position, negative ones included, has its exact angle
+ *   inverse    1: by the opposite angles (amplitude unchanged), which is the gradient of the rotation
+ * Products and sums are float32, rounded once.
+ * FA_ERR_ALIAS: two heads of a y share a place, or y shares one with x or the other y.  Heads side by side in common rows do not.
+ */
+int fa_rotary(const fa_rotary_table_t *table, const fa_heads_t *x, const fa_heads_t *y, int n, int B, int T,
+              const int32_t *start, const int32_t *position, int inverse, int dtype, fa_stream_t stream);
+
 /*
  * fa_gemm -- tiled matrix product with an optional fused epilogue, the tutorial's building
  * block for both attention products ("Guia Prático de Programação de GPU com Tiles", section 5:
@@ -355,6 +390,23 @@ int fa_tree_fwd(const fa_cache_t *cache, const void *q, const void *k_new, const
 int fa_cache_append(const fa_cache_t *cache, const void *k_new, const void *v_new, const int32_t *path,
                     const int32_t *count, const int32_t *start, float *weight, int32_t *pos, int T,
                     fa_stream_t stream);
+
+/*
+ * fa_rotary_append -- what a layer does with its projection's rows in one launch: queries x[0] and keys x[1] of each sequence's
+ * T new tokens turn by their positions (fa_rotary) and go, with the values x[2], to y[0], y[1], y[2]; keys and
+ * values also go to the cache, slot seq_len[b] + i (fa_cache_append).
+ *   x, y         three views each; x[0] has any multiple of Hkv heads (0: no queries), x[1] and x[2] have Hkv.  y[i].data may be
+ *                NULL: not written.  y[i] may be x[i] itself
+ *   start        [B] position of the first new token, or NULL: seq_len[b];  position [B, T] instead: of each token
+ *   count        [B] new tokens of each sequence (clamped to [0, T]), or NULL: T.  Tokens behind are not read and their rows of y,
+ *                slots, weights and positions are left as they were
+ *   weight, pos  as for fa_cache_append: the new slots' weight becomes 0, their position the token's
+ * Tokens that do not fit behind the capacity, or whose page does not exist, are not stored; their rows of y are written all the same.
+ * seq_len is not changed.  Attention of the new tokens (fa_tree_fwd with y[0], y[1] and y[2]) takes seq_len as it was.
+ */
+int fa_rotary_append(const fa_cache_t *cache, const fa_rotary_table_t *table, const fa_heads_t *x, const fa_heads_t *y,
+                     int T, const int32_t *start, const int32_t *position, const int32_t *count, float *weight,
+                     int32_t *pos, fa_stream_t stream);
 
 /*
  * fa_cache_weights -- adds to each slot the attention weight that it receives from a set of queries:

@@ -24,4 +24,8 @@ def __getattr__(name):
         from . import grad
         globals()[name] = value = getattr(grad, name)
         return value
+    if name in ("RotaryTable", "rotary_frequencies", "rotary", "rotary_append", "rotary_ad"):
+        from . import positions
+        globals()[name] = value = getattr(positions, name)
+        return value
     raise AttributeError(name)

@@ -74,6 +74,23 @@ bool good_scale(float s) { return s > 0.f && std::isfinite((float)((double)s * 1
 
 int gcd(int a, int b) { return b ? gcd(b, a % b) : a; }
 
+size_t pool_bytes(const fa_cache_t *c) { return (size_t)c->num_pages * c->Hkv * c->page * c->D * 2; }
+
+Pages pages_of(const fa_cache_t *c) { return Pages{c->table, c->page, c->max_pages, c->num_pages}; }
+
+// K or V of a cache as a (D, page, Hkv, num_pages) tensor.  An empty pool (the capacity is 0 then, so no length
+// makes a kernel read it) is given one page of extent so that the map can be encoded over any valid address.
+bool encode_pool(CUtensorMap *m, const void *base, const void *any, const fa_cache_t *c, int rows)
+{
+    const long long ext[4] = {c->D, c->page, c->Hkv, c->num_pages > 0 ? c->num_pages : 1};
+    return encode(m, c->num_pages > 0 ? base : any, c->dtype == 0, 4, ext, rows);
+}
+
+} // namespace
+
+namespace fa {
+namespace cache {
+
 // Checks of a cache's own fields, shared by every entry point.
 int check_cache(const fa_cache_t *c)
 {
@@ -100,19 +117,8 @@ int check_cache_pointers(const fa_cache_t *c)
     return FA_OK;
 }
 
-size_t pool_bytes(const fa_cache_t *c) { return (size_t)c->num_pages * c->Hkv * c->page * c->D * 2; }
-
-Pages pages_of(const fa_cache_t *c) { return Pages{c->table, c->page, c->max_pages, c->num_pages}; }
-
-// K or V of a cache as a (D, page, Hkv, num_pages) tensor.  An empty pool (the capacity is 0 then, so no length
-// makes a kernel read it) is given one page of extent so that the map can be encoded over any valid address.
-bool encode_pool(CUtensorMap *m, const void *base, const void *any, const fa_cache_t *c, int rows)
-{
-    const long long ext[4] = {c->D, c->page, c->Hkv, c->num_pages > 0 ? c->num_pages : 1};
-    return encode(m, c->num_pages > 0 ? base : any, c->dtype == 0, 4, ext, rows);
-}
-
-} // namespace
+} // namespace cache
+} // namespace fa
 
 extern "C" {
 

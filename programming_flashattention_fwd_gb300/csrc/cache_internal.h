@@ -7,6 +7,8 @@
 
 #include "cache_schedule.h"
 
+struct fa_cache;   // include/fa.h
+
 namespace fa {
 namespace cache {
 
@@ -34,6 +36,10 @@ cudaError_t launch_overlapped(Kernel kern, dim3 grid, unsigned threads, size_t s
     cfg.numAttrs = cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kern, args...);
 }
+
+// Checks of a cache's own fields, and of the pointers of a non-empty one, shared by the entry points: FA_OK or the status code.
+int check_cache(const fa_cache *c);
+int check_cache_pointers(const fa_cache *c);
 
 // Where the slots of a sequence are: slot s on row s % page of page table[b * max_pages + s / page]
 // (page b * max_pages + s / page without a table).

@@ -1,0 +1,244 @@
+"""Rotary positions: argument marshalling over libfa_gb300.so.
+
+``RotaryTable`` holds the frequencies of a model's heads; ``rotary`` turns queries and keys by their positions (fa_rotary of
+include/fa.h), ``rotary_append`` also writes keys and values to a cache (fa_rotary_append), and ``rotary_ad`` is ``rotary`` as a
+node of torch's autograd graph.  As in ``binding``, every step of the computation runs in the library's CUDA kernels and a non-zero
+status raises ``FaError``.
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+import struct
+from typing import Optional, Sequence
+
+import torch
+
+from .binding import load_library
+from .cache import _capturing, _current, _DTYPES, _F32, _I32, _launch, _need, _on, KVCache
+
+_P, _I, _C = ctypes.c_void_p, ctypes.c_int, ctypes.c_char_p
+_TABLE = struct.Struct("P3if").pack          # fa_rotary_table_t: freq; D, rot, interleaved; amplitude
+_HEADS = struct.Struct("P3qi4x").pack        # fa_heads_t: data; stride_b, stride_h, stride_t; heads
+_NONE = _HEADS(0, 0, 0, 0, 0)
+_lib = None
+
+
+def _library() -> ctypes.CDLL:
+    global _lib
+    if _lib is None:
+        lib = load_library()
+        lib.fa_rotary.restype, lib.fa_rotary.argtypes = _I, [_C, _C, _C, _I, _I, _I, _P, _P, _I, _I, _P]
+        lib.fa_rotary_append.restype, lib.fa_rotary_append.argtypes = _I, [_C, _C, _C, _C, _I] + [_P] * 6
+        _lib = lib
+    return _lib
+
+
+def rotary_frequencies(rot: int, base: float = 10000.0, scaling: Optional[str] = None, factor: float = 1.0, original: int = 0, fast: float = 32.0,
+                       slow: float = 1.0) -> Sequence[float]:
+    """Radians a position of each of rot / 2 pairs: base ** (-2 p / rot), as they are or for contexts `factor` times as long:
+
+    "linear"  every one divided by factor
+    "base"    a larger base, base * factor ** (rot / (rot - 2)): the slowest pair is divided by factor, the fastest stays
+    "ramp"    pairs that turn more than `fast` times in `original` positions stay, those that turn less than `slow` times are divided by
+              factor, those between by a share that grows with the pair's number"""
+    if rot < 0 or rot % 2:
+        raise ValueError("rot must be even")
+    if not base > 0 or not factor > 0:
+        raise ValueError("base and factor must be positive")
+    if scaling == "base":
+        if rot <= 2:
+            raise ValueError("scaling the base needs more than one pair")
+        base *= factor ** (rot / (rot - 2))
+    f = [base ** (-2 * p / rot) for p in range(rot // 2)]
+    if scaling == "linear":
+        return [x / factor for x in f]
+    if scaling == "ramp":
+        if not original > 0 or not fast > slow > 0 or not base > 1:
+            raise ValueError("a ramp needs original > 0, fast > slow > 0 and base > 1")
+        at = lambda turns: rot * math.log(original / (turns * 2 * math.pi)) / (2 * math.log(base))  # noqa: E731
+        lo, hi = max(math.floor(at(fast)), 0), min(math.ceil(at(slow)), rot - 1)
+        share = [min(max((p - lo) / max(hi - lo, 0.001), 0.0), 1.0) for p in range(rot // 2)]
+        return [x * (1 - s) + x / factor * s for x, s in zip(f, share)]
+    if scaling not in (None, "base"):
+        raise ValueError(f"scaling is None, 'linear', 'base' or 'ramp', not {scaling!r}")
+    return f
+
+
+class RotaryTable:
+    """The rotation of heads of D elements (fa_rotary_table_t): which are rotated, in which pairs, how fast.
+
+    rot           rotated elements, the first of the head (None: all); even
+    interleaved   pairs of neighbours (2p, 2p + 1); False: of halves (p, p + rot / 2)
+    base, scaling, factor, original, fast, slow   the frequencies, as rotary_frequencies takes them; or
+    frequencies   rot / 2 numbers, radians a position
+    amplitude     multiplies what is rotated; None: 0.1 ln(factor) + 1 for a "ramp" with a factor above 1, else 1
+    device        where the table is kept"""
+    __slots__ = ("freq", "D", "rot", "interleaved", "amplitude", "frequencies", "index", "_c")
+
+    def __init__(self, D: int, rot: Optional[int] = None, base: float = 10000.0, interleaved: bool = False, scaling: Optional[str] = None, factor: float = 1.0,
+                 original: int = 0, fast: float = 32.0, slow: float = 1.0, frequencies: Optional[Sequence[float]] = None, amplitude: Optional[float] = None,
+                 device="cuda"):
+        rot = D if rot is None else rot
+        if frequencies is None:
+            frequencies = rotary_frequencies(rot, base, scaling, factor, original, fast, slow)
+        frequencies = [float(x) for x in frequencies]
+        if rot % 2 or not 0 <= rot <= D or len(frequencies) != rot // 2:
+            raise ValueError("rot must be even, at most D, and have rot / 2 frequencies")
+        if not all(math.isfinite(x) for x in frequencies):
+            raise ValueError("frequencies must be finite")
+        if amplitude is None:
+            amplitude = 0.1 * math.log(factor) + 1.0 if scaling == "ramp" and factor > 1.0 else 1.0
+        turns = [round(x / (2 * math.pi) * 2.0 ** 64) & (2 ** 64 - 1) for x in frequencies]
+        self.freq = torch.tensor([x - 2 ** 64 if x >= 2 ** 63 else x for x in turns], dtype=torch.int64).to(device)
+        self.frequencies = tuple(frequencies)
+        self.D, self.rot, self.interleaved, self.amplitude = D, rot, bool(interleaved), float(amplitude)
+        self.index = self.freq.get_device()
+        if self.index < 0:
+            raise ValueError("a table is kept on a CUDA device")
+        self._c = _TABLE(self.freq.data_ptr(), D, rot, int(self.interleaved), self.amplitude)
+
+    def __reduce__(self):
+        # a copy has a table of its own, at another address
+        return _table, (self.D, self.rot, self.interleaved, self.frequencies, self.amplitude, self.freq.device)
+
+
+def _table(D, rot, interleaved, frequencies, amplitude, device):
+    return RotaryTable(D, rot=rot, interleaved=interleaved, frequencies=frequencies, amplitude=amplitude, device=device)
+
+
+def _view(name: str, t, B: int, H: Optional[int], T: int, D: int, dtype, index: int) -> bytes:
+    """fa_heads_t of a [B, H, T, D] tensor with any strides but the last dimension's, which is 1."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 4:
+        raise ValueError(f"{name} must be a [B, H, T, D] tensor")
+    shape = t.shape
+    if shape[0] != B or shape[2] != T or shape[3] != D or (H is not None and shape[1] != H):
+        raise ValueError(f"{name} must have shape {(B, 'H' if H is None else H, T, D)}, not {tuple(shape)}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device} but the call is on cuda:{index}: every tensor of one call must be on the same GPU")
+    sb, sh, st, se = t.stride()
+    if se != 1 and t.numel():
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+    return _HEADS(t.data_ptr(), sb, sh, st, shape[1])
+
+
+def _first(name: str, t, table: RotaryTable):
+    if not isinstance(table, RotaryTable):
+        raise TypeError("table must be a RotaryTable")
+    if not isinstance(t, torch.Tensor) or t.dim() != 4:
+        raise ValueError(f"{name} must be a [B, H, T, D] tensor")
+    if t.shape[3] != table.D:
+        raise ValueError(f"{name} must have the table's head dimension {table.D}")
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name} must be bf16 or fp16, not {t.dtype}")
+    if t.get_device() != table.index:
+        raise ValueError(f"{name} is on {t.device} but the table is on cuda:{table.index}: every tensor of one call must be on the same GPU")
+    return code
+
+
+def rotary(table: RotaryTable, q, k=None, start=None, position=None, inverse: bool = False, q_out=None, k_out=None, stream=None):
+    """q [B, Hq, T, D], and k [B, Hk, T, D] in the same launch, turned by their positions (fa_rotary): position [B, T] int32, or
+    start[b] + t with start [B] int32, or t.  The tensors may be views with any strides (of the rows of one projection, say)
+    whose last dimension is contiguous; results are new dense tensors, or q_out and k_out, views too, which may be q and k
+    themselves.  inverse: by the opposite angles, which takes the results' gradients to those of q and k.  Returns q's result, or both."""
+    if stream is not None:
+        return _on(stream, q, rotary, table, q, k, start, position, inverse, q_out, k_out)
+    code = _first("q", q, table)
+    i, dt = table.index, q.dtype
+    B, _, T, D = q.shape
+    if start is not None and position is not None:
+        raise ValueError("positions are given by start or by position, not by both")
+    x = _view("q", q, B, None, T, D, dt, i)
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=dt, device=q.device)
+    y = _view("q_out", q_out, B, q.shape[1], T, D, dt, i)
+    if k is not None:
+        x += _view("k", k, B, None, T, D, dt, i)
+        if k_out is None:
+            k_out = torch.empty(k.shape, dtype=dt, device=q.device)
+        y += _view("k_out", k_out, B, k.shape[1], T, D, dt, i)
+    elif k_out is not None:
+        raise ValueError("k_out needs k")
+    lib = _lib or _library()
+    _launch(lib.fa_rotary, i, _current(i),
+            (table._c, x, y, 1 if k is None else 2, B, T, None if start is None else _need("start", start, (B,), _I32, i),
+             None if position is None else _need("position", position, (B, T), _I32, i), 1 if inverse else 0, code))
+    return q_out if k is None else (q_out, k_out)
+
+
+def rotary_append(cache: KVCache, table: RotaryTable, q, k, v, start=None, position=None, count=None, weight=None, pos=None, q_out=None, k_out=None, v_out=None,
+                  stream=None):
+    """The queries, keys and values of T new tokens of every sequence, out of a projection's rows (fa_rotary_append): q [B, Hq, T, D]
+    and k [B, Hkv, T, D] turned by their positions (start[b] + i, position[b, i], or seq_len[b] + i), and keys and values
+    v [B, Hkv, T, D] written to the cache's slots seq_len[b] + i, i < count[b] (None: T).  Returns (q, k, v), dense and turned, as
+    ``tree_attention`` (with seq_len as it was) or ``attention`` takes them: in q_out, k_out, v_out where these are given; k_out or
+    v_out False: not written, None in its place.  q, k, v and the results may be views with any strides whose last dimension is
+    contiguous.  Rows at or behind count are left as they were.  weight, pos: as in ``cache_append``, which serves tokens
+    that are accepted later; seq_len is not changed: add count to it after the last layer."""
+    if stream is not None:
+        return _on(stream, cache, rotary_append, cache, table, q, k, v, start, position, count, weight, pos, q_out, k_out, v_out)
+    _first("q", q, table)
+    i, dt, B, Hkv = cache.index, cache.dtype, cache.B, cache.Hkv
+    if start is not None and position is not None:
+        raise ValueError("positions are given by start or by position, not by both")
+    T, D = q.shape[2], table.D
+    if D != cache.D:
+        raise ValueError(f"the table is for heads of {D}, the cache's have {cache.D}")
+    new, slots = (B, Hkv, T, D), (B, Hkv, cache.capacity)
+    x = _view("q", q, B, None, T, D, dt, i) + _view("k", k, B, Hkv, T, D, dt, i) + _view("v", v, B, Hkv, T, D, dt, i)
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=dt, device=q.device)
+    y = _view("q_out", q_out, B, q.shape[1], T, D, dt, i)
+    out = [q_out]
+    for name, t in (("k_out", k_out), ("v_out", v_out)):
+        if t is None:
+            t = torch.empty(new, dtype=dt, device=q.device)
+        if t is False:
+            y += _HEADS(0, 0, 0, 0, Hkv)
+            t = None
+        else:
+            y += _view(name, t, B, Hkv, T, D, dt, i)
+        out.append(t)
+    lib = _lib or _library()
+    _launch(lib.fa_rotary_append, i, _current(i),
+            (cache._c, table._c, x, y, T, None if start is None else _need("start", start, (B,), _I32, i),
+             None if position is None else _need("position", position, (B, T), _I32, i), None if count is None else _need("count", count, (B,), _I32, i),
+             None if weight is None else _need("weight", weight, slots, _F32, i), None if pos is None else _need("pos", pos, slots, _I32, i)))
+    return tuple(out)
+
+
+def _dense(t):
+    """t, or a dense copy where its rows are not where the library takes them."""
+    return t if t.stride(-1) == 1 and t.data_ptr() % 16 == 0 and not any(x % 8 for x in t.stride()[:-1]) else t.contiguous()
+
+
+class _Rotary(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, table, start, position):
+        ctx.table = table
+        ctx.save_for_backward(start, position)
+        ctx.set_materialize_grads(False)
+        return rotary(table, q, k, start, position)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dq, dk=None):
+        start, position = ctx.saved_tensors
+        if dq is not None and dk is not None:
+            dq, dk = rotary(ctx.table, _dense(dq), _dense(dk), start, position, inverse=True)
+        else:
+            dq, dk = (None if g is None else rotary(ctx.table, _dense(g), None, start, position, inverse=True) for g in (dq, dk))
+        return dq, dk, None, None, None
+
+
+def rotary_ad(table: RotaryTable, q, k=None, start=None, position=None):
+    """``rotary`` for training: differentiable by torch's autograd with respect to q and k.
+
+    Not for a call that is captured into a CUDA graph (see ``attention_ad``): a captured step calls ``rotary``, and ``rotary``
+    with inverse."""
+    if torch.is_grad_enabled() and any(isinstance(x, torch.Tensor) and x.requires_grad for x in (q, k)) and _capturing():
+        raise RuntimeError("rotary_ad is not captured into a graph: call rotary there, and again with inverse")
+    return _Rotary.apply(q, k, table, start, position)
