@@ -37,10 +37,11 @@ namespace bwd {
 
 __device__ unsigned int g_bwd_status;
 
+#ifndef FA_CW
+#define FA_CW 8
+#endif
 namespace {
 
-constexpr int THREADS = 384;
-constexpr int kComputeWarps = 8;
 constexpr uint64_t kDefaultTimeoutNs = 2000000000ull;
 
 enum Site : uint32_t { S_EMPTY = 1, S_RES = 2, S_FULL = 3, S_P = 4, S_S = 5, S_DP = 6, S_DS = 7, S_ACC = 8, S_VEC = 9, S_DRAIN = 10, S_SMEM = 11 };
@@ -53,6 +54,9 @@ struct Cfg {
     static constexpr bool HAS_DV = MODE == kKV || MODE == kV;
     static constexpr int BN = step_rows(D);
     static constexpr int PANELS = D / 64;
+    static constexpr int CW = FA_CW;                           // warps that compute
+    static constexpr int THREADS = 128 + 32 * CW;
+    static constexpr int HB = BN / (CW / 4), HD = D / (CW / 4);   // a thread's columns of a step, and of the results
     // Resident operands in tensor memory (16-bit pairs, D / 2 columns), where it has room: a product with both
     // operands in shared memory takes as long to read them as to compute.
     static constexpr bool A1T = MODE == kQ || D == 256;
@@ -68,12 +72,15 @@ struct Cfg {
 
     static constexpr int RTILE = kRows * D * 2, RPANEL = kRows * 128;
     static constexpr int STILE = BN * D * 2, SPANEL = BN * 128;
-    static constexpr int NR = HAS_DS ? 2 : 1;                  // resident operands
-    static constexpr int NSLOT = D == 64 ? 8 : (D == 128 ? 5 : (MODE == kV ? 4 : 3));
+    // At D = 256 the first resident operand, which goes on to tensor memory, comes through the ring, two slots of it,
+    // instead of a 64 KB buffer of its own that would leave the ring 3 slots and the products waiting for every tile.
+    static constexpr int RUSES = D == 256 ? RTILE / STILE : 0;
+    static constexpr int NRES = (RUSES ? 0 : 1) + (HAS_DS ? 1 : 0);   // resident operands in shared memory
+    static constexpr int NSLOT = D == 64 ? 8 : (NRES ? 5 : 7);
     static constexpr int NVEC = ROWQ ? 0 : 2;                  // buffers of streamed lse and delta
     static constexpr int VEC = 2 * BN * 4;
     static constexpr int OFF_R = 0;
-    static constexpr int OFF_RING = NR * RTILE;
+    static constexpr int OFF_RING = NRES * RTILE;
     static constexpr int OFF_VEC = OFF_RING + NSLOT * STILE;
     static constexpr int OFF_BAR = OFF_VEC + NVEC * VEC;
     static constexpr int NBAR = 2 * NSLOT + 2 + 2 + 2 + 1 + 1 + 1 + 2 + 2;
@@ -115,27 +122,53 @@ __device__ __forceinline__ void ld_shared_2x64(uint32_t addr, uint64_t &a, uint6
     asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "r"(addr) : "memory");
 }
 
-// Row r of tile t of a result, columns [c0, c0 + n): 32 sums a time out of tensor memory, scaled and rounded (or, for a
-// part of a cut unit, as they are).
-template <int D, bool BF16>
-__device__ __forceinline__ void write_row(uint32_t tAcc, void *out, float *part, size_t row, bool valid, int c0, int n, float scale, uint32_t al32)
+// N columns of a lane, between tensor memory and registers.
+template <int N>
+__device__ __forceinline__ void load_columns(uint32_t taddr, uint32_t *r)
 {
+    static_assert(N == 16 || N == 32, "widths of a load");
+    if constexpr (N == 32) tmem_ld_x32(taddr, *reinterpret_cast<uint32_t(*)[32]>(r));
+    else tmem_ld_x16(taddr, *reinterpret_cast<uint32_t(*)[16]>(r));
+}
+template <int N>
+__device__ __forceinline__ void fence_columns(uint32_t *r)
+{
+    if constexpr (N == 32) reg_fence_x32(*reinterpret_cast<uint32_t(*)[32]>(r));
+    else reg_fence_x16(*reinterpret_cast<uint32_t(*)[16]>(r));
+}
+template <int N>
+__device__ __forceinline__ void store_columns(uint32_t taddr, const uint32_t *r)
+{
+    static_assert(N == 8 || N == 16, "widths of a store");
+    if constexpr (N == 16)
+        tmem_st_x16(taddr, *reinterpret_cast<const uint32_t(*)[16]>(r));
+    else
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+                     "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]) : "memory");
+}
+
+// Row r of tile t of a result, columns [c0, c0 + n): up to 32 sums a time out of tensor memory, scaled and rounded (or, for a
+// part of a cut unit, as they are).
+template <int D, int N, bool BF16>
+__device__ __forceinline__ void write_row(uint32_t tAcc, void *out, float *part, size_t row, bool valid, int c0, float scale, uint32_t al32)
+{
+    constexpr int W = N < 32 ? N : 32;
     const uint64_t s2 = f2_pack(scale, scale);
 #pragma unroll 1
-    for (int c = c0; c < c0 + n; c += 32) {
-        uint32_t v[32];
-        tmem_ld_x32(tAcc + c, v);
+    for (int c = c0; c < c0 + N; c += W) {
+        uint32_t v[W];
+        load_columns<W>(tAcc + c, v);
         tmem_wait_ld();
-        reg_fence_x32(v);
+        fence_columns<W>(v);
         if (part) {
             float *to = part + row * D + c;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) st_global_v8(to + 8 * i, v + 8 * i);
+            for (int i = 0; i < W; i += 8) st_global_v8(to + i, v + i);
             continue;
         }
-        uint32_t pk[16];
+        uint32_t pk[W / 2];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
+        for (int e = 0; e < W / 2; ++e) {
             float lo, hi;
             f2_unpack(f2_mul(f2_pack(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), s2), lo, hi);
             pk[e] = pack2<BF16>(lo, hi);
@@ -143,11 +176,11 @@ __device__ __forceinline__ void write_row(uint32_t tAcc, void *out, float *part,
         uint8_t *to = static_cast<uint8_t *>(out) + (row * D + c) * 2;
         if (valid) {
             if (al32) {
-                st_global_v8(to, pk);
-                st_global_v8(to + 32, pk + 8);
+#pragma unroll
+                for (int i = 0; i < W / 2; i += 8) st_global_v8(to + 4 * i, pk + i);
             } else {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) st_global_v4(to + 16 * i, pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+                for (int i = 0; i < W / 2; i += 4) st_global_v4(to + 4 * i, pk[i], pk[i + 1], pk[i + 2], pk[i + 3]);
             }
         }
         __syncwarp();   // the next load takes the whole warp
@@ -166,7 +199,7 @@ __device__ __forceinline__ void fill_row(void *out, float *part, size_t row, boo
 }
 
 template <int MODE, int D, bool BF16>
-__global__ void __launch_bounds__(THREADS, 1)
+__global__ void __launch_bounds__((Cfg<MODE, D>::THREADS), 1)
     bwd_kernel(const __grid_constant__ CUtensorMap tmR1, const __grid_constant__ CUtensorMap tmR2, const __grid_constant__ CUtensorMap tmS1,
                const __grid_constant__ CUtensorMap tmS2, const __grid_constant__ Params p)
 {
@@ -179,7 +212,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t sb = raw + pad;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-    const uint32_t sR1 = sb + C::OFF_R, sR2 = sR1 + C::RTILE, sRing = sb + C::OFF_RING, sVec = sb + C::OFF_VEC, bar0 = sb + C::OFF_BAR;
+    const uint32_t sR1 = sb + C::OFF_R, sR2 = sR1 + (C::RUSES ? 0 : C::RTILE), sRing = sb + C::OFF_RING, sVec = sb + C::OFF_VEC, bar0 = sb + C::OFF_BAR;
     auto bar_full = [&](uint32_t s) { return bar0 + 8u * s; };
     auto bar_empty = [&](uint32_t s) { return bar0 + 8u * (C::NSLOT + s); };
     const uint32_t barRes = bar0 + 8u * (2 * C::NSLOT);   // resident tiles loaded
@@ -195,15 +228,15 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint64_t tmo = p.timeout_ns;
 
     const int r = (warp & 3) * 32 + lane;   // resident row of a computing thread
-    const int half = (warp - 4) >> 2;       // its half of a step's columns and of the results' columns
+    const int part_of = (warp - 4) >> 2;    // its part of a step's columns and of the results' columns
     auto each_unit_filled = [&](uint32_t word) {
         Unit u;
         for (int round = 0; unit_at<C::ROWQ, BN>(p.s, gridDim.x, blockIdx.x, round, u); ++round) {
             const int row = u.t * kRows + r;
             const bool valid = row < p.s.rows;
             const size_t at = p.part || p.part_v ? (size_t)u.slot * kRows + r : (size_t)u.z * p.s.rows + row;
-            if (C::HAS_DS) fill_row<D>(p.out, p.part, at, valid, half * (D / 2), D / 2, word);
-            if (C::HAS_DV) fill_row<D>(p.out_v, p.part_v, at, valid, half * (D / 2), D / 2, word);
+            if (C::HAS_DS) fill_row<D>(p.out, p.part, at, valid, part_of * C::HD, C::HD, word);
+            if (C::HAS_DV) fill_row<D>(p.out_v, p.part_v, at, valid, part_of * C::HD, C::HD, word);
         }
     };
 
@@ -221,12 +254,12 @@ __global__ void __launch_bounds__(THREADS, 1)
         mbar_init(barFree, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(barS + 8 * i, 1);
-            mbar_init(barP + 8 * i, kComputeWarps);
+            mbar_init(barP + 8 * i, C::CW);
             mbar_init(barVec + 8 * i, 1);
-            mbar_init(barVecFree + 8 * i, kComputeWarps);
+            mbar_init(barVecFree + 8 * i, C::CW);
         }
         mbar_init(barDP, 1);
-        mbar_init(barDS, kComputeWarps);
+        mbar_init(barDS, C::CW);
         mbar_init(barAcc, 1);
         *abort_flag = 0;
         fence_mbar_init();
@@ -247,9 +280,12 @@ __global__ void __launch_bounds__(THREADS, 1)
             const bool inj = (p.inject & 1u) || ((p.inject & 2u) && blockIdx.x == 0);
             const uint64_t keep = l2_policy_evict_last();
             bool ok = true;
+            auto slot_free = [&]() {
+                return bounded_wait(bar_empty(use % C::NSLOT), ((use / C::NSLOT) & 1) ^ 1, abort_flag, tmo, S_EMPTY, status);
+            };
             auto load = [&](const CUtensorMap *m, int tile, int plane, bool second) {
                 const uint32_t s = use % C::NSLOT;
-                if (!bounded_wait(bar_empty(s), ((use / C::NSLOT) & 1) ^ 1, abort_flag, tmo, S_EMPTY, status)) return false;
+                if (!slot_free()) return false;
                 if (inj && second && skip == ~0u) {
                     skip = use++;
                     return true;
@@ -263,6 +299,14 @@ __global__ void __launch_bounds__(THREADS, 1)
             };
             Unit u;
             for (int round = 0; ok && unit_at<C::ROWQ, BN>(p.s, gridDim.x, blockIdx.x, round, u); ++round) {
+                for (int i = 0; i < C::RUSES && u.n > 0 && ok; ++i) {   // two panels of the resident tile a slot
+                    ok = slot_free();
+                    if (!ok) break;
+                    const uint32_t s = use++ % C::NSLOT;
+                    mbar_arrive_expect_tx(bar_full(s), C::STILE);
+                    for (int k = 0; k < 2; ++k)
+                        tma_load_3d(sRing + s * C::STILE + k * C::RPANEL, &tmR1, (2 * i + k) * 64, u.t * kRows, u.z, bar_full(s));
+                }
                 int plane = u.plane, tile = u.tile;
                 for (int j = 0; j < u.n && ok; ++j) {
                     ok = load(&tmS1, tile, plane, false) && load(&tmS2, tile, plane, true);
@@ -283,11 +327,11 @@ __global__ void __launch_bounds__(THREADS, 1)
             Unit u;
             for (int round = 0; ok && unit_at<C::ROWQ, BN>(p.s, gridDim.x, blockIdx.x, round, u); ++round) {
                 if (u.n == 0) continue;
-                if (units > 0 && !bounded_wait(barFree, (units - 1) & 1, abort_flag, tmo, S_RES, status)) break;
-                mbar_arrive_expect_tx(barRes, C::NR * C::RTILE);
+                if (C::NRES && units > 0 && !bounded_wait(barFree, (units - 1) & 1, abort_flag, tmo, S_RES, status)) break;
+                if (C::NRES) mbar_arrive_expect_tx(barRes, C::NRES * C::RTILE);
 #pragma unroll
                 for (int pn = 0; pn < C::PANELS; ++pn) {
-                    tma_load_3d(sR1 + pn * C::RPANEL, &tmR1, pn * 64, u.t * kRows, u.z, barRes);
+                    if (!C::RUSES) tma_load_3d(sR1 + pn * C::RPANEL, &tmR1, pn * 64, u.t * kRows, u.z, barRes);
                     if (C::HAS_DS) tma_load_3d(sR2 + pn * C::RPANEL, &tmR2, pn * 64, u.t * kRows, u.z, barRes);
                 }
                 ++units;
@@ -308,7 +352,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     }
                 }
             }
-            if (units > 0) bounded_wait(barRes, (units - 1) & 1, abort_flag, tmo, S_DRAIN, status, false);
+            if (C::NRES && units > 0) bounded_wait(barRes, (units - 1) & 1, abort_flag, tmo, S_DRAIN, status, false);
             for (uint32_t x = g > 2 ? g - 2 : 0; x < g; ++x) bounded_wait(barVec + 8 * (x & 1), (x >> 1) & 1, abort_flag, tmo, S_DRAIN, status, false);
         }
     } else if (warp == 1) {
@@ -333,76 +377,88 @@ __global__ void __launch_bounds__(THREADS, 1)
         // sums += (P or dS, 16-bit pairs, each half of the columns over its own scores) x streamed rows (MN-major)
         auto issue_sums = [&](uint32_t d, uint32_t tP, uint32_t sB, bool first) {
             const uint32_t blo = sdesc_lo(sB, C::SPANEL);
-            if constexpr (BN == 128) {
-                mma_ts4_elect<8, 16, 24, 128>(d, tP, blo, HI, idAcc, first ? 0u : 1u);
-                mma_ts4_elect<8, 16, 24, 128>(d, tP + 64, blo + 512, HI, idAcc, 1u);
-            } else {
-                mma_ts4_elect<8, 32, 40, 128>(d, tP, blo, HI, idAcc, first ? 0u : 1u);
-            }
+#pragma unroll
+            for (int k = 0; k < BN; k += 64)   // 16 values (8 columns) of a step, HB / 16 of them side by side
+                mma_ts4_elect<C::HB == 16 ? 16 : 8, C::HB == 64 ? 16 : 32, C::HB == 64 ? 24 : C::HB == 32 ? 40 : 48, 128>(
+                    d, tP + k, blo + 8 * k, HI, idAcc, first && k == 0 ? 0u : 1u);
         };
         auto tS = [&](uint32_t gs) { return tmem + C::COL_S + (C::NSB == 2 ? (gs & 1) * BN : 0); };
-        uint32_t g = 0, units = 0;   // steps and units so far; step g's tiles are the ring's loads 2 g and 2 g + 1
+        uint32_t g = 0, units = 0, use = 0;   // steps, units and ring slots so far
         bool ok = true;
-        auto do_s = [&](uint32_t gs) {
-            if (!wait_full(2 * gs)) return false;
+        // step gs, whose tiles are the ring's loads x and x + 1
+        auto do_s = [&](uint32_t gs, uint32_t x) {
+            if (!wait_full(x)) return false;
             tc_fence_after();
-            issue_scores(tS(gs), C::A1T, tmem + C::COL_A1, sR1, slot(2 * gs));
+            issue_scores(tS(gs), C::A1T, tmem + C::COL_A1, sR1, slot(x));
             tc_commit_elect(barS + 8 * (gs & 1));
-            if (!C::HAS_DS) free_slot(2 * gs);
+            if (!C::HAS_DS) free_slot(x);
             return true;
         };
-        auto do_dp = [&](uint32_t gs, bool last) {
-            if (!wait_full(2 * gs + 1)) return false;
+        auto do_dp = [&](uint32_t x, bool last) {
+            if (!wait_full(x + 1)) return false;
             tc_fence_after();
-            issue_scores(tmem + C::COL_DP, C::A2T, tmem + C::COL_A2, sR2, slot(2 * gs + 1));
+            issue_scores(tmem + C::COL_DP, C::A2T, tmem + C::COL_A2, sR2, slot(x + 1));
             tc_commit_elect(barDP);
-            if (!C::HAS_DV) free_slot(2 * gs + 1);
+            if (!C::HAS_DV) free_slot(x + 1);
             if (last && !(C::A1T && C::A2T)) tc_commit_elect(barFree);   // S and dP were the readers of the resident tiles
             return true;
         };
         Unit u;
         for (int round = 0; ok && unit_at<C::ROWQ, BN>(p.s, gridDim.x, blockIdx.x, round, u); ++round) {
             if (u.n == 0) continue;
-            ok = wait(barRes, units & 1, S_RES);
+            ok = !C::NRES || wait(barRes, units & 1, S_RES);
             if (!ok) break;
             ++units;
-            tc_fence_after();
-            // The readers of the operands' columns, the scores of the unit before, are done: their last results were
-            // read before the last wait above.
+            // Into tensor memory.  The readers of the operands' columns, the scores of the unit before, are done: their last
+            // results were read before the last wait above.
+            if constexpr (C::RUSES > 0) {
+                for (int i = 0; i < C::RUSES && ok; ++i) {
+                    ok = wait_full(use);
+                    if (!ok) break;
+                    tc_fence_after();
 #pragma unroll
-            for (int pn = 0; pn < C::PANELS; ++pn)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    if (C::A1T) copy_elect(tmem + C::COL_A1 + 32 * pn + 8 * k, sdesc_lo(sR1 + pn * C::RPANEL, 16) + 2 * k, HI);
-                    if (C::A2T) copy_elect(tmem + C::COL_A2 + 32 * pn + 8 * k, sdesc_lo(sR2 + pn * C::RPANEL, 16) + 2 * k, HI);
+                    for (int k = 0; k < 8; ++k)
+                        copy_elect(tmem + C::COL_A1 + 64 * i + 8 * k, sdesc_lo(slot(use) + (k / 4) * C::RPANEL, 16) + 2 * (k % 4), HI);
+                    free_slot(use++);
                 }
-            if (C::A1T && (C::A2T || !C::HAS_DS)) tc_commit_elect(barFree);
-            ok = do_s(g);
-            if (ok && C::HAS_DS) ok = do_dp(g, u.n == 1);
-            for (int j = 0; j < u.n && ok; ++j) {
+                if (!ok) break;
+            } else {
+                tc_fence_after();
+#pragma unroll
+                for (int pn = 0; pn < C::PANELS; ++pn)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        if (C::A1T) copy_elect(tmem + C::COL_A1 + 32 * pn + 8 * k, sdesc_lo(sR1 + pn * C::RPANEL, 16) + 2 * k, HI);
+                        if (C::A2T) copy_elect(tmem + C::COL_A2 + 32 * pn + 8 * k, sdesc_lo(sR2 + pn * C::RPANEL, 16) + 2 * k, HI);
+                    }
+                if (C::A1T && C::A2T) tc_commit_elect(barFree);
+            }
+            ok = do_s(g, use);
+            if (ok && C::HAS_DS) ok = do_dp(use, u.n == 1);
+            for (int j = 0; j < u.n && ok; ++j, use += 2) {
                 const uint32_t gs = g + j;
                 const bool more = j + 1 < u.n;
-                if (C::NSB == 2 && more) ok = do_s(gs + 1);
+                if (C::NSB == 2 && more) ok = do_s(gs + 1, use + 2);
                 ok = ok && wait(barP + 8 * (gs & 1), (gs >> 1) & 1, S_P);
                 if (!ok) break;
                 tc_fence_after();
                 if constexpr (C::HAS_DV) {
                     if (!C::HAS_DS) {   // otherwise dP's products have waited for the tile
-                        ok = wait_full(2 * gs + 1);
+                        ok = wait_full(use + 1);
                         if (!ok) break;
                         tc_fence_after();
                     }
-                    issue_sums(tmem + C::COL_ACCV, tS(gs), slot(2 * gs + 1), j == 0);
-                    free_slot(2 * gs + 1);
+                    issue_sums(tmem + C::COL_ACCV, tS(gs), slot(use + 1), j == 0);
+                    free_slot(use + 1);
                 }
-                if (C::NSB == 1 && more) ok = do_s(gs + 1);
+                if (C::NSB == 1 && more) ok = do_s(gs + 1, use + 2);
                 if constexpr (C::HAS_DS) {
                     ok = ok && wait(barDS, gs & 1, S_DS);
                     if (!ok) break;
                     tc_fence_after();
-                    issue_sums(tmem + C::COL_ACC, tmem + C::COL_DP, slot(2 * gs), j == 0);
-                    free_slot(2 * gs);
-                    if (more) ok = do_dp(gs + 1, j + 2 == u.n);
+                    issue_sums(tmem + C::COL_ACC, tmem + C::COL_DP, slot(use), j == 0);
+                    free_slot(use);
+                    if (more) ok = do_dp(use + 2, j + 2 == u.n);
                 }
             }
             if (!ok) break;
@@ -412,14 +468,14 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (!ok) tc_commit_elect(barAcc);   // everything issued ends before tensor memory is given back
         bounded_wait(barAcc, (units - 1) & 1, abort_flag, tmo, S_DRAIN, status, false);
         if (ok && units > 0) {   // no arrival is still on its way to this CTA's barriers when it ends
-            bounded_wait(barFree, (units - 1) & 1, abort_flag, tmo, S_DRAIN, status, false);
-            for (uint32_t x = 2 * g > C::NSLOT ? 2 * g - C::NSLOT : 0; x < 2 * g; ++x)
+            if (C::NRES) bounded_wait(barFree, (units - 1) & 1, abort_flag, tmo, S_DRAIN, status, false);
+            for (uint32_t x = use > C::NSLOT ? use - C::NSLOT : 0; x < use; ++x)
                 bounded_wait(bar_empty(x % C::NSLOT), (x / C::NSLOT) & 1, abort_flag, tmo, S_DRAIN, status, false);
         }
         __syncwarp();
     } else if (warp >= 4) {
         // ------------------------------------------------------------ probabilities, gradients, results
-        constexpr int HB = BN / 2;   // columns of a thread
+        constexpr int HB = C::HB, W = HB < 32 ? HB : 32;   // columns of a load
         const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
         const cache::WarpWait wait{abort_flag, tmo, status};
         const uint64_t sl2 = f2_pack(p.sl2, p.sl2), cc = f2_pack(p.dscale, p.dscale);
@@ -437,8 +493,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             const size_t at = parts ? (size_t)u.slot * kRows + r : (size_t)u.z * p.s.rows + row;
             float *part = parts ? p.part : nullptr, *part_v = parts ? p.part_v : nullptr;
             if (u.n == 0) {   // nothing is seen: the sums are empty
-                if (C::HAS_DS) fill_row<D>(p.out, part, at, valid, half * (D / 2), D / 2, 0u);
-                if (C::HAS_DV) fill_row<D>(p.out_v, part_v, at, valid, half * (D / 2), D / 2, 0u);
+                if (C::HAS_DS) fill_row<D>(p.out, part, at, valid, part_of * C::HD, C::HD, 0u);
+                if (C::HAS_DV) fill_row<D>(p.out_v, part_v, at, valid, part_of * C::HD, C::HD, 0u);
                 continue;
             }
             uint64_t nl_row = 0, dc_row = 0;
@@ -450,18 +506,18 @@ __global__ void __launch_bounds__(THREADS, 1)
             int tile = u.tile;
             for (int j = 0; j < u.n; ++j) {
                 const uint32_t gs = g + j, par = (gs >> 1) & 1;
-                const uint32_t tSb = tmem + lane_off + C::COL_S + (C::NSB == 2 ? (gs & 1) * BN : 0) + half * HB;
-                const uint32_t vec = sVec + (gs & 1) * C::VEC + half * HB * 4;
+                const uint32_t tSb = tmem + lane_off + C::COL_S + (C::NSB == 2 ? (gs & 1) * BN : 0) + part_of * HB;
+                const uint32_t vec = sVec + (gs & 1) * C::VEC + part_of * HB * 4;
                 if (!C::ROWQ) ok = wait(barVec + 8 * (gs & 1), par, S_VEC);
                 ok = ok && wait(barS + 8 * (gs & 1), par, S_S);
                 if (!ok) break;
                 tc_fence_after();
                 uint32_t sv[HB];
 #pragma unroll
-                for (int c = 0; c < HB; c += 32) tmem_ld_x32(tSb + c, *reinterpret_cast<uint32_t(*)[32]>(sv + c));
+                for (int c = 0; c < HB; c += W) load_columns<W>(tSb + c, sv + c);
                 tmem_wait_ld();
 #pragma unroll
-                for (int c = 0; c < HB; c += 32) reg_fence_x32(*reinterpret_cast<uint32_t(*)[32]>(sv + c));
+                for (int c = 0; c < HB; c += W) fence_columns<W>(sv + c);
                 if (!C::HAS_DV) publish(barP + 8 * (gs & 1));   // the scores may be overwritten
                 float *s = reinterpret_cast<float *>(sv);
 #pragma unroll
@@ -482,13 +538,13 @@ __global__ void __launch_bounds__(THREADS, 1)
                     if (base + BN > p.s.cols || (p.s.causal && base + BN - 1 > u.t * kRows + p.s.coff)) {
                         long long lim = p.s.cols - 1;
                         if (p.s.causal) lim = min(lim, (long long)row + p.s.coff);
-                        const int last = (int)max(lim - base - half * HB, -1ll);
+                        const int last = (int)max(lim - base - part_of * HB, -1ll);
 #pragma unroll
                         for (int c = 0; c < HB; ++c)
                             if (c > last) s[c] = 0.f;
                     }
                 } else if (p.s.causal && (long long)u.t * kRows + kRows - 1 - p.s.coff > base) {
-                    const long long lim = (long long)row - p.s.coff - base - half * HB;
+                    const long long lim = (long long)row - p.s.coff - base - part_of * HB;
                     const int from = (int)min(max(lim, 0ll), (long long)HB);
 #pragma unroll
                     for (int c = 0; c < HB; ++c)
@@ -496,29 +552,29 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
                 if constexpr (C::HAS_DV) {
 #pragma unroll
-                    for (int c = 0; c < HB; c += 32) {
-                        uint32_t pk[16];
+                    for (int c = 0; c < HB; c += W) {
+                        uint32_t pk[W / 2];
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) pk[e] = pack2<BF16>(s[c + 2 * e], s[c + 2 * e + 1]);
-                        tmem_st_x16(tSb + c / 2, pk);
+                        for (int e = 0; e < W / 2; ++e) pk[e] = pack2<BF16>(s[c + 2 * e], s[c + 2 * e + 1]);
+                        store_columns<W / 2>(tSb + c / 2, pk);
                     }
                     tmem_wait_st();
                     publish(barP + 8 * (gs & 1));
                 }
                 if constexpr (C::HAS_DS) {
-                    const uint32_t tDP = tmem + lane_off + C::COL_DP + half * HB;
+                    const uint32_t tDP = tmem + lane_off + C::COL_DP + part_of * HB;
                     ok = wait(barDP, gs & 1, S_DP);
                     if (!ok) break;
                     tc_fence_after();
                     uint32_t ds[HB / 2];
 #pragma unroll
-                    for (int c = 0; c < HB; c += 32) {
-                        uint32_t dv[32];
-                        tmem_ld_x32(tDP + c, dv);
+                    for (int c = 0; c < HB; c += W) {
+                        uint32_t dv[W];
+                        load_columns<W>(tDP + c, dv);
                         tmem_wait_ld();
-                        reg_fence_x32(dv);
+                        fence_columns<W>(dv);
 #pragma unroll
-                        for (int e = 0; e < 32; e += 4) {
+                        for (int e = 0; e < W; e += 4) {
                             uint64_t d0 = dc_row, d1 = dc_row;
                             if constexpr (!C::ROWQ) ld_shared_2x64(vec + BN * 4 + 4 * (c + e), d0, d1);   
                             const uint64_t x0 = f2_fma(f2_pack(__uint_as_float(dv[e]), __uint_as_float(dv[e + 1])), cc, d0);
@@ -531,7 +587,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         }
                     }
 #pragma unroll
-                    for (int c = 0; c < HB; c += 32) tmem_st_x16(tDP + c / 2, *reinterpret_cast<uint32_t(*)[16]>(ds + c / 2));
+                    for (int c = 0; c < HB; c += W) store_columns<W / 2>(tDP + c / 2, ds + c / 2);
                     tmem_wait_st();
                     publish(barDS);
                 }
@@ -546,8 +602,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             tc_fence_after();
             g += u.n;
             ++units;
-            if (C::HAS_DS) write_row<D, BF16>(tmem + lane_off + C::COL_ACC, p.out, part, at, valid, half * (D / 2), D / 2, p.out_scale, p.al32);
-            if (C::HAS_DV) write_row<D, BF16>(tmem + lane_off + C::COL_ACCV, p.out_v, part_v, at, valid, half * (D / 2), D / 2, p.out_v_scale, p.al32);
+            if (C::HAS_DS) write_row<D, C::HD, BF16>(tmem + lane_off + C::COL_ACC, p.out, part, at, valid, part_of * C::HD, p.out_scale, p.al32);
+            if (C::HAS_DV) write_row<D, C::HD, BF16>(tmem + lane_off + C::COL_ACCV, p.out_v, part_v, at, valid, part_of * C::HD, p.out_v_scale, p.al32);
         }
     }
 
@@ -586,7 +642,7 @@ cudaError_t launch_one(const Maps &m, const Params &p, cudaStream_t stream)
     Params q = p;
     if (q.timeout_ns == 0) q.timeout_ns = kDefaultTimeoutNs;
     const int sms = sm_count[dev].load(std::memory_order_relaxed), grid = q.s.num < sms ? q.s.num : sms;
-    kern<<<grid, THREADS, C::ALLOC, stream>>>(m.r1, m.r2, m.s1, m.s2, q);
+    kern<<<grid, C::THREADS, C::ALLOC, stream>>>(m.r1, m.r2, m.s1, m.s2, q);
     return cudaGetLastError();
 }
 

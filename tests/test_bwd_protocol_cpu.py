@@ -10,12 +10,13 @@ import random
 
 import pytest
 
-# mode: dS and dQ or dK; dV; a row of lse a thread (queries resident); operands in tensor memory; score buffers; ring slots
+# dS and dQ or dK; dV; lse of the streamed rows; operands in tensor memory; score buffers; ring slots; slots through which the first
+# resident operand comes (0: a buffer of its own)
 MODES = {
     "q64": dict(ds=1, dv=0, vec=0, a1t=1, a2t=1, nsb=2, slots=8), "q128": dict(ds=1, dv=0, vec=0, a1t=1, a2t=1, nsb=1, slots=5),
-    "q256": dict(ds=1, dv=0, vec=0, a1t=1, a2t=0, nsb=1, slots=3), "kv64": dict(ds=1, dv=1, vec=1, a1t=0, a2t=0, nsb=2, slots=8),
-    "kv128": dict(ds=1, dv=1, vec=1, a1t=0, a2t=0, nsb=1, slots=5), "k256": dict(ds=1, dv=0, vec=1, a1t=1, a2t=0, nsb=1, slots=3),
-    "v256": dict(ds=0, dv=1, vec=1, a1t=1, a2t=0, nsb=2, slots=4),
+    "q256": dict(ds=1, dv=0, vec=0, a1t=1, a2t=0, nsb=1, slots=5, ring=2), "kv64": dict(ds=1, dv=1, vec=1, a1t=0, a2t=0, nsb=2, slots=8),
+    "kv128": dict(ds=1, dv=1, vec=1, a1t=0, a2t=0, nsb=1, slots=5), "k256": dict(ds=1, dv=0, vec=1, a1t=1, a2t=0, nsb=1, slots=5, ring=2),
+    "v256": dict(ds=0, dv=1, vec=1, a1t=1, a2t=0, nsb=2, slots=7, ring=2),
 }
 WARPS = 3
 
@@ -53,7 +54,8 @@ class Bar:
 
 
 def simulate(mode, seed, leave_out=None):
-    m, rnd = MODES[mode], random.Random(seed)
+    m, rnd = dict(dict(ring=0), **MODES[mode]), random.Random(seed)
+    nres = (0 if m["ring"] else 1) + m["ds"]   # resident operands with a buffer
     units = [rnd.choice((1, 1, 2, 3, 5)) for _ in range(rnd.randint(1, 5))]
     N, nsb = m["slots"], m["nsb"]
     full, empty = [Bar(1) for _ in range(N)], [Bar(1) for _ in range(N)]
@@ -77,24 +79,24 @@ def simulate(mode, seed, leave_out=None):
     def ring():
         use = 0
         for u, n in enumerate(units):
-            for j in range(n):
-                for which in (0, 1):
-                    s = use % N
-                    yield from wait(empty[s], ((use // N) & 1) ^ 1, "empty")
-                    full[s].arrive(1)
-                    slot[s] = None
-                    landing.append((slot, s, use, full[s]))
-                    use += 1
-                    yield
+            for what in [("r", u, i) for i in range(m["ring"])] + [(i, sum(units[:u]) + j) for j in range(n) for i in (0, 1)]:
+                s = use % N
+                yield from wait(empty[s], ((use // N) & 1) ^ 1, "empty")
+                full[s].arrive(1)
+                slot[s] = None
+                landing.append((slot, s, what, full[s]))
+                use += 1
+                yield
 
     def second():
         g = 0
         for u, n in enumerate(units):
-            if u:
-                yield from wait(free, (u - 1) & 1, "free")
-            res.arrive(1)
-            resident[0] = None
-            landing.append((resident, 0, u, res))
+            if nres:
+                if u:
+                    yield from wait(free, (u - 1) & 1, "free")
+                res.arrive(1)
+                resident[0] = None
+                landing.append((resident, 0, u, res))
             for j in range(n if m["vec"] else 0):
                 v = g & 1
                 yield from wait(vec_free[v], ((g >> 1) & 1) ^ 1, "vec_free")
@@ -119,30 +121,30 @@ def simulate(mode, seed, leave_out=None):
             yield
 
     def mma():
-        g = 0
+        g = use = 0
 
-        def op_s(u, gs):
+        def op_s(u, gs, x):
             def f():
-                need(slot[2 * gs % N] == 2 * gs, "scores read another tile")
+                need(slot[x % N] == (0, gs), "scores read another tile")
                 need((operand[0] if m["a1t"] else resident[0]) == u, "scores read another resident tile")
                 b = gs % nsb
                 need(scores[b] is None or (scores[b][0] == "free" and len(p_by[b]) in (0, WARPS)), "scores written over values in use")
                 scores[b], p_by[b] = ("s", gs), set()
             return f
 
-        def op_dp(u, gs):
+        def op_dp(u, gs, x):
             def f():
-                need(slot[(2 * gs + 1) % N] == 2 * gs + 1, "dP reads another tile")
+                need(slot[(x + 1) % N] == (1, gs), "dP reads another tile")
                 need((operand[0] if m["a2t"] else resident[0]) == u, "dP reads another resident tile")
                 need(grads[0] is None or grads[0][0] == "free", "dP written over values in use")
                 grads[0] = ("dp", gs)
                 ds_by.clear()
             return f
 
-        def op_dv(u, gs, first):
+        def op_dv(u, gs, x, first):
             def f():
                 b = gs % nsb
-                need(slot[(2 * gs + 1) % N] == 2 * gs + 1, "dV reads another tile")
+                need(slot[(x + 1) % N] == (1, gs), "dV reads another tile")
                 need(p_by[b] == set(range(WARPS)) and scores[b] == ("s", gs), "dV reads values that are not P")
                 scores[b] = ("free", gs)
                 if first:
@@ -150,9 +152,9 @@ def simulate(mode, seed, leave_out=None):
                 sums["accv"].append(gs)
             return f
 
-        def op_acc(u, gs, first):
+        def op_acc(u, gs, x, first):
             def f():
-                need(slot[2 * gs % N] == 2 * gs, "dQ or dK reads another tile")
+                need(slot[x % N] == (0, gs), "dQ or dK reads another tile")
                 need(ds_by == set(range(WARPS)) and grads[0] == ("dp", gs), "dQ or dK reads values that are not dS")
                 grads[0] = ("free", gs)
                 if first:
@@ -163,52 +165,63 @@ def simulate(mode, seed, leave_out=None):
         commit = lambda bar: pipe.append(bar.arrive)  # noqa: E731
         full_of = lambda use, name: wait(full[use % N], (use // N) & 1, name)  # noqa: E731
 
-        def do_s(u, gs):
-            yield from full_of(2 * gs, "full1")
-            pipe.append(op_s(u, gs))
+        def do_s(u, gs, x):
+            yield from full_of(x, "full1")
+            pipe.append(op_s(u, gs, x))
             commit(bar_s[gs & 1])
             if not m["ds"]:
-                commit(empty[2 * gs % N])
+                commit(empty[x % N])
 
-        def do_dp(u, gs, last):
-            yield from full_of(2 * gs + 1, "full2")
-            pipe.append(op_dp(u, gs))
+        def do_dp(u, gs, x, last):
+            yield from full_of(x + 1, "full2")
+            pipe.append(op_dp(u, gs, x))
             commit(dp)
             if not m["dv"]:
-                commit(empty[(2 * gs + 1) % N])
+                commit(empty[(x + 1) % N])
             if last and not (m["a1t"] and m["a2t"]):
                 commit(free)
 
         for u, n in enumerate(units):
-            yield from wait(res, u & 1, "res")
-            if m["a1t"]:
+            if nres:
+                yield from wait(res, u & 1, "res")
+            for i in range(m["ring"]):
+                yield from full_of(use, "full_r")
+
+                def copy_slot(u=u, i=i, use=use):
+                    need(slot[use % N] == ("r", u, i), "another tile is copied")
+                    operand[0] = u if i == m["ring"] - 1 else None
+                pipe.append(copy_slot)
+                commit(empty[use % N])
+                use += 1
+            if m["a1t"] and not m["ring"]:
                 def copy(u=u):
                     need(resident[0] == u, "another resident tile is copied")
                     operand[0] = u
                 pipe.append(copy)
-            if m["a1t"] and (m["a2t"] or not m["ds"]):
+            if m["a1t"] and m["a2t"]:
                 commit(free)
-            yield from do_s(u, g)
+            yield from do_s(u, g, use)
             if m["ds"]:
-                yield from do_dp(u, g, n == 1)
+                yield from do_dp(u, g, use, n == 1)
             for j in range(n):
                 gs, more = g + j, j + 1 < n
                 if nsb == 2 and more:
-                    yield from do_s(u, gs + 1)
+                    yield from do_s(u, gs + 1, use + 2)
                 yield from wait(bar_p[gs & 1], (gs >> 1) & 1, "p")
                 if m["dv"]:
                     if not m["ds"]:
-                        yield from full_of(2 * gs + 1, "full2")
-                    pipe.append(op_dv(u, gs, j == 0))
-                    commit(empty[(2 * gs + 1) % N])
+                        yield from full_of(use + 1, "full2")
+                    pipe.append(op_dv(u, gs, use, j == 0))
+                    commit(empty[(use + 1) % N])
                 if nsb == 1 and more:
-                    yield from do_s(u, gs + 1)
+                    yield from do_s(u, gs + 1, use + 2)
                 if m["ds"]:
                     yield from wait(ds, gs & 1, "ds")
-                    pipe.append(op_acc(u, gs, j == 0))
-                    commit(empty[2 * gs % N])
+                    pipe.append(op_acc(u, gs, use, j == 0))
+                    commit(empty[use % N])
                     if more:
-                        yield from do_dp(u, gs + 1, j + 2 == n)
+                        yield from do_dp(u, gs + 1, use + 2, j + 2 == n)
+                use += 2
             commit(acc)
             g += n
         yield from wait(acc, (len(units) - 1) & 1)
@@ -277,7 +290,8 @@ def test_protocol(mode):
 
 
 # what each mode waits for, and what goes wrong without
-@pytest.mark.parametrize("mode,name", [(m, n) for m, c in MODES.items() for n in ("full1", "full2", "empty", "res", "free", "s", "acc") +
+@pytest.mark.parametrize("mode,name", [(m, n) for m, c in MODES.items() for n in ("full1", "full2", "empty", "s", "acc") +
+                                       (("full_r",) if c.get("ring") else ()) + (("res", "free") if c["ds"] or not c.get("ring") else ()) +
                                        (("p",) if c["dv"] or c["nsb"] == 1 else ()) +   # else implied by the wait for dS
                                        (("dp", "ds") if c["ds"] else ()) + (("vec", "vec_free") if c["vec"] else ())])
 def test_a_wait_left_out_is_found(mode, name):
