@@ -147,8 +147,10 @@ int fa_bwd_debug(const void *q, const void *k, const void *v, const void *o, con
             a.part = part_k;
             a.part_v = part_v;
         }
+        a.first = 1;
         if (D == 256) {
             e = launch_bwd(kV, D, bf16, mk, a, s);
+            a.first = 0;
             if (e == cudaSuccess) e = launch_bwd(kK, D, bf16, mk, a, s);
         } else {
             e = launch_bwd(kKV, D, bf16, mk, a, s);
@@ -158,6 +160,7 @@ int fa_bwd_debug(const void *q, const void *k, const void *v, const void *o, con
         Params a = p;
         a.s = plan.q;
         a.out = dq;
+        a.first = !dk;
         a.al32 = aligned(dq, 32);
         if (plan.q.parts > 1) a.part = part_q;
         e = launch_bwd(kQ, D, bf16, mq, a, s);

@@ -137,6 +137,7 @@ struct Params {
     float dscale;            // 2^-shift
     float out_scale, out_v_scale;
     uint32_t al32;           // outputs are 32-byte aligned
+    uint32_t first;          // the first kernel behind lse and delta
     uint64_t timeout_ns;
     uint32_t inject;         // fault injection: the first second tile is never loaded (bit 0: in every CTA, bit 1: in CTA 0)
 };

@@ -37,9 +37,6 @@ namespace bwd {
 
 __device__ unsigned int g_bwd_status;
 
-#ifndef FA_CW
-#define FA_CW 8
-#endif
 namespace {
 
 constexpr uint64_t kDefaultTimeoutNs = 2000000000ull;
@@ -54,7 +51,7 @@ struct Cfg {
     static constexpr bool HAS_DV = MODE == kKV || MODE == kV;
     static constexpr int BN = step_rows(D);
     static constexpr int PANELS = D / 64;
-    static constexpr int CW = FA_CW;                           // warps that compute
+    static constexpr int CW = 8;                               // warps that compute (16: the same time)
     static constexpr int THREADS = 128 + 32 * CW;
     static constexpr int HB = BN / (CW / 4), HD = D / (CW / 4);   // a thread's columns of a step, and of the results
     // Resident operands in tensor memory (16-bit pairs, D / 2 columns), where it has room: a product with both
@@ -242,6 +239,7 @@ __global__ void __launch_bounds__((Cfg<MODE, D>::THREADS), 1)
 
     if (pad + (uint32_t)C::BYTES > dynamic_smem_size_u32()) {
         if (threadIdx.x == 0) atomicOr(status, 1u | (S_SMEM << 8));
+        cache::grid_wait();
         if (warp >= 4) each_unit_filled(~0u);
         return;
     }
@@ -272,6 +270,12 @@ __global__ void __launch_bounds__((Cfg<MODE, D>::THREADS), 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_holder;
+
+    // Each kernel of a pass may start while the one before it drains.  The first waits for lse and delta (and with them for everything
+    // before the call); those behind it start after that wait, need nothing that it computes, and wait for its end at
+    // their own, so that what follows the last kernel follows them all.
+    if (p.first) cache::grid_wait();
+    cache::grid_done_soon();
 
     if (warp == 0) {
         // ------------------------------------------------------------ streamed tiles, in the order of their first use
@@ -616,6 +620,7 @@ __global__ void __launch_bounds__((Cfg<MODE, D>::THREADS), 1)
     } else if (warp >= 4 && *abort_flag) {
         each_unit_filled(~0u);   // this CTA gave up on a wait: NaN in every row that it was given
     }
+    if (!p.first) cache::grid_wait();
 }
 
 template <int MODE, int D, bool BF16>
@@ -642,8 +647,7 @@ cudaError_t launch_one(const Maps &m, const Params &p, cudaStream_t stream)
     Params q = p;
     if (q.timeout_ns == 0) q.timeout_ns = kDefaultTimeoutNs;
     const int sms = sm_count[dev].load(std::memory_order_relaxed), grid = q.s.num < sms ? q.s.num : sms;
-    kern<<<grid, C::THREADS, C::ALLOC, stream>>>(m.r1, m.r2, m.s1, m.s2, q);
-    return cudaGetLastError();
+    return cache::launch_overlapped(kern, dim3((unsigned)grid), C::THREADS, C::ALLOC, 1, stream, m.r1, m.r2, m.s1, m.s2, q);
 }
 
 // ---------------------------------------------------------------- lse and delta
@@ -656,6 +660,8 @@ template <int D, bool BF16>
 __global__ void __launch_bounds__(kPrepThreads) prep_kernel(const uint4 *o, const uint4 *d_o, const float *lse, const float *dlse, float *nl, float *dc,
                                                             long long rows, int Sq, int pad, float shift, float down)
 {
+    cache::grid_wait();
+    cache::grid_done_soon();
     constexpr int L = D / 8;
     const long long i = (long long)blockIdx.x * (kPrepThreads / L) + threadIdx.x / L;   // row of the padded arrays
     const int lane = threadIdx.x % L;
@@ -700,15 +706,16 @@ cudaError_t prep_one(const void *o, const void *d_o, const float *lse, const flo
 {
     constexpr int per = kPrepThreads / (D / 8);
     const long long rows = planes * pad, blocks = (rows + per - 1) / per;
-    prep_kernel<D, BF16><<<(unsigned)blocks, kPrepThreads, 0, st>>>(static_cast<const uint4 *>(o), static_cast<const uint4 *>(d_o), lse, dlse, nl, dc, rows, Sq, pad,
-                                                                   shift, exp2f(-shift));
-    return cudaGetLastError();
+    return cache::launch_overlapped(prep_kernel<D, BF16>, dim3((unsigned)blocks), kPrepThreads, 0, 1, st, static_cast<const uint4 *>(o),
+                                    static_cast<const uint4 *>(d_o), lse, dlse, nl, dc, rows, Sq, pad, shift, exp2f(-shift));
 }
 
 // ---------------------------------------------------------------- parts of cut units, added in their order
 template <bool BF16>
 __global__ void __launch_bounds__(256) join_kernel(const float4 *part, uint2 *out, int parts, int rows, int tiles, int quads, long long n, float scale)
 {
+    cache::grid_wait();
+    cache::grid_done_soon();
     const long long i = (long long)blockIdx.x * 256 + threadIdx.x;   // four columns of one row of a unit
     if (i >= n) return;
     const int in_unit = kRows * quads;
@@ -748,12 +755,8 @@ cudaError_t launch_bwd(int mode, int D, bool bf16, const Maps &m, const Params &
 cudaError_t launch_join(const float *part, void *out, const Shape &s, int D, bool bf16, float scale, cudaStream_t st)
 {
     const long long n = (long long)s.planes * s.tiles * kRows * (D / 4);
-    const unsigned blocks = (unsigned)((n + 255) / 256);
-    if (bf16)
-        join_kernel<true><<<blocks, 256, 0, st>>>(reinterpret_cast<const float4 *>(part), static_cast<uint2 *>(out), s.parts, s.rows, s.tiles, D / 4, n, scale);
-    else
-        join_kernel<false><<<blocks, 256, 0, st>>>(reinterpret_cast<const float4 *>(part), static_cast<uint2 *>(out), s.parts, s.rows, s.tiles, D / 4, n, scale);
-    return cudaGetLastError();
+    return cache::launch_overlapped(bf16 ? join_kernel<true> : join_kernel<false>, dim3((unsigned)((n + 255) / 256)), 256, 0, 1, st,
+                                    reinterpret_cast<const float4 *>(part), static_cast<uint2 *>(out), s.parts, s.rows, s.tiles, D / 4, n, scale);
 }
 
 cudaError_t read_and_clear_bwd_status(uint32_t *word)
