@@ -167,7 +167,7 @@ int fa_fwd_debug(const void *q, const void *k, const void *v, void *o, float *ls
  * FA_ERR_TOO_LARGE: workspace_bytes is too small.  A device wait that gives up leaves NaN in the rows concerned
  * (fa_device_status).
  */
-size_t fa_bwd_workspace_bytes(int B, int Hq, int Hkv, int Sq, int Sk, int D);
+size_t fa_bwd_workspace_bytes(int B, int Hq, int Hkv, int Sq, int Sk, int D, int causal);
 int fa_bwd(const void *q, const void *k, const void *v, const void *o, const float *lse, const void *d_o, const float *dlse,
            void *dq, void *dk, void *dv, int B, int Hq, int Hkv, int Sq, int Sk, int D, int causal, float scale,
            int dtype, void *workspace, size_t workspace_bytes, fa_stream_t stream);

@@ -31,21 +31,22 @@ float shift_of(int dtype) { return dtype == 1 ? 12.f : 0.f; }
 // What a call's workspace holds: lse and delta of the padded rows, then the sums of cut units.
 struct Plan {
     Shape q, kv;
+    Cuts cut_q, cut_kv;
+    Join join_q, join_kv;
     long long pad;
     size_t vec, part_q, part_kv;   // bytes of one vector, of dQ's parts, of dK's (and again of dV's)
     size_t bytes() const { return 2 * vec + part_q + 2 * part_kv; }
 };
 
-Plan plan_of(int B, int Hq, int Hkv, int Sq, int Sk, int D, int causal)
+void make_plan(Plan &p, int B, int Hq, int Hkv, int Sq, int Sk, int D, int causal, bool want_q, bool want_kv)
 {
-    Plan p;
     p.pad = ((long long)Sq + kRows - 1) / kRows * kRows;
     p.vec = (size_t)B * Hq * p.pad * 4;
     p.q = make_shape(true, B, Hq, Hkv, Sq, Sk, D, causal);
     p.kv = make_shape(false, B, Hq, Hkv, Sq, Sk, D, causal);
-    p.part_q = p.q.parts > 1 ? (size_t)p.q.num * kRows * D * 4 : 0;
-    p.part_kv = p.kv.parts > 1 ? (size_t)p.kv.num * kRows * D * 4 : 0;
-    return p;
+    plan_cuts(p.q, p.kv, D, want_q, want_kv, p.cut_q, p.join_q, p.cut_kv, p.join_kv);
+    p.part_q = (size_t)parts_of(p.cut_q) * kRows * D * 4;
+    p.part_kv = (size_t)parts_of(p.cut_kv) * kRows * D * 4;
 }
 
 // Sizes that the schedule's 32-bit counts hold.
@@ -66,10 +67,16 @@ int check_sizes(int B, int Hq, int Hkv, int Sq, int Sk, int D, int causal)
 
 extern "C" {
 
-size_t fa_bwd_workspace_bytes(int B, int Hq, int Hkv, int Sq, int Sk, int D)
+size_t fa_bwd_workspace_bytes(int B, int Hq, int Hkv, int Sq, int Sk, int D, int causal)
 {
-    if (check_sizes(B, Hq, Hkv, Sq, Sk, D, 0) != FA_OK || B == 0 || Sq == 0 || Sk == 0) return 0;
-    return plan_of(B, Hq, Hkv, Sq, Sk, D, 0).bytes();
+    if (check_sizes(B, Hq, Hkv, Sq, Sk, D, causal) != FA_OK || B == 0 || Sq == 0 || Sk == 0) return 0;
+    Plan plan;
+    size_t most = 0;   // a call that leaves results out may cut others
+    for (int want = 1; want < 4; ++want) {
+        make_plan(plan, B, Hq, Hkv, Sq, Sk, D, causal, want & 1, want & 2);
+        if (plan.bytes() > most) most = plan.bytes();
+    }
+    return most;
 }
 
 int fa_bwd_debug(const void *q, const void *k, const void *v, const void *o, const float *lse, const void *d_o, const float *dlse, void *dq, void *dk, void *dv,
@@ -89,7 +96,8 @@ int fa_bwd_debug(const void *q, const void *k, const void *v, const void *o, con
     if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(o, 16) || !aligned(d_o, 16) || !aligned(dq, 16) || !aligned(dk, 16) ||
         !aligned(dv, 16) || !aligned(lse, 4) || !aligned(dlse, 4) || !aligned(workspace, 32))
         return FA_ERR_ALIGN;
-    const Plan plan = plan_of(B, Hq, Hkv, Sq, Sk, D, causal);
+    Plan plan;
+    if (Sq > 0) make_plan(plan, B, Hq, Hkv, Sq, Sk, D, causal, dq != nullptr, dk != nullptr);
     const size_t need = Sq > 0 ? plan.bytes() : 0;
     if (workspace_bytes < need) return FA_ERR_TOO_LARGE;
     const Range all[] = {range(dq, nq), range(dk, nk), range(dv, nk), range(workspace, need), range(q, nq), range(k, nk),
@@ -143,10 +151,9 @@ int fa_bwd_debug(const void *q, const void *k, const void *v, const void *o, con
         a.out = dk;
         a.out_v = dv;
         a.al32 = aligned(dk, 32) && aligned(dv, 32);
-        if (plan.kv.parts > 1) {
-            a.part = part_k;
-            a.part_v = part_v;
-        }
+        a.cuts = plan.cut_kv;
+        a.part = part_k;
+        a.part_v = part_v;
         a.first = 1;
         if (D == 256) {
             e = launch_bwd(kV, D, bf16, mk, a, s);
@@ -162,14 +169,12 @@ int fa_bwd_debug(const void *q, const void *k, const void *v, const void *o, con
         a.out = dq;
         a.first = !dk;
         a.al32 = aligned(dq, 32);
-        if (plan.q.parts > 1) a.part = part_q;
+        a.cuts = plan.cut_q;
+        a.part = part_q;
         e = launch_bwd(kQ, D, bf16, mq, a, s);
     }
-    if (e == cudaSuccess && dk && plan.kv.parts > 1) {
-        e = launch_join(part_k, dk, plan.kv, D, bf16, p.out_scale, s);
-        if (e == cudaSuccess) e = launch_join(part_v, dv, plan.kv, D, bf16, p.out_v_scale, s);
-    }
-    if (e == cudaSuccess && dq && plan.q.parts > 1) e = launch_join(part_q, dq, plan.q, D, bf16, p.out_scale, s);
+    if (e == cudaSuccess && plan.join_q.num + plan.join_kv.num > 0)
+        e = launch_join(JoinParams{plan.q, plan.kv, plan.join_q, plan.join_kv, part_q, part_k, part_v, dq, dk, dv, p.out_scale, p.out_v_scale}, D, bf16, s);
     return e == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
 }
 

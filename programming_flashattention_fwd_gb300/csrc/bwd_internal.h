@@ -19,10 +19,10 @@ enum Mode { kQ = 0, kKV = 1, kK = 2, kV = 3 };
 
 constexpr int kRows = 128;                                         // resident rows
 constexpr int step_rows(int D) { return D == 256 ? 64 : 128; }     // streamed rows of a step
-constexpr int kMaxParts = 160;   // parts of cut units that a workspace has room for
+constexpr int kCtas = 152;   // the SMs of a GB300: CTAs of a kernel whose steps are cut evenly
 
-// One kernel's line of work: units of (head plane, tile of 128 resident rows), each cut into `parts` runs of
-// its steps.  A step is one tile of step_rows streamed rows.
+// One kernel's line of work: units of (head plane, tile of 128 resident rows), whose steps are tiles of step_rows
+// streamed rows.
 struct Shape {
     int rows, cols;       // resident and streamed rows of a head: (Sq, Sk) or (Sk, Sq)
     int heads, group;     // resident heads of a sequence; query heads of a KV head
@@ -30,16 +30,31 @@ struct Shape {
     int causal;
     int tiles, steps;     // tiles of resident rows, of streamed rows
     int planes;           // B * heads
-    int parts, num;       // parts of a unit; planes * tiles * parts
-    FastDiv f_planes, f_tiles, f_heads, f_group, f_parts;
+    int num;              // planes * tiles
+    FastDiv f_planes, f_tiles, f_heads, f_group;
+};
+
+// How the units are dealt out.  Whole (ctas 0), or the line of all steps cut evenly: CTA c takes those from step `step[c]`
+// of unit `unit[c]` to step `step[c + 1]` of unit `unit[c + 1]`.  A unit that a cut crosses leaves a part for each CTA, in
+// slots that follow one another; units without steps, from `empty` on, are dealt out whole.
+struct Cuts {
+    int ctas, empty;
+    int unit[kCtas + 1], step[kCtas + 1];
+    int slot[kCtas + 1];   // the CTA's first part
+};
+
+// The units that are cut: unit[i] has the parts slot[i] .. slot[i + 1] - 1.
+struct Join {
+    int num;
+    int unit[kCtas], slot[kCtas + 1];
 };
 
 struct Unit {
     int z, t;             // resident plane and tile
-    int n;                // steps of this part
+    int n;                // steps (of this part)
     int plane, tile;      // streamed plane and tile of its first step
     int first, end;       // streamed tiles of a plane: [first, end)
-    int slot;             // (unit, part): where a cut unit's part is left
+    int slot;             // where a part is left, or -1: whole
 };
 
 // Steps of the tile t: [first, end) of each streamed plane.
@@ -63,45 +78,44 @@ __host__ __device__ __forceinline__ void seen(const Shape &s, int t, int &first,
 // The unit that CTA c of G takes in `round`; false where it has no more.  With a mask the heaviest tiles come first
 // (the last queries, the first keys), without one neighbouring units share the streamed heads.
 template <bool ROWQ, int BN>
-__host__ __device__ __forceinline__ bool unit_at(const Shape &s, int G, int c, int round, Unit &u)
+__host__ __device__ __forceinline__ bool unit_at(const Shape &s, const Cuts &cuts, int G, int c, int round, Unit &u)
 {
-    const long long g64 = unit_index(G, c, round);
-    if (g64 >= s.num) return false;
-    const uint32_t g = (uint32_t)g64, w = fdiv(g, s.f_parts);
-    const int part = (int)(g - w * s.f_parts.d);
-    if (s.causal) {
-        const uint32_t q = fdiv(w, s.f_planes);
-        u.t = ROWQ ? s.tiles - 1 - (int)q : (int)q;
-        u.z = (int)(w - q * s.f_planes.d);
+    long long w;
+    int n0 = 0, n1 = -1;
+    if (cuts.ctas == 0) {
+        w = unit_index(G, c, round);
     } else {
-        const uint32_t q = fdiv(w, s.f_tiles);
+        const int a = cuts.unit[c], b = cuts.unit[c + 1], e = cuts.step[c + 1], own = b - a + (e > 0);
+        w = a + round;
+        if (round >= own) {
+            w = (long long)cuts.empty + c + (long long)(round - own) * G;
+        } else {
+            if (round == 0) n0 = cuts.step[c];
+            if (w == b) n1 = e;
+        }
+    }
+    if (w >= s.num) return false;
+    if (s.causal) {
+        const uint32_t q = fdiv((uint32_t)w, s.f_planes);
+        u.t = ROWQ ? s.tiles - 1 - (int)q : (int)q;
+        u.z = (int)((uint32_t)w - q * s.f_planes.d);
+    } else {
+        const uint32_t q = fdiv((uint32_t)w, s.f_tiles);
         u.z = (int)q;
-        u.t = (int)(w - q * s.f_tiles.d);
+        u.t = (int)((uint32_t)w - q * s.f_tiles.d);
     }
     const int b = (int)fdiv((uint32_t)u.z, s.f_heads), h = u.z - b * s.heads;
     seen<ROWQ, BN>(s, u.t, u.first, u.end);
-    const int per = u.end - u.first;
-    const long long all = ROWQ ? per : (long long)per * s.group;
-    const int n0 = (int)(all * part / s.parts), n1 = (int)(all * (part + 1) / s.parts);
+    const int per = u.end - u.first, all = ROWQ ? per : per * s.group;
+    if (n1 < 0) n1 = all;
     u.n = n1 - n0;
+    u.slot = u.n == all ? -1 : cuts.slot[c] + (round > 0 && cuts.step[c] > 0 ? 1 : 0);
     const int skip = per > 0 ? n0 / per : 0;
     u.plane = ROWQ ? b * (s.heads / s.group) + (int)fdiv((uint32_t)h, s.f_group) : u.z * s.group + skip;
     u.tile = u.first + (ROWQ ? n0 : n0 - skip * per);
-    u.slot = (u.z * s.tiles + u.t) * s.parts + part;
     return true;
 }
 
-inline void set_divisors(Shape &s)
-{
-    s.f_planes = make_fastdiv((uint32_t)s.planes);
-    s.f_tiles = make_fastdiv((uint32_t)s.tiles);
-    s.f_heads = make_fastdiv((uint32_t)s.heads);
-    s.f_group = make_fastdiv((uint32_t)s.group);
-    s.f_parts = make_fastdiv((uint32_t)s.parts);
-}
-
-// The shape of a kernel's work.  Where the units alone would leave SMs idle, their steps are cut into parts, as
-// many as fit kMaxParts slots and leave at least two steps to a part.
 inline Shape make_shape(bool rowq, int B, int Hq, int Hkv, int Sq, int Sk, int D, int causal)
 {
     Shape s = {};
@@ -115,24 +129,152 @@ inline Shape make_shape(bool rowq, int B, int Hq, int Hkv, int Sq, int Sk, int D
     s.tiles = (s.rows + kRows - 1) / kRows;
     s.steps = (s.cols + BN - 1) / BN;
     s.planes = B * s.heads;
-    const long long units = (long long)s.planes * s.tiles, longest = (long long)s.steps * (rowq ? 1 : s.group);
-    s.parts = 1;
-    if (units > 0 && units * 2 <= kMaxParts) {
-        const long long most = kMaxParts / units, able = longest / 2;
-        s.parts = (int)(most < able ? most : able);
-        if (s.parts < 1) s.parts = 1;
-    }
-    s.num = (int)(units * s.parts);
-    set_divisors(s);
+    s.num = s.planes * s.tiles;
+    s.f_planes = make_fastdiv((uint32_t)s.planes);
+    s.f_tiles = make_fastdiv((uint32_t)s.tiles);
+    s.f_heads = make_fastdiv((uint32_t)s.heads);
+    s.f_group = make_fastdiv((uint32_t)s.group);
     return s;
 }
 
+// Runs of units with as many steps each, in the order of unit_at: f(first unit, units, steps of each).
+template <bool ROWQ, int BN, typename F>
+inline void for_runs(const Shape &s, F f)
+{
+    if (!s.causal) {
+        f(0, s.num, ROWQ ? (long long)s.steps : (long long)s.steps * s.group);
+        return;
+    }
+    for (int q = 0; q < s.tiles; ++q) {
+        int first, end;
+        seen<ROWQ, BN>(s, ROWQ ? s.tiles - 1 - q : q, first, end);
+        f(q * s.planes, s.planes, (long long)(end - first) * (ROWQ ? 1 : s.group));
+    }
+}
+
+// Steps of unit w.
+template <bool ROWQ, int BN>
+inline long long unit_steps(const Shape &s, long long w)
+{
+    int first = 0, end = s.steps;
+    if (s.causal) {
+        const int q = (int)(w / s.planes);
+        seen<ROWQ, BN>(s, ROWQ ? s.tiles - 1 - q : q, first, end);
+    }
+    return (long long)(end - first) * (ROWQ ? 1 : s.group);
+}
+
+// What a kernel has to do, in steps: all of it, and the longest line where whole units are dealt out (it begins with the
+// heaviest unit, or is among those of the last round).
+struct Load {
+    long long total, units, longest;   // units: those that have steps
+};
+
+template <bool ROWQ, int BN>
+inline Load load_of(const Shape &s)
+{
+    Load l = {0, 0, 0};
+    for_runs<ROWQ, BN>(s, [&](long long, long long n, long long steps) {
+        l.total += n * steps;
+        if (steps > 0) l.units += n;
+    });
+    const long long rounds = (s.num + kCtas - 1) / kCtas, tail = s.num - (rounds - 1) * kCtas;
+    if (rounds > 64) {   // a unit is small against a line
+        l.longest = l.total / kCtas;
+        return l;
+    }
+    for (long long cta : {0ll, tail - 1, (long long)kCtas - tail, (long long)kCtas - 1}) {
+        long long line = 0;
+        for (int r = 0; r < rounds; ++r) {
+            const long long w = unit_index(kCtas, (int)cta, r);
+            if (w < s.num) line += unit_steps<ROWQ, BN>(s, w);
+        }
+        if (line > l.longest) l.longest = line;
+    }
+    return l;
+}
+
+// Cuts the line of all steps into even shares.
+template <bool ROWQ, int BN>
+inline void cut_evenly(const Shape &s, const Load &l, Cuts &c, Join &j)
+{
+    // a part of two steps is the least that is worth its sums
+    const int G = (int)(l.total / 2 < kCtas ? (l.total / 2 > 0 ? l.total / 2 : 1) : kCtas);
+    c.ctas = G;
+    c.empty = (int)l.units;
+    int k = 0;
+    long long before = 0;
+    for_runs<ROWQ, BN>(s, [&](long long first, long long n, long long steps) {
+        for (; k <= G; ++k) {
+            const long long at = l.total * k / G - before;
+            if (at >= n * steps) break;
+            c.unit[k] = (int)(first + at / steps);
+            c.step[k] = (int)(at % steps);
+        }
+        before += n * steps;
+    });
+    c.unit[G] = c.empty;
+    c.step[G] = 0;
+    int slots = 0;
+    for (int i = 0; i < G; ++i) {
+        c.slot[i] = slots;
+        const int a = c.unit[i], b = c.unit[i + 1], e = c.step[i + 1];
+        if (c.step[i] > 0 || a == b) {   // a part of its first unit
+            if (c.step[i] == 0) {
+                j.unit[j.num] = a;
+                j.slot[j.num++] = slots;
+            }
+            ++slots;
+        }
+        if (b > a && e > 0) {            // and the beginning of its last
+            j.unit[j.num] = b;
+            j.slot[j.num++] = slots;
+            ++slots;
+        }
+    }
+    c.slot[G] = slots;
+    j.slot[j.num] = slots;
+}
+
+// Whether the keys' pass, and the queries', is cut evenly rather than dealt out in whole units.  The queries' kernel fills the SMs that
+// the keys' leaves idle, so a call takes about as long as the longest line of the keys' pass, or as all steps shared
+// evenly and what the queries' lines differ by at the end.  Parts cost their bytes, written and read, and 6 us, 14 in the keys' pass,
+// of more starts, last stores and the joining kernel.  And lines that are cut do not run in step, so that what they stream
+// has to stay in L2: 4096 tokens of 2 x 32 heads at D = 128 (134 MB of q and do) take 378 us whole and 510 cut.
+// Measured, whole / cut: 8 heads over one KV head, 2048 tokens 190 / 50 us, 8192 tokens 724 / 304; 300 queries of 2 heads over 9000
+// keys 73 / 30; 6 heads of 2000 at D = 256 70 / 120 (not cut).
+inline void plan_cuts(const Shape &q, const Shape &kv, int D, bool want_q, bool want_kv, Cuts &cq, Join &jq, Cuts &ck, Join &jk)
+{
+    cq.ctas = cq.empty = ck.ctas = ck.empty = 0;
+    jq.num = jk.num = 0;
+    jq.slot[0] = jk.slot[0] = 0;
+    const Load lq = D == 256 ? load_of<true, step_rows(256)>(q) : load_of<true, step_rows(64)>(q);
+    const Load lk = D == 256 ? load_of<false, step_rows(256)>(kv) : load_of<false, step_rows(64)>(kv);
+    if (lq.total == 0) return;
+    // microseconds of a step, measured (D = 256: both kernels of the keys' pass)
+    const double tk = D == 64 ? 1.0 : D == 128 ? 1.1 : 1.5, tq = D == 64 ? 0.8 : D == 128 ? 0.85 : 0.95;
+    const double kBytesPerUs = 4e6, kL2 = 48e6;
+    auto parts_us = [&](const Load &l, int results, double start) {
+        const double parts = kCtas + (double)(l.units < kCtas ? l.units : kCtas);
+        return start + parts * kRows * D * 4.0 * results * 2.0 / kBytesPerUs;
+    };
+    const double even_q = want_q ? (double)lq.total / kCtas * tq : 0., even_k = want_kv ? (double)lk.total / kCtas * tk : 0.;
+    const double line_k = want_kv ? (double)lk.longest * tk : 0., over = line_k - even_q - even_k;
+    const bool cut_k = want_kv && 4.0 * D * q.planes * q.rows <= kL2 && over > parts_us(lk, 2, 14.0);
+    const bool cut_q = want_q && 4.0 * D * kv.planes * kv.rows <= kL2 && (double)lq.longest * tq - even_q > parts_us(lq, 1, 6.0) + (cut_k || over < 0. ? 0. : over);
+    if (cut_k) D == 256 ? cut_evenly<false, step_rows(256)>(kv, lk, ck, jk) : cut_evenly<false, step_rows(64)>(kv, lk, ck, jk);
+    if (cut_q) D == 256 ? cut_evenly<true, step_rows(256)>(q, lq, cq, jq) : cut_evenly<true, step_rows(64)>(q, lq, cq, jq);
+}
+
+inline int parts_of(const Cuts &c) { return c.ctas ? c.slot[c.ctas] : 0; }
+
 struct Params {
     Shape s;
+    Cuts cuts;
     const float *nl, *dc;    // [B * Hq][pad] -lse log2 e + shift, and delta 2^-shift; rows at or behind Sq: -inf, 0
     int pad;                 // Sq rounded up to 128
     void *out, *out_v;       // dq, or dk and dv
-    float *part, *part_v;    // [slots][128][D] sums of cut units (parts > 1)
+    float *part, *part_v;    // [slots][128][D] sums of cut units
     float sl2;               // scale log2 e
     float dscale;            // 2^-shift
     float out_scale, out_v_scale;
@@ -150,8 +292,15 @@ struct Maps {
 cudaError_t launch_prep(const void *o, const void *d_o, const float *lse, const float *dlse, float *nl, float *dc, long long planes, int Sq, int pad, int D,
                         bool bf16, float shift, cudaStream_t st);
 cudaError_t launch_bwd(int mode, int D, bool bf16, const Maps &m, const Params &p, cudaStream_t st);
-// out [planes, rows, D] = round(scale * sum of the parts)
-cudaError_t launch_join(const float *part, void *out, const Shape &s, int D, bool bf16, float scale, cudaStream_t st);
+// out [planes, rows, D] = round(scale * sum of the parts), for the units that are cut: dQ, and dK and dV, whose units are the same.
+struct JoinParams {
+    Shape q, kv;
+    Join jq, jk;
+    const float *part_q, *part_k, *part_v;
+    void *dq, *dk, *dv;
+    float scale, scale_v;
+};
+cudaError_t launch_join(const JoinParams &p, int D, bool bf16, cudaStream_t st);
 cudaError_t read_and_clear_bwd_status(uint32_t *word);
 
 } // namespace bwd

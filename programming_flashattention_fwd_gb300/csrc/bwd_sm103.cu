@@ -228,12 +228,12 @@ __global__ void __launch_bounds__((Cfg<MODE, D>::THREADS), 1)
     const int part_of = (warp - 4) >> 2;    // its part of a step's columns and of the results' columns
     auto each_unit_filled = [&](uint32_t word) {
         Unit u;
-        for (int round = 0; unit_at<C::ROWQ, BN>(p.s, gridDim.x, blockIdx.x, round, u); ++round) {
+        for (int round = 0; unit_at<C::ROWQ, BN>(p.s, p.cuts, gridDim.x, blockIdx.x, round, u); ++round) {
             const int row = u.t * kRows + r;
             const bool valid = row < p.s.rows;
-            const size_t at = p.part || p.part_v ? (size_t)u.slot * kRows + r : (size_t)u.z * p.s.rows + row;
-            if (C::HAS_DS) fill_row<D>(p.out, p.part, at, valid, part_of * C::HD, C::HD, word);
-            if (C::HAS_DV) fill_row<D>(p.out_v, p.part_v, at, valid, part_of * C::HD, C::HD, word);
+            const size_t at = u.slot >= 0 ? (size_t)u.slot * kRows + r : (size_t)u.z * p.s.rows + row;
+            if (C::HAS_DS) fill_row<D>(p.out, u.slot >= 0 ? p.part : nullptr, at, valid, part_of * C::HD, C::HD, word);
+            if (C::HAS_DV) fill_row<D>(p.out_v, u.slot >= 0 ? p.part_v : nullptr, at, valid, part_of * C::HD, C::HD, word);
         }
     };
 
@@ -272,8 +272,8 @@ __global__ void __launch_bounds__((Cfg<MODE, D>::THREADS), 1)
     const uint32_t tmem = *tmem_holder;
 
     // Each kernel of a pass may start while the one before it drains.  The first waits for lse and delta (and with them for everything
-    // before the call); those behind it start after that wait, need nothing that it computes, and wait for its end at
-    // their own, so that what follows the last kernel follows them all.
+    // before the call); those behind it start after that wait and need nothing that it computes.  Their last CTA waits for its end,
+    // so that what follows the last kernel follows them all (only the last: a CTA that waits keeps its SM from the others).
     if (p.first) cache::grid_wait();
     cache::grid_done_soon();
 
@@ -302,7 +302,7 @@ __global__ void __launch_bounds__((Cfg<MODE, D>::THREADS), 1)
                 return true;
             };
             Unit u;
-            for (int round = 0; ok && unit_at<C::ROWQ, BN>(p.s, gridDim.x, blockIdx.x, round, u); ++round) {
+            for (int round = 0; ok && unit_at<C::ROWQ, BN>(p.s, p.cuts, gridDim.x, blockIdx.x, round, u); ++round) {
                 for (int i = 0; i < C::RUSES && u.n > 0 && ok; ++i) {   // two panels of the resident tile a slot
                     ok = slot_free();
                     if (!ok) break;
@@ -329,7 +329,7 @@ __global__ void __launch_bounds__((Cfg<MODE, D>::THREADS), 1)
             uint32_t units = 0, g = 0;
             bool ok = true;
             Unit u;
-            for (int round = 0; ok && unit_at<C::ROWQ, BN>(p.s, gridDim.x, blockIdx.x, round, u); ++round) {
+            for (int round = 0; ok && unit_at<C::ROWQ, BN>(p.s, p.cuts, gridDim.x, blockIdx.x, round, u); ++round) {
                 if (u.n == 0) continue;
                 if (C::NRES && units > 0 && !bounded_wait(barFree, (units - 1) & 1, abort_flag, tmo, S_RES, status)) break;
                 if (C::NRES) mbar_arrive_expect_tx(barRes, C::NRES * C::RTILE);
@@ -408,7 +408,7 @@ __global__ void __launch_bounds__((Cfg<MODE, D>::THREADS), 1)
             return true;
         };
         Unit u;
-        for (int round = 0; ok && unit_at<C::ROWQ, BN>(p.s, gridDim.x, blockIdx.x, round, u); ++round) {
+        for (int round = 0; ok && unit_at<C::ROWQ, BN>(p.s, p.cuts, gridDim.x, blockIdx.x, round, u); ++round) {
             if (u.n == 0) continue;
             ok = !C::NRES || wait(barRes, units & 1, S_RES);
             if (!ok) break;
@@ -491,9 +491,9 @@ __global__ void __launch_bounds__((Cfg<MODE, D>::THREADS), 1)
         uint32_t g = 0, units = 0;
         bool ok = true;
         Unit u;
-        for (int round = 0; ok && unit_at<C::ROWQ, BN>(p.s, gridDim.x, blockIdx.x, round, u); ++round) {
+        for (int round = 0; ok && unit_at<C::ROWQ, BN>(p.s, p.cuts, gridDim.x, blockIdx.x, round, u); ++round) {
             const int row = u.t * kRows + r;
-            const bool valid = row < p.s.rows, parts = p.s.parts > 1;
+            const bool valid = row < p.s.rows, parts = u.slot >= 0;
             const size_t at = parts ? (size_t)u.slot * kRows + r : (size_t)u.z * p.s.rows + row;
             float *part = parts ? p.part : nullptr, *part_v = parts ? p.part_v : nullptr;
             if (u.n == 0) {   // nothing is seen: the sums are empty
@@ -620,7 +620,7 @@ __global__ void __launch_bounds__((Cfg<MODE, D>::THREADS), 1)
     } else if (warp >= 4 && *abort_flag) {
         each_unit_filled(~0u);   // this CTA gave up on a wait: NaN in every row that it was given
     }
-    if (!p.first) cache::grid_wait();
+    if (!p.first && blockIdx.x == gridDim.x - 1) cache::grid_wait();
 }
 
 template <int MODE, int D, bool BF16>
@@ -646,7 +646,7 @@ cudaError_t launch_one(const Maps &m, const Params &p, cudaStream_t stream)
     }
     Params q = p;
     if (q.timeout_ns == 0) q.timeout_ns = kDefaultTimeoutNs;
-    const int sms = sm_count[dev].load(std::memory_order_relaxed), grid = q.s.num < sms ? q.s.num : sms;
+    const int sms = sm_count[dev].load(std::memory_order_relaxed), grid = q.cuts.ctas ? q.cuts.ctas : q.s.num < sms ? q.s.num : sms;
     return cache::launch_overlapped(kern, dim3((unsigned)grid), C::THREADS, C::ALLOC, 1, stream, m.r1, m.r2, m.s1, m.s2, q);
 }
 
@@ -711,26 +711,41 @@ cudaError_t prep_one(const void *o, const void *d_o, const float *lse, const flo
 }
 
 // ---------------------------------------------------------------- parts of cut units, added in their order
+// A block has 1024 values of a unit; all parts of a value are read by one thread.
 template <bool BF16>
-__global__ void __launch_bounds__(256) join_kernel(const float4 *part, uint2 *out, int parts, int rows, int tiles, int quads, long long n, float scale)
+__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinParams p, int quads)
 {
     cache::grid_wait();
     cache::grid_done_soon();
-    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;   // four columns of one row of a unit
-    if (i >= n) return;
-    const int in_unit = kRows * quads;
-    const long long unit = i / in_unit;
-    const int e = (int)(i - unit * in_unit), row = (int)(unit % tiles) * kRows + e / quads;
-    if (row >= rows) return;
+    const bool of_q = (int)blockIdx.y >= 2 * p.jk.num, of_v = !of_q && (int)blockIdx.y >= p.jk.num;
+    const Shape &sh = of_q ? p.q : p.kv;
+    const Join &jn = of_q ? p.jq : p.jk;
+    const int i = blockIdx.y - (of_q ? 2 * p.jk.num : of_v ? p.jk.num : 0), w = jn.unit[i];
+    const int e = blockIdx.x * 256 + threadIdx.x;   // four columns of one row of unit w
+    int t, z;
+    if (sh.causal) {
+        const int q = (int)fdiv((uint32_t)w, sh.f_planes);
+        t = of_q ? sh.tiles - 1 - q : q;
+        z = w - q * sh.planes;
+    } else {
+        z = (int)fdiv((uint32_t)w, sh.f_tiles);
+        t = w - z * sh.tiles;
+    }
+    const int row = t * kRows + e / quads;
+    if (row >= sh.rows) return;
+    const float4 *part = reinterpret_cast<const float4 *>(of_q ? p.part_q : of_v ? p.part_v : p.part_k);
+    const float scale = of_v ? p.scale_v : p.scale;
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k = 0; k < parts; ++k) {
-        const float4 x = part[(unit * parts + k) * in_unit + e];
+#pragma unroll 4
+    for (int k = jn.slot[i]; k < jn.slot[i + 1]; ++k) {
+        const float4 x = part[(size_t)k * kRows * quads + e];
         s.x += x.x;
         s.y += x.y;
         s.z += x.z;
         s.w += x.w;
     }
-    out[((unit / tiles) * rows + row) * quads + e % quads] = make_uint2(pack2<BF16>(s.x * scale, s.y * scale), pack2<BF16>(s.z * scale, s.w * scale));
+    uint2 *out = static_cast<uint2 *>(of_q ? p.dq : of_v ? p.dv : p.dk);
+    out[((size_t)z * sh.rows + row) * quads + e % quads] = make_uint2(pack2<BF16>(s.x * scale, s.y * scale), pack2<BF16>(s.z * scale, s.w * scale));
 }
 
 } // namespace
@@ -752,11 +767,11 @@ cudaError_t launch_bwd(int mode, int D, bool bf16, const Maps &m, const Params &
     return cudaErrorInvalidValue;
 }
 
-cudaError_t launch_join(const float *part, void *out, const Shape &s, int D, bool bf16, float scale, cudaStream_t st)
+cudaError_t launch_join(const JoinParams &p, int D, bool bf16, cudaStream_t st)
 {
-    const long long n = (long long)s.planes * s.tiles * kRows * (D / 4);
-    return cache::launch_overlapped(bf16 ? join_kernel<true> : join_kernel<false>, dim3((unsigned)((n + 255) / 256)), 256, 0, 1, st,
-                                    reinterpret_cast<const float4 *>(part), static_cast<uint2 *>(out), s.parts, s.rows, s.tiles, D / 4, n, scale);
+    const int quads = D / 4;
+    return cache::launch_overlapped(bf16 ? join_kernel<true> : join_kernel<false>, dim3((unsigned)(kRows * quads / 256), (unsigned)(2 * p.jk.num + p.jq.num)), 256, 0, 1, st,
+                                    p, quads);
 }
 
 cudaError_t read_and_clear_bwd_status(uint32_t *word)

@@ -24,7 +24,7 @@ def _library() -> ctypes.CDLL:
     global _lib
     if _lib is None:
         lib = load_library()
-        lib.fa_bwd_workspace_bytes.restype, lib.fa_bwd_workspace_bytes.argtypes = _Z, [_I] * 6
+        lib.fa_bwd_workspace_bytes.restype, lib.fa_bwd_workspace_bytes.argtypes = _Z, [_I] * 7
         lib.fa_bwd.restype, lib.fa_bwd.argtypes = _I, [_P] * 10 + [_I] * 7 + [_F, _I, _P, _Z, _P]
         lib.fa_bwd_debug.restype = _I
         lib.fa_bwd_debug.argtypes = [_P] * 10 + [_I] * 7 + [_F, _I, _P, _Z, _P, ctypes.c_uint64, ctypes.c_uint32]
@@ -33,9 +33,9 @@ def _library() -> ctypes.CDLL:
 
 
 @functools.lru_cache(maxsize=256)
-def bwd_workspace_bytes(B: int, Hq: int, Hkv: int, Sq: int, Sk: int, D: int) -> int:
+def bwd_workspace_bytes(B: int, Hq: int, Hkv: int, Sq: int, Sk: int, D: int, causal: int = 0) -> int:
     """Bytes of the workspace of ``attention_bwd``."""
-    return _library().fa_bwd_workspace_bytes(B, Hq, Hkv, Sq, Sk, D)
+    return _library().fa_bwd_workspace_bytes(B, Hq, Hkv, Sq, Sk, D, _b._causal_code(causal))
 
 
 def attention_bwd(q, k, v, o, lse, do, causal=False, scale: Optional[float] = None, dlse=None, dq=None, dk=None, dv=None, workspace=None,
@@ -81,8 +81,9 @@ def attention_bwd(q, k, v, o, lse, do, causal=False, scale: Optional[float] = No
     else:
         args += [None, None]
     lib = _lib or _library()
-    _, at, size = _workspace(bwd_workspace_bytes(B, Hq, Hkv, Sq, Sk, D), workspace, q, kept)
-    _launch(lib.fa_bwd, i, current, (*args, B, Hq, Hkv, Sq, Sk, D, _b._causal_code(causal), D ** -0.5 if scale is None else float(scale), code, at, size))
+    mask = _b._causal_code(causal)
+    _, at, size = _workspace(bwd_workspace_bytes(B, Hq, Hkv, Sq, Sk, D, mask), workspace, q, kept)
+    _launch(lib.fa_bwd, i, current, (*args, B, Hq, Hkv, Sq, Sk, D, mask, D ** -0.5 if scale is None else float(scale), code, at, size))
     return dq, dk, dv
 
 

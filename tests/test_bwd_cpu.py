@@ -62,13 +62,14 @@ def test_nothing_to_do(lib):
 
 
 def test_workspace_bytes(lib):
-    """Two padded vectors; parts where the units would leave SMs idle, never more than 160 of them a result."""
+    """Two padded vectors; parts where whole units would leave SMs idle, at most two of a CTA for a result."""
     f = lib.fa_bwd_workspace_bytes
-    assert f(2, 32, 8, 4096, 4096, 128) == 2 * 2 * 32 * 4096 * 4
-    assert f(1, 32, 8, 100, 100, 96) == 0 and f(0, 4, 2, 100, 100, 64) == 0 and f(1, 3, 2, 100, 100, 64) == 0
+    assert f(1, 38, 38, 512, 512, 128, 0) == 2 * 38 * 512 * 4   # 152 units as long as each other
+    assert f(1, 32, 8, 100, 100, 96, 0) == 0 and f(0, 4, 2, 100, 100, 64, 0) == 0 and f(1, 3, 2, 100, 100, 64, 0) == 0 and f(1, 4, 2, 100, 100, 64, 3) == 0
     for args in ((1, 1, 1, 1, 100000, 64), (1, 32, 1, 4096, 4096, 128), (1, 2, 2, 128, 128, 64), (3, 5, 5, 700, 64, 256)):
         B, Hq, Hkv, Sq, Sk, D = args
-        assert f(*args) - 2 * B * Hq * -(-Sq // 128) * 128 * 4 in range(0, 3 * 160 * 128 * D * 4 + 1), args
+        for causal in (0, 1, 2):
+            assert f(*args, causal) - 2 * B * Hq * -(-Sq // 128) * 128 * 4 in range(0, 3 * 2 * 152 * 128 * D * 4 + 1), args
 
 
 def test_binding_refuses():

@@ -123,6 +123,21 @@ def test_several_rounds(fa, shape, dtype, causal):
     near(run(fa, c), c, dtype)
 
 
+# few units of many steps: their steps are cut, and the parts joined
+@pytest.mark.parametrize("shape,dtype,causal", [
+    ((1, 2, 2, 130, 9000, 64), "bf16", 2), ((1, 8, 1, 1024, 1024, 128), "bf16", 1), ((1, 14, 1, 600, 2000, 128), "fp16", 2), ((1, 2, 1, 100, 3000, 256), "bf16", 0),
+    ((1, 8, 1, 700, 700, 256), "fp16", 1), ((1, 16, 1, 900, 64, 64), "bf16", 0), ((1, 8, 1, 3000, 700, 128), "bf16", 2), ((1, 8, 2, 1500, 4000, 64), "bf16", 1),
+], ids=str)
+def test_cut_units(fa, shape, dtype, causal):
+    c = make(12, *shape, dtype, causal, dlse=True)
+    assert fa.bwd_workspace_bytes(*shape, causal) > 2 * shape[0] * shape[1] * -(-shape[3] // 128) * 128 * 4
+    full = [torch.full_like(c[x], float("nan")) for x in "qkv"]
+    got = run(fa, c, dq=full[0], dk=full[1], dv=full[2])
+    near(got, c, dtype)
+    again = run(fa, c)
+    assert all(torch.equal(x, y) for x, y in zip(got, again))
+
+
 @pytest.mark.parametrize("scale", [0.0, -0.125, 0.9])
 def test_scales(fa, scale):
     """Negative and zero scales, as the forward pass takes them, and large logits."""
