@@ -16,6 +16,7 @@ from . import binding as _b
 from .binding import load_library
 from .cache import _capturing, _current, _DTYPES, _F32, _kept, _launch, _need, _on, _workspace
 
+_DENSE = torch.contiguous_format
 _P, _I, _F, _Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
 _lib = None
 
@@ -47,43 +48,52 @@ def attention_bwd(q, k, v, o, lse, do, causal=False, scale: Optional[float] = No
     returned for them).  workspace: bwd_workspace_bytes(...) bytes that no other call in flight uses; None: one that is kept for the calling
     thread and the stream, or, in a call that is captured into a graph, one of the graph's own.  stream: where the call
     runs, and what it allocates then belongs to; None: the current stream."""
-    if not isinstance(q, torch.Tensor) or q.dim() != 4 or not isinstance(k, torch.Tensor) or k.dim() != 4:
-        raise ValueError("q, k, v must be 4-D [B, H, S, D] tensors")
+    try:
+        shape, keys, dt, i = q.shape, k.shape, q.dtype, q.get_device()
+        B, Hq, Sq, D = shape
+        Bk, Hkv, Sk, Dk = keys
+    except (AttributeError, TypeError, ValueError):
+        raise ValueError("q, k, v must be 4-D [B, H, S, D] tensors") from None
     if stream is not None:
         return _on(stream, q, attention_bwd, q, k, v, o, lse, do, causal, scale, dlse, dq, dk, dv, workspace, None, need_q, need_kv)
-    i, dt = q.get_device(), q.dtype
     code = _DTYPES.get(dt)
     if code is None:
         raise ValueError(f"attention is bf16 or fp16, not {dt}")
     if i < 0:
         raise ValueError("q must be a CUDA tensor")
-    shape, keys = q.shape, k.shape
-    B, Hq, Sq, D = shape
-    Hkv, Sk = keys[1], keys[2]
-    if keys[0] != B or keys[3] != D:
+    if Bk != B or Dk != D:
         raise ValueError("k and v must be [B, Hkv, Sk, D] with q's B and D")
-    if (not need_q and dq is not None) or (not need_kv and (dk is not None or dv is not None)):
-        raise ValueError("a result is given that is not to be computed")
-    rows = shape[:3]
-    args = [_need("q", q, shape, dt, i), _need("k", k, keys, dt, i), _need("v", v, keys, dt, i), _need("o", o, shape, dt, i),
-            _need("lse", lse, rows, _F32, i), _need("do", do, shape, dt, i), None if dlse is None else _need("dlse", dlse, rows, _F32, i)]
-    current = _current(i)
-    kept = _kept(i, current)
+    rows = (B, Hq, Sq)
+    pq = pk = pv = None
     if need_q:
-        dq = torch.empty_like(q) if dq is None else dq
-        args.append(_need("dq", dq, shape, dt, i))
-    else:
-        args.append(None)
+        if dq is None:
+            dq = torch.empty_like(q, memory_format=_DENSE)
+            pq = dq.data_ptr()
+        else:
+            pq = _need("dq", dq, shape, dt, i)
+    elif dq is not None:
+        raise ValueError("dq is given but not to be computed")
     if need_kv:
-        dk = torch.empty_like(k) if dk is None else dk
-        dv = torch.empty_like(v) if dv is None else dv
-        args += [_need("dk", dk, keys, dt, i), _need("dv", dv, keys, dt, i)]
-    else:
-        args += [None, None]
-    lib = _lib or _library()
+        if dk is None:
+            dk = torch.empty_like(k, memory_format=_DENSE)
+            pk = dk.data_ptr()
+        else:
+            pk = _need("dk", dk, keys, dt, i)
+        if dv is None:
+            dv = torch.empty_like(k, memory_format=_DENSE)
+            pv = dv.data_ptr()
+        else:
+            pv = _need("dv", dv, keys, dt, i)
+    elif dk is not None or dv is not None:
+        raise ValueError("dk or dv is given but not to be computed")
     mask = _b._causal_code(causal)
-    _, at, size = _workspace(bwd_workspace_bytes(B, Hq, Hkv, Sq, Sk, D, mask), workspace, q, kept)
-    _launch(lib.fa_bwd, i, current, (*args, B, Hq, Hkv, Sq, Sk, D, mask, D ** -0.5 if scale is None else float(scale), code, at, size))
+    current = _current(i)
+    lib = _lib or _library()
+    _, at, size = _workspace(bwd_workspace_bytes(B, Hq, Hkv, Sq, Sk, D, mask), workspace, q, _kept(i, current))
+    _launch(lib.fa_bwd, i, current,
+            (_need("q", q, shape, dt, i), _need("k", k, keys, dt, i), _need("v", v, keys, dt, i), _need("o", o, shape, dt, i), _need("lse", lse, rows, _F32, i),
+             _need("do", do, shape, dt, i), None if dlse is None else _need("dlse", dlse, rows, _F32, i), pq, pk, pv,
+             B, Hq, Hkv, Sq, Sk, D, mask, D ** -0.5 if scale is None else scale, code, at, size))
     return dq, dk, dv
 
 

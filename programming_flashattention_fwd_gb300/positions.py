@@ -20,7 +20,6 @@ from .cache import _capturing, _current, _DTYPES, _F32, _I32, _launch, _need, _o
 _P, _I, _C = ctypes.c_void_p, ctypes.c_int, ctypes.c_char_p
 _TABLE = struct.Struct("P3if").pack          # fa_rotary_table_t: freq; D, rot, interleaved; amplitude
 _HEADS = struct.Struct("P3qi4x").pack        # fa_heads_t: data; stride_b, stride_h, stride_t; heads
-_NONE = _HEADS(0, 0, 0, 0, 0)
 _lib = None
 
 
@@ -109,6 +108,18 @@ def _table(D, rot, interleaved, frequencies, amplitude, device):
 
 def _view(name: str, t, B: int, H: Optional[int], T: int, D: int, dtype, index: int) -> bytes:
     """fa_heads_t of a [B, H, T, D] tensor with any strides but the last dimension's, which is 1."""
+    try:
+        b, h, n, d = t.shape
+        sb, sh, st, se = t.stride()
+        if b == B and n == T and d == D and se == 1 and (h == H or H is None) and t.dtype is dtype and t.get_device() == index:
+            return _HEADS(t.data_ptr(), sb, sh, st, h)
+    except (AttributeError, TypeError, ValueError):
+        pass
+    return _refuse_view(name, t, B, H, T, D, dtype, index)
+
+
+def _refuse_view(name: str, t, B: int, H: Optional[int], T: int, D: int, dtype, index: int) -> bytes:
+    """What is wrong with a tensor that _view does not take (nothing, where it has no elements)."""
     if not isinstance(t, torch.Tensor) or t.dim() != 4:
         raise ValueError(f"{name} must be a [B, H, T, D] tensor")
     shape = t.shape
@@ -118,25 +129,27 @@ def _view(name: str, t, B: int, H: Optional[int], T: int, D: int, dtype, index: 
         raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
     if t.get_device() != index:
         raise ValueError(f"{name} is on {t.device} but the call is on cuda:{index}: every tensor of one call must be on the same GPU")
-    sb, sh, st, se = t.stride()
-    if se != 1 and t.numel():
+    if t.numel():
         raise ValueError(f"{name}'s last dimension must be contiguous")
-    return _HEADS(t.data_ptr(), sb, sh, st, shape[1])
+    return _HEADS(t.data_ptr(), 0, 0, 0, shape[1])
 
 
 def _first(name: str, t, table: RotaryTable):
-    if not isinstance(table, RotaryTable):
+    """The sizes and the type's code of a call's first tensor, which must fit the table."""
+    if type(table) is not RotaryTable:
         raise TypeError("table must be a RotaryTable")
-    if not isinstance(t, torch.Tensor) or t.dim() != 4:
-        raise ValueError(f"{name} must be a [B, H, T, D] tensor")
-    if t.shape[3] != table.D:
+    try:
+        B, H, T, D = t.shape
+        code = _DTYPES.get(t.dtype)
+    except (AttributeError, TypeError, ValueError):
+        raise ValueError(f"{name} must be a [B, H, T, D] tensor") from None
+    if D != table.D:
         raise ValueError(f"{name} must have the table's head dimension {table.D}")
-    code = _DTYPES.get(t.dtype)
     if code is None:
         raise ValueError(f"{name} must be bf16 or fp16, not {t.dtype}")
     if t.get_device() != table.index:
         raise ValueError(f"{name} is on {t.device} but the table is on cuda:{table.index}: every tensor of one call must be on the same GPU")
-    return code
+    return B, H, T, D, code
 
 
 def rotary(table: RotaryTable, q, k=None, start=None, position=None, inverse: bool = False, q_out=None, k_out=None, stream=None):
@@ -146,20 +159,20 @@ def rotary(table: RotaryTable, q, k=None, start=None, position=None, inverse: bo
     themselves.  inverse: by the opposite angles, which takes the results' gradients to those of q and k.  Returns q's result, or both."""
     if stream is not None:
         return _on(stream, q, rotary, table, q, k, start, position, inverse, q_out, k_out)
-    code = _first("q", q, table)
+    B, H, T, D, code = _first("q", q, table)
     i, dt = table.index, q.dtype
-    B, _, T, D = q.shape
     if start is not None and position is not None:
         raise ValueError("positions are given by start or by position, not by both")
-    x = _view("q", q, B, None, T, D, dt, i)
+    x = _view("q", q, B, H, T, D, dt, i)
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=dt, device=q.device)
-    y = _view("q_out", q_out, B, q.shape[1], T, D, dt, i)
+        q_out = torch.empty((B, H, T, D), dtype=dt, device=q.device)
+    y = _view("q_out", q_out, B, H, T, D, dt, i)
     if k is not None:
         x += _view("k", k, B, None, T, D, dt, i)
+        H = k.shape[1]
         if k_out is None:
-            k_out = torch.empty(k.shape, dtype=dt, device=q.device)
-        y += _view("k_out", k_out, B, k.shape[1], T, D, dt, i)
+            k_out = torch.empty((B, H, T, D), dtype=dt, device=q.device)
+        y += _view("k_out", k_out, B, H, T, D, dt, i)
     elif k_out is not None:
         raise ValueError("k_out needs k")
     lib = _lib or _library()
@@ -180,34 +193,30 @@ def rotary_append(cache: KVCache, table: RotaryTable, q, k, v, start=None, posit
     that are accepted later; seq_len is not changed: add count to it after the last layer."""
     if stream is not None:
         return _on(stream, cache, rotary_append, cache, table, q, k, v, start, position, count, weight, pos, q_out, k_out, v_out)
-    _first("q", q, table)
+    _, H, T, D, _ = _first("q", q, table)
     i, dt, B, Hkv = cache.index, cache.dtype, cache.B, cache.Hkv
     if start is not None and position is not None:
         raise ValueError("positions are given by start or by position, not by both")
-    T, D = q.shape[2], table.D
     if D != cache.D:
         raise ValueError(f"the table is for heads of {D}, the cache's have {cache.D}")
     new, slots = (B, Hkv, T, D), (B, Hkv, cache.capacity)
-    x = _view("q", q, B, None, T, D, dt, i) + _view("k", k, B, Hkv, T, D, dt, i) + _view("v", v, B, Hkv, T, D, dt, i)
+    x = _view("q", q, B, H, T, D, dt, i) + _view("k", k, B, Hkv, T, D, dt, i) + _view("v", v, B, Hkv, T, D, dt, i)
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=dt, device=q.device)
-    y = _view("q_out", q_out, B, q.shape[1], T, D, dt, i)
-    out = [q_out]
-    for name, t in (("k_out", k_out), ("v_out", v_out)):
-        if t is None:
-            t = torch.empty(new, dtype=dt, device=q.device)
-        if t is False:
-            y += _HEADS(0, 0, 0, 0, Hkv)
-            t = None
-        else:
-            y += _view(name, t, B, Hkv, T, D, dt, i)
-        out.append(t)
+        q_out = torch.empty((B, H, T, D), dtype=dt, device=q.device)
+    if k_out is None:
+        k_out = torch.empty(new, dtype=dt, device=q.device)
+    if v_out is None:
+        v_out = torch.empty(new, dtype=dt, device=q.device)
+    none = _HEADS(0, 0, 0, 0, Hkv)
+    y = _view("q_out", q_out, B, H, T, D, dt, i)
+    y += none if k_out is False else _view("k_out", k_out, B, Hkv, T, D, dt, i)
+    y += none if v_out is False else _view("v_out", v_out, B, Hkv, T, D, dt, i)
     lib = _lib or _library()
     _launch(lib.fa_rotary_append, i, _current(i),
             (cache._c, table._c, x, y, T, None if start is None else _need("start", start, (B,), _I32, i),
              None if position is None else _need("position", position, (B, T), _I32, i), None if count is None else _need("count", count, (B,), _I32, i),
              None if weight is None else _need("weight", weight, slots, _F32, i), None if pos is None else _need("pos", pos, slots, _I32, i)))
-    return tuple(out)
+    return q_out, None if k_out is False else k_out, None if v_out is False else v_out
 
 
 def _dense(t):
