@@ -175,8 +175,8 @@ int check_heads(const fa_heads_t *x, const fa_heads_t *y, int n, int B, int T, i
         if (x[i].heads < 0 || y[i].heads != x[i].heads) return FA_ERR_HEADS;
         heads += x[i].heads;
     }
-    // blocks over tokens and over heads
-    if (heads > 65535 || (double)B * T * D / 2 / 256 + 1 > 2147483647.0) return FA_ERR_BAD_DIM;
+    // blocks over heads, and over tokens, which are counted in 32 bits
+    if (heads > 65535 || (double)B * T > 2147483647.0) return FA_ERR_BAD_DIM;
     return FA_OK;
 }
 

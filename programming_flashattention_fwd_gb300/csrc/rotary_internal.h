@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 
 #include "cache_internal.h"
+#include "fa_internal.h"
 
 namespace fa {
 namespace rotary {
@@ -28,6 +29,7 @@ struct Params {
     float amplitude, sign;    // sign -1: the inverse rotation
     int B, T, D, rot, interleaved;
     int heads, per;           // all heads; heads of a thread
+    FastDiv f_T;
     // the cache (fa_rotary_append)
     cache::Pages pages;
     void *k, *v;

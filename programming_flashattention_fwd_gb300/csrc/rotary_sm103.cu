@@ -5,9 +5,9 @@
 // product; its upper 32 bits, as a signed number of half turns, are the argument of sincospif.  (The angle itself in fp32 would be
 // off by 0.004 rad at position 65536.)
 //
-// A thread has 8 pairs of one token (16 elements, two 16-byte chunks) and goes through a run of heads with them, so that sines and
-// cosines are computed once for several heads; four heads' loads are in flight at a time.  Neighbouring threads have
-// neighbouring chunks, then neighbouring tokens.  Bound by memory.
+// A thread has 16 elements of a head (two 16-byte chunks, 8 pairs) of one token and goes through a run of heads with them, so that
+// sines and cosines are computed once for several heads; four heads' loads are in flight at a time, the first of them
+// while the angles are computed.  Neighbouring threads have neighbouring chunks, then neighbouring tokens.  Bound by memory.
 #include <atomic>
 #include <cstdint>
 
@@ -16,6 +16,7 @@
 #include "cache_device.cuh"
 #include "ptx.cuh"
 #include "rotary_internal.h"
+#include "schedule.h"
 
 namespace fa {
 namespace rotary {
@@ -65,134 +66,200 @@ __device__ __forceinline__ void turn_words(uint4 &lo, uint4 &hi, bool interleave
     }
 }
 
-// PAIRS pairs of a thread: 8, or 1 where rot is not a multiple of 16 (4-byte or 2-byte accesses).
-template <bool BF16, int PAIRS, bool APPEND>
+// cos and sin of `position` times a frequency, times the amplitude (and the direction).
+__device__ __forceinline__ float2 angle(const Params &p, int position, int pair)
+{
+    const uint64_t phase = (uint64_t)(long long)position * p.freq[pair];
+    float s, c;
+    sincospif((float)(int)(phase >> 32) * 0x1p-31f, &s, &c);
+    return make_float2(c * p.amplitude, s * p.amplitude * p.sign);
+}
+
+// What a thread knows of its token (b, t).
+struct Token {
+    bool here;            // there is such a token, and it counts
+    int b, t, position;
+    long long slot, row;  // of the cache: the slot, and its row of KV head 0 (-1: none)
+};
+
+template <bool APPEND>
+__device__ __forceinline__ Token token_at(const Params &p, long long bt)
+{
+    Token k = {bt < (long long)p.B * p.T, 0, 0, 0, 0, -1};
+    if (!k.here) return k;
+    k.b = (int)fdiv((uint32_t)bt, p.f_T);   // B T < 2^31
+    k.t = (int)bt - k.b * p.T;
+    int start = 0;
+    if constexpr (APPEND) {
+        k.here = !p.count || k.t < p.count[k.b];
+        if (!k.here) return k;
+        const int n = max(p.seq_len[k.b], 0);
+        k.slot = (long long)n + k.t;
+        start = n;
+        if (k.slot < p.capacity) {
+            int pid, r;
+            cache::page_of(p.pages, k.b, (int)k.slot, pid, r);
+            if (pid >= 0 && pid < p.pages.num_pages) k.row = (long long)pid * p.Hkv * p.pages.page + r;
+        }
+    }
+    k.position = p.position ? p.position[bt] : (p.start ? p.start[k.b] : start) + k.t;
+    return k;
+}
+
+// Where head h of all segments is read and written.
+template <typename T>
+__device__ __forceinline__ const Segment &segment_of(const Params &p, const Token &k, int h, const T *&x, T *&y, int &head)
+{
+    const int n = h < p.seg[0].end ? 0 : h < p.seg[1].end ? 1 : 2;
+    const Segment &g = p.seg[n];
+    head = h - (n ? p.seg[n - 1].end : 0);
+    x = static_cast<const T *>(g.x) + k.b * g.xb + head * g.xh + k.t * g.xt;
+    y = g.y ? static_cast<T *>(g.y) + k.b * g.yb + head * g.yh + k.t * g.yt : nullptr;
+    return g;
+}
+
+// Weight and position of the token's slot of KV heads [from, to).
+__device__ __forceinline__ void note(const Params &p, const Token &k, int from, int to)
+{
+    if (k.slot >= p.capacity) return;
+    for (int h = from; h < to; ++h) {
+        const size_t i = ((size_t)k.b * p.Hkv + h) * p.capacity + (size_t)k.slot;
+        if (p.weight) p.weight[i] = 0.f;
+        if (p.pos) p.pos[i] = k.position;
+    }
+}
+
+// rot a multiple of 16: 8 pairs a thread.
+template <bool BF16, bool APPEND>
 __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ Params p)
 {
     cache::grid_wait();
     cache::grid_done_soon();
-    const int U = p.D / (2 * PAIRS);
-    const long long at = (long long)blockIdx.x * kThreads + threadIdx.x, bt = at / U;
-    if (bt >= (long long)p.B * p.T) return;
-    const int u = (int)(at - bt * U), b = (int)(bt / p.T), t = (int)(bt - (long long)b * p.T);
-    int start = 0;
-    long long row = -1;   // of the cache, of KV head 0
-    long long slot = 0;
-    if constexpr (APPEND) {
-        if (p.count && t >= p.count[b]) return;
-        slot = (long long)max(p.seq_len[b], 0) + t;
-        if (!p.start) start = max(p.seq_len[b], 0);
-        if (slot < p.capacity) {
-            int pid, r;
-            cache::page_of(p.pages, b, (int)slot, pid, r);
-            if (pid >= 0 && pid < p.pages.num_pages) row = (long long)pid * p.Hkv * p.pages.page + r;
-        }
-    }
-    const int position = p.position ? p.position[bt] : (p.start ? p.start[b] : start) + t;
-    // the thread's elements: e0 .. and e1 ..
-    const bool mine = u * PAIRS < p.rot / 2;   // rotated ones
-    int e0, e1;
-    if (!mine || p.interleaved) {
-        e0 = u * 2 * PAIRS;
-        e1 = e0 + PAIRS;
-    } else {
-        e0 = u * PAIRS;
-        e1 = e0 + p.rot / 2;
-    }
-    float c[PAIRS], s[PAIRS];
-    if (mine) {
-#pragma unroll
-        for (int i = 0; i < PAIRS; ++i) {
-            const uint64_t phase = (uint64_t)(long long)position * p.freq[u * PAIRS + i];
-            sincospif((float)(int)(phase >> 32) * 0x1p-31f, &s[i], &c[i]);
-            c[i] *= p.amplitude;
-            s[i] *= p.amplitude * p.sign;
-        }
-    }
-    const int h0 = blockIdx.y * p.per, h1 = min(h0 + p.per, p.heads);
-    if (APPEND && u == 0 && slot < p.capacity) {   // bookkeeping of the keys' heads
-        const int k0 = p.heads - 2 * p.Hkv;
-        for (int h = max(h0, k0); h < min(h1, k0 + p.Hkv); ++h) {
-            const size_t i = ((size_t)b * p.Hkv + (h - k0)) * p.capacity + (size_t)slot;
-            if (p.weight) p.weight[i] = 0.f;
-            if (p.pos) p.pos[i] = position;
-        }
+    const int shift = p.D == 64 ? 2 : p.D == 128 ? 3 : 4, half = p.rot / 2;   // log2 of the units of a head
+    const int u = threadIdx.x & ((1 << shift) - 1);
+    const Token k = token_at<APPEND>(p, ((long long)blockIdx.x * kThreads + threadIdx.x) >> shift);
+    if (!k.here) return;
+    // The thread's elements: e0 .. e0 + 7 and e1 .. e1 + 7.
+    const bool mine = u * 8 < half;   // rotated ones
+    int e0 = u * 16, e1 = u * 16 + 8;
+    if (mine && !p.interleaved) {
+        e0 = u * 8;
+        e1 = e0 + half;
     }
     constexpr int BATCH = 4;
-    for (int h = h0; h < h1; h += BATCH) {
-        uint4 lo[BATCH], hi[BATCH];
-        uint16_t lo1[BATCH], hi1[BATCH];
+    const int h0 = blockIdx.y * p.per, h1 = min(h0 + p.per, p.heads);
+    uint4 lo[BATCH], hi[BATCH];
+    auto load = [&](int first) {
 #pragma unroll
         for (int i = 0; i < BATCH; ++i) {
-            if (h + i >= h1) break;
-            const int n = h + i < p.seg[0].end ? 0 : h + i < p.seg[1].end ? 1 : 2, head = h + i - (n ? p.seg[n - 1].end : 0);
-            const Segment &g = p.seg[n];
-            const uint16_t *x = static_cast<const uint16_t *>(g.x) + b * g.xb + head * g.xh + t * g.xt;
-            if constexpr (PAIRS == 8) {
-                lo[i] = *reinterpret_cast<const uint4 *>(x + e0);
-                hi[i] = *reinterpret_cast<const uint4 *>(x + e1);
-            } else {
-                lo1[i] = x[e0];
-                hi1[i] = x[e1];
-            }
+            if (first + i >= h1) break;
+            const uint16_t *x;
+            uint16_t *y;
+            int head;
+            segment_of(p, k, first + i, x, y, head);
+            lo[i] = *reinterpret_cast<const uint4 *>(x + e0);
+            hi[i] = *reinterpret_cast<const uint4 *>(x + e1);
         }
+    };
+    load(h0);
+    float c[8], s[8];
+    if (mine) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float2 v = angle(p, k.position, u * 8 + i);
+            c[i] = v.x;
+            s[i] = v.y;
+        }
+    }
+    if (APPEND && u == 0) note(p, k, max(h0 - (p.heads - 2 * p.Hkv), 0), min(h1 - (p.heads - 2 * p.Hkv), p.Hkv));
+    for (int first = h0; first < h1; first += BATCH) {
+        if (first != h0) load(first);
 #pragma unroll
         for (int i = 0; i < BATCH; ++i) {
-            if (h + i >= h1) break;
-            const int n = h + i < p.seg[0].end ? 0 : h + i < p.seg[1].end ? 1 : 2, head = h + i - (n ? p.seg[n - 1].end : 0);
-            const Segment &g = p.seg[n];
-            if (mine && g.turned) {
-                if constexpr (PAIRS == 8) {
-                    turn_words<BF16>(lo[i], hi[i], p.interleaved, c, s);
-                } else {
-                    float2 f = unpack<BF16>((uint32_t)lo1[i] | (uint32_t)hi1[i] << 16);
-                    turn(f.x, f.y, c[0], s[0]);
-                    const uint32_t w = pack2<BF16>(f.x, f.y);
-                    lo1[i] = (uint16_t)w;
-                    hi1[i] = (uint16_t)(w >> 16);
-                }
-            }
-            auto store = [&](uint16_t *y) {
-                if constexpr (PAIRS == 8) {
-                    *reinterpret_cast<uint4 *>(y + e0) = lo[i];
-                    *reinterpret_cast<uint4 *>(y + e1) = hi[i];
-                } else {
-                    y[e0] = lo1[i];
-                    y[e1] = hi1[i];
-                }
+            if (first + i >= h1) break;
+            const uint16_t *x;
+            uint16_t *y;
+            int head;
+            const Segment &g = segment_of(p, k, first + i, x, y, head);
+            if (mine && g.turned) turn_words<BF16>(lo[i], hi[i], p.interleaved, c, s);
+            auto store = [&](uint16_t *to) {
+                *reinterpret_cast<uint4 *>(to + e0) = lo[i];
+                *reinterpret_cast<uint4 *>(to + e1) = hi[i];
             };
-            if (g.y) store(static_cast<uint16_t *>(g.y) + b * g.yb + head * g.yh + t * g.yt);
-            if (APPEND && g.pool && row >= 0)
-                store(static_cast<uint16_t *>(g.pool == 1 ? p.k : p.v) + ((size_t)row + (size_t)head * p.pages.page) * p.D);
+            if (y) store(y);
+            if (APPEND && g.pool && k.row >= 0)
+                store(static_cast<uint16_t *>(g.pool == 1 ? p.k : p.v) + ((size_t)k.row + (size_t)head * p.pages.page) * p.D);
         }
     }
 }
 
-template <bool BF16, int PAIRS, bool APPEND>
+// Any even rot: a pair a thread, element by element.
+template <bool BF16, bool APPEND>
+__global__ void __launch_bounds__(kThreads) rotary_pairs_kernel(const __grid_constant__ Params p)
+{
+    cache::grid_wait();
+    cache::grid_done_soon();
+    const int U = p.D / 2;
+    const long long at = (long long)blockIdx.x * kThreads + threadIdx.x, bt = at / U;
+    const Token k = token_at<APPEND>(p, bt);
+    if (!k.here) return;
+    const int u = (int)(at - bt * U);
+    const bool mine = u < p.rot / 2;
+    int e0 = 2 * u, e1 = 2 * u + 1;
+    if (mine && !p.interleaved) {
+        e0 = u;
+        e1 = u + p.rot / 2;
+    }
+    const float2 cs = mine ? angle(p, k.position, u) : make_float2(1.f, 0.f);
+    const int h0 = blockIdx.y * p.per, h1 = min(h0 + p.per, p.heads);
+    if (APPEND && u == 0) note(p, k, max(h0 - (p.heads - 2 * p.Hkv), 0), min(h1 - (p.heads - 2 * p.Hkv), p.Hkv));
+    for (int h = h0; h < h1; ++h) {
+        const uint16_t *x;
+        uint16_t *y;
+        int head;
+        const Segment &g = segment_of(p, k, h, x, y, head);
+        uint32_t w = (uint32_t)x[e0] | (uint32_t)x[e1] << 16;
+        if (mine && g.turned) {
+            float2 f = unpack<BF16>(w);
+            turn(f.x, f.y, cs.x, cs.y);
+            w = pack2<BF16>(f.x, f.y);
+        }
+        auto store = [&](uint16_t *to) {
+            to[e0] = (uint16_t)w;
+            to[e1] = (uint16_t)(w >> 16);
+        };
+        if (y) store(y);
+        if (APPEND && g.pool && k.row >= 0)
+            store(static_cast<uint16_t *>(g.pool == 1 ? p.k : p.v) + ((size_t)k.row + (size_t)head * p.pages.page) * p.D);
+    }
+}
+
+// A thread goes through `per` heads: one where even so there are few blocks (the smallest call is all latency: 8 tokens of 40 heads
+// 2.3 us, 3.8 with 8 heads a thread), otherwise three at least, which share the angles (512 tokens of 40 heads 4.5 us, 5.5 with one), and
+// more where that still leaves 8 blocks an SM.  16384 tokens of 40 heads at D = 128 54 us (6.2 TB/s; with values and the cache's
+// writes 76 us, 6.1 TB/s); 3 x 1777 tokens of 32 heads at D = 64, into the rows of a projection, 11.5 us (3.8 TB/s: a wave and a
+// half of blocks).  Angles in shared memory, computed once for a block's 8 warps with other heads each: 57, 12.2 us, and 11 instead of
+// 5 us for 8 x 2000 tokens of 4 heads.
+template <bool BF16, bool APPEND>
 cudaError_t launch_one(Params p, cudaStream_t st)
 {
-    const long long threads = (long long)p.B * p.T * (p.D / (2 * PAIRS)), blocks = (threads + kThreads - 1) / kThreads;
-    // A thread goes through `per` heads: one where there are few tokens (the smallest call is all latency), more where
-    // there are threads enough to fill the card.
-    const long long want = (long long)152 * 2048;
-    long long per = threads * p.heads / want;
-    per = per < 1 ? 1 : per > p.heads ? p.heads : per;
+    const bool wide = p.rot % 16 == 0;
+    const long long threads = (long long)p.B * p.T * (wide ? p.D / 16 : p.D / 2), blocks = (threads + kThreads - 1) / kThreads;
+    const long long groups = (8 * 152 + blocks - 1) / blocks;
+    long long per = (p.heads + groups - 1) / groups;
+    if (per < 3 && blocks * p.heads > 2 * 152) per = 3 < p.heads ? 3 : p.heads;
     p.per = (int)per;
-    return cache::launch_overlapped(rotary_kernel<BF16, PAIRS, APPEND>, dim3((unsigned)blocks, (unsigned)((p.heads + per - 1) / per)), kThreads, 0, 1, st, p);
+    p.f_T = make_fastdiv((uint32_t)p.T);
+    const dim3 grid((unsigned)blocks, (unsigned)((p.heads + per - 1) / per));
+    return cache::launch_overlapped(wide ? rotary_kernel<BF16, APPEND> : rotary_pairs_kernel<BF16, APPEND>, grid, kThreads, 0, 1, st, p);
 }
 
 } // namespace
 
 cudaError_t launch_rotary(const Params &p, bool bf16, bool append, cudaStream_t st)
 {
-    // 8 pairs a thread where both of its chunks are whole and aligned
-    const bool wide = p.rot % 16 == 0;
-    if (append) {
-        if (wide) return bf16 ? launch_one<true, 8, true>(p, st) : launch_one<false, 8, true>(p, st);
-        return bf16 ? launch_one<true, 1, true>(p, st) : launch_one<false, 1, true>(p, st);
-    }
-    if (wide) return bf16 ? launch_one<true, 8, false>(p, st) : launch_one<false, 8, false>(p, st);
-    return bf16 ? launch_one<true, 1, false>(p, st) : launch_one<false, 1, false>(p, st);
+    if (append) return bf16 ? launch_one<true, true>(p, st) : launch_one<false, true>(p, st);
+    return bf16 ? launch_one<true, false>(p, st) : launch_one<false, false>(p, st);
 }
 
 } // namespace rotary
