@@ -80,7 +80,7 @@ struct Cfg {
     static constexpr int OFF_RING = NRES * RTILE;
     static constexpr int OFF_VEC = OFF_RING + NSLOT * STILE;
     static constexpr int OFF_BAR = OFF_VEC + NVEC * VEC;
-    static constexpr int NBAR = 2 * NSLOT + 2 + 2 + 2 + 1 + 1 + 1 + 2 + 2;
+    static constexpr int NBAR = 2 * NSLOT + 2 + 2 + 2 + 2 + 1 + 1 + 1 + 2 + 2;
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
     static constexpr int BYTES = OFF_MISC + 16;
     static constexpr int ALLOC = BYTES + 1024 <= 232448 ? BYTES + 1024 : 232448;
@@ -212,13 +212,13 @@ __global__ void __launch_bounds__((Cfg<MODE, D>::THREADS), 1)
     const uint32_t sR1 = sb + C::OFF_R, sR2 = sR1 + (C::RUSES ? 0 : C::RTILE), sRing = sb + C::OFF_RING, sVec = sb + C::OFF_VEC, bar0 = sb + C::OFF_BAR;
     auto bar_full = [&](uint32_t s) { return bar0 + 8u * s; };
     auto bar_empty = [&](uint32_t s) { return bar0 + 8u * (C::NSLOT + s); };
-    const uint32_t barRes = bar0 + 8u * (2 * C::NSLOT);   // resident tiles loaded
-    const uint32_t barFree = barRes + 8;                  // resident tiles no longer read
+    const uint32_t barRes = bar0 + 8u * (2 * C::NSLOT);   // resident tiles loaded (the first, the second)
+    const uint32_t barFree = barRes + 16;                 // and no longer read
     // Step g signals S ready and P written (or S read) on barS / barP + 8 (g & 1), phase (g / 2) & 1: with two score buffers
     // the threads that compute may be a step ahead of the MMA warp's wait.
-    const uint32_t barS = barRes + 16, barP = barRes + 32;
-    const uint32_t barDP = barRes + 48, barDS = barRes + 56, barAcc = barRes + 64;
-    const uint32_t barVec = barRes + 72, barVecFree = barRes + 88;
+    const uint32_t barS = barRes + 32, barP = barRes + 48;
+    const uint32_t barDP = barRes + 64, barDS = barRes + 72, barAcc = barRes + 80;
+    const uint32_t barVec = barRes + 88, barVecFree = barRes + 104;
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(smem + C::OFF_MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 4);
     unsigned int *status = &g_bwd_status;
@@ -248,9 +248,9 @@ __global__ void __launch_bounds__((Cfg<MODE, D>::THREADS), 1)
             mbar_init(bar_full(s), 1);
             mbar_init(bar_empty(s), 1);
         }
-        mbar_init(barRes, 1);
-        mbar_init(barFree, 1);
         for (int i = 0; i < 2; ++i) {
+            mbar_init(barRes + 8 * i, 1);
+            mbar_init(barFree + 8 * i, 1);
             mbar_init(barS + 8 * i, 1);
             mbar_init(barP + 8 * i, C::CW);
             mbar_init(barVec + 8 * i, 1);
@@ -326,19 +326,22 @@ __global__ void __launch_bounds__((Cfg<MODE, D>::THREADS), 1)
     } else if (warp == 2) {
         // ------------------------------------------------------------ resident tiles; lse and delta of streamed queries
         if (lane == 0) {
-            uint32_t units = 0, g = 0;
+            uint32_t loads[2] = {0, 0}, g = 0;   // of the first and of the second resident operand
             bool ok = true;
             Unit u;
             for (int round = 0; ok && unit_at<C::ROWQ, BN>(p.s, p.cuts, gridDim.x, blockIdx.x, round, u); ++round) {
                 if (u.n == 0) continue;
-                if (C::NRES && units > 0 && !bounded_wait(barFree, (units - 1) & 1, abort_flag, tmo, S_RES, status)) break;
-                if (C::NRES) mbar_arrive_expect_tx(barRes, C::NRES * C::RTILE);
+                auto resident = [&](const CUtensorMap *m, uint32_t dst, uint32_t i) {
+                    if (loads[i] > 0 && !bounded_wait(barFree + 8 * i, (loads[i] - 1) & 1, abort_flag, tmo, S_RES, status)) return false;
+                    mbar_arrive_expect_tx(barRes + 8 * i, C::RTILE);
 #pragma unroll
-                for (int pn = 0; pn < C::PANELS; ++pn) {
-                    if (!C::RUSES) tma_load_3d(sR1 + pn * C::RPANEL, &tmR1, pn * 64, u.t * kRows, u.z, barRes);
-                    if (C::HAS_DS) tma_load_3d(sR2 + pn * C::RPANEL, &tmR2, pn * 64, u.t * kRows, u.z, barRes);
-                }
-                ++units;
+                    for (int pn = 0; pn < C::PANELS; ++pn) tma_load_3d(dst + pn * C::RPANEL, m, pn * 64, u.t * kRows, u.z, barRes + 8 * i);
+                    ++loads[i];
+                    return true;
+                };
+                if (!C::RUSES) ok = resident(&tmR1, sR1, 0);
+                if (C::HAS_DS) ok = ok && resident(&tmR2, sR2, 1);
+                if (!ok) break;
                 if constexpr (!C::ROWQ) {
                     int plane = u.plane, tile = u.tile;
                     for (int j = 0; j < u.n && ok; ++j, ++g) {
@@ -356,7 +359,8 @@ __global__ void __launch_bounds__((Cfg<MODE, D>::THREADS), 1)
                     }
                 }
             }
-            if (C::NRES && units > 0) bounded_wait(barRes, (units - 1) & 1, abort_flag, tmo, S_DRAIN, status, false);
+            for (int i = 0; i < 2; ++i)
+                if (loads[i] > 0) bounded_wait(barRes + 8 * i, (loads[i] - 1) & 1, abort_flag, tmo, S_DRAIN, status, false);
             for (uint32_t x = g > 2 ? g - 2 : 0; x < g; ++x) bounded_wait(barVec + 8 * (x & 1), (x >> 1) & 1, abort_flag, tmo, S_DRAIN, status, false);
         }
     } else if (warp == 1) {
@@ -390,12 +394,13 @@ __global__ void __launch_bounds__((Cfg<MODE, D>::THREADS), 1)
         uint32_t g = 0, units = 0, use = 0;   // steps, units and ring slots so far
         bool ok = true;
         // step gs, whose tiles are the ring's loads x and x + 1
-        auto do_s = [&](uint32_t gs, uint32_t x) {
+        auto do_s = [&](uint32_t gs, uint32_t x, bool last) {
             if (!wait_full(x)) return false;
             tc_fence_after();
             issue_scores(tS(gs), C::A1T, tmem + C::COL_A1, sR1, slot(x));
             tc_commit_elect(barS + 8 * (gs & 1));
             if (!C::HAS_DS) free_slot(x);
+            if (last && !C::A1T) tc_commit_elect(barFree);       // the unit's last reader of its first resident tile
             return true;
         };
         auto do_dp = [&](uint32_t x, bool last) {
@@ -404,13 +409,14 @@ __global__ void __launch_bounds__((Cfg<MODE, D>::THREADS), 1)
             issue_scores(tmem + C::COL_DP, C::A2T, tmem + C::COL_A2, sR2, slot(x + 1));
             tc_commit_elect(barDP);
             if (!C::HAS_DV) free_slot(x + 1);
-            if (last && !(C::A1T && C::A2T)) tc_commit_elect(barFree);   // S and dP were the readers of the resident tiles
+            if (last && !C::A2T) tc_commit_elect(barFree + 8);   // and of its second
             return true;
         };
         Unit u;
         for (int round = 0; ok && unit_at<C::ROWQ, BN>(p.s, p.cuts, gridDim.x, blockIdx.x, round, u); ++round) {
             if (u.n == 0) continue;
-            ok = !C::NRES || wait(barRes, units & 1, S_RES);
+            if (!C::RUSES) ok = wait(barRes, units & 1, S_RES);
+            if (C::A2T) ok = ok && wait(barRes + 8, units & 1, S_RES);
             if (!ok) break;
             ++units;
             // Into tensor memory.  The readers of the operands' columns, the scores of the unit before, are done: their last
@@ -435,14 +441,16 @@ __global__ void __launch_bounds__((Cfg<MODE, D>::THREADS), 1)
                         if (C::A1T) copy_elect(tmem + C::COL_A1 + 32 * pn + 8 * k, sdesc_lo(sR1 + pn * C::RPANEL, 16) + 2 * k, HI);
                         if (C::A2T) copy_elect(tmem + C::COL_A2 + 32 * pn + 8 * k, sdesc_lo(sR2 + pn * C::RPANEL, 16) + 2 * k, HI);
                     }
-                if (C::A1T && C::A2T) tc_commit_elect(barFree);
+                if (C::A1T) tc_commit_elect(barFree);
+                if (C::A2T) tc_commit_elect(barFree + 8);
             }
-            ok = do_s(g, use);
+            ok = do_s(g, use, u.n == 1);
+            if (C::HAS_DS && !C::A2T) ok = ok && wait(barRes + 8, (units - 1) & 1, S_RES);
             if (ok && C::HAS_DS) ok = do_dp(use, u.n == 1);
             for (int j = 0; j < u.n && ok; ++j, use += 2) {
                 const uint32_t gs = g + j;
                 const bool more = j + 1 < u.n;
-                if (C::NSB == 2 && more) ok = do_s(gs + 1, use + 2);
+                if (C::NSB == 2 && more) ok = do_s(gs + 1, use + 2, j + 2 == u.n);
                 ok = ok && wait(barP + 8 * (gs & 1), (gs >> 1) & 1, S_P);
                 if (!ok) break;
                 tc_fence_after();
@@ -455,7 +463,7 @@ __global__ void __launch_bounds__((Cfg<MODE, D>::THREADS), 1)
                     issue_sums(tmem + C::COL_ACCV, tS(gs), slot(use + 1), j == 0);
                     free_slot(use + 1);
                 }
-                if (C::NSB == 1 && more) ok = do_s(gs + 1, use + 2);
+                if (C::NSB == 1 && more) ok = do_s(gs + 1, use + 2, j + 2 == u.n);
                 if constexpr (C::HAS_DS) {
                     ok = ok && wait(barDS, gs & 1, S_DS);
                     if (!ok) break;
@@ -472,7 +480,8 @@ __global__ void __launch_bounds__((Cfg<MODE, D>::THREADS), 1)
         if (!ok) tc_commit_elect(barAcc);   // everything issued ends before tensor memory is given back
         bounded_wait(barAcc, (units - 1) & 1, abort_flag, tmo, S_DRAIN, status, false);
         if (ok && units > 0) {   // no arrival is still on its way to this CTA's barriers when it ends
-            if (C::NRES) bounded_wait(barFree, (units - 1) & 1, abort_flag, tmo, S_DRAIN, status, false);
+            if (!C::RUSES) bounded_wait(barFree, (units - 1) & 1, abort_flag, tmo, S_DRAIN, status, false);
+            if (C::HAS_DS) bounded_wait(barFree + 8, (units - 1) & 1, abort_flag, tmo, S_DRAIN, status, false);
             for (uint32_t x = use > C::NSLOT ? use - C::NSLOT : 0; x < use; ++x)
                 bounded_wait(bar_empty(x % C::NSLOT), (x / C::NSLOT) & 1, abort_flag, tmo, S_DRAIN, status, false);
         }

@@ -55,15 +55,15 @@ class Bar:
 
 def simulate(mode, seed, leave_out=None):
     m, rnd = dict(dict(ring=0), **MODES[mode]), random.Random(seed)
-    nres = (0 if m["ring"] else 1) + m["ds"]   # resident operands with a buffer
+    buffers = ([] if m["ring"] else [0]) + ([1] if m["ds"] else [])   # of the resident operands
     units = [rnd.choice((1, 1, 2, 3, 5)) for _ in range(rnd.randint(1, 5))]
     N, nsb = m["slots"], m["nsb"]
     full, empty = [Bar(1) for _ in range(N)], [Bar(1) for _ in range(N)]
-    res, free, acc = Bar(1), Bar(1), Bar(1)
+    res, free, acc = [Bar(1), Bar(1)], [Bar(1), Bar(1)], Bar(1)
     bar_s, bar_p = [Bar(1), Bar(1)], [Bar(WARPS), Bar(WARPS)]
     dp, ds = Bar(1), Bar(WARPS)
     vec, vec_free = [Bar(1), Bar(1)], [Bar(WARPS), Bar(WARPS)]
-    slot, resident, operand, vecs = [None] * N, [None], [None], [None, None]    # what memory holds
+    slot, resident, operand, vecs = [None] * N, [None, None], [None, None], [None, None]    # what memory holds
     landing, pipe = [], []
     scores, grads = [None, None], [None]           # ("s", g), or per warp ("p", g) written over it
     p_by = [set(), set()]
@@ -91,12 +91,13 @@ def simulate(mode, seed, leave_out=None):
     def second():
         g = 0
         for u, n in enumerate(units):
-            if nres:
+            for i in buffers:
                 if u:
-                    yield from wait(free, (u - 1) & 1, "free")
-                res.arrive(1)
-                resident[0] = None
-                landing.append((resident, 0, u, res))
+                    yield from wait(free[i], (u - 1) & 1, f"free{i}")
+                res[i].arrive(1)
+                resident[i] = None
+                landing.append((resident, i, u, res[i]))
+                yield
             for j in range(n if m["vec"] else 0):
                 v = g & 1
                 yield from wait(vec_free[v], ((g >> 1) & 1) ^ 1, "vec_free")
@@ -135,7 +136,7 @@ def simulate(mode, seed, leave_out=None):
         def op_dp(u, gs, x):
             def f():
                 need(slot[(x + 1) % N] == (1, gs), "dP reads another tile")
-                need((operand[0] if m["a2t"] else resident[0]) == u, "dP reads another resident tile")
+                need((operand[1] if m["a2t"] else resident[1]) == u, "dP reads another resident tile")
                 need(grads[0] is None or grads[0][0] == "free", "dP written over values in use")
                 grads[0] = ("dp", gs)
                 ds_by.clear()
@@ -165,12 +166,14 @@ def simulate(mode, seed, leave_out=None):
         commit = lambda bar: pipe.append(bar.arrive)  # noqa: E731
         full_of = lambda use, name: wait(full[use % N], (use // N) & 1, name)  # noqa: E731
 
-        def do_s(u, gs, x):
+        def do_s(u, gs, x, last):
             yield from full_of(x, "full1")
             pipe.append(op_s(u, gs, x))
             commit(bar_s[gs & 1])
             if not m["ds"]:
                 commit(empty[x % N])
+            if last and not m["a1t"]:
+                commit(free[0])
 
         def do_dp(u, gs, x, last):
             yield from full_of(x + 1, "full2")
@@ -178,12 +181,14 @@ def simulate(mode, seed, leave_out=None):
             commit(dp)
             if not m["dv"]:
                 commit(empty[(x + 1) % N])
-            if last and not (m["a1t"] and m["a2t"]):
-                commit(free)
+            if last and not m["a2t"]:
+                commit(free[1])
 
         for u, n in enumerate(units):
-            if nres:
-                yield from wait(res, u & 1, "res")
+            if not m["ring"]:
+                yield from wait(res[0], u & 1, "res0")
+            if m["a2t"]:
+                yield from wait(res[1], u & 1, "res1")
             for i in range(m["ring"]):
                 yield from full_of(use, "full_r")
 
@@ -194,19 +199,23 @@ def simulate(mode, seed, leave_out=None):
                 commit(empty[use % N])
                 use += 1
             if m["a1t"] and not m["ring"]:
-                def copy(u=u):
-                    need(resident[0] == u, "another resident tile is copied")
-                    operand[0] = u
-                pipe.append(copy)
-            if m["a1t"] and m["a2t"]:
-                commit(free)
-            yield from do_s(u, g, use)
+                def copy(i, u=u):
+                    need(resident[i] == u, "another resident tile is copied")
+                    operand[i] = u
+                pipe.append(lambda copy=copy: copy(0))
+                commit(free[0])
+                if m["a2t"]:
+                    pipe.append(lambda copy=copy: copy(1))
+                    commit(free[1])
+            yield from do_s(u, g, use, n == 1)
             if m["ds"]:
+                if not m["a2t"]:
+                    yield from wait(res[1], u & 1, "res1")
                 yield from do_dp(u, g, use, n == 1)
             for j in range(n):
                 gs, more = g + j, j + 1 < n
                 if nsb == 2 and more:
-                    yield from do_s(u, gs + 1, use + 2)
+                    yield from do_s(u, gs + 1, use + 2, j + 2 == n)
                 yield from wait(bar_p[gs & 1], (gs >> 1) & 1, "p")
                 if m["dv"]:
                     if not m["ds"]:
@@ -214,7 +223,7 @@ def simulate(mode, seed, leave_out=None):
                     pipe.append(op_dv(u, gs, use, j == 0))
                     commit(empty[(use + 1) % N])
                 if nsb == 1 and more:
-                    yield from do_s(u, gs + 1, use + 2)
+                    yield from do_s(u, gs + 1, use + 2, j + 2 == n)
                 if m["ds"]:
                     yield from wait(ds, gs & 1, "ds")
                     pipe.append(op_acc(u, gs, use, j == 0))
@@ -268,10 +277,11 @@ def simulate(mode, seed, leave_out=None):
 
     roles = [ring(), second(), mma()] + [compute(w) for w in range(WARPS)]
     machines = [engine(), tensor()]
-    for _ in range(200000):
+    speed = {id(r): rnd.choice((1, 10, 10, 100)) for r in roles + machines}   # some lag behind, some run ahead
+    for _ in range(400000):
         if not roles:
             break
-        r = rnd.choice(roles + machines)
+        r, = rnd.choices(roles + machines, [speed[id(x)] for x in roles + machines])
         try:
             next(r)
         except StopIteration:
@@ -285,13 +295,13 @@ def simulate(mode, seed, leave_out=None):
 
 @pytest.mark.parametrize("mode", MODES)
 def test_protocol(mode):
-    for seed in range(150):
+    for seed in range(60):
         simulate(mode, seed)
 
 
 # what each mode waits for, and what goes wrong without
 @pytest.mark.parametrize("mode,name", [(m, n) for m, c in MODES.items() for n in ("full1", "full2", "empty", "s", "acc") +
-                                       (("full_r",) if c.get("ring") else ()) + (("res", "free") if c["ds"] or not c.get("ring") else ()) +
+                                       (("full_r",) if c.get("ring") else ()) + (("res1", "free1") if c["ds"] else ()) + (() if c.get("ring") else ("res0", "free0")) +
                                        (("p",) if c["dv"] or c["nsb"] == 1 else ()) +   # else implied by the wait for dS
                                        (("dp", "ds") if c["ds"] else ()) + (("vec", "vec_free") if c["vec"] else ())])
 def test_a_wait_left_out_is_found(mode, name):
