@@ -163,3 +163,230 @@ def test_keys_that_nobody_sees(fa):
         assert all(x is y for x, y in zip(got, full))
         near(got, c, "fp16")
         assert (got[1][:, :, 70:] == 0).all() and (got[2][:, :, 70:] == 0).all()
+
+
+def test_no_queries(fa):
+    """Sq = 0: dk and dv are zeros."""
+    z = lambda *s: torch.ones(*s, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    dq, dk, dv = fa.attention_bwd(z(2, 4, 0, 64), z(2, 2, 9, 64), z(2, 2, 9, 64), z(2, 4, 0, 64), torch.ones(2, 4, 0, device="cuda"), z(2, 4, 0, 64),
+                                  dk=z(2, 2, 9, 64), dv=z(2, 2, 9, 64))
+    assert dq.shape == (2, 4, 0, 64) and (dk == 0).all() and (dv == 0).all()
+
+
+def test_parts_of_the_results(fa):
+    """dq alone, dk and dv alone: the same bits as together; nothing else is returned."""
+    for shape in ((1, 4, 2, 200, 333, 64), (1, 8, 1, 1024, 1024, 128)):
+        c = make(13, *shape, "bf16", 1)
+        dq, dk, dv = run(fa, c)
+        a, b = run(fa, c, need_kv=False), run(fa, c, need_q=False)
+        near((a[0], b[1], b[2]), c, "bf16")
+        assert a[1] is None and a[2] is None and b[0] is None
+        assert run(fa, c, need_q=False, need_kv=False) == (None, None, None)
+        if shape[1] == 4:   # not cut, so the order of the sums is the same
+            assert torch.equal(a[0], dq) and torch.equal(b[1], dk) and torch.equal(b[2], dv)
+
+
+def test_alignment(fa):
+    """Tensors on 16 bytes but not on 32."""
+    for D in (64, 128, 256):
+        c = make(14, 1, 2, 1, 150, 170, D, "bf16", 1)
+        want_ = run(fa, c)
+
+        def off(x):
+            flat = torch.zeros(x.numel() + 8, dtype=x.dtype, device="cuda")
+            y = flat[8:].view(x.shape)
+            assert y.data_ptr() % 32 == 16
+            return y.copy_(x)
+        moved = dict(c, **{n: off(c[n]) for n in ("q", "k", "v", "o", "do")})
+        got = run(fa, moved, dq=off(c["q"]), dk=off(c["k"]), dv=off(c["v"]))
+        assert all(torch.equal(x, y) for x, y in zip(got, want_))
+
+
+def test_streams_graphs_and_workspaces(fa):
+    """A call on a stream of its own; calls on two streams at once; two graphs with calls that are cut (parts in a workspace of the graph's own),
+    replayed at once over new inputs."""
+    c = make(15, 1, 8, 1, 1024, 1024, 128, "bf16", 1)
+    d = make(16, 1, 8, 1, 1024, 1024, 128, "bf16", 1)
+    wc, wd = run(fa, c), run(fa, d)
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    got = [(run(fa, c, stream=s1), run(fa, d, stream=s2)) for _ in range(4)]
+    torch.cuda.synchronize()
+    for x, y in got:
+        assert all(torch.equal(a, b) for a, b in zip(x + y, wc + wd))
+    graphs = []
+    for t in (c, d):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = run(fa, t)
+        graphs.append((g, out))
+    for x in ("q", "k", "v", "o", "do", "lse"):   # the other's inputs
+        a = c[x].clone()
+        c[x].copy_(d[x])
+        d[x].copy_(a)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        with torch.cuda.stream(s1):
+            graphs[0][0].replay()
+        with torch.cuda.stream(s2):
+            graphs[1][0].replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(graphs[0][1] + graphs[1][1], wd + wc))
+
+
+def test_given_workspace(fa):
+    c = make(17, 1, 8, 1, 1024, 1024, 128, "bf16", 1)
+    n = fa.bwd_workspace_bytes(1, 8, 1, 1024, 1024, 128, True)
+    ws = torch.full((n + 64,), 255, dtype=torch.uint8, device="cuda")   # NaN, whatever it is read as
+    got = run(fa, c, workspace=ws[:n])
+    assert all(torch.equal(a, b) for a, b in zip(got, run(fa, c))) and (ws[n:] == 255).all()
+    with pytest.raises(fa.FaError):
+        run(fa, c, workspace=ws[:n - 32])
+
+
+def test_more_than_32_bits_of_elements(fa):
+    """65792 head planes of 256 x 128 elements: 2.2e9 in each tensor; the last sequence is as it is alone."""
+    B, H, S, D = 257 * 8, 32, 256, 128
+    g = torch.Generator("cuda").manual_seed(0)
+    t = {x: torch.empty(B, H, S, D, dtype=torch.bfloat16, device="cuda") for x in ("q", "k", "v", "do")}
+    assert t["q"].numel() > 2 ** 31
+    for x in t.values():
+        x[:-1] = 0.25
+        x[-1] = torch.randn(H, S, D, generator=g, device="cuda")
+    o, lse = fa.attention(t["q"], t["k"], t["v"], causal=True)
+    got = fa.attention_bwd(t["q"], t["k"], t["v"], o, lse, t["do"], causal=True)
+    one = {x: y[-1:].clone() for x, y in t.items()}
+    alone = fa.attention_bwd(one["q"], one["k"], one["v"], o[-1:].clone(), lse[-1:].clone(), one["do"], causal=True)
+    assert all(torch.equal(x[-1:], y) for x, y in zip(got, alone))
+    c = dict(one, o=o[-1:].clone(), lse=lse[-1:].clone(), dlse=None, causal=1, scale=D ** -0.5)
+    near(alone, c, "bf16")
+
+
+def test_against_differences(fa):
+    """Along random directions the gradients' products are the loss's differences: L = sum(do o) + sum(dlse lse) in float64.
+
+    Tolerance: the tests' own (sum of its places times |direction|), that of o and lse, which the call takes rounded to the type
+    (in `want`, delta is of the rounded o too: its error u sum |do||o| reaches ds times p), and the differences' own:
+    step h = 1e-4 leaves h^2 / 6 of the third derivative and 1e-16 / h of rounding, together under 1e-6 of the sums here."""
+    shape, dtype = (1, 4, 2, 90, 110, 64), "bf16"
+    c = make(18, *shape, dtype, 2, dlse=True)
+    got = run(fa, c)
+    _, tol = want(c, dtype)
+    B, Hq, Hkv, Sq, Sk, D = shape
+    shut = shut_of(Sq, Sk, 2)
+
+    def loss(q, k, v):
+        kk, vv = k.repeat_interleave(Hq // Hkv, 1), v.repeat_interleave(Hq // Hkv, 1)
+        s = (q @ kk.transpose(2, 3) * c["scale"]).masked_fill(shut, -float("inf"))
+        return (torch.softmax(s, 3) @ vv * c["do"].double()).sum() + (torch.logsumexp(s, 3) * c["dlse"].double()).sum()
+    x = [c[n].double() for n in "qkv"]
+    # what the rounding of o does to ds: p u sum |do||o|, then through k and q
+    kk = x[1].repeat_interleave(Hq // Hkv, 1)
+    s = (x[0] @ kk.transpose(2, 3) * c["scale"]).masked_fill(shut, -float("inf"))
+    e = torch.softmax(s, 3) * (U[dtype] * (c["do"].double().abs() * c["o"].double().abs()).sum(3))[..., None]
+    extra = [c["scale"] * (e @ kk.abs()), (c["scale"] * (e.transpose(2, 3) @ x[0].abs())).reshape(B, Hkv, -1, Sk, D).sum(2), torch.zeros_like(x[2])]
+    g = torch.Generator("cuda").manual_seed(5)
+    for i in range(3):
+        d = torch.randn(x[i].shape, generator=g, device="cuda", dtype=torch.float64)
+        h = 1e-4
+        ends = [loss(*(y + sign * h * d if j == i else y for j, y in enumerate(x))) for sign in (1, -1)]
+        slope = (ends[0] - ends[1]) / (2 * h)
+        far = ((tol[i] + extra[i]) * d.abs()).sum() + 1e-6 * (got[i].double().abs() * d.abs()).sum()
+        assert (slope - (got[i].double() * d).sum()).abs() <= far
+
+
+def test_autograd(fa):
+    """attention_ad's gradients are attention_bwd's, also through lse alone and for some of the inputs; a second order is refused."""
+    g = torch.Generator("cuda").manual_seed(19)
+    n = lambda *s: torch.randn(s, generator=g, device="cuda").to(torch.bfloat16)  # noqa: E731
+    q, k, v, do, dlse = n(2, 4, 70, 64), n(2, 2, 90, 64), n(2, 2, 90, 64), n(2, 4, 70, 64), torch.randn(2, 4, 70, generator=g, device="cuda")
+    o, lse = fa.attention(q, k, v, causal="bottom_right", scale=0.2)
+
+    def leaves(*need):
+        return [x.clone().requires_grad_(y) for x, y in zip((q, k, v), need)]
+    a = leaves(True, True, True)
+    ao, alse = fa.attention_ad(*a, causal="bottom_right", scale=0.2)
+    assert torch.equal(ao, o) and torch.equal(alse, lse)
+    torch.autograd.backward((ao, alse), (do, dlse))
+    want_ = fa.attention_bwd(q, k, v, o, lse, do, causal=2, scale=0.2, dlse=dlse)
+    assert all(torch.equal(x.grad, y) for x, y in zip(a, want_))
+    a = leaves(True, False, False)
+    fa.attention_ad(*a, causal=2, scale=0.2)[1].sum().backward()   # lse alone; its gradient is an expanded one
+    want_ = fa.attention_bwd(q, k, v, o, lse, torch.zeros_like(o), causal=2, scale=0.2, dlse=torch.ones_like(lse), need_kv=False)
+    assert torch.equal(a[0].grad, want_[0]) and a[1].grad is None and a[2].grad is None
+    a = leaves(False, False, True)
+    x, _ = fa.attention_ad(*a, causal=2, scale=0.2)
+    x.transpose(1, 2).backward(do.transpose(1, 2))   # a gradient with other strides
+    want_ = fa.attention_bwd(q, k, v, o, lse, do, causal=2, scale=0.2, need_q=False)
+    assert torch.equal(a[2].grad, want_[2]) and a[0].grad is None and a[1].grad is None
+    a = leaves(True, True, True)
+    x = torch.autograd.grad(fa.attention_ad(*a)[0].float().pow(2).sum(), a, create_graph=True)[0]
+    with pytest.raises(RuntimeError):
+        x.sum().backward()
+
+
+def test_autograd_is_not_captured(fa):
+    """attention_ad and rotary_ad refuse a capture whose gradients would be captured too; without gradients they are captured."""
+    q = torch.zeros(1, 2, 8, 64, dtype=torch.bfloat16, device="cuda")
+    leaf, table = q.clone().requires_grad_(), fa.RotaryTable(64)
+    fa.attention_ad(q, q, q), fa.rotary_ad(table, q)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for bad in (lambda: fa.attention_ad(leaf, q, q), lambda: fa.rotary_ad(table, leaf)):
+            with pytest.raises(RuntimeError, match="captured"):
+                bad()
+        fa.attention_ad(q, q, q), fa.rotary_ad(table, q)
+    g.replay()
+    torch.cuda.synchronize()
+
+
+def test_a_layer_s_gradients(fa):
+    """Projection, rotation, attention and their gradients as a training step runs them, against float64 autograd over the same
+    products.  Tolerance: every tensor between is rounded to the type, and what comes out has passed seven such roundings
+    (rotated q and k, o, P, dS, the gradients of rotated q and k, and the results): in the 2-norm each adds u / sqrt(3) of its
+    own size at most, and the Jacobians between scale these like the values themselves; 16 u in all leaves a factor of 4."""
+    B, T, Hq, Hkv, D = 2, 150, 4, 2, 64
+    g = torch.Generator("cuda").manual_seed(21)
+    x = torch.randn(B, T, (Hq + 2 * Hkv) * D, generator=g, device="cuda").to(torch.bfloat16)
+    do = torch.randn(B, Hq, T, D, generator=g, device="cuda").to(torch.bfloat16)
+    table = fa.RotaryTable(D, rot=32, interleaved=True)
+    split = lambda y: (y.view(B, T, -1, D).transpose(1, 2)[:, :Hq], y.view(B, T, -1, D).transpose(1, 2)[:, Hq:Hq + Hkv],  # noqa: E731
+                       y.view(B, T, -1, D).transpose(1, 2)[:, Hq + Hkv:])
+    leaf = x.clone().requires_grad_()
+    q, k, v = split(leaf)
+    q, k = fa.rotary_ad(table, q, k)
+    fa.attention_ad(q, k, v.contiguous(), causal=True)[0].backward(do)
+    ref = x.double().requires_grad_()
+    q, k, v = split(ref)
+    t = torch.arange(T, device="cuda", dtype=torch.float64)[:, None] * torch.tensor(table.frequencies, device="cuda", dtype=torch.float64)
+
+    def turn(y):
+        a, b = y[..., 0:32:2], y[..., 1:32:2]
+        pair = torch.stack((a * t.cos() - b * t.sin(), a * t.sin() + b * t.cos()), -1).flatten(-2)
+        return torch.cat((pair, y[..., 32:]), -1)
+    q, k = turn(q), turn(k).repeat_interleave(Hq // Hkv, 1)
+    s = (q @ k.transpose(2, 3) * D ** -0.5).masked_fill(shut_of(T, T, 1), -float("inf"))
+    (torch.softmax(s, 3) @ v.repeat_interleave(Hq // Hkv, 1)).backward(do.double())
+    for a, b in zip(split(leaf.grad.double()), split(ref.grad)):
+        assert (a - b).norm() <= 16 * U["bf16"] * b.norm()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_a_wait_that_runs_out(fa, D):
+    """Every CTA leaves out its first load of v or d_o: the call ends, reports it, and leaves NaN in every row; the next is whole."""
+    from programming_flashattention_fwd_gb300 import grad
+    for shape in ((2, 4, 2, 300, 300, D), (1, 8, 1, 1024, 1024, D)):   # whole units, cut ones
+        c = make(22, *shape, "bf16", 1)
+        out = [torch.zeros_like(c[x]) for x in "qkv"]
+        n = fa.bwd_workspace_bytes(*shape, 1)
+        ws = torch.zeros(n, dtype=torch.uint8, device="cuda")
+        B, Hq, Hkv, Sq, Sk, _ = shape
+        st = grad._library().fa_bwd_debug(*(c[x].data_ptr() for x in ("q", "k", "v", "o", "lse", "do")), None, *(x.data_ptr() for x in out), B, Hq, Hkv, Sq, Sk, D, 1,
+                                          c["scale"], 0, ws.data_ptr(), n, torch.cuda.current_stream().cuda_stream, 2_000_000, 1)
+        assert st == 0
+        status, word = fa.fa_device_status()
+        assert status == 12 and word & 1
+        assert all(torch.isnan(x).all() for x in out)
+        assert fa.fa_device_status()[0] == 0
+        near(run(fa, c), c, "bf16")
+        assert fa.fa_device_status()[0] == 0

@@ -267,3 +267,56 @@ def test_binding_refuses(fa):  # noqa: F811
         fa.rotary(table, data(1, "bf16", 1, 2, 4, 68)[..., 4:])
     with pytest.raises(TypeError):
         fa.rotary(None, x)
+
+
+def test_more_than_32_bits_of_elements(fa):  # noqa: F811
+    """2.2e9 elements read and written, and a pool of as many: the last heads, tokens and pages are as they are alone."""
+    B, H, T, D = 4, 33, 131072, 128
+    table = fa.RotaryTable(D)
+    x = torch.full((B, T, H, D), 0.5, dtype=torch.bfloat16, device="cuda").transpose(1, 2)
+    assert x.numel() > 2 ** 31
+    tail = data(40, "bf16", 1, 2, 100, D)
+    x[-1:, -2:, -100:] = tail
+    y = fa.rotary(table, x, start=ints([0, 0, 0, 7]))
+    assert torch.equal(y[-1:, -2:, -100:], fa.rotary(table, tail, start=ints([7 + T - 100])))
+    del x, y
+    Hkv, page = 8, 128
+    num = 2 ** 31 // (Hkv * page * D) + 8
+    k, v = (torch.zeros(num, Hkv, page, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    cache = fa.KVCache(k, v, ints([3]), ints([[num - 1]]))
+    q, kn, vn = (data(41 + i, "bf16", 1, h, 5, D) for i, h in enumerate((8, 8, 8)))
+    _, kr, _ = fa.rotary_append(cache, table, q, kn, vn)
+    assert torch.equal(k[num - 1, :, 3:8], kr[0]) and torch.equal(v[num - 1, :, 3:8], vn[0])
+    assert not k[num - 1, :, 8:].any() and not k[num - 1, :, :3].any() and not k[num - 2].any() and not k[0].any()
+
+
+def test_calls_with_nothing_between(fa):  # noqa: F811
+    """Rotation, append, attention and append again back to back, each reading what the one before writes, over and over in
+    the same buffers, against the same calls with a wait behind each."""
+    B, Hq, Hkv, D, T, page, n = 4, 8, 2, 64, 3, 16, 60
+    table = fa.RotaryTable(D)
+    per = -(-(n + 30 * T) // page)
+
+    def make():
+        return dict(k=data(50, "bf16", B * per, Hkv, page, D), v=data(51, "bf16", B * per, Hkv, page, D), len=ints([n, 5, 33, 48]),
+                    q=torch.zeros(B, Hq, T, D, dtype=torch.bfloat16, device="cuda"), kn=torch.zeros(B, Hkv, T, D, dtype=torch.bfloat16, device="cuda"),
+                    vn=torch.zeros(B, Hkv, T, D, dtype=torch.bfloat16, device="cuda"), o=torch.zeros(B, Hq, T, D, dtype=torch.bfloat16, device="cuda"),
+                    rows=torch.zeros(B, T, (Hq + 2 * Hkv) * D, dtype=torch.bfloat16, device="cuda"))
+    rows = data(52, "bf16", 20, B, T, (Hq + 2 * Hkv) * D)
+
+    def step(c, i, wait):
+        cache = fa.KVCache(c["k"], c["v"], c["len"])
+        c["rows"].copy_(rows[i])
+        h = c["rows"].view(B, T, -1, D).transpose(1, 2)
+        fa.rotary_append(cache, table, h[:, :Hq], h[:, Hq:Hq + Hkv], h[:, Hq + Hkv:], q_out=c["q"], k_out=c["kn"], v_out=c["vn"])
+        wait()
+        fa.tree_attention(c["q"], c["kn"], c["vn"], cache, o=c["o"])
+        wait()
+        c["len"] += T
+        fa.rotary(table, c["o"], start=c["len"], q_out=c["q"])
+        wait()
+        return c["q"].clone()
+    a, b = make(), make()
+    got = [step(a, i, lambda: None) for i in range(20)]
+    want = [step(b, i, torch.cuda.synchronize) for i in range(20)]
+    assert all(torch.equal(x, y) for x, y in zip(got, want)) and torch.equal(a["k"], b["k"]) and torch.equal(a["v"], b["v"])
