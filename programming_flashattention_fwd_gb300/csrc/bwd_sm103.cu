@@ -24,6 +24,7 @@
 // dP(i); dK(i), dP(i + 1) while P(i + 1) is.  Tensor memory has room for one S and one dP at D = 128 (256 columns) beside the two sums.
 #include <atomic>
 #include <cstdint>
+#include <type_traits>
 
 #include <cuda_fp16.h>
 
@@ -533,44 +534,48 @@ __global__ void __launch_bounds__((Cfg<MODE, D>::THREADS), 1)
                 for (int c = 0; c < HB; c += W) fence_columns<W>(sv + c);
                 if (!C::HAS_DV) publish(barP + 8 * (gs & 1));   // the scores may be overwritten
                 float *s = reinterpret_cast<float *>(sv);
-#pragma unroll
-                for (int c = 0; c < HB; c += 4) {
-                    uint64_t n0 = nl_row, n1 = nl_row;
-                    if constexpr (!C::ROWQ) ld_shared_2x64(vec + 4 * c, n0, n1);
-                    float t0, t1, t2, t3;
-                    f2_unpack(f2_fma(f2_pack(s[c], s[c + 1]), sl2, n0), t0, t1);
-                    f2_unpack(f2_fma(f2_pack(s[c + 2], s[c + 3]), sl2, n1), t2, t3);
-                    s[c] = ex2_approx(t0);
-                    s[c + 1] = ex2_approx(t1);
-                    s[c + 2] = ex2_approx(t2);
-                    s[c + 3] = ex2_approx(t3);
-                }
-                // Masked pairs; streamed queries behind the last have lse = inf, that is p = 0, already.
+                // Pairs outside [from, last] are masked; streamed queries behind the last have lse = inf, that is p = 0, already.
                 const int base = tile * BN;
+                int from = 0, last = HB - 1;
+                bool masked = false;
                 if constexpr (C::ROWQ) {
-                    if (base + BN > p.s.cols || (p.s.causal && base + BN - 1 > u.t * kRows + p.s.coff)) {
-                        long long lim = p.s.cols - 1;
-                        if (p.s.causal) lim = min(lim, (long long)row + p.s.coff);
-                        const int last = (int)max(lim - base - part_of * HB, -1ll);
-#pragma unroll
-                        for (int c = 0; c < HB; ++c)
-                            if (c > last) s[c] = 0.f;
-                    }
-                } else if (p.s.causal && (long long)u.t * kRows + kRows - 1 - p.s.coff > base) {
-                    const long long lim = (long long)row - p.s.coff - base - part_of * HB;
-                    const int from = (int)min(max(lim, 0ll), (long long)HB);
-#pragma unroll
-                    for (int c = 0; c < HB; ++c)
-                        if (c < from) s[c] = 0.f;
+                    masked = base + BN > p.s.cols || (p.s.causal && base + BN - 1 > u.t * kRows + p.s.coff);
+                    long long lim = p.s.cols - 1;
+                    if (p.s.causal) lim = min(lim, (long long)row + p.s.coff);
+                    if (masked) last = (int)max(min(lim - base - part_of * HB, (long long)HB - 1), -1ll);
+                } else if (p.s.causal) {
+                    masked = (long long)u.t * kRows + kRows - 1 - p.s.coff > base;
+                    if (masked) from = (int)min(max((long long)row - p.s.coff - base - part_of * HB, 0ll), (long long)HB);
                 }
-                if constexpr (C::HAS_DV) {
+                auto probabilities = [&](int c, auto mask) {   // of W columns
 #pragma unroll
-                    for (int c = 0; c < HB; c += W) {
+                    for (int e = c; e < c + W; e += 4) {
+                        uint64_t n0 = nl_row, n1 = nl_row;
+                        if constexpr (!C::ROWQ) ld_shared_2x64(vec + 4 * e, n0, n1);
+                        float t[4];
+                        f2_unpack(f2_fma(f2_pack(s[e], s[e + 1]), sl2, n0), t[0], t[1]);
+                        f2_unpack(f2_fma(f2_pack(s[e + 2], s[e + 3]), sl2, n1), t[2], t[3]);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            s[e + i] = ex2_approx(t[i]);
+                            if (decltype(mask)::value && (e + i < from || e + i > last)) s[e + i] = 0.f;
+                        }
+                    }
+                    if constexpr (C::HAS_DV) {
                         uint32_t pk[W / 2];
 #pragma unroll
                         for (int e = 0; e < W / 2; ++e) pk[e] = pack2<BF16>(s[c + 2 * e], s[c + 2 * e + 1]);
                         store_columns<W / 2>(tSb + c / 2, pk);
                     }
+                };
+                if (masked) {
+#pragma unroll
+                    for (int c = 0; c < HB; c += W) probabilities(c, std::true_type{});
+                } else {
+#pragma unroll
+                    for (int c = 0; c < HB; c += W) probabilities(c, std::false_type{});
+                }
+                if constexpr (C::HAS_DV) {
                     tmem_wait_st();
                     publish(barP + 8 * (gs & 1));
                 }
@@ -589,9 +594,10 @@ __global__ void __launch_bounds__((Cfg<MODE, D>::THREADS), 1)
 #pragma unroll
                         for (int e = 0; e < W; e += 4) {
                             uint64_t d0 = dc_row, d1 = dc_row;
-                            if constexpr (!C::ROWQ) ld_shared_2x64(vec + BN * 4 + 4 * (c + e), d0, d1);   
-                            const uint64_t x0 = f2_fma(f2_pack(__uint_as_float(dv[e]), __uint_as_float(dv[e + 1])), cc, d0);
-                            const uint64_t x1 = f2_fma(f2_pack(__uint_as_float(dv[e + 2]), __uint_as_float(dv[e + 3])), cc, d1);
+                            if constexpr (!C::ROWQ) ld_shared_2x64(vec + BN * 4 + 4 * (c + e), d0, d1);
+                            const uint32_t *y = dv + e;
+                            const uint64_t x0 = f2_fma(f2_pack(__uint_as_float(y[0]), __uint_as_float(y[1])), cc, d0);
+                            const uint64_t x1 = f2_fma(f2_pack(__uint_as_float(y[2]), __uint_as_float(y[3])), cc, d1);
                             float a, b;
                             f2_unpack(f2_mul(x0, f2_pack(s[c + e], s[c + e + 1])), a, b);
                             ds[(c + e) / 2] = pack2<BF16>(a, b);
@@ -600,7 +606,7 @@ __global__ void __launch_bounds__((Cfg<MODE, D>::THREADS), 1)
                         }
                     }
 #pragma unroll
-                    for (int c = 0; c < HB; c += W) store_columns<W / 2>(tDP + c / 2, ds + c / 2);
+                    for (int c = 0; c < HB; c += W) store_columns<W / 2>(tDP + c / 2, ds + c / 2);   // (each chunk's at once: 5 % slower)
                     tmem_wait_st();
                     publish(barDS);
                 }
