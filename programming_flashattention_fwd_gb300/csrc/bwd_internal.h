@@ -20,6 +20,7 @@ enum Mode { kQ = 0, kKV = 1, kK = 2, kV = 3 };
 constexpr int kRows = 128;                                         // resident rows
 constexpr int step_rows(int D) { return D == 256 ? 64 : 128; }     // streamed rows of a step
 constexpr int kCtas = 152;   // the SMs of a GB300: CTAs of a kernel whose steps are cut evenly
+constexpr int kUnitCost = 2; // what a unit's beginning and end take, in steps (3.4 us of dK and dV at D = 128, where a step takes 1.3)
 
 // One kernel's line of work: units of (head plane, tile of 128 resident rows), whose steps are tiles of step_rows
 // streamed rows.
@@ -164,8 +165,8 @@ inline long long unit_steps(const Shape &s, long long w)
     return (long long)(end - first) * (ROWQ ? 1 : s.group);
 }
 
-// What a kernel has to do, in steps: all of it, and the longest line where whole units are dealt out (it begins with the
-// heaviest unit, or is among those of the last round).
+// What a kernel has to do, in steps and kUnitCost a unit: all of it, and the longest line where whole units are dealt out (it
+// begins with the heaviest unit, or is among those of the last round).
 struct Load {
     long long total, units, longest;   // units: those that have steps
 };
@@ -175,8 +176,9 @@ inline Load load_of(const Shape &s)
 {
     Load l = {0, 0, 0};
     for_runs<ROWQ, BN>(s, [&](long long, long long n, long long steps) {
-        l.total += n * steps;
-        if (steps > 0) l.units += n;
+        if (steps == 0) return;
+        l.total += n * (steps + kUnitCost);
+        l.units += n;
     });
     const long long rounds = (s.num + kCtas - 1) / kCtas, tail = s.num - (rounds - 1) * kCtas;
     if (rounds > 64) {   // a unit is small against a line
@@ -187,7 +189,8 @@ inline Load load_of(const Shape &s)
         long long line = 0;
         for (int r = 0; r < rounds; ++r) {
             const long long w = unit_index(kCtas, (int)cta, r);
-            if (w < s.num) line += unit_steps<ROWQ, BN>(s, w);
+            const long long steps = w < s.num ? unit_steps<ROWQ, BN>(s, w) : 0;
+            if (steps > 0) line += steps + kUnitCost;
         }
         if (line > l.longest) l.longest = line;
     }
@@ -198,20 +201,23 @@ inline Load load_of(const Shape &s)
 template <bool ROWQ, int BN>
 inline void cut_evenly(const Shape &s, const Load &l, Cuts &c, Join &j)
 {
-    // a part of two steps is the least that is worth its sums
-    const int G = (int)(l.total / 2 < kCtas ? (l.total / 2 > 0 ? l.total / 2 : 1) : kCtas);
+    // a part of about two steps is the least that is worth its sums
+    const int G = (int)(l.total / 4 < kCtas ? (l.total / 4 > 0 ? l.total / 4 : 1) : kCtas);
     c.ctas = G;
     c.empty = (int)l.units;
     int k = 0;
     long long before = 0;
     for_runs<ROWQ, BN>(s, [&](long long first, long long n, long long steps) {
+        if (steps == 0) return;
+        const long long each = steps + kUnitCost;
         for (; k <= G; ++k) {
             const long long at = l.total * k / G - before;
-            if (at >= n * steps) break;
-            c.unit[k] = (int)(first + at / steps);
-            c.step[k] = (int)(at % steps);
+            if (at >= n * each) break;
+            const long long step = at % each - kUnitCost;   // a cut in a unit's beginning is made before it
+            c.unit[k] = (int)(first + at / each);
+            c.step[k] = step > 0 ? (int)step : 0;
         }
-        before += n * steps;
+        before += n * each;
     });
     c.unit[G] = c.empty;
     c.step[G] = 0;
@@ -219,7 +225,7 @@ inline void cut_evenly(const Shape &s, const Load &l, Cuts &c, Join &j)
     for (int i = 0; i < G; ++i) {
         c.slot[i] = slots;
         const int a = c.unit[i], b = c.unit[i + 1], e = c.step[i + 1];
-        if (c.step[i] > 0 || a == b) {   // a part of its first unit
+        if (c.step[i] > 0 || (a == b && e > 0)) {   // a part of its first unit
             if (c.step[i] == 0) {
                 j.unit[j.num] = a;
                 j.slot[j.num++] = slots;
@@ -241,8 +247,8 @@ inline void cut_evenly(const Shape &s, const Load &l, Cuts &c, Join &j)
 // evenly and what the queries' lines differ by at the end.  Parts cost their bytes, written and read, and 6 us, 14 in the keys' pass,
 // of more starts, last stores and the joining kernel.  And lines that are cut do not run in step, so that what they stream
 // has to stay in L2: 4096 tokens of 2 x 32 heads at D = 128 (134 MB of q and do) take 378 us whole and 510 cut.
-// Measured, whole / cut: 8 heads over one KV head, 2048 tokens 190 / 50 us, 8192 tokens 724 / 304; 300 queries of 2 heads over 9000
-// keys 73 / 30; 6 heads of 2000 at D = 256 70 / 120 (not cut).
+// Measured, whole / cut: 8 heads over one KV head, 2048 tokens 190 / 49 us, 8192 tokens 724 / 288; 300 queries of 2 heads over 9000
+// keys 73 / 27; 6 heads of 2000 at D = 256 70 / 120 (not cut).
 inline void plan_cuts(const Shape &q, const Shape &kv, int D, bool want_q, bool want_kv, Cuts &cq, Join &jq, Cuts &ck, Join &jk)
 {
     cq.ctas = cq.empty = ck.ctas = ck.empty = 0;

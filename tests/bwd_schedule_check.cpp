@@ -54,12 +54,12 @@ static void walk(int B, int Hq, int Hkv, int Sq, int Sk, int D, int causal, int 
             auto &of = tiles[{u.z, u.t}];
             CHECK(of.find(u.slot) == of.end() && (of.empty() || u.slot >= 0));
             of[u.slot] = at;
-            load[c] += u.n;
+            load[c] += u.n > 0 ? u.n + kUnitCost : 0;
             CHECK(u.slot < 0 || u.n > 0);
         }
     }
     if (cut)
-        for (int x : load) CHECK(x <= load[0] + 1 && x + 1 >= load[0]);
+        for (int x : load) CHECK(x <= load[0] + 2 * kUnitCost + 1);   // shares alike but for what a cut inside a unit repeats
     for (int x : seen_slots) CHECK(x == 1);
     for (int i = 0; i < join.num; ++i) {   // each cut unit's parts, and no others
         const int w = join.unit[i], q = s.causal ? w / s.planes : 0;
