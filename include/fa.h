@@ -55,12 +55,14 @@ typedef enum {
     FA_OK = 0,
     FA_ERR_NULL_PTR = 1,        /* q, k, v, o or lse (a tensor that the call needs) is NULL for a non-empty problem */
     FA_ERR_BAD_DIM = 2,         /* B, Sq, Sk < 0, or Sk == 0 while B*Hq*Sq > 0, or too large; (cache operators) a page
-                                   that is no multiple of 16, slots without pages, T, keep, first or last out of range */
-    FA_ERR_HEADS = 3,           /* Hq < 1, Hkv < 1, or Hq % Hkv != 0                         */
+                                   that is no multiple of 16, slots without pages, T, keep, first or last out of range;
+                                   (rotary positions) rot odd or out of [0, D], a negative stride */
+    FA_ERR_HEADS = 3,           /* Hq < 1, Hkv < 1, or Hq % Hkv != 0; (rotary positions) views of unlike numbers of heads */
     FA_ERR_UNSUPPORTED_D = 4,   /* D not in {64, 128, 256} (or not supported by the chosen kernel) */
-    FA_ERR_ALIGN = 5,           /* q/k/v/o not 16-byte aligned, or lse (any other tensor) not 4-byte aligned */
+    FA_ERR_ALIGN = 5,           /* q/k/v/o (their gradients, rows of heads) not 16-byte aligned, or lse (any other tensor) not
+                                   4-byte aligned */
     FA_ERR_ALIAS = 6,           /* o or lse (a tensor that is written) overlaps an input or another output */
-    FA_ERR_SCALE = 7,           /* scale is NaN or infinite; (cache operators) or not positive */
+    FA_ERR_SCALE = 7,           /* scale is NaN or infinite; (cache operators) or not positive; (rotary positions) the amplitude */
     FA_ERR_NO_DEVICE = 8,       /* no CUDA device / runtime error querying it                */
     FA_ERR_ARCH = 9,            /* current device is not compute capability 10.3 (sm_103)    */
     FA_ERR_TENSORMAP = 10,      /* cuTensorMapEncodeTiled unavailable or rejected the layout */
@@ -68,9 +70,10 @@ typedef enum {
     FA_ERR_DEVICE_TIMEOUT = 12, /* (fa_device_status) a bounded device-side wait expired     */
     FA_ERR_CAUSAL = 13,         /* causal not in {0, 1, 2}                                   */
     FA_ERR_SHAPE = 14,          /* (fa_gemm) K or N not a multiple of 8 (16-byte rows)       */
-    FA_ERR_ARG = 15,            /* an enum-like argument (dtype, output type, epilogue) is out of range */
+    FA_ERR_ARG = 15,            /* an enum-like argument (dtype, output type, epilogue) is out of range; (rotary positions)
+                                   start and position both given */
     FA_ERR_TOO_LARGE = 16       /* (fa_fwd_host_noalloc) the problem needs more than FA_HOST_NOALLOC_MAX_BYTES of staging;
-                                   (cache operators) the workspace is smaller than the call needs */
+                                   (gradients, cache operators) the workspace is smaller than the call needs */
 } fa_status_t;
 
 /*

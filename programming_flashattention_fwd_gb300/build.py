@@ -33,7 +33,7 @@ def nvcc() -> str:
 
 
 def sources():
-    return [os.path.join(CSRC, f) for f in ("fa_fwd_sm103.cu", "fa_fwd1_sm103.cu", "gemm_sm103.cu", "softmax_sm103.cu", "fa_api.cpp",
+    return [os.path.join(CSRC, f) for f in ("fa_fwd_sm103.cu", "fa_fwd1_sm103.cu", "gemm_sm103.cu", "softmax_sm103.cu", "fa_api.cpp", "device_status.cpp",
                                                   "host_pipeline.cpp", "host_noalloc.cu", "cache_api.cpp", "tree_sm103.cu", "weigh_sm103.cu",
                                                   "bwd_api.cpp", "bwd_sm103.cu", "rotary_api.cpp", "rotary_sm103.cu",
                                                   "cache_sm103.cu")]

@@ -10,8 +10,6 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
-#include "bwd_internal.h"
-#include "cache_internal.h"
 #include "fa.h"
 #include "fa_internal.h"
 #include "schedule.h"
@@ -297,12 +295,12 @@ const char *fa_strerror(int status)
     case FA_OK: return "FA_OK: success";
     case FA_ERR_NULL_PTR: return "FA_ERR_NULL_PTR: a tensor pointer is NULL";
     case FA_ERR_BAD_DIM: return "FA_ERR_BAD_DIM: negative size, Sk == 0 for a non-empty problem, or problem too large (a cache: page not a multiple of 16, "
-                                "no pages for its slots, T == 0, keep < 1 or first + last > keep)";
-    case FA_ERR_HEADS: return "FA_ERR_HEADS: Hq and Hkv must be >= 1 with Hq % Hkv == 0";
+                                "no pages for its slots, T == 0, keep < 1 or first + last > keep; rotary positions: rot odd or above D, a negative stride)";
+    case FA_ERR_HEADS: return "FA_ERR_HEADS: Hq and Hkv must be >= 1 with Hq % Hkv == 0 (rotary positions: as many heads written as read, the cache's of keys and values)";
     case FA_ERR_UNSUPPORTED_D: return "FA_ERR_UNSUPPORTED_D: D must be 64, 128 or 256 (and supported by the selected kernel)";
-    case FA_ERR_ALIGN: return "FA_ERR_ALIGN: q/k/v/o and matrices must be 16-byte aligned, lse and other tensors 4-byte aligned, a workspace as documented";
+    case FA_ERR_ALIGN: return "FA_ERR_ALIGN: q/k/v/o, their gradients, matrices and rows of heads must be 16-byte aligned, lse and other tensors 4-byte aligned, a workspace as documented";
     case FA_ERR_ALIAS: return "FA_ERR_ALIAS: a tensor that is written overlaps another one";
-    case FA_ERR_SCALE: return "FA_ERR_SCALE: scale is NaN or infinite (a cache: or not positive)";
+    case FA_ERR_SCALE: return "FA_ERR_SCALE: scale is NaN or infinite (a cache: or not positive; rotary positions: the amplitude)";
     case FA_ERR_NO_DEVICE: return "FA_ERR_NO_DEVICE: no usable CUDA device";
     case FA_ERR_ARCH: return "FA_ERR_ARCH: the current device is not sm_103 (GB300)";
     case FA_ERR_TENSORMAP: return "FA_ERR_TENSORMAP: TMA descriptor encoding failed";
@@ -310,26 +308,10 @@ const char *fa_strerror(int status)
     case FA_ERR_DEVICE_TIMEOUT: return "FA_ERR_DEVICE_TIMEOUT: a bounded device-side wait expired";
     case FA_ERR_CAUSAL: return "FA_ERR_CAUSAL: causal must be 0 (none), 1 (top-left) or 2 (bottom-right)";
     case FA_ERR_SHAPE: return "FA_ERR_SHAPE: matrix rows must be 16-byte multiples (K and N multiples of 8)";
-    case FA_ERR_ARG: return "FA_ERR_ARG: dtype, output type or epilogue selector out of range";
+    case FA_ERR_ARG: return "FA_ERR_ARG: dtype, output type, epilogue or another selector out of range, or positions given twice";
     case FA_ERR_TOO_LARGE: return "FA_ERR_TOO_LARGE: the problem needs more staging than FA_HOST_NOALLOC_MAX_BYTES, or more workspace than it was given";
     default: return "unknown fa status code";
     }
-}
-
-int fa_device_status(fa_stream_t stream, uint32_t *detail)
-{
-    // every kernel's word is read and cleared; of those that are set the first in this order is reported
-    uint32_t word[7] = {};
-    if (fa::read_and_clear_status(reinterpret_cast<cudaStream_t>(stream), &word[0]) != cudaSuccess ||
-        fa::read_and_clear_fa1_status(&word[1]) != cudaSuccess || fa::read_and_clear_gemm_status(&word[2]) != cudaSuccess ||
-        fa::read_and_clear_softmax_status(&word[3]) != cudaSuccess || fa::cache::read_and_clear_tree_status(&word[4]) != cudaSuccess ||
-        fa::cache::read_and_clear_weigh_status(&word[5]) != cudaSuccess || fa::bwd::read_and_clear_bwd_status(&word[6]) != cudaSuccess)
-        return FA_ERR_NO_DEVICE;
-    uint32_t w = word[0];
-    for (uint32_t x : word)
-        if (!(w & 1u)) w = x;
-    if (detail) *detail = w;
-    return (w & 1u) ? FA_ERR_DEVICE_TIMEOUT : FA_OK;
 }
 
 } // extern "C"
