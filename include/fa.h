@@ -163,7 +163,7 @@ int fa_fwd_debug(const void *q, const void *k, const void *v, void *o, float *ls
  *   dq, dk, dv   like q, k, v: written whole.  dq may be NULL (not computed), and so may dk and dv, both
  *   workspace    fa_bwd_workspace_bytes(...) bytes, 32-byte aligned; needs no initial value.  A call uses it until its work
  *                on `stream` is done: calls (and captured graphs) that may run at the same time need workspaces of their own
- * A query that sees nothing (lse = -inf) adds nothing, a key that no query sees has zero gradients; with Sq == 0 dk and dv are
+ * A query that sees nothing (lse = -inf) adds nothing, whatever its dlse; a key that no query sees has zero gradients; with Sq == 0 dk and dv are
  * zeros.  Sums are float32 in a fixed order: the result does not vary from run to run.  p and ds are rounded to
  * the 16-bit type before the sums over them (in fp16, |do_i.v_j - delta_i| above 65504 becomes infinite).  Inputs are expected to
  * be finite: an infinity or NaN in a row reaches what shares a tile with it, also where the mask parts them.

@@ -679,7 +679,7 @@ cudaError_t launch_one(const Maps &m, const Params &p, cudaStream_t stream)
 
 // ---------------------------------------------------------------- lse and delta
 // nl = -lse log2 e + shift and dc = (do.o - dlse) 2^-shift of every row, sums in fp32; rows at or behind Sq, and rows that saw nothing
-// (lse = -inf), get nl = -inf, so that their probabilities are 0 without another mask.  Bound by memory: do and o
+// (lse = -inf), get nl = -inf and dc = 0, so that their probabilities are 0 without another mask.  Bound by memory: do and o
 // are read once, 16 bytes a lane, D / 8 lanes a row.
 constexpr int kPrepThreads = 256;
 
@@ -720,7 +720,7 @@ __global__ void __launch_bounds__(kPrepThreads) prep_kernel(const uint4 *o, cons
         if (q < Sq) {
             const float l = lse[row];
             n = l == -INFINITY ? -INFINITY : fmaf(-l, 1.4426950408889634f, shift);
-            c = -(sum - (dlse ? dlse[row] : 0.f)) * down;
+            if (l != -INFINITY) c = -(sum - (dlse ? dlse[row] : 0.f)) * down;   // nothing seen: dlse, which may be NaN there, has no effect
         }
         nl[i] = n;
         dc[i] = c;

@@ -154,6 +154,19 @@ def test_rows_that_see_nothing(fa):
         assert torch.isinf(c["lse"][:, :, :360]).all() and (dq[:, :, :360] == 0).all()
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_gradient_of_an_empty_row_s_lse(fa, D):
+    """A row that sees nothing has lse = -inf, whose gradient is often NaN or infinite (that of exp(lse - m), say): it has no effect."""
+    c = make(27, 1, 2, 1, 200, 90, D, "bf16", 2, dlse=True)
+    empty = torch.isinf(c["lse"])
+    assert empty.sum() == 2 * 110
+    plain = run(fa, c)
+    near(plain, c, "bf16")
+    for x in (float("nan"), float("inf"), -float("inf")):
+        c["dlse"] = c["dlse"].masked_fill(empty, x)
+        assert all(torch.equal(a, b) for a, b in zip(run(fa, c), plain))
+
+
 def test_keys_that_nobody_sees(fa):
     """Top-left with more keys than queries: dk and dv of the keys behind are zero, whatever was there."""
     for D in (64, 128, 256):
