@@ -27,7 +27,7 @@ bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 struct View {
     const void *data;
     long long n[3], s[3];
-    int D;
+    long long D;
     size_t bytes() const
     {
         long long last = D;
@@ -46,7 +46,8 @@ View view(const fa_heads_t &h, int B, int T, int D)
 int check_view(const View &v)
 {
     for (int i = 0; i < 3; ++i) {
-        if (v.s[i] < 0 || (double)v.s[i] * (double)v.n[i] > 4611686018427387904.0) return FA_ERR_BAD_DIM;
+        if (v.s[i] < 0 || (double)v.s[i] * (double)v.n[i] > 576460752303423488.0)   // 2^59: three of them are added up
+            return FA_ERR_BAD_DIM;
         if (v.s[i] % 8 != 0) return FA_ERR_ALIGN;
     }
     return aligned(v.data, 16) ? FA_OK : FA_ERR_ALIGN;
@@ -81,10 +82,7 @@ bool meet(const View &a, const View &b)
     const long long gap = (long long)(reinterpret_cast<uintptr_t>(y.data) - reinterpret_cast<uintptr_t>(x.data)) / 2;
     if (x.s[0] != y.s[0] || x.s[2] != y.s[2]) return true;
     const long long wx = x.D + (x.n[1] - 1) * x.s[1], wy = y.D + (y.n[1] - 1) * y.s[1];
-    long long row = 0;   // the smallest step from one row to another
-    for (int i : {0, 2})
-        if (x.n[i] > 1 && (row == 0 || x.s[i] < row)) row = x.s[i];
-    if (wx <= gap && (row == 0 || gap + wy <= row)) return false;
+    if (wx <= gap && distinct(View{x.data, {x.n[0], 1, x.n[2]}, {x.s[0], 0, x.s[2]}, gap + wy})) return false;
     const long long sh = x.s[1] ? x.s[1] : y.s[1] ? y.s[1] : x.D;
     if ((x.s[1] && x.s[1] != sh) || (y.s[1] && y.s[1] != sh) || gap % sh != 0 || gap / sh < x.n[1]) return true;
     return !distinct(View{x.data, {x.n[0], gap / sh + y.n[1], x.n[2]}, {x.s[0], sh, x.s[2]}, x.D});

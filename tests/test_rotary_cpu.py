@@ -91,6 +91,16 @@ def test_heads_side_by_side_pass_the_checks(lib):
     assert call(lib, y=(heads(QO, HQ, sb=whole), heads(QO + 2 * (HQ + 1) * T * D, HK, sb=whole))) == 6   # into the next sequence
 
 
+def test_rows_that_interleave_are_refused(lib):
+    """Two views whose rows are apart from token to token, but whose sequences begin between each other's tokens."""
+    wx, wy = HQ * D, HK * D
+    rows = lambda at, n, off: heads(at + 2 * off, n, wy + wx + wy, D, wx + wy)  # noqa: E731
+    assert call(lib, T=2, y=(rows(QO, HQ, 0), rows(QO, HK, wx))) == 6
+    assert call(lib, T=2, x=(rows(QO, HQ, 0), heads(K, HK)), y=(heads(KO, HQ), rows(QO, HK, wx))) == 6
+    far = 2 ** 60   # the ends of such views do not fit 64 bits
+    assert call(lib, x=(heads(Q, HQ, far, far, far), heads(K, HK))) == 2
+
+
 class Cache(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "table", "seq_len")] + [(n, ctypes.c_int) for n in ("B", "Hkv", "D", "page", "max_pages", "num_pages", "dtype")]
 
