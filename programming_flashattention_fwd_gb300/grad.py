@@ -109,6 +109,8 @@ class _Attention(torch.autograd.Function):
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, do, dlse):
+        if _capturing():
+            raise RuntimeError("attention_ad's backward is not captured into a graph: call attention and attention_bwd there")
         q, k, v, o, lse = ctx.saved_tensors
         if do is None and dlse is None:
             return None, None, None, None, None
@@ -122,7 +124,7 @@ class _Attention(torch.autograd.Function):
 def attention_ad(q, k, v, causal=False, scale: Optional[float] = None) -> Tuple[torch.Tensor, torch.Tensor]:
     """``attention`` for training: (o, lse), both differentiable by torch's autograd with respect to q, k and v.
 
-    Not for a call that is captured into a CUDA graph: the gradient nodes of leaves that an eager graph shares belong to that graph's
+    Neither the call nor its backward is captured into a CUDA graph: the gradient nodes of leaves that an eager graph shares belong to that graph's
     stream.  A captured step calls ``attention`` and ``attention_bwd``."""
     if torch.is_grad_enabled() and any(isinstance(x, torch.Tensor) and x.requires_grad for x in (q, k, v)) and _capturing():
         raise RuntimeError("attention_ad is not captured into a graph: call attention and attention_bwd there")

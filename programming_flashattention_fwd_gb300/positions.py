@@ -235,6 +235,8 @@ class _Rotary(torch.autograd.Function):
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dq, dk=None):
+        if _capturing():
+            raise RuntimeError("rotary_ad's backward is not captured into a graph: call rotary there with inverse")
         start, position = ctx.saved_tensors
         if dq is not None and dk is not None:
             dq, dk = rotary(ctx.table, _dense(dq), _dense(dk), start, position, inverse=True)
@@ -246,8 +248,8 @@ class _Rotary(torch.autograd.Function):
 def rotary_ad(table: RotaryTable, q, k=None, start=None, position=None):
     """``rotary`` for training: differentiable by torch's autograd with respect to q and k.
 
-    Not for a call that is captured into a CUDA graph (see ``attention_ad``): a captured step calls ``rotary``, and ``rotary``
-    with inverse."""
+    Neither the call nor its backward is captured into a CUDA graph (see ``attention_ad``): a captured step calls ``rotary``, and
+    ``rotary`` with inverse."""
     if torch.is_grad_enabled() and any(isinstance(x, torch.Tensor) and x.requires_grad for x in (q, k)) and _capturing():
         raise RuntimeError("rotary_ad is not captured into a graph: call rotary there, and again with inverse")
     return _Rotary.apply(q, k, table, start, position)

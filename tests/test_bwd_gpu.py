@@ -353,6 +353,28 @@ def test_autograd_is_not_captured(fa):
     torch.cuda.synchronize()
 
 
+def test_a_backward_pass_is_not_captured(fa):
+    """Nor is the backward of a call that was made before the capture, on the same stream; the call's graph serves afterwards."""
+    s, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    q, table = torch.zeros(1, 2, 8, 64, dtype=torch.bfloat16, device="cuda"), fa.RotaryTable(64)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        leaves = [q.clone().requires_grad_() for _ in range(2)]
+        outs, do = (fa.attention_ad(leaves[0], q, q)[0], fa.rotary_ad(table, leaves[1])), torch.ones_like(q)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g, stream=s):
+        for o, x in zip(outs, leaves):
+            with pytest.raises(RuntimeError, match="captured"):
+                torch.autograd.grad(o, x, do, retain_graph=True)
+        fa.attention(q, q, q)
+    g.replay()
+    with torch.cuda.stream(s):
+        for o, x in zip(outs, leaves):
+            o.backward(do)
+            assert x.grad is not None
+    torch.cuda.synchronize()
+
+
 def test_a_layer_s_gradients(fa):
     """Projection, rotation, attention and their gradients as a training step runs them, against float64 autograd over the same
     products.  Tolerance: every tensor between is rounded to the type, and what comes out has passed seven such roundings
