@@ -6,8 +6,10 @@
 // off by 0.004 rad at position 65536.)
 //
 // A thread has 16 elements of a head (two 16-byte chunks, 8 pairs) of one token and goes through a run of heads with them, so that
-// sines and cosines are computed once for several heads; four heads' loads are in flight at a time, the first of them
-// while the angles are computed.  Neighbouring threads have neighbouring chunks, then neighbouring tokens.  Bound by memory.
+// sines and cosines are computed once for several heads; three heads' loads are in flight at a time, the first of them
+// while the angles are computed.  Neighbouring threads have neighbouring chunks, then neighbouring tokens: where a thread's own two
+// chunks lie side by side instead, every 32-byte sector is written in two parts (3 x 1777 tokens of 32 heads at D = 64 11.5 us, 9.3 so).
+// Bound by memory.
 #include <atomic>
 #include <cstdint>
 
@@ -40,21 +42,26 @@ __device__ __forceinline__ void turn(float &a, float &b, float c, float s)
     b = fmaf(x, s, y * c);
 }
 
-// Pairs (lo, hi) held in matching halves of two words, or in one word each.
+// Pairs (lo, hi) held in matching halves of two words, or, interleaved, in one word each: lo holds four, hi four others.
 template <bool BF16>
-__device__ __forceinline__ void turn_words(uint4 &lo, uint4 &hi, bool interleaved, const float *c, const float *s)
+__device__ __forceinline__ void turn_words(uint4 &lo, uint4 &hi, bool interleaved, bool turn_lo, bool turn_hi, const float *c, const float *s)
 {
     uint32_t *x = &lo.x, *y = &hi.x;
-    if (interleaved) {   // words of lo hold pairs 0 .. 3, words of hi 4 .. 7
+    if (interleaved) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            float2 f = unpack<BF16>(x[i]), g = unpack<BF16>(y[i]);
-            turn(f.x, f.y, c[i], s[i]);
-            turn(g.x, g.y, c[i + 4], s[i + 4]);
-            x[i] = pack2<BF16>(f.x, f.y);
-            y[i] = pack2<BF16>(g.x, g.y);
+            if (turn_lo) {
+                float2 f = unpack<BF16>(x[i]);
+                turn(f.x, f.y, c[i], s[i]);
+                x[i] = pack2<BF16>(f.x, f.y);
+            }
+            if (turn_hi) {
+                float2 g = unpack<BF16>(y[i]);
+                turn(g.x, g.y, c[i + 4], s[i + 4]);
+                y[i] = pack2<BF16>(g.x, g.y);
+            }
         }
-    } else {
+    } else if (turn_lo) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             float2 f = unpack<BF16>(x[i]), g = unpack<BF16>(y[i]);
@@ -131,7 +138,7 @@ __device__ __forceinline__ void note(const Params &p, const Token &k, int from, 
 
 // rot a multiple of 16: 8 pairs a thread.
 template <bool BF16, bool APPEND>
-__global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ Params p)
+__global__ void __launch_bounds__(kThreads, 4) rotary_kernel(const __grid_constant__ Params p)
 {
     cache::grid_wait();
     cache::grid_done_soon();
@@ -139,14 +146,18 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
     const int u = threadIdx.x & ((1 << shift) - 1);
     const Token k = token_at<APPEND>(p, ((long long)blockIdx.x * kThreads + threadIdx.x) >> shift);
     if (!k.here) return;
-    // The thread's elements: e0 .. e0 + 7 and e1 .. e1 + 7.
-    const bool mine = u * 8 < half;   // rotated ones
-    int e0 = u * 16, e1 = u * 16 + 8;
-    if (mine && !p.interleaved) {
-        e0 = u * 8;
+    // The thread's elements: e0 .. e0 + 7 and e1 .. e1 + 7, each beside the next thread's.  Of halves, rotated threads take a pair's two
+    // sides, those behind them the two halves of what is not rotated.
+    int e0 = u * 8, e1 = e0 + p.D / 2;
+    if (!p.interleaved) {
         e1 = e0 + half;
+        if (e0 >= half) {
+            e0 += half;
+            e1 = e0 + p.D / 2 - half;
+        }
     }
-    constexpr int BATCH = 4;
+    const bool turn_lo = e0 < p.rot, turn_hi = e1 < p.rot;   // of halves, both or neither
+    constexpr int BATCH = 3;   // (4: 80 registers and 13.5 instead of 12.7 us for 8 x 500 tokens of 48 heads at D = 64)
     const int h0 = blockIdx.y * p.per, h1 = min(h0 + p.per, p.heads);
     uint4 lo[BATCH], hi[BATCH];
     auto load = [&](int first) {
@@ -163,10 +174,10 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
     };
     load(h0);
     float c[8], s[8];
-    if (mine) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float2 v = angle(p, k.position, u * 8 + i);
+    for (int i = 0; i < 8; ++i) {
+        if (i < 4 || !p.interleaved ? turn_lo : turn_hi) {
+            const float2 v = angle(p, k.position, p.interleaved ? (i < 4 ? e0 : e1) / 2 + i % 4 : e0 + i);
             c[i] = v.x;
             s[i] = v.y;
         }
@@ -181,7 +192,7 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
             uint16_t *y;
             int head;
             const Segment &g = segment_of(p, k, first + i, x, y, head);
-            if (mine && g.turned) turn_words<BF16>(lo[i], hi[i], p.interleaved, c, s);
+            if (g.turned) turn_words<BF16>(lo[i], hi[i], p.interleaved, turn_lo, turn_hi, c, s);
             auto store = [&](uint16_t *to) {
                 *reinterpret_cast<uint4 *>(to + e0) = lo[i];
                 *reinterpret_cast<uint4 *>(to + e1) = hi[i];
@@ -235,17 +246,17 @@ __global__ void __launch_bounds__(kThreads) rotary_pairs_kernel(const __grid_con
 }
 
 // A thread goes through `per` heads: one where even so there are few blocks (the smallest call is all latency: 8 tokens of 40 heads
-// 2.3 us, 3.8 with 8 heads a thread), otherwise three at least, which share the angles (512 tokens of 40 heads 4.5 us, 5.5 with one), and
-// more where that still leaves 8 blocks an SM.  16384 tokens of 40 heads at D = 128 54 us (6.2 TB/s; with values and the cache's
-// writes 76 us, 6.1 TB/s); 3 x 1777 tokens of 32 heads at D = 64, into the rows of a projection, 11.5 us (3.8 TB/s: a wave and a
-// half of blocks).  Angles in shared memory, computed once for a block's 8 warps with other heads each: 57, 12.2 us, and 11 instead of
-// 5 us for 8 x 2000 tokens of 4 heads.
+// 2.3 us, 3.8 with 8 heads a thread), otherwise three at least, which share the angles and are loaded at once (512 tokens of 40
+// heads 3.8 us, 5.1 with one), and more where that still leaves 12 blocks an SM.  16384 tokens of 40 heads at D = 128 53 us (6.3 TB/s;
+// with values and the cache's writes 76 us, 6.2 TB/s); 3 x 1777 tokens of 32 heads at D = 64, into the rows of a projection, 9.3 us (4.7
+// TB/s).  Angles in shared memory, computed once for a block's 8 warps with other heads each: 5 % slower, and 11 instead of 5 us for
+// 8 x 2000 tokens of 4 heads.
 template <bool BF16, bool APPEND>
 cudaError_t launch_one(Params p, cudaStream_t st)
 {
     const bool wide = p.rot % 16 == 0;
     const long long threads = (long long)p.B * p.T * (wide ? p.D / 16 : p.D / 2), blocks = (threads + kThreads - 1) / kThreads;
-    const long long groups = (8 * 152 + blocks - 1) / blocks;
+    const long long groups = (12 * 152 + blocks - 1) / blocks;
     long long per = (p.heads + groups - 1) / groups;
     if (per < 3 && blocks * p.heads > 2 * 152) per = 3 < p.heads ? 3 : p.heads;
     p.per = (int)per;
