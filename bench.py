@@ -86,6 +86,9 @@ KERNEL_SOURCES = {
     "fa::cache::weigh_kernel": ("weigh_sm103.cu",) + CACHE_SOURCES,
     "fa::cache::weigh_prompt_kernel": ("weigh_sm103.cu",) + CACHE_SOURCES,
     "fa::cache::evict_kernel": ("cache_sm103.cu",) + CACHE_SOURCES,
+    "fa::bwd::bwd_kernel": ("bwd_sm103.cu", "bwd_api.cpp", "bwd_internal.h", "schedule.h", "cache_device.cuh", "cache_internal.h"),
+    "fa::rotary::rotary_kernel": ("rotary_sm103.cu", "rotary_api.cpp", "rotary_internal.h", "schedule.h", "cache_device.cuh",
+                                  "cache_internal.h"),
 }
 
 

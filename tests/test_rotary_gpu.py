@@ -7,6 +7,8 @@ of the last place (2^-23); the amplitude and the two products add 2^-24 each:
 What is not rotated is copied: equal.
 """
 import copy
+import os
+import re
 
 import numpy as np
 import pytest
@@ -320,3 +322,51 @@ def test_calls_with_nothing_between(fa):  # noqa: F811
     got = [step(a, i, lambda: None) for i in range(20)]
     want = [step(b, i, torch.cuda.synchronize) for i in range(20)]
     assert all(torch.equal(x, y) for x, y in zip(got, want)) and torch.equal(a["k"], b["k"]) and torch.equal(a["v"], b["v"])
+
+
+def readme(word):
+    """The README's one block of Python that contains `word`."""
+    with open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "README.md")) as f:
+        block, = [b for b in re.findall(r"```python\n(.*?)```", f.read(), re.S) if word in b]
+    return compile(block, "README.md", "exec")
+
+
+def test_the_readme_s_training_step(fa):  # noqa: F811
+    """As it stands there, against the same steps one by one; the gradient arrives in the projection's rows."""
+    B, T, Hq, Hkv, D = 2, 70, 4, 2, 64
+    qkv = data(40, "bf16", B, T, Hq + 2 * Hkv, D).requires_grad_()
+    env = dict(qkv=qkv, D=D, Hq=Hq, Hkv=Hkv)
+    exec(readme("attention_ad("), env)
+    do = data(41, "bf16", B, Hq, T, D)
+    env["o"].backward(do)
+    rows, table = qkv.detach().transpose(1, 2), fa.RotaryTable(D)
+    q, k = fa.rotary(table, rows[:, :Hq], rows[:, Hq:Hq + Hkv])
+    v = rows[:, Hq + Hkv:].contiguous()
+    o, lse = fa.attention(q, k, v, causal=True)
+    assert torch.equal(env["o"], o) and torch.equal(env["lse"], lse)
+    dq, dk, dv = fa.attention_bwd(q, k, v, o, lse, do, causal=True)
+    want = torch.cat((*fa.rotary(table, dq, dk, inverse=True), dv), 1).transpose(1, 2)
+    assert torch.equal(qkv.grad, want)
+
+
+def test_the_readme_s_serving_step(fa):  # noqa: F811
+    """A prompt and single tokens over two layers, as it stands there, against attention over all rows at once."""
+    B, Hq, Hkv, D, page, layers, total = 2, 4, 2, 64, 16, 2, 41
+    pools = [[torch.zeros(B * 4, Hkv, page, D, dtype=torch.bfloat16, device="cuda") for _ in range(2)] for _ in range(layers)]
+    seq_len, next_pos = ints([0] * B), ints([0] * B)
+    whole = [data(42 + i, "bf16", B, total, Hq + 2 * Hkv, D) for i in range(layers)]
+    env = dict(caches=[fa.KVCache(*p, seq_len) for p in pools], Hq=Hq, Hkv=Hkv, table=fa.RotaryTable(D), seq_len=seq_len, next_pos=next_pos)
+    out, at = [[] for _ in range(layers)], 0
+    for T in (39, 1, 1):
+        env.update(T=T, qkv=[x[:, at:at + T] for x in whole], o=[None] * layers, lse=[None] * layers)
+        exec(readme("rotary_append("), env)
+        for i in range(layers):
+            out[i].append(env["o"][i])
+        at += T
+    assert seq_len.tolist() == next_pos.tolist() == [total] * B
+    for i in range(layers):
+        q, k, v = whole[i].transpose(1, 2).split([Hq, Hkv, Hkv], 1)
+        q, k = fa.rotary(env["table"], q, k)
+        want, _ = fa.attention(q, k, v.contiguous(), causal=True)
+        # two kernels with sums in other orders: each within half a step of P's rounding, of |v| <= 5, and of its own
+        assert (torch.cat(out[i], 2).double() - want.double()).abs().max() <= 5 * 2 * 2.0 ** -8 + 2 * 2.0 ** -8 * want.double().abs().max()
