@@ -197,12 +197,14 @@ inline Load load_of(const Shape &s)
     return l;
 }
 
+// CTAs that share the steps: a part of about two is the least that is worth its sums.
+inline int share_ctas(const Load &l) { return (int)(l.total / 4 < kCtas ? (l.total / 4 > 0 ? l.total / 4 : 1) : kCtas); }
+
 // Cuts the line of all steps into even shares.
 template <bool ROWQ, int BN>
 inline void cut_evenly(const Shape &s, const Load &l, Cuts &c, Join &j)
 {
-    // a part of about two steps is the least that is worth its sums
-    const int G = (int)(l.total / 4 < kCtas ? (l.total / 4 > 0 ? l.total / 4 : 1) : kCtas);
+    const int G = share_ctas(l);
     c.ctas = G;
     c.empty = (int)l.units;
     int k = 0;
@@ -242,13 +244,17 @@ inline void cut_evenly(const Shape &s, const Load &l, Cuts &c, Join &j)
     j.slot[j.num] = slots;
 }
 
-// Whether the keys' pass, and the queries', is cut evenly rather than dealt out in whole units.  The queries' kernel fills the SMs that
-// the keys' leaves idle, so a call takes about as long as the longest line of the keys' pass, or as all steps shared
-// evenly and what the queries' lines differ by at the end.  Parts cost their bytes, written and read, and 6 us, 14 in the keys' pass,
-// of more starts, last stores and the joining kernel.  And lines that are cut do not run in step, so that what they stream
-// has to stay in L2: 4096 tokens of 2 x 32 heads at D = 128 (134 MB of q and do) take 378 us whole and 510 cut.
-// Measured, whole / cut: 8 heads over one KV head, 2048 tokens 190 / 49 us, 8192 tokens 724 / 288; 300 queries of 2 heads over 9000
-// keys 73 / 27; 6 heads of 2000 at D = 256 70 / 120 (not cut).
+// Whether the keys' pass, and the queries', is cut evenly rather than dealt out in whole units.  A CTA of the queries' kernel starts on
+// the first SM that is free and has as much to do as the others, so a call takes about as long as the longest line of the keys' pass and an
+// even share of the queries'.  Cutting the keys' pass saves what its longest line has above an even share, and cutting the
+// queries' what theirs has (where the keys' lines differ by less: otherwise the SMs do not come free at the same time).  Parts cost their
+// bytes, written and read, and 6 us, 10 in the keys' pass, of more starts, last stores and the joining kernel.  And lines
+// that are cut do not run in step, so that what they stream has to stay in L2: 4096 tokens of 2 x 32 heads at D = 128 (134 MB of q
+// and do) take 378 us whole and 510 cut.
+// Measured, whole / cut, us: the keys' pass of 8 heads over one KV head, 2048 tokens 190 / 49, 8192 tokens 724 / 288; of 32 heads over 8, 512
+// tokens 31 / 25, 1024 60 / 46, 2048 129 / 111 (D = 64 95 / 74, D = 256 262 / 243), 3000 222 / 196; not cut: 4096 tokens 323 / 344, 4 x 16
+// heads of 1024 at D = 64 50 / 57, 6 heads of 2000 at D = 256 68 / 91.  The queries' pass of 2 heads, 300 over 9000 keys, 73 / 27; not cut: 32
+// heads of 2048 (keys cut) 111 / 118.
 inline void plan_cuts(const Shape &q, const Shape &kv, int D, bool want_q, bool want_kv, Cuts &cq, Join &jq, Cuts &ck, Join &jk)
 {
     cq.ctas = cq.empty = ck.ctas = ck.empty = 0;
@@ -257,17 +263,16 @@ inline void plan_cuts(const Shape &q, const Shape &kv, int D, bool want_q, bool 
     const Load lq = D == 256 ? load_of<true, step_rows(256)>(q) : load_of<true, step_rows(64)>(q);
     const Load lk = D == 256 ? load_of<false, step_rows(256)>(kv) : load_of<false, step_rows(64)>(kv);
     if (lq.total == 0) return;
-    // microseconds of a step, measured (D = 256: both kernels of the keys' pass)
-    const double tk = D == 64 ? 1.0 : D == 128 ? 1.1 : 1.5, tq = D == 64 ? 0.8 : D == 128 ? 0.85 : 0.95;
-    const double kBytesPerUs = 4e6, kL2 = 48e6;
+    // microseconds of a step, measured (D = 256: the keys' pass is two kernels, of which the second fills what the first leaves idle)
+    const double tk = D == 64 ? 1.0 : D == 128 ? 1.45 : 0.65, tq = D == 64 ? 0.8 : D == 128 ? 1.1 : 1.3;
+    const double kBytesPerUs = 5e6, kL2 = 72e6;
     auto parts_us = [&](const Load &l, int results, double start) {
-        const double parts = kCtas + (double)(l.units < kCtas ? l.units : kCtas);
+        const double ctas = share_ctas(l), parts = ctas + ((double)l.units < ctas ? (double)l.units : ctas);
         return start + parts * kRows * D * 4.0 * results * 2.0 / kBytesPerUs;
     };
-    const double even_q = want_q ? (double)lq.total / kCtas * tq : 0., even_k = want_kv ? (double)lk.total / kCtas * tk : 0.;
-    const double line_k = want_kv ? (double)lk.longest * tk : 0., over = line_k - even_q - even_k;
-    const bool cut_k = want_kv && 4.0 * D * q.planes * q.rows <= kL2 && over > parts_us(lk, 2, 14.0);
-    const bool cut_q = want_q && 4.0 * D * kv.planes * kv.rows <= kL2 && (double)lq.longest * tq - even_q > parts_us(lq, 1, 6.0) + (cut_k || over < 0. ? 0. : over);
+    const double over_q = ((double)lq.longest - (double)lq.total / kCtas) * tq, over_k = want_kv ? ((double)lk.longest - (double)lk.total / kCtas) * tk : 0.;
+    const bool cut_k = want_kv && 4.0 * D * q.planes * q.rows <= kL2 && over_k > parts_us(lk, 2, 10.0);
+    const bool cut_q = want_q && 4.0 * D * kv.planes * kv.rows <= kL2 && over_q > parts_us(lq, 1, 6.0) + (cut_k ? 0. : over_k);
     if (cut_k) D == 256 ? cut_evenly<false, step_rows(256)>(kv, lk, ck, jk) : cut_evenly<false, step_rows(64)>(kv, lk, ck, jk);
     if (cut_q) D == 256 ? cut_evenly<true, step_rows(256)>(q, lq, cq, jq) : cut_evenly<true, step_rows(64)>(q, lq, cq, jq);
 }
