@@ -340,12 +340,13 @@ __global__ void __launch_bounds__((Cfg<MODE, D>::THREADS), 1)
         // ------------------------------------------------------------ resident tiles; lse and delta of streamed queries
         if (lane == 0) {
             uint32_t loads[2] = {0, 0}, g = 0;   // of the first and of the second resident operand
+            uint64_t whole = tmo;                // the other waits are for a step or two, these for all of a unit's (at most 2 us each)
             bool ok = true;
             Unit u;
             for (int round = 0; ok && unit_at<C::ROWQ, BN>(p.s, p.cuts, gridDim.x, blockIdx.x, round, u); ++round) {
                 if (u.n == 0) continue;
                 auto resident = [&](const CUtensorMap *m, uint32_t dst, uint32_t i) {
-                    if (loads[i] > 0 && !bounded_wait(barFree + 8 * i, (loads[i] - 1) & 1, abort_flag, tmo, S_RES, status)) return false;
+                    if (loads[i] > 0 && !bounded_wait(barFree + 8 * i, (loads[i] - 1) & 1, abort_flag, whole, S_RES, status)) return false;
                     mbar_arrive_expect_tx(barRes + 8 * i, C::RTILE);
 #pragma unroll
                     for (int pn = 0; pn < C::PANELS; ++pn) tma_load_3d(dst + pn * C::RPANEL, m, pn * 64, u.t * kRows, u.z, barRes + 8 * i);
@@ -355,6 +356,7 @@ __global__ void __launch_bounds__((Cfg<MODE, D>::THREADS), 1)
                 if (!C::RUSES) ok = resident(&tmR1, sR1, 0);
                 if (C::HAS_DS) ok = ok && resident(&tmR2, sR2, 1);
                 if (!ok) break;
+                whole = tmo * (1 + (uint64_t)(u.n >> 10));
                 if constexpr (!C::ROWQ) {
                     int plane = u.plane, tile = u.tile;
                     for (int j = 0; j < u.n && ok; ++j, ++g) {

@@ -425,3 +425,19 @@ def test_a_wait_that_runs_out(fa, D):
         assert fa.fa_device_status()[0] == 0
         near(run(fa, c), c, "bf16")
         assert fa.fa_device_status()[0] == 0
+
+
+def test_a_wait_for_a_long_unit(fa):
+    """Units of 8192 steps (more than 8 ms) under a limit of 4 ms, which is for a step or two: the wait for a whole unit has more."""
+    from programming_flashattention_fwd_gb300 import grad
+    B, Hq, Hkv, Sq, Sk, D = shape = 1, 160, 1, 1, 8192 * 64, 256
+    g = torch.Generator("cuda").manual_seed(28)
+    q, o, do, k, v = (torch.randn(s, generator=g, device="cuda", dtype=torch.bfloat16) for s in [(B, Hq, Sq, D)] * 3 + [(B, Hkv, Sk, D)] * 2)
+    lse = torch.full((B, Hq, Sq), 13.0, device="cuda")
+    want_, _, _ = fa.attention_bwd(q, k, v, o, lse, do, need_kv=False)
+    dq = torch.zeros_like(q)
+    ws = torch.zeros(fa.bwd_workspace_bytes(*shape), dtype=torch.uint8, device="cuda")
+    st = grad._library().fa_bwd_debug(*(x.data_ptr() for x in (q, k, v, o, lse, do)), None, dq.data_ptr(), None, None, *shape, 0, D ** -0.5, 0, ws.data_ptr(),
+                                      ws.nbytes, torch.cuda.current_stream().cuda_stream, 4_000_000, 0)
+    assert st == 0 and fa.fa_device_status()[0] == 0
+    assert torch.isfinite(dq.float()).all() and torch.equal(dq, want_)
