@@ -77,6 +77,7 @@ TARGET_FRAC = 0.60    # of the dense bf16 peak, stated for the D = 128 workloads
 # device headers and the host code that encodes its tensor maps and launch shape.
 COMMON_SOURCES = ("ptx.cuh", "watchdog.cuh", "fa_internal.h", "fa_api.cpp")
 CACHE_SOURCES = ("cache_api.cpp", "cache_device.cuh", "cache_internal.h", "cache_schedule.h")
+BWD_SOURCES = ("bwd_api.cpp", "bwd_internal.h", "schedule.h", "cache_device.cuh", "cache_internal.h")
 KERNEL_SOURCES = {
     "fa::fa_fwd_kernel": ("fa_fwd_sm103.cu", "schedule.h"),
     "fa::fa_fwd1_kernel": ("fa_fwd1_sm103.cu", "schedule.h"),
@@ -86,7 +87,8 @@ KERNEL_SOURCES = {
     "fa::cache::weigh_kernel": ("weigh_sm103.cu",) + CACHE_SOURCES,
     "fa::cache::weigh_prompt_kernel": ("weigh_sm103.cu",) + CACHE_SOURCES,
     "fa::cache::evict_kernel": ("cache_sm103.cu",) + CACHE_SOURCES,
-    "fa::bwd::bwd_kernel": ("bwd_sm103.cu", "bwd_api.cpp", "bwd_internal.h", "schedule.h", "cache_device.cuh", "cache_internal.h"),
+    "fa::bwd::bwd_kernel": ("bwd_sm103.cu",) + BWD_SOURCES,
+    "fa::bwd::bwd_mode_kernel": ("bwd_sm103.cu",) + BWD_SOURCES,
     "fa::rotary::rotary_kernel": ("rotary_sm103.cu", "rotary_api.cpp", "rotary_internal.h", "schedule.h", "cache_device.cuh",
                                   "cache_internal.h"),
 }

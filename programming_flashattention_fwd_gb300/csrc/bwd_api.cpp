@@ -15,6 +15,8 @@ namespace {
 
 using namespace fa::bwd;
 
+constexpr uint64_t kDefaultTimeoutNs = 2000000000ull;
+
 struct Range {
     uintptr_t at;
     size_t bytes;
@@ -117,62 +119,54 @@ int fa_bwd_debug(const void *q, const void *k, const void *v, const void *o, con
     const bool bf16 = dtype == 0;
     const int BN = step_rows(D);
     const long long zq = (long long)B * Hq, zk = (long long)B * Hkv;
-    Maps mq, mk;
-    std::memset(&mq, 0, sizeof(mq));
-    std::memset(&mk, 0, sizeof(mk));
+    Args a;
+    std::memset(&a, 0, sizeof(a));
     using fa::encode_tiles;
-    if (dq && (!encode_tiles(&mq.r1, q, bf16, D, Sq, zq, kRows) || !encode_tiles(&mq.r2, d_o, bf16, D, Sq, zq, kRows) ||
-               !encode_tiles(&mq.s1, k, bf16, D, Sk, zk, BN) || !encode_tiles(&mq.s2, v, bf16, D, Sk, zk, BN)))
+    Maps &m = a.m;
+    if (!encode_tiles(&m.q, q, bf16, D, Sq, zq, kRows) || !encode_tiles(&m.d_o, d_o, bf16, D, Sq, zq, kRows) || !encode_tiles(&m.k, k, bf16, D, Sk, zk, kRows) ||
+        !encode_tiles(&m.v, v, bf16, D, Sk, zk, kRows))
         return FA_ERR_TENSORMAP;
-    if (dk && (!encode_tiles(&mk.r1, k, bf16, D, Sk, zk, kRows) || !encode_tiles(&mk.r2, v, bf16, D, Sk, zk, kRows) ||
-               !encode_tiles(&mk.s1, q, bf16, D, Sq, zq, BN) || !encode_tiles(&mk.s2, d_o, bf16, D, Sq, zq, BN)))
+    if (BN != kRows &&
+        (!encode_tiles(&m.q_step, q, bf16, D, Sq, zq, BN) || !encode_tiles(&m.do_step, d_o, bf16, D, Sq, zq, BN) ||
+         !encode_tiles(&m.k_step, k, bf16, D, Sk, zk, BN) || !encode_tiles(&m.v_step, v, bf16, D, Sk, zk, BN)))
         return FA_ERR_TENSORMAP;
 
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     float *vec_nl = reinterpret_cast<float *>(ws), *vec_dc = reinterpret_cast<float *>(ws + plan.vec);
     float *part_q = reinterpret_cast<float *>(ws + 2 * plan.vec), *part_k = reinterpret_cast<float *>(ws + 2 * plan.vec + plan.part_q),
           *part_v = reinterpret_cast<float *>(ws + 2 * plan.vec + plan.part_q + plan.part_kv);
-    Params p;
-    std::memset(&p, 0, sizeof(p));
+    const float shift = shift_of(dtype);
+    Params &p = a.q;
     p.nl = vec_nl;
     p.dc = vec_dc;
     p.pad = (int)plan.pad;
     p.sl2 = (float)((double)scale * 1.4426950408889634);
-    const float shift = shift_of(dtype);
     p.dscale = std::exp2f(-shift);
     p.out_scale = scale;
     p.out_v_scale = p.dscale;
-    p.timeout_ns = timeout_ns;
+    p.timeout_ns = timeout_ns ? timeout_ns : kDefaultTimeoutNs;
     p.inject = inject;
+    a.kv = p;
+    if (dk) {
+        a.want_kv = true;
+        a.kv.s = plan.kv;
+        a.kv.out = dk;
+        a.kv.out_v = dv;
+        a.kv.al32 = aligned(dk, 32) && aligned(dv, 32);
+        a.kv.cuts = plan.cut_kv;
+        a.kv.part = part_k;
+        a.kv.part_v = part_v;
+    }
+    if (dq) {
+        a.want_q = true;
+        p.s = plan.q;
+        p.out = dq;
+        p.al32 = aligned(dq, 32);
+        p.cuts = plan.cut_q;
+        p.part = part_q;
+    }
     cudaError_t e = launch_prep(o, d_o, lse, dlse, vec_nl, vec_dc, zq, Sq, p.pad, D, bf16, shift, s);
-    if (e == cudaSuccess && dk) {
-        Params a = p;
-        a.s = plan.kv;
-        a.out = dk;
-        a.out_v = dv;
-        a.al32 = aligned(dk, 32) && aligned(dv, 32);
-        a.cuts = plan.cut_kv;
-        a.part = part_k;
-        a.part_v = part_v;
-        a.first = 1;
-        if (D == 256) {
-            e = launch_bwd(kV, D, bf16, mk, a, s);
-            a.first = 0;
-            if (e == cudaSuccess) e = launch_bwd(kK, D, bf16, mk, a, s);
-        } else {
-            e = launch_bwd(kKV, D, bf16, mk, a, s);
-        }
-    }
-    if (e == cudaSuccess && dq) {
-        Params a = p;
-        a.s = plan.q;
-        a.out = dq;
-        a.first = !dk;
-        a.al32 = aligned(dq, 32);
-        a.cuts = plan.cut_q;
-        a.part = part_q;
-        e = launch_bwd(kQ, D, bf16, mq, a, s);
-    }
+    if (e == cudaSuccess) e = launch_bwd(a, D, bf16, s);
     if (e == cudaSuccess && plan.join_q.num + plan.join_kv.num > 0)
         e = launch_join(JoinParams{plan.q, plan.kv, plan.join_q, plan.join_kv, part_q, part_k, part_v, dq, dk, dv, p.out_scale, p.out_v_scale}, D, bf16, s);
     return e == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;

@@ -244,7 +244,7 @@ inline void cut_evenly(const Shape &s, const Load &l, Cuts &c, Join &j)
     j.slot[j.num] = slots;
 }
 
-// Whether the keys' pass, and the queries', is cut evenly rather than dealt out in whole units.  A CTA of the queries' kernel starts on
+// Whether the keys' pass, and the queries', is cut evenly rather than dealt out in whole units.  A CTA of the queries' pass starts on
 // the first SM that is free and has as much to do as the others, so a call takes about as long as the longest line of the keys' pass and an
 // even share of the queries'.  Cutting the keys' pass saves what its longest line has above an even share, and cutting the
 // queries' what theirs has (where the keys' lines differ by less: otherwise the SMs do not come free at the same time).  Parts cost their
@@ -281,7 +281,6 @@ inline int parts_of(const Cuts &c) { return c.ctas ? c.slot[c.ctas] : 0; }
 
 struct Params {
     Shape s;
-    Cuts cuts;
     const float *nl, *dc;    // [B * Hq][pad] -lse log2 e + shift, and delta 2^-shift; rows at or behind Sq: -inf, 0
     int pad;                 // Sq rounded up to 128
     void *out, *out_v;       // dq, or dk and dv
@@ -290,19 +289,26 @@ struct Params {
     float dscale;            // 2^-shift
     float out_scale, out_v_scale;
     uint32_t al32;           // outputs are 32-byte aligned
-    uint32_t first;          // the first kernel behind lse and delta
-    uint64_t timeout_ns;
+    uint64_t timeout_ns;     // of each device wait
     uint32_t inject;         // fault injection: the first second tile is never loaded (bit 0: in every CTA, bit 1: in CTA 0)
+    Cuts cuts;               // (behind what the steps read)
 };
 
-// The operands: resident first and second (q and do, or k and v), streamed first and second (k and v, or q and do).
+// The operands in tiles of a resident tile's rows and, where a step has fewer (D = 256), of a step's.
 struct Maps {
-    CUtensorMap r1, r2, s1, s2;
+    CUtensorMap q, d_o, k, v, q_step, do_step, k_step, v_step;
+};
+
+// Both passes, or the one that is wanted.
+struct Args {
+    Maps m;
+    Params kv, q;
+    bool want_kv, want_q;
 };
 
 cudaError_t launch_prep(const void *o, const void *d_o, const float *lse, const float *dlse, float *nl, float *dc, long long planes, int Sq, int pad, int D,
                         bool bf16, float shift, cudaStream_t st);
-cudaError_t launch_bwd(int mode, int D, bool bf16, const Maps &m, const Params &p, cudaStream_t st);
+cudaError_t launch_bwd(const Args &a, int D, bool bf16, cudaStream_t st);
 // out [planes, rows, D] = round(scale * sum of the parts), for the units that are cut: dQ, and dK and dV, whose units are the same.
 struct JoinParams {
     Shape q, kv;
