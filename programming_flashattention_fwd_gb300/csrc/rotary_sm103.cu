@@ -3,7 +3,7 @@
 // Pair p of a head turns by position * freq[p]: (a, b) -> amplitude (a cos - b sin, a sin + b cos).  Frequencies are turns in
 // 64-bit fixed point, so that position * freq modulo 2^64 is the exact fraction of a turn, at any position, by one integer
 // product; its upper 32 bits, as a signed number of half turns, are the argument of sincospif.  (The angle itself in fp32 would be
-// off by 0.004 rad at position 65536.)
+// off by 0.004 rad at position 65536.)  Products and sums are fp32, rounded to the type once; what is not turned is copied.
 //
 // A thread has 16 elements of a head (two 16-byte chunks, 8 pairs) of one token and goes through a run of heads with them, so that
 // sines and cosines are computed once for several heads; three heads' loads are in flight at a time, the first of them
